@@ -85,7 +85,8 @@ typedef enum lmkv_status {
                                    for the copy before it exits).  The GPU is then not serving
                                    memory requests: treat the context as unusable. */
     LMKV_ERR_SCRATCH_LIMIT = 8, /* host: the batch needs more than the library's built-in scratch */
-    LMKV_ERR_BAD_DATA = 9       /* device: an encoded blob is inconsistent (stream skipped) */
+    LMKV_ERR_BAD_DATA = 9,      /* device: an encoded blob is inconsistent (stream skipped) */
+    LMKV_ERR_BAD_LENGTH = 10    /* device: a length outside the bounds of its call (clamped) */
 } lmkv_status;
 
 /* The paged KV pool.  layer_base is a DEVICE array of num_layers DEVICE
@@ -533,6 +534,193 @@ int lmkv_cachegen_retrieve_chunks(const lmkv_pool_t* pool, const int32_t* block_
                                   const int32_t* bins, void* const* blob_ptrs, const uint64_t* sizes,
                                   void* workspace, uint64_t workspace_bytes, int32_t* d_status,
                                   void* stream);
+
+/* ---- Attention-side operators on the paged pool -------------------------
+ * What an engine computes on the pages between a store and a retrieve: write
+ * new keys (rotated) and values into pages, place a retrieved chunk at another
+ * position, attend to the pages of a batch that shares a prefix, and evict by
+ * accumulated attention weight.  All follow this file's rules on ownership,
+ * streams, CUDA graphs and errors.
+ *
+ * Element types.  These entry points compute, so they take the pool's type:
+ * lmkv_dtype_t must match pool->elem_bytes (2 for bf16 and fp16, 4 for fp32;
+ * UNSUPPORTED otherwise).  Sums and softmax statistics are held in fp32 and
+ * every result is rounded once, to nearest even. */
+typedef enum lmkv_dtype {
+    LMKV_BF16 = 0,
+    LMKV_FP16 = 1,
+    LMKV_FP32 = 2       /* rotary calls only */
+} lmkv_dtype_t;
+
+/* Rows of heads on the DEVICE, x[token][head][head_dim]: element strides of a
+ * token and of a head (any sign or order; a head's head_dim elements are
+ * contiguous).  `data` is aligned to its element. */
+typedef struct lmkv_rows {
+    void* data;
+    int64_t token_stride;
+    int64_t head_stride;
+} lmkv_rows_t;
+
+/* A ragged batch.  Request r has n_r = q_start[r+1] - q_start[r] new tokens,
+ * rows q_start[r] .. q_start[r+1] - 1 of the row arguments, and kv_len[r]
+ * cached tokens in its own pages, the new ones included and last: new token i
+ * is cached token kv_len[r] - n_r + i.  The lengths live on the DEVICE, so a
+ * captured call follows them; the HOST gives their bounds.  Rows behind
+ * q_start[num_req] (a padded batch) are left as they are.  A length outside
+ * its bounds is clamped and reported as BAD_LENGTH. */
+typedef struct lmkv_batch {
+    const int32_t* q_start;       /* DEVICE [num_req + 1], ascending from >= 0 */
+    const int32_t* kv_len;        /* DEVICE [num_req] */
+    const int32_t* block_table;   /* DEVICE [num_req][max_blocks] */
+    int32_t max_blocks;
+    int32_t num_req;
+    int32_t num_tokens;           /* rows there are: q_start[num_req] <= num_tokens */
+    int32_t max_new;              /* n_r <= max_new */
+    int32_t max_kv_len;           /* kv_len[r] <= max_kv_len <= max_blocks * block_size */
+} lmkv_batch_t;
+
+/* Rotary position encoding (Su et al., "RoFormer", 2021): pair i < rot_dim/2
+ * of a head, (a, b), at position p becomes
+ *   (a cos t - b sin t, a sin t + b cos t) * magnitude,  t = p * inv_freq[i].
+ * The pair is elements (i, i + rot_dim/2), or (2i, 2i+1) when interleaved;
+ * elements from rot_dim on are unchanged.  Angles are reduced exactly: the
+ * kernels multiply p by inv_freq / 2 pi as a 64-bit fraction of a turn, so a
+ * far position loses nothing. */
+#define LMKV_ROTARY_MAX_PAIRS 128
+typedef struct lmkv_rotary {
+    int32_t rot_dim;              /* even, 2 .. min(head_dim, 256) */
+    int32_t interleaved;
+    double magnitude;
+    double inv_freq[LMKV_ROTARY_MAX_PAIRS];   /* radians per position */
+} lmkv_rotary_t;
+
+typedef enum lmkv_rotary_scaling {
+    LMKV_ROTARY_PLAIN = 0,
+    LMKV_ROTARY_LINEAR = 1,   /* every frequency / factor */
+    LMKV_ROTARY_BASE = 2,     /* base * factor^(rot_dim / (rot_dim - 2)) */
+    LMKV_ROTARY_BANDS = 3,    /* by turns over `original` positions, n = original f / 2 pi:
+                                 n <= low: f / factor; n >= high: f; linear in n between */
+    LMKV_ROTARY_RAMP = 4      /* linear in the pair's index between the (fractional) pairs
+                                 that make `high` and `low` turns over `original` positions:
+                                 f on the fast side, f / factor on the slow side; the
+                                 magnitude is 0.1 ln(factor) + 1 ("YaRN", Peng et al., 2023) */
+} lmkv_rotary_scaling_t;
+
+/* Fill *out (host only): inv_freq[i] = base^(-2i / rot_dim), scaled.  `low`,
+ * `high` and `original` are read by BANDS and RAMP.  INVALID_ARG for an odd
+ * or out-of-range rot_dim, base <= 1, factor < 1, low >= high or low <= 0, original
+ * <= 0, a value that is not finite, or an unknown scaling. */
+int lmkv_rotary_init(lmkv_rotary_t* out, int32_t rot_dim, int32_t interleaved, double base,
+                     int32_t scaling, double factor, double low, double high, double original);
+
+/* Write a batch's new tokens into one layer: q is rotated into q_out (which
+ * may be q itself), k is rotated and v copied into the pages of cached token
+ * kv_len[r] - n_r + i.
+ *   positions : DEVICE int64 [num_tokens], each new token's position, or NULL:
+ *               its cached token number (they differ once tokens were evicted)
+ *   q, k, v   : num_q_heads, num_kv_heads, num_kv_heads heads per token
+ * A new token without a cached place (kv_len[r] < n_r: BAD_LENGTH; a block id
+ * out of range: BAD_BLOCK) is not written to the pages; its q_out is.
+ * INVALID_ARG for null pointers, sizes <= 0, num_q_heads not a multiple of
+ * num_kv_heads, max_kv_len beyond the table, or a rotary that does not fit.
+ * num_tokens == 0 launches nothing.  max_new is not read.  Overlap of q_out
+ * with q other than q itself, or of either with k or v, is not allowed. */
+int lmkv_append_layer(const lmkv_pool_t* pool, int32_t dtype, int32_t layer, const lmkv_batch_t* batch,
+                      int32_t num_q_heads, const lmkv_rows_t* q, const lmkv_rows_t* k,
+                      const lmkv_rows_t* v, const lmkv_rows_t* q_out, const int64_t* positions,
+                      const lmkv_rotary_t* rotary, int32_t* d_status, void* stream);
+
+/* Retrieve at another position: lmkv_scatter_chunks (or _layer), except that
+ * the keys of request r are turned by shift[r] positions (HOST int64, any
+ * sign) on their way into the pages, so that a chunk computed at positions
+ * p.. serves at p + shift[r]...  Values are copied.  rotary is the encoding
+ * the keys were made with, its magnitude not applied again: keys are only
+ * turned.  shift[r] == 0 copies the keys as they are.  Errors as
+ * lmkv_scatter_chunks, plus INVALID_ARG for a null shift or a rotary that
+ * does not fit, UNSUPPORTED for the type. */
+int lmkv_scatter_chunks_shifted(const lmkv_pool_t* pool, int32_t dtype, const int32_t* block_table,
+                                int32_t max_blocks, const int64_t* start, const int64_t* end,
+                                int32_t num_req, int32_t chunk_size, int32_t save_unfull_chunk,
+                                void* const* chunk_ptrs, const int64_t* shift,
+                                const lmkv_rotary_t* rotary, int32_t* d_status, void* stream);
+
+int lmkv_scatter_layer_shifted(const lmkv_pool_t* pool, int32_t dtype, const int32_t* block_table,
+                               int32_t max_blocks, const int64_t* start, const int64_t* end,
+                               int32_t num_req, int32_t chunk_size, int32_t save_unfull_chunk,
+                               void* const* chunk_ptrs, const int64_t* shift,
+                               const lmkv_rotary_t* rotary, int32_t layer, int32_t* d_status,
+                               void* stream);
+
+/* Attention of a batch's new tokens to one layer's pages.  Every request sees
+ * the first prefix_len tokens of prefix_table (DEVICE int32
+ * [ceil(prefix_len / block_size)], the shared prefix; its pages are read once for the
+ * whole batch) and then its own cached tokens, causally: new token i of
+ * request r sees own tokens j <= kv_len[r] - n_r + i.  With x = scale * q.k,
+ *   out = sum softmax(x) v   and   lse = ln sum exp(x),
+ * query head h using KV head h / (num_q_heads / num_kv_heads).
+ *   out : rows like q's, not overlapping it;  lse : DEVICE float32 [num_tokens][num_q_heads] or NULL
+ *   workspace : DEVICE, 16-byte aligned, lmkv_attend_workspace_bytes bytes,
+ *               contents irrelevant, not shared with calls that may run at
+ *               the same time (two captured graphs included)
+ * A token that sees nothing gets out = 0 and lse = -infinity.  A cached token
+ * in a block with an id out of range is not attended to (BAD_BLOCK).  Page
+ * slots past kv_len are never read, whatever they hold; within a request a
+ * value that is not finite may reach the rows of new tokens before it.
+ * head_dim 64 or 128, bf16 or fp16 (UNSUPPORTED otherwise); scale finite.
+ * Products of bf16 / fp16 are accumulated in fp32; softmax weights are
+ * rounded to the pool's type before they meet v. */
+int lmkv_attend_workspace_bytes(const lmkv_pool_t* pool, int32_t num_q_heads, int32_t num_tokens,
+                                int32_t num_req, int32_t max_new, int64_t prefix_len,
+                                int32_t max_kv_len, uint64_t* bytes);
+
+int lmkv_attend_layer(const lmkv_pool_t* pool, int32_t dtype, int32_t layer, const lmkv_batch_t* batch,
+                      int32_t num_q_heads, const lmkv_rows_t* q, const int32_t* prefix_table,
+                      int64_t prefix_len, float scale, const lmkv_rows_t* out, float* lse,
+                      void* workspace, uint64_t workspace_bytes, int32_t* d_status, void* stream);
+
+/* Accumulate the attention weight each own cached token received in one
+ * layer from the batch's new tokens ("H2O: Heavy-Hitter Oracle", Zhang et
+ * al., 2023), per KV head:
+ *   scores_out[r][h][j] = decay * scores[r][h][j] + sum exp(scale * q.k_j - lse)
+ * over new tokens i that see j and the query heads of KV head h, for j <
+ * kv_len[r]; other entries are left as they are.
+ *   lse        : DEVICE float32 [num_tokens][num_q_heads], of lmkv_attend_layer (rows of
+ *                -infinity add nothing)
+ *   scores     : DEVICE float32 [num_req][num_kv_heads][score_stride]; not read
+ *                when decay == 0, where it may be NULL
+ *   scores_out : the same shape; may be scores itself, else not overlapping it
+ * score_stride >= max_kv_len.  The sum's order is fixed: repeated calls give
+ * the same bits.  A token in a block with an id out of range receives
+ * nothing (BAD_BLOCK).  Types and head_dim as lmkv_attend_layer. */
+int lmkv_weigh_layer(const lmkv_pool_t* pool, int32_t dtype, int32_t layer, const lmkv_batch_t* batch,
+                     int32_t num_q_heads, const lmkv_rows_t* q, const float* lse, float scale,
+                     float decay, const float* scores, float* scores_out, int64_t score_stride,
+                     int32_t* d_status, void* stream);
+
+/* Evict own cached tokens of one layer down to `budget` per request, each KV
+ * head choosing its own (H2O, as above): kept are the first `sinks` tokens,
+ * the last `recent`, and the highest scores among the others, up to budget in
+ * all; equal scores (-0 and +0 are equal) go to the lowest token number, a NaN is lower than any
+ * number.  The kept tokens' K and V rows move, in their order, to the front
+ * of the request's pages, in place: slot i of head h receives token
+ * keep[r][h][i].  Requests of at most `budget` tokens keep all.
+ *   kv_len      : DEVICE int32 [num_req] (outside 0..max_kv_len: clamped, BAD_LENGTH)
+ *   scores      : DEVICE float32 [num_req][num_kv_heads][score_stride]
+ *   keep        : DEVICE int32 [num_req][num_kv_heads][budget], written: kept
+ *                 token numbers, ascending, then -1
+ *   new_len     : DEVICE int32 [num_req], written: min(kv_len, budget); kv_len itself
+ *                 is not (other layers need it), new_len may not be kv_len
+ *   kept_scores : DEVICE float32 [num_req][num_kv_heads][kept_stride], written: the kept tokens'
+ *                 scores for i < new_len, then 0 up to budget; or NULL; not overlapping scores
+ * Any element size.  A token whose block id, or whose new slot's, is out of
+ * range does not move (BAD_BLOCK).  INVALID_ARG for sinks + recent > budget,
+ * budget < 1, score_stride < max_kv_len, kept_stride < budget, or max_kv_len
+ * beyond the table. */
+int lmkv_evict_layer(const lmkv_pool_t* pool, int32_t layer, const int32_t* block_table,
+                     int32_t max_blocks, const int32_t* kv_len, int32_t num_req, int32_t max_kv_len,
+                     const float* scores, int64_t score_stride, int32_t budget, int32_t sinks,
+                     int32_t recent, int32_t* keep, int32_t* new_len, float* kept_scores,
+                     int64_t kept_stride, int32_t* d_status, void* stream);
 
 /* Human-readable name of a status code (static storage). */
 const char* lmkv_status_string(int status);

@@ -9,6 +9,7 @@
 #include "lmkv.h"
 #include "lmkv_internal.h"
 #include "lmkv_fp8.cuh"
+#include "lmkv_shift.cuh"
 
 #include <atomic>
 #include <map>
@@ -34,6 +35,7 @@ inline int cuda_status(cudaError_t err) {
 // per-layer calls).
 constexpr int kLsuThreads = 256;
 constexpr int kLsuUnroll = 8;
+constexpr int kShiftUnroll = 4;           // unit pairs in flight per thread (shifted scatter)
 constexpr int kQuantThreads = 256;        // staged quantiser
 constexpr int kQuantRegThreads = 512;     // register-staged fallback (slices beyond shared memory)
 constexpr int kQuantVPT = 8;
@@ -334,6 +336,71 @@ int move_entry(bool gather, const lmkv_pool_t* pool, const int32_t* block_table,
         return gather ? launch_move<lmkv::BatchSmall, true>(c, s)
                       : launch_move<lmkv::BatchSmall, false>(c, s);
     return gather ? launch_move<lmkv::Batch, true>(c, s) : launch_move<lmkv::Batch, false>(c, s);
+}
+
+template <class B, class T, int V, bool kInterleaved>
+int launch_shift_kernel(const Call& c, const lmkv_rotary_detail::Rotary& rot, const int64_t* shift,
+                        cudaStream_t stream) {
+    return for_each_block<B>(c, nullptr, [&](const B& b) {
+        using U = lmkv_rotary_detail::Units<T, V, kInterleaved>;
+        B s = b;
+        s.rot = rot;
+        s.head_dim = c.pool->head_dim;
+        s.by_head = lmkv_paged::FastDiv((uint32_t)U::count(rot.half, c.pool->head_dim));
+        s.row_units = c.pool->num_kv_heads * (int32_t)s.by_head.d;
+        for (int i = 0; i < B::kCapacity; ++i) s.shift[i] = i < s.num_req ? shift[s.req_row[i]] : 0;
+        const int64_t items = lmkv::batch_items(s);
+        return launch_pdl(lmkv::shift_scatter_kernel<B, T, V, kInterleaved, kLsuThreads, kShiftUnroll>, items,
+                          kLsuThreads, stream, s, items);
+    });
+}
+
+template <class B, class T>
+int launch_shift(const Call& c, const lmkv_rotary_detail::Rotary& rot, const int64_t* shift, cudaStream_t stream) {
+    constexpr int V = 16 / sizeof(T);
+    const bool vector = lmkv_rotary_detail::vector_fits(rot.half, rot.interleaved, c.pool->head_dim, sizeof(T));
+    if (rot.interleaved)
+        return vector ? launch_shift_kernel<B, T, V, true>(c, rot, shift, stream)
+                      : launch_shift_kernel<B, T, 2, true>(c, rot, shift, stream);
+    return vector ? launch_shift_kernel<B, T, V, false>(c, rot, shift, stream)
+                  : launch_shift_kernel<B, T, 1, false>(c, rot, shift, stream);
+}
+
+template <class B>
+int launch_shift_typed(const Call& c, int32_t dtype, const lmkv_rotary_detail::Rotary& rot, const int64_t* shift,
+                       cudaStream_t stream) {
+    if (dtype == LMKV_BF16) return launch_shift<B, __nv_bfloat16>(c, rot, shift, stream);
+    if (dtype == LMKV_FP16) return launch_shift<B, __half>(c, rot, shift, stream);
+    return launch_shift<B, float>(c, rot, shift, stream);
+}
+
+// The scatter with keys turned by shift[r] positions; layer < 0: all layers.
+int shift_entry(const lmkv_pool_t* pool, int32_t dtype, const int32_t* block_table, int32_t max_blocks,
+                const int64_t* start, const int64_t* end, int32_t num_req, int32_t chunk_size,
+                int32_t save_unfull, void* const* chunk_ptrs, const int64_t* shift,
+                const lmkv_rotary_t* rotary, int32_t layer, int32_t* d_status, void* stream) {
+    const int rc0 = check_pool(pool);
+    if (rc0 != LMKV_OK) return rc0;
+    if (!lmkv_paged::type_fits(pool, dtype)) return LMKV_ERR_UNSUPPORTED;
+    if (num_req > 0 && shift == nullptr) return LMKV_ERR_INVALID_ARG;
+    lmkv_rotary_detail::Rotary rot;
+    const int rc1 = lmkv_rotary_detail::make_rotary(rotary, pool->head_dim, &rot);
+    if (rc1 != LMKV_OK) return rc1;
+    Call c{pool, block_table, max_blocks, start, end, num_req, chunk_size, save_unfull,
+           chunk_ptrs, d_status, 0, pool->num_layers, 1, 0, 0, nullptr};
+    if (layer >= 0) {
+        if (layer >= pool->num_layers) return LMKV_ERR_INVALID_ARG;
+        c.layer_lo = layer;
+        c.layer_n = 1;
+        c.prefetch_ahead = lsu_prefetch_ahead(reinterpret_cast<cudaStream_t>(stream));
+    }
+    c.parts = choose_parts(pool);
+    const int rc = validate(c);
+    if (rc != LMKV_OK || c.num_chunks == 0) return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (c.nonempty <= lmkv::kSmallBatch)
+        return launch_shift_typed<lmkv::ShiftBatchT<lmkv::kSmallBatch>>(c, dtype, rot, shift, s);
+    return launch_shift_typed<lmkv::ShiftBatchT<lmkv::kMaxReqPerLaunch>>(c, dtype, rot, shift, s);
 }
 
 // Layer-wise pipeline: per layer, wait on its ready event, move it, record its
@@ -695,6 +762,8 @@ void lmkv_internal_add_launches(int64_t n) { g_launches.fetch_add(n, std::memory
 
 int lmkv_internal_cuda_status(cudaError_t err) { return cuda_status(err); }
 
+int lmkv_internal_check_pool(const lmkv_pool_t* pool) { return check_pool(pool); }
+
 int lmkv_internal_list_chunks(const lmkv_pool_t* pool, const int32_t* block_table, int32_t max_blocks,
                               const int64_t* start, const int64_t* end, int32_t num_req,
                               int32_t chunk_size, int32_t save_unfull, std::vector<LmkvChunkRef>* out) {
@@ -866,6 +935,26 @@ int lmkv_scatter_layer(const lmkv_pool_t* pool, const int32_t* block_table, int3
                       save_unfull_chunk, chunk_ptrs, layer, d_status, stream);
 }
 
+int lmkv_scatter_chunks_shifted(const lmkv_pool_t* pool, int32_t dtype, const int32_t* block_table,
+                                int32_t max_blocks, const int64_t* start, const int64_t* end,
+                                int32_t num_req, int32_t chunk_size, int32_t save_unfull_chunk,
+                                void* const* chunk_ptrs, const int64_t* shift,
+                                const lmkv_rotary_t* rotary, int32_t* d_status, void* stream) {
+    return shift_entry(pool, dtype, block_table, max_blocks, start, end, num_req, chunk_size,
+                       save_unfull_chunk, chunk_ptrs, shift, rotary, -1, d_status, stream);
+}
+
+int lmkv_scatter_layer_shifted(const lmkv_pool_t* pool, int32_t dtype, const int32_t* block_table,
+                               int32_t max_blocks, const int64_t* start, const int64_t* end,
+                               int32_t num_req, int32_t chunk_size, int32_t save_unfull_chunk,
+                               void* const* chunk_ptrs, const int64_t* shift,
+                               const lmkv_rotary_t* rotary, int32_t layer, int32_t* d_status,
+                               void* stream) {
+    if (layer < 0) return LMKV_ERR_INVALID_ARG;
+    return shift_entry(pool, dtype, block_table, max_blocks, start, end, num_req, chunk_size,
+                       save_unfull_chunk, chunk_ptrs, shift, rotary, layer, d_status, stream);
+}
+
 int lmkv_store_layers(const lmkv_pool_t* pool, const int32_t* block_table, int32_t max_blocks,
                       const int64_t* start, const int64_t* end, int32_t num_req,
                       int32_t chunk_size, int32_t save_unfull_chunk, void* const* chunk_ptrs,
@@ -963,6 +1052,7 @@ const char* lmkv_status_string(int status) {
         case LMKV_ERR_TIMEOUT: return "bounded device wait gave up";
         case LMKV_ERR_SCRATCH_LIMIT: return "batch needs more than the built-in staging area";
         case LMKV_ERR_BAD_DATA: return "encoded blob inconsistent with its size (stream skipped)";
+        case LMKV_ERR_BAD_LENGTH: return "length outside the bounds of its call (clamped)";
         default: return "unknown status";
     }
 }

@@ -16,6 +16,9 @@ void lmkv_internal_add_launches(int64_t n);
 // and returns LMKV_ERR_CUDA.
 int lmkv_internal_cuda_status(cudaError_t err);
 
+// Validates a pool as every entry point does.
+int lmkv_internal_check_pool(const lmkv_pool_t* pool);
+
 // One chunk of a store / retrieve call: request row, first token, tokens.
 struct LmkvChunkRef {
     int32_t req;

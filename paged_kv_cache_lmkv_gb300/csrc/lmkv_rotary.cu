@@ -1,0 +1,258 @@
+// lmkv_rotary.cu -- rotary set-up (host) and the append of new tokens to the
+// pages of one layer.
+#include "lmkv_rotary.cuh"
+
+#include <cmath>
+
+namespace lmkv_rotary_detail {
+
+int make_rotary(const lmkv_rotary_t* in, int32_t head_dim, Rotary* out) {
+    if (in == nullptr || in->rot_dim < 2 || in->rot_dim % 2 != 0 || in->rot_dim > head_dim ||
+        in->rot_dim > 2 * LMKV_ROTARY_MAX_PAIRS || !std::isfinite(in->magnitude))
+        return LMKV_ERR_INVALID_ARG;
+    out->half = in->rot_dim / 2;
+    out->interleaved = in->interleaved != 0;
+    out->magnitude = (float)in->magnitude;
+    for (int i = 0; i < LMKV_ROTARY_MAX_PAIRS; ++i) {
+        out->turns[i] = 0;
+        if (i >= out->half) continue;
+        if (!std::isfinite(in->inv_freq[i])) return LMKV_ERR_INVALID_ARG;
+        double t = in->inv_freq[i] * 0.15915494309189533577;    // 1 / 2 pi
+        t -= std::floor(t);                                     // whole turns change nothing
+        const double scaled = std::ldexp(t, 64);
+        out->turns[i] = scaled >= 18446744073709551616.0 ? 0 : (uint64_t)scaled;
+    }
+    return LMKV_OK;
+}
+
+}  // namespace lmkv_rotary_detail
+
+namespace {
+
+using namespace lmkv_paged;
+using namespace lmkv_rotary_detail;
+
+struct Rows {
+    void* data;
+    int64_t token_stride;
+    int64_t head_stride;
+    static Rows of(const lmkv_rows_t* x) { return Rows{x->data, x->token_stride, x->head_stride}; }
+};
+
+struct AppendParams {
+    Layer layer;
+    Seqs seqs;
+    Rows q, k, v, q_out;
+    const int64_t* positions;
+    int32_t* status;
+    int32_t q_heads, kv_heads, head_dim;
+    Rotary rot;
+};
+
+constexpr int kThreads = 256;
+
+// kTok tokens a CTA.  A warp per token finds its request, position and page
+// row; the (cos, sin) of every (token, pair) go to shared memory once and
+// serve all heads; then each thread takes units of the heads (Units), the
+// same unit of each of the kTok tokens, so that their loads are in flight
+// together.  Bound by the rows' bytes: q read and written, k and v read and
+// written into the pages.
+template <class T, int V, bool kInterleaved, int kTok>
+__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p) {
+    __shared__ float2 cs[kTok][LMKV_ROTARY_MAX_PAIRS];
+    __shared__ int64_t page_off[kTok];
+    __shared__ int64_t position[kTok];
+    __shared__ int32_t live[kTok];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t tok0 = blockIdx.x * kTok;
+    uint8_t* const base = p.layer.base();
+    if (warp < kTok) {
+        const int32_t t = tok0 + warp;
+        int32_t r = 0;
+        if (t < p.seqs.num_tokens)
+            r = find_request(p.seqs.num_req, t, [&](int32_t i) { return p.seqs.q_start[i]; });
+        if (lane == 0) {
+            int64_t off = -1, pos = 0;
+            int32_t on = 0;
+            if (t < p.seqs.num_tokens) {
+                const Req q = load_req(p.seqs, r);
+                // rows past max_new of a request are rows of the call all the same
+                const int32_t end = min(max(p.seqs.q_start[r + 1], q.q0), p.seqs.num_tokens);
+                if (t >= q.q0 && t < end) {
+                    on = 1;
+                    const int32_t index = q.len - (end - q.q0) + (t - q.q0);
+                    pos = p.positions != nullptr ? p.positions[t] : (int64_t)index;
+                    const bool whole = q.len == p.seqs.kv_len[r] && q.q0 == p.seqs.q_start[r] &&
+                                       end == p.seqs.q_start[r + 1];
+                    if (base == nullptr) {
+                        report(p.status, LMKV_ERR_BAD_POINTER);
+                    } else if (!whole || index < 0) {
+                        // a clamped length says nothing about where the tokens go
+                        report(p.status, LMKV_ERR_BAD_LENGTH);
+                    } else {
+                        off = p.layer.token_offset(p.seqs.table + (int64_t)r * p.seqs.table_stride, index);
+                        if (off < 0) report(p.status, LMKV_ERR_BAD_BLOCK);
+                    }
+                }
+            }
+            page_off[warp] = off;
+            position[warp] = pos;
+            live[warp] = on;
+        }
+    }
+    __syncthreads();
+    const int half = p.rot.half;
+    for (int i = threadIdx.x; i < kTok * half; i += kThreads) {
+        const int t = i / half, pair = i - t * half;
+        const float2 w = cos_sin(p.rot.turns[pair], position[t]);
+        cs[t][pair] = make_float2(w.x * p.rot.magnitude, w.y * p.rot.magnitude);
+    }
+    __syncthreads();
+
+    using U = Units<T, V, kInterleaved>;
+    const int units = U::count(half, p.head_dim);
+    const int turning_slots = (p.q_heads + p.kv_heads) * units;
+    const int copy_units = p.head_dim / V;
+    const int slots = turning_slots + p.kv_heads * copy_units;
+    const int64_t half_bytes = p.layer.half_bytes();
+    for (int slot = threadIdx.x; slot < slots; slot += kThreads) {
+        if (slot < turning_slots) {
+            const int head = slot / units, u = slot - head * units;
+            const bool is_q = head < p.q_heads;
+            const Rows& in = is_q ? p.q : p.k;
+            const int h = is_q ? head : head - p.q_heads;
+            U x[kTok];
+#pragma unroll
+            for (int t = 0; t < kTok; ++t)
+                if (live[t] && (is_q || page_off[t] >= 0))
+                    x[t].load(static_cast<const T*>(in.data) + (int64_t)(tok0 + t) * in.token_stride +
+                                  (int64_t)h * in.head_stride, u, half);
+#pragma unroll
+            for (int t = 0; t < kTok; ++t) {
+                if (!live[t] || !(is_q || page_off[t] >= 0)) continue;
+                x[t].turn(cs[t], u, half);
+                T* out = is_q ? static_cast<T*>(p.q_out.data) + (int64_t)(tok0 + t) * p.q_out.token_stride +
+                                    (int64_t)h * p.q_out.head_stride
+                              : reinterpret_cast<T*>(base + page_off[t]) + (int64_t)h * p.head_dim;
+                x[t].store(out, u, half);
+            }
+        } else {
+            const int c = slot - turning_slots;
+            const int h = c / copy_units, u = c - h * copy_units;
+            Vec<T, V> x[kTok];
+#pragma unroll
+            for (int t = 0; t < kTok; ++t)
+                if (page_off[t] >= 0)
+                    x[t] = ld_vec<T, V>(static_cast<const T*>(p.v.data) + (int64_t)(tok0 + t) * p.v.token_stride +
+                                        (int64_t)h * p.v.head_stride + u * V);
+#pragma unroll
+            for (int t = 0; t < kTok; ++t)
+                if (page_off[t] >= 0)
+                    st_vec<T, V>(reinterpret_cast<T*>(base + page_off[t] + half_bytes) + (int64_t)h * p.head_dim +
+                                     u * V, x[t]);
+        }
+    }
+}
+
+template <class T, int V, bool kInterleaved>
+int launch_append(const AppendParams& p, void* stream) {
+    if (p.seqs.num_tokens <= 2 * 152)
+        return launch(append_kernel<T, V, kInterleaved, 1>, p.seqs.num_tokens, kThreads, 0, stream, 1, p);
+    return launch(append_kernel<T, V, kInterleaved, 4>, (p.seqs.num_tokens + 3) / 4, kThreads, 0, stream, 1, p);
+}
+
+template <class T>
+int append_typed(const AppendParams& p, bool vector, void* stream) {
+    constexpr int V = 16 / sizeof(T);
+    if (p.rot.interleaved)
+        return vector ? launch_append<T, V, true>(p, stream) : launch_append<T, 2, true>(p, stream);
+    return vector ? launch_append<T, V, false>(p, stream) : launch_append<T, 1, false>(p, stream);
+}
+
+bool finite_all(double a, double b, double c, double d, double e) {
+    return std::isfinite(a) && std::isfinite(b) && std::isfinite(c) && std::isfinite(d) && std::isfinite(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+int lmkv_rotary_init(lmkv_rotary_t* out, int32_t rot_dim, int32_t interleaved, double base, int32_t scaling,
+                     double factor, double low, double high, double original) {
+    const double two_pi = 6.283185307179586477;
+    if (out == nullptr || rot_dim < 2 || rot_dim % 2 != 0 || rot_dim > 2 * LMKV_ROTARY_MAX_PAIRS ||
+        !finite_all(base, factor, low, high, original) || !(base > 1.0) || !(factor >= 1.0))
+        return LMKV_ERR_INVALID_ARG;
+    if (scaling < LMKV_ROTARY_PLAIN || scaling > LMKV_ROTARY_RAMP) return LMKV_ERR_INVALID_ARG;
+    if ((scaling == LMKV_ROTARY_BANDS || scaling == LMKV_ROTARY_RAMP) &&
+        (!(low > 0.0) || !(low < high) || !(original > 0.0)))
+        return LMKV_ERR_INVALID_ARG;
+    if (scaling == LMKV_ROTARY_BASE) {
+        if (rot_dim <= 2) return LMKV_ERR_INVALID_ARG;
+        base *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
+        if (!std::isfinite(base)) return LMKV_ERR_INVALID_ARG;
+    }
+    lmkv_rotary_t r = {};
+    r.rot_dim = rot_dim;
+    r.interleaved = interleaved != 0;
+    r.magnitude = scaling == LMKV_ROTARY_RAMP ? 0.1 * std::log(factor) + 1.0 : 1.0;
+    // the (fractional) pair that makes n turns over `original` positions
+    auto pair_of = [&](double n) { return rot_dim * std::log(original / (n * two_pi)) / (2.0 * std::log(base)); };
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        const double f = std::pow(base, -2.0 * i / rot_dim);
+        double keep = 1.0;      // share of the unscaled frequency
+        if (scaling == LMKV_ROTARY_LINEAR) {
+            keep = 0.0;
+        } else if (scaling == LMKV_ROTARY_BANDS) {
+            keep = (original * f / two_pi - low) / (high - low);
+        } else if (scaling == LMKV_ROTARY_RAMP) {
+            const double first = pair_of(high), last = pair_of(low);     // first < last
+            keep = 1.0 - (i - first) / (last - first);
+        }
+        keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+        r.inv_freq[i] = f * keep + f / factor * (1.0 - keep);
+    }
+    *out = r;
+    return LMKV_OK;
+}
+
+int lmkv_append_layer(const lmkv_pool_t* pool, int32_t dtype, int32_t layer, const lmkv_batch_t* batch,
+                      int32_t num_q_heads, const lmkv_rows_t* q, const lmkv_rows_t* k, const lmkv_rows_t* v,
+                      const lmkv_rows_t* q_out, const int64_t* positions, const lmkv_rotary_t* rotary,
+                      int32_t* d_status, void* stream) {
+    int rc = lmkv_internal_check_pool(pool);
+    if (rc != LMKV_OK) return rc;
+    if (!type_fits(pool, dtype)) return LMKV_ERR_UNSUPPORTED;
+    if (layer < 0 || layer >= pool->num_layers) return LMKV_ERR_INVALID_ARG;
+    rc = check_batch(pool, batch, num_q_heads);
+    if (rc != LMKV_OK) return rc;
+    AppendParams p = {};
+    rc = make_rotary(rotary, pool->head_dim, &p.rot);
+    if (rc != LMKV_OK) return rc;
+    if (batch->num_req == 0 || batch->num_tokens == 0) return LMKV_OK;
+    const int32_t e = pool->elem_bytes;
+    if (!rows_ok(q, e) || !rows_ok(k, e) || !rows_ok(v, e) || !rows_ok(q_out, e)) return LMKV_ERR_INVALID_ARG;
+    p.layer = Layer::of(pool, layer);
+    p.seqs = Seqs::of(batch);
+    p.q = Rows::of(q);
+    p.k = Rows::of(k);
+    p.v = Rows::of(v);
+    p.q_out = Rows::of(q_out);
+    p.positions = positions;
+    p.status = d_status;
+    p.q_heads = num_q_heads;
+    p.kv_heads = pool->num_kv_heads;
+    p.head_dim = pool->head_dim;
+    // 16-byte vectors where every row starts on 16 bytes and they divide a head
+    bool vector = vector_fits(p.rot.half, p.rot.interleaved, p.head_dim, e);
+    for (const lmkv_rows_t* x : {q, k, v, q_out})
+        vector = vector && reinterpret_cast<uintptr_t>(x->data) % 16 == 0 && x->token_stride * e % 16 == 0 &&
+                 x->head_stride * e % 16 == 0;
+    if (dtype == LMKV_BF16) return append_typed<__nv_bfloat16>(p, vector, stream);
+    if (dtype == LMKV_FP16) return append_typed<__half>(p, vector, stream);
+    return append_typed<float>(p, vector, stream);
+}
+
+}  // extern "C"

@@ -28,6 +28,10 @@ ERR_BAD_POINTER = 6
 ERR_TIMEOUT = 7
 ERR_SCRATCH_LIMIT = 8
 ERR_BAD_DATA = 9
+ERR_BAD_LENGTH = 10
+BF16, FP16, FP32 = 0, 1, 2                  # lmkv_dtype_t
+ROTARY_MAX_PAIRS = 128
+ROTARY_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
 NOALLOC_STAGING_BYTES = 64 << 20
 CACHEGEN_BATCH = 256
 CACHEGEN_MAX_CHANNELS = 2048
@@ -47,6 +51,9 @@ ENTRY_POINTS = (
     "lmkv_cachegen_store_chunks", "lmkv_cachegen_retrieve_chunks",
     "lmkv_last_cuda_error", "lmkv_cuda_error_name",
     "lmkv_store_layers_overlapped", "lmkv_retrieve_layers_overlapped",
+    "lmkv_rotary_init", "lmkv_append_layer", "lmkv_scatter_chunks_shifted",
+    "lmkv_scatter_layer_shifted", "lmkv_attend_workspace_bytes", "lmkv_attend_layer",
+    "lmkv_weigh_layer", "lmkv_evict_layer",
 )
 
 
@@ -74,6 +81,23 @@ class CachegenLayout(ctypes.Structure):
     _fields_ = [("max1_offset", ctypes.c_uint64), ("cdf_offset", ctypes.c_uint64),
                 ("lengths_offset", ctypes.c_uint64), ("bytes_offset", ctypes.c_uint64),
                 ("max_bytes", ctypes.c_uint64)]
+
+
+class _RowsT(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class _BatchT(ctypes.Structure):
+    _fields_ = [("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("max_blocks", ctypes.c_int32),
+                ("num_req", ctypes.c_int32), ("num_tokens", ctypes.c_int32),
+                ("max_new", ctypes.c_int32), ("max_kv_len", ctypes.c_int32)]
+
+
+class _RotaryT(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("magnitude", ctypes.c_double), ("inv_freq", ctypes.c_double * ROTARY_MAX_PAIRS)]
 
 
 class _PoolT(ctypes.Structure):
@@ -141,7 +165,24 @@ def load() -> ctypes.CDLL:
         cg_pool = [pool_p, P, i32, P, P, i32, i32, i32, P, P, P, P, ctypes.c_uint64, P, P]
         lib.lmkv_cachegen_store_chunks.argtypes = cg_pool
         lib.lmkv_cachegen_retrieve_chunks.argtypes = cg_pool
-        for name in ("lmkv_count_chunks", "lmkv_enumerate_chunks", "lmkv_gather_chunks",
+        f64, f32 = ctypes.c_double, ctypes.c_float
+        rows_p, batch_p, rot_p = (ctypes.POINTER(t) for t in (_RowsT, _BatchT, _RotaryT))
+        lib.lmkv_rotary_init.argtypes = [rot_p, i32, i32, f64, i32, f64, f64, f64, f64]
+        lib.lmkv_append_layer.argtypes = [pool_p, i32, i32, batch_p, i32, rows_p, rows_p, rows_p, rows_p,
+                                          P, rot_p, P, P]
+        shifted = [pool_p, i32, P, i32, P, P, i32, i32, i32, P, P, rot_p]
+        lib.lmkv_scatter_chunks_shifted.argtypes = shifted + [P, P]
+        lib.lmkv_scatter_layer_shifted.argtypes = shifted + [i32, P, P]
+        lib.lmkv_attend_workspace_bytes.argtypes = [pool_p, i32, i32, i32, i32, i64, i32, P]
+        lib.lmkv_attend_layer.argtypes = [pool_p, i32, i32, batch_p, i32, rows_p, P, i64, f32, rows_p, P,
+                                          P, ctypes.c_uint64, P, P]
+        lib.lmkv_weigh_layer.argtypes = [pool_p, i32, i32, batch_p, i32, rows_p, P, f32, f32, P, P, i64, P, P]
+        lib.lmkv_evict_layer.argtypes = [pool_p, i32, P, i32, P, i32, i32, P, i64, i32, i32, i32, P, P, P,
+                                         i64, P, P]
+        for name in ("lmkv_rotary_init", "lmkv_append_layer", "lmkv_scatter_chunks_shifted",
+                     "lmkv_scatter_layer_shifted", "lmkv_attend_workspace_bytes", "lmkv_attend_layer",
+                     "lmkv_weigh_layer", "lmkv_evict_layer",
+                     "lmkv_count_chunks", "lmkv_enumerate_chunks", "lmkv_gather_chunks",
                      "lmkv_cachegen_default_bins", "lmkv_cachegen_layout",
                      "lmkv_cachegen_workspace_bytes", "lmkv_cachegen_encode", "lmkv_cachegen_decode",
                      "lmkv_cachegen_store_chunks", "lmkv_cachegen_retrieve_chunks",
@@ -687,6 +728,227 @@ class CachegenCodec:
         check(cachegen_decode(bptr, sizes, ntok, self.num_layers, self.channels, self.bins, cptr, ws,
                               status, stream), "lmkv_cachegen_decode")
         return chunks
+
+
+# ---- attention-side operators -------------------------------------------
+
+_DTYPES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
+
+
+class Rotary:
+    """A rotary encoding (lmkv_rotary_t): inv_freq[i] = base^(-2i / rot_dim), scaled as
+    lmkv_rotary_init describes, or the given inv_freq (radians per position)."""
+
+    def __init__(self, rot_dim: int, base: float = 10000.0, interleaved: bool = False,
+                 scaling: str = "plain", factor: float = 1.0, low: float = 1.0, high: float = 32.0,
+                 original: float = 4096.0, inv_freq=None, magnitude: float | None = None):
+        if scaling not in ROTARY_SCALINGS:
+            raise ValueError(f"scaling must be one of {sorted(ROTARY_SCALINGS)}")
+        self._struct = _RotaryT()
+        rc = load().lmkv_rotary_init(ctypes.byref(self._struct), int(rot_dim), int(interleaved), float(base),
+                                     ROTARY_SCALINGS[scaling], float(factor), float(low), float(high),
+                                     float(original))
+        if rc != OK:
+            raise LmkvError(rc, "lmkv_rotary_init")
+        if inv_freq is not None:
+            f = np.ascontiguousarray(inv_freq, dtype=np.float64)
+            if f.shape != (int(rot_dim) // 2,):
+                raise ValueError("inv_freq must hold rot_dim / 2 frequencies")
+            self._struct.inv_freq[:len(f)] = f.tolist()
+        if magnitude is not None:
+            self._struct.magnitude = float(magnitude)
+
+    @property
+    def rot_dim(self) -> int:
+        return self._struct.rot_dim
+
+    @property
+    def magnitude(self) -> float:
+        return self._struct.magnitude
+
+    @property
+    def inv_freq(self) -> np.ndarray:
+        return np.array(self._struct.inv_freq[:self._struct.rot_dim // 2], np.float64)
+
+    @property
+    def struct(self):
+        return ctypes.byref(self._struct)
+
+
+def _on(pool: Pool, **tensors) -> int:
+    """The pool's lmkv_dtype_t, after checking that every tensor is on the pool's
+    device and that this device is the current one (the library launches there)."""
+    t0 = pool.layers[0]
+    for name, t in tensors.items():
+        if t is not None and t.device != t0.device:
+            raise ValueError(f"{name} is on {t.device}, the pool on {t0.device}")
+    if t0.is_cuda and torch.cuda.current_device() != t0.device.index:
+        raise ValueError(f"the pool's device {t0.device} is not the current one")
+    dtype = _DTYPES.get(t0.dtype)
+    if dtype is None:
+        raise ValueError(f"no operators for a pool of {t0.dtype}")
+    return dtype
+
+
+def _rows(name: str, t: torch.Tensor, pool: Pool, heads: int, tokens: int | None = None) -> _RowsT:
+    """lmkv_rows_t of a [tokens][heads][head_dim] tensor of the pool's type, any
+    strides over tokens and heads."""
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != pool.head_dim:
+        raise ValueError(f"{name} must be [tokens][{heads}][{pool.head_dim}], got {list(shape)}")
+    if tokens is not None and shape[0] != tokens:
+        raise ValueError(f"{name} has {shape[0]} tokens, q has {tokens}")
+    if t.dtype != pool.layers[0].dtype:
+        raise ValueError(f"{name} is {t.dtype}, the pool {pool.layers[0].dtype}")
+    ts, hs, es = t.stride()
+    if es != 1:
+        raise ValueError(f"{name}: a head's elements must be contiguous")
+    return _RowsT(t.data_ptr(), ts, hs)
+
+
+def _whole(name: str, t: torch.Tensor, dtype, shape) -> int:
+    """Pointer of a contiguous tensor of this type and shape (None entries are free)."""
+    if t.dtype != dtype or t.dim() != len(shape) or not t.is_contiguous() or \
+            any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _batch(pool: Pool, block_table, q_start, kv_len, num_tokens, max_new, max_kv_len) -> _BatchT:
+    n = kv_len.shape[0]
+    cols = block_table.shape[-1]
+    return _BatchT(_whole("q_start", q_start, torch.int32, (n + 1,)),
+                   _whole("kv_len", kv_len, torch.int32, (n,)),
+                   _whole("block_table", block_table, torch.int32, (n, cols)), cols, n, num_tokens,
+                   num_tokens if max_new is None else int(max_new),
+                   cols * pool.block_size if max_kv_len is None else int(max_kv_len))
+
+
+def append_layer(pool, layer, block_table, q, k, v, q_out, q_start, kv_len, rotary, positions=None,
+                 status=None, stream=None) -> int:
+    """lmkv_append_layer: rotate q into q_out (may be q), rotate k and copy v into
+    the pages of the last q_start[r+1] - q_start[r] cached tokens of each
+    request.  q, k, v: [tokens][heads][head_dim]; returns the status code."""
+    dtype = _on(pool, block_table=block_table, q=q, k=k, v=v, q_out=q_out, q_start=q_start, kv_len=kv_len,
+                positions=positions, status=status)
+    tokens, heads = q.shape[0], q.shape[1]
+    a = [_rows("q", q, pool, heads), _rows("k", k, pool, pool.num_kv_heads, tokens),
+         _rows("v", v, pool, pool.num_kv_heads, tokens), _rows("q_out", q_out, pool, heads, tokens)]
+    b = _batch(pool, block_table, q_start, kv_len, tokens, None, None)
+    pos = None if positions is None else _whole("positions", positions, torch.int64, (tokens,))
+    return load().lmkv_append_layer(pool.struct, dtype, int(layer), ctypes.byref(b), heads,
+                                    *(ctypes.byref(x) for x in a), pos, rotary.struct, _ptr(status),
+                                    _stream_handle(stream))
+
+
+def _shifted_args(pool, block_table, start, end, chunk_size, save_unfull, chunk_ptrs, shift, rotary):
+    dtype = _on(pool, block_table=block_table, chunk_ptrs=chunk_ptrs)
+    a, keep = _common(pool, block_table, start, end)
+    sh = _i64_array(shift)
+    if sh.shape != keep[0].shape:
+        raise ValueError("shift must have one entry per request")
+    return (a[0], dtype, *a[1:], chunk_size, int(save_unfull), _ptr(chunk_ptrs), sh.ctypes.data,
+            rotary.struct), (keep, sh)
+
+
+def scatter_chunks_shifted(pool, block_table, start, end, chunk_size, save_unfull, chunk_ptrs, shift, rotary,
+                           status=None, stream=None) -> int:
+    """lmkv_scatter_chunks_shifted: scatter_chunks with request r's keys turned by
+    shift[r] positions."""
+    a, _keep = _shifted_args(pool, block_table, start, end, chunk_size, save_unfull, chunk_ptrs, shift, rotary)
+    return load().lmkv_scatter_chunks_shifted(*a, _ptr(status), _stream_handle(stream))
+
+
+def scatter_layer_shifted(pool, block_table, start, end, chunk_size, save_unfull, chunk_ptrs, shift, rotary,
+                          layer, status=None, stream=None) -> int:
+    """lmkv_scatter_layer_shifted: scatter_layer with request r's keys turned by
+    shift[r] positions."""
+    a, _keep = _shifted_args(pool, block_table, start, end, chunk_size, save_unfull, chunk_ptrs, shift, rotary)
+    return load().lmkv_scatter_layer_shifted(*a, int(layer), _ptr(status), _stream_handle(stream))
+
+
+def attend_workspace_bytes(pool, num_q_heads: int, num_tokens: int, num_req: int, max_new: int,
+                           prefix_len: int = 0, max_kv_len: int = 0) -> int:
+    """Bytes of workspace an attend_layer call of these bounds needs."""
+    out = ctypes.c_uint64(0)
+    check(load().lmkv_attend_workspace_bytes(pool.struct, int(num_q_heads), int(num_tokens), int(num_req),
+                                             int(max_new), int(prefix_len), int(max_kv_len),
+                                             ctypes.byref(out)), "lmkv_attend_workspace_bytes")
+    return out.value
+
+
+def attend_layer(pool, layer, q, out, q_start, kv_len, block_table, scale, workspace, prefix_table=None,
+                 prefix_len=0, lse=None, max_new=None, max_kv_len=None, status=None, stream=None) -> int:
+    """lmkv_attend_layer: attention of q [tokens][heads][head_dim] to the shared
+    prefix and the requests' own cached tokens, into out (and lse, float32
+    [tokens][heads]).  max_new and max_kv_len bound the lengths on the device
+    (default: the rows of q, the table's width); tight ones cost less.
+    workspace: uint8 of attend_workspace_bytes for the same bounds."""
+    dtype = _on(pool, q=q, out=out, q_start=q_start, kv_len=kv_len, block_table=block_table,
+                workspace=workspace, prefix_table=prefix_table, lse=lse, status=status)
+    tokens, heads = q.shape[0], q.shape[1]
+    rq, ro = _rows("q", q, pool, heads), _rows("out", out, pool, heads, tokens)
+    b = _batch(pool, block_table, q_start, kv_len, tokens, max_new, max_kv_len)
+    table = None
+    if prefix_len > 0:
+        if prefix_table is None or prefix_table.numel() * pool.block_size < prefix_len:
+            raise ValueError("prefix_table does not cover prefix_len")
+        table = _whole("prefix_table", prefix_table, torch.int32, (None,))
+    lp = None if lse is None else _whole("lse", lse, torch.float32, (tokens, heads))
+    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return load().lmkv_attend_layer(pool.struct, dtype, int(layer), ctypes.byref(b), heads, ctypes.byref(rq),
+                                    table, int(prefix_len), float(scale), ctypes.byref(ro), lp,
+                                    _ptr(workspace), size, _ptr(status), _stream_handle(stream))
+
+
+def weigh_layer(pool, layer, q, lse, q_start, kv_len, block_table, scale, scores, scores_out, decay=1.0,
+                max_new=None, max_kv_len=None, status=None, stream=None) -> int:
+    """lmkv_weigh_layer: scores_out = decay * scores + the attention weight every
+    own cached token receives from q, per KV head.  scores, scores_out:
+    float32 [requests][kv heads][stride]; scores_out may be scores, and scores
+    None when decay is 0.  max_kv_len defaults to what the table and the
+    scores have room for."""
+    dtype = _on(pool, q=q, lse=lse, q_start=q_start, kv_len=kv_len, block_table=block_table, scores=scores,
+                scores_out=scores_out, status=status)
+    tokens, heads = q.shape[0], q.shape[1]
+    rq = _rows("q", q, pool, heads)
+    if max_kv_len is None:
+        max_kv_len = min(block_table.shape[-1] * pool.block_size, scores_out.shape[-1])
+    b = _batch(pool, block_table, q_start, kv_len, tokens, max_new, max_kv_len)
+    shape = (b.num_req, pool.num_kv_heads, scores_out.shape[-1])
+    to = _whole("scores_out", scores_out, torch.float32, shape)
+    old = None if scores is None else _whole("scores", scores, torch.float32, shape)
+    return load().lmkv_weigh_layer(pool.struct, dtype, int(layer), ctypes.byref(b), heads, ctypes.byref(rq),
+                                   _whole("lse", lse, torch.float32, (tokens, heads)), float(scale),
+                                   float(decay), old, to, shape[2], _ptr(status), _stream_handle(stream))
+
+
+def evict_layer(pool, layer, block_table, kv_len, scores, sinks, recent, keep, new_len, kept_scores=None,
+                max_kv_len=None, status=None, stream=None) -> int:
+    """lmkv_evict_layer: keep the first `sinks`, the last `recent` and the highest
+    scores of each request's cached tokens, keep.shape[-1] in all, per KV head,
+    and move their rows to the front of the request's pages.  Writes keep
+    (int32 [requests][kv heads][budget]), new_len and kept_scores; the caller
+    then takes new_len as kv_len and frees the pages behind it.  max_kv_len
+    defaults to what the table and the scores have room for."""
+    n, cols = kv_len.shape[0], block_table.shape[-1]
+    t0 = pool.layers[0]
+    for name, t in (("block_table", block_table), ("kv_len", kv_len), ("scores", scores), ("keep", keep),
+                    ("new_len", new_len), ("kept_scores", kept_scores), ("status", status)):
+        if t is not None and t.device != t0.device:
+            raise ValueError(f"{name} is on {t.device}, the pool on {t0.device}")
+    if t0.is_cuda and torch.cuda.current_device() != t0.device.index:
+        raise ValueError(f"the pool's device {t0.device} is not the current one")
+    kh = pool.num_kv_heads
+    kp = None if kept_scores is None else _whole("kept_scores", kept_scores, torch.float32, (n, kh, None))
+    return load().lmkv_evict_layer(
+        pool.struct, int(layer), _whole("block_table", block_table, torch.int32, (n, cols)), cols,
+        _whole("kv_len", kv_len, torch.int32, (n,)), n,
+        min(cols * pool.block_size, scores.shape[-1]) if max_kv_len is None else int(max_kv_len),
+        _whole("scores", scores, torch.float32, (n, kh, None)), scores.shape[-1], keep.shape[-1], int(sinks),
+        int(recent), _whole("keep", keep, torch.int32, (n, kh, None)),
+        _whole("new_len", new_len, torch.int32, (n,)), kp, 0 if kp is None else kept_scores.shape[-1],
+        _ptr(status), _stream_handle(stream))
 
 
 def check(rc: int, what: str = "lmkv") -> None:
