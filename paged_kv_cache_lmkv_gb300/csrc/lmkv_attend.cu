@@ -12,6 +12,7 @@
 // its own rows; and a last kernel joins the parts.  Powers are of 2, with
 // scale * log2(e) folded into x.
 #include "lmkv_mma.cuh"
+#include "lmkv_tcgen05.cuh"
 
 #include <cmath>
 
@@ -33,6 +34,12 @@ struct Rows {
     }
 };
 
+// A request whose rows per KV head (new tokens x heads of the group) reach
+// kBigRows has its own pages attended to by the tile kernel, after the prefix
+// and in the same pass; the others', with too few rows for a tile of 128, by
+// the row kernel.
+constexpr int kBigRows = 64;
+
 struct AttendParams {
     Layer layer;
     Seqs seqs;
@@ -40,19 +47,34 @@ struct AttendParams {
     float* lse;
     const int32_t* prefix_table;
     int32_t* status;
-    float* part_o;          // [splits][rows][D]
-    float2* part_ml;        // [splits][rows]: m (powers of 2), l
-    float scale_log2;
+    // Partial results: m (powers of 2), l and the weighted sum of v.  First
+    // [prefix_parts][rows], row = token * q_heads + head, then
+    // [own_splits][own_rows], row = (r * own_cap + row of r) * kv_heads + KV head.
+    float* part_o;
+    float2* part_ml;
+    float scale_log2;       // of |scale|
+    int32_t scale_sign;     // -1, 0 or 1
     int32_t prefix_len;
     int32_t q_heads, kv_heads;
     int32_t rows;           // num_tokens * q_heads
-    int32_t prefix_tiles;   // row tiles of the prefix part
-    int32_t prefix_splits, prefix_span;   // splits of the prefix, keys in each
-    int32_t own_slots;      // row tile slots of the own part
+    int32_t row_tiles;      // row kernel: row tiles of the prefix part (0: the tile kernel has it)
+    int32_t prefix_parts, prefix_span;    // parts of the prefix (row kernel: keys in each)
+    int32_t tiles;          // tile kernel: row tiles (0: not launched)
+    int32_t own_cap;        // rows of a request that the row kernel takes at most
+    int32_t own_tiles;      // row tiles of that many rows
     int32_t own_splits, own_span;
-    bool direct;            // one part in all: it writes out and lse itself
+    bool big;               // a request may have kBigRows rows
+    bool own_final;         // the own part is all of a small request: no join
     bool q_pairs;           // q rows are 4-byte aligned
+    bool q_vec;             // q rows are 16-byte aligned
+    bool out_vec;           // out rows are 16-byte aligned
     FastDiv by_group;
+
+    __device__ __forceinline__ int64_t own_part(int32_t split, int32_t r, int32_t row, int32_t h) const {
+        return (int64_t)prefix_parts * rows +
+               (int64_t)split * ((int64_t)seqs.num_req * own_cap * kv_heads) +
+               ((int64_t)r * own_cap + row) * kv_heads + h;
+    }
 };
 
 constexpr int kRowTile = 16;      // rows of a tile: one mma.sync operand
@@ -61,35 +83,34 @@ constexpr int kChunk = 16;        // keys a warp takes at a time
 constexpr int kStages = 3;
 constexpr float kLn2 = 0.69314718055994530942f;
 
-// A tile's place in the batch.
+// A row tile's place in the batch.
 struct Tile {
     const int32_t* table;
     int32_t k0, k1;        // keys of this part
     int32_t h;             // KV head
-    int32_t part;          // index into the partial results
+    int32_t part;
+    int32_t r;             // request, or -1: rows of the whole batch
     int32_t t0, row0;      // row i of the tile is row row0 + i of the rows that begin at token t0
     int32_t nrows;         // rows from row0 on (may exceed the tile)
     int32_t limit0;        // row row0 + i sees keys below limit0 + (row0 + i) / group * causal
     int32_t causal;
 };
 
-// The tile of CTA `bid`; false when it has none.  Called by whole warps.
-// Row tiles of the own part: request r's rows begin at slot
-// floor(q_start[r] * group / 16) + r, which leaves room for every request's
-// last partial tile, so the slots need no scan over the requests.
-__device__ __forceinline__ bool find_tile(const AttendParams& p, int32_t bid, int rows_per_tile, Tile& t) {
+// The row tile of CTA `bid`; false when it has none.
+__device__ __forceinline__ bool find_tile(const AttendParams& p, int32_t bid, Tile& t) {
     const int32_t group = (int32_t)p.by_group.d;
-    const int32_t prefix_ctas = p.prefix_tiles * p.kv_heads * p.prefix_splits;
+    const int32_t prefix_ctas = p.row_tiles * p.kv_heads * p.prefix_parts;
     if (bid < prefix_ctas) {
-        const int32_t tile = bid % p.prefix_tiles;
-        const int32_t x = bid / p.prefix_tiles;
+        const int32_t tile = bid % p.row_tiles;
+        const int32_t x = bid / p.row_tiles;
         t.h = x % p.kv_heads;
         t.part = x / p.kv_heads;
+        t.r = -1;
         t.table = p.prefix_table;
         t.k0 = t.part * p.prefix_span;
         t.k1 = min(t.k0 + p.prefix_span, p.prefix_len);
         t.t0 = 0;
-        t.row0 = tile * rows_per_tile;
+        t.row0 = tile * kRowTile;
         const int32_t end = min(max(p.seqs.q_start[p.seqs.num_req], 0), p.seqs.num_tokens);
         t.nrows = end * group - t.row0;
         t.limit0 = p.prefix_len;
@@ -97,26 +118,26 @@ __device__ __forceinline__ bool find_tile(const AttendParams& p, int32_t bid, in
         return t.nrows > 0;
     }
     bid -= prefix_ctas;
+    // heads change fastest: the heads' CTAs of the same tokens read the same pages' rows
     t.h = bid % p.kv_heads;
-    const int32_t x = bid / p.kv_heads;
-    const int32_t slot = x % p.own_slots;
-    const int32_t split = x / p.own_slots;
-    auto first_slot = [&](int32_t i) { return (int32_t)((int64_t)p.seqs.q_start[i] * group / rows_per_tile) + i; };
-    const int32_t r = find_request(p.seqs.num_req, slot, first_slot);
-    const Req q = load_req(p.seqs, r);
-    if (!q.ok && (threadIdx.x & 31) == 0) report(p.status, LMKV_ERR_BAD_LENGTH);
-    t.part = p.prefix_splits + split;
-    t.row0 = (slot - first_slot(r)) * rows_per_tile;
+    int32_t x = bid / p.kv_heads;
+    const int32_t tile = x % p.own_tiles;
+    x /= p.own_tiles;
+    t.r = x % p.seqs.num_req;
+    t.part = x / p.seqs.num_req;
+    const Req q = load_req(p.seqs, t.r);
+    if (!q.ok && threadIdx.x == 0) report(p.status, LMKV_ERR_BAD_LENGTH);
+    t.row0 = tile * kRowTile;
     t.nrows = q.n * group - t.row0;
-    if (t.row0 < 0 || t.nrows <= 0) return false;
-    t.table = p.seqs.table + (int64_t)r * p.seqs.table_stride;
+    if (t.nrows <= 0 || (p.big && q.n * group >= kBigRows)) return false;
+    t.table = p.seqs.table + (int64_t)t.r * p.seqs.table_stride;
     t.t0 = q.q0;
     t.limit0 = q.len - q.n + 1;
     t.causal = 1;
-    const int32_t last = (int32_t)p.by_group.div((uint32_t)(t.row0 + min(t.nrows, rows_per_tile) - 1));
-    t.k0 = split * p.own_span;
+    const int32_t last = (int32_t)p.by_group.div((uint32_t)(t.row0 + min(t.nrows, kRowTile) - 1));
+    t.k0 = t.part * p.own_span;
     t.k1 = max(t.k0, min(t.k0 + p.own_span, t.limit0 + last));
-    return p.direct || t.k0 < q.len;
+    return p.own_final || t.k0 < q.len;
 }
 
 // Row tiles of 16 by mma.sync.  Bound by the bytes of K and V: with a few rows
@@ -132,13 +153,13 @@ attend_rows_kernel(const __grid_constant__ AttendParams p) {
     constexpr int kVecs = kRowBytes / 16;            // 16-byte pieces of a row
     constexpr int kTileBytes = kChunk * kRowBytes;   // K (or V) rows of a stage
     constexpr int kSteps = D / 16;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ float2 ml[kWarps][kRowTile];
     pdl_launch_dependents();
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     Tile t;
-    if (!find_tile(p, blockIdx.x, kRowTile, t)) return;
+    if (!find_tile(p, blockIdx.x, t)) return;
     const uint8_t* base = p.layer.base();
     if (base == nullptr) {
         if (threadIdx.x == 0) report(p.status, LMKV_ERR_BAD_POINTER);
@@ -193,6 +214,7 @@ attend_rows_kernel(const __grid_constant__ AttendParams p) {
         return mask;
     };
 
+    const float signed_scale = p.scale_log2 * (float)p.scale_sign;
     float o[D / 8][4];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -239,7 +261,7 @@ attend_rows_kernel(const __grid_constant__ AttendParams p) {
                         const int at = n * 8 + j;
                         const bool seen = key0 + at < limit[r] && ((mask >> (at + (lane & 3) * 2)) & 1);
                         float& x = sc[n][2 * r + j];
-                        x = seen ? x * p.scale_log2 : -INFINITY;
+                        x = seen ? x * signed_scale : -INFINITY;
                         top = fmaxf(top, x);
                     }
                 top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
@@ -315,7 +337,7 @@ attend_rows_kernel(const __grid_constant__ AttendParams p) {
         const int32_t n = (int32_t)p.by_group.div((uint32_t)(t.row0 + rr));
         const int32_t tok = t.t0 + n, head = t.h * group + (t.row0 + rr - n * group);
         const int32_t row = tok * p.q_heads + head;
-        if (p.direct) {
+        if (t.r >= 0 && p.own_final) {
             const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
             T* dst = p.out.row<T>(tok, head) + c;
             dst[0] = Elem<T>::from_float(acc.x * inv);
@@ -324,31 +346,489 @@ attend_rows_kernel(const __grid_constant__ AttendParams p) {
             dst[3] = Elem<T>::from_float(acc.w * inv);
             if (c == 0 && p.lse != nullptr) p.lse[row] = (mu + log2f(sum)) * kLn2;
         } else {
-            const int64_t at = (int64_t)t.part * p.rows + row;
+            const int64_t at = t.r < 0 ? (int64_t)t.part * p.rows + row : p.own_part(t.part, t.r, t.row0 + rr, t.h);
             *reinterpret_cast<float4*>(p.part_o + at * D + c) = acc;
             if (c == 0) p.part_ml[at] = make_float2(top, sum);
         }
     }
 }
 
-// Joins the parts of every row: a warp per (token, query head).
+// ---- tiles of 128 rows on the tensor core -------------------------------
+
+using namespace lmkv_tc;
+
+constexpr int kTileRows = 256;        // two tiles of 128 rows share every K and V block
+constexpr int kBlock = 128;           // keys of a block
+constexpr int kTileThreads = 384;     // softmax 2 x 128, loads 64, products 1 (of 64)
+constexpr int kLoadWarps = 2;
+constexpr int kMaxSegs = 8;           // the prefix and every big request that 256 rows can touch
+constexpr int kMaskSlots = 8;
+
+// Keys in a row's order: the prefix, then each big request of the tile.
+struct Seg {
+    const int32_t* table;
+    int32_t end;       // keys [0, end)
+    int32_t first;     // number of its first block
+    int32_t q0, n;     // its tokens; the prefix: n < 0
+    int32_t limit0;    // token q0 + i sees keys below limit0 + i
+};
+
+template <int D>
+struct TileShape {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kHalfBytes = 128 * 128;
+    static constexpr int kStageBytes = kHalves * kHalfBytes;       // 128 rows of K, V or q
+    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr int kLag = kStages - 2;                       // loads in flight behind the newest
+    static constexpr int kSmem = (2 + kStages) * kStageBytes;
+};
+
+// Rows of all requests, (token, head of the group) in token order, 256 to a
+// CTA, against the prefix and then against the own pages of the big requests
+// among them.  Products and powers are both near their limits, so the two
+// tiles of 128 rows take turns: while the tensor core works on one tile's
+// weights x V and next q x K, the other tile's softmax runs.
+//   warps 0-3, 4-7   softmax of tile 0, 1: a thread holds a row.  Scores come
+//                    from tensor memory, weights go back over them as the next
+//                    product's first operand; the output stays in tensor
+//                    memory until the end.
+//   warps 8-9        K and V blocks of 128 keys, cp.async row by row (pages
+//                    may end anywhere), through a ring in shared memory that
+//                    both tiles read
+//   warp 10          one thread issues every product
+// The running maximum may lag: an output is rescaled only when a row's
+// maximum has grown by more than 2^8 since, else weights simply exceed 1 (by
+// 2^8 at most), which costs nothing in fp32 sums or floating-point weights.
+// Tensor memory: scores of tile 0, 1 at columns 0, 128; outputs at 256, 384.
 template <class T, int D>
+__global__ void __launch_bounds__(kTileThreads, 1)
+attend_tiles_kernel(const __grid_constant__ AttendParams p) {
+    using S = TileShape<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ uint64_t bars[2 * S::kStages + 6];
+    __shared__ uint32_t tmem_base;
+    __shared__ int gave_up;
+    __shared__ Seg segs[kMaxSegs];
+    __shared__ int32_t num_segs, num_blocks;
+    __shared__ uint4 key_mask[kMaskSlots];
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t full = smem_u32(bars), empty = full + 8 * S::kStages, s_full = empty + 8 * S::kStages,
+                   p_ready = s_full + 16, o_full = p_ready + 16;
+    const uint32_t q_smem = smem_u32(smem), kv_smem = q_smem + 2 * S::kStageBytes;
+    if (tid == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(full + 8 * i, kLoadWarps);
+            mbar_init(empty + 8 * i, 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(s_full + 8 * t, 1);
+            mbar_init(p_ready + 8 * t, 128);
+            mbar_init(o_full + 8 * t, 1);
+        }
+        gave_up = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 10) tmem_alloc<512>(smem_u32(&tmem_base));
+    pdl_wait();
+
+    const int32_t group = (int32_t)p.by_group.d;
+    const int32_t tile = blockIdx.x % p.tiles;
+    const int32_t h = blockIdx.x / p.tiles % p.kv_heads;
+    const int32_t part = blockIdx.x / p.tiles / p.kv_heads;
+    const int32_t live_tokens = min(max(p.seqs.q_start[p.seqs.num_req], 0), p.seqs.num_tokens);
+    const int32_t row0 = tile * kTileRows;
+    const int32_t live_rows = live_tokens * group;
+    uint8_t* const base = p.layer.base();
+    if (warp == 0 && row0 < live_rows) {
+        const int32_t t_first = (int32_t)p.by_group.div((uint32_t)row0);
+        const int32_t t_last = (int32_t)p.by_group.div((uint32_t)(min(row0 + kTileRows, live_rows) - 1));
+        int32_t count = 0;
+        if (p.prefix_len > 0) {
+            if (lane == 0) segs[0] = Seg{p.prefix_table, p.prefix_len, 0, 0, -1, 0};
+            count = 1;
+        }
+        if (p.big) {
+            auto key = [&](int32_t i) { return p.seqs.q_start[i]; };
+            const int32_t r_first = find_request(p.seqs.num_req, t_first, key);
+            const int32_t r_last = find_request(p.seqs.num_req, t_last, key);
+            for (int32_t r0 = r_first; r0 <= r_last; r0 += 32) {
+                const int32_t r = r0 + lane;
+                bool on = false;
+                Seg s = {};
+                if (r <= r_last) {
+                    const Req q = load_req(p.seqs, r);
+                    if (!q.ok) report(p.status, LMKV_ERR_BAD_LENGTH);
+                    on = q.n * group >= kBigRows && q.q0 <= t_last && q.q0 + q.n > t_first;
+                    s.table = p.seqs.table + (int64_t)r * p.seqs.table_stride;
+                    s.q0 = q.q0;
+                    s.n = q.n;
+                    s.limit0 = q.len - q.n + 1;
+                    s.end = max(0, s.limit0 + min(q.n - 1, t_last - q.q0));
+                }
+                const uint32_t votes = __ballot_sync(0xFFFFFFFFu, on);
+                const int32_t at = count + __popc(votes & ((1u << lane) - 1));
+                if (on && at < kMaxSegs) segs[at] = s;       // lengths that overlap could give more
+                count = min(count + __popc(votes), kMaxSegs);
+            }
+        }
+        __syncwarp();
+        if (lane == 0) {
+            int32_t blocks = 0;
+            for (int32_t i = 0; i < count; ++i) {
+                segs[i].first = blocks;
+                blocks += (segs[i].end + kBlock - 1) / kBlock;
+            }
+            num_segs = count;
+            num_blocks = base == nullptr ? 0 : blocks;
+            if (base == nullptr) report(p.status, LMKV_ERR_BAD_POINTER);
+        }
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = tmem_base;
+    if (row0 < live_rows) {
+        const int32_t nseg = num_segs;
+        const int32_t b0 = (int32_t)((int64_t)num_blocks * part / p.prefix_parts);
+        const int32_t b1 = (int32_t)((int64_t)num_blocks * (part + 1) / p.prefix_parts);
+        const int tiles = live_rows - row0 > 128 ? 2 : 1;
+
+        if (warp < 8) {
+            const int t = warp >> 2;
+            const int32_t R = row0 + tid;
+            const bool live = R < live_rows;
+            const int32_t tok = (int32_t)p.by_group.div((uint32_t)(live ? R : 0));
+            const int32_t head = h * group + (live ? R - tok * group : 0);
+            if (t < tiles) {
+                // my row of q, negated for a negative scale, into shared memory
+                const T* src = p.q.row<T>(tok, head);
+                const uint32_t dst = q_smem + t * S::kStageBytes + (tid & 127) * 128;
+                const uint32_t flip = p.scale_sign < 0 ? 0x80008000u : 0u, all = p.scale_sign == 0 || !live ? 0u : ~0u;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    int4 v;
+                    if (p.q_vec) {
+                        v = *reinterpret_cast<const int4*>(src + c * 8);
+                    } else {
+                        v.x = (int)load_pair(src + c * 8, p.q_pairs);
+                        v.y = (int)load_pair(src + c * 8 + 2, p.q_pairs);
+                        v.z = (int)load_pair(src + c * 8 + 4, p.q_pairs);
+                        v.w = (int)load_pair(src + c * 8 + 6, p.q_pairs);
+                    }
+                    const uint32_t at = dst + (c >> 3) * S::kHalfBytes + (((c & 7) ^ (tid & 7)) << 4);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"((v.x ^ flip) & all),
+                                 "r"((v.y ^ flip) & all), "r"((v.z ^ flip) & all), "r"((v.w ^ flip) & all)
+                                 : "memory");
+                }
+                fence_async_shared();
+                mbar_arrive(p_ready + 8 * t);          // phase 0: q is there
+
+                int32_t own = -1;
+                for (int32_t i = 0; i < nseg; ++i)
+                    if (segs[i].n >= 0 && tok >= segs[i].q0 && tok < segs[i].q0 + segs[i].n) own = i;
+                const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21);     // lane 32 * (warp % 4)
+                const uint32_t s_at = lane_base + t * 128, o_at = lane_base + 256 + t * 128;
+                const float scale = p.scale_log2;
+                float m = -INFINITY;              // what weights are relative to, in units of raw scores
+                float2 l2 = make_float2(0.f, 0.f);
+                int32_t si = 0;
+                bool ok = true;
+                for (int32_t b = b0; b < b1; ++b) {
+                    while (si + 1 < nseg && b >= segs[si + 1].first) ++si;
+                    const Seg& sg = segs[si];
+                    const int32_t k = (b - sg.first) * kBlock;
+                    int32_t seen = min(sg.end - k, kBlock);
+                    if (sg.n >= 0) seen = si == own ? min(seen, sg.limit0 + (tok - sg.q0) - k) : 0;
+                    if (!mbar_wait(s_full + 8 * t, (b - b0) & 1, &gave_up)) {
+                        ok = false;
+                        break;
+                    }
+                    fence_after_sync();
+                    const uint4 mask = key_mask[(b - b0) % kMaskSlots];
+                    const uint32_t words[4] = {mask.x, mask.y, mask.z, mask.w};
+                    const bool whole = __all_sync(0xFFFFFFFFu, seen >= kBlock && (mask.x & mask.y & mask.z & mask.w) == ~0u);
+                    // scores of 32 keys, those not seen as -infinity
+                    auto take = [&](uint32_t (&x)[32], int i) {
+                        if (whole) return;
+                        const int32_t n = seen - 32 * i;
+                        const uint32_t bits = words[i] & (n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (!((bits >> j) & 1)) x[j] = 0xFF800000u;
+                    };
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 4; i += 2) {
+                        uint32_t x[32], y[32];
+                        tmem_ld32(x, s_at + 32 * i);
+                        tmem_ld32(y, s_at + 32 * i + 32);
+                        wait_ld();
+                        loaded(x);
+                        loaded(y);
+                        take(x, i);
+                        take(y, i + 1);
+                        float a = -INFINITY, c = -INFINITY;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            a = fmaxf(a, __uint_as_float(x[j]));
+                            c = fmaxf(c, __uint_as_float(y[j]));
+                        }
+                        mx = fmaxf(mx, fmaxf(a, c));
+                    }
+                    // weights are relative to m; m moves when it would be exceeded by more than 2^8
+                    const bool grow = mx > m && !((mx - m) * scale <= 8.f);
+                    if (__any_sync(0xFFFFFFFFu, grow)) {
+                        const float mn = grow ? mx : m;
+                        const float f = grow && m != -INFINITY ? exp2_fast((m - mn) * scale) : grow ? 0.f : 1.f;
+                        m = mn;
+                        l2.x *= f;
+                        l2.y *= f;
+                        if (b > b0) {
+                            // the scores were there, so the product before them, into the output, is done
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 16) tmem_scale16(o_at + c, f);
+                        }
+                    }
+                    const float neg = m == -INFINITY ? 0.f : -m * scale;
+                    const float2 sc2 = make_float2(scale, scale), ng2 = make_float2(neg, neg);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t x[32], w[16];
+                        tmem_ld32(x, s_at + 32 * i);
+                        wait_ld();
+                        loaded(x);
+                        take(x, i);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            float2 e = fma2(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), sc2, ng2);
+                            e.x = exp2_fast(e.x);
+                            e.y = exp2_fast(e.y);
+                            l2 = add2(l2, e);
+                            // weights are rounded to T for the product with V, the sum takes them whole
+                            w[j] = Elem<T>::pack(e.x, e.y);
+                        }
+                        tmem_st16(s_at + 16 * i, w);       // over scores that have been read
+                    }
+                    wait_st();
+                    fence_before_sync();
+                    mbar_arrive(p_ready + 8 * t);
+                }
+                // my row of the result
+                const float l = l2.x + l2.y;
+                if (ok && b1 > b0) ok = mbar_wait(o_full + 8 * t, 0, &gave_up);
+                if (ok) {
+                    fence_after_sync();
+                    // without a prefix a small request's rows have nothing here
+                    const bool wanted = live && (own >= 0 || p.prefix_len > 0);
+                    const bool final = own >= 0 && p.prefix_parts == 1;
+                    const int64_t row = (int64_t)tok * p.q_heads + head;
+                    const int64_t at = (int64_t)part * p.rows + row;
+                    const float m2 = m == -INFINITY ? -INFINITY : m * scale;
+                    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+                    T* const out = p.out.row<T>(tok, head);
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t y[32];
+                        if (b1 > b0) {
+                            tmem_ld32(y, o_at + 32 * c);
+                            wait_ld();
+                            loaded(y);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) y[j] = 0u;
+                        }
+                        if (!wanted) continue;
+                        if (final) {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 8) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    w[i] = Elem<T>::pack(__uint_as_float(y[j + 2 * i]) * inv,
+                                                         __uint_as_float(y[j + 2 * i + 1]) * inv);
+                                T* dst = out + 32 * c + j;
+                                if (p.out_vec) {
+                                    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+                                } else {
+                                    uint16_t* d16 = reinterpret_cast<uint16_t*>(dst);
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        d16[2 * i] = (uint16_t)w[i];
+                                        d16[2 * i + 1] = (uint16_t)(w[i] >> 16);
+                                    }
+                                }
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 4)
+                                *reinterpret_cast<uint4*>(p.part_o + at * D + 32 * c + j) =
+                                    make_uint4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+                        }
+                    }
+                    if (wanted && final && p.lse != nullptr)
+                        p.lse[row] = ((m == -INFINITY ? 0.f : m2) + log2f(l)) * kLn2;
+                    if (wanted && !final) p.part_ml[at] = make_float2(m2, l);
+                }
+            }
+        } else if (warp < 8 + kLoadWarps) {
+            const int w = warp - 8;
+            constexpr int kVecs = D / 8;             // 16-byte pieces of a row
+            constexpr int kRowsPer = 32 / kVecs;     // rows of a warp-wide copy
+            constexpr int kGroups = kBlock / 32 / kLoadWarps;     // groups of 32 rows of this warp
+            const int64_t half_bytes = p.layer.half_bytes();
+            const int c = lane % kVecs, rsub = lane / kVecs;
+            const int64_t piece = (int64_t)h * (D * 2) + c * 16;
+            int32_t si = 0, item = 0;
+            int64_t next[kGroups];
+            auto lookup = [&](int32_t b) {
+                while (si + 1 < nseg && b >= segs[si + 1].first) ++si;
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    const int32_t tok = (b - segs[si].first) * kBlock + (w * kGroups + g) * 32 + lane;
+                    next[g] = tok < segs[si].end ? p.layer.token_offset(segs[si].table, tok) : -2;
+                }
+            };
+            bool ok = true;
+            auto signal = [&](int32_t i) {           // my loads of item i are done
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full + 8 * (i % S::kStages));
+            };
+            if (b0 < b1) lookup(b0);
+            for (int32_t b = b0; b < b1 && ok; ++b) {
+                int64_t off[kGroups];
+                uint32_t there[kGroups];
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    off[g] = next[g];
+                    if (off[g] == -1) report(p.status, LMKV_ERR_BAD_BLOCK);
+                    there[g] = __ballot_sync(0xFFFFFFFFu, off[g] >= 0);
+                }
+                if (b + 1 < b1) lookup(b + 1);
+#pragma unroll 1
+                for (int kv = 0; kv < 2; ++kv, ++item) {
+                    const int st = item % S::kStages;
+                    if (item >= S::kStages && !mbar_wait(empty + 8 * st, (item / S::kStages - 1) & 1, &gave_up)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t dst0 = kv_smem + st * S::kStageBytes + (c >> 3) * S::kHalfBytes;
+                    const uint8_t* const from = base + piece + (kv ? half_bytes : 0);
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g) {
+                        if (kv == 0 && lane == 0)
+                            reinterpret_cast<uint32_t*>(&key_mask[(b - b0) % kMaskSlots])[w * kGroups + g] = there[g];
+                        const uint32_t dst = dst0 + (w * kGroups + g) * 32 * 128;
+#pragma unroll
+                        for (int v = 0; v < kVecs; ++v) {
+                            const int row = v * kRowsPer + rsub;
+                            const int64_t o = __shfl_sync(0xFFFFFFFFu, off[g], row);
+                            cp_async16(dst + row * 128 + (((c & 7) ^ (row & 7)) << 4), o >= 0 ? from + o : base, o >= 0);
+                        }
+                    }
+                    cp_commit();
+                    if (item >= S::kLag) {
+                        cp_wait<S::kLag>();
+                        signal(item - S::kLag);
+                    }
+                }
+            }
+            cp_wait<0>();
+            if (ok)
+                for (int32_t i = max(0, item - S::kLag); i < item; ++i) signal(i);
+        } else {
+            if (warp == 10 && lane == 0 && b1 > b0) {
+                constexpr uint32_t qk = instr_desc<T, kBlock, false>(), pv = instr_desc<T, D, true>();
+                const int32_t blocks = b1 - b0;
+                auto stage = [&](int32_t item) { return kv_smem + (item % S::kStages) * S::kStageBytes; };
+                auto loaded_item = [&](int32_t item) {
+                    return mbar_wait(full + 8 * (item % S::kStages), (item / S::kStages) & 1, &gave_up);
+                };
+                auto scores = [&](int t, int32_t j) {          // tile t's q x K of block j
+                    const uint32_t a = q_smem + t * S::kStageBytes, k = stage(2 * j);
+#pragma unroll
+                    for (int s = 0; s < D / 16; ++s) {
+                        const uint32_t at = (s >> 2) * S::kHalfBytes + (s & 3) * 32;
+                        mma_ss(tmem + t * 128, desc_k_major(a + at), desc_k_major(k + at), qk, s > 0);
+                    }
+                    mma_commit(s_full + 8 * t);
+                };
+                bool ok = loaded_item(0);
+                for (int t = 0; t < tiles && ok; ++t) {
+                    ok = mbar_wait(p_ready + 8 * t, 0, &gave_up);
+                    if (ok) scores(t, 0);
+                }
+                if (ok) mma_commit(empty);                     // item 0's stage
+                for (int32_t j = 0; j < blocks && ok; ++j) {
+                    ok = loaded_item(2 * j + 1) && (j + 1 >= blocks || loaded_item(2 * j + 2));
+                    for (int t = 0; t < tiles && ok; ++t) {
+                        ok = mbar_wait(p_ready + 8 * t, (j + 1) & 1, &gave_up);
+                        if (!ok) break;
+                        fence_after_sync();
+                        const uint32_t v = stage(2 * j + 1);
+#pragma unroll
+                        for (int s = 0; s < kBlock / 16; ++s)
+                            mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * s, desc_n_major(v + s * 2048, S::kHalfBytes),
+                                   pv, j > 0 || s > 0);
+                        if (t == tiles - 1) mma_commit(empty + 8 * ((2 * j + 1) % S::kStages));
+                        // issued behind the product that reads the weights from the same columns
+                        if (j + 1 < blocks) scores(t, j + 1);
+                        else mma_commit(o_full + 8 * t);
+                    }
+                    if (ok && j + 1 < blocks) mma_commit(empty + 8 * ((2 * j + 2) % S::kStages));
+                }
+            }
+        }
+    }
+    __syncwarp();
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    if (tid == 0 && gave_up) report(p.status, LMKV_ERR_TIMEOUT);
+    if (warp == 10) tmem_free<512>(tmem);
+}
+
+// Joins the parts of the rows that have more than one: a warp per row, of all
+// rows (kOwnRows false) or of the small requests' only.
+template <class T, int D, bool kOwnRows>
 __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ AttendParams p) {
     constexpr int kPer = D / 32;
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31;
-    const int32_t row = blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (row >= p.rows) return;
-    const int32_t tok = row / p.q_heads, head = row - tok * p.q_heads;
-    const int32_t r = find_request(p.seqs.num_req, tok, [&](int32_t i) { return p.seqs.q_start[i]; });
-    const Req q = load_req(p.seqs, r);
-    if (!q.ok && lane == 0) report(p.status, LMKV_ERR_BAD_LENGTH);
-    if (tok < q.q0 || tok >= q.q0 + q.n) return;       // a padded row
-    const int32_t parts = p.prefix_splits + (q.len + p.own_span - 1) / p.own_span;
+    const int32_t group = (int32_t)p.by_group.d;
+    int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    int32_t r, row_of_r, h;
+    Req q;
+    if (kOwnRows) {
+        if (i >= (int64_t)p.seqs.num_req * p.own_cap * p.kv_heads) return;
+        h = (int32_t)(i % p.kv_heads);
+        i /= p.kv_heads;
+        r = (int32_t)(i / p.own_cap);
+        row_of_r = (int32_t)(i % p.own_cap);
+        q = load_req(p.seqs, r);
+        if (row_of_r >= q.n * group) return;
+    } else {
+        if (i >= p.rows) return;
+        const int32_t tok = (int32_t)(i / p.q_heads), head = (int32_t)(i % p.q_heads);
+        r = find_request(p.seqs.num_req, tok, [&](int32_t k) { return p.seqs.q_start[k]; });
+        q = load_req(p.seqs, r);
+        if (!q.ok && lane == 0) report(p.status, LMKV_ERR_BAD_LENGTH);
+        if (tok < q.q0 || tok >= q.q0 + q.n) return;       // a padded row
+        h = head / group;
+        row_of_r = (tok - q.q0) * group + (head - h * group);
+    }
+    const bool big = p.big && q.n * group >= kBigRows;
+    if (big ? p.prefix_parts == 1 : p.own_final) return;   // written already
+    const int32_t n = (int32_t)p.by_group.div((uint32_t)row_of_r);
+    const int32_t tok = q.q0 + n, head = h * group + (row_of_r - n * group);
+    const int64_t row = (int64_t)tok * p.q_heads + head;
+    const int32_t shared = big || p.prefix_len > 0 ? p.prefix_parts : 0;
+    const int32_t parts = shared + (big ? 0 : (q.len + p.own_span - 1) / p.own_span);
     float top = -INFINITY, sum = 0.f, acc[kPer] = {};
     for (int32_t s = 0; s < parts; ++s) {
-        const int64_t at = (int64_t)s * p.rows + row;
+        const int64_t at = s < shared ? (int64_t)s * p.rows + row : p.own_part(s - shared, r, row_of_r, h);
         const float2 v = p.part_ml[at];
         float x[kPer];
         const float* src = p.part_o + at * D + lane * kPer;
@@ -360,12 +840,12 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
         top = mn;
         sum = sum * fa + v.y * fb;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) acc[i] = acc[i] * fa + x[i] * fb;
+        for (int k = 0; k < kPer; ++k) acc[k] = acc[k] * fa + x[k] * fb;
     }
     const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
     T* dst = p.out.row<T>(tok, head) + lane * kPer;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) dst[i] = Elem<T>::from_float(acc[i] * inv);
+    for (int k = 0; k < kPer; ++k) dst[k] = Elem<T>::from_float(acc[k] * inv);
     if (lane == 0 && p.lse != nullptr)
         p.lse[row] = ((top == -INFINITY ? 0.f : top) + log2f(sum)) * kLn2;
 }
@@ -373,16 +853,17 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
 // ---- host ---------------------------------------------------------------
 
 struct Plan {
-    int32_t prefix_tiles, prefix_splits, prefix_span;
-    int32_t own_slots, own_splits, own_span;
-    bool direct;
-    int64_t rows;
+    int32_t row_tiles, tiles, prefix_parts, prefix_span;
+    int32_t own_cap, own_tiles, own_splits, own_span;
+    bool big, own_final, join;
+    int64_t rows, own_rows;
     uint64_t o_bytes, bytes;
 };
 
 constexpr int32_t kSms = 152;
 
-// Splits: enough CTAs for two on every SM, none below 128 keys.
+// Splits of `keys` keys over `ctas` CTAs each: enough for four on every SM,
+// none below 128 keys.
 void split(int64_t ctas, int32_t keys, int32_t* splits, int32_t* span) {
     const int64_t want = (4 * kSms + ctas - 1) / ctas;
     const int64_t most = (keys + 127) / 128;
@@ -393,24 +874,52 @@ void split(int64_t ctas, int32_t keys, int32_t* splits, int32_t* span) {
     *splits = (int32_t)((keys + s - 1) / s);
 }
 
-Plan make_plan(const lmkv_pool_t* pool, int32_t q_heads, int32_t num_tokens, int32_t num_req, int32_t prefix_len,
-               int32_t max_kv_len) {
+// Parts of the tile kernel's blocks: the number that leaves the fewest rounds
+// of one CTA per SM, a part's cost being its blocks and the writing and
+// joining of its rows (about two blocks' time).
+int32_t tile_parts(int64_t ctas, int64_t blocks) {
+    int32_t best = 1;
+    double best_cost = 0;
+    for (int32_t n = 1; n <= 64 && n <= blocks; ++n) {
+        const double rounds = (double)((ctas * n + kSms - 1) / kSms);
+        const double cost = rounds * ((double)((blocks + n - 1) / n) + (n > 1 ? 2.0 : 0.0)) + (n > 1 ? 1.0 : 0.0);
+        if (n == 1 || cost < best_cost) {
+            best = n;
+            best_cost = cost;
+        }
+    }
+    return best;
+}
+
+Plan make_plan(const lmkv_pool_t* pool, int32_t q_heads, int32_t num_tokens, int32_t num_req, int32_t max_new,
+               int32_t prefix_len, int32_t max_kv_len) {
     Plan x = {};
     const int64_t group = q_heads / pool->num_kv_heads;
+    const int64_t batch_rows = (int64_t)num_tokens * group;            // per KV head
+    const int64_t req_rows = (int64_t)(max_new < num_tokens ? max_new : num_tokens) * group;
     x.rows = (int64_t)num_tokens * q_heads;
-    if (prefix_len > 0) {
-        x.prefix_tiles = (int32_t)((num_tokens * group + kRowTile - 1) / kRowTile);
-        split((int64_t)x.prefix_tiles * pool->num_kv_heads, prefix_len, &x.prefix_splits, &x.prefix_span);
+    x.big = req_rows >= kBigRows;
+    if (x.big || (prefix_len > 0 && batch_rows > kRowTile)) {
+        x.tiles = (int32_t)((batch_rows + kTileRows - 1) / kTileRows);
+        const int64_t blocks = ((int64_t)prefix_len + kBlock - 1) / kBlock +
+                               (x.big ? ((int64_t)max_kv_len + kBlock - 1) / kBlock : 0);
+        x.prefix_parts = tile_parts((int64_t)x.tiles * pool->num_kv_heads, blocks);
+    } else if (prefix_len > 0) {
+        x.row_tiles = (int32_t)((batch_rows + kRowTile - 1) / kRowTile);
+        split((int64_t)x.row_tiles * pool->num_kv_heads, prefix_len, &x.prefix_parts, &x.prefix_span);
     }
     x.own_span = 1;
-    if (max_kv_len > 0 || prefix_len == 0) {
-        x.own_slots = (int32_t)(num_tokens * group / kRowTile) + num_req;
-        split((int64_t)x.own_slots * pool->num_kv_heads, max_kv_len > 0 ? max_kv_len : 1, &x.own_splits, &x.own_span);
-    }
-    x.direct = x.prefix_splits + x.own_splits == 1 && x.own_splits == 1;
-    const uint64_t parts = x.direct ? 0 : (uint64_t)(x.prefix_splits + x.own_splits);
-    x.o_bytes = parts * x.rows * pool->head_dim * 4;
-    x.bytes = x.o_bytes + parts * x.rows * 8;
+    x.own_cap = (int32_t)(x.big ? kBigRows - 1 : req_rows);
+    x.own_tiles = (x.own_cap + kRowTile - 1) / kRowTile;
+    if (max_kv_len > 0 || prefix_len == 0)
+        split((int64_t)x.own_tiles * num_req * pool->num_kv_heads, max_kv_len > 0 ? max_kv_len : 1, &x.own_splits,
+              &x.own_span);
+    x.own_rows = (int64_t)num_req * x.own_cap * pool->num_kv_heads;
+    x.own_final = prefix_len == 0 && x.own_splits == 1;
+    x.join = x.prefix_parts > 1 || !x.own_final;
+    const uint64_t parts = x.join ? (uint64_t)x.prefix_parts * x.rows + (uint64_t)x.own_splits * x.own_rows : 0;
+    x.o_bytes = parts * pool->head_dim * 4;
+    x.bytes = x.o_bytes + parts * 8;
     return x;
 }
 
@@ -425,11 +934,19 @@ template <class T, int D>
 int attend_typed(AttendParams& p, const Plan& x, void* stream) {
     constexpr int smem = kWarps * kStages * 2 * kChunk * D * 2;
     int rc = allow_smem<attend_rows_kernel<T, D>, smem>();
+    if (rc == LMKV_OK) rc = allow_smem<attend_tiles_kernel<T, D>, TileShape<D>::kSmem>();
+    if (rc == LMKV_OK)
+        rc = launch(attend_tiles_kernel<T, D>, (int64_t)x.tiles * p.kv_heads * x.prefix_parts, kTileThreads,
+                    TileShape<D>::kSmem, stream, 1, p);
     if (rc != LMKV_OK) return rc;
-    const int64_t grid = ((int64_t)x.prefix_tiles * x.prefix_splits + (int64_t)x.own_slots * x.own_splits) * p.kv_heads;
+    const int64_t grid = ((int64_t)x.row_tiles * x.prefix_parts +
+                          (int64_t)x.own_tiles * p.seqs.num_req * x.own_splits) * p.kv_heads;
     rc = launch(attend_rows_kernel<T, D>, grid, kWarps * 32, smem, stream, 1, p);
-    if (rc != LMKV_OK || x.direct) return rc;
-    return launch(attend_join_kernel<T, D>, (x.rows + 7) / 8, 256, 0, stream, 1, p);
+    if (rc != LMKV_OK || !x.join) return rc;
+    // with one part of the tiles only the small requests' rows have more than one
+    if (x.prefix_parts <= 1)
+        return launch(attend_join_kernel<T, D, true>, (x.own_rows + 7) / 8, 256, 0, stream, 1, p);
+    return launch(attend_join_kernel<T, D, false>, (x.rows + 7) / 8, 256, 0, stream, 1, p);
 }
 
 }  // namespace
@@ -445,7 +962,8 @@ int lmkv_attend_workspace_bytes(const lmkv_pool_t* pool, int32_t num_q_heads, in
         (int64_t)num_tokens * num_q_heads > (int64_t)1 << 30)
         return LMKV_ERR_INVALID_ARG;
     *bytes = num_tokens == 0 || num_req == 0
-                 ? 0 : make_plan(pool, num_q_heads, num_tokens, num_req, (int32_t)prefix_len, max_kv_len).bytes;
+                 ? 0 : make_plan(pool, num_q_heads, num_tokens, num_req, max_new, (int32_t)prefix_len,
+                             max_kv_len).bytes;
     return LMKV_OK;
 }
 
@@ -464,8 +982,8 @@ int lmkv_attend_layer(const lmkv_pool_t* pool, int32_t dtype, int32_t layer, con
         return LMKV_ERR_INVALID_ARG;
     if (batch->num_req == 0 || batch->num_tokens == 0) return LMKV_OK;
     if (!rows_ok(q, 2) || !rows_ok(out, 2)) return LMKV_ERR_INVALID_ARG;
-    const Plan x = make_plan(pool, num_q_heads, batch->num_tokens, batch->num_req, (int32_t)prefix_len,
-                             batch->max_kv_len);
+    const Plan x = make_plan(pool, num_q_heads, batch->num_tokens, batch->num_req, batch->max_new,
+                             (int32_t)prefix_len, batch->max_kv_len);
     if (x.bytes > 0 && (workspace == nullptr || workspace_bytes < x.bytes)) return LMKV_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(workspace) & 15) return LMKV_ERR_MISALIGNED;
     AttendParams p = {};
@@ -478,19 +996,28 @@ int lmkv_attend_layer(const lmkv_pool_t* pool, int32_t dtype, int32_t layer, con
     p.status = d_status;
     p.part_o = static_cast<float*>(workspace);
     p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + x.o_bytes);
-    p.scale_log2 = scale * 1.44269504088896340736f;
+    p.scale_sign = scale > 0.f ? 1 : scale < 0.f ? -1 : 0;
+    p.scale_log2 = scale == 0.f ? 1.f : std::fabs(scale) * 1.44269504088896340736f;
     p.prefix_len = (int32_t)prefix_len;
     p.q_heads = num_q_heads;
     p.kv_heads = pool->num_kv_heads;
     p.rows = (int32_t)x.rows;
-    p.prefix_tiles = x.prefix_tiles;
-    p.prefix_splits = x.prefix_splits;
+    p.row_tiles = x.row_tiles;
+    p.tiles = x.tiles;
+    p.prefix_parts = x.prefix_parts;
     p.prefix_span = x.prefix_span;
-    p.own_slots = x.own_slots;
+    p.own_cap = x.own_cap;
+    p.own_tiles = x.own_tiles;
     p.own_splits = x.own_splits;
     p.own_span = x.own_span;
-    p.direct = x.direct;
-    p.q_pairs = reinterpret_cast<uintptr_t>(q->data) % 4 == 0 && q->token_stride % 2 == 0 && q->head_stride % 2 == 0;
+    p.big = x.big;
+    p.own_final = x.own_final;
+    auto aligned = [](const lmkv_rows_t* r, int64_t to) {
+        return reinterpret_cast<uintptr_t>(r->data) % to == 0 && r->token_stride * 2 % to == 0 && r->head_stride * 2 % to == 0;
+    };
+    p.q_vec = aligned(q, 16);
+    p.out_vec = aligned(out, 16);
+    p.q_pairs = aligned(q, 4);
     p.by_group = FastDiv((uint32_t)(num_q_heads / pool->num_kv_heads));
     if (dtype == LMKV_BF16)
         return pool->head_dim == 64 ? attend_typed<__nv_bfloat16, 64>(p, x, stream)

@@ -351,6 +351,17 @@ def test_attend_large_values():
     within(lse, want_l, tol_l, "lse")
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.11, 1.0, -1e-6])
+def test_attend_scales(scale):
+    b = Batch([1, 40, 2], [60, 90, 17], 4, 2, 64, BF, prefix=130)
+    b.scale = scale
+    out, lse = attend(b)
+    torch.cuda.synchronize()
+    want, want_l, tol, tol_l = b.attend()
+    within(out, want, tol, "out")
+    within(lse, want_l, tol_l, "lse")
+
+
 def test_attend_not_finite():
     """A NaN key reaches exactly the rows that see it; an infinite score makes a row NaN."""
     b = Batch([1, 1], [40, 40], 2, 1, 64, BF, prefix=20)
