@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Sequence
 
@@ -119,6 +120,9 @@ _lock = threading.Lock()
 def load() -> ctypes.CDLL:
     """Load liblmkv.so (raises if it is missing: build it with build.build())."""
     global _lib
+    lib = _lib
+    if lib is not None:
+        return lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -166,7 +170,8 @@ def load() -> ctypes.CDLL:
         lib.lmkv_cachegen_store_chunks.argtypes = cg_pool
         lib.lmkv_cachegen_retrieve_chunks.argtypes = cg_pool
         f64, f32 = ctypes.c_double, ctypes.c_float
-        rows_p, batch_p, rot_p = (ctypes.POINTER(t) for t in (_RowsT, _BatchT, _RotaryT))
+        rows_p = batch_p = P
+        rot_p = ctypes.POINTER(_RotaryT)
         lib.lmkv_rotary_init.argtypes = [rot_p, i32, i32, f64, i32, f64, f64, f64, f64]
         lib.lmkv_append_layer.argtypes = [pool_p, i32, i32, batch_p, i32, rows_p, rows_p, rows_p, rows_p,
                                           P, rot_p, P, P]
@@ -775,53 +780,83 @@ class Rotary:
         return ctypes.byref(self._struct)
 
 
-def _on(pool: Pool, **tensors) -> int:
-    """The pool's lmkv_dtype_t, after checking that every tensor is on the pool's
-    device and that this device is the current one (the library launches there)."""
-    t0 = pool.layers[0]
-    for name, t in tensors.items():
-        if t is not None and t.device != t0.device:
-            raise ValueError(f"{name} is on {t.device}, the pool on {t0.device}")
-    if t0.is_cuda and torch.cuda.current_device() != t0.device.index:
-        raise ValueError(f"the pool's device {t0.device} is not the current one")
+# A decode step makes these calls once per layer with microseconds of GPU work
+# in each, so the marshalling is written for few Python operations: structures
+# are packed into bytes and the checks compare whole shapes.
+_ROWS = struct.Struct("@Pqq")               # lmkv_rows_t
+_BATCH = struct.Struct("@PPPiiiii")         # lmkv_batch_t
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(pool: Pool, dev: int, stream):
+    """The stream handle of a call on the pool's device, which has to be the
+    current one (the library launches there)."""
+    if dev >= 0 and torch.cuda.current_device() != dev:
+        raise ValueError(f"the pool's device cuda:{dev} is not the current one")
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream if _raw_stream is None or dev < 0 else _raw_stream(dev)
+    return _stream_handle(stream)
+
+
+def _elsewhere(dev, names, tensors):
+    """Raises for the first tensor that is not on the pool's device."""
+    for name, t in zip(names, tensors):
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, the pool on {'cuda:%d' % dev if dev >= 0 else 'the CPU'}")
+
+
+def _dtype_of(t0: torch.Tensor) -> int:
     dtype = _DTYPES.get(t0.dtype)
     if dtype is None:
         raise ValueError(f"no operators for a pool of {t0.dtype}")
     return dtype
 
 
-def _rows(name: str, t: torch.Tensor, pool: Pool, heads: int, tokens: int | None = None) -> _RowsT:
+def _rows(name: str, t: torch.Tensor, dtype, dev: int, shape) -> bytes:
     """lmkv_rows_t of a [tokens][heads][head_dim] tensor of the pool's type, any
     strides over tokens and heads."""
-    shape = t.shape
-    if len(shape) != 3 or shape[1] != heads or shape[2] != pool.head_dim:
-        raise ValueError(f"{name} must be [tokens][{heads}][{pool.head_dim}], got {list(shape)}")
-    if tokens is not None and shape[0] != tokens:
-        raise ValueError(f"{name} has {shape[0]} tokens, q has {tokens}")
-    if t.dtype != pool.layers[0].dtype:
-        raise ValueError(f"{name} is {t.dtype}, the pool {pool.layers[0].dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)} ([tokens][heads][head_dim]), got {list(t.shape)}")
+    if t.dtype != dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be {dtype} on the pool's device, got {t.dtype} on {t.device}")
     ts, hs, es = t.stride()
     if es != 1:
         raise ValueError(f"{name}: a head's elements must be contiguous")
-    return _RowsT(t.data_ptr(), ts, hs)
+    return _ROWS.pack(t.data_ptr(), ts, hs)
 
 
-def _whole(name: str, t: torch.Tensor, dtype, shape) -> int:
-    """Pointer of a contiguous tensor of this type and shape (None entries are free)."""
-    if t.dtype != dtype or t.dim() != len(shape) or not t.is_contiguous() or \
-            any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+def _whole(name: str, t: torch.Tensor, dtype, dev: int, shape) -> int:
+    """Pointer of a contiguous tensor of this type and shape on the pool's device."""
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on the pool's device, got {t.dtype} "
+                         f"{list(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _batch(pool: Pool, block_table, q_start, kv_len, num_tokens, max_new, max_kv_len) -> _BatchT:
-    n = kv_len.shape[0]
-    cols = block_table.shape[-1]
-    return _BatchT(_whole("q_start", q_start, torch.int32, (n + 1,)),
-                   _whole("kv_len", kv_len, torch.int32, (n,)),
-                   _whole("block_table", block_table, torch.int32, (n, cols)), cols, n, num_tokens,
-                   num_tokens if max_new is None else int(max_new),
-                   cols * pool.block_size if max_kv_len is None else int(max_kv_len))
+def _status(status, dev: int):
+    if status is None:
+        return None
+    if status.dtype != torch.int32 or status.get_device() != dev:
+        raise ValueError("status must be int32 on the pool's device")
+    return status.data_ptr()
+
+
+def _heads_of(name: str, t: torch.Tensor):
+    """(tokens, heads) of a [tokens][heads][head_dim] tensor."""
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [tokens][heads][head_dim], got {list(shape)}")
+    return shape[0], shape[1]
+
+
+def _batch(pool: Pool, dev: int, block_table, q_start, kv_len, num_tokens, max_new, max_kv_len):
+    """(lmkv_batch_t, number of requests)."""
+    n, cols = kv_len.shape[0], block_table.shape[-1]
+    i32 = torch.int32
+    return _BATCH.pack(_whole("q_start", q_start, i32, dev, (n + 1,)), _whole("kv_len", kv_len, i32, dev, (n,)),
+                       _whole("block_table", block_table, i32, dev, (n, cols)), cols, n, num_tokens,
+                       num_tokens if max_new is None else max_new,
+                       cols * pool.block_size if max_kv_len is None else max_kv_len), n
 
 
 def append_layer(pool, layer, block_table, q, k, v, q_out, q_start, kv_len, rotary, positions=None,
@@ -829,42 +864,46 @@ def append_layer(pool, layer, block_table, q, k, v, q_out, q_start, kv_len, rota
     """lmkv_append_layer: rotate q into q_out (may be q), rotate k and copy v into
     the pages of the last q_start[r+1] - q_start[r] cached tokens of each
     request.  q, k, v: [tokens][heads][head_dim]; returns the status code."""
-    dtype = _on(pool, block_table=block_table, q=q, k=k, v=v, q_out=q_out, q_start=q_start, kv_len=kv_len,
-                positions=positions, status=status)
-    tokens, heads = q.shape[0], q.shape[1]
-    a = [_rows("q", q, pool, heads), _rows("k", k, pool, pool.num_kv_heads, tokens),
-         _rows("v", v, pool, pool.num_kv_heads, tokens), _rows("q_out", q_out, pool, heads, tokens)]
-    b = _batch(pool, block_table, q_start, kv_len, tokens, None, None)
-    pos = None if positions is None else _whole("positions", positions, torch.int64, (tokens,))
-    return load().lmkv_append_layer(pool.struct, dtype, int(layer), ctypes.byref(b), heads,
-                                    *(ctypes.byref(x) for x in a), pos, rotary.struct, _ptr(status),
-                                    _stream_handle(stream))
+    t0 = pool.layers[0]
+    dt, dev = t0.dtype, t0.get_device()
+    tokens, heads = _heads_of("q", q)
+    qs, ks = (tokens, heads, pool.head_dim), (tokens, pool.num_kv_heads, pool.head_dim)
+    b, _ = _batch(pool, dev, block_table, q_start, kv_len, tokens, None, None)
+    return load().lmkv_append_layer(
+        pool.struct, _dtype_of(t0), int(layer), b, heads, _rows("q", q, dt, dev, qs), _rows("k", k, dt, dev, ks),
+        _rows("v", v, dt, dev, ks), _rows("q_out", q_out, dt, dev, qs),
+        None if positions is None else _whole("positions", positions, torch.int64, dev, (tokens,)),
+        rotary.struct, _status(status, dev), _stream_of(pool, dev, stream))
 
 
-def _shifted_args(pool, block_table, start, end, chunk_size, save_unfull, chunk_ptrs, shift, rotary):
-    dtype = _on(pool, block_table=block_table, chunk_ptrs=chunk_ptrs)
-    a, keep = _common(pool, block_table, start, end)
-    sh = _i64_array(shift)
-    if sh.shape != keep[0].shape:
-        raise ValueError("shift must have one entry per request")
-    return (a[0], dtype, *a[1:], chunk_size, int(save_unfull), _ptr(chunk_ptrs), sh.ctypes.data,
-            rotary.struct), (keep, sh)
+def _shifted_args(pool, block_table, start, end, chunk_size, save_unfull, chunk_ptrs, shift, rotary, status):
+    t0 = pool.layers[0]
+    dev = t0.get_device()
+    _elsewhere(dev, ("block_table", "chunk_ptrs", "status"), (block_table, chunk_ptrs, status))
+    if block_table.dtype != torch.int32:
+        raise ValueError("block_table must be int32")
+    s, e, sh = _i64_array(start), _i64_array(end), _i64_array(shift)
+    if s.shape != e.shape or s.shape != sh.shape:
+        raise ValueError("start, end and shift must have one entry per request")
+    # the host arrays go as bytes: they are read during the call
+    return (pool.struct, _dtype_of(t0), block_table.data_ptr(), block_table.shape[-1], s.tobytes(), e.tobytes(),
+            len(s), chunk_size, int(save_unfull), _ptr(chunk_ptrs), sh.tobytes(), rotary.struct), dev
 
 
 def scatter_chunks_shifted(pool, block_table, start, end, chunk_size, save_unfull, chunk_ptrs, shift, rotary,
                            status=None, stream=None) -> int:
     """lmkv_scatter_chunks_shifted: scatter_chunks with request r's keys turned by
     shift[r] positions."""
-    a, _keep = _shifted_args(pool, block_table, start, end, chunk_size, save_unfull, chunk_ptrs, shift, rotary)
-    return load().lmkv_scatter_chunks_shifted(*a, _ptr(status), _stream_handle(stream))
+    a, dev = _shifted_args(pool, block_table, start, end, chunk_size, save_unfull, chunk_ptrs, shift, rotary, status)
+    return load().lmkv_scatter_chunks_shifted(*a, _ptr(status), _stream_of(pool, dev, stream))
 
 
 def scatter_layer_shifted(pool, block_table, start, end, chunk_size, save_unfull, chunk_ptrs, shift, rotary,
                           layer, status=None, stream=None) -> int:
     """lmkv_scatter_layer_shifted: scatter_layer with request r's keys turned by
     shift[r] positions."""
-    a, _keep = _shifted_args(pool, block_table, start, end, chunk_size, save_unfull, chunk_ptrs, shift, rotary)
-    return load().lmkv_scatter_layer_shifted(*a, int(layer), _ptr(status), _stream_handle(stream))
+    a, dev = _shifted_args(pool, block_table, start, end, chunk_size, save_unfull, chunk_ptrs, shift, rotary, status)
+    return load().lmkv_scatter_layer_shifted(*a, int(layer), _ptr(status), _stream_of(pool, dev, stream))
 
 
 def attend_workspace_bytes(pool, num_q_heads: int, num_tokens: int, num_req: int, max_new: int,
@@ -884,21 +923,25 @@ def attend_layer(pool, layer, q, out, q_start, kv_len, block_table, scale, works
     [tokens][heads]).  max_new and max_kv_len bound the lengths on the device
     (default: the rows of q, the table's width); tight ones cost less.
     workspace: uint8 of attend_workspace_bytes for the same bounds."""
-    dtype = _on(pool, q=q, out=out, q_start=q_start, kv_len=kv_len, block_table=block_table,
-                workspace=workspace, prefix_table=prefix_table, lse=lse, status=status)
-    tokens, heads = q.shape[0], q.shape[1]
-    rq, ro = _rows("q", q, pool, heads), _rows("out", out, pool, heads, tokens)
-    b = _batch(pool, block_table, q_start, kv_len, tokens, max_new, max_kv_len)
+    t0 = pool.layers[0]
+    dt, dev = t0.dtype, t0.get_device()
+    tokens, heads = _heads_of("q", q)
+    qs = (tokens, heads, pool.head_dim)
+    b, _ = _batch(pool, dev, block_table, q_start, kv_len, tokens, max_new, max_kv_len)
     table = None
     if prefix_len > 0:
         if prefix_table is None or prefix_table.numel() * pool.block_size < prefix_len:
             raise ValueError("prefix_table does not cover prefix_len")
-        table = _whole("prefix_table", prefix_table, torch.int32, (None,))
-    lp = None if lse is None else _whole("lse", lse, torch.float32, (tokens, heads))
-    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    return load().lmkv_attend_layer(pool.struct, dtype, int(layer), ctypes.byref(b), heads, ctypes.byref(rq),
-                                    table, int(prefix_len), float(scale), ctypes.byref(ro), lp,
-                                    _ptr(workspace), size, _ptr(status), _stream_handle(stream))
+        table = _whole("prefix_table", prefix_table, torch.int32, dev, (prefix_table.numel(),))
+    wp, size = None, 0
+    if workspace is not None:
+        wp = _whole("workspace", workspace, torch.uint8, dev, (workspace.numel(),))
+        size = workspace.numel()
+    return load().lmkv_attend_layer(
+        pool.struct, _dtype_of(t0), int(layer), b, heads, _rows("q", q, dt, dev, qs), table, int(prefix_len),
+        float(scale), _rows("out", out, dt, dev, qs),
+        None if lse is None else _whole("lse", lse, torch.float32, dev, (tokens, heads)), wp, size,
+        _status(status, dev), _stream_of(pool, dev, stream))
 
 
 def weigh_layer(pool, layer, q, lse, q_start, kv_len, block_table, scale, scores, scores_out, decay=1.0,
@@ -908,19 +951,20 @@ def weigh_layer(pool, layer, q, lse, q_start, kv_len, block_table, scale, scores
     float32 [requests][kv heads][stride]; scores_out may be scores, and scores
     None when decay is 0.  max_kv_len defaults to what the table and the
     scores have room for."""
-    dtype = _on(pool, q=q, lse=lse, q_start=q_start, kv_len=kv_len, block_table=block_table, scores=scores,
-                scores_out=scores_out, status=status)
-    tokens, heads = q.shape[0], q.shape[1]
-    rq = _rows("q", q, pool, heads)
+    t0 = pool.layers[0]
+    dt, dev = t0.dtype, t0.get_device()
+    tokens, heads = _heads_of("q", q)
+    stride = scores_out.shape[-1]
     if max_kv_len is None:
-        max_kv_len = min(block_table.shape[-1] * pool.block_size, scores_out.shape[-1])
-    b = _batch(pool, block_table, q_start, kv_len, tokens, max_new, max_kv_len)
-    shape = (b.num_req, pool.num_kv_heads, scores_out.shape[-1])
-    to = _whole("scores_out", scores_out, torch.float32, shape)
-    old = None if scores is None else _whole("scores", scores, torch.float32, shape)
-    return load().lmkv_weigh_layer(pool.struct, dtype, int(layer), ctypes.byref(b), heads, ctypes.byref(rq),
-                                   _whole("lse", lse, torch.float32, (tokens, heads)), float(scale),
-                                   float(decay), old, to, shape[2], _ptr(status), _stream_handle(stream))
+        max_kv_len = min(block_table.shape[-1] * pool.block_size, stride)
+    b, n = _batch(pool, dev, block_table, q_start, kv_len, tokens, max_new, max_kv_len)
+    shape = (n, pool.num_kv_heads, stride)
+    return load().lmkv_weigh_layer(
+        pool.struct, _dtype_of(t0), int(layer), b, heads, _rows("q", q, dt, dev, (tokens, heads, pool.head_dim)),
+        _whole("lse", lse, torch.float32, dev, (tokens, heads)), float(scale), float(decay),
+        None if scores is None else _whole("scores", scores, torch.float32, dev, shape),
+        _whole("scores_out", scores_out, torch.float32, dev, shape), stride, _status(status, dev),
+        _stream_of(pool, dev, stream))
 
 
 def evict_layer(pool, layer, block_table, kv_len, scores, sinks, recent, keep, new_len, kept_scores=None,
@@ -931,24 +975,22 @@ def evict_layer(pool, layer, block_table, kv_len, scores, sinks, recent, keep, n
     (int32 [requests][kv heads][budget]), new_len and kept_scores; the caller
     then takes new_len as kv_len and frees the pages behind it.  max_kv_len
     defaults to what the table and the scores have room for."""
-    n, cols = kv_len.shape[0], block_table.shape[-1]
-    t0 = pool.layers[0]
-    for name, t in (("block_table", block_table), ("kv_len", kv_len), ("scores", scores), ("keep", keep),
-                    ("new_len", new_len), ("kept_scores", kept_scores), ("status", status)):
-        if t is not None and t.device != t0.device:
-            raise ValueError(f"{name} is on {t.device}, the pool on {t0.device}")
-    if t0.is_cuda and torch.cuda.current_device() != t0.device.index:
-        raise ValueError(f"the pool's device {t0.device} is not the current one")
-    kh = pool.num_kv_heads
-    kp = None if kept_scores is None else _whole("kept_scores", kept_scores, torch.float32, (n, kh, None))
+    dev = pool.layers[0].get_device()
+    n, cols, kh = kv_len.shape[0], block_table.shape[-1], pool.num_kv_heads
+    stride, budget = scores.shape[-1], keep.shape[-1]
+    i32, f32 = torch.int32, torch.float32
+    kp, kept_stride = None, 0
+    if kept_scores is not None:
+        kept_stride = kept_scores.shape[-1]
+        kp = _whole("kept_scores", kept_scores, f32, dev, (n, kh, kept_stride))
+    if max_kv_len is None:
+        max_kv_len = min(cols * pool.block_size, stride)
     return load().lmkv_evict_layer(
-        pool.struct, int(layer), _whole("block_table", block_table, torch.int32, (n, cols)), cols,
-        _whole("kv_len", kv_len, torch.int32, (n,)), n,
-        min(cols * pool.block_size, scores.shape[-1]) if max_kv_len is None else int(max_kv_len),
-        _whole("scores", scores, torch.float32, (n, kh, None)), scores.shape[-1], keep.shape[-1], int(sinks),
-        int(recent), _whole("keep", keep, torch.int32, (n, kh, None)),
-        _whole("new_len", new_len, torch.int32, (n,)), kp, 0 if kp is None else kept_scores.shape[-1],
-        _ptr(status), _stream_handle(stream))
+        pool.struct, int(layer), _whole("block_table", block_table, i32, dev, (n, cols)), cols,
+        _whole("kv_len", kv_len, i32, dev, (n,)), n, int(max_kv_len),
+        _whole("scores", scores, f32, dev, (n, kh, stride)), stride, budget, int(sinks), int(recent), _whole("keep", keep, i32, dev, (n, kh, budget)),
+        _whole("new_len", new_len, i32, dev, (n,)), kp, kept_stride, _status(status, dev),
+        _stream_of(pool, dev, stream))
 
 
 def check(rc: int, what: str = "lmkv") -> None:
