@@ -359,7 +359,7 @@ using namespace lmkv_tc;
 
 constexpr int kTileRows = 256;        // two tiles of 128 rows share every K and V block
 constexpr int kBlock = 128;           // keys of a block
-constexpr int kTileThreads = 384;     // softmax 2 x 128, loads 64, products 1 (of 64)
+constexpr int kTileThreads = 352;     // softmax 2 x 128, loads 64, products 1 (of 32)
 constexpr int kLoadWarps = 2;
 constexpr int kMaxSegs = 8;           // the prefix and every big request that 256 rows can touch
 constexpr int kMaskSlots = 8;
@@ -423,7 +423,7 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(s_full + 8 * t, 1);
-            mbar_init(p_ready + 8 * t, 128);
+            mbar_init(p_ready + 8 * t, 4);
             mbar_init(o_full + 8 * t, 1);
         }
         gave_up = 0;
@@ -522,7 +522,8 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
                                  : "memory");
                 }
                 fence_async_shared();
-                mbar_arrive(p_ready + 8 * t);          // phase 0: q is there
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_ready + 8 * t);          // phase 0: q is there
 
                 int32_t own = -1;
                 for (int32_t i = 0; i < nseg; ++i)
@@ -557,24 +558,24 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
                         for (int j = 0; j < 32; ++j)
                             if (!((bits >> j) & 1)) x[j] = 0xFF800000u;
                     };
+                    uint32_t x[4][32];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tmem_ld32(x[i], s_at + 32 * i);
+                    wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        loaded(x[i]);
+                        take(x[i], i);
+                    }
                     float mx = -INFINITY;
+                    {
+                        float a[8];
 #pragma unroll
-                    for (int i = 0; i < 4; i += 2) {
-                        uint32_t x[32], y[32];
-                        tmem_ld32(x, s_at + 32 * i);
-                        tmem_ld32(y, s_at + 32 * i + 32);
-                        wait_ld();
-                        loaded(x);
-                        loaded(y);
-                        take(x, i);
-                        take(y, i + 1);
-                        float a = -INFINITY, c = -INFINITY;
+                        for (int i = 0; i < 8; ++i) a[i] = __uint_as_float(x[0][i]);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            a = fmaxf(a, __uint_as_float(x[j]));
-                            c = fmaxf(c, __uint_as_float(y[j]));
-                        }
-                        mx = fmaxf(mx, fmaxf(a, c));
+                        for (int j = 8; j < 128; ++j) a[j & 7] = fmaxf(a[j & 7], __uint_as_float(x[j >> 5][j & 31]));
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, a[i]);
                     }
                     // weights are relative to m; m moves when it would be exceeded by more than 2^8
                     const bool grow = mx > m && !((mx - m) * scale <= 8.f);
@@ -592,27 +593,27 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
                     }
                     const float neg = m == -INFINITY ? 0.f : -m * scale;
                     const float2 sc2 = make_float2(scale, scale), ng2 = make_float2(neg, neg);
+                    float2 sums[4] = {l2, make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        uint32_t x[32], w[16];
-                        tmem_ld32(x, s_at + 32 * i);
-                        wait_ld();
-                        loaded(x);
-                        take(x, i);
+                        uint32_t w[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
-                            float2 e = fma2(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), sc2, ng2);
+                            float2 e = fma2(make_float2(__uint_as_float(x[i][2 * j]), __uint_as_float(x[i][2 * j + 1])),
+                                            sc2, ng2);
                             e.x = exp2_fast(e.x);
                             e.y = exp2_fast(e.y);
-                            l2 = add2(l2, e);
+                            sums[j & 3] = add2(sums[j & 3], e);
                             // weights are rounded to T for the product with V, the sum takes them whole
                             w[j] = Elem<T>::pack(e.x, e.y);
                         }
                         tmem_st16(s_at + 16 * i, w);       // over scores that have been read
                     }
+                    l2 = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
                     wait_st();
                     fence_before_sync();
-                    mbar_arrive(p_ready + 8 * t);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_ready + 8 * t);
                 }
                 // my row of the result
                 const float l = l2.x + l2.y;

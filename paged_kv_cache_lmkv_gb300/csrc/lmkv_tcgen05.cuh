@@ -32,22 +32,24 @@ __device__ __forceinline__ uint64_t now_ns() {
 }
 // Waits for the phase of this parity, at most a second (or until another
 // thread of the CTA gave up).  False: gave up; every role then leaves its loop.
+// The clock is read once in kPolls polls: reading it takes longer than the
+// waits of a running pipeline do.
 constexpr uint64_t kWaitNs = 1000000000ull;
-__device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int* gave_up) {
-    const uint64_t t0 = now_ns();
-    while (!mbar_test(bar, parity)) {
-        if (*gave_up) return false;
-        if (now_ns() - t0 > kWaitNs) {
+constexpr int kPolls = 512;
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+    if (mbar_test(bar, parity)) return true;
+    uint64_t t0 = 0;
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < kPolls; ++i)
+            if (mbar_test(bar, parity)) return true;
+        const uint64_t t = now_ns();
+        if (t0 == 0) t0 = t;
+        if (*gave_up || t - t0 > kWaitNs) {
             *gave_up = 1;
             return false;
         }
     }
-    return true;
-}
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
-    for (int i = 0; i < 16; ++i)
-        if (mbar_test(bar, parity)) return true;
-    return mbar_wait_long(bar, parity, gave_up);
 }
 
 __device__ __forceinline__ void fence_async_shared() {
