@@ -360,7 +360,7 @@ using namespace lmkv_tc;
 constexpr int kTileRows = 256;        // two tiles of 128 rows share every K and V block
 constexpr int kBlock = 128;           // keys of a block
 constexpr int kTileThreads = 352;     // softmax 2 x 128, loads 64, products 1 (of 32)
-constexpr int kLoadWarps = 2;
+constexpr int kLoadWarps = 2;         // two groups of 32 rows each
 constexpr int kMaxSegs = 8;           // the prefix and every big request that 256 rows can touch
 constexpr int kMaskSlots = 8;
 
@@ -677,67 +677,100 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
             constexpr int kVecs = D / 8;             // 16-byte pieces of a row
             constexpr int kRowsPer = 32 / kVecs;     // rows of a warp-wide copy
             constexpr int kGroups = kBlock / 32 / kLoadWarps;     // groups of 32 rows of this warp
-            const int64_t half_bytes = p.layer.half_bytes();
+            constexpr int kPatterns = 8 / kRowsPer;  // copies until the swizzle repeats
+            constexpr uint32_t kNoRow = Layer::kNoRow, kPast = kNoRow - 1;
             const int c = lane % kVecs, rsub = lane / kVecs;
-            const int64_t piece = (int64_t)h * (D * 2) + c * 16;
-            int32_t si = 0, item = 0;
-            int64_t next[kGroups];
+            const uint8_t* const from_k = base + (int64_t)h * (D * 2) + c * 16;
+            const uint8_t* const from_v = from_k + p.layer.half_bytes();
+            const uint32_t row_bytes = (uint32_t)p.layer.row_bytes;
+            uint32_t pattern[kPatterns];
+#pragma unroll
+            for (int k = 0; k < kPatterns; ++k) {
+                const int row = k * kRowsPer + rsub;
+                pattern[k] = kv_smem + (c >> 3) * S::kHalfBytes + (w * kGroups * 32 + row) * 128 + (((c & 7) ^ (row & 7)) << 4);
+            }
+            int32_t si = 0, item = 0, signalled = 0;
+            uint32_t next[kGroups];
             auto lookup = [&](int32_t b) {
                 while (si + 1 < nseg && b >= segs[si + 1].first) ++si;
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
                     const int32_t tok = (b - segs[si].first) * kBlock + (w * kGroups + g) * 32 + lane;
-                    next[g] = tok < segs[si].end ? p.layer.token_offset(segs[si].table, tok) : -2;
+                    next[g] = tok < segs[si].end ? p.layer.token_row(segs[si].table, tok) : kPast;
                 }
             };
             bool ok = true;
-            auto signal = [&](int32_t i) {           // my loads of item i are done
+            auto signal = [&](int32_t upto) {        // my loads of the items before upto are done
                 fence_async_shared();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(full + 8 * (i % S::kStages));
+                for (; signalled < upto; ++signalled)
+                    if (lane == 0) mbar_arrive(full + 8 * (signalled % S::kStages));
             };
             if (b0 < b1) lookup(b0);
             for (int32_t b = b0; b < b1 && ok; ++b) {
-                int64_t off[kGroups];
-                uint32_t there[kGroups];
+                uint32_t rows[kGroups], there[kGroups], all = ~0u;
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
-                    off[g] = next[g];
-                    if (off[g] == -1) report(p.status, LMKV_ERR_BAD_BLOCK);
-                    there[g] = __ballot_sync(0xFFFFFFFFu, off[g] >= 0);
+                    rows[g] = next[g];
+                    if (rows[g] == kNoRow) report(p.status, LMKV_ERR_BAD_BLOCK);
+                    there[g] = __ballot_sync(0xFFFFFFFFu, rows[g] < kPast);
+                    all &= there[g];
                 }
                 if (b + 1 < b1) lookup(b + 1);
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv, ++item) {
                     const int st = item % S::kStages;
-                    if (item >= S::kStages && !mbar_wait(empty + 8 * st, (item / S::kStages - 1) & 1, &gave_up)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t dst0 = kv_smem + st * S::kStageBytes + (c >> 3) * S::kHalfBytes;
-                    const uint8_t* const from = base + piece + (kv ? half_bytes : 0);
-#pragma unroll
-                    for (int g = 0; g < kGroups; ++g) {
-                        if (kv == 0 && lane == 0)
-                            reinterpret_cast<uint32_t*>(&key_mask[(b - b0) % kMaskSlots])[w * kGroups + g] = there[g];
-                        const uint32_t dst = dst0 + (w * kGroups + g) * 32 * 128;
-#pragma unroll
-                        for (int v = 0; v < kVecs; ++v) {
-                            const int row = v * kRowsPer + rsub;
-                            const int64_t o = __shfl_sync(0xFFFFFFFFu, off[g], row);
-                            cp_async16(dst + row * 128 + (((c & 7) ^ (row & 7)) << 4), o >= 0 ? from + o : base, o >= 0);
+                    if (item >= S::kStages) {
+                        const uint32_t bar = empty + 8 * st, parity = (item / S::kStages - 1) & 1;
+                        // No room: the loads in flight are signalled before waiting for it,
+                        // as the products that make room may be waiting for them.
+                        if (!__all_sync(0xFFFFFFFFu, mbar_peek(bar, parity))) {
+                            cp_wait<0>();
+                            signal(item);
+                            if (!mbar_wait(bar, parity, &gave_up)) {
+                                ok = false;
+                                break;
+                            }
                         }
+                    }
+                    const uint32_t stage = st * S::kStageBytes;
+                    const uint8_t* const from = kv ? from_v : from_k;
+                    if (kv == 0 && lane < kGroups) {
+                        uint32_t* const slot = reinterpret_cast<uint32_t*>(&key_mask[(b - b0) % kMaskSlots]);
+#pragma unroll
+                        for (int g = 0; g < kGroups; ++g)
+                            if (lane == g) slot[w * kGroups + g] = there[g];
+                    }
+                    if (all == ~0u) {
+#pragma unroll
+                        for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+                            for (int v = 0; v < kVecs; ++v) {
+                                const uint32_t row = __shfl_sync(0xFFFFFFFFu, rows[g], v * kRowsPer + rsub);
+                                cp_async16(pattern[v % kPatterns] + stage + (g * 32 + v / kPatterns * 8) * 128,
+                                           from + (uint64_t)row * row_bytes);
+                            }
+                    } else {
+#pragma unroll 1
+                        for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+                            for (int v = 0; v < kVecs; ++v) {
+                                const uint32_t r0 = g == 0 ? rows[0] : rows[kGroups - 1];
+                                const uint32_t row = __shfl_sync(0xFFFFFFFFu, r0, v * kRowsPer + rsub);
+                                const bool on = row < kPast;
+                                cp_async16(pattern[v % kPatterns] + stage + (g * 32 + v / kPatterns * 8) * 128,
+                                           from + (on ? (uint64_t)row * row_bytes : 0), on);
+                            }
                     }
                     cp_commit();
                     if (item >= S::kLag) {
                         cp_wait<S::kLag>();
-                        signal(item - S::kLag);
+                        signal(item - S::kLag + 1);
                     }
                 }
             }
             cp_wait<0>();
-            if (ok)
-                for (int32_t i = max(0, item - S::kLag); i < item; ++i) signal(i);
+            if (ok) signal(item);
         } else {
             if (warp == 10 && lane == 0 && b1 > b0) {
                 constexpr uint32_t qk = instr_desc<T, kBlock, false>(), pv = instr_desc<T, D, true>();

@@ -69,6 +69,15 @@ struct Layer {
         if (blk < 0 || blk >= num_blocks) return -1;
         return (blk * block_size + (tok - (int32_t)(col * (uint32_t)block_size))) * row_bytes;
     }
+    // The row's number in the K half (below 2^32 in any memory: rows of 128
+    // bytes and more), or kNoRow.
+    __device__ __forceinline__ uint32_t token_row(const int32_t* table, int32_t tok) const {
+        const uint32_t col = by_block.div((uint32_t)tok);
+        const int32_t blk = table[col];
+        if (blk < 0 || blk >= num_blocks) return kNoRow;
+        return (uint32_t)blk * (uint32_t)block_size + ((uint32_t)tok - col * (uint32_t)block_size);
+    }
+    static constexpr uint32_t kNoRow = 0xFFFFFFFFu;
 };
 
 __device__ __forceinline__ void report(int32_t* status, int code) {
