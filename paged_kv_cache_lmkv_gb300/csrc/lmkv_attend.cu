@@ -379,7 +379,6 @@ struct TileShape {
     static constexpr int kHalfBytes = 128 * 128;
     static constexpr int kStageBytes = kHalves * kHalfBytes;       // 128 rows of K, V or q
     static constexpr int kStages = D == 128 ? 5 : 8;
-    static constexpr int kLag = kStages - 2;                       // loads in flight behind the newest
     static constexpr int kSmem = (2 + kStages) * kStageBytes;
 };
 
@@ -405,7 +404,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 attend_tiles_kernel(const __grid_constant__ AttendParams p) {
     using S = TileShape<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ uint64_t bars[2 * S::kStages + 6];
+    __shared__ uint64_t bars[2 * S::kStages + 8];
     __shared__ uint32_t tmem_base;
     __shared__ int gave_up;
     __shared__ Seg segs[kMaxSegs];
@@ -414,16 +413,17 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
     pdl_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t full = smem_u32(bars), empty = full + 8 * S::kStages, s_full = empty + 8 * S::kStages,
-                   p_ready = s_full + 16, o_full = p_ready + 16;
+                   p_ready = s_full + 16, o_full = p_ready + 32;
     const uint32_t q_smem = smem_u32(smem), kv_smem = q_smem + 2 * S::kStageBytes;
     if (tid == 0) {
         for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(full + 8 * i, kLoadWarps);
+            mbar_init(full + 8 * i, kLoadWarps * 33);
             mbar_init(empty + 8 * i, 1);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(s_full + 8 * t, 1);
-            mbar_init(p_ready + 8 * t, 4);
+            mbar_init(p_ready + 16 * t, 4);
+            mbar_init(p_ready + 16 * t + 8, 4);
             mbar_init(o_full + 8 * t, 1);
         }
         gave_up = 0;
@@ -523,7 +523,7 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
                 }
                 fence_async_shared();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_ready + 8 * t);          // phase 0: q is there
+                if (lane == 0) mbar_arrive(p_ready + 16 * t + 8);     // its phase 0: q is there
 
                 int32_t own = -1;
                 for (int32_t i = 0; i < nseg; ++i)
@@ -608,12 +608,14 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
                             w[j] = Elem<T>::pack(e.x, e.y);
                         }
                         tmem_st16(s_at + 16 * i, w);       // over scores that have been read
+                        if (i & 1) {                       // 64 keys' weights are there
+                            wait_st();
+                            fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(p_ready + 16 * t + 8 * (i >> 1));
+                        }
                     }
                     l2 = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
-                    wait_st();
-                    fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(p_ready + 8 * t);
                 }
                 // my row of the result
                 const float l = l2.x + l2.y;
@@ -689,7 +691,7 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
                 const int row = k * kRowsPer + rsub;
                 pattern[k] = kv_smem + (c >> 3) * S::kHalfBytes + (w * kGroups * 32 + row) * 128 + (((c & 7) ^ (row & 7)) << 4);
             }
-            int32_t si = 0, item = 0, signalled = 0;
+            int32_t si = 0, item = 0;
             uint32_t next[kGroups];
             auto lookup = [&](int32_t b) {
                 while (si + 1 < nseg && b >= segs[si + 1].first) ++si;
@@ -700,12 +702,6 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
                 }
             };
             bool ok = true;
-            auto signal = [&](int32_t upto) {        // my loads of the items before upto are done
-                fence_async_shared();
-                __syncwarp();
-                for (; signalled < upto; ++signalled)
-                    if (lane == 0) mbar_arrive(full + 8 * (signalled % S::kStages));
-            };
             if (b0 < b1) lookup(b0);
             for (int32_t b = b0; b < b1 && ok; ++b) {
                 uint32_t rows[kGroups], there[kGroups], all = ~0u;
@@ -720,18 +716,9 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv, ++item) {
                     const int st = item % S::kStages;
-                    if (item >= S::kStages) {
-                        const uint32_t bar = empty + 8 * st, parity = (item / S::kStages - 1) & 1;
-                        // No room: the loads in flight are signalled before waiting for it,
-                        // as the products that make room may be waiting for them.
-                        if (!__all_sync(0xFFFFFFFFu, mbar_peek(bar, parity))) {
-                            cp_wait<0>();
-                            signal(item);
-                            if (!mbar_wait(bar, parity, &gave_up)) {
-                                ok = false;
-                                break;
-                            }
-                        }
+                    if (item >= S::kStages && !mbar_wait(empty + 8 * st, (item / S::kStages - 1) & 1, &gave_up)) {
+                        ok = false;
+                        break;
                     }
                     const uint32_t stage = st * S::kStageBytes;
                     const uint8_t* const from = kv ? from_v : from_k;
@@ -762,55 +749,73 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
                                            from + (on ? (uint64_t)row * row_bytes : 0), on);
                             }
                     }
-                    cp_commit();
-                    if (item >= S::kLag) {
-                        cp_wait<S::kLag>();
-                        signal(item - S::kLag + 1);
-                    }
+                    // an arrival of each thread when its copies have landed, and one of the warp for the key mask
+                    mbar_arrive_copies(full + 8 * st);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full + 8 * st);
                 }
             }
-            cp_wait<0>();
-            if (ok) signal(item);
+            asm volatile("cp.async.wait_all;" ::: "memory");
         } else {
             if (warp == 10 && lane == 0 && b1 > b0) {
                 constexpr uint32_t qk = instr_desc<T, kBlock, false>(), pv = instr_desc<T, D, true>();
                 const int32_t blocks = b1 - b0;
-                auto stage = [&](int32_t item) { return kv_smem + (item % S::kStages) * S::kStageBytes; };
-                auto loaded_item = [&](int32_t item) {
-                    return mbar_wait(full + 8 * (item % S::kStages), (item / S::kStages) & 1, &gave_up);
+                const Desc q0 = desc_k_major(q_smem), k0 = desc_k_major(kv_smem),
+                           v0 = desc_n_major(kv_smem, S::kHalfBytes);
+                // places of the next K and V items in the ring, and their phases
+                int32_t ks = 0, vs = 1;
+                uint32_t kph = 0, vph = 0;
+                auto advance = [](int32_t& st, uint32_t& ph) {
+                    st += 2;
+                    if (st >= S::kStages) {
+                        st -= S::kStages;
+                        ph ^= 1;
+                    }
                 };
-                auto scores = [&](int t, int32_t j) {          // tile t's q x K of block j
-                    const uint32_t a = q_smem + t * S::kStageBytes, k = stage(2 * j);
+                auto scores = [&](int t, int32_t st) {         // tile t's q x K
+                    const Desc a = q0.at(t * S::kStageBytes), k = k0.at(st * S::kStageBytes);
 #pragma unroll
                     for (int s = 0; s < D / 16; ++s) {
                         const uint32_t at = (s >> 2) * S::kHalfBytes + (s & 3) * 32;
-                        mma_ss(tmem + t * 128, desc_k_major(a + at), desc_k_major(k + at), qk, s > 0);
+                        mma_ss(tmem + t * 128, a.at(at), k.at(at), qk, s > 0);
                     }
                     mma_commit(s_full + 8 * t);
                 };
-                bool ok = loaded_item(0);
+                bool ok = mbar_wait(full, 0, &gave_up);
+                fence_async_shared();                          // the copies, before the products that read them
                 for (int t = 0; t < tiles && ok; ++t) {
-                    ok = mbar_wait(p_ready + 8 * t, 0, &gave_up);
+                    ok = mbar_wait(p_ready + 16 * t + 8, 0, &gave_up);
                     if (ok) scores(t, 0);
                 }
                 if (ok) mma_commit(empty);                     // item 0's stage
+                advance(ks, kph);
                 for (int32_t j = 0; j < blocks && ok; ++j) {
-                    ok = loaded_item(2 * j + 1) && (j + 1 >= blocks || loaded_item(2 * j + 2));
-                    for (int t = 0; t < tiles && ok; ++t) {
-                        ok = mbar_wait(p_ready + 8 * t, (j + 1) & 1, &gave_up);
-                        if (!ok) break;
-                        fence_after_sync();
-                        const uint32_t v = stage(2 * j + 1);
+                    const bool more = j + 1 < blocks;
+                    const Desc v = v0.at(vs * S::kStageBytes);
+                    ok = mbar_wait(full + 8 * vs, vph, &gave_up) && (!more || mbar_wait(full + 8 * ks, kph, &gave_up));
+                    fence_async_shared();
 #pragma unroll
-                        for (int s = 0; s < kBlock / 16; ++s)
-                            mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * s, desc_n_major(v + s * 2048, S::kHalfBytes),
-                                   pv, j > 0 || s > 0);
-                        if (t == tiles - 1) mma_commit(empty + 8 * ((2 * j + 1) % S::kStages));
+                    for (int t = 0; t < 2; ++t) {
+                        if (t >= tiles || !ok) break;
+                        // the weights come in two halves of 64 keys, a barrier each
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            ok = ok && mbar_wait(p_ready + 16 * t + 8 * half, (j + half) & 1, &gave_up);
+                            if (!ok) break;
+                            fence_after_sync();
+#pragma unroll
+                            for (int s = half * 4; s < half * 4 + 4; ++s)
+                                mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * s, v.at(s * 2048), pv, j > 0 || s > 0);
+                        }
+                        if (!ok) break;
+                        if (t == tiles - 1) mma_commit(empty + 8 * vs);
                         // issued behind the product that reads the weights from the same columns
-                        if (j + 1 < blocks) scores(t, j + 1);
+                        if (more) scores(t, ks);
                         else mma_commit(o_full + 8 * t);
                     }
-                    if (ok && j + 1 < blocks) mma_commit(empty + 8 * ((2 * j + 2) % S::kStages));
+                    if (ok && more) mma_commit(empty + 8 * ks);
+                    advance(ks, kph);
+                    advance(vs, vph);
                 }
             }
         }

@@ -16,21 +16,15 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// One arrival once this thread's asynchronous copies so far have landed.
+__device__ __forceinline__ void mbar_arrive_copies(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    return ok != 0;
-}
-// The same without waiting at all (try_wait may suspend the thread for a while).
-__device__ __forceinline__ bool mbar_peek(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
@@ -127,15 +121,20 @@ __device__ __forceinline__ void tmem_scale16(uint32_t addr, float f) {
 // Shared-memory tiles are kept as [column half of 64 elements][row][128 bytes],
 // the eight 16-byte pieces of a row exchanged by the row number (128-byte
 // swizzle): atoms of 8 rows x 128 bytes, 1024-byte aligned.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead_bytes, uint32_t stride_bytes) {
-    return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)(lead_bytes >> 4) << 16) |
-           ((uint64_t)(stride_bytes >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// An operand's descriptor, as its two words: the low one holds the address
+// (in 16 bytes) and the lead offset, so a step along the tile is one addition.
+struct Desc {
+    uint32_t lo, hi;
+    __device__ __forceinline__ Desc at(uint32_t bytes) const { return Desc{lo + (bytes >> 4), hi}; }
+};
+__device__ __forceinline__ Desc smem_desc(uint32_t addr, uint32_t lead_bytes, uint32_t stride_bytes) {
+    return Desc{((addr & 0x3FFFF) >> 4) | ((lead_bytes >> 4) << 16), (stride_bytes >> 4) | (1u << 14) | (2u << 29)};
 }
 // Rows of the tile are the operand's M or N, columns its K.
-__device__ __forceinline__ uint64_t desc_k_major(uint32_t addr) { return smem_desc(addr, 16, 1024); }
+__device__ __forceinline__ Desc desc_k_major(uint32_t addr) { return smem_desc(addr, 16, 1024); }
 // Rows of the tile are the operand's K, columns its N (half_bytes from one
 // half of 64 columns to the next).
-__device__ __forceinline__ uint64_t desc_n_major(uint32_t addr, uint32_t half_bytes) {
+__device__ __forceinline__ Desc desc_n_major(uint32_t addr, uint32_t half_bytes) {
     return smem_desc(addr, half_bytes, 1024);
 }
 // Instruction descriptor: fp32 accumulator, A and B of one 16-bit type.
@@ -145,20 +144,20 @@ __device__ __forceinline__ constexpr uint32_t instr_desc() {
     return (1u << 4) | (type << 7) | (type << 10) | ((kBNMajor ? 1u : 0u) << 16) | ((uint32_t)(kN >> 3) << 17) |
            ((uint32_t)(128 >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ss(uint32_t d, Desc a, Desc b, uint32_t idesc, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.u32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, Desc b, uint32_t idesc, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "setp.ne.u32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
 // The barrier's next arrival is when all products issued by this thread so far are done.
