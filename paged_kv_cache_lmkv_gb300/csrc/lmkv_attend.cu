@@ -545,6 +545,12 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
                         ok = false;
                         break;
                     }
+                    if (t == tiles - 1 && (tid & 127) == 0) {
+                        // every product up to these scores is done: K of this block and V of the last are free
+                        const int32_t j = b - b0;
+                        mbar_arrive(empty + 8 * (2 * j % S::kStages));
+                        if (j > 0) mbar_arrive(empty + 8 * ((2 * j - 1) % S::kStages));
+                    }
                     fence_after_sync();
                     const uint4 mask = key_mask[(b - b0) % kMaskSlots];
                     const uint32_t words[4] = {mask.x, mask.y, mask.z, mask.w};
@@ -559,24 +565,21 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
                             if (!((bits >> j) & 1)) x[j] = 0xFF800000u;
                     };
                     uint32_t x[4][32];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) tmem_ld32(x[i], s_at + 32 * i);
-                    wait_ld();
+                    float mx = -INFINITY, my = -INFINITY;
+                    tmem_ld32(x[0], s_at);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
+                        wait_ld();
                         loaded(x[i]);
+                        if (i < 3) tmem_ld32(x[i + 1], s_at + 32 * (i + 1));
                         take(x[i], i);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            mx = max3(mx, __uint_as_float(x[i][j]), __uint_as_float(x[i][j + 1]));
+                            my = max3(my, __uint_as_float(x[i][j + 2]), __uint_as_float(x[i][j + 3]));
+                        }
                     }
-                    float mx = -INFINITY;
-                    {
-                        float a[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) a[i] = __uint_as_float(x[0][i]);
-#pragma unroll
-                        for (int j = 8; j < 128; ++j) a[j & 7] = fmaxf(a[j & 7], __uint_as_float(x[j >> 5][j & 31]));
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, a[i]);
-                    }
+                    mx = fmaxf(mx, my);
                     // weights are relative to m; m moves when it would be exceeded by more than 2^8
                     const bool grow = mx > m && !((mx - m) * scale <= 8.f);
                     if (__any_sync(0xFFFFFFFFu, grow)) {
@@ -692,22 +695,30 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
                 pattern[k] = kv_smem + (c >> 3) * S::kHalfBytes + (w * kGroups * 32 + row) * 128 + (((c & 7) ^ (row & 7)) << 4);
             }
             int32_t si = 0, item = 0;
-            uint32_t next[kGroups];
+            // table entries of the next block, one block ahead
+            int32_t next_tok[kGroups], next_blk[kGroups];
+            uint32_t next_col[kGroups];
             auto lookup = [&](int32_t b) {
                 while (si + 1 < nseg && b >= segs[si + 1].first) ++si;
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
                     const int32_t tok = (b - segs[si].first) * kBlock + (w * kGroups + g) * 32 + lane;
-                    next[g] = tok < segs[si].end ? p.layer.token_row(segs[si].table, tok) : kPast;
+                    const bool on = tok < segs[si].end;
+                    next_tok[g] = on ? tok : -1;
+                    next_col[g] = p.layer.column(on ? tok : 0);
+                    next_blk[g] = on ? segs[si].table[next_col[g]] : 0;
                 }
             };
+            // Pages of a multiple of 16 tokens: 16 rows from a multiple of 16 on lie in one page.
+            const bool runs = p.layer.block_size % 16 == 0;
+            const uint32_t step = row_bytes * kRowsPer;
             bool ok = true;
             if (b0 < b1) lookup(b0);
             for (int32_t b = b0; b < b1 && ok; ++b) {
                 uint32_t rows[kGroups], there[kGroups], all = ~0u;
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
-                    rows[g] = next[g];
+                    rows[g] = next_tok[g] < 0 ? kPast : p.layer.row_of(next_blk[g], next_tok[g], next_col[g]);
                     if (rows[g] == kNoRow) report(p.status, LMKV_ERR_BAD_BLOCK);
                     there[g] = __ballot_sync(0xFFFFFFFFu, rows[g] < kPast);
                     all &= there[g];
@@ -728,7 +739,20 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
                         for (int g = 0; g < kGroups; ++g)
                             if (lane == g) slot[w * kGroups + g] = there[g];
                     }
-                    if (all == ~0u) {
+                    if (all == ~0u && runs) {
+#pragma unroll
+                        for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                const uint32_t row = __shfl_sync(0xFFFFFFFFu, rows[g], u * 16) + rsub;
+                                const uint8_t* src = from + (uint64_t)row * row_bytes;
+#pragma unroll
+                                for (int v = 0; v < kVecs / 2; ++v)
+                                    cp_async16(pattern[(u * (kVecs / 2) + v) % kPatterns] + stage +
+                                                   (g * 32 + (u * (kVecs / 2) + v) / kPatterns * 8) * 128,
+                                               src + v * step);
+                            }
+                    } else if (all == ~0u) {
 #pragma unroll
                         for (int g = 0; g < kGroups; ++g)
 #pragma unroll
@@ -757,9 +781,12 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
         } else {
-            if (warp == 10 && lane == 0 && b1 > b0) {
+            if (warp == 10 && b1 > b0) {
                 constexpr uint32_t qk = instr_desc<T, kBlock, false>(), pv = instr_desc<T, D, true>();
+                // all of tensor memory is this CTA's, so its columns count from 0
+                constexpr uint32_t kScores = 0, kOut = 256;
                 const int32_t blocks = b1 - b0;
+                const uint32_t lead = elect_lead();
                 const Desc q0 = desc_k_major(q_smem), k0 = desc_k_major(kv_smem),
                            v0 = desc_n_major(kv_smem, S::kHalfBytes);
                 // places of the next K and V items in the ring, and their phases
@@ -777,23 +804,27 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
 #pragma unroll
                     for (int s = 0; s < D / 16; ++s) {
                         const uint32_t at = (s >> 2) * S::kHalfBytes + (s & 3) * 32;
-                        mma_ss(tmem + t * 128, a.at(at), k.at(at), qk, s > 0);
+                        mma_ss(lead, kScores + t * 128, a.at(at), k.at(at), qk, s > 0);
                     }
-                    mma_commit(s_full + 8 * t);
+                    mma_commit(lead, s_full + 8 * t);
                 };
-                bool ok = mbar_wait(full, 0, &gave_up);
-                fence_async_shared();                          // the copies, before the products that read them
+                // the copies of an item, before the products that read them
+                auto landed = [&](int32_t st, uint32_t ph) {
+                    const bool there = mbar_wait(full + 8 * st, ph, &gave_up);
+                    fence_async_shared();
+                    return there;
+                };
+                bool ok = landed(0, 0);
                 for (int t = 0; t < tiles && ok; ++t) {
                     ok = mbar_wait(p_ready + 16 * t + 8, 0, &gave_up);
                     if (ok) scores(t, 0);
                 }
-                if (ok) mma_commit(empty);                     // item 0's stage
                 advance(ks, kph);
+                ok = ok && landed(vs, vph);
                 for (int32_t j = 0; j < blocks && ok; ++j) {
                     const bool more = j + 1 < blocks;
                     const Desc v = v0.at(vs * S::kStageBytes);
-                    ok = mbar_wait(full + 8 * vs, vph, &gave_up) && (!more || mbar_wait(full + 8 * ks, kph, &gave_up));
-                    fence_async_shared();
+                    advance(vs, vph);
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         if (t >= tiles || !ok) break;
@@ -805,17 +836,20 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
                             fence_after_sync();
 #pragma unroll
                             for (int s = half * 4; s < half * 4 + 4; ++s)
-                                mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * s, v.at(s * 2048), pv, j > 0 || s > 0);
+                                mma_ts(lead, kOut + t * 128, kScores + t * 128 + 8 * s, v.at(s * 2048), pv, j > 0 || s > 0);
                         }
                         if (!ok) break;
-                        if (t == tiles - 1) mma_commit(empty + 8 * vs);
-                        // issued behind the product that reads the weights from the same columns
-                        if (more) scores(t, ks);
-                        else mma_commit(o_full + 8 * t);
+                        // waits for loads stand where the tensor core has work
+                        if (more) {
+                            if (t == 0) ok = landed(ks, kph);
+                            // issued behind the product that reads the weights from the same columns
+                            if (ok) scores(t, ks);
+                            if (t == 0) ok = ok && landed(vs, vph);
+                        } else {
+                            mma_commit(lead, o_full + 8 * t);
+                        }
                     }
-                    if (ok && more) mma_commit(empty + 8 * ks);
                     advance(ks, kph);
-                    advance(vs, vph);
                 }
             }
         }

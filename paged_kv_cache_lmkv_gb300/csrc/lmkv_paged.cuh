@@ -69,11 +69,11 @@ struct Layer {
         if (blk < 0 || blk >= num_blocks) return -1;
         return (blk * block_size + (tok - (int32_t)(col * (uint32_t)block_size))) * row_bytes;
     }
-    // The row's number in the K half (below 2^32 in any memory: rows of 128
-    // bytes and more), or kNoRow.
-    __device__ __forceinline__ uint32_t token_row(const int32_t* table, int32_t tok) const {
-        const uint32_t col = by_block.div((uint32_t)tok);
-        const int32_t blk = table[col];
+    // The same in two steps, so that the table entry's load need not be waited
+    // for at once: its place, then the row's number in the K half (below 2^32
+    // in any memory: rows of 128 bytes and more), or kNoRow.
+    __device__ __forceinline__ uint32_t column(int32_t tok) const { return by_block.div((uint32_t)tok); }
+    __device__ __forceinline__ uint32_t row_of(int32_t blk, int32_t tok, uint32_t col) const {
         if (blk < 0 || blk >= num_blocks) return kNoRow;
         return (uint32_t)blk * (uint32_t)block_size + ((uint32_t)tok - col * (uint32_t)block_size);
     }
