@@ -171,24 +171,6 @@ attend_rows_kernel(const __grid_constant__ AttendParams p) {
     uint8_t* const ring = smem + warp * (kStages * 2 * kTileBytes);
     const uint32_t ring_u = smem_u32(ring);
 
-    // this thread's two rows: lane / 4 and lane / 4 + 8
-    int32_t limit[2];
-    uint32_t qf[kSteps][4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int32_t rr = (lane >> 2) + 8 * i;
-        const bool on = rr < t.nrows;
-        const int32_t n = (int32_t)p.by_group.div((uint32_t)(t.row0 + (on ? rr : 0)));
-        limit[i] = on ? t.limit0 + t.causal * n : 0;
-        const T* src = p.q.row<T>(t.t0 + n, t.h * group + (t.row0 + rr - n * group));
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            const int e = s * 16 + (lane & 3) * 2;
-            qf[s][i] = on ? load_pair(src + e, p.q_pairs) : 0u;
-            qf[s][2 + i] = on ? load_pair(src + e + 8, p.q_pairs) : 0u;
-        }
-    }
-
     const int32_t chunks = (t.k1 - t.k0 + kChunk - 1) / kChunk;
     const int32_t mine = chunks > warp ? (chunks - warp + kWarps - 1) / kWarps : 0;
     uint32_t there[kStages];       // key masks of the stages (constant indices after unrolling)
@@ -214,17 +196,36 @@ attend_rows_kernel(const __grid_constant__ AttendParams p) {
         return mask;
     };
 
+    // the first rows are on their way while q comes
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+        there[s] = s < mine ? fill(s) : 0u;
+        cp_commit();
+    }
+    // this thread's two rows: lane / 4 and lane / 4 + 8
+    int32_t limit[2];
+    uint32_t qf[kSteps][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int32_t rr = (lane >> 2) + 8 * i;
+        const bool on = rr < t.nrows;
+        const int32_t n = (int32_t)p.by_group.div((uint32_t)(t.row0 + (on ? rr : 0)));
+        limit[i] = on ? t.limit0 + t.causal * n : 0;
+        const T* src = p.q.row<T>(t.t0 + n, t.h * group + (t.row0 + rr - n * group));
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            const int e = s * 16 + (lane & 3) * 2;
+            qf[s][i] = on ? load_pair(src + e, p.q_pairs) : 0u;
+            qf[s][2 + i] = on ? load_pair(src + e + 8, p.q_pairs) : 0u;
+        }
+    }
+
     const float signed_scale = p.scale_log2 * (float)p.scale_sign;
     float o[D / 8][4];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) {
-        there[s] = s < mine ? fill(s) : 0u;
-        cp_commit();
-    }
     for (int32_t i0 = 0; i0 < mine; i0 += kStages) {
 #pragma unroll
         for (int u = 0; u < kStages; ++u) {
@@ -899,21 +900,46 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     const int64_t row = (int64_t)tok * p.q_heads + head;
     const int32_t shared = big || p.prefix_len > 0 ? p.prefix_parts : 0;
     const int32_t parts = shared + (big ? 0 : (q.len + p.own_span - 1) / p.own_span);
+    // m and l of 32 parts at a time, one a lane; then the parts' sums, whose loads
+    // no longer wait for one another
+    const int64_t own_stride = (int64_t)p.seqs.num_req * p.own_cap * p.kv_heads;
+    const int64_t own0 = p.own_part(0, r, row_of_r, h);
+    auto place = [&](int32_t s) { return s < shared ? (int64_t)s * p.rows + row : own0 + (s - shared) * own_stride; };
     float top = -INFINITY, sum = 0.f, acc[kPer] = {};
-    for (int32_t s = 0; s < parts; ++s) {
-        const int64_t at = s < shared ? (int64_t)s * p.rows + row : p.own_part(s - shared, r, row_of_r, h);
-        const float2 v = p.part_ml[at];
-        float x[kPer];
-        const float* src = p.part_o + at * D + lane * kPer;
-        if constexpr (kPer == 4) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(src);
-        else *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(src);
-        const float mn = fmaxf(top, v.x);
-        const float mu = mn == -INFINITY ? 0.f : mn;
-        const float fa = exp2_fast(top - mu), fb = exp2_fast(v.x - mu);
-        top = mn;
-        sum = sum * fa + v.y * fb;
+    for (int32_t s0 = 0; s0 < parts; s0 += 32) {
+        const int32_t n = min(32, parts - s0);
+        const float2 v = lane < n ? p.part_ml[place(s0 + lane)] : make_float2(-INFINITY, 0.f);
+        float mn = v.x;
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) acc[k] = acc[k] * fa + x[k] * fb;
+        for (int d = 16; d > 0; d >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, d));
+        mn = fmaxf(mn, top);
+        const float mu = mn == -INFINITY ? 0.f : mn;
+        const float f = exp2_fast(v.x - mu), before = exp2_fast(top - mu);
+        top = mn;
+        float l = v.y * f;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+        sum = sum * before + l;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) acc[k] *= before;
+        constexpr int kAhead = 8;
+        for (int32_t s = 0; s < n; s += kAhead) {
+            float x[kAhead][kPer];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const float* src = p.part_o + place(min(s0 + s + u, parts - 1)) * D + lane * kPer;
+                if constexpr (kPer == 4) *reinterpret_cast<float4*>(x[u]) = *reinterpret_cast<const float4*>(src);
+                else *reinterpret_cast<float2*>(x[u]) = *reinterpret_cast<const float2*>(src);
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const float fs = __shfl_sync(0xFFFFFFFFu, f, (s + u) & 31);
+                if (s + u < n) {
+#pragma unroll
+                    for (int k = 0; k < kPer; ++k) acc[k] += x[u][k] * fs;
+                }
+            }
+        }
     }
     const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
     T* dst = p.out.row<T>(tok, head) + lane * kPer;

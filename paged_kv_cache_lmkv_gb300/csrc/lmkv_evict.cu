@@ -225,20 +225,56 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 }
 
 constexpr int kSelectThreads = 1024;
+constexpr int kBins = 2048;
+constexpr int kSelectTokens = 50 * 1024;      // keys that fit in shared memory
+
+// Exclusive sums over the CTA of two counts a thread, in thread order.
+__device__ __forceinline__ int2 scan_pairs(int2 mine, int2* warp_sums) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int2 v = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(0xFFFFFFFFu, v.x, d), y = __shfl_up_sync(0xFFFFFFFFu, v.y, d);
+        if (lane >= d) {
+            v.x += x;
+            v.y += y;
+        }
+    }
+    if (lane == 31) warp_sums[warp] = v;
+    __syncthreads();
+    int2 t = warp_sums[lane];
+    const int2 t0 = t;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(0xFFFFFFFFu, t.x, d), y = __shfl_up_sync(0xFFFFFFFFu, t.y, d);
+        if (lane >= d) {
+            t.x += x;
+            t.y += y;
+        }
+    }
+    const int bx = __shfl_sync(0xFFFFFFFFu, t.x - t0.x, warp), by = __shfl_sync(0xFFFFFFFFu, t.y - t0.y, warp);
+    return make_int2(bx + v.x - mine.x, by + v.y - mine.y);
+}
 
 // A CTA per (request, head).  The need-th largest key of the candidates
-// (tokens that are neither sinks nor recent) is found digit by digit, most
-// significant first, with a histogram of 256 counters over the candidates
-// that share the digits found so far; then one ordered pass writes the kept
-// tokens, the first ties among them.
+// (tokens that are neither sinks nor recent) is found digit by digit (11, 11
+// and 10 bits), most significant first, with a histogram over the candidates
+// that share the digits found so far; then every thread counts what it keeps
+// of a run of consecutive tokens, one scan places the runs, and the kept
+// tokens are written in order, the first ties among them.  The keys are read
+// once, into shared memory (kStaged; more than kSelectTokens are read again
+// from L2 instead).  Wide digits are for the counters: scores crowd into few
+// exponents, and threads that meet on a counter take turns.
+template <bool kStaged>
 __global__ void __launch_bounds__(kSelectThreads)
 select_kernel(const __grid_constant__ EvictParams p) {
-    __shared__ uint32_t hist[256];
+    __shared__ uint32_t hist[kBins];
     __shared__ uint32_t digit_s, above_s;
-    __shared__ int32_t warp_sum[2][32];
+    __shared__ int2 warp_sums[32];
+    extern __shared__ uint32_t keys[];
     pdl_launch_dependents();
     pdl_wait();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x;
     const int32_t h = blockIdx.x % p.kv_heads, r = blockIdx.x / p.kv_heads;
     const int32_t len = clamped_len(p, r);
     if (tid == 0 && h == 0) {
@@ -259,111 +295,93 @@ select_kernel(const __grid_constant__ EvictParams p) {
     const int32_t lo = p.sinks, hi = len - p.recent;
     const int32_t need = p.budget - p.sinks - p.recent;       // < hi - lo
     uint32_t prefix = 0, want = (uint32_t)need;               // want: still to take among the prefix's
-    for (int shift = 24; shift >= 0 && need > 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
+    if (kStaged)
+        for (int32_t i = tid; i < len; i += kSelectThreads) keys[i] = order_key(w[i]);
+    auto key_of = [&](int32_t i) { return kStaged ? keys[i] : order_key(w[i]); };
+    int top = 32;                                             // bits above are found
+    while (top > 0 && need > 0) {
+        const int low = top > 11 ? top - 11 : 0;
+        const uint32_t digits = (1u << (top - low)) - 1u;
+        for (int i = tid; i < kBins; i += kSelectThreads) hist[i] = 0;
         __syncthreads();
         for (int32_t i = lo + tid; i < hi; i += kSelectThreads) {
-            const uint32_t k = order_key(w[i]);
-            if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255], 1u);
+            const uint32_t k = key_of(i);
+            if (top == 32 || (k >> top) == (prefix >> top)) atomicAdd(&hist[(k >> low) & digits], 1u);
         }
         __syncthreads();
-        if (warp == 0) {
-            // lane l holds digits 255 - 8 l .. 248 - 8 l, largest first
-            uint32_t c[8], sum = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sum += c[j] = hist[255 - 8 * lane - j];
-            uint32_t before = sum;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, before, d);
-                if (lane >= d) before += y;
-            }
-            before -= sum;                                    // in larger digits
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (before < want && want <= before + c[j]) {
-                    digit_s = 255 - 8 * lane - j;
-                    above_s = before;
-                }
-                before += c[j];
-            }
+        // thread t holds the t-th pair of counters from the top
+        const int hi_bin = kBins - 1 - 2 * tid;
+        const int c0 = (int)hist[hi_bin], c1 = (int)hist[hi_bin - 1];
+        const int2 before = scan_pairs(make_int2(c0 + c1, 0), warp_sums);
+        const uint32_t b0 = (uint32_t)before.x, b1 = b0 + c0;
+        if (b0 < want && want <= b0 + c0) {
+            digit_s = hi_bin;
+            above_s = b0;
+        }
+        if (b1 < want && want <= b1 + c1) {
+            digit_s = hi_bin - 1;
+            above_s = b1;
         }
         __syncthreads();
-        prefix |= digit_s << shift;
+        prefix |= digit_s << low;
         want -= above_s;
+        top = low;
         __syncthreads();
     }
-    // ordered pass: `want` of the keys equal to prefix are kept, all larger ones
-    int32_t out = 0, ties = 0;
-    for (int32_t i0 = 0; i0 < len; i0 += kSelectThreads) {
-        const int32_t i = i0 + tid;
-        bool always = false, tie = false;
-        float s = 0.f;
-        if (i < len) {
-            s = w[i];
-            if (i < lo || i >= hi) {
-                always = true;
-            } else if (need > 0) {
-                const uint32_t k = order_key(s);
-                always = k > prefix;
-                tie = k == prefix;
+    // `want` of the keys equal to prefix are kept, all larger ones.  A run is an odd
+    // number of tokens, so that the threads' places lie in different banks.
+    const int32_t run = ((len + kSelectThreads - 1) / kSelectThreads) | 1;
+    const int32_t from = min(tid * run, len), to = min(from + run, len);
+    int2 count = make_int2(0, 0);                             // kept for certain, ties
+    __syncthreads();
+    for (int32_t i = from; i < to; ++i) {
+        if (i < lo || i >= hi) {
+            ++count.x;
+        } else if (need > 0) {
+            const uint32_t k = key_of(i);
+            count.x += k > prefix;
+            count.y += k == prefix;
+        }
+    }
+    int2 at = scan_pairs(count, warp_sums);
+    for (int32_t i = from; i < to; ++i) {
+        bool keeps = i < lo || i >= hi, tie = false;
+        if (!keeps && need > 0) {
+            const uint32_t k = key_of(i);
+            keeps = k > prefix;
+            tie = k == prefix;
+        }
+        if (keeps || (tie && at.y < (int32_t)want)) {
+            const int32_t slot = at.x + min(at.y, (int32_t)want);
+            if (slot < p.budget) {
+                keep[slot] = i;
+                if (kept != nullptr) kept[slot] = w[i];
             }
         }
-        const uint32_t below = (1u << lane) - 1;
-        const uint32_t tb = __ballot_sync(0xFFFFFFFFu, tie), ab = __ballot_sync(0xFFFFFFFFu, always);
-        if (lane == 0) {
-            warp_sum[0][warp] = __popc(tb);
-            warp_sum[1][warp] = __popc(ab);
-        }
-        __syncthreads();
-        int32_t t_before = 0, a_before = 0, t_all = 0, a_all = 0;
-        {
-            int32_t t = warp_sum[0][lane], a = warp_sum[1][lane];
-            const int32_t t0 = t, a0 = a;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int32_t y = __shfl_up_sync(0xFFFFFFFFu, t, d), z = __shfl_up_sync(0xFFFFFFFFu, a, d);
-                if (lane >= d) {
-                    t += y;
-                    a += z;
-                }
-            }
-            t_all = __shfl_sync(0xFFFFFFFFu, t, 31);
-            a_all = __shfl_sync(0xFFFFFFFFu, a, 31);
-            t_before = __shfl_sync(0xFFFFFFFFu, t - t0, warp);
-            a_before = __shfl_sync(0xFFFFFFFFu, a - a0, warp);
-        }
-        const int32_t t_rank = ties + t_before + __popc(tb & below);          // ties before this token
-        const int32_t t_kept = min(t_rank, (int32_t)want);
-        if (always || (tie && t_rank < (int32_t)want)) {
-            const int32_t at = out + a_before + __popc(ab & below) + t_kept;  // `out` counts no ties
-            if (at < p.budget) {
-                keep[at] = i;
-                if (kept != nullptr) kept[at] = s;
-            }
-        }
-        out += a_all;
-        ties += t_all;
-        __syncthreads();
+        at.x += keeps;
+        at.y += tie;
     }
 }
 
 // ---- compaction ---------------------------------------------------------
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveUnroll = 4;
+constexpr int kMoveDepth = 8;              // batches of rows on their way
 
 // Moves the kept rows of one (request, head, K or V, column piece) to the
 // front of the request's pages, in place.  keep is ascending, so keep[i] >= i
-// and a batch of slots in order may be written once its own rows are read:
-// what later batches read lies behind.  Slots whose token stays (a leading
-// run, as keep[i] - i never falls) are skipped.
+// and a batch of slots in order may be written once its own rows, and those of
+// the batches before it, have been read: what later batches read lies behind.
+// So rows may be fetched as early as one likes: kMoveDepth batches are under
+// way in shared memory (cp.async), each thread storing what it fetched itself,
+// with one barrier a batch, and the tokens and pages of the next ones are
+// looked up before they are needed.  Slots whose token stays (a leading run,
+// as keep[i] - i never falls) are skipped.  Bound by reading and writing the
+// moved rows.
 template <int kBytes>
 __global__ void __launch_bounds__(kMoveThreads)
 compact_kernel(const __grid_constant__ EvictParams p, int32_t pieces, int32_t piece_vecs) {
-    struct __align__(kBytes) Unit {
-        uint8_t b[kBytes];
-    };
+    __shared__ __align__(16) uint8_t ring[kMoveDepth][kMoveThreads * kBytes];
     pdl_launch_dependents();
     pdl_wait();
     int32_t x = blockIdx.x;
@@ -379,7 +397,6 @@ compact_kernel(const __grid_constant__ EvictParams p, int32_t pieces, int32_t pi
         if (threadIdx.x == 0) report(p.status, LMKV_ERR_BAD_POINTER);
         return;
     }
-    base += kv * p.layer.half_bytes() + (int64_t)h * p.head_bytes + (int64_t)piece * piece_vecs * kBytes;
     const int32_t vecs = min(piece_vecs, p.head_bytes / kBytes - piece * piece_vecs);
     const int32_t* table = p.table + (int64_t)r * p.table_stride;
     const int32_t* keep = p.keep + ((int64_t)r * p.kv_heads + h) * p.budget;
@@ -389,39 +406,73 @@ compact_kernel(const __grid_constant__ EvictParams p, int32_t pieces, int32_t pi
         if (keep[mid] == mid) first = mid + 1;
         else end = mid;
     }
-    const int32_t total = (p.budget - first) * vecs;
-    for (int32_t i0 = 0; i0 < total; i0 += kMoveThreads * kMoveUnroll) {
-        Unit v[kMoveUnroll];
-        int64_t to[kMoveUnroll];
-#pragma unroll
-        for (int u = 0; u < kMoveUnroll; ++u) {
-            const int32_t i = i0 + u * kMoveThreads + threadIdx.x;
-            to[u] = -1;
-            if (i < total) {
-                const int32_t s = i / vecs;
-                const int64_t c = (int64_t)(i - s * vecs) * kBytes;
-                const int64_t from = p.layer.token_offset(table, keep[first + s]);
-                const int64_t dst = p.layer.token_offset(table, first + s);
-                if (from < 0 || dst < 0) {
-                    report(p.status, LMKV_ERR_BAD_BLOCK);
-                } else {
-                    v[u] = *reinterpret_cast<const Unit*>(base + from + c);
-                    to[u] = dst + c;
-                }
+    // thread -> (slot of the batch, vector of the piece)
+    const int32_t per_batch = kMoveThreads / vecs;
+    const int32_t mine = threadIdx.x / vecs, vec = threadIdx.x - mine * vecs;
+    const bool idle = mine >= per_batch;
+    base += kv * p.layer.half_bytes() + (int64_t)h * p.head_bytes + ((int64_t)piece * piece_vecs + vec) * kBytes;
+    const int32_t batches = (p.budget - first + per_batch - 1) / per_batch;
+    auto slot_of = [&](int32_t i) {                    // my slot in batch i, or -1
+        const int32_t s = first + i * per_batch + mine;
+        return idle || s >= p.budget ? -1 : s;
+    };
+    uint32_t came = 0;                                 // bit i % 32: batch i's row is on its way
+    auto fetch = [&](int32_t i, int32_t tok) {
+        came &= ~(1u << (i & 31));
+        if (tok >= 0) {
+            const int64_t from = p.layer.token_offset(table, tok);
+            if (from < 0) report(p.status, LMKV_ERR_BAD_BLOCK);
+            else came |= 1u << (i & 31);
+            uint8_t* const to = &ring[i % kMoveDepth][threadIdx.x * kBytes];
+            if (from >= 0) {
+                if constexpr (kBytes == 16) cp_async16(smem_u32(to), base + from);
+                else if constexpr (kBytes == 4)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(base + from) : "memory");
+                else *to = base[from];
             }
         }
-        __syncthreads();
-#pragma unroll
-        for (int u = 0; u < kMoveUnroll; ++u)
-            if (to[u] >= 0) *reinterpret_cast<Unit*>(base + to[u]) = v[u];
-        // the next batch reads behind this one's slots: no barrier needed here
+        cp_commit();
+    };
+    auto token_of = [&](int32_t i) {                   // the token that batch i's slot receives
+        const int32_t s = i < batches ? slot_of(i) : -1;
+        return s >= 0 ? keep[s] : -1;
+    };
+    int32_t ahead[2] = {token_of(0), token_of(1)};     // tokens of the next batches to fetch
+#pragma unroll 1
+    for (int32_t i = 0; i < kMoveDepth - 1; ++i) {
+        const int32_t tok = ahead[0];
+        ahead[0] = ahead[1];
+        ahead[1] = token_of(i + 2);
+        fetch(i, tok);
     }
+#pragma unroll 1
+    for (int32_t i = 0; i < batches; ++i) {
+        int64_t to = -1;
+        if ((came >> (i & 31)) & 1) {
+            to = p.layer.token_offset(table, slot_of(i));
+            if (to < 0) report(p.status, LMKV_ERR_BAD_BLOCK);
+        }
+        cp_wait<kMoveDepth - 2>();
+        __syncthreads();               // batch i and those before it have been read by every thread
+        if (to >= 0) {
+            const uint8_t* const src = &ring[i % kMoveDepth][threadIdx.x * kBytes];
+            if constexpr (kBytes == 16) *reinterpret_cast<int4*>(base + to) = *reinterpret_cast<const int4*>(src);
+            else if constexpr (kBytes == 4) *reinterpret_cast<int32_t*>(base + to) = *reinterpret_cast<const int32_t*>(src);
+            else base[to] = *src;
+        }
+        const int32_t tok = ahead[0];
+        ahead[0] = ahead[1];
+        ahead[1] = token_of(i + kMoveDepth + 1);
+        fetch(i + kMoveDepth - 1, tok);
+    }
+    cp_wait<0>();
 }
 
 template <int kBytes>
 int launch_compact(const EvictParams& p, void* stream) {
     const int32_t vecs = p.head_bytes / kBytes;
-    const int32_t piece = vecs < 4 ? vecs : 4;
+    const int32_t most = 64 / kBytes;                  // 64-byte pieces: more CTAs, whole sectors
+    const int32_t piece = vecs < most ? vecs : most;
     const int32_t pieces = (vecs + piece - 1) / piece;
     return launch(compact_kernel<kBytes>, (int64_t)p.num_req * p.kv_heads * 2 * pieces, kMoveThreads, 0, stream, 1, p,
                   pieces, piece);
@@ -520,7 +571,14 @@ int lmkv_evict_layer(const lmkv_pool_t* pool, int32_t layer, const int32_t* bloc
     p.sinks = sinks;
     p.recent = recent;
     p.head_bytes = pool->head_dim * pool->elem_bytes;
-    rc = launch(select_kernel, (int64_t)num_req * p.kv_heads, kSelectThreads, 0, stream, 1, p);
+    if (max_kv_len <= kSelectTokens) {
+        rc = allow_smem<select_kernel<true>, kSelectTokens * 4>();
+        if (rc == LMKV_OK)
+            rc = launch(select_kernel<true>, (int64_t)num_req * p.kv_heads, kSelectThreads, (size_t)max_kv_len * 4, stream,
+                        1, p);
+    } else {
+        rc = launch(select_kernel<false>, (int64_t)num_req * p.kv_heads, kSelectThreads, 0, stream, 1, p);
+    }
     if (rc != LMKV_OK || max_kv_len <= budget) return rc;
     // a head's row starts on a multiple of its own bytes: the largest unit that divides them
     if (p.head_bytes % 16 == 0) return launch_compact<16>(p, stream);

@@ -505,6 +505,7 @@ def test_evict_long():
     evict_case([9000, 4097, 2500], 2048, 4, 100, kv_heads=1, dim=64)
     evict_case([40000], 100, 4, 10, kv_heads=2, dim=64)
     evict_case([20011], 15000, 0, 0, kv_heads=1, dim=128)
+    evict_case([60001, 300, 51201], 5000, 4, 10, kv_heads=1, dim=64)      # more keys than shared memory holds
 
 
 def test_evict_odd_rows():
