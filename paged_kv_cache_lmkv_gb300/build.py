@@ -13,7 +13,8 @@ LIB = os.path.join(PKG, "liblmkv.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("lmkv_api.cu", "lmkv_cachegen.cu", "lmkv_rotary.cu",
                                            "lmkv_attend.cu", "lmkv_evict.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("lmkv_kernels.cuh", "lmkv_fp8.cuh", "lmkv_internal.h",
-                                                  "lmkv_paged.cuh", "lmkv_mma.cuh", "lmkv_tcgen05.cuh", "lmkv_rotary.cuh",
+                                                  "lmkv_paged.cuh", "lmkv_mma.cuh", "lmkv_tcgen05.cuh", "lmkv_blocks.cuh",
+                                                  "lmkv_rotary.cuh",
                                                   "lmkv_shift.cuh")]
 DEPS += [os.path.join(INCLUDE, "lmkv.h")]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"

@@ -11,8 +11,7 @@
 // at once, tile by tile, and read once for the batch; a request's own pages by
 // its own rows; and a last kernel joins the parts.  Powers are of 2, with
 // scale * log2(e) folded into x.
-#include "lmkv_mma.cuh"
-#include "lmkv_tcgen05.cuh"
+#include "lmkv_blocks.cuh"
 
 #include <cmath>
 
@@ -80,7 +79,7 @@ struct AttendParams {
 constexpr int kRowTile = 16;      // rows of a tile: one mma.sync operand
 constexpr int kWarps = 4;
 constexpr int kChunk = 16;        // keys a warp takes at a time
-constexpr int kStages = 3;
+constexpr int kStages = 2;          // three CTAs an SM: more in flight than with three stages and two CTAs
 constexpr float kLn2 = 0.69314718055994530942f;
 
 // A row tile's place in the batch.
@@ -359,9 +358,7 @@ attend_rows_kernel(const __grid_constant__ AttendParams p) {
 using namespace lmkv_tc;
 
 constexpr int kTileRows = 256;        // two tiles of 128 rows share every K and V block
-constexpr int kBlock = 128;           // keys of a block
 constexpr int kTileThreads = 352;     // softmax 2 x 128, loads 64, products 1 (of 32)
-constexpr int kLoadWarps = 2;         // two groups of 32 rows each
 constexpr int kMaxSegs = 8;           // the prefix and every big request that 256 rows can touch
 constexpr int kMaskSlots = 8;
 
@@ -376,9 +373,8 @@ struct Seg {
 
 template <int D>
 struct TileShape {
-    static constexpr int kHalves = D / 64;
-    static constexpr int kHalfBytes = 128 * 128;
-    static constexpr int kStageBytes = kHalves * kHalfBytes;       // 128 rows of K, V or q
+    static constexpr int kHalfBytes = BlockShape<D>::kHalfBytes;
+    static constexpr int kStageBytes = BlockShape<D>::kBytes;      // 128 rows of K, V or q
     static constexpr int kStages = D == 128 ? 5 : 8;
     static constexpr int kSmem = (2 + kStages) * kStageBytes;
 };
@@ -418,7 +414,7 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
     const uint32_t q_smem = smem_u32(smem), kv_smem = q_smem + 2 * S::kStageBytes;
     if (tid == 0) {
         for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(full + 8 * i, kLoadWarps * 33);
+            mbar_init(full + 8 * i, kCopyArrivals);
             mbar_init(empty + 8 * i, 1);
         }
         for (int t = 0; t < 2; ++t) {
@@ -679,51 +675,18 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
                 }
             }
         } else if (warp < 8 + kLoadWarps) {
-            const int w = warp - 8;
-            constexpr int kVecs = D / 8;             // 16-byte pieces of a row
-            constexpr int kRowsPer = 32 / kVecs;     // rows of a warp-wide copy
-            constexpr int kGroups = kBlock / 32 / kLoadWarps;     // groups of 32 rows of this warp
-            constexpr int kPatterns = 8 / kRowsPer;  // copies until the swizzle repeats
-            constexpr uint32_t kNoRow = Layer::kNoRow, kPast = kNoRow - 1;
-            const int c = lane % kVecs, rsub = lane / kVecs;
-            const uint8_t* const from_k = base + (int64_t)h * (D * 2) + c * 16;
+            BlockCopy<D> rows(p.layer, base, kv_smem, warp - 8);
+            const uint8_t* const from_k = rows.piece(h);
             const uint8_t* const from_v = from_k + p.layer.half_bytes();
-            const uint32_t row_bytes = (uint32_t)p.layer.row_bytes;
-            uint32_t pattern[kPatterns];
-#pragma unroll
-            for (int k = 0; k < kPatterns; ++k) {
-                const int row = k * kRowsPer + rsub;
-                pattern[k] = kv_smem + (c >> 3) * S::kHalfBytes + (w * kGroups * 32 + row) * 128 + (((c & 7) ^ (row & 7)) << 4);
-            }
             int32_t si = 0, item = 0;
-            // table entries of the next block, one block ahead
-            int32_t next_tok[kGroups], next_blk[kGroups];
-            uint32_t next_col[kGroups];
             auto lookup = [&](int32_t b) {
                 while (si + 1 < nseg && b >= segs[si + 1].first) ++si;
-#pragma unroll
-                for (int g = 0; g < kGroups; ++g) {
-                    const int32_t tok = (b - segs[si].first) * kBlock + (w * kGroups + g) * 32 + lane;
-                    const bool on = tok < segs[si].end;
-                    next_tok[g] = on ? tok : -1;
-                    next_col[g] = p.layer.column(on ? tok : 0);
-                    next_blk[g] = on ? segs[si].table[next_col[g]] : 0;
-                }
+                rows.lookup(segs[si].table, (b - segs[si].first) * kBlock, segs[si].end);
             };
-            // Pages of a multiple of 16 tokens: 16 rows from a multiple of 16 on lie in one page.
-            const bool runs = p.layer.block_size % 16 == 0;
-            const uint32_t step = row_bytes * kRowsPer;
             bool ok = true;
             if (b0 < b1) lookup(b0);
             for (int32_t b = b0; b < b1 && ok; ++b) {
-                uint32_t rows[kGroups], there[kGroups], all = ~0u;
-#pragma unroll
-                for (int g = 0; g < kGroups; ++g) {
-                    rows[g] = next_tok[g] < 0 ? kPast : p.layer.row_of(next_blk[g], next_tok[g], next_col[g]);
-                    if (rows[g] == kNoRow) report(p.status, LMKV_ERR_BAD_BLOCK);
-                    there[g] = __ballot_sync(0xFFFFFFFFu, rows[g] < kPast);
-                    all &= there[g];
-                }
+                rows.take(p.status);
                 if (b + 1 < b1) lookup(b + 1);
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv, ++item) {
@@ -732,52 +695,9 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
                         ok = false;
                         break;
                     }
-                    const uint32_t stage = st * S::kStageBytes;
-                    const uint8_t* const from = kv ? from_v : from_k;
-                    if (kv == 0 && lane < kGroups) {
-                        uint32_t* const slot = reinterpret_cast<uint32_t*>(&key_mask[(b - b0) % kMaskSlots]);
-#pragma unroll
-                        for (int g = 0; g < kGroups; ++g)
-                            if (lane == g) slot[w * kGroups + g] = there[g];
-                    }
-                    if (all == ~0u && runs) {
-#pragma unroll
-                        for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                const uint32_t row = __shfl_sync(0xFFFFFFFFu, rows[g], u * 16) + rsub;
-                                const uint8_t* src = from + (uint64_t)row * row_bytes;
-#pragma unroll
-                                for (int v = 0; v < kVecs / 2; ++v)
-                                    cp_async16(pattern[(u * (kVecs / 2) + v) % kPatterns] + stage +
-                                                   (g * 32 + (u * (kVecs / 2) + v) / kPatterns * 8) * 128,
-                                               src + v * step);
-                            }
-                    } else if (all == ~0u) {
-#pragma unroll
-                        for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-                            for (int v = 0; v < kVecs; ++v) {
-                                const uint32_t row = __shfl_sync(0xFFFFFFFFu, rows[g], v * kRowsPer + rsub);
-                                cp_async16(pattern[v % kPatterns] + stage + (g * 32 + v / kPatterns * 8) * 128,
-                                           from + (uint64_t)row * row_bytes);
-                            }
-                    } else {
-#pragma unroll 1
-                        for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-                            for (int v = 0; v < kVecs; ++v) {
-                                const uint32_t r0 = g == 0 ? rows[0] : rows[kGroups - 1];
-                                const uint32_t row = __shfl_sync(0xFFFFFFFFu, r0, v * kRowsPer + rsub);
-                                const bool on = row < kPast;
-                                cp_async16(pattern[v % kPatterns] + stage + (g * 32 + v / kPatterns * 8) * 128,
-                                           from + (on ? (uint64_t)row * row_bytes : 0), on);
-                            }
-                    }
-                    // an arrival of each thread when its copies have landed, and one of the warp for the key mask
-                    mbar_arrive_copies(full + 8 * st);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(full + 8 * st);
+                    if (kv == 0) rows.put_mask(reinterpret_cast<uint32_t*>(&key_mask[(b - b0) % kMaskSlots]));
+                    rows.copy(kv ? from_v : from_k, st * S::kStageBytes);
+                    copies_arrive(full + 8 * st);
                 }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
@@ -961,10 +881,10 @@ struct Plan {
 
 constexpr int32_t kSms = 152;
 
-// Splits of `keys` keys over `ctas` CTAs each: enough for four on every SM,
+// Splits of `keys` keys over `ctas` CTAs each: enough for six on every SM (two rounds of three),
 // none below 128 keys.
 void split(int64_t ctas, int32_t keys, int32_t* splits, int32_t* span) {
-    const int64_t want = (4 * kSms + ctas - 1) / ctas;
+    const int64_t want = (6 * kSms + ctas - 1) / ctas;
     const int64_t most = (keys + 127) / 128;
     const int64_t n = want < most ? want : most;
     int64_t s = (keys + n - 1) / n;

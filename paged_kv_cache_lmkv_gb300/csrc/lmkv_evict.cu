@@ -2,7 +2,7 @@
 // of the tokens that received least of it ("H2O: Heavy-Hitter Oracle for
 // Efficient Generative Inference of Large Language Models", Zhang et al.,
 // 2023).
-#include "lmkv_mma.cuh"
+#include "lmkv_blocks.cuh"
 
 #include <cmath>
 
@@ -10,10 +10,15 @@ namespace {
 
 using namespace lmkv_paged;
 using namespace lmkv_mma;
+using namespace lmkv_tc;
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // ---- weights ------------------------------------------------------------
+//
+// scores_out = decay * scores + column sums of e^(scale q.k - lse).  Products
+// are taken transposed, keys x rows, so that a key's sum stays in one thread
+// (or quad), in an order that never changes.
 
 struct WeighParams {
     Layer layer;
@@ -27,172 +32,416 @@ struct WeighParams {
     int32_t* status;
     float scale_log2, decay;
     int32_t q_heads, kv_heads;
-    int32_t splits, span;          // key splits of a request, keys in each (a multiple of 64)
-    int32_t row_cap;               // rows of a shared-memory row tile (a multiple of 8)
+    int32_t splits, span;          // key splits of a request, keys in each
     bool q_vec;                    // q rows start on 16 bytes
     FastDiv by_group;
+
+    // Row `row` of request q's rows, of KV head h.
+    template <class T>
+    __device__ __forceinline__ const T* q_row(int32_t tok, int32_t head) const {
+        return reinterpret_cast<const T*>(q) + (int64_t)tok * q_token_stride + (int64_t)head * q_head_stride;
+    }
 };
+
+// 16 bytes of a row of q.
+template <class T>
+__device__ __forceinline__ int4 load_q(const T* src, bool vec) {
+    if (vec) return *reinterpret_cast<const int4*>(src);
+    return make_int4((int)load_pair(src, false), (int)load_pair(src + 2, false), (int)load_pair(src + 4, false),
+                     (int)load_pair(src + 6, false));
+}
+
+// A CTA's keys: its request, head and range; false when it has none.  Heads
+// change fastest: the heads' CTAs of the same tokens read the same pages' rows.
+struct WeighPart {
+    Req q;
+    int32_t h, k0, k1;
+    const int32_t* table;
+};
+__device__ __forceinline__ bool weigh_part(const WeighParams& p, WeighPart& x) {
+    x.h = blockIdx.x % p.kv_heads;
+    const int32_t i = blockIdx.x / p.kv_heads;
+    const int32_t r = i % p.seqs.num_req;
+    x.k0 = i / p.seqs.num_req * p.span;
+    x.q = load_req(p.seqs, r);
+    if (!x.q.ok && threadIdx.x == 0) report(p.status, LMKV_ERR_BAD_LENGTH);
+    x.k1 = min(x.k0 + p.span, x.q.len);
+    x.table = p.seqs.table + (int64_t)r * p.seqs.table_stride;
+    return x.k0 < x.k1;
+}
 
 constexpr int kWarps = 4;
 constexpr int kChunk = 16;         // keys a warp takes at a time
-constexpr int kStages = 4;
-constexpr int kMaxRowCap = 128;    // rows of a row tile at most
-constexpr int kSpan = 256;         // keys of a CTA
+constexpr int kRowTile = 64;       // rows whose q is in shared memory at a time
+constexpr int kRowSpan = 1024;     // keys of a CTA
 
-// scores_out = decay * scores + column sums of e^(scale q.k - lse).
-// The products are taken transposed, keys x rows: a warp holds 16 keys as the
-// first operand and runs over the rows (new tokens x heads of the group),
-// eight at a time, so a key's sum stays in one quad's registers and its order
-// is fixed.  K is read once from HBM; a request with more rows than row_cap
-// goes over its CTA's keys again from L2.  With few rows bound by the bytes of K.
+// Few rows (a decode step): mma.sync of 16 keys x 8 rows, bound by the bytes
+// of K, which go from the pages straight into the registers of the first
+// operand.  That operand wants elements 2 i, 2 i + 1 and 2 i + 8, 2 i + 9 of
+// every 16 in lane i of a quad; but a product may take its d elements in any
+// order as long as both operands do, so lane i loads elements 8 i .. 8 i + 7
+// of every 32 as one 16-byte piece for two steps, and q is laid out likewise.
+// No shared memory, no barriers: a warp has one chunk of 16 keys in flight
+// while it works on the one before, and looks up the pages of the one after.
 template <class T, int D>
-__global__ void __launch_bounds__(kWarps * 32)
-weigh_kernel(const __grid_constant__ WeighParams p) {
-    constexpr int kRowBytes = D * 2;
-    constexpr int kVecs = kRowBytes / 16;
-    constexpr int kTileBytes = kChunk * kRowBytes;
-    constexpr int kSteps = D / 16;
-    extern __shared__ __align__(128) uint8_t smem[];
+__global__ void __launch_bounds__(kWarps * 32, 4)
+weigh_rows_kernel(const __grid_constant__ WeighParams p) {
+    constexpr int kPieces = D / 32;
+    // [group of 8 rows][piece][lane]: two steps' second operands
+    __shared__ uint4 qf[kRowTile / 8][kPieces][32];
+    __shared__ float row_lse[kRowTile];         // times log2 e
+    __shared__ int32_t row_limit[kRowTile];
     pdl_launch_dependents();
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // heads change fastest: the heads' CTAs of the same tokens read the same pages' rows
-    const int32_t h = blockIdx.x % p.kv_heads;
-    const int32_t x = blockIdx.x / p.kv_heads;
-    const int32_t r = x % p.seqs.num_req;
-    const int32_t k0 = x / p.seqs.num_req * p.span;
-    const Req q = load_req(p.seqs, r);
-    if (!q.ok && threadIdx.x == 0) report(p.status, LMKV_ERR_BAD_LENGTH);
-    const int32_t k1 = min(k0 + p.span, q.len);
-    if (k0 >= k1) return;
-    const uint8_t* base = p.layer.base();
+    WeighPart x;
+    if (!weigh_part(p, x)) return;
+    const uint8_t* const base = p.layer.base();
     if (base == nullptr && threadIdx.x == 0) report(p.status, LMKV_ERR_BAD_POINTER);
-    const int32_t* table = p.seqs.table + (int64_t)r * p.seqs.table_stride;
     const int32_t group = (int32_t)p.by_group.d;
-    const int32_t rows = base == nullptr ? 0 : q.n * group;
+    const int32_t rows = base == nullptr ? 0 : x.q.n * group;
+    const int64_t half_bytes = (int64_t)x.h * (D * 2) + (lane & 3) * 16;
+    const int64_t at = ((int64_t)x.q.r * p.kv_heads + x.h) * p.score_stride;
 
-    uint8_t* const ring = smem + warp * (kStages * kTileBytes);
-    const uint32_t ring_u = smem_u32(ring);
-    uint8_t* const qt = smem + kWarps * kStages * kTileBytes;                  // [row_cap][D] swizzled
-    const uint32_t qt_u = smem_u32(qt);
-    float* const row_lse = reinterpret_cast<float*>(qt + p.row_cap * kRowBytes);    // times log2 e
-    int32_t* const row_limit = reinterpret_cast<int32_t*>(row_lse + p.row_cap);
-    float* const acc = reinterpret_cast<float*>(row_limit + p.row_cap);             // [span]
-
-    for (int i = threadIdx.x; i < p.span; i += kWarps * 32) acc[i] = 0.f;
-    const int32_t chunks = (k1 - k0 + kChunk - 1) / kChunk;
+    // my two keys of chunk i: lane / 4 and lane / 4 + 8
+    auto key_of = [&](int32_t i) { return x.k0 + (i * kWarps + warp) * kChunk + (lane >> 2); };
+    const int32_t chunks = (x.k1 - x.k0 + kChunk - 1) / kChunk;
     const int32_t mine = chunks > warp ? (chunks - warp + kWarps - 1) / kWarps : 0;
-
-    auto fill = [&](int32_t i) {
-        const int32_t tok = k0 + (i * kWarps + warp) * kChunk + (lane & 15);
-        int64_t off = -1;
-        if (tok < k1) {
-            off = p.layer.token_offset(table, tok);
-            if (off < 0 && lane < 16) report(p.status, LMKV_ERR_BAD_BLOCK);
-        }
-        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, off >= 0) & 0xFFFFu;
-        const uint32_t dst = ring_u + (i % kStages) * kTileBytes;
+    int32_t blk[2];
+    auto lookup = [&](int32_t i) {
 #pragma unroll
-        for (int v = 0; v < kChunk * kVecs / 32; ++v) {
-            const int row = (v * 32 + lane) / kVecs, c = (v * 32 + lane) % kVecs;
-            const int64_t o = __shfl_sync(0xFFFFFFFFu, off, row);
-            cp_async16(dst + swizzled<kRowBytes>(row, c),
-                       o >= 0 ? base + o + (int64_t)h * kRowBytes + c * 16 : base, o >= 0);
+        for (int u = 0; u < 2; ++u) {
+            const int32_t key = key_of(i) + 8 * u;
+            blk[u] = i < mine && key < x.k1 ? x.table[p.layer.column(key)] : -1;
         }
-        return mask;
+    };
+    uint4 kf[2][kPieces];                          // [key][piece] of the chunk in flight
+    uint32_t there = 0;
+    auto fetch = [&](int32_t i) {
+        there = 0;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int32_t key = key_of(i) + 8 * u;
+            uint32_t row = Layer::kNoRow;
+            if (i < mine && key < x.k1) {
+                row = p.layer.row_of(blk[u], key, p.layer.column(key));
+                if (row == Layer::kNoRow) report(p.status, LMKV_ERR_BAD_BLOCK);
+                else there |= 1u << u;
+            }
+            const uint8_t* src = base + (row == Layer::kNoRow ? 0 : (uint64_t)row * (uint64_t)p.layer.row_bytes + half_bytes);
+#pragma unroll
+            for (int c = 0; c < kPieces; ++c)
+                kf[u][c] = row == Layer::kNoRow ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(src + c * 64);
+        }
     };
 
-    for (int32_t row0 = 0; row0 < rows; row0 += p.row_cap) {
-        const int32_t nrows = min(p.row_cap, rows - row0);
-        const int32_t padded = (nrows + 7) & ~7;
+    for (int32_t row0 = 0; row0 == 0 || row0 < rows; row0 += kRowTile) {
+        const int32_t nrows = min(kRowTile, rows - row0);
+        const int32_t groups = (nrows + 7) >> 3;
+        if (rows > 0) {
+            lookup(0);
+            fetch(0);
+            lookup(1);
+        }
         __syncthreads();
-        for (int i = threadIdx.x; i < padded * kVecs; i += kWarps * 32) {
-            const int rr = i / kVecs, c = i % kVecs;
+        for (int i = threadIdx.x; i < groups * 8 * (D / 8); i += kWarps * 32) {
+            const int rr = i / (D / 8), c = i % (D / 8);
             int4 v = make_int4(0, 0, 0, 0);
+            float lse = INFINITY;
+            int32_t limit = 0;
             if (rr < nrows) {
                 const int32_t n = (int32_t)p.by_group.div((uint32_t)(row0 + rr));
-                const int32_t head = h * group + (row0 + rr - n * group);
-                const T* src = reinterpret_cast<const T*>(p.q) + (int64_t)(q.q0 + n) * p.q_token_stride +
-                               (int64_t)head * p.q_head_stride + c * 8;
-                if (p.q_vec) {
-                    v = *reinterpret_cast<const int4*>(src);
-                } else {
-                    v.x = (int)load_pair(src, false);
-                    v.y = (int)load_pair(src + 2, false);
-                    v.z = (int)load_pair(src + 4, false);
-                    v.w = (int)load_pair(src + 6, false);
-                }
+                const int32_t head = x.h * group + (row0 + rr - n * group);
+                v = load_q(p.q_row<T>(x.q.q0 + n, head) + c * 8, p.q_vec);
                 if (c == 0) {
-                    const float e = p.lse[(int64_t)(q.q0 + n) * p.q_heads + head];
-                    row_lse[rr] = e * kLog2e;
-                    row_limit[rr] = e == -INFINITY ? 0 : q.len - q.n + n + 1;
+                    lse = p.lse[(int64_t)(x.q.q0 + n) * p.q_heads + head];
+                    limit = lse == -INFINITY ? 0 : x.q.len - x.q.n + n + 1;
                 }
-            } else if (c == 0) {
-                row_lse[rr] = 0.f;
-                row_limit[rr] = 0;
             }
-            *reinterpret_cast<int4*>(qt + swizzled<kRowBytes>(rr, c)) = v;
+            qf[rr >> 3][c >> 2][(rr & 7) * 4 + (c & 3)] = make_uint4(v.x, v.y, v.z, v.w);
+            if (c == 0) {
+                row_lse[rr] = lse * kLog2e;
+                row_limit[rr] = limit;
+            }
         }
         __syncthreads();
-        uint32_t there[kStages];
+        for (int32_t i = 0; i < mine; ++i) {
+            uint4 k[2][kPieces];
 #pragma unroll
-        for (int s = 0; s < kStages - 1; ++s) {
-            there[s] = s < mine ? fill(s) : 0u;
-            cp_commit();
-        }
-        for (int32_t i0 = 0; i0 < mine; i0 += kStages) {
+            for (int c = 0; c < kPieces; ++c) {
+                k[0][c] = kf[0][c];
+                k[1][c] = kf[1][c];
+            }
+            const uint32_t on = there;
+            const int32_t key = key_of(i);
+            float old[2] = {0.f, 0.f};
 #pragma unroll
-            for (int u = 0; u < kStages; ++u) {
-                const int32_t i = i0 + u;
-                if (i >= mine) break;
-                __syncwarp();
-                constexpr int kAhead = kStages - 1;
-                there[(u + kAhead) % kStages] = i + kAhead < mine ? fill(i + kAhead) : 0u;
-                cp_commit();
-                cp_wait<kStages - 1>();
-                __syncwarp();
-                const uint32_t kt = ring_u + u * kTileBytes;
-                uint32_t kf[kSteps][4];
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s)       // keys 0-7 / 8-15 x d 0-7, then x d 8-15
-                    ldmatrix4(kf[s], kt + swizzled<kRowBytes>(lane & 15, 2 * s + (lane >> 4)));
-                const int32_t local = (i * kWarps + warp) * kChunk + (lane >> 2);
-                const bool ok0 = (there[u] >> (lane >> 2)) & 1, ok1 = (there[u] >> ((lane >> 2) + 8)) & 1;
-                float s0 = 0.f, s1 = 0.f;
-                for (int32_t g = 0; g < padded; g += 8) {
-                    float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int s = 0; s < kSteps; s += 2) {
-                        uint32_t b[4];                 // rows x d of two steps
-                        ldmatrix4(b, qt_u + swizzled<kRowBytes>(g + (lane & 7), 2 * s + (lane >> 3)));
-                        mma16816<T>(c, kf[s], b[0], b[1]);
-                        mma16816<T>(c, kf[s + 1], b[2], b[3]);
-                    }
-                    const int rr = g + (lane & 3) * 2;
-                    const float2 e = *reinterpret_cast<const float2*>(row_lse + rr);
-                    const int2 lim = *reinterpret_cast<const int2*>(row_limit + rr);
-                    const int32_t key = k0 + local;
-                    if (key < lim.x) s0 += exp2_fast(fmaf(c[0], p.scale_log2, -e.x));
-                    if (key < lim.y) s0 += exp2_fast(fmaf(c[1], p.scale_log2, -e.y));
-                    if (key + 8 < lim.x) s1 += exp2_fast(fmaf(c[2], p.scale_log2, -e.x));
-                    if (key + 8 < lim.y) s1 += exp2_fast(fmaf(c[3], p.scale_log2, -e.y));
+            for (int u = 0; u < 2; ++u)
+                if ((lane & 3) == 0 && key + 8 * u < x.k1) {
+                    if (row0 > 0) old[u] = p.scores_out[at + key + 8 * u];
+                    else if (p.decay != 0.f) old[u] = p.decay * p.scores[at + key + 8 * u];
                 }
-                s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, 1);
-                s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, 1);
-                s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, 2);
-                s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, 2);
-                if ((lane & 3) == 0) {
-                    if (ok0) acc[local] += s0;
-                    if (ok1) acc[local + 8] += s1;
+            if (rows > 0) {
+                fetch(i + 1);
+                lookup(i + 2);
+            }
+            float s0 = 0.f, s1 = 0.f;
+            for (int32_t g = 0; g < groups; ++g) {
+                float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j < kPieces; ++j) {
+                    const uint4 b = qf[g][j][lane];
+                    const uint32_t a0[4] = {k[0][j].x, k[1][j].x, k[0][j].y, k[1][j].y};
+                    const uint32_t a1[4] = {k[0][j].z, k[1][j].z, k[0][j].w, k[1][j].w};
+                    mma16816<T>(c, a0, b.x, b.y);
+                    mma16816<T>(c, a1, b.z, b.w);
                 }
+                const int rr = g * 8 + (lane & 3) * 2;
+                const float2 e = *reinterpret_cast<const float2*>(row_lse + rr);
+                const int2 lim = *reinterpret_cast<const int2*>(row_limit + rr);
+                if (key < lim.x) s0 += exp2_fast(fmaf(c[0], p.scale_log2, -e.x));
+                if (key < lim.y) s0 += exp2_fast(fmaf(c[1], p.scale_log2, -e.y));
+                if (key + 8 < lim.x) s1 += exp2_fast(fmaf(c[2], p.scale_log2, -e.x));
+                if (key + 8 < lim.y) s1 += exp2_fast(fmaf(c[3], p.scale_log2, -e.y));
+            }
+            s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, 1);
+            s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, 1);
+            s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, 2);
+            s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, 2);
+            if ((lane & 3) == 0) {
+                if (key < x.k1) p.scores_out[at + key] = old[0] + (on & 1 ? s0 : 0.f);
+                if (key + 8 < x.k1) p.scores_out[at + key + 8] = old[1] + (on & 2 ? s1 : 0.f);
             }
         }
-        cp_wait<0>();
     }
+}
+
+// Many rows (an observation window): tcgen05 products of 128 keys x 128 rows.
+//   warps 0-7   a thread holds a key and sums over the rows, whose scores come
+//               from tensor memory: warps 0-3 take the even blocks, 4-7 the odd
+//   warps 8-9   K blocks through a ring in shared memory
+//   warp 10     issues the products of a block with up to 256 rows, into the
+//               half of tensor memory that the warps of that block have left
+// Bound by the powers and the bytes of K alike; rows beyond 256 go over the
+// CTA's keys again, from L2.
+constexpr int kTileThreads = 352;
+constexpr int kTileRows = 256;
+constexpr int kTileSpan = 1024;       // keys of a CTA
+
+template <int D>
+struct WeighShape {
+    static constexpr int kStages = D == 128 ? 4 : 6;
+    static constexpr int kSmem = (2 + kStages) * BlockShape<D>::kBytes;
+};
+
+template <class T, int D>
+__global__ void __launch_bounds__(kTileThreads, 1)
+weigh_tiles_kernel(const __grid_constant__ WeighParams p) {
+    using S = WeighShape<D>;
+    using B = BlockShape<D>;
+    constexpr int kMaskSlots = 8;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ uint64_t bars[2 * S::kStages + 5];
+    __shared__ uint32_t tmem_base;
+    __shared__ int gave_up;
+    __shared__ int32_t least_limit[2];             // of the pass's rows, by its parity
+    __shared__ uint4 key_mask[kMaskSlots];
+    __shared__ __align__(16) float row_lse[kTileRows];     // minus lse log2 e
+    __shared__ __align__(16) int32_t row_limit[kTileRows];
+    __shared__ float sums[kTileSpan];              // of the passes before
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t full = smem_u32(bars), empty = full + 8 * S::kStages, s_full = empty + 8 * S::kStages,
+                   s_free = s_full + 16, q_ready = s_free + 16;
+    const uint32_t q_smem = smem_u32(smem), k_smem = q_smem + 2 * B::kBytes;
+    if (tid == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(full + 8 * i, kCopyArrivals);
+            mbar_init(empty + 8 * i, 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(s_full + 8 * t, 1);
+            mbar_init(s_free + 8 * t, 4);
+        }
+        mbar_init(q_ready, 8);
+        gave_up = 0;
+        least_limit[0] = least_limit[1] = INT32_MAX;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 10) tmem_alloc<512>(smem_u32(&tmem_base));
+    pdl_wait();
+    WeighPart x;
+    const bool some = weigh_part(p, x);
+    uint8_t* const base = p.layer.base();
+    if (some && base == nullptr && tid == 0) report(p.status, LMKV_ERR_BAD_POINTER);
+    const int32_t group = (int32_t)p.by_group.d;
+    const int32_t rows = base == nullptr ? 0 : x.q.n * group;
+    const int32_t blocks = some ? (x.k1 - x.k0 + kBlock - 1) / kBlock : 0;
+    const int32_t passes = (rows + kTileRows - 1) / kTileRows;
+    const int64_t at = ((int64_t)x.q.r * p.kv_heads + x.h) * p.score_stride;
+    fence_before_sync();
     __syncthreads();
-    const int64_t at = ((int64_t)r * p.kv_heads + h) * p.score_stride + k0;
-    for (int i = threadIdx.x; i < k1 - k0; i += kWarps * 32)
-        p.scores_out[at + i] = p.decay == 0.f ? acc[i] : fmaf(p.decay, p.scores[at + i], acc[i]);
+    fence_after_sync();
+    if (some && passes == 0) {                      // nothing but the decay
+        for (int32_t k = x.k0 + tid; k < x.k1; k += kTileThreads)
+            p.scores_out[at + k] = p.decay == 0.f ? 0.f : p.decay * p.scores[at + k];
+    } else if (some && warp < 8) {
+        const int half = warp >> 2;
+        const uint32_t s_at = tmem_base + ((uint32_t)(warp & 3) << 21) + half * 256;
+        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+        // A wait that gave up (ok false) skips the work and not the barriers, which
+        // the other warps may be waiting at.
+        bool ok = true;
+        int32_t it = 0;
+        for (int32_t pass = 0; pass < passes; ++pass) {
+            const int32_t row0 = pass * kTileRows, nrows = min(kTileRows, rows - row0);
+            {
+                // a row of q for each thread; rows that are not there weigh nothing
+                const bool on = tid < nrows;
+                const int32_t n = (int32_t)p.by_group.div((uint32_t)(row0 + (on ? tid : 0)));
+                const int32_t head = x.h * group + (on ? row0 + tid - n * group : 0);
+                const T* src = p.q_row<T>(x.q.q0 + n, head);
+                const uint32_t dst = q_smem + (tid >> 7) * B::kBytes + (tid & 127) * 128;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    int4 v = make_int4(0, 0, 0, 0);
+                    if (on) v = load_q(src + c * 8, p.q_vec);
+                    const uint32_t to = dst + (c >> 3) * B::kHalfBytes + (((c & 7) ^ (tid & 7)) << 4);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(v.x), "r"(v.y), "r"(v.z),
+                                 "r"(v.w) : "memory");
+                }
+                const float lse = on ? p.lse[(int64_t)(x.q.q0 + n) * p.q_heads + head] : INFINITY;
+                const int32_t limit = !on || lse == -INFINITY ? 0 : x.q.len - x.q.n + n + 1;
+                row_lse[tid] = -lse * kLog2e;
+                row_limit[tid] = limit;
+                if (on) atomicMin(&least_limit[pass & 1], limit);
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_ready);
+                bar_sync(1, 256);                   // lse and limits are there
+            }
+            const int32_t least = least_limit[pass & 1];
+            const int32_t chunks = (nrows + 31) >> 5;
+            for (int32_t i = 0; i < blocks; ++i, ++it) {
+                if ((it & 1) != half || !ok) continue;
+                const int32_t key = x.k0 + i * kBlock + (warp & 3) * 32 + lane;
+                float old = 0.f;
+                const bool last = pass + 1 == passes;
+                if (last && key < x.k1 && p.decay != 0.f) old = p.decay * p.scores[at + key];
+                ok = mbar_wait(s_full + 8 * half, (it >> 1) & 1, &gave_up);
+                if (!ok) continue;
+                if ((warp & 3) == 0 && lane == 0) mbar_arrive(empty + 8 * (it % S::kStages));    // K has been used
+                fence_after_sync();
+                const bool there = (reinterpret_cast<const uint32_t*>(&key_mask[it % kMaskSlots])[warp & 3] >> lane) & 1;
+                const bool whole = x.k0 + i * kBlock + (warp & 3) * 32 + 31 < least;     // every row sees these keys
+                float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                uint32_t y[32], z[32];
+                tmem_ld32(y, s_at);
+                auto add = [&](const uint32_t (&v)[32], int32_t c) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 e = *reinterpret_cast<const float4*>(row_lse + 32 * c + j);
+                        float2 a = fma2(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), sc2, make_float2(e.x, e.y));
+                        float2 b = fma2(make_float2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])), sc2, make_float2(e.z, e.w));
+                        a.x = exp2_fast(a.x);
+                        a.y = exp2_fast(a.y);
+                        b.x = exp2_fast(b.x);
+                        b.y = exp2_fast(b.y);
+                        if (!whole) {
+                            const int4 lim = *reinterpret_cast<const int4*>(row_limit + 32 * c + j);
+                            a.x = key < lim.x ? a.x : 0.f;
+                            a.y = key < lim.y ? a.y : 0.f;
+                            b.x = key < lim.z ? b.x : 0.f;
+                            b.y = key < lim.w ? b.y : 0.f;
+                        }
+                        acc[0] = add2(acc[0], a);
+                        acc[1] = add2(acc[1], b);
+                    }
+                };
+                // the next 32 rows' scores come in while these are summed
+                for (int32_t c = 0; c < chunks; c += 2) {
+                    wait_ld();
+                    loaded(y);
+                    if (c + 1 < chunks) tmem_ld32(z, s_at + 32 * (c + 1));
+                    add(y, c);
+                    if (c + 1 < chunks) {
+                        wait_ld();
+                        loaded(z);
+                        if (c + 2 < chunks) tmem_ld32(y, s_at + 32 * (c + 2));
+                        add(z, c + 1);
+                    }
+                }
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_free + 8 * half);
+                float total = there ? (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y) : 0.f;
+                const int32_t place = i * kBlock + (warp & 3) * 32 + lane;
+                if (pass > 0) total += sums[place];
+                if (!last) sums[place] = total;
+                else if (key < x.k1) p.scores_out[at + key] = old + total;
+            }
+            if (pass + 1 < passes) {
+                // every product with this pass's q is done once both halves' scores have come
+                bar_sync(1, 256);
+                if (tid == 0) least_limit[(pass + 1) & 1] = INT32_MAX;
+                bar_sync(1, 256);
+            }
+        }
+    } else if (some && warp < 8 + kLoadWarps) {
+        BlockCopy<D> k(p.layer, base, k_smem, warp - 8);
+        const uint8_t* const from = k.piece(x.h);
+        const int32_t total = blocks * passes;
+        bool ok = true;
+        int32_t i = 0;                               // block of the pass
+        if (total > 0) k.lookup(x.table, x.k0, x.k1);
+        for (int32_t it = 0; it < total && ok; ++it) {
+            k.take(p.status);
+            if (++i == blocks) i = 0;
+            if (it + 1 < total) k.lookup(x.table, x.k0 + i * kBlock, x.k1);
+            const int st = it % S::kStages;
+            if (it >= S::kStages) ok = mbar_wait(empty + 8 * st, (it / S::kStages - 1) & 1, &gave_up);
+            if (!ok) break;
+            k.put_mask(reinterpret_cast<uint32_t*>(&key_mask[it % kMaskSlots]));
+            k.copy(from, st * B::kBytes);
+            copies_arrive(full + 8 * st);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (some && warp == 10) {
+        constexpr uint32_t id = instr_desc<T, kBlock, false>();
+        const uint32_t lead = elect_lead();
+        const Desc q0 = desc_k_major(q_smem), k0 = desc_k_major(k_smem);
+        bool ok = true;
+        int32_t it = 0;
+        for (int32_t pass = 0; pass < passes && ok; ++pass) {
+            const bool two = rows - pass * kTileRows > 128;
+            ok = mbar_wait(q_ready, pass & 1, &gave_up);
+            for (int32_t i = 0; i < blocks && ok; ++i, ++it) {
+                const int half = it & 1, st = it % S::kStages;
+                ok = mbar_wait(full + 8 * st, (it / S::kStages) & 1, &gave_up) &&
+                     (it < 2 || mbar_wait(s_free + 8 * half, ((it >> 1) - 1) & 1, &gave_up));
+                if (!ok) break;
+                fence_async_shared();
+                fence_after_sync();
+                const Desc a = k0.at(st * B::kBytes);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (t > 0 && !two) break;
+#pragma unroll
+                    for (int s = 0; s < D / 16; ++s) {
+                        const uint32_t to = (s >> 2) * B::kHalfBytes + (s & 3) * 32;
+                        mma_ss(lead, half * 256 + t * 128, a.at(to), q0.at(t * B::kBytes + to), id, s > 0);
+                    }
+                }
+                mma_commit(lead, s_full + 8 * half);
+            }
+        }
+    }
+    __syncwarp();
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    if (tid == 0 && gave_up) report(p.status, LMKV_ERR_TIMEOUT);
+    if (warp == 10) tmem_free<512>(tmem_base);
 }
 
 // ---- selection ----------------------------------------------------------
@@ -478,13 +727,21 @@ int launch_compact(const EvictParams& p, void* stream) {
                   pieces, piece);
 }
 
+// Rows per KV head from which the tile kernel takes a batch: below, the row
+// kernel's products cost less than a tile of 128 rows that is mostly empty.
+constexpr int kTileMinRows = 48;
+
 template <class T, int D>
-int weigh_typed(const WeighParams& p, void* stream) {
-    const size_t smem = (size_t)kWarps * kStages * kChunk * D * 2 + (size_t)p.row_cap * (D * 2 + 8) + (size_t)p.span * 4;
-    constexpr int most = kWarps * kStages * kChunk * D * 2 + kMaxRowCap * (D * 2 + 8) + kSpan * 4;
-    const int rc = allow_smem<weigh_kernel<T, D>, most>();
+int weigh_typed(WeighParams& p, void* stream) {
+    const int64_t rows = (int64_t)(p.seqs.max_new < p.seqs.num_tokens ? p.seqs.max_new : p.seqs.num_tokens) * p.by_group.d;
+    const bool tiles = rows >= kTileMinRows;
+    p.span = tiles ? kTileSpan : kRowSpan;
+    p.splits = (p.seqs.max_kv_len + p.span - 1) / p.span;
+    const int64_t grid = (int64_t)p.seqs.num_req * p.kv_heads * p.splits;
+    if (!tiles) return launch(weigh_rows_kernel<T, D>, grid, kWarps * 32, 0, stream, 1, p);
+    const int rc = allow_smem<weigh_tiles_kernel<T, D>, WeighShape<D>::kSmem>();
     if (rc != LMKV_OK) return rc;
-    return launch(weigh_kernel<T, D>, (int64_t)p.seqs.num_req * p.kv_heads * p.splits, kWarps * 32, smem, stream, 1, p);
+    return launch(weigh_tiles_kernel<T, D>, grid, kTileThreads, WeighShape<D>::kSmem, stream, 1, p);
 }
 
 }  // namespace
@@ -527,10 +784,6 @@ int lmkv_weigh_layer(const lmkv_pool_t* pool, int32_t dtype, int32_t layer, cons
     p.q_heads = num_q_heads;
     p.kv_heads = pool->num_kv_heads;
     p.by_group = FastDiv((uint32_t)(num_q_heads / pool->num_kv_heads));
-    const int64_t rows = (int64_t)batch->max_new * p.by_group.d;
-    p.row_cap = rows < 8 ? 8 : rows > kMaxRowCap ? kMaxRowCap : (int32_t)((rows + 7) / 8 * 8);
-    p.span = kSpan;
-    p.splits = (batch->max_kv_len + p.span - 1) / p.span;
     if (dtype == LMKV_BF16)
         return pool->head_dim == 64 ? weigh_typed<__nv_bfloat16, 64>(p, stream) : weigh_typed<__nv_bfloat16, 128>(p, stream);
     return pool->head_dim == 64 ? weigh_typed<__half, 64>(p, stream) : weigh_typed<__half, 128>(p, stream);

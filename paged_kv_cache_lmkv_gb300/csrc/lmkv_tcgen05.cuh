@@ -177,6 +177,10 @@ __device__ __forceinline__ void mma_commit(uint32_t lead, uint32_t bar) {
         : "memory");
 }
 
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 // The largest of three (a NaN gives way to a number).
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
