@@ -149,7 +149,6 @@ template <class T, int D>
 __global__ void __launch_bounds__(kWarps * 32)
 attend_rows_kernel(const __grid_constant__ AttendParams p) {
     constexpr int kRowBytes = D * 2;
-    constexpr int kVecs = kRowBytes / 16;            // 16-byte pieces of a row
     constexpr int kTileBytes = kChunk * kRowBytes;   // K (or V) rows of a stage
     constexpr int kSteps = D / 16;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -165,8 +164,6 @@ attend_rows_kernel(const __grid_constant__ AttendParams p) {
         t.k1 = t.k0;
     }
     const int32_t group = (int32_t)p.by_group.d;
-    const int64_t half_bytes = p.layer.half_bytes();
-    const int64_t head_bytes = (int64_t)t.h * kRowBytes;
     uint8_t* const ring = smem + warp * (kStages * 2 * kTileBytes);
     const uint32_t ring_u = smem_u32(ring);
 
@@ -174,28 +171,14 @@ attend_rows_kernel(const __grid_constant__ AttendParams p) {
     const int32_t mine = chunks > warp ? (chunks - warp + kWarps - 1) / kWarps : 0;
     uint32_t there[kStages];       // key masks of the stages (constant indices after unrolling)
 
-    auto fill = [&](int32_t i) -> uint32_t {           // my i-th chunk into its stage
-        const int32_t tok = t.k0 + (i * kWarps + warp) * kChunk + (lane & 15);
-        int64_t off = -1;
-        if (tok < t.k1) {
-            off = p.layer.token_offset(t.table, tok);
-            if (off < 0 && lane < 16) report(p.status, LMKV_ERR_BAD_BLOCK);
-        }
-        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, off >= 0) & 0xFFFFu;
-        const uint32_t dst = ring_u + (i % kStages) * (2 * kTileBytes);
-#pragma unroll
-        for (int v = 0; v < kChunk * kVecs / 32; ++v) {
-            const int row = (v * 32 + lane) / kVecs, c = (v * 32 + lane) % kVecs;
-            const int64_t o = __shfl_sync(0xFFFFFFFFu, off, row);
-            const uint8_t* src = o >= 0 ? base + o + head_bytes + c * 16 : base;
-            const uint32_t at = dst + swizzled<kRowBytes>(row, c);
-            cp_async16(at, src, o >= 0);
-            cp_async16(at + kTileBytes, src + (o >= 0 ? half_bytes : 0), o >= 0);
-        }
-        return mask;
+    ChunkCopy<D, true> rows(p.layer, t.table, base, t.h, t.k1);
+    auto key_of = [&](int32_t i) { return t.k0 + (i * kWarps + warp) * kChunk; };       // my i-th chunk
+    auto fill = [&](int32_t i) {                       // into its stage
+        return rows.copy(key_of(i), ring_u + (i % kStages) * (2 * kTileBytes), key_of(i + 1), p.status);
     };
 
     // the first rows are on their way while q comes
+    rows.lookup(key_of(0));
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) {
         there[s] = s < mine ? fill(s) : 0u;

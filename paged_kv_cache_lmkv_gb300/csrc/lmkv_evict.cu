@@ -32,7 +32,7 @@ struct WeighParams {
     int32_t* status;
     float scale_log2, decay;
     int32_t q_heads, kv_heads;
-    int32_t splits, span;          // key splits of a request, keys in each
+    int32_t splits;                // tile kernel: CTAs that share a request's keys; row kernel: a batch's
     bool q_vec;                    // q rows start on 16 bytes
     FastDiv by_group;
 
@@ -51,167 +51,160 @@ __device__ __forceinline__ int4 load_q(const T* src, bool vec) {
                      (int)load_pair(src + 6, false));
 }
 
-// A CTA's keys: its request, head and range; false when it has none.  Heads
-// change fastest: the heads' CTAs of the same tokens read the same pages' rows.
+// A CTA's keys: its request, head and range.
 struct WeighPart {
     Req q;
     int32_t h, k0, k1;
     const int32_t* table;
 };
-__device__ __forceinline__ bool weigh_part(const WeighParams& p, WeighPart& x) {
-    x.h = blockIdx.x % p.kv_heads;
-    const int32_t i = blockIdx.x / p.kv_heads;
-    const int32_t r = i % p.seqs.num_req;
-    x.k0 = i / p.seqs.num_req * p.span;
-    x.q = load_req(p.seqs, r);
-    if (!x.q.ok && threadIdx.x == 0) report(p.status, LMKV_ERR_BAD_LENGTH);
-    x.k1 = min(x.k0 + p.span, x.q.len);
-    x.table = p.seqs.table + (int64_t)r * p.seqs.table_stride;
-    return x.k0 < x.k1;
-}
 
 constexpr int kWarps = 4;
 constexpr int kChunk = 16;         // keys a warp takes at a time
+constexpr int kStages = 2;
 constexpr int kRowTile = 64;       // rows whose q is in shared memory at a time
-constexpr int kRowSpan = 1024;     // keys of a CTA
+constexpr int kUnit = kWarps * kChunk;
+constexpr int kRowCtas = 5;        // CTAs an SM
 
-// Few rows (a decode step): mma.sync of 16 keys x 8 rows, bound by the bytes
-// of K, which go from the pages straight into the registers of the first
-// operand.  That operand wants elements 2 i, 2 i + 1 and 2 i + 8, 2 i + 9 of
-// every 16 in lane i of a quad; but a product may take its d elements in any
-// order as long as both operands do, so lane i loads elements 8 i .. 8 i + 7
-// of every 32 as one 16-byte piece for two steps, and q is laid out likewise.
-// No shared memory, no barriers: a warp has one chunk of 16 keys in flight
-// while it works on the one before, and looks up the pages of the one after.
-template <class T, int D>
-__global__ void __launch_bounds__(kWarps * 32, 4)
+// Few rows (a decode step): mma.sync of 16 keys x 8 rows.  Bound by the bytes
+// of K: every warp runs by itself, 16 keys (a page) at a time through its own
+// ring, and keeps a chunk's keys as the first operand while it goes over the
+// rows, eight at a time; kOne: no request has more than eight, whose q stays
+// in registers.  One round of CTAs takes equal shares of the batch's tokens
+// (find_share): with a CTA per 1024 tokens the last round's idle SMs cost up to a
+// fifth.  Heads change fastest: the heads' CTAs of the same tokens read the
+// same pages' rows.
+template <class T, int D, bool kOne>
+__global__ void __launch_bounds__(kWarps * 32, kRowCtas)
 weigh_rows_kernel(const __grid_constant__ WeighParams p) {
-    constexpr int kPieces = D / 32;
-    // [group of 8 rows][piece][lane]: two steps' second operands
-    __shared__ uint4 qf[kRowTile / 8][kPieces][32];
-    __shared__ float row_lse[kRowTile];         // times log2 e
-    __shared__ int32_t row_limit[kRowTile];
+    constexpr int kRowBytes = D * 2;
+    constexpr int kTileBytes = kChunk * kRowBytes;
+    constexpr int kSteps = D / 16;
+    constexpr int kRows = kOne ? 8 : kRowTile;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ __align__(128) uint8_t qt[kRows * kRowBytes];      // swizzled
+    __shared__ float row_lse[kRows];         // times log2 e
+    __shared__ int32_t row_limit[kRows];
     pdl_launch_dependents();
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    WeighPart x;
-    if (!weigh_part(p, x)) return;
     const uint8_t* const base = p.layer.base();
     if (base == nullptr && threadIdx.x == 0) report(p.status, LMKV_ERR_BAD_POINTER);
     const int32_t group = (int32_t)p.by_group.d;
-    const int32_t rows = base == nullptr ? 0 : x.q.n * group;
-    const int64_t half_bytes = (int64_t)x.h * (D * 2) + (lane & 3) * 16;
-    const int64_t at = ((int64_t)x.q.r * p.kv_heads + x.h) * p.score_stride;
+    const uint32_t ring = smem_u32(smem) + warp * (kStages * kTileBytes), q_u = smem_u32(qt);
+    WeighPart x;
+    x.h = blockIdx.x % p.kv_heads;
+    Share share = find_share(p.seqs, kUnit, blockIdx.x / p.kv_heads, p.splits, p.status);
+    for (; share.n > 0; ++share.r, share.first = 0) {
+        x.q = load_req(p.seqs, share.r);
+        if (!x.q.ok && threadIdx.x == 0) report(p.status, LMKV_ERR_BAD_LENGTH);
+        const int64_t here = min((int64_t)(x.q.len + kUnit - 1) / kUnit - share.first, share.n);
+        if (here <= 0) continue;
+        share.n -= here;
+        x.k0 = (int32_t)share.first * kUnit;
+        x.k1 = min(x.k0 + (int32_t)here * kUnit, x.q.len);
+        x.table = p.seqs.table + (int64_t)share.r * p.seqs.table_stride;
+        const int32_t rows = base == nullptr ? 0 : x.q.n * group;
+        const int64_t at = ((int64_t)x.q.r * p.kv_heads + x.h) * p.score_stride;
+        const int32_t chunks = (x.k1 - x.k0 + kChunk - 1) / kChunk;
+        const int32_t mine = chunks > warp ? (chunks - warp + kWarps - 1) / kWarps : 0;
+        auto key_of = [&](int32_t i) { return x.k0 + (i * kWarps + warp) * kChunk; };       // my i-th chunk
+        ChunkCopy<D, false> copy(p.layer, x.table, base, x.h, x.k1);
+        auto fill = [&](int32_t i) {
+            return copy.copy(key_of(i), ring + (i % kStages) * kTileBytes, key_of(i + 1), p.status);
+        };
 
-    // my two keys of chunk i: lane / 4 and lane / 4 + 8
-    auto key_of = [&](int32_t i) { return x.k0 + (i * kWarps + warp) * kChunk + (lane >> 2); };
-    const int32_t chunks = (x.k1 - x.k0 + kChunk - 1) / kChunk;
-    const int32_t mine = chunks > warp ? (chunks - warp + kWarps - 1) / kWarps : 0;
-    int32_t blk[2];
-    auto lookup = [&](int32_t i) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int32_t key = key_of(i) + 8 * u;
-            blk[u] = i < mine && key < x.k1 ? x.table[p.layer.column(key)] : -1;
-        }
-    };
-    uint4 kf[2][kPieces];                          // [key][piece] of the chunk in flight
-    uint32_t there = 0;
-    auto fetch = [&](int32_t i) {
-        there = 0;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int32_t key = key_of(i) + 8 * u;
-            uint32_t row = Layer::kNoRow;
-            if (i < mine && key < x.k1) {
-                row = p.layer.row_of(blk[u], key, p.layer.column(key));
-                if (row == Layer::kNoRow) report(p.status, LMKV_ERR_BAD_BLOCK);
-                else there |= 1u << u;
+        for (int32_t row0 = 0; row0 == 0 || row0 < rows; row0 += kRows) {
+            const int32_t nrows = min(kRows, rows - row0);
+            const int32_t padded = (nrows + 7) & ~7;
+            uint32_t there[kStages];
+            __syncthreads();
+            copy.lookup(key_of(0));
+    #pragma unroll
+            for (int s = 0; s < kStages - 1; ++s) {
+                there[s] = rows > 0 && s < mine ? fill(s) : 0u;
+                cp_commit();
             }
-            const uint8_t* src = base + (row == Layer::kNoRow ? 0 : (uint64_t)row * (uint64_t)p.layer.row_bytes + half_bytes);
-#pragma unroll
-            for (int c = 0; c < kPieces; ++c)
-                kf[u][c] = row == Layer::kNoRow ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(src + c * 64);
-        }
-    };
-
-    for (int32_t row0 = 0; row0 == 0 || row0 < rows; row0 += kRowTile) {
-        const int32_t nrows = min(kRowTile, rows - row0);
-        const int32_t groups = (nrows + 7) >> 3;
-        if (rows > 0) {
-            lookup(0);
-            fetch(0);
-            lookup(1);
-        }
-        __syncthreads();
-        for (int i = threadIdx.x; i < groups * 8 * (D / 8); i += kWarps * 32) {
-            const int rr = i / (D / 8), c = i % (D / 8);
-            int4 v = make_int4(0, 0, 0, 0);
-            float lse = INFINITY;
-            int32_t limit = 0;
-            if (rr < nrows) {
-                const int32_t n = (int32_t)p.by_group.div((uint32_t)(row0 + rr));
-                const int32_t head = x.h * group + (row0 + rr - n * group);
-                v = load_q(p.q_row<T>(x.q.q0 + n, head) + c * 8, p.q_vec);
+            for (int i = threadIdx.x; i < padded * (D / 8); i += kWarps * 32) {
+                const int rr = i / (D / 8), c = i % (D / 8);
+                int4 v = make_int4(0, 0, 0, 0);
+                float lse = INFINITY;
+                int32_t limit = 0;
+                if (rr < nrows) {
+                    const int32_t n = (int32_t)p.by_group.div((uint32_t)(row0 + rr));
+                    const int32_t head = x.h * group + (row0 + rr - n * group);
+                    v = load_q(p.q_row<T>(x.q.q0 + n, head) + c * 8, p.q_vec);
+                    if (c == 0) {
+                        lse = p.lse[(int64_t)(x.q.q0 + n) * p.q_heads + head];
+                        limit = lse == -INFINITY ? 0 : x.q.len - x.q.n + n + 1;
+                    }
+                }
+                *reinterpret_cast<int4*>(qt + swizzled<kRowBytes>(rr, c)) = v;
                 if (c == 0) {
-                    lse = p.lse[(int64_t)(x.q.q0 + n) * p.q_heads + head];
-                    limit = lse == -INFINITY ? 0 : x.q.len - x.q.n + n + 1;
+                    row_lse[rr] = lse * kLog2e;
+                    row_limit[rr] = limit;
                 }
             }
-            qf[rr >> 3][c >> 2][(rr & 7) * 4 + (c & 3)] = make_uint4(v.x, v.y, v.z, v.w);
-            if (c == 0) {
-                row_lse[rr] = lse * kLog2e;
-                row_limit[rr] = limit;
+            __syncthreads();
+            uint32_t qf[kSteps / 2][4];                    // second operands of two steps
+            if (kOne) {
+    #pragma unroll
+                for (int s = 0; s < kSteps / 2; ++s)
+                    ldmatrix4(qf[s], q_u + swizzled<kRowBytes>(lane & 7, 4 * s + (lane >> 3)));
             }
-        }
-        __syncthreads();
-        for (int32_t i = 0; i < mine; ++i) {
-            uint4 k[2][kPieces];
-#pragma unroll
-            for (int c = 0; c < kPieces; ++c) {
-                k[0][c] = kf[0][c];
-                k[1][c] = kf[1][c];
-            }
-            const uint32_t on = there;
-            const int32_t key = key_of(i);
-            float old[2] = {0.f, 0.f};
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-                if ((lane & 3) == 0 && key + 8 * u < x.k1) {
-                    if (row0 > 0) old[u] = p.scores_out[at + key + 8 * u];
-                    else if (p.decay != 0.f) old[u] = p.decay * p.scores[at + key + 8 * u];
+            for (int32_t i0 = 0; i0 < mine; i0 += kStages) {
+    #pragma unroll
+                for (int u = 0; u < kStages; ++u) {
+                    const int32_t i = i0 + u;
+                    if (i >= mine) break;
+                    __syncwarp();
+                    constexpr int kAhead = kStages - 1;
+                    there[(u + kAhead) % kStages] = rows > 0 && i + kAhead < mine ? fill(i + kAhead) : 0u;
+                    cp_commit();
+                    const int32_t key = key_of(i) + (lane >> 2);      // and key + 8
+                    float old[2] = {0.f, 0.f};
+    #pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if ((lane & 3) == 0 && key + 8 * k < x.k1) {
+                            if (row0 > 0) old[k] = p.scores_out[at + key + 8 * k];
+                            else if (p.decay != 0.f) old[k] = p.decay * p.scores[at + key + 8 * k];
+                        }
+                    cp_wait<kStages - 1>();
+                    __syncwarp();
+                    const uint32_t kt = ring + u * kTileBytes;
+                    uint32_t kf[kSteps][4];
+    #pragma unroll
+                    for (int s = 0; s < kSteps; ++s)       // keys 0-7 / 8-15 x d 0-7, then x d 8-15
+                        ldmatrix4(kf[s], kt + swizzled<kRowBytes>(lane & 15, 2 * s + (lane >> 4)));
+                    float s0 = 0.f, s1 = 0.f;
+    #pragma unroll 1
+                    for (int32_t g = 0; g < padded; g += 8) {
+                        float c[4] = {0.f, 0.f, 0.f, 0.f};
+    #pragma unroll
+                        for (int s = 0; s < kSteps / 2; ++s) {
+                            if (!kOne) ldmatrix4(qf[s], q_u + swizzled<kRowBytes>(g + (lane & 7), 4 * s + (lane >> 3)));
+                            mma16816<T>(c, kf[2 * s], qf[s][0], qf[s][1]);
+                            mma16816<T>(c, kf[2 * s + 1], qf[s][2], qf[s][3]);
+                        }
+                        const int rr = g + (lane & 3) * 2;
+                        const float2 e = *reinterpret_cast<const float2*>(row_lse + rr);
+                        const int2 lim = *reinterpret_cast<const int2*>(row_limit + rr);
+                        if (key < lim.x) s0 += exp2_fast(fmaf(c[0], p.scale_log2, -e.x));
+                        if (key < lim.y) s0 += exp2_fast(fmaf(c[1], p.scale_log2, -e.y));
+                        if (key + 8 < lim.x) s1 += exp2_fast(fmaf(c[2], p.scale_log2, -e.x));
+                        if (key + 8 < lim.y) s1 += exp2_fast(fmaf(c[3], p.scale_log2, -e.y));
+                    }
+                    s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, 1);
+                    s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, 1);
+                    s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, 2);
+                    s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, 2);
+                    if ((lane & 3) == 0) {
+                        if (key < x.k1) p.scores_out[at + key] = old[0] + ((there[u] >> (lane >> 2)) & 1 ? s0 : 0.f);
+                        if (key + 8 < x.k1)
+                            p.scores_out[at + key + 8] = old[1] + ((there[u] >> ((lane >> 2) + 8)) & 1 ? s1 : 0.f);
+                    }
                 }
-            if (rows > 0) {
-                fetch(i + 1);
-                lookup(i + 2);
             }
-            float s0 = 0.f, s1 = 0.f;
-            for (int32_t g = 0; g < groups; ++g) {
-                float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int j = 0; j < kPieces; ++j) {
-                    const uint4 b = qf[g][j][lane];
-                    const uint32_t a0[4] = {k[0][j].x, k[1][j].x, k[0][j].y, k[1][j].y};
-                    const uint32_t a1[4] = {k[0][j].z, k[1][j].z, k[0][j].w, k[1][j].w};
-                    mma16816<T>(c, a0, b.x, b.y);
-                    mma16816<T>(c, a1, b.z, b.w);
-                }
-                const int rr = g * 8 + (lane & 3) * 2;
-                const float2 e = *reinterpret_cast<const float2*>(row_lse + rr);
-                const int2 lim = *reinterpret_cast<const int2*>(row_limit + rr);
-                if (key < lim.x) s0 += exp2_fast(fmaf(c[0], p.scale_log2, -e.x));
-                if (key < lim.y) s0 += exp2_fast(fmaf(c[1], p.scale_log2, -e.y));
-                if (key + 8 < lim.x) s1 += exp2_fast(fmaf(c[2], p.scale_log2, -e.x));
-                if (key + 8 < lim.y) s1 += exp2_fast(fmaf(c[3], p.scale_log2, -e.y));
-            }
-            s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, 1);
-            s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, 1);
-            s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, 2);
-            s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, 2);
-            if ((lane & 3) == 0) {
-                if (key < x.k1) p.scores_out[at + key] = old[0] + (on & 1 ? s0 : 0.f);
-                if (key + 8 < x.k1) p.scores_out[at + key + 8] = old[1] + (on & 2 ? s1 : 0.f);
-            }
+            cp_wait<0>();
         }
     }
 }
@@ -226,7 +219,6 @@ weigh_rows_kernel(const __grid_constant__ WeighParams p) {
 // CTA's keys again, from L2.
 constexpr int kTileThreads = 352;
 constexpr int kTileRows = 256;
-constexpr int kTileSpan = 1024;       // keys of a CTA
 
 template <int D>
 struct WeighShape {
@@ -248,7 +240,6 @@ weigh_tiles_kernel(const __grid_constant__ WeighParams p) {
     __shared__ uint4 key_mask[kMaskSlots];
     __shared__ __align__(16) float row_lse[kTileRows];     // minus lse log2 e
     __shared__ __align__(16) int32_t row_limit[kTileRows];
-    __shared__ float sums[kTileSpan];              // of the passes before
     pdl_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t full = smem_u32(bars), empty = full + 8 * S::kStages, s_full = empty + 8 * S::kStages,
@@ -270,8 +261,20 @@ weigh_tiles_kernel(const __grid_constant__ WeighParams p) {
     }
     if (warp == 10) tmem_alloc<512>(smem_u32(&tmem_base));
     pdl_wait();
+    // equal shares of what the request has, whatever the bound was
     WeighPart x;
-    const bool some = weigh_part(p, x);
+    x.h = blockIdx.x % p.kv_heads;
+    {
+        const int32_t i = blockIdx.x / p.kv_heads;
+        const int32_t r = i % p.seqs.num_req, part = i / p.seqs.num_req;
+        x.q = load_req(p.seqs, r);
+        if (!x.q.ok && tid == 0) report(p.status, LMKV_ERR_BAD_LENGTH);
+        const int64_t units = (x.q.len + kBlock - 1) / kBlock;
+        x.k0 = (int32_t)(units * part / p.splits) * kBlock;
+        x.k1 = min((int32_t)(units * (part + 1) / p.splits) * kBlock, x.q.len);
+        x.table = p.seqs.table + (int64_t)r * p.seqs.table_stride;
+    }
+    const bool some = x.k0 < x.k1;
     uint8_t* const base = p.layer.base();
     if (some && base == nullptr && tid == 0) report(p.status, LMKV_ERR_BAD_POINTER);
     const int32_t group = (int32_t)p.by_group.d;
@@ -326,8 +329,10 @@ weigh_tiles_kernel(const __grid_constant__ WeighParams p) {
                 if ((it & 1) != half || !ok) continue;
                 const int32_t key = x.k0 + i * kBlock + (warp & 3) * 32 + lane;
                 float old = 0.f;
-                const bool last = pass + 1 == passes;
-                if (last && key < x.k1 && p.decay != 0.f) old = p.decay * p.scores[at + key];
+                if (key < x.k1) {
+                    if (pass > 0) old = p.scores_out[at + key];
+                    else if (p.decay != 0.f) old = p.decay * p.scores[at + key];
+                }
                 ok = mbar_wait(s_full + 8 * half, (it >> 1) & 1, &gave_up);
                 if (!ok) continue;
                 if ((warp & 3) == 0 && lane == 0) mbar_arrive(empty + 8 * (it % S::kStages));    // K has been used
@@ -374,14 +379,12 @@ weigh_tiles_kernel(const __grid_constant__ WeighParams p) {
                 fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_free + 8 * half);
-                float total = there ? (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y) : 0.f;
-                const int32_t place = i * kBlock + (warp & 3) * 32 + lane;
-                if (pass > 0) total += sums[place];
-                if (!last) sums[place] = total;
-                else if (key < x.k1) p.scores_out[at + key] = old + total;
+                const float total = there ? (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y) : 0.f;
+                if (key < x.k1) p.scores_out[at + key] = old + total;
             }
             if (pass + 1 < passes) {
-                // every product with this pass's q is done once both halves' scores have come
+                // every product with this pass's q is done once both halves' scores have
+                // come, and what either has written the other may add to
                 bar_sync(1, 256);
                 if (tid == 0) least_limit[(pass + 1) & 1] = INT32_MAX;
                 bar_sync(1, 256);
@@ -735,10 +738,26 @@ template <class T, int D>
 int weigh_typed(WeighParams& p, void* stream) {
     const int64_t rows = (int64_t)(p.seqs.max_new < p.seqs.num_tokens ? p.seqs.max_new : p.seqs.num_tokens) * p.by_group.d;
     const bool tiles = rows >= kTileMinRows;
-    p.span = tiles ? kTileSpan : kRowSpan;
-    p.splits = (p.seqs.max_kv_len + p.span - 1) / p.span;
-    const int64_t grid = (int64_t)p.seqs.num_req * p.kv_heads * p.splits;
-    if (!tiles) return launch(weigh_rows_kernel<T, D>, grid, kWarps * 32, 0, stream, 1, p);
+    const int64_t heads = p.kv_heads, req = p.seqs.num_req;
+    int64_t grid;
+    if (tiles) {
+        // about two CTAs an SM, one after the other
+        const int64_t want = 2 * 152 / (heads * req), most = ((int64_t)p.seqs.max_kv_len + kBlock - 1) / kBlock;
+        p.splits = (int32_t)(want < 1 ? 1 : want > most ? most : want);
+        grid = heads * req * p.splits;
+    } else {
+        const int64_t want = kRowCtas * 152 / heads, most = ((int64_t)p.seqs.max_kv_len + kUnit - 1) / kUnit * req;
+        p.splits = (int32_t)(want < 1 ? 1 : want > most ? most : want);
+        grid = heads * p.splits;
+    }
+    if (!tiles) {
+        constexpr int ring = kWarps * kStages * kChunk * D * 2;
+        int rc = allow_smem<weigh_rows_kernel<T, D, true>, ring>();
+        if (rc == LMKV_OK) rc = allow_smem<weigh_rows_kernel<T, D, false>, ring>();
+        if (rc != LMKV_OK) return rc;
+        return rows <= 8 ? launch(weigh_rows_kernel<T, D, true>, grid, kWarps * 32, ring, stream, 1, p)
+                         : launch(weigh_rows_kernel<T, D, false>, grid, kWarps * 32, ring, stream, 1, p);
+    }
     const int rc = allow_smem<weigh_tiles_kernel<T, D>, WeighShape<D>::kSmem>();
     if (rc != LMKV_OK) return rc;
     return launch(weigh_tiles_kernel<T, D>, grid, kTileThreads, WeighShape<D>::kSmem, stream, 1, p);

@@ -67,6 +67,80 @@ __device__ __forceinline__ uint32_t swizzled(int r, int c) {
     return (uint32_t)(r * kRowBytes + ((c ^ (r & 7)) << 4));
 }
 
+// Chunks of 16 cached tokens' rows of one head (K, or K and V) by one warp into
+// its own shared memory, swizzled; rows that are not there are zeros.  In
+// pages of a multiple of 16 tokens a chunk that begins at a multiple of 16
+// lies in one page: its entry is fetched a chunk ahead, and a copy's address is
+// an addition.
+template <int D, bool kValues>
+struct ChunkCopy {
+    static constexpr int kRowBytes = D * 2;
+    static constexpr int kVecs = kRowBytes / 16;
+    static constexpr int kTileBytes = 16 * kRowBytes;
+    static constexpr int kRowsPer = 32 / kVecs;
+    static constexpr int kPatterns = 8 / kRowsPer;
+
+    const lmkv_paged::Layer& layer;
+    const int32_t* table;
+    const uint8_t* base;         // the layer's K half
+    const uint8_t* mine;         // with this lane's row and piece of a chunk of the head
+    int64_t half_bytes;
+    uint32_t row_bytes;
+    int32_t end;                 // keys
+    bool runs;
+    uint32_t pattern[kPatterns];
+    int32_t next_blk;
+
+    __device__ __forceinline__ ChunkCopy(const lmkv_paged::Layer& l, const int32_t* t, const uint8_t* layer_base,
+                                         int32_t head, int32_t last)
+        : layer(l), table(t), base(layer_base), half_bytes(l.half_bytes()), row_bytes((uint32_t)l.row_bytes), end(last) {
+        const int lane = threadIdx.x & 31, rsub = lane / kVecs, c = lane % kVecs;
+        mine = base + (int64_t)head * kRowBytes + c * 16 + (int64_t)rsub * row_bytes;
+        runs = l.block_size % 16 == 0;
+#pragma unroll
+        for (int k = 0; k < kPatterns; ++k) pattern[k] = swizzled<kRowBytes>(k * kRowsPer + rsub, c);
+        next_blk = -1;
+    }
+    __device__ __forceinline__ void lookup(int32_t key0) {
+        next_blk = runs && key0 < end ? table[layer.column(key0)] : -1;
+    }
+    // The chunk at key0 (looked up before) to dst; then looks up the one at
+    // after.  Returns which of the 16 keys there are.
+    __device__ __forceinline__ uint32_t copy(int32_t key0, uint32_t dst, int32_t after, int32_t* status) {
+        const int lane = threadIdx.x & 31;
+        const int32_t blk = next_blk;
+        lookup(after);
+        if (runs && key0 + 16 <= end && blk >= 0 && blk < layer.num_blocks) {
+            const uint8_t* src = mine + (uint64_t)layer.row_of(blk, key0, layer.column(key0)) * row_bytes;
+#pragma unroll
+            for (int v = 0; v < kVecs / 2; ++v) {
+                const uint32_t at = dst + pattern[v % kPatterns] + v / kPatterns * 8 * kRowBytes;
+                cp_async16(at, src + v * (kRowsPer * row_bytes));
+                if (kValues) cp_async16(at + kTileBytes, src + v * (kRowsPer * row_bytes) + half_bytes);
+            }
+            return 0xFFFFu;
+        }
+        const int32_t tok = key0 + (lane & 15);
+        int64_t off = -1;
+        if (tok < end) {
+            off = layer.token_offset(table, tok);
+            if (off < 0 && lane < 16) lmkv_paged::report(status, LMKV_ERR_BAD_BLOCK);
+        }
+        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, off >= 0) & 0xFFFFu;
+        const uint8_t* const piece = mine - (int64_t)(lane / kVecs) * row_bytes;
+#pragma unroll
+        for (int v = 0; v < kVecs / 2; ++v) {
+            const int row = v * kRowsPer + lane / kVecs;
+            const int64_t o = __shfl_sync(0xFFFFFFFFu, off, row);
+            const uint32_t at = dst + pattern[v % kPatterns] + v / kPatterns * 8 * kRowBytes;
+            const uint8_t* src = o >= 0 ? piece + o : base;
+            cp_async16(at, src, o >= 0);
+            if (kValues) cp_async16(at + kTileBytes, src + (o >= 0 ? half_bytes : 0), o >= 0);
+        }
+        return mask;
+    }
+};
+
 // Two consecutive elements as one word (low half first); one load if `pairs`
 // (4-byte aligned rows).
 template <class T>

@@ -140,6 +140,53 @@ __device__ __forceinline__ int32_t find_request(int32_t num_req, int32_t x, Key 
     return lo;
 }
 
+// An equal share of a batch's cached tokens, in units of `unit` tokens (a
+// request's last one may be short) counted over the requests in turn: units
+// [all * part / parts, all * (part + 1) / parts).  Whatever the lengths are,
+// CTAs that take a share each end together.
+struct Share {
+    int32_t r;          // request of the first unit
+    int64_t first;      // that unit, counted from the request's first
+    int64_t n;          // units
+};
+// Called by a whole warp; reads every request's length.
+__device__ __forceinline__ Share find_share(const Seqs& s, int32_t unit, int32_t part, int32_t parts, int32_t* status) {
+    const int lane = threadIdx.x & 31;
+    int64_t all = 0;
+    for (int32_t i = lane; i < s.num_req; i += 32) {
+        const int32_t len = s.kv_len[i];
+        if (len < 0 || len > s.max_kv_len) report(status, LMKV_ERR_BAD_LENGTH);
+        all += (min(max(len, 0), s.max_kv_len) + unit - 1) / unit;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, d);
+    const int64_t begin = all * part / parts, end = all * (part + 1) / parts;
+    Share x{0, 0, end - begin};
+    if (x.n == 0) return x;
+    int64_t before = 0;
+    for (int32_t r0 = 0; r0 < s.num_req; r0 += 32) {
+        const int32_t i = r0 + lane;
+        const int64_t own = i < s.num_req ? (min(max(s.kv_len[i], 0), s.max_kv_len) + unit - 1) / unit : 0;
+        int64_t upto = own;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+            if (lane >= d) upto += y;
+        }
+        upto += before;
+        const uint32_t votes = __ballot_sync(0xFFFFFFFFu, begin < upto);
+        if (votes != 0) {
+            const int k = __ffs(votes) - 1;
+            x.r = r0 + k;
+            x.first = begin - __shfl_sync(0xFFFFFFFFu, upto - own, k);
+            return x;
+        }
+        before = __shfl_sync(0xFFFFFFFFu, upto, 31);
+    }
+    x.n = 0;      // not reached: begin < all
+    return x;
+}
+
 // ---- element types ------------------------------------------------------
 template <class T>
 struct Elem;
