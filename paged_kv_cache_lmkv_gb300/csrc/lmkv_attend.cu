@@ -485,17 +485,19 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
                 const T* src = p.q.row<T>(tok, head);
                 const uint32_t dst = q_smem + t * S::kStageBytes + (tid & 127) * 128;
                 const uint32_t flip = p.scale_sign < 0 ? 0x80008000u : 0u, all = p.scale_sign == 0 || !live ? 0u : ~0u;
+                int4 qv[D / 8];              // all loads on their way before the first is waited for
+                if (p.q_vec) {
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) qv[c] = *reinterpret_cast<const int4*>(src + c * 8);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c)
+                        qv[c] = make_int4((int)load_pair(src + c * 8, p.q_pairs), (int)load_pair(src + c * 8 + 2, p.q_pairs),
+                                          (int)load_pair(src + c * 8 + 4, p.q_pairs), (int)load_pair(src + c * 8 + 6, p.q_pairs));
+                }
 #pragma unroll
                 for (int c = 0; c < D / 8; ++c) {
-                    int4 v;
-                    if (p.q_vec) {
-                        v = *reinterpret_cast<const int4*>(src + c * 8);
-                    } else {
-                        v.x = (int)load_pair(src + c * 8, p.q_pairs);
-                        v.y = (int)load_pair(src + c * 8 + 2, p.q_pairs);
-                        v.z = (int)load_pair(src + c * 8 + 4, p.q_pairs);
-                        v.w = (int)load_pair(src + c * 8 + 6, p.q_pairs);
-                    }
+                    const int4 v = qv[c];
                     const uint32_t at = dst + (c >> 3) * S::kHalfBytes + (((c & 7) ^ (tid & 7)) << 4);
                     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"((v.x ^ flip) & all),
                                  "r"((v.y ^ flip) & all), "r"((v.z ^ flip) & all), "r"((v.w ^ flip) & all)

@@ -51,6 +51,21 @@ __device__ __forceinline__ int4 load_q(const T* src, bool vec) {
                      (int)load_pair(src + 6, false));
 }
 
+// A whole row of q, all its loads on their way before the first is waited for.
+template <class T, int D>
+__device__ __forceinline__ void load_q_row(int4 (&v)[D / 8], const T* src, bool vec, bool on) {
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) v[c] = make_int4(0, 0, 0, 0);
+    if (!on) return;
+    if (vec) {
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) v[c] = *reinterpret_cast<const int4*>(src + c * 8);
+    } else {
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) v[c] = load_q(src + c * 8, false);
+    }
+}
+
 // A CTA's keys: its request, head and range.
 struct WeighPart {
     Req q;
@@ -305,10 +320,11 @@ weigh_tiles_kernel(const __grid_constant__ WeighParams p) {
                 const int32_t head = x.h * group + (on ? row0 + tid - n * group : 0);
                 const T* src = p.q_row<T>(x.q.q0 + n, head);
                 const uint32_t dst = q_smem + (tid >> 7) * B::kBytes + (tid & 127) * 128;
+                int4 qv[D / 8];
+                load_q_row<T, D>(qv, src, p.q_vec, on);
 #pragma unroll
                 for (int c = 0; c < D / 8; ++c) {
-                    int4 v = make_int4(0, 0, 0, 0);
-                    if (on) v = load_q(src + c * 8, p.q_vec);
+                    const int4 v = qv[c];
                     const uint32_t to = dst + (c >> 3) * B::kHalfBytes + (((c & 7) ^ (tid & 7)) << 4);
                     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(v.x), "r"(v.y), "r"(v.z),
                                  "r"(v.w) : "memory");
@@ -342,7 +358,8 @@ weigh_tiles_kernel(const __grid_constant__ WeighParams p) {
                 float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                 uint32_t y[32], z[32];
                 tmem_ld32(y, s_at);
-                auto add = [&](const uint32_t (&v)[32], int32_t c) {
+                // one path a chunk: a choice within it would keep its powers from overlapping
+                auto add_rows = [&](const uint32_t (&v)[32], int32_t c, auto masked) {
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
                         const float4 e = *reinterpret_cast<const float4*>(row_lse + 32 * c + j);
@@ -352,7 +369,7 @@ weigh_tiles_kernel(const __grid_constant__ WeighParams p) {
                         a.y = exp2_fast(a.y);
                         b.x = exp2_fast(b.x);
                         b.y = exp2_fast(b.y);
-                        if (!whole) {
+                        if constexpr (decltype(masked)::value) {
                             const int4 lim = *reinterpret_cast<const int4*>(row_limit + 32 * c + j);
                             a.x = key < lim.x ? a.x : 0.f;
                             a.y = key < lim.y ? a.y : 0.f;
@@ -362,6 +379,10 @@ weigh_tiles_kernel(const __grid_constant__ WeighParams p) {
                         acc[0] = add2(acc[0], a);
                         acc[1] = add2(acc[1], b);
                     }
+                };
+                auto add = [&](const uint32_t (&v)[32], int32_t c) {
+                    if (whole) add_rows(v, c, std::false_type());
+                    else add_rows(v, c, std::true_type());
                 };
                 // the next 32 rows' scores come in while these are summed
                 for (int32_t c = 0; c < chunks; c += 2) {
