@@ -32,7 +32,7 @@ struct WeighParams {
     int32_t* status;
     float scale_log2, decay;
     int32_t q_heads, kv_heads;
-    int32_t splits;                // tile kernel: CTAs that share a request's keys; row kernel: a batch's
+    int32_t splits;                // shares of the batch's tokens, a CTA each for every head
     bool q_vec;                    // q rows start on 16 bytes
     FastDiv by_group;
 
@@ -51,7 +51,7 @@ __device__ __forceinline__ int4 load_q(const T* src, bool vec) {
                      (int)load_pair(src + 6, false));
 }
 
-// A whole row of q, all its loads on their way before the first is waited for.
+// D elements of a row of q, all their loads on their way before the first is waited for.
 template <class T, int D>
 __device__ __forceinline__ void load_q_row(int4 (&v)[D / 8], const T* src, bool vec, bool on) {
 #pragma unroll
@@ -225,20 +225,52 @@ weigh_rows_kernel(const __grid_constant__ WeighParams p) {
 }
 
 // Many rows (an observation window): tcgen05 products of 128 keys x 128 rows.
-//   warps 0-7   a thread holds a key and sums over the rows, whose scores come
-//               from tensor memory: warps 0-3 take the even blocks, 4-7 the odd
-//   warps 8-9   K blocks through a ring in shared memory
-//   warp 10     issues the products of a block with up to 256 rows, into the
+//   warps 0-15  a thread holds a key and sums over 128 rows, whose scores come
+//               from tensor memory: of the even blocks and the odd in turn
+//               (warps 0-7, 8-15), rows 0-127 and 128-255 (four warps each)
+//   warps 16-17 K blocks through a ring in shared memory
+//   warp 18     issues the products of a block with up to 256 rows, into the
 //               half of tensor memory that the warps of that block have left
-// Bound by the powers and the bytes of K alike; rows beyond 256 go over the
-// CTA's keys again, from L2.
-constexpr int kTileThreads = 352;
+// A power for each (row, key) and the bytes of K bound it alike.  Shares as
+// the row kernel's, a CTA an SM; a request's rows beyond 256 go over the share
+// again, from L2.
+constexpr int kTileThreads = 608;
 constexpr int kTileRows = 256;
 
 template <int D>
 struct WeighShape {
     static constexpr int kStages = D == 128 ? 4 : 6;
     static constexpr int kSmem = (2 + kStages) * BlockShape<D>::kBytes;
+};
+
+// The share's parts in turn: keys of one request at a time.  Every role walks
+// them alike.
+struct WeighWalk {
+    const WeighParams& p;
+    Share share;
+    WeighPart x;
+    int32_t rows, blocks, passes;
+    int64_t at;            // of the part's first key's score
+
+    __device__ __forceinline__ bool next(bool there) {
+        for (; share.n > 0; ++share.r, share.first = 0) {
+            x.q = load_req(p.seqs, share.r);
+            const int64_t here = min((int64_t)(x.q.len + kBlock - 1) / kBlock - share.first, share.n);
+            if (here <= 0) continue;
+            share.n -= here;
+            x.k0 = (int32_t)share.first * kBlock;
+            x.k1 = min(x.k0 + (int32_t)here * kBlock, x.q.len);
+            x.table = p.seqs.table + (int64_t)share.r * p.seqs.table_stride;
+            rows = there ? x.q.n * (int32_t)p.by_group.d : 0;
+            blocks = (int32_t)here;
+            passes = (rows + kTileRows - 1) / kTileRows;
+            at = ((int64_t)share.r * p.kv_heads + x.h) * p.score_stride + x.k0;
+            ++share.r;
+            share.first = 0;
+            return true;
+        }
+        return false;
+    }
 };
 
 template <class T, int D>
@@ -251,10 +283,12 @@ weigh_tiles_kernel(const __grid_constant__ WeighParams p) {
     __shared__ uint64_t bars[2 * S::kStages + 5];
     __shared__ uint32_t tmem_base;
     __shared__ int gave_up;
+    __shared__ Share share_s;
     __shared__ int32_t least_limit[2];             // of the pass's rows, by its parity
     __shared__ uint4 key_mask[kMaskSlots];
     __shared__ __align__(16) float row_lse[kTileRows];     // minus lse log2 e
     __shared__ __align__(16) int32_t row_limit[kTileRows];
+    __shared__ float upper[2][2][kBlock];          // sums over rows 128-255, two blocks of each parity
     pdl_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t full = smem_u32(bars), empty = full + 8 * S::kStages, s_full = empty + 8 * S::kStages,
@@ -267,196 +301,196 @@ weigh_tiles_kernel(const __grid_constant__ WeighParams p) {
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(s_full + 8 * t, 1);
-            mbar_init(s_free + 8 * t, 4);
+            mbar_init(s_free + 8 * t, 8);
         }
-        mbar_init(q_ready, 8);
+        mbar_init(q_ready, 16);
         gave_up = 0;
         least_limit[0] = least_limit[1] = INT32_MAX;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 10) tmem_alloc<512>(smem_u32(&tmem_base));
+    if (warp == 18) tmem_alloc<512>(smem_u32(&tmem_base));
     pdl_wait();
-    // equal shares of what the request has, whatever the bound was
-    WeighPart x;
-    x.h = blockIdx.x % p.kv_heads;
-    {
-        const int32_t i = blockIdx.x / p.kv_heads;
-        const int32_t r = i % p.seqs.num_req, part = i / p.seqs.num_req;
-        x.q = load_req(p.seqs, r);
-        if (!x.q.ok && tid == 0) report(p.status, LMKV_ERR_BAD_LENGTH);
-        const int64_t units = (x.q.len + kBlock - 1) / kBlock;
-        x.k0 = (int32_t)(units * part / p.splits) * kBlock;
-        x.k1 = min((int32_t)(units * (part + 1) / p.splits) * kBlock, x.q.len);
-        x.table = p.seqs.table + (int64_t)r * p.seqs.table_stride;
-    }
-    const bool some = x.k0 < x.k1;
     uint8_t* const base = p.layer.base();
-    if (some && base == nullptr && tid == 0) report(p.status, LMKV_ERR_BAD_POINTER);
-    const int32_t group = (int32_t)p.by_group.d;
-    const int32_t rows = base == nullptr ? 0 : x.q.n * group;
-    const int32_t blocks = some ? (x.k1 - x.k0 + kBlock - 1) / kBlock : 0;
-    const int32_t passes = (rows + kTileRows - 1) / kTileRows;
-    const int64_t at = ((int64_t)x.q.r * p.kv_heads + x.h) * p.score_stride;
+    if (base == nullptr && tid == 0) report(p.status, LMKV_ERR_BAD_POINTER);
+    if (warp == 0) {
+        const Share s = find_share(p.seqs, kBlock, blockIdx.x / p.kv_heads, p.splits, p.status);
+        if (lane == 0) share_s = s;
+    }
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    if (some && passes == 0) {                      // nothing but the decay
-        for (int32_t k = x.k0 + tid; k < x.k1; k += kTileThreads)
-            p.scores_out[at + k] = p.decay == 0.f ? 0.f : p.decay * p.scores[at + k];
-    } else if (some && warp < 8) {
-        const int half = warp >> 2;
-        const uint32_t s_at = tmem_base + ((uint32_t)(warp & 3) << 21) + half * 256;
+    WeighWalk walk{p, share_s};
+    walk.x.h = blockIdx.x % p.kv_heads;
+    const WeighPart& x = walk.x;
+    const int32_t group = (int32_t)p.by_group.d;
+    if (warp < 16) {
+        const int parity = warp >> 3, high = (warp >> 2) & 1;
+        const uint32_t s_at = tmem_base + ((uint32_t)(warp & 3) << 21) + parity * 256 + high * 128;
         const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
         // A wait that gave up (ok false) skips the work and not the barriers, which
         // the other warps may be waiting at.
         bool ok = true;
-        int32_t it = 0;
-        for (int32_t pass = 0; pass < passes; ++pass) {
-            const int32_t row0 = pass * kTileRows, nrows = min(kTileRows, rows - row0);
-            {
-                // a row of q for each thread; rows that are not there weigh nothing
-                const bool on = tid < nrows;
-                const int32_t n = (int32_t)p.by_group.div((uint32_t)(row0 + (on ? tid : 0)));
-                const int32_t head = x.h * group + (on ? row0 + tid - n * group : 0);
-                const T* src = p.q_row<T>(x.q.q0 + n, head);
-                const uint32_t dst = q_smem + (tid >> 7) * B::kBytes + (tid & 127) * 128;
-                int4 qv[D / 8];
-                load_q_row<T, D>(qv, src, p.q_vec, on);
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    const int4 v = qv[c];
-                    const uint32_t to = dst + (c >> 3) * B::kHalfBytes + (((c & 7) ^ (tid & 7)) << 4);
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(v.x), "r"(v.y), "r"(v.z),
-                                 "r"(v.w) : "memory");
-                }
-                const float lse = on ? p.lse[(int64_t)(x.q.q0 + n) * p.q_heads + head] : INFINITY;
-                const int32_t limit = !on || lse == -INFINITY ? 0 : x.q.len - x.q.n + n + 1;
-                row_lse[tid] = -lse * kLog2e;
-                row_limit[tid] = limit;
-                if (on) atomicMin(&least_limit[pass & 1], limit);
-                fence_async_shared();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(q_ready);
-                bar_sync(1, 256);                   // lse and limits are there
+        int32_t it = 0, pass_no = 0;
+        while (walk.next(base != nullptr)) {
+            if (!x.q.ok && tid == 0) report(p.status, LMKV_ERR_BAD_LENGTH);
+            const int32_t keys = x.k1 - x.k0;
+            if (walk.passes == 0) {                 // nothing but the decay
+                for (int32_t k = tid; k < keys; k += 512)
+                    p.scores_out[walk.at + k] = p.decay == 0.f ? 0.f : p.decay * p.scores[walk.at + k];
             }
-            const int32_t least = least_limit[pass & 1];
-            const int32_t chunks = (nrows + 31) >> 5;
-            for (int32_t i = 0; i < blocks; ++i, ++it) {
-                if ((it & 1) != half || !ok) continue;
-                const int32_t key = x.k0 + i * kBlock + (warp & 3) * 32 + lane;
-                float old = 0.f;
-                if (key < x.k1) {
-                    if (pass > 0) old = p.scores_out[at + key];
-                    else if (p.decay != 0.f) old = p.decay * p.scores[at + key];
+            for (int32_t pass = 0; pass < walk.passes; ++pass, ++pass_no) {
+                const int32_t row0 = pass * kTileRows, nrows = min(kTileRows, walk.rows - row0);
+                if (it > 0) {
+                    // every product with the q before is done once all scores have come, and what
+                    // one thread has written to scores_out another may add to
+                    bar_sync(1, 512);
+                    if (tid == 0) least_limit[pass_no & 1] = INT32_MAX;
+                    bar_sync(1, 512);
                 }
-                ok = mbar_wait(s_full + 8 * half, (it >> 1) & 1, &gave_up);
-                if (!ok) continue;
-                if ((warp & 3) == 0 && lane == 0) mbar_arrive(empty + 8 * (it % S::kStages));    // K has been used
-                fence_after_sync();
-                const bool there = (reinterpret_cast<const uint32_t*>(&key_mask[it % kMaskSlots])[warp & 3] >> lane) & 1;
-                const bool whole = x.k0 + i * kBlock + (warp & 3) * 32 + 31 < least;     // every row sees these keys
-                float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                uint32_t y[32], z[32];
-                tmem_ld32(y, s_at);
-                // one path a chunk: a choice within it would keep its powers from overlapping
-                auto add_rows = [&](const uint32_t (&v)[32], int32_t c, auto masked) {
+                {
+                    // half a row of q for each thread; rows that are not there weigh nothing
+                    const int row = tid >> 1, part = tid & 1;
+                    const bool on = row < nrows;
+                    const int32_t n = (int32_t)p.by_group.div((uint32_t)(row0 + (on ? row : 0)));
+                    const int32_t head = x.h * group + (on ? row0 + row - n * group : 0);
+                    int4 qv[D / 16];
+                    load_q_row<T, D / 2>(qv, p.q_row<T>(x.q.q0 + n, head) + part * (D / 2), p.q_vec, on);
+                    const float lse = on ? p.lse[(int64_t)(x.q.q0 + n) * p.q_heads + head] : INFINITY;
+                    const uint32_t dst = q_smem + (row >> 7) * B::kBytes + (row & 127) * 128;
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float4 e = *reinterpret_cast<const float4*>(row_lse + 32 * c + j);
-                        float2 a = fma2(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), sc2, make_float2(e.x, e.y));
-                        float2 b = fma2(make_float2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])), sc2, make_float2(e.z, e.w));
-                        a.x = exp2_fast(a.x);
-                        a.y = exp2_fast(a.y);
-                        b.x = exp2_fast(b.x);
-                        b.y = exp2_fast(b.y);
-                        if constexpr (decltype(masked)::value) {
-                            const int4 lim = *reinterpret_cast<const int4*>(row_limit + 32 * c + j);
-                            a.x = key < lim.x ? a.x : 0.f;
-                            a.y = key < lim.y ? a.y : 0.f;
-                            b.x = key < lim.z ? b.x : 0.f;
-                            b.y = key < lim.w ? b.y : 0.f;
+                    for (int i = 0; i < D / 16; ++i) {
+                        const int c = part * (D / 16) + i;
+                        const uint32_t to = dst + (c >> 3) * B::kHalfBytes + (((c & 7) ^ (row & 7)) << 4);
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(qv[i].x), "r"(qv[i].y),
+                                     "r"(qv[i].z), "r"(qv[i].w) : "memory");
+                    }
+                    const int32_t limit = !on || lse == -INFINITY ? 0 : x.q.len - x.q.n + n + 1;
+                    if (part == 0) {
+                        row_lse[row] = -lse * kLog2e;
+                        row_limit[row] = limit;
+                        if (on) atomicMin(&least_limit[pass_no & 1], limit);
+                    }
+                    fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(q_ready);
+                    bar_sync(1, 512);               // lse and limits are there
+                }
+                const int32_t least = least_limit[pass_no & 1];
+                const int32_t chunks = min(max(nrows - high * 128, 0) + 31, 128) >> 5;
+                for (int32_t i = 0; i < walk.blocks; ++i, ++it) {
+                    if ((it & 1) != parity) continue;
+                    const int32_t place = i * kBlock + (warp & 3) * 32 + lane, key = x.k0 + place;
+                    float old = 0.f;
+                    if (!high && place < keys) {
+                        if (pass > 0) old = p.scores_out[walk.at + place];
+                        else if (p.decay != 0.f) old = p.decay * p.scores[walk.at + place];
+                    }
+                    ok = ok && mbar_wait(s_full + 8 * parity, (it >> 1) & 1, &gave_up);
+                    float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    bool there = false;
+                    if (ok) {
+                        if ((warp & 7) == 0 && lane == 0) mbar_arrive(empty + 8 * (it % S::kStages));    // K has been used
+                        fence_after_sync();
+                        there = (reinterpret_cast<const uint32_t*>(&key_mask[it % kMaskSlots])[warp & 3] >> lane) & 1;
+                        const bool whole = x.k0 + i * kBlock + (warp & 3) * 32 + 31 < least;     // every row sees these keys
+                        // one path a chunk: a choice within it would keep its powers from overlapping
+                        auto add_rows = [&](const uint32_t (&v)[32], int32_t c, auto masked) {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 4) {
+                                const int row = high * 128 + 32 * c + j;
+                                const float4 e = *reinterpret_cast<const float4*>(row_lse + row);
+                                float2 a = fma2(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), sc2,
+                                                make_float2(e.x, e.y));
+                                float2 b = fma2(make_float2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])), sc2,
+                                                make_float2(e.z, e.w));
+                                a.x = exp2_fast(a.x);
+                                a.y = exp2_fast(a.y);
+                                b.x = exp2_fast(b.x);
+                                b.y = exp2_fast(b.y);
+                                if constexpr (decltype(masked)::value) {
+                                    const int4 lim = *reinterpret_cast<const int4*>(row_limit + row);
+                                    a.x = key < lim.x ? a.x : 0.f;
+                                    a.y = key < lim.y ? a.y : 0.f;
+                                    b.x = key < lim.z ? b.x : 0.f;
+                                    b.y = key < lim.w ? b.y : 0.f;
+                                }
+                                acc[0] = add2(acc[0], a);
+                                acc[1] = add2(acc[1], b);
+                            }
+                        };
+                        // what a chunk waits for the scheduler's other three warps fill
+#pragma unroll 1
+                        for (int32_t c = 0; c < chunks; ++c) {
+                            uint32_t y[32];
+                            tmem_ld32(y, s_at + 32 * c);
+                            wait_ld();
+                            loaded(y);
+                            if (whole) add_rows(y, c, std::false_type());
+                            else add_rows(y, c, std::true_type());
                         }
-                        acc[0] = add2(acc[0], a);
-                        acc[1] = add2(acc[1], b);
+                        fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(s_free + 8 * parity);
                     }
-                };
-                auto add = [&](const uint32_t (&v)[32], int32_t c) {
-                    if (whole) add_rows(v, c, std::false_type());
-                    else add_rows(v, c, std::true_type());
-                };
-                // the next 32 rows' scores come in while these are summed
-                for (int32_t c = 0; c < chunks; c += 2) {
-                    wait_ld();
-                    loaded(y);
-                    if (c + 1 < chunks) tmem_ld32(z, s_at + 32 * (c + 1));
-                    add(y, c);
-                    if (c + 1 < chunks) {
-                        wait_ld();
-                        loaded(z);
-                        if (c + 2 < chunks) tmem_ld32(y, s_at + 32 * (c + 2));
-                        add(z, c + 1);
-                    }
+                    float total = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+                    float* const other = &upper[parity][(it >> 1) & 1][(warp & 3) * 32 + lane];
+                    if (high) *other = total;
+                    bar_sync(2 + parity, 256);
+                    if (!high && ok && place < keys) p.scores_out[walk.at + place] = old + (there ? total + *other : 0.f);
                 }
-                fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(s_free + 8 * half);
-                const float total = there ? (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y) : 0.f;
-                if (key < x.k1) p.scores_out[at + key] = old + total;
-            }
-            if (pass + 1 < passes) {
-                // every product with this pass's q is done once both halves' scores have
-                // come, and what either has written the other may add to
-                bar_sync(1, 256);
-                if (tid == 0) least_limit[(pass + 1) & 1] = INT32_MAX;
-                bar_sync(1, 256);
             }
         }
-    } else if (some && warp < 8 + kLoadWarps) {
-        BlockCopy<D> k(p.layer, base, k_smem, warp - 8);
+    } else if (warp < 16 + kLoadWarps) {
+        BlockCopy<D> k(p.layer, base, k_smem, warp - 16);
         const uint8_t* const from = k.piece(x.h);
-        const int32_t total = blocks * passes;
         bool ok = true;
-        int32_t i = 0;                               // block of the pass
-        if (total > 0) k.lookup(x.table, x.k0, x.k1);
-        for (int32_t it = 0; it < total && ok; ++it) {
-            k.take(p.status);
-            if (++i == blocks) i = 0;
-            if (it + 1 < total) k.lookup(x.table, x.k0 + i * kBlock, x.k1);
-            const int st = it % S::kStages;
-            if (it >= S::kStages) ok = mbar_wait(empty + 8 * st, (it / S::kStages - 1) & 1, &gave_up);
-            if (!ok) break;
-            k.put_mask(reinterpret_cast<uint32_t*>(&key_mask[it % kMaskSlots]));
-            k.copy(from, st * B::kBytes);
-            copies_arrive(full + 8 * st);
+        int32_t it = 0;
+        while (ok && walk.next(base != nullptr)) {
+            const int32_t total = walk.blocks * walk.passes;
+            int32_t i = 0;                               // block of the pass
+            if (total > 0) k.lookup(x.table, x.k0, x.k1);
+            for (int32_t n = 0; n < total; ++n, ++it) {
+                k.take(p.status);
+                if (++i == walk.blocks) i = 0;
+                if (n + 1 < total) k.lookup(x.table, x.k0 + i * kBlock, x.k1);
+                const int st = it % S::kStages;
+                if (it >= S::kStages) ok = mbar_wait(empty + 8 * st, (it / S::kStages - 1) & 1, &gave_up);
+                if (!ok) break;
+                k.put_mask(reinterpret_cast<uint32_t*>(&key_mask[it % kMaskSlots]));
+                k.copy(from, st * B::kBytes);
+                copies_arrive(full + 8 * st);
+            }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (some && warp == 10) {
+    } else {
         constexpr uint32_t id = instr_desc<T, kBlock, false>();
         const uint32_t lead = elect_lead();
         const Desc q0 = desc_k_major(q_smem), k0 = desc_k_major(k_smem);
         bool ok = true;
-        int32_t it = 0;
-        for (int32_t pass = 0; pass < passes && ok; ++pass) {
-            const bool two = rows - pass * kTileRows > 128;
-            ok = mbar_wait(q_ready, pass & 1, &gave_up);
-            for (int32_t i = 0; i < blocks && ok; ++i, ++it) {
-                const int half = it & 1, st = it % S::kStages;
-                ok = mbar_wait(full + 8 * st, (it / S::kStages) & 1, &gave_up) &&
-                     (it < 2 || mbar_wait(s_free + 8 * half, ((it >> 1) - 1) & 1, &gave_up));
-                if (!ok) break;
-                fence_async_shared();
-                fence_after_sync();
-                const Desc a = k0.at(st * B::kBytes);
+        int32_t it = 0, pass_no = 0;
+        while (ok && walk.next(base != nullptr)) {
+            for (int32_t pass = 0; pass < walk.passes && ok; ++pass, ++pass_no) {
+                const bool two = walk.rows - pass * kTileRows > 128;
+                ok = mbar_wait(q_ready, pass_no & 1, &gave_up);
+                for (int32_t i = 0; i < walk.blocks && ok; ++i, ++it) {
+                    const int parity = it & 1, st = it % S::kStages;
+                    ok = mbar_wait(full + 8 * st, (it / S::kStages) & 1, &gave_up) &&
+                         (it < 2 || mbar_wait(s_free + 8 * parity, ((it >> 1) - 1) & 1, &gave_up));
+                    if (!ok) break;
+                    fence_async_shared();
+                    fence_after_sync();
+                    const Desc a = k0.at(st * B::kBytes);
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (t > 0 && !two) break;
+                    for (int t = 0; t < 2; ++t) {
+                        if (t > 0 && !two) break;
 #pragma unroll
-                    for (int s = 0; s < D / 16; ++s) {
-                        const uint32_t to = (s >> 2) * B::kHalfBytes + (s & 3) * 32;
-                        mma_ss(lead, half * 256 + t * 128, a.at(to), q0.at(t * B::kBytes + to), id, s > 0);
+                        for (int s = 0; s < D / 16; ++s) {
+                            const uint32_t to = (s >> 2) * B::kHalfBytes + (s & 3) * 32;
+                            mma_ss(lead, parity * 256 + t * 128, a.at(to), q0.at(t * B::kBytes + to), id, s > 0);
+                        }
                     }
+                    mma_commit(lead, s_full + 8 * parity);
                 }
-                mma_commit(lead, s_full + 8 * half);
             }
         }
     }
@@ -465,7 +499,7 @@ weigh_tiles_kernel(const __grid_constant__ WeighParams p) {
     __syncthreads();
     fence_after_sync();
     if (tid == 0 && gave_up) report(p.status, LMKV_ERR_TIMEOUT);
-    if (warp == 10) tmem_free<512>(tmem_base);
+    if (warp == 18) tmem_free<512>(tmem_base);
 }
 
 // ---- selection ----------------------------------------------------------
@@ -760,17 +794,11 @@ int weigh_typed(WeighParams& p, void* stream) {
     const int64_t rows = (int64_t)(p.seqs.max_new < p.seqs.num_tokens ? p.seqs.max_new : p.seqs.num_tokens) * p.by_group.d;
     const bool tiles = rows >= kTileMinRows;
     const int64_t heads = p.kv_heads, req = p.seqs.num_req;
-    int64_t grid;
-    if (tiles) {
-        // about two CTAs an SM, one after the other
-        const int64_t want = 2 * 152 / (heads * req), most = ((int64_t)p.seqs.max_kv_len + kBlock - 1) / kBlock;
-        p.splits = (int32_t)(want < 1 ? 1 : want > most ? most : want);
-        grid = heads * req * p.splits;
-    } else {
-        const int64_t want = kRowCtas * 152 / heads, most = ((int64_t)p.seqs.max_kv_len + kUnit - 1) / kUnit * req;
-        p.splits = (int32_t)(want < 1 ? 1 : want > most ? most : want);
-        grid = heads * p.splits;
-    }
+    // one round of CTAs
+    const int64_t unit = tiles ? kBlock : kUnit;
+    const int64_t want = (tiles ? 1 : kRowCtas) * 152 / heads, most = ((int64_t)p.seqs.max_kv_len + unit - 1) / unit * req;
+    p.splits = (int32_t)(want < 1 ? 1 : want > most ? most : want);
+    const int64_t grid = heads * p.splits;
     if (!tiles) {
         constexpr int ring = kWarps * kStages * kChunk * D * 2;
         int rc = allow_smem<weigh_rows_kernel<T, D, true>, ring>();
