@@ -31,6 +31,7 @@ struct WeighParams {
     int64_t score_stride;
     int32_t* status;
     float scale_log2, decay;
+    float lse_scale;               // 1 / scale (tile kernel)
     int32_t q_heads, kv_heads;
     int32_t splits;                // shares of the batch's tokens, a CTA each for every head
     bool q_vec;                    // q rows start on 16 bytes
@@ -231,17 +232,36 @@ weigh_rows_kernel(const __grid_constant__ WeighParams p) {
 //   warps 16-17 K blocks through a ring in shared memory
 //   warp 18     issues the products of a block with up to 256 rows, into the
 //               half of tensor memory that the warps of that block have left
-// A power for each (row, key) and the bytes of K bound it alike.  Shares as
-// the row kernel's, a CTA an SM; a request's rows beyond 256 go over the share
-// again, from L2.
+// The product brings -lse along: 16 more columns, of q the three parts of
+// -lse / scale that the type can hold, of k what they count for (extra_parts),
+// so that a thread needs nothing but the scores: reading 128 rows' lse from
+// shared memory took as much of its bandwidth as the product's operands do,
+// and bound the kernel (2350 cycles a block, of which the powers take 1024).
+// Shares as the row kernel's, a CTA an SM; a request's rows beyond 256 go over
+// the share again, from L2.
 constexpr int kTileThreads = 608;
 constexpr int kTileRows = 256;
 
 template <int D>
 struct WeighShape {
     static constexpr int kStages = D == 128 ? 4 : 6;
-    static constexpr int kSmem = (2 + kStages) * BlockShape<D>::kBytes;
+    static constexpr int kQBytes = kTileRows * D * 2;              // [half of 64 columns][256 rows][128 bytes]
+    static constexpr int kExtraQ = kQBytes + kStages * BlockShape<D>::kBytes;
+    static constexpr int kExtraK = kExtraQ + kTileRows * 32;
+    static constexpr int kSmem = kExtraK + kBlock * 32;
 };
+
+// x as a sum of three numbers of type T, each times its weight: hi 2^10 + mid +
+// lo 2^-10.  fp16 parts reach +-2^26 and hold 33 bits of it, bf16 parts 24 bits of any fp32.
+template <class T>
+__device__ __forceinline__ void extra_parts(float x, uint32_t* hi_mid, uint32_t* lo) {
+    const T hi = Elem<T>::from_float(x * 0x1p-10f);
+    float rest = isfinite(x) ? x - Elem<T>::to_float(hi) * 0x1p10f : 0.f;
+    const T mid = Elem<T>::from_float(rest);
+    rest -= Elem<T>::to_float(mid);
+    *hi_mid = Elem<T>::pack(Elem<T>::to_float(hi), Elem<T>::to_float(mid));
+    *lo = Elem<T>::pack(rest * 0x1p10f, 0.f);
+}
 
 // The share's parts in turn: keys of one request at a time.  Every role walks
 // them alike.
@@ -286,14 +306,19 @@ weigh_tiles_kernel(const __grid_constant__ WeighParams p) {
     __shared__ Share share_s;
     __shared__ int32_t least_limit[2];             // of the pass's rows, by its parity
     __shared__ uint4 key_mask[kMaskSlots];
-    __shared__ __align__(16) float row_lse[kTileRows];     // minus lse log2 e
     __shared__ __align__(16) int32_t row_limit[kTileRows];
     __shared__ float upper[2][2][kBlock];          // sums over rows 128-255, two blocks of each parity
     pdl_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t full = smem_u32(bars), empty = full + 8 * S::kStages, s_full = empty + 8 * S::kStages,
                    s_free = s_full + 16, q_ready = s_free + 16;
-    const uint32_t q_smem = smem_u32(smem), k_smem = q_smem + 2 * B::kBytes;
+    const uint32_t q_smem = smem_u32(smem), k_smem = q_smem + S::kQBytes;
+    if (tid < kBlock) {
+        // every key's extra columns: what the parts of -lse / scale count for
+        *reinterpret_cast<uint4*>(smem + S::kExtraK + plain16_offset(tid, 0)) =
+            make_uint4(Elem<T>::pack(0x1p10f, 1.f), Elem<T>::pack(0x1p-10f, 0.f), 0u, 0u);
+        *reinterpret_cast<uint4*>(smem + S::kExtraK + plain16_offset(tid, 1)) = make_uint4(0u, 0u, 0u, 0u);
+    }
     if (tid == 0) {
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(full + 8 * i, kCopyArrivals);
@@ -356,24 +381,29 @@ weigh_tiles_kernel(const __grid_constant__ WeighParams p) {
                     int4 qv[D / 16];
                     load_q_row<T, D / 2>(qv, p.q_row<T>(x.q.q0 + n, head) + part * (D / 2), p.q_vec, on);
                     const float lse = on ? p.lse[(int64_t)(x.q.q0 + n) * p.q_heads + head] : INFINITY;
-                    const uint32_t dst = q_smem + (row >> 7) * B::kBytes + (row & 127) * 128;
+                    const uint32_t dst = q_smem + row * 128;
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {
                         const int c = part * (D / 16) + i;
-                        const uint32_t to = dst + (c >> 3) * B::kHalfBytes + (((c & 7) ^ (row & 7)) << 4);
+                        const uint32_t to = dst + (c >> 3) * (kTileRows * 128) + (((c & 7) ^ (row & 7)) << 4);
                         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(qv[i].x), "r"(qv[i].y),
                                      "r"(qv[i].z), "r"(qv[i].w) : "memory");
                     }
                     const int32_t limit = !on || lse == -INFINITY ? 0 : x.q.len - x.q.n + n + 1;
-                    if (part == 0) {
-                        row_lse[row] = -lse * kLog2e;
-                        row_limit[row] = limit;
-                        if (on) atomicMin(&least_limit[pass_no & 1], limit);
+                    {
+                        // a row that sees nothing weighs nothing: as one of infinite lse
+                        uint4 e = make_uint4(0u, 0u, 0u, 0u);
+                        if (part == 0)
+                            extra_parts<T>(-(lse == -INFINITY ? INFINITY : lse) * p.lse_scale, &e.x, &e.y);
+                        *reinterpret_cast<uint4*>(smem + S::kExtraQ + plain16_offset(row, part)) = e;
                     }
+                    if (part == 0) row_limit[row] = limit;
+                    const int32_t least_here = __reduce_min_sync(0xFFFFFFFFu, on ? limit : INT32_MAX);
+                    if (lane == 0) atomicMin(&least_limit[pass_no & 1], least_here);
                     fence_async_shared();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(q_ready);
-                    bar_sync(1, 512);               // lse and limits are there
+                    bar_sync(1, 512);               // the limits are there
                 }
                 const int32_t least = least_limit[pass_no & 1];
                 const int32_t chunks = min(max(nrows - high * 128, 0) + 31, 128) >> 5;
@@ -397,18 +427,14 @@ weigh_tiles_kernel(const __grid_constant__ WeighParams p) {
                         auto add_rows = [&](const uint32_t (&v)[32], int32_t c, auto masked) {
 #pragma unroll
                             for (int j = 0; j < 32; j += 4) {
-                                const int row = high * 128 + 32 * c + j;
-                                const float4 e = *reinterpret_cast<const float4*>(row_lse + row);
-                                float2 a = fma2(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), sc2,
-                                                make_float2(e.x, e.y));
-                                float2 b = fma2(make_float2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])), sc2,
-                                                make_float2(e.z, e.w));
+                                float2 a = mul2(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), sc2);
+                                float2 b = mul2(make_float2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])), sc2);
                                 a.x = exp2_fast(a.x);
                                 a.y = exp2_fast(a.y);
                                 b.x = exp2_fast(b.x);
                                 b.y = exp2_fast(b.y);
                                 if constexpr (decltype(masked)::value) {
-                                    const int4 lim = *reinterpret_cast<const int4*>(row_limit + row);
+                                    const int4 lim = *reinterpret_cast<const int4*>(row_limit + high * 128 + 32 * c + j);
                                     a.x = key < lim.x ? a.x : 0.f;
                                     a.y = key < lim.y ? a.y : 0.f;
                                     b.x = key < lim.z ? b.x : 0.f;
@@ -463,9 +489,10 @@ weigh_tiles_kernel(const __grid_constant__ WeighParams p) {
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
-        constexpr uint32_t id = instr_desc<T, kBlock, false>();
+        constexpr uint32_t id128 = instr_desc<T, 128, false>(), id256 = instr_desc<T, 256, false>();
         const uint32_t lead = elect_lead();
         const Desc q0 = desc_k_major(q_smem), k0 = desc_k_major(k_smem);
+        const Desc qx = desc_plain16(q_smem + S::kExtraQ), kx = desc_plain16(q_smem + S::kExtraK);
         bool ok = true;
         int32_t it = 0, pass_no = 0;
         while (ok && walk.next(base != nullptr)) {
@@ -480,15 +507,12 @@ weigh_tiles_kernel(const __grid_constant__ WeighParams p) {
                     fence_async_shared();
                     fence_after_sync();
                     const Desc a = k0.at(st * B::kBytes);
+                    const uint32_t id = two ? id256 : id128;
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (t > 0 && !two) break;
-#pragma unroll
-                        for (int s = 0; s < D / 16; ++s) {
-                            const uint32_t to = (s >> 2) * B::kHalfBytes + (s & 3) * 32;
-                            mma_ss(lead, parity * 256 + t * 128, a.at(to), q0.at(t * B::kBytes + to), id, s > 0);
-                        }
-                    }
+                    for (int s = 0; s < D / 16; ++s)
+                        mma_ss(lead, parity * 256, a.at((s >> 2) * B::kHalfBytes + (s & 3) * 32),
+                               q0.at((s >> 2) * (kTileRows * 128) + (s & 3) * 32), id, s > 0);
+                    mma_ss(lead, parity * 256, kx, qx, id, true);
                     mma_commit(lead, s_full + 8 * parity);
                 }
             }
@@ -792,7 +816,9 @@ constexpr int kTileMinRows = 48;
 template <class T, int D>
 int weigh_typed(WeighParams& p, void* stream) {
     const int64_t rows = (int64_t)(p.seqs.max_new < p.seqs.num_tokens ? p.seqs.max_new : p.seqs.num_tokens) * p.by_group.d;
-    const bool tiles = rows >= kTileMinRows;
+    // (the tile kernel carries -lse / scale, in fp16 up to 2^26: lse up to 16384 at the smallest scale it takes)
+    const bool tiles = rows >= kTileMinRows && std::fabs(p.scale_log2) >= 0x1p-12f * kLog2e;
+    p.lse_scale = kLog2e / p.scale_log2;
     const int64_t heads = p.kv_heads, req = p.seqs.num_req;
     // one round of CTAs
     const int64_t unit = tiles ? kBlock : kUnit;

@@ -137,6 +137,14 @@ __device__ __forceinline__ Desc desc_k_major(uint32_t addr) { return smem_desc(a
 __device__ __forceinline__ Desc desc_n_major(uint32_t addr, uint32_t half_bytes) {
     return smem_desc(addr, half_bytes, 1024);
 }
+// A tile of 16 columns without swizzle: groups of 8 rows, in each the first 8
+// columns of its rows (16 bytes a row), then the other 8.
+__device__ __forceinline__ uint32_t plain16_offset(int row, int piece) {
+    return (uint32_t)((row >> 3) * 256 + piece * 128 + (row & 7) * 16);
+}
+__device__ __forceinline__ Desc desc_plain16(uint32_t addr) {
+    return Desc{((addr & 0x3FFFF) >> 4) | ((128u >> 4) << 16), (256u >> 4) | (1u << 14)};
+}
 // Instruction descriptor: fp32 accumulator, A and B of one 16-bit type.
 template <class T, int kN, bool kBNMajor>
 __device__ __forceinline__ constexpr uint32_t instr_desc() {
