@@ -35,7 +35,7 @@ inline int cuda_status(cudaError_t err) {
 // per-layer calls).
 constexpr int kLsuThreads = 256;
 constexpr int kLsuUnroll = 8;
-constexpr int kShiftUnroll = 4;           // unit pairs in flight per thread (shifted scatter)
+constexpr int kShiftUnroll = 2;           // unit pairs in flight per thread (shifted scatter)
 constexpr int kQuantThreads = 256;        // staged quantiser
 constexpr int kQuantRegThreads = 512;     // register-staged fallback (slices beyond shared memory)
 constexpr int kQuantVPT = 8;

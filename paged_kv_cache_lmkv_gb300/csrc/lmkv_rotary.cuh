@@ -28,11 +28,15 @@ struct Rotary {
 // is not finite.
 int make_rotary(const lmkv_rotary_t* in, int32_t head_dim, Rotary* out);
 
+// For 16-bit rows the special function unit's sine and cosine will do: on
+// [-pi, pi] they are within 2^-21.4, a thousandth of those types' half step.
+template <class T>
 __device__ __forceinline__ float2 cos_sin(uint64_t turns, int64_t pos) {
     const uint64_t frac = turns * (uint64_t)pos;
     const float half_turns = (float)(int32_t)(uint32_t)(frac >> 32) * 4.656612873077393e-10f;   // 2^-31
     float s, c;
-    sincospif(half_turns, &s, &c);
+    if constexpr (sizeof(T) == 2) __sincosf(half_turns * 3.14159265358979f, &s, &c);
+    else sincospif(half_turns, &s, &c);
     return make_float2(c, s);
 }
 
@@ -42,20 +46,34 @@ template <class T, int V>
 struct Vec {
     T x[V];
 };
-template <class T, int V>
+// Rows are read once: past L1.  kStream: they are not this kernel's own output
+// either, and what is written is not needed soon.
+template <class T, int V, bool kStream>
 __device__ __forceinline__ Vec<T, V> ld_vec(const T* p) {
     Vec<T, V> v;
-    if constexpr (V * sizeof(T) == 16) *reinterpret_cast<int4*>(v.x) = *reinterpret_cast<const int4*>(p);
-    else {
+    if constexpr (V * sizeof(T) == 16) {
+        int4& r = *reinterpret_cast<int4*>(v.x);
+        if constexpr (kStream)
+            asm("ld.global.nc.L1::no_allocate.v4.s32 {%0, %1, %2, %3}, [%4];"
+                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+        else
+            asm volatile("ld.global.L1::no_allocate.v4.s32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+    } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) v.x[i] = p[i];
     }
     return v;
 }
-template <class T, int V>
+template <class T, int V, bool kStream>
 __device__ __forceinline__ void st_vec(T* p, const Vec<T, V>& v) {
-    if constexpr (V * sizeof(T) == 16) *reinterpret_cast<int4*>(p) = *reinterpret_cast<const int4*>(v.x);
-    else {
+    if constexpr (V * sizeof(T) == 16) {
+        const int4 r = *reinterpret_cast<const int4*>(v.x);
+        if constexpr (kStream)
+            asm volatile("st.global.cs.v4.s32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w)
+                         : "memory");
+        else *reinterpret_cast<int4*>(p) = r;
+    } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) p[i] = v.x[i];
     }
@@ -66,8 +84,15 @@ __device__ __forceinline__ void st_vec(T* p, const Vec<T, V>& v) {
 // turns the V / 2 pairs of the vector at u * V.  The units after these copy
 // the vectors behind rot_dim.  V is 16 bytes' worth where pointers, strides
 // and half allow it, else 1 element (half) or 2 (interleaved).
-template <class T, int V, bool kInterleaved>
+// (cos, sin) of the pairs lie in shared memory as [pair of the unit][unit], so
+// that the units of a warp read consecutive places.
+template <class T, int V, bool kInterleaved, bool kStream = false>
 struct Units {
+    static constexpr int kPairs = kInterleaved ? V / 2 : V;      // of a unit
+    // The place of pair i's (cos, sin).
+    static __device__ __forceinline__ int place(int i, int half) {
+        return (i % kPairs) * turning(half) + i / kPairs;
+    }
     static __device__ __host__ __forceinline__ int turning(int half) {
         return kInterleaved ? 2 * half / V : half / V;
     }
@@ -79,19 +104,20 @@ struct Units {
     __device__ __forceinline__ void load(const T* head, int u, int half) {
         const int nt = turning(half);
         if (kInterleaved || u >= nt) {
-            a = ld_vec<T, V>(head + (u < nt ? u * V : 2 * half + (u - nt) * V));
+            a = ld_vec<T, V, kStream>(head + (u < nt ? u * V : 2 * half + (u - nt) * V));
         } else {
-            a = ld_vec<T, V>(head + u * V);
-            b = ld_vec<T, V>(head + half + u * V);
+            a = ld_vec<T, V, kStream>(head + u * V);
+            b = ld_vec<T, V, kStream>(head + half + u * V);
         }
     }
     // cs: this token's (cos, sin) table.
     __device__ __forceinline__ void turn(const float2* cs, int u, int half) {
-        if (u >= turning(half)) return;
+        const int nt = turning(half);
+        if (u >= nt) return;
         if constexpr (kInterleaved) {
 #pragma unroll
             for (int i = 0; i < V / 2; ++i) {
-                const float2 w = cs[u * (V / 2) + i];
+                const float2 w = cs[i * nt + u];
                 const float x = Elem<T>::to_float(a.x[2 * i]), y = Elem<T>::to_float(a.x[2 * i + 1]);
                 a.x[2 * i] = Elem<T>::from_float(x * w.x - y * w.y);
                 a.x[2 * i + 1] = Elem<T>::from_float(x * w.y + y * w.x);
@@ -99,7 +125,7 @@ struct Units {
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float2 w = cs[u * V + i];
+                const float2 w = cs[i * nt + u];
                 const float x = Elem<T>::to_float(a.x[i]), y = Elem<T>::to_float(b.x[i]);
                 a.x[i] = Elem<T>::from_float(x * w.x - y * w.y);
                 b.x[i] = Elem<T>::from_float(x * w.y + y * w.x);
@@ -109,10 +135,10 @@ struct Units {
     __device__ __forceinline__ void store(T* head, int u, int half) const {
         const int nt = turning(half);
         if (kInterleaved || u >= nt) {
-            st_vec<T, V>(head + (u < nt ? u * V : 2 * half + (u - nt) * V), a);
+            st_vec<T, V, kStream>(head + (u < nt ? u * V : 2 * half + (u - nt) * V), a);
         } else {
-            st_vec<T, V>(head + u * V, a);
-            st_vec<T, V>(head + half + u * V, b);
+            st_vec<T, V, kStream>(head + u * V, a);
+            st_vec<T, V, kStream>(head + half + u * V, b);
         }
     }
 };

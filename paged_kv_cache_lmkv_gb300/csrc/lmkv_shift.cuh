@@ -26,7 +26,7 @@ struct ShiftBatchT : BatchT<kCap> {
 template <class B, class T, int V, bool kInterleaved, int kThreads, int kUnroll>
 __global__ void __launch_bounds__(kThreads)
 shift_scatter_kernel(const __grid_constant__ B p, int64_t num_items) {
-    using U = lmkv_rotary_detail::Units<T, V, kInterleaved>;
+    using U = lmkv_rotary_detail::Units<T, V, kInterleaved, true>;
     __shared__ float2 cs[LMKV_ROTARY_MAX_PAIRS];
     pdl_launch_dependents();
     pdl_wait();
@@ -67,7 +67,7 @@ shift_scatter_kernel(const __grid_constant__ B p, int64_t num_items) {
         }
         if (first) {
             for (int i = threadIdx.x; i < half; i += kThreads)
-                cs[i] = lmkv_rotary_detail::cos_sin(p.rot.turns[i], shift);
+                cs[U::place(i, half)] = lmkv_rotary_detail::cos_sin<T>(p.rot.turns[i], shift);
             __syncthreads();
             first = false;
         }
