@@ -555,6 +555,8 @@ __device__ __forceinline__ uint32_t order_key(float x) {
     return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
+constexpr uint32_t kZeroKey = 0x80000000u;     // of a score of zero
+
 constexpr int kSelectThreads = 1024;
 constexpr int kBins = 2048;
 constexpr int kSelectTokens = 50 * 1024;      // keys that fit in shared memory
@@ -595,7 +597,8 @@ __device__ __forceinline__ int2 scan_pairs(int2 mine, int2* warp_sums) {
 // tokens are written in order, the first ties among them.  The keys are read
 // once, into shared memory (kStaged; more than kSelectTokens are read again
 // from L2 instead).  Wide digits are for the counters: scores crowd into few
-// exponents, and threads that meet on a counter take turns.
+// exponents, and threads that meet on a counter take turns; the score that
+// most tokens may share, zero, is counted in registers.
 template <bool kStaged>
 __global__ void __launch_bounds__(kSelectThreads)
 select_kernel(const __grid_constant__ EvictParams p) {
@@ -626,8 +629,17 @@ select_kernel(const __grid_constant__ EvictParams p) {
     const int32_t lo = p.sinks, hi = len - p.recent;
     const int32_t need = p.budget - p.sinks - p.recent;       // < hi - lo
     uint32_t prefix = 0, want = (uint32_t)need;               // want: still to take among the prefix's
-    if (kStaged)
-        for (int32_t i = tid; i < len; i += kSelectThreads) keys[i] = order_key(w[i]);
+    if (kStaged) {
+        constexpr int kLoads = 8;
+        for (int32_t i0 = tid; i0 < len; i0 += kSelectThreads * kLoads) {
+            float s[kLoads];
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) s[k] = i0 + k * kSelectThreads < len ? w[i0 + k * kSelectThreads] : 0.f;
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k)
+                if (i0 + k * kSelectThreads < len) keys[i0 + k * kSelectThreads] = order_key(s[k]);
+        }
+    }
     auto key_of = [&](int32_t i) { return kStaged ? keys[i] : order_key(w[i]); };
     int top = 32;                                             // bits above are found
     while (top > 0 && need > 0) {
@@ -635,10 +647,17 @@ select_kernel(const __grid_constant__ EvictParams p) {
         const uint32_t digits = (1u << (top - low)) - 1u;
         for (int i = tid; i < kBins; i += kSelectThreads) hist[i] = 0;
         __syncthreads();
+        uint32_t zeros = 0;
+#pragma unroll 4
         for (int32_t i = lo + tid; i < hi; i += kSelectThreads) {
             const uint32_t k = key_of(i);
-            if (top == 32 || (k >> top) == (prefix >> top)) atomicAdd(&hist[(k >> low) & digits], 1u);
+            if (top == 32 || (k >> top) == (prefix >> top)) {
+                if (k == kZeroKey) ++zeros;
+                else atomicAdd(&hist[(k >> low) & digits], 1u);
+            }
         }
+        zeros = __reduce_add_sync(0xFFFFFFFFu, zeros);
+        if ((tid & 31) == 0 && zeros > 0) atomicAdd(&hist[(kZeroKey >> low) & digits], zeros);
         __syncthreads();
         // thread t holds the t-th pair of counters from the top
         const int hi_bin = kBins - 1 - 2 * tid;
@@ -696,23 +715,27 @@ select_kernel(const __grid_constant__ EvictParams p) {
 
 // ---- compaction ---------------------------------------------------------
 
-constexpr int kMoveThreads = 256;
-constexpr int kMoveDepth = 8;              // batches of rows on their way
+constexpr int kMoveThreads = 128;
+constexpr int kMoveSlots = kMoveThreads;   // slots of a batch
+constexpr int kMoveDepth = 3;              // batches of rows on their way or being written
+constexpr int kPieceBytes = 64;            // of a head's row: more CTAs, whole sectors
 
 // Moves the kept rows of one (request, head, K or V, column piece) to the
 // front of the request's pages, in place.  keep is ascending, so keep[i] >= i
 // and a batch of slots in order may be written once its own rows, and those of
 // the batches before it, have been read: what later batches read lies behind.
-// So rows may be fetched as early as one likes: kMoveDepth batches are under
-// way in shared memory (cp.async), each thread storing what it fetched itself,
-// with one barrier a batch, and the tokens and pages of the next ones are
-// looked up before they are needed.  Slots whose token stays (a leading run,
-// as keep[i] - i never falls) are skipped.  Bound by reading and writing the
-// moved rows.
+// So rows may be fetched as early as one likes: the next batches' are under
+// way in shared memory (cp.async) while one is written, each thread writing
+// what it fetched itself, with one barrier a batch.  Where rows come from and
+// go to is looked up two batches ahead of the fetch, a slot a thread.  Slots whose token
+// stays (a leading run, as keep[i] - i never falls) are skipped.  Bound by
+// reading and writing the moved rows.
 template <int kBytes>
 __global__ void __launch_bounds__(kMoveThreads)
 compact_kernel(const __grid_constant__ EvictParams p, int32_t pieces, int32_t piece_vecs) {
-    __shared__ __align__(16) uint8_t ring[kMoveDepth][kMoveThreads * kBytes];
+    extern __shared__ __align__(16) uint8_t move_smem[];       // [kMoveDepth][kMoveSlots][piece]
+    constexpr int kPlaces = kMoveDepth + 1;
+    __shared__ int64_t from[kPlaces][kMoveSlots], to[kPlaces][kMoveSlots];
     pdl_launch_dependents();
     pdl_wait();
     int32_t x = blockIdx.x;
@@ -737,64 +760,68 @@ compact_kernel(const __grid_constant__ EvictParams p, int32_t pieces, int32_t pi
         if (keep[mid] == mid) first = mid + 1;
         else end = mid;
     }
-    // thread -> (slot of the batch, vector of the piece)
-    const int32_t per_batch = kMoveThreads / vecs;
-    const int32_t mine = threadIdx.x / vecs, vec = threadIdx.x - mine * vecs;
-    const bool idle = mine >= per_batch;
-    base += kv * p.layer.half_bytes() + (int64_t)h * p.head_bytes + ((int64_t)piece * piece_vecs + vec) * kBytes;
-    const int32_t batches = (p.budget - first + per_batch - 1) / per_batch;
-    auto slot_of = [&](int32_t i) {                    // my slot in batch i, or -1
-        const int32_t s = first + i * per_batch + mine;
-        return idle || s >= p.budget ? -1 : s;
+    base += kv * p.layer.half_bytes() + (int64_t)h * p.head_bytes + (int64_t)piece * piece_vecs * kBytes;
+    const int32_t batches = (p.budget - first + kMoveSlots - 1) / kMoveSlots;
+    const int32_t ring = kMoveSlots * piece_vecs * kBytes;
+    const int32_t units = kMoveSlots * vecs;
+
+    // Batch i's slot of this thread: its token (-1: none), one batch ahead of the look-up.
+    auto token_of = [&](int32_t i) {
+        const int32_t s = first + i * kMoveSlots + (int32_t)threadIdx.x;
+        return i < batches && s < p.budget ? keep[s] : -1;
     };
-    uint32_t came = 0;                                 // bit i % 32: batch i's row is on its way
-    auto fetch = [&](int32_t i, int32_t tok) {
-        came &= ~(1u << (i & 31));
+    auto look_up = [&](int32_t i, int32_t tok) {
+        int64_t a = -1, b = -1;
         if (tok >= 0) {
-            const int64_t from = p.layer.token_offset(table, tok);
-            if (from < 0) report(p.status, LMKV_ERR_BAD_BLOCK);
-            else came |= 1u << (i & 31);
-            uint8_t* const to = &ring[i % kMoveDepth][threadIdx.x * kBytes];
-            if (from >= 0) {
-                if constexpr (kBytes == 16) cp_async16(smem_u32(to), base + from);
+            a = p.layer.token_offset(table, tok);
+            b = p.layer.token_offset(table, first + i * kMoveSlots + (int32_t)threadIdx.x);
+            if (a < 0 || b < 0) {
+                report(p.status, LMKV_ERR_BAD_BLOCK);
+                a = b = -1;
+            }
+        }
+        from[i % kPlaces][threadIdx.x] = a;
+        to[i % kPlaces][threadIdx.x] = b;
+    };
+    auto fetch = [&](int32_t i) {
+        if (i < batches) {
+            uint8_t* const stage = move_smem + i % kMoveDepth * ring;
+            for (int32_t u = threadIdx.x; u < units; u += kMoveThreads) {
+                const int32_t s = u / vecs, v = u - s * vecs;
+                const int64_t a = from[i % kPlaces][s];
+                if (a < 0) continue;
+                uint8_t* const dst = stage + (s * piece_vecs + v) * kBytes;
+                const uint8_t* const src = base + a + v * kBytes;
+                if constexpr (kBytes == 16) cp_async16(smem_u32(dst), src);
                 else if constexpr (kBytes == 4)
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(base + from) : "memory");
-                else *to = base[from];
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+                else *dst = *src;
             }
         }
         cp_commit();
     };
-    auto token_of = [&](int32_t i) {                   // the token that batch i's slot receives
-        const int32_t s = i < batches ? slot_of(i) : -1;
-        return s >= 0 ? keep[s] : -1;
-    };
-    int32_t ahead[2] = {token_of(0), token_of(1)};     // tokens of the next batches to fetch
-#pragma unroll 1
-    for (int32_t i = 0; i < kMoveDepth - 1; ++i) {
-        const int32_t tok = ahead[0];
-        ahead[0] = ahead[1];
-        ahead[1] = token_of(i + 2);
-        fetch(i, tok);
-    }
+    for (int32_t i = 0; i < kMoveDepth; ++i) look_up(i, token_of(i));
+    int32_t next = token_of(kMoveDepth);
+    __syncthreads();
+    for (int32_t i = 0; i < kMoveDepth - 1; ++i) fetch(i);
 #pragma unroll 1
     for (int32_t i = 0; i < batches; ++i) {
-        int64_t to = -1;
-        if ((came >> (i & 31)) & 1) {
-            to = p.layer.token_offset(table, slot_of(i));
-            if (to < 0) report(p.status, LMKV_ERR_BAD_BLOCK);
-        }
         cp_wait<kMoveDepth - 2>();
         __syncthreads();               // batch i and those before it have been read by every thread
-        if (to >= 0) {
-            const uint8_t* const src = &ring[i % kMoveDepth][threadIdx.x * kBytes];
-            if constexpr (kBytes == 16) *reinterpret_cast<int4*>(base + to) = *reinterpret_cast<const int4*>(src);
-            else if constexpr (kBytes == 4) *reinterpret_cast<int32_t*>(base + to) = *reinterpret_cast<const int32_t*>(src);
-            else base[to] = *src;
+        fetch(i + kMoveDepth - 1);
+        const uint8_t* const stage = move_smem + i % kMoveDepth * ring;
+        for (int32_t u = threadIdx.x; u < units; u += kMoveThreads) {
+            const int32_t s = u / vecs, v = u - s * vecs;
+            const int64_t b = to[i % kPlaces][s];
+            if (b < 0) continue;
+            const uint8_t* const src = stage + (s * piece_vecs + v) * kBytes;
+            uint8_t* const dst = base + b + v * kBytes;
+            if constexpr (kBytes == 16) *reinterpret_cast<int4*>(dst) = *reinterpret_cast<const int4*>(src);
+            else if constexpr (kBytes == 4) *reinterpret_cast<int32_t*>(dst) = *reinterpret_cast<const int32_t*>(src);
+            else *dst = *src;
         }
-        const int32_t tok = ahead[0];
-        ahead[0] = ahead[1];
-        ahead[1] = token_of(i + kMoveDepth + 1);
-        fetch(i + kMoveDepth - 1, tok);
+        look_up(i + kMoveDepth, next);                 // the places of batch i - 1, which every thread has left
+        next = token_of(i + kMoveDepth + 1);
     }
     cp_wait<0>();
 }
@@ -802,10 +829,13 @@ compact_kernel(const __grid_constant__ EvictParams p, int32_t pieces, int32_t pi
 template <int kBytes>
 int launch_compact(const EvictParams& p, void* stream) {
     const int32_t vecs = p.head_bytes / kBytes;
-    const int32_t most = 64 / kBytes;                  // 64-byte pieces: more CTAs, whole sectors
+    constexpr int most = kPieceBytes / kBytes;
     const int32_t piece = vecs < most ? vecs : most;
     const int32_t pieces = (vecs + piece - 1) / piece;
-    return launch(compact_kernel<kBytes>, (int64_t)p.num_req * p.kv_heads * 2 * pieces, kMoveThreads, 0, stream, 1, p,
+    constexpr int ring = kMoveDepth * kMoveSlots * kPieceBytes;
+    const int rc = allow_smem<compact_kernel<kBytes>, ring>();
+    if (rc != LMKV_OK) return rc;
+    return launch(compact_kernel<kBytes>, (int64_t)p.num_req * p.kv_heads * 2 * pieces, kMoveThreads, ring, stream, 1, p,
                   pieces, piece);
 }
 
