@@ -559,7 +559,7 @@ constexpr uint32_t kZeroKey = 0x80000000u;     // of a score of zero
 
 constexpr int kSelectThreads = 1024;
 constexpr int kBins = 2048;
-constexpr int kSelectTokens = 50 * 1024;      // keys that fit in shared memory
+constexpr int kSelectTokens = 50 * 1024;      // scores that fit in shared memory
 
 // Exclusive sums over the CTA of two counts a thread, in thread order.
 __device__ __forceinline__ int2 scan_pairs(int2 mine, int2* warp_sums) {
@@ -594,9 +594,9 @@ __device__ __forceinline__ int2 scan_pairs(int2 mine, int2* warp_sums) {
 // and 10 bits), most significant first, with a histogram over the candidates
 // that share the digits found so far; then every thread counts what it keeps
 // of a run of consecutive tokens, one scan places the runs, and the kept
-// tokens are written in order, the first ties among them.  The keys are read
-// once, into shared memory (kStaged; more than kSelectTokens are read again
-// from L2 instead).  Wide digits are for the counters: scores crowd into few
+// tokens are written in order, the first ties among them.  The scores are
+// read once, into shared memory (kStaged; more than kSelectTokens are read
+// again from L2 instead).  Wide digits are for the counters: scores crowd into few
 // exponents, and threads that meet on a counter take turns; the score that
 // most tokens may share, zero, is counted in registers.
 template <bool kStaged>
@@ -605,7 +605,7 @@ select_kernel(const __grid_constant__ EvictParams p) {
     __shared__ uint32_t hist[kBins];
     __shared__ uint32_t digit_s, above_s;
     __shared__ int2 warp_sums[32];
-    extern __shared__ uint32_t keys[];
+    extern __shared__ float staged[];
     pdl_launch_dependents();
     pdl_wait();
     const int tid = threadIdx.x;
@@ -630,17 +630,14 @@ select_kernel(const __grid_constant__ EvictParams p) {
     const int32_t need = p.budget - p.sinks - p.recent;       // < hi - lo
     uint32_t prefix = 0, want = (uint32_t)need;               // want: still to take among the prefix's
     if (kStaged) {
-        constexpr int kLoads = 8;
-        for (int32_t i0 = tid; i0 < len; i0 += kSelectThreads * kLoads) {
-            float s[kLoads];
-#pragma unroll
-            for (int k = 0; k < kLoads; ++k) s[k] = i0 + k * kSelectThreads < len ? w[i0 + k * kSelectThreads] : 0.f;
-#pragma unroll
-            for (int k = 0; k < kLoads; ++k)
-                if (i0 + k * kSelectThreads < len) keys[i0 + k * kSelectThreads] = order_key(s[k]);
-        }
+        // every score of the thread on its way before the first is waited for
+        for (int32_t i = tid; i < len; i += kSelectThreads)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(staged + i)), "l"(w + i) : "memory");
+        cp_commit();
+        cp_wait<0>();
     }
-    auto key_of = [&](int32_t i) { return kStaged ? keys[i] : order_key(w[i]); };
+    auto score = [&](int32_t i) { return kStaged ? staged[i] : w[i]; };
+    auto key_of = [&](int32_t i) { return order_key(score(i)); };
     int top = 32;                                             // bits above are found
     while (top > 0 && need > 0) {
         const int low = top > 11 ? top - 11 : 0;
@@ -705,7 +702,7 @@ select_kernel(const __grid_constant__ EvictParams p) {
             const int32_t slot = at.x + min(at.y, (int32_t)want);
             if (slot < p.budget) {
                 keep[slot] = i;
-                if (kept != nullptr) kept[slot] = w[i];
+                if (kept != nullptr) kept[slot] = score(i);
             }
         }
         at.x += keeps;
@@ -732,7 +729,7 @@ constexpr int kPieceBytes = 64;            // of a head's row: more CTAs, whole 
 // reading and writing the moved rows.
 template <int kBytes>
 __global__ void __launch_bounds__(kMoveThreads)
-compact_kernel(const __grid_constant__ EvictParams p, int32_t pieces, int32_t piece_vecs) {
+compact_kernel(const __grid_constant__ EvictParams p, int32_t pieces) {
     extern __shared__ __align__(16) uint8_t move_smem[];       // [kMoveDepth][kMoveSlots][piece]
     constexpr int kPlaces = kMoveDepth + 1;
     __shared__ int64_t from[kPlaces][kMoveSlots], to[kPlaces][kMoveSlots];
@@ -751,7 +748,7 @@ compact_kernel(const __grid_constant__ EvictParams p, int32_t pieces, int32_t pi
         if (threadIdx.x == 0) report(p.status, LMKV_ERR_BAD_POINTER);
         return;
     }
-    const int32_t vecs = min(piece_vecs, p.head_bytes / kBytes - piece * piece_vecs);
+    const int32_t vecs = (p.head_bytes - piece * kPieceBytes) / kBytes;      // of this piece (kVecs at most are moved)
     const int32_t* table = p.table + (int64_t)r * p.table_stride;
     const int32_t* keep = p.keep + ((int64_t)r * p.kv_heads + h) * p.budget;
     int32_t first = 0, end = p.budget;                 // first slot that moves
@@ -760,10 +757,15 @@ compact_kernel(const __grid_constant__ EvictParams p, int32_t pieces, int32_t pi
         if (keep[mid] == mid) first = mid + 1;
         else end = mid;
     }
-    base += kv * p.layer.half_bytes() + (int64_t)h * p.head_bytes + (int64_t)piece * piece_vecs * kBytes;
+    base += kv * p.layer.half_bytes() + (int64_t)h * p.head_bytes + piece * kPieceBytes;
     const int32_t batches = (p.budget - first + kMoveSlots - 1) / kMoveSlots;
-    const int32_t ring = kMoveSlots * piece_vecs * kBytes;
-    const int32_t units = kMoveSlots * vecs;
+    // unit k of thread t: vector t % kVecs of slot t / kVecs + k * kMoveThreads / kVecs
+    constexpr int kVecs = kPieceBytes / kBytes, kUnits = kMoveSlots * kVecs / kMoveThreads;
+    constexpr int kStep = kMoveThreads / kVecs;
+    const int32_t v = threadIdx.x % kVecs, s0 = threadIdx.x / kVecs;
+    const bool mine = v < vecs;
+    uint8_t* const at = base + v * kBytes;
+    uint8_t* const ring = move_smem + threadIdx.x * kBytes;
 
     // Batch i's slot of this thread: its token (-1: none), one batch ahead of the look-up.
     auto token_of = [&](int32_t i) {
@@ -784,18 +786,17 @@ compact_kernel(const __grid_constant__ EvictParams p, int32_t pieces, int32_t pi
         to[i % kPlaces][threadIdx.x] = b;
     };
     auto fetch = [&](int32_t i) {
-        if (i < batches) {
-            uint8_t* const stage = move_smem + i % kMoveDepth * ring;
-            for (int32_t u = threadIdx.x; u < units; u += kMoveThreads) {
-                const int32_t s = u / vecs, v = u - s * vecs;
-                const int64_t a = from[i % kPlaces][s];
+        if (i < batches && mine) {
+            uint8_t* const stage = ring + i % kMoveDepth * (kMoveSlots * kPieceBytes);
+#pragma unroll
+            for (int k = 0; k < kUnits; ++k) {
+                const int64_t a = from[i % kPlaces][s0 + k * kStep];
                 if (a < 0) continue;
-                uint8_t* const dst = stage + (s * piece_vecs + v) * kBytes;
-                const uint8_t* const src = base + a + v * kBytes;
-                if constexpr (kBytes == 16) cp_async16(smem_u32(dst), src);
+                uint8_t* const dst = stage + k * kMoveThreads * kBytes;
+                if constexpr (kBytes == 16) cp_async16(smem_u32(dst), at + a);
                 else if constexpr (kBytes == 4)
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-                else *dst = *src;
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(at + a) : "memory");
+                else *dst = at[a];
             }
         }
         cp_commit();
@@ -809,16 +810,17 @@ compact_kernel(const __grid_constant__ EvictParams p, int32_t pieces, int32_t pi
         cp_wait<kMoveDepth - 2>();
         __syncthreads();               // batch i and those before it have been read by every thread
         fetch(i + kMoveDepth - 1);
-        const uint8_t* const stage = move_smem + i % kMoveDepth * ring;
-        for (int32_t u = threadIdx.x; u < units; u += kMoveThreads) {
-            const int32_t s = u / vecs, v = u - s * vecs;
-            const int64_t b = to[i % kPlaces][s];
-            if (b < 0) continue;
-            const uint8_t* const src = stage + (s * piece_vecs + v) * kBytes;
-            uint8_t* const dst = base + b + v * kBytes;
-            if constexpr (kBytes == 16) *reinterpret_cast<int4*>(dst) = *reinterpret_cast<const int4*>(src);
-            else if constexpr (kBytes == 4) *reinterpret_cast<int32_t*>(dst) = *reinterpret_cast<const int32_t*>(src);
-            else *dst = *src;
+        if (mine) {
+            const uint8_t* const stage = ring + i % kMoveDepth * (kMoveSlots * kPieceBytes);
+#pragma unroll
+            for (int k = 0; k < kUnits; ++k) {
+                const int64_t b = to[i % kPlaces][s0 + k * kStep];
+                if (b < 0) continue;
+                const uint8_t* const src = stage + k * kMoveThreads * kBytes;
+                if constexpr (kBytes == 16) *reinterpret_cast<int4*>(at + b) = *reinterpret_cast<const int4*>(src);
+                else if constexpr (kBytes == 4) *reinterpret_cast<int32_t*>(at + b) = *reinterpret_cast<const int32_t*>(src);
+                else at[b] = *src;
+            }
         }
         look_up(i + kMoveDepth, next);                 // the places of batch i - 1, which every thread has left
         next = token_of(i + kMoveDepth + 1);
@@ -828,15 +830,12 @@ compact_kernel(const __grid_constant__ EvictParams p, int32_t pieces, int32_t pi
 
 template <int kBytes>
 int launch_compact(const EvictParams& p, void* stream) {
-    const int32_t vecs = p.head_bytes / kBytes;
-    constexpr int most = kPieceBytes / kBytes;
-    const int32_t piece = vecs < most ? vecs : most;
-    const int32_t pieces = (vecs + piece - 1) / piece;
+    const int32_t pieces = (p.head_bytes + kPieceBytes - 1) / kPieceBytes;
     constexpr int ring = kMoveDepth * kMoveSlots * kPieceBytes;
     const int rc = allow_smem<compact_kernel<kBytes>, ring>();
     if (rc != LMKV_OK) return rc;
     return launch(compact_kernel<kBytes>, (int64_t)p.num_req * p.kv_heads * 2 * pieces, kMoveThreads, ring, stream, 1, p,
-                  pieces, piece);
+                  pieces);
 }
 
 // Rows per KV head from which the tile kernel takes a batch: below, the row
