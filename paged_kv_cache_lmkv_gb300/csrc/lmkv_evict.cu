@@ -549,13 +549,15 @@ __device__ __forceinline__ int32_t clamped_len(const EvictParams& p, int32_t r) 
 
 // Order of the scores as unsigned numbers: NaN lowest, then -inf up to +inf,
 // -0 equal to +0.
+constexpr uint32_t kNoKey = 0u;                // of places behind the last token
+constexpr uint32_t kNanKey = 1u;
+constexpr uint32_t kZeroKey = 0x80000000u;     // of a score of zero
+constexpr uint32_t kKeepKey = 0xFFFFFFFFu;     // of tokens that are kept whatever their score
 __device__ __forceinline__ uint32_t order_key(float x) {
-    if (x != x) return 0u;
+    if (x != x) return kNanKey;
     const uint32_t b = __float_as_uint(x + 0.f);      // -0 + 0 = +0
     return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
-
-constexpr uint32_t kZeroKey = 0x80000000u;     // of a score of zero
 
 constexpr int kSelectThreads = 1024;
 constexpr int kBins = 2048;
@@ -589,23 +591,25 @@ __device__ __forceinline__ int2 scan_pairs(int2 mine, int2* warp_sums) {
     return make_int2(bx + v.x - mine.x, by + v.y - mine.y);
 }
 
-// A CTA per (request, head).  The need-th largest key of the candidates
-// (tokens that are neither sinks nor recent) is found digit by digit (11, 11
-// and 10 bits), most significant first, with a histogram over the candidates
-// that share the digits found so far; then every thread counts what it keeps
-// of a run of consecutive tokens, one scan places the runs, and the kept
-// tokens are written in order, the first ties among them.  The scores are
-// read once, into shared memory (kStaged; more than kSelectTokens are read
-// again from L2 instead).  Wide digits are for the counters: scores crowd into few
-// exponents, and threads that meet on a counter take turns; the score that
-// most tokens may share, zero, is counted in registers.
+// A CTA per (request, head).  Sinks and recent tokens have the largest key of
+// all, so what is kept is the budget largest.  The last of these is found
+// digit by digit (11, 11 and 10 bits), most significant first, with a histogram
+// over the keys that share the digits found so far; then every thread counts
+// what it keeps of a run of consecutive tokens, one scan places the runs, and
+// the kept tokens are written in order, the first ties among them.  The keys
+// are made once, into shared memory (kStaged; more than kSelectTokens are made
+// again from L2 instead), and taken four at a time: the kernel is bound by its
+// instructions, on the SM of the longest request.  Wide digits are for the
+// counters: scores crowd into few exponents, and threads that meet on a
+// counter take turns; the score that most tokens may share, zero, is counted
+// in registers.
 template <bool kStaged>
 __global__ void __launch_bounds__(kSelectThreads)
 select_kernel(const __grid_constant__ EvictParams p) {
     __shared__ uint32_t hist[kBins];
     __shared__ uint32_t digit_s, above_s;
     __shared__ int2 warp_sums[32];
-    extern __shared__ float staged[];
+    extern __shared__ __align__(16) uint32_t keys[];
     pdl_launch_dependents();
     pdl_wait();
     const int tid = threadIdx.x;
@@ -626,32 +630,54 @@ select_kernel(const __grid_constant__ EvictParams p) {
         }
         return;
     }
-    const int32_t lo = p.sinks, hi = len - p.recent;
-    const int32_t need = p.budget - p.sinks - p.recent;       // < hi - lo
-    uint32_t prefix = 0, want = (uint32_t)need;               // want: still to take among the prefix's
+    const int32_t lo = p.sinks, hi = len - p.recent, quads = (len + 3) >> 2;
+    auto make_key = [&](int32_t i, float s) {
+        return i >= len ? kNoKey : i < lo || i >= hi ? kKeepKey : order_key(s);
+    };
     if (kStaged) {
         // every score of the thread on its way before the first is waited for
         for (int32_t i = tid; i < len; i += kSelectThreads)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(staged + i)), "l"(w + i) : "memory");
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(keys + i)), "l"(w + i) : "memory");
         cp_commit();
         cp_wait<0>();
     }
-    auto score = [&](int32_t i) { return kStaged ? staged[i] : w[i]; };
-    auto key_of = [&](int32_t i) { return order_key(score(i)); };
-    int top = 32;                                             // bits above are found
-    while (top > 0 && need > 0) {
+    // four tokens' keys; `raw`: from the scores, which the first pass over
+    // shared memory turns into keys
+    auto quad = [&](int32_t q, bool raw) {
+        uint4* const place = reinterpret_cast<uint4*>(keys) + q;
+        if (kStaged && !raw) return *place;
+        uint32_t k[4];
+        if (kStaged) {
+            const uint4 s = *place;
+            k[0] = s.x, k[1] = s.y, k[2] = s.z, k[3] = s.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) k[j] = 4 * q + j < len ? __float_as_uint(w[4 * q + j]) : 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) k[j] = make_key(4 * q + j, __uint_as_float(k[j]));
+        const uint4 x = make_uint4(k[0], k[1], k[2], k[3]);
+        if (kStaged) *place = x;
+        return x;
+    };
+    uint32_t prefix = 0, want = (uint32_t)p.budget;       // want: still to take among the prefix's
+    for (int top = 32; top > 0;) {                         // bits from top on are found
         const int low = top > 11 ? top - 11 : 0;
         const uint32_t digits = (1u << (top - low)) - 1u;
         for (int i = tid; i < kBins; i += kSelectThreads) hist[i] = 0;
         __syncthreads();
         uint32_t zeros = 0;
-#pragma unroll 4
-        for (int32_t i = lo + tid; i < hi; i += kSelectThreads) {
-            const uint32_t k = key_of(i);
-            if (top == 32 || (k >> top) == (prefix >> top)) {
-                if (k == kZeroKey) ++zeros;
-                else atomicAdd(&hist[(k >> low) & digits], 1u);
-            }
+        auto count = [&](uint32_t k) {
+            if (top < 32 && (k >> top) != (prefix >> top)) return;
+            if (k == kZeroKey) ++zeros;
+            else atomicAdd(&hist[(k >> low) & digits], 1u);
+        };
+        for (int32_t q = tid; q < quads; q += kSelectThreads) {
+            const uint4 k = quad(q, top == 32);
+            count(k.x);
+            count(k.y);
+            count(k.z);
+            count(k.w);
         }
         zeros = __reduce_add_sync(0xFFFFFFFFu, zeros);
         if ((tid & 31) == 0 && zeros > 0) atomicAdd(&hist[(kZeroKey >> low) & digits], zeros);
@@ -676,37 +702,65 @@ select_kernel(const __grid_constant__ EvictParams p) {
         __syncthreads();
     }
     // `want` of the keys equal to prefix are kept, all larger ones.  A run is an odd
-    // number of tokens, so that the threads' places lie in different banks.
-    const int32_t run = ((len + kSelectThreads - 1) / kSelectThreads) | 1;
-    const int32_t from = min(tid * run, len), to = min(from + run, len);
-    int2 count = make_int2(0, 0);                             // kept for certain, ties
-    __syncthreads();
-    for (int32_t i = from; i < to; ++i) {
-        if (i < lo || i >= hi) {
-            ++count.x;
-        } else if (need > 0) {
-            const uint32_t k = key_of(i);
-            count.x += k > prefix;
-            count.y += k == prefix;
-        }
+    // number of quads, so that the threads' places lie in different banks.
+    const int32_t run = ((quads + kSelectThreads - 1) / kSelectThreads) | 1;
+    const int32_t from = min(tid * run, quads), to = min(from + run, quads);
+    int2 mine = make_int2(0, 0);                              // kept for certain, ties
+    for (int32_t q = from; q < to; ++q) {
+        const uint4 k = quad(q, false);
+        mine.x += (k.x > prefix) + (k.y > prefix) + (k.z > prefix) + (k.w > prefix);
+        mine.y += (k.x == prefix) + (k.y == prefix) + (k.z == prefix) + (k.w == prefix);
     }
-    int2 at = scan_pairs(count, warp_sums);
-    for (int32_t i = from; i < to; ++i) {
-        bool keeps = i < lo || i >= hi, tie = false;
-        if (!keeps && need > 0) {
-            const uint32_t k = key_of(i);
-            keeps = k > prefix;
-            tie = k == prefix;
+    int2 at = scan_pairs(mine, warp_sums);
+    // 32 tokens at a time as bits, of which only the kept ones are gone through
+    auto bits = [&](int32_t q0, uint32_t* more, uint32_t* tie) {
+        *more = *tie = 0;
+#pragma unroll
+        for (int32_t u = 0; u < 8; ++u) {
+            if (q0 + u >= to) break;
+            const uint4 k = quad(q0 + u, false);
+            *more |= ((k.x > prefix) | (k.y > prefix) << 1 | (k.z > prefix) << 2 | (k.w > prefix) << 3) << (4 * u);
+            *tie |= ((k.x == prefix) | (k.y == prefix) << 1 | (k.z == prefix) << 2 | (k.w == prefix) << 3) << (4 * u);
         }
-        if (keeps || (tie && at.y < (int32_t)want)) {
-            const int32_t slot = at.x + min(at.y, (int32_t)want);
-            if (slot < p.budget) {
-                keep[slot] = i;
-                if (kept != nullptr) kept[slot] = score(i);
+    };
+    auto walk = [&](int32_t q0, uint32_t more, uint32_t tie, auto put) {
+        for (uint32_t left = more | tie; left != 0; left &= left - 1) {
+            const int bit = __ffs(left) - 1;
+            const bool sure = (more >> bit) & 1;
+            if (sure || at.y < (int32_t)want) {
+                const int32_t slot = at.x + min(at.y, (int32_t)want);
+                if (slot < p.budget) put(slot, 4 * q0 + bit);
             }
+            at.x += sure;
+            at.y += !sure;
         }
-        at.x += keeps;
-        at.y += tie;
+    };
+    if (kStaged) {
+        // the keys make room for the list of tokens, which is then written out side by side
+        constexpr int kWords = (kSelectTokens / kSelectThreads + 4 + 31) / 32;
+        uint32_t more[kWords], tie[kWords];
+#pragma unroll
+        for (int n = 0; n < kWords; ++n) bits(from + 8 * n, &more[n], &tie[n]);
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < kWords; ++n)
+            walk(from + 8 * n, more[n], tie[n], [&](int32_t slot, int32_t i) { keys[slot] = (uint32_t)i; });
+        __syncthreads();
+#pragma unroll 4
+        for (int32_t s = tid; s < p.budget; s += kSelectThreads) {
+            const int32_t i = (int32_t)keys[s];
+            keep[s] = i;
+            if (kept != nullptr) kept[s] = w[i];
+        }
+    } else {
+        for (int32_t q0 = from; q0 < to; q0 += 8) {
+            uint32_t more, tie;
+            bits(q0, &more, &tie);
+            walk(q0, more, tie, [&](int32_t slot, int32_t i) {
+                keep[slot] = i;
+                if (kept != nullptr) kept[slot] = w[i];
+            });
+        }
     }
 }
 
@@ -950,7 +1004,7 @@ int lmkv_evict_layer(const lmkv_pool_t* pool, int32_t layer, const int32_t* bloc
     if (max_kv_len <= kSelectTokens) {
         rc = allow_smem<select_kernel<true>, kSelectTokens * 4>();
         if (rc == LMKV_OK)
-            rc = launch(select_kernel<true>, (int64_t)num_req * p.kv_heads, kSelectThreads, (size_t)max_kv_len * 4, stream,
+            rc = launch(select_kernel<true>, (int64_t)num_req * p.kv_heads, kSelectThreads, ((size_t)max_kv_len + 3) / 4 * 16, stream,
                         1, p);
     } else {
         rc = launch(select_kernel<false>, (int64_t)num_req * p.kv_heads, kSelectThreads, 0, stream, 1, p);
