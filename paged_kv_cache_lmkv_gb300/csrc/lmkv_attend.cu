@@ -947,8 +947,8 @@ int attend_typed(AttendParams& p, const Plan& x, void* stream) {
                           (int64_t)x.own_tiles * p.seqs.num_req * x.own_splits) * p.kv_heads;
     rc = launch(attend_rows_kernel<T, D>, grid, kWarps * 32, smem, stream, 1, p);
     if (rc != LMKV_OK || !x.join) return rc;
-    // with one part of the tiles only the small requests' rows have more than one
-    if (x.prefix_parts <= 1)
+    // the small requests' rows, where there are no others or those are done already
+    if (!x.big || x.prefix_parts <= 1)
         return launch(attend_join_kernel<T, D, true>, (x.own_rows + 7) / 8, 256, 0, stream, 1, p);
     return launch(attend_join_kernel<T, D, false>, (x.rows + 7) / 8, 256, 0, stream, 1, p);
 }

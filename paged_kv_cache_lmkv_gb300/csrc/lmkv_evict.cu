@@ -109,8 +109,9 @@ weigh_rows_kernel(const __grid_constant__ WeighParams p) {
     const uint32_t ring = smem_u32(smem) + warp * (kStages * kTileBytes), q_u = smem_u32(qt);
     WeighPart x;
     x.h = blockIdx.x % p.kv_heads;
-    Share share = find_share(p.seqs, kUnit, blockIdx.x / p.kv_heads, p.splits, p.status);
-    for (; share.n > 0; ++share.r, share.first = 0) {
+    Share share = find_share(p.seqs.num_req, blockIdx.x / p.kv_heads, p.splits,
+                             [&](int32_t i) { return units_of(p.seqs, i, kUnit, p.status); });
+    for (; share.n > 0 && share.r < p.seqs.num_req; ++share.r, share.first = 0) {
         x.q = load_req(p.seqs, share.r);
         if (!x.q.ok && threadIdx.x == 0) report(p.status, LMKV_ERR_BAD_LENGTH);
         const int64_t here = min((int64_t)(x.q.len + kUnit - 1) / kUnit - share.first, share.n);
@@ -273,7 +274,7 @@ struct WeighWalk {
     int64_t at;            // of the part's first key's score
 
     __device__ __forceinline__ bool next(bool there) {
-        for (; share.n > 0; ++share.r, share.first = 0) {
+        for (; share.n > 0 && share.r < p.seqs.num_req; ++share.r, share.first = 0) {
             x.q = load_req(p.seqs, share.r);
             const int64_t here = min((int64_t)(x.q.len + kBlock - 1) / kBlock - share.first, share.n);
             if (here <= 0) continue;
@@ -338,7 +339,8 @@ weigh_tiles_kernel(const __grid_constant__ WeighParams p) {
     uint8_t* const base = p.layer.base();
     if (base == nullptr && tid == 0) report(p.status, LMKV_ERR_BAD_POINTER);
     if (warp == 0) {
-        const Share s = find_share(p.seqs, kBlock, blockIdx.x / p.kv_heads, p.splits, p.status);
+        const Share s = find_share(p.seqs.num_req, blockIdx.x / p.kv_heads, p.splits,
+                                   [&](int32_t i) { return units_of(p.seqs, i, kBlock, p.status); });
         if (lane == 0) share_s = s;
     }
     fence_before_sync();

@@ -140,33 +140,34 @@ __device__ __forceinline__ int32_t find_request(int32_t num_req, int32_t x, Key 
     return lo;
 }
 
-// An equal share of a batch's cached tokens, in units of `unit` tokens (a
+// An equal share of a batch's cached tokens, in units (of some tokens; a
 // request's last one may be short) counted over the requests in turn: units
 // [all * part / parts, all * (part + 1) / parts).  Whatever the lengths are,
-// CTAs that take a share each end together.
+// CTAs that take a share each end together.  No share before the last ones is
+// empty, so a request's units lie in shares that follow one another.
 struct Share {
     int32_t r;          // request of the first unit
     int64_t first;      // that unit, counted from the request's first
     int64_t n;          // units
 };
-// Called by a whole warp; reads every request's length.
-__device__ __forceinline__ Share find_share(const Seqs& s, int32_t unit, int32_t part, int32_t parts, int32_t* status) {
+// Called by a whole warp, which goes over all requests; units(i): request i's.
+template <class Units>
+__device__ __forceinline__ Share find_share(int32_t num_req, int32_t part, int32_t parts, Units units) {
     const int lane = threadIdx.x & 31;
     int64_t all = 0;
-    for (int32_t i = lane; i < s.num_req; i += 32) {
-        const int32_t len = s.kv_len[i];
-        if (len < 0 || len > s.max_kv_len) report(status, LMKV_ERR_BAD_LENGTH);
-        all += (min(max(len, 0), s.max_kv_len) + unit - 1) / unit;
-    }
+    for (int32_t i = lane; i < num_req; i += 32) all += units(i);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, d);
-    const int64_t begin = all * part / parts, end = all * (part + 1) / parts;
-    Share x{0, 0, end - begin};
-    if (x.n == 0) return x;
+    // fewer units than shares: one each, the last shares have none
+    const int64_t use = min((int64_t)parts, all);
+    Share x{0, 0, 0};
+    if (part >= use) return x;
+    const int64_t begin = all * part / use, end = all * (part + 1) / use;
+    x.n = end - begin;
     int64_t before = 0;
-    for (int32_t r0 = 0; r0 < s.num_req; r0 += 32) {
+    for (int32_t r0 = 0; r0 < num_req; r0 += 32) {
         const int32_t i = r0 + lane;
-        const int64_t own = i < s.num_req ? (min(max(s.kv_len[i], 0), s.max_kv_len) + unit - 1) / unit : 0;
+        const int64_t own = i < num_req ? (int64_t)units(i) : 0;
         int64_t upto = own;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -185,6 +186,12 @@ __device__ __forceinline__ Share find_share(const Seqs& s, int32_t unit, int32_t
     }
     x.n = 0;      // not reached: begin < all
     return x;
+}
+// Units of a request's cached tokens.
+__device__ __forceinline__ int64_t units_of(const Seqs& s, int32_t i, int32_t unit, int32_t* status) {
+    const int32_t len = s.kv_len[i];
+    if (len < 0 || len > s.max_kv_len) report(status, LMKV_ERR_BAD_LENGTH);
+    return (min(max(len, 0), s.max_kv_len) + unit - 1) / unit;
 }
 
 // ---- element types ------------------------------------------------------
