@@ -47,8 +47,9 @@ struct AttendParams {
     const int32_t* prefix_table;
     int32_t* status;
     // Partial results: m (powers of 2), l and the weighted sum of v.  First
-    // [prefix_parts][rows], row = token * q_heads + head, then
-    // [own_splits][own_rows], row = (r * own_cap + row of r) * kv_heads + KV head.
+    // [prefix_parts][rows], row = token * q_heads + head, then the own parts:
+    // [stream + row tile of the batch's requests][row of the tile][KV head] (a
+    // stream's and a tile's number rise from part to part, so their sum names it).
     float* part_o;
     float2* part_ml;
     float scale_log2;       // of |scale|
@@ -59,9 +60,12 @@ struct AttendParams {
     int32_t row_tiles;      // row kernel: row tiles of the prefix part (0: the tile kernel has it)
     int32_t prefix_parts, prefix_span;    // parts of the prefix (row kernel: keys in each)
     int32_t tiles;          // tile kernel: row tiles (0: not launched)
+    int32_t tile_ctas;      // its CTAs that take tiles; those after them run streams
     int32_t own_cap;        // rows of a request that the row kernel takes at most
     int32_t own_tiles;      // row tiles of that many rows
-    int32_t own_splits, own_span;
+    int32_t tile_rows;      // rows of a tile that there may be
+    int32_t streams;        // warps that share the own tokens for a KV head; 0: a CTA per row tile
+    int2* own_range;        // [request][row tile]: first and last stream that has some of it
     bool big;               // a request may have kBigRows rows
     bool own_final;         // the own part is all of a small request: no join
     bool q_pairs;           // q rows are 4-byte aligned
@@ -69,17 +73,16 @@ struct AttendParams {
     bool out_vec;           // out rows are 16-byte aligned
     FastDiv by_group;
 
-    __device__ __forceinline__ int64_t own_part(int32_t split, int32_t r, int32_t row, int32_t h) const {
-        return (int64_t)prefix_parts * rows +
-               (int64_t)split * ((int64_t)seqs.num_req * own_cap * kv_heads) +
-               ((int64_t)r * own_cap + row) * kv_heads + h;
+    __device__ __forceinline__ int64_t own_part(int32_t stream, int32_t tile_no, int32_t row, int32_t h) const {
+        return (int64_t)prefix_parts * rows + (((int64_t)stream + tile_no) * tile_rows + row) * kv_heads + h;
     }
 };
 
 constexpr int kRowTile = 16;      // rows of a tile: one mma.sync operand
 constexpr int kWarps = 4;
 constexpr int kChunk = 16;        // keys a warp takes at a time
-constexpr int kStages = 2;          // three CTAs an SM: more in flight than with three stages and two CTAs
+constexpr int kStages = 2;
+constexpr int kRowCtas = 3;       // CTAs an SM: more in flight than with three stages and two CTAs
 constexpr float kLn2 = 0.69314718055994530942f;
 
 // A row tile's place in the batch.
@@ -122,8 +125,8 @@ __device__ __forceinline__ bool find_tile(const AttendParams& p, int32_t bid, Ti
     int32_t x = bid / p.kv_heads;
     const int32_t tile = x % p.own_tiles;
     x /= p.own_tiles;
-    t.r = x % p.seqs.num_req;
-    t.part = x / p.seqs.num_req;
+    t.r = x;
+    t.part = 0;
     const Req q = load_req(p.seqs, t.r);
     if (!q.ok && threadIdx.x == 0) report(p.status, LMKV_ERR_BAD_LENGTH);
     t.row0 = tile * kRowTile;
@@ -134,23 +137,131 @@ __device__ __forceinline__ bool find_tile(const AttendParams& p, int32_t bid, Ti
     t.limit0 = q.len - q.n + 1;
     t.causal = 1;
     const int32_t last = (int32_t)p.by_group.div((uint32_t)(t.row0 + min(t.nrows, kRowTile) - 1));
-    t.k0 = t.part * p.own_span;
-    t.k1 = max(t.k0, min(t.k0 + p.own_span, t.limit0 + last));
-    return p.own_final || t.k0 < q.len;
+    t.k0 = 0;
+    t.k1 = max(0, min(q.len, t.limit0 + last));
+    return true;
 }
 
-// Row tiles of 16 by mma.sync.  Bound by the bytes of K and V: with a few rows
-// per KV head the products are a fraction of the loads' time, so the four
-// warps of a CTA share the rows, take 16 keys (a page) each in turn, and run
-// by themselves: every warp has its own ring of kStages x 16 K and V rows,
-// filled by cp.async, and its own running maximum, sum and output; they are
-// joined in shared memory at the end.
+// One warp's 16 rows against chunks of 16 keys, by mma.sync: q, and the running
+// maximum, sum and output.
+template <class T, int D>
+struct WarpRows {
+    static constexpr int kRowBytes = D * 2;
+    static constexpr int kTileBytes = kChunk * kRowBytes;   // K (or V) rows of a stage
+    static constexpr int kSteps = D / 16;
+
+    // this thread's two rows: lane / 4 and lane / 4 + 8
+    int32_t limit[2];
+    uint32_t qf[kSteps][4];
+    float o[D / 8][4];
+    float m[2], l[2];
+
+    __device__ __forceinline__ void begin(const AttendParams& p, const Tile& t) {
+        const int lane = threadIdx.x & 31;
+        const int32_t group = (int32_t)p.by_group.d;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int32_t rr = (lane >> 2) + 8 * i;
+            const bool on = rr < t.nrows;
+            const int32_t n = (int32_t)p.by_group.div((uint32_t)(t.row0 + (on ? rr : 0)));
+            limit[i] = on ? t.limit0 + t.causal * n : 0;
+            const T* src = p.q.row<T>(t.t0 + n, t.h * group + (t.row0 + rr - n * group));
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                const int e = s * 16 + (lane & 3) * 2;
+                qf[s][i] = on ? load_pair(src + e, p.q_pairs) : 0u;
+                qf[s][2 + i] = on ? load_pair(src + e + 8, p.q_pairs) : 0u;
+            }
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    }
+
+    // The chunk at key `key0` whose K rows are at kt and V rows behind them;
+    // mask: which of its keys there are.
+    __device__ __forceinline__ void chunk(uint32_t kt, int32_t key0, uint32_t mask, float scale) {
+        const int lane = threadIdx.x & 31;
+        const uint32_t vt = kt + kTileBytes;
+        float sc[2][4] = {};
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            uint32_t b[4];
+            // matrices: keys 0-7 x d 0-7, keys 0-7 x d 8-15, keys 8-15 x d 0-7, keys 8-15 x d 8-15
+            ldmatrix4(b, kt + swizzled<kRowBytes>((lane & 7) + ((lane >> 4) << 3), 2 * s + ((lane >> 3) & 1)));
+            mma16816<T>(sc[0], qf[s], b[0], b[1]);
+            mma16816<T>(sc[1], qf[s], b[2], b[3]);
+        }
+        key0 += (lane & 3) * 2;
+        float pr[2][4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int at = n * 8 + j;
+                    const bool seen = key0 + at < limit[r] && ((mask >> (at + (lane & 3) * 2)) & 1);
+                    float& x = sc[n][2 * r + j];
+                    x = seen ? x * scale : -INFINITY;
+                    top = fmaxf(top, x);
+                }
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            const float mn = fmaxf(m[r], top);
+            const float mu = mn == -INFINITY ? 0.f : mn;      // nothing seen yet: every power is 0
+            const float corr = exp2_fast(m[r] - mu);
+            m[r] = mn;
+            float sum = 0.f;
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) sum += pr[n][2 * r + j] = exp2_fast(sc[n][2 * r + j] - mu);
+            l[r] = l[r] * corr + sum;
+            if (corr != 1.f) {
+#pragma unroll
+                for (int d = 0; d < D / 8; ++d) {
+                    o[d][2 * r] *= corr;
+                    o[d][2 * r + 1] *= corr;
+                }
+            }
+        }
+        // Weights are rounded to T for the product with V (relative error at
+        // most half a step of T each, of either sign, against the sums in fp32).
+        const uint32_t pf[4] = {Elem<T>::pack(pr[0][0], pr[0][1]), Elem<T>::pack(pr[0][2], pr[0][3]),
+                                Elem<T>::pack(pr[1][0], pr[1][1]), Elem<T>::pack(pr[1][2], pr[1][3])};
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+            uint32_t b[4];
+            ldmatrix4_trans(b, vt + swizzled<kRowBytes>(lane & 15, 2 * d + (lane >> 4)));
+            mma16816<T>(o[2 * d], pf, b[0], b[1]);
+            mma16816<T>(o[2 * d + 1], pf, b[2], b[3]);
+        }
+    }
+
+    // l becomes the whole row's.
+    __device__ __forceinline__ void end() {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 2);
+        }
+    }
+};
+
+// Small batches and short contexts: a CTA per row tile (and part of the
+// prefix).  Bound by the bytes of K and V: with a few rows per KV head the
+// products are a fraction of the loads' time, so the four warps of a CTA share
+// the rows, take 16 keys (a page) each in turn, and run by themselves: every
+// warp has its own ring of kStages x 16 K and V rows, filled by cp.async, and
+// its own running maximum, sum and output; they are joined in shared memory at
+// the end.
 template <class T, int D>
 __global__ void __launch_bounds__(kWarps * 32)
 attend_rows_kernel(const __grid_constant__ AttendParams p) {
-    constexpr int kRowBytes = D * 2;
-    constexpr int kTileBytes = kChunk * kRowBytes;   // K (or V) rows of a stage
-    constexpr int kSteps = D / 16;
+    using W = WarpRows<T, D>;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ float2 ml[kWarps][kRowTile];
     pdl_launch_dependents();
@@ -164,19 +275,15 @@ attend_rows_kernel(const __grid_constant__ AttendParams p) {
         t.k1 = t.k0;
     }
     const int32_t group = (int32_t)p.by_group.d;
-    uint8_t* const ring = smem + warp * (kStages * 2 * kTileBytes);
-    const uint32_t ring_u = smem_u32(ring);
-
+    const uint32_t ring = smem_u32(smem) + warp * (kStages * 2 * W::kTileBytes);
     const int32_t chunks = (t.k1 - t.k0 + kChunk - 1) / kChunk;
     const int32_t mine = chunks > warp ? (chunks - warp + kWarps - 1) / kWarps : 0;
     uint32_t there[kStages];       // key masks of the stages (constant indices after unrolling)
-
     ChunkCopy<D, true> rows(p.layer, t.table, base, t.h, t.k1);
     auto key_of = [&](int32_t i) { return t.k0 + (i * kWarps + warp) * kChunk; };       // my i-th chunk
     auto fill = [&](int32_t i) {                       // into its stage
-        return rows.copy(key_of(i), ring_u + (i % kStages) * (2 * kTileBytes), key_of(i + 1), p.status);
+        return rows.copy(key_of(i), ring + (i % kStages) * (2 * W::kTileBytes), key_of(i + 1), p.status);
     };
-
     // the first rows are on their way while q comes
     rows.lookup(key_of(0));
 #pragma unroll
@@ -184,117 +291,37 @@ attend_rows_kernel(const __grid_constant__ AttendParams p) {
         there[s] = s < mine ? fill(s) : 0u;
         cp_commit();
     }
-    // this thread's two rows: lane / 4 and lane / 4 + 8
-    int32_t limit[2];
-    uint32_t qf[kSteps][4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int32_t rr = (lane >> 2) + 8 * i;
-        const bool on = rr < t.nrows;
-        const int32_t n = (int32_t)p.by_group.div((uint32_t)(t.row0 + (on ? rr : 0)));
-        limit[i] = on ? t.limit0 + t.causal * n : 0;
-        const T* src = p.q.row<T>(t.t0 + n, t.h * group + (t.row0 + rr - n * group));
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            const int e = s * 16 + (lane & 3) * 2;
-            qf[s][i] = on ? load_pair(src + e, p.q_pairs) : 0u;
-            qf[s][2 + i] = on ? load_pair(src + e + 8, p.q_pairs) : 0u;
-        }
-    }
-
+    W x;
+    x.begin(p, t);
     const float signed_scale = p.scale_log2 * (float)p.scale_sign;
-    float o[D / 8][4];
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
     for (int32_t i0 = 0; i0 < mine; i0 += kStages) {
 #pragma unroll
         for (int u = 0; u < kStages; ++u) {
             const int32_t i = i0 + u;
             if (i >= mine) break;
             __syncwarp();      // the stage filled next was read by every lane
-            {
-                constexpr int kAhead = kStages - 1;
-                there[(u + kAhead) % kStages] = i + kAhead < mine ? fill(i + kAhead) : 0u;
-                cp_commit();
-            }
+            constexpr int kAhead = kStages - 1;
+            there[(u + kAhead) % kStages] = i + kAhead < mine ? fill(i + kAhead) : 0u;
+            cp_commit();
             cp_wait<kStages - 1>();
             __syncwarp();
-            const uint32_t kt = ring_u + u * (2 * kTileBytes), vt = kt + kTileBytes;
-            const uint32_t mask = there[u];
-            float sc[2][4] = {};
-#pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-                uint32_t b[4];
-                // matrices: keys 0-7 x d 0-7, keys 0-7 x d 8-15, keys 8-15 x d 0-7, keys 8-15 x d 8-15
-                ldmatrix4(b, kt + swizzled<kRowBytes>((lane & 7) + ((lane >> 4) << 3), 2 * s + ((lane >> 3) & 1)));
-                mma16816<T>(sc[0], qf[s], b[0], b[1]);
-                mma16816<T>(sc[1], qf[s], b[2], b[3]);
-            }
-            const int32_t key0 = t.k0 + (i * kWarps + warp) * kChunk + (lane & 3) * 2;
-            float pr[2][4];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float top = -INFINITY;
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int at = n * 8 + j;
-                        const bool seen = key0 + at < limit[r] && ((mask >> (at + (lane & 3) * 2)) & 1);
-                        float& x = sc[n][2 * r + j];
-                        x = seen ? x * signed_scale : -INFINITY;
-                        top = fmaxf(top, x);
-                    }
-                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                const float mn = fmaxf(m[r], top);
-                const float mu = mn == -INFINITY ? 0.f : mn;      // nothing seen yet: every power is 0
-                const float corr = exp2_fast(m[r] - mu);
-                m[r] = mn;
-                float sum = 0.f;
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) sum += pr[n][2 * r + j] = exp2_fast(sc[n][2 * r + j] - mu);
-                l[r] = l[r] * corr + sum;
-                if (corr != 1.f) {
-#pragma unroll
-                    for (int d = 0; d < D / 8; ++d) {
-                        o[d][2 * r] *= corr;
-                        o[d][2 * r + 1] *= corr;
-                    }
-                }
-            }
-            // Weights are rounded to T for the product with V (relative error at
-            // most half a step of T each, of either sign, against the sums in fp32).
-            const uint32_t pf[4] = {Elem<T>::pack(pr[0][0], pr[0][1]), Elem<T>::pack(pr[0][2], pr[0][3]),
-                                    Elem<T>::pack(pr[1][0], pr[1][1]), Elem<T>::pack(pr[1][2], pr[1][3])};
-#pragma unroll
-            for (int d = 0; d < D / 16; ++d) {
-                uint32_t b[4];
-                ldmatrix4_trans(b, vt + swizzled<kRowBytes>(lane & 15, 2 * d + (lane >> 4)));
-                mma16816<T>(o[2 * d], pf, b[0], b[1]);
-                mma16816<T>(o[2 * d + 1], pf, b[2], b[3]);
-            }
+            x.chunk(ring + u * (2 * W::kTileBytes), key_of(i), there[u], signed_scale);
         }
     }
     cp_wait<0>();
     __syncthreads();
 
-    // join the warps: sums over the quad first, then over warps in shared memory
+    // join the warps in shared memory
+    x.end();
     float* const wo = reinterpret_cast<float*>(smem) + warp * kRowTile * D;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-        l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 2);
         const int rr = (lane >> 2) + 8 * r;
-        if ((lane & 3) == 0) ml[warp][rr] = make_float2(m[r], l[r]);
+        if ((lane & 3) == 0) ml[warp][rr] = make_float2(x.m[r], x.l[r]);
 #pragma unroll
         for (int d = 0; d < D / 8; ++d)
             *reinterpret_cast<float2*>(wo + rr * D + d * 8 + (lane & 3) * 2) =
-                make_float2(o[d][2 * r], o[d][2 * r + 1]);
+                make_float2(x.o[d][2 * r], x.o[d][2 * r + 1]);
     }
     __syncthreads();
     const float* const all = reinterpret_cast<const float*>(smem);
@@ -310,12 +337,12 @@ attend_rows_kernel(const __grid_constant__ AttendParams p) {
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const float f = exp2_fast(ml[w][rr].x - mu);
-            const float4 x = *reinterpret_cast<const float4*>(all + (w * kRowTile + rr) * D + c);
+            const float4 y = *reinterpret_cast<const float4*>(all + (w * kRowTile + rr) * D + c);
             sum += f * ml[w][rr].y;
-            acc.x += f * x.x;
-            acc.y += f * x.y;
-            acc.z += f * x.z;
-            acc.w += f * x.w;
+            acc.x += f * y.x;
+            acc.y += f * y.y;
+            acc.z += f * y.z;
+            acc.w += f * y.w;
         }
         const int32_t n = (int32_t)p.by_group.div((uint32_t)(t.row0 + rr));
         const int32_t tok = t.t0 + n, head = t.h * group + (t.row0 + rr - n * group);
@@ -329,11 +356,125 @@ attend_rows_kernel(const __grid_constant__ AttendParams p) {
             dst[3] = Elem<T>::from_float(acc.w * inv);
             if (c == 0 && p.lse != nullptr) p.lse[row] = (mu + log2f(sum)) * kLn2;
         } else {
-            const int64_t at = t.r < 0 ? (int64_t)t.part * p.rows + row : p.own_part(t.part, t.r, t.row0 + rr, t.h);
+            const int64_t at = t.r < 0 ? (int64_t)t.part * p.rows + row
+                                       : p.own_part(0, t.r * p.own_tiles + t.row0 / kRowTile, rr, t.h);
             *reinterpret_cast<float4*>(p.part_o + at * D + c) = acc;
             if (c == 0) p.part_ml[at] = make_float2(top, sum);
         }
     }
+}
+
+// Longer own contexts: streams.  The chunks of all small requests' row tiles,
+// one after the other, are shared equally among warps, whatever the lengths
+// are; a warp runs through its share by itself, with no barrier, and leaves a
+// partial result for each row tile that it had some of.  Stream g of KV head h
+// is warp `g * kv_heads + h` of the launch: the heads' warps of the same tokens run
+// side by side and read the same pages' rows.
+template <class T, int D, int kRing>
+__device__ __forceinline__ void run_stream(const AttendParams& p, int32_t worker, uint32_t ring) {
+    using W = WarpRows<T, D>;
+    const int lane = threadIdx.x & 31;
+    const int32_t group = (int32_t)p.by_group.d;
+    const int32_t g = worker / p.kv_heads;
+    if (g >= p.streams) return;
+    Tile t;
+    t.h = worker - g * p.kv_heads;
+    t.causal = 1;
+    const uint8_t* const base = p.layer.base();
+    if (base == nullptr && worker == 0 && lane == 0) report(p.status, LMKV_ERR_BAD_POINTER);
+    // row tiles of a request, and chunks of each
+    auto tiles_of = [&](const Req& q) {
+        const int32_t n = q.n * group;
+        return p.big && n >= kBigRows ? 0 : (n + kRowTile - 1) / kRowTile;
+    };
+    Share share = find_share(p.seqs.num_req, g, p.streams, [&](int32_t i) -> int64_t {
+        const Req q = load_req(p.seqs, i);
+        if (!q.ok) report(p.status, LMKV_ERR_BAD_LENGTH);
+        return (int64_t)tiles_of(q) * ((q.len + kChunk - 1) / kChunk);
+    });
+    const float signed_scale = p.scale_log2 * (float)p.scale_sign;
+    W x;
+    while (share.n > 0 && share.r < p.seqs.num_req) {
+        const Req q = load_req(p.seqs, share.r);
+        const int32_t per_tile = (q.len + kChunk - 1) / kChunk;
+        const int32_t tile = per_tile > 0 ? (int32_t)(share.first / per_tile) : 0;
+        if (per_tile == 0 || tile >= tiles_of(q)) {
+            ++share.r;
+            share.first = 0;
+            continue;
+        }
+        const int32_t c0 = (int32_t)(share.first - (int64_t)tile * per_tile);
+        const int32_t n = (int32_t)min((int64_t)(per_tile - c0), share.n);
+        share.first += n;
+        share.n -= n;
+        t.r = share.r;
+        t.table = p.seqs.table + (int64_t)share.r * p.seqs.table_stride;
+        t.t0 = q.q0;
+        t.limit0 = q.len - q.n + 1;
+        t.row0 = tile * kRowTile;
+        t.nrows = q.n * group - t.row0;
+        const int32_t tile_no = share.r * p.own_tiles + tile;
+        if (t.h == 0 && lane == 0) {
+            if (c0 == 0) p.own_range[tile_no].x = g;
+            if (c0 + n == per_tile) p.own_range[tile_no].y = g;
+        }
+        // keys that the tile's last row does not see are left out
+        const int32_t last = (int32_t)p.by_group.div((uint32_t)(t.row0 + min(t.nrows, kRowTile) - 1));
+        const int32_t k0 = c0 * kChunk;
+        const int32_t k1 = base == nullptr ? k0 : max(k0, min(min(k0 + n * kChunk, q.len), t.limit0 + last));
+        const int32_t mine = (k1 - k0 + kChunk - 1) / kChunk;
+        uint32_t there[kRing];
+        ChunkCopy<D, true> rows(p.layer, t.table, base, t.h, k1);
+        auto fill = [&](int32_t i) {
+            return rows.copy(k0 + i * kChunk, ring + (i % kRing) * (2 * W::kTileBytes), k0 + (i + 1) * kChunk, p.status);
+        };
+        __syncwarp();
+        rows.lookup(k0);
+#pragma unroll
+        for (int s = 0; s < kRing - 1; ++s) {
+            there[s] = s < mine ? fill(s) : 0u;
+            cp_commit();
+        }
+        x.begin(p, t);
+        for (int32_t i0 = 0; i0 < mine; i0 += kRing) {
+#pragma unroll
+            for (int u = 0; u < kRing; ++u) {
+                const int32_t i = i0 + u;
+                if (i >= mine) break;
+                __syncwarp();      // the stage filled next was read by every lane
+                constexpr int kAhead = kRing - 1;
+                there[(u + kAhead) % kRing] = i + kAhead < mine ? fill(i + kAhead) : 0u;
+                cp_commit();
+                cp_wait<kRing - 1>();
+                __syncwarp();
+                x.chunk(ring + u * (2 * W::kTileBytes), k0 + i * kChunk, there[u], signed_scale);
+            }
+        }
+        cp_wait<0>();
+        x.end();
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int rr = (lane >> 2) + 8 * r;
+            if (rr >= t.nrows) continue;
+            const int64_t at = p.own_part(g, tile_no, rr, t.h);
+            if ((lane & 3) == 0) p.part_ml[at] = make_float2(x.m[r], x.l[r]);
+#pragma unroll
+            for (int d = 0; d < D / 8; ++d)
+                *reinterpret_cast<float2*>(p.part_o + at * D + d * 8 + (lane & 3) * 2) =
+                    make_float2(x.o[d][2 * r], x.o[d][2 * r + 1]);
+        }
+    }
+}
+
+template <class T, int D>
+__global__ void __launch_bounds__(kWarps * 32, kRowCtas)
+attend_streams_kernel(const __grid_constant__ AttendParams p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int warp = threadIdx.x >> 5;
+    run_stream<T, D, kStages>(p, blockIdx.x * kWarps + warp,
+                              smem_u32(smem) + warp * (kStages * 2 * WarpRows<T, D>::kTileBytes));
 }
 
 // ---- tiles of 128 rows on the tensor core -------------------------------
@@ -344,6 +485,7 @@ constexpr int kTileRows = 256;        // two tiles of 128 rows share every K and
 constexpr int kTileThreads = 352;     // softmax 2 x 128, loads 64, products 1 (of 32)
 constexpr int kMaxSegs = 8;           // the prefix and every big request that 256 rows can touch
 constexpr int kMaskSlots = 8;
+constexpr int kStreamWarps = 8;       // streams of a CTA that has no tiles
 
 // Keys in a row's order: the prefix, then each big request of the tile.
 struct Seg {
@@ -379,6 +521,9 @@ struct TileShape {
 // maximum has grown by more than 2^8 since, else weights simply exceed 1 (by
 // 2^8 at most), which costs nothing in fp32 sums or floating-point weights.
 // Tensor memory: scores of tile 0, 1 at columns 0, 128; outputs at 256, 384.
+// Few tiles (a decode step's) do not fill the SMs for long and leave the memory
+// idle that the own pages' streams are bound by: then some of the SMs' CTAs take the
+// tiles and the others run the streams at the same time.
 template <class T, int D>
 __global__ void __launch_bounds__(kTileThreads, 1)
 attend_tiles_kernel(const __grid_constant__ AttendParams p) {
@@ -392,6 +537,15 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
     __shared__ uint4 key_mask[kMaskSlots];
     pdl_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if ((int32_t)blockIdx.x >= p.tile_ctas) {
+        pdl_wait();
+        constexpr int kRing = 3, kBytes = kRing * 2 * WarpRows<T, D>::kTileBytes;
+        static_assert(kStreamWarps * kBytes <= S::kSmem, "the streams' rings fit");
+        if (warp < kStreamWarps)
+            run_stream<T, D, kRing>(p, ((int32_t)blockIdx.x - p.tile_ctas) * kStreamWarps + warp,
+                                    smem_u32(smem) + warp * kBytes);
+        return;
+    }
     const uint32_t full = smem_u32(bars), empty = full + 8 * S::kStages, s_full = empty + 8 * S::kStages,
                    p_ready = s_full + 16, o_full = p_ready + 32;
     const uint32_t q_smem = smem_u32(smem), kv_smem = q_smem + 2 * S::kStageBytes;
@@ -804,11 +958,21 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     const int32_t tok = q.q0 + n, head = h * group + (row_of_r - n * group);
     const int64_t row = (int64_t)tok * p.q_heads + head;
     const int32_t shared = big || p.prefix_len > 0 ? p.prefix_parts : 0;
-    const int32_t parts = shared + (big ? 0 : (q.len + p.own_span - 1) / p.own_span);
+    const int32_t tile_no = r * p.own_tiles + row_of_r / kRowTile, row_of_tile = row_of_r % kRowTile;
+    int32_t g = 0, own = 0;                // the tile's own parts: streams g, g + 1, ...
+    if (!big && q.len > 0) {
+        own = 1;
+        if (p.streams > 0) {
+            const int2 range = p.own_range[tile_no];
+            g = range.x;
+            own = range.y - range.x + 1;
+        }
+    }
+    const int32_t parts = shared + own;
     // m and l of 32 parts at a time, one a lane; then the parts' sums, whose loads
     // no longer wait for one another
-    const int64_t own_stride = (int64_t)p.seqs.num_req * p.own_cap * p.kv_heads;
-    const int64_t own0 = p.own_part(0, r, row_of_r, h);
+    const int64_t own_stride = (int64_t)p.tile_rows * p.kv_heads;
+    const int64_t own0 = p.own_part(g, tile_no, row_of_tile, h);
     auto place = [&](int32_t s) { return s < shared ? (int64_t)s * p.rows + row : own0 + (s - shared) * own_stride; };
     float top = -INFINITY, sum = 0.f, acc[kPer] = {};
     for (int32_t s0 = 0; s0 < parts; s0 += 32) {
@@ -858,10 +1022,11 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
 
 struct Plan {
     int32_t row_tiles, tiles, prefix_parts, prefix_span;
-    int32_t own_cap, own_tiles, own_splits, own_span;
-    bool big, own_final, join;
-    int64_t rows, own_rows;
-    uint64_t o_bytes, bytes;
+    int32_t own_cap, own_tiles, tile_rows, streams;
+    bool own, big, own_final, join;
+    int32_t stream_ctas;      // of the tile kernel; 0: the streams have their own launch
+    int64_t rows;
+    uint64_t o_bytes, ml_bytes, bytes;
 };
 
 constexpr int32_t kSms = 152;
@@ -912,18 +1077,40 @@ Plan make_plan(const lmkv_pool_t* pool, int32_t q_heads, int32_t num_tokens, int
         x.row_tiles = (int32_t)((batch_rows + kRowTile - 1) / kRowTile);
         split((int64_t)x.row_tiles * pool->num_kv_heads, prefix_len, &x.prefix_parts, &x.prefix_span);
     }
-    x.own_span = 1;
     x.own_cap = (int32_t)(x.big ? kBigRows - 1 : req_rows);
     x.own_tiles = (x.own_cap + kRowTile - 1) / kRowTile;
-    if (max_kv_len > 0 || prefix_len == 0)
-        split((int64_t)x.own_tiles * num_req * pool->num_kv_heads, max_kv_len > 0 ? max_kv_len : 1, &x.own_splits,
-              &x.own_span);
-    x.own_rows = (int64_t)num_req * x.own_cap * pool->num_kv_heads;
-    x.own_final = prefix_len == 0 && x.own_splits == 1;
+    x.tile_rows = x.own_cap < kRowTile ? x.own_cap : kRowTile;
+    x.own = max_kv_len > 0 || prefix_len == 0;
+    // a CTA per row tile while that is at most eight chunks a warp, else streams: as
+    // many warps as fit at once
+    if (max_kv_len > 8 * kWarps * kChunk) {
+        const int64_t heads = pool->num_kv_heads, tile_heads = x.tiles * heads;
+        int64_t warps = kRowCtas * kSms * kWarps;
+        if (!x.big && x.tiles > 0 && tile_heads <= kSms / 2) {
+            // The SMs are divided by what each side would take of them: 1.6 us for 256 rows x 128
+            // keys, 45 GB/s of an SM for the own pages, half of whose bound is there; the
+            // tiles get three eighths at least, as the bound may be far off.
+            const double tile_us = 1.6 * (double)tile_heads * (double)((prefix_len + kBlock - 1) / kBlock);
+            const double own_us = (double)num_req * heads * max_kv_len * 0.5 * pool->head_dim * 4 / 45e3;
+            int64_t n = (int64_t)(kSms * tile_us / (tile_us + own_us));
+            n = n < kSms * 3 / 8 ? kSms * 3 / 8 : n > kSms - 16 ? kSms - 16 : n;
+            const int64_t blocks = (prefix_len + kBlock - 1) / kBlock;
+            int64_t parts = n / tile_heads > 0 ? n / tile_heads : 1;
+            parts = parts > blocks ? blocks : parts;
+            x.prefix_parts = (int32_t)parts;
+            x.stream_ctas = (int32_t)(kSms - tile_heads * parts);
+            warps = (int64_t)x.stream_ctas * kStreamWarps;
+        }
+        x.streams = (int32_t)(warps / heads > 0 ? warps / heads : 1);
+        if (x.stream_ctas > 0) x.stream_ctas = (int32_t)((x.streams * heads + kStreamWarps - 1) / kStreamWarps);
+    }
+    x.own_final = prefix_len == 0 && x.streams == 0;
     x.join = x.prefix_parts > 1 || !x.own_final;
-    const uint64_t parts = x.join ? (uint64_t)x.prefix_parts * x.rows + (uint64_t)x.own_splits * x.own_rows : 0;
+    const uint64_t own_rows = ((uint64_t)x.streams + (uint64_t)num_req * x.own_tiles) * x.tile_rows * pool->num_kv_heads;
+    const uint64_t parts = x.join ? (uint64_t)x.prefix_parts * x.rows + own_rows : 0;
     x.o_bytes = parts * pool->head_dim * 4;
-    x.bytes = x.o_bytes + parts * 8;
+    x.ml_bytes = parts * 8;
+    x.bytes = x.o_bytes + x.ml_bytes + (x.join ? (uint64_t)num_req * x.own_tiles * 8 : 0);
     return x;
 }
 
@@ -938,18 +1125,24 @@ template <class T, int D>
 int attend_typed(AttendParams& p, const Plan& x, void* stream) {
     constexpr int smem = kWarps * kStages * 2 * kChunk * D * 2;
     int rc = allow_smem<attend_rows_kernel<T, D>, smem>();
+    if (rc == LMKV_OK) rc = allow_smem<attend_streams_kernel<T, D>, smem>();
     if (rc == LMKV_OK) rc = allow_smem<attend_tiles_kernel<T, D>, TileShape<D>::kSmem>();
     if (rc == LMKV_OK)
-        rc = launch(attend_tiles_kernel<T, D>, (int64_t)x.tiles * p.kv_heads * x.prefix_parts, kTileThreads,
+        rc = launch(attend_tiles_kernel<T, D>, (int64_t)x.tiles * p.kv_heads * x.prefix_parts + x.stream_ctas, kTileThreads,
                     TileShape<D>::kSmem, stream, 1, p);
     if (rc != LMKV_OK) return rc;
-    const int64_t grid = ((int64_t)x.row_tiles * x.prefix_parts +
-                          (int64_t)x.own_tiles * p.seqs.num_req * x.own_splits) * p.kv_heads;
-    rc = launch(attend_rows_kernel<T, D>, grid, kWarps * 32, smem, stream, 1, p);
+    const int64_t ctas = ((int64_t)x.row_tiles * x.prefix_parts +
+                          (x.own && x.streams == 0 ? (int64_t)x.own_tiles * p.seqs.num_req : 0)) * p.kv_heads;
+    rc = launch(attend_rows_kernel<T, D>, ctas, kWarps * 32, smem, stream, 1, p);
+    if (rc != LMKV_OK) return rc;
+    if (x.streams > 0 && x.stream_ctas == 0)
+        rc = launch(attend_streams_kernel<T, D>, ((int64_t)x.streams * p.kv_heads + kWarps - 1) / kWarps, kWarps * 32, smem,
+                    stream, 1, p);
     if (rc != LMKV_OK || !x.join) return rc;
     // the small requests' rows, where there are no others or those are done already
     if (!x.big || x.prefix_parts <= 1)
-        return launch(attend_join_kernel<T, D, true>, (x.own_rows + 7) / 8, 256, 0, stream, 1, p);
+        return launch(attend_join_kernel<T, D, true>, ((int64_t)p.seqs.num_req * x.own_cap * p.kv_heads + 7) / 8, 256, 0,
+                      stream, 1, p);
     return launch(attend_join_kernel<T, D, false>, (x.rows + 7) / 8, 256, 0, stream, 1, p);
 }
 
@@ -1000,6 +1193,7 @@ int lmkv_attend_layer(const lmkv_pool_t* pool, int32_t dtype, int32_t layer, con
     p.status = d_status;
     p.part_o = static_cast<float*>(workspace);
     p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + x.o_bytes);
+    p.own_range = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + x.o_bytes + x.ml_bytes);
     p.scale_sign = scale > 0.f ? 1 : scale < 0.f ? -1 : 0;
     p.scale_log2 = scale == 0.f ? 1.f : std::fabs(scale) * 1.44269504088896340736f;
     p.prefix_len = (int32_t)prefix_len;
@@ -1008,12 +1202,13 @@ int lmkv_attend_layer(const lmkv_pool_t* pool, int32_t dtype, int32_t layer, con
     p.rows = (int32_t)x.rows;
     p.row_tiles = x.row_tiles;
     p.tiles = x.tiles;
+    p.tile_ctas = x.tiles * p.kv_heads * x.prefix_parts;
     p.prefix_parts = x.prefix_parts;
     p.prefix_span = x.prefix_span;
     p.own_cap = x.own_cap;
     p.own_tiles = x.own_tiles;
-    p.own_splits = x.own_splits;
-    p.own_span = x.own_span;
+    p.tile_rows = x.tile_rows;
+    p.streams = x.streams;
     p.big = x.big;
     p.own_final = x.own_final;
     auto aligned = [](const lmkv_rows_t* r, int64_t to) {

@@ -270,6 +270,16 @@ def test_attend_long():
     attend_case([300], [2500], 2, 1, 64, BF, prefix=2049)
 
 
+@pytest.mark.parametrize("dtype,dim", [(BF, 128), (FP, 64)])
+@pytest.mark.parametrize("prefix", [0, 200])
+def test_attend_longer_own_contexts(dtype, dim, prefix):
+    """Contexts that several warps share, short and empty ones and several row tiles among them."""
+    attend_case([1, 1, 1, 1, 0, 1], [600, 3, 0, 1100, 700, 16], 8, 2, dim, dtype, prefix=prefix, extra_rows=1)
+    attend_case([3, 15, 1, 7], [700, 900, 0, 20], 8, 2, dim, dtype, prefix=prefix, page=24)
+    attend_case([2, 30, 5], [1, 650, 513], 8, 2, dim, dtype, prefix=prefix)     # unseen keys, a big request
+    attend_case([1, 15], [3000, 2], 16, 4, dim, dtype, prefix=prefix)
+
+
 def test_attend_many_requests():
     n = 200
     attend_case([1] * n, [1 + (i * 13) % 60 for i in range(n)], 4, 1, 64, BF, prefix=333)
