@@ -963,9 +963,10 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     if (!big && q.len > 0) {
         own = 1;
         if (p.streams > 0) {
+            // (clamped: lengths that change while the call runs give a wrong sum, not a wild address)
             const int2 range = p.own_range[tile_no];
-            g = range.x;
-            own = range.y - range.x + 1;
+            g = min(max(range.x, 0), p.streams - 1);
+            own = min(max(range.y, g), p.streams - 1) - g + 1;
         }
     }
     const int32_t parts = shared + own;
@@ -1087,10 +1088,12 @@ Plan make_plan(const lmkv_pool_t* pool, int32_t q_heads, int32_t num_tokens, int
         const int64_t heads = pool->num_kv_heads, tile_heads = x.tiles * heads;
         int64_t warps = kRowCtas * kSms * kWarps;
         if (!x.big && x.tiles > 0 && tile_heads <= kSms / 2) {
-            // The SMs are divided by what each side would take of them: 1.6 us for 256 rows x 128
-            // keys, 45 GB/s of an SM for the own pages, half of whose bound is there; the
-            // tiles get three eighths at least, as the bound may be far off.
-            const double tile_us = 1.6 * (double)tile_heads * (double)((prefix_len + kBlock - 1) / kBlock);
+            // The SMs are divided by what each side would take of them: 2.3 us for 256 rows x 128
+            // keys with its share of start and end, 45 GB/s of an SM for the own pages, half of
+            // whose bound is there; the tiles get three eighths at least, as the bound may be
+            // far off.  (64 users behind 16384 tokens, us by SMs for the tiles: 40: 74, 57: 58,
+            // 64: 55, 72: 53, 80: 55, 96: 63; one launch after the other: 70.)
+            const double tile_us = 2.3 * (double)tile_heads * (double)((prefix_len + kBlock - 1) / kBlock);
             const double own_us = (double)num_req * heads * max_kv_len * 0.5 * pool->head_dim * 4 / 45e3;
             int64_t n = (int64_t)(kSms * tile_us / (tile_us + own_us));
             n = n < kSms * 3 / 8 ? kSms * 3 / 8 : n > kSms - 16 ? kSms - 16 : n;
