@@ -714,8 +714,8 @@ int lmkv_weigh_layer(const lmkv_pool_t* pool, int32_t dtype, int32_t layer, cons
  *                 scores for i < new_len, then 0 up to budget; or NULL; not overlapping scores
  * Any element size.  A token whose block id, or whose new slot's, is out of
  * range does not move (BAD_BLOCK).  INVALID_ARG for sinks + recent > budget,
- * budget < 1, score_stride < max_kv_len, kept_stride < budget, or max_kv_len
- * beyond the table. */
+ * budget < 1, score_stride < max_kv_len, kept_stride < budget, max_kv_len
+ * beyond the table, or a layer of 2^32 - 1 token slots or more. */
 int lmkv_evict_layer(const lmkv_pool_t* pool, int32_t layer, const int32_t* block_table,
                      int32_t max_blocks, const int32_t* kv_len, int32_t num_req, int32_t max_kv_len,
                      const float* scores, int64_t score_stride, int32_t budget, int32_t sinks,

@@ -788,7 +788,7 @@ __global__ void __launch_bounds__(kMoveThreads)
 compact_kernel(const __grid_constant__ EvictParams p, int32_t pieces) {
     extern __shared__ __align__(16) uint8_t move_smem[];       // [kMoveDepth][kMoveSlots][piece]
     constexpr int kPlaces = kMoveDepth + 1;
-    __shared__ int64_t from[kPlaces][kMoveSlots], to[kPlaces][kMoveSlots];
+    __shared__ uint32_t from[kPlaces][kMoveSlots], to[kPlaces][kMoveSlots];     // rows of the K or V half
     pdl_launch_dependents();
     pdl_wait();
     int32_t x = blockIdx.x;
@@ -829,13 +829,15 @@ compact_kernel(const __grid_constant__ EvictParams p, int32_t pieces) {
         return i < batches && s < p.budget ? keep[s] : -1;
     };
     auto look_up = [&](int32_t i, int32_t tok) {
-        int64_t a = -1, b = -1;
+        uint32_t a = Layer::kNoRow, b = Layer::kNoRow;
         if (tok >= 0) {
-            a = p.layer.token_offset(table, tok);
-            b = p.layer.token_offset(table, first + i * kMoveSlots + (int32_t)threadIdx.x);
-            if (a < 0 || b < 0) {
+            const int32_t s = first + i * kMoveSlots + (int32_t)threadIdx.x;
+            const uint32_t ca = p.layer.column(tok), cb = p.layer.column(s);
+            a = p.layer.row_of(table[ca], tok, ca);
+            b = p.layer.row_of(table[cb], s, cb);
+            if (a == Layer::kNoRow || b == Layer::kNoRow) {
                 report(p.status, LMKV_ERR_BAD_BLOCK);
-                a = b = -1;
+                a = b = Layer::kNoRow;
             }
         }
         from[i % kPlaces][threadIdx.x] = a;
@@ -846,8 +848,9 @@ compact_kernel(const __grid_constant__ EvictParams p, int32_t pieces) {
             uint8_t* const stage = ring + i % kMoveDepth * (kMoveSlots * kPieceBytes);
 #pragma unroll
             for (int k = 0; k < kUnits; ++k) {
-                const int64_t a = from[i % kPlaces][s0 + k * kStep];
-                if (a < 0) continue;
+                const uint32_t row = from[i % kPlaces][s0 + k * kStep];
+                if (row == Layer::kNoRow) continue;
+                const int64_t a = (int64_t)((uint64_t)row * (uint64_t)p.layer.row_bytes);
                 uint8_t* const dst = stage + k * kMoveThreads * kBytes;
                 if constexpr (kBytes == 16) cp_async16(smem_u32(dst), at + a);
                 else if constexpr (kBytes == 4)
@@ -870,8 +873,9 @@ compact_kernel(const __grid_constant__ EvictParams p, int32_t pieces) {
             const uint8_t* const stage = ring + i % kMoveDepth * (kMoveSlots * kPieceBytes);
 #pragma unroll
             for (int k = 0; k < kUnits; ++k) {
-                const int64_t b = to[i % kPlaces][s0 + k * kStep];
-                if (b < 0) continue;
+                const uint32_t row = to[i % kPlaces][s0 + k * kStep];
+                if (row == Layer::kNoRow) continue;
+                const int64_t b = (int64_t)((uint64_t)row * (uint64_t)p.layer.row_bytes);
                 const uint8_t* const src = stage + k * kMoveThreads * kBytes;
                 if constexpr (kBytes == 16) *reinterpret_cast<int4*>(at + b) = *reinterpret_cast<const int4*>(src);
                 else if constexpr (kBytes == 4) *reinterpret_cast<int32_t*>(at + b) = *reinterpret_cast<const int32_t*>(src);
@@ -975,7 +979,8 @@ int lmkv_evict_layer(const lmkv_pool_t* pool, int32_t layer, const int32_t* bloc
     int rc = lmkv_internal_check_pool(pool);
     if (rc != LMKV_OK) return rc;
     if (layer < 0 || layer >= pool->num_layers || num_req < 0 || num_req > (1 << 24) || max_blocks < 0 ||
-        max_kv_len < 0 || max_kv_len > INT32_MAX - 65536 || max_kv_len > (int64_t)max_blocks * pool->block_size)
+        max_kv_len < 0 || max_kv_len > INT32_MAX - 65536 || max_kv_len > (int64_t)max_blocks * pool->block_size ||
+        pool->num_blocks * pool->block_size >= (int64_t)Layer::kNoRow)          // rows are numbered with 32 bits
         return LMKV_ERR_INVALID_ARG;
     if (budget < 1 || sinks < 0 || recent < 0 || (int64_t)sinks + recent > budget || score_stride < max_kv_len ||
         (kept_scores != nullptr && kept_stride < budget))

@@ -180,6 +180,7 @@ def test_evict_refusals(lib):
                 dict(table=None), dict(kept=PTR, kept_stride=31), dict(kept=PTR + 64, kept_stride=32)):
         assert evict(lib, **bad) == inv, bad
     assert evict(lib, p=pool(num_kv_heads=1, head_dim=3)) == lmkv.ERR_MISALIGNED
+    assert evict(lib, p=pool(num_blocks=2 ** 28)) == inv         # token slots are numbered with 32 bits
     assert evict(lib, num_req=0) == lmkv.OK
     assert lmkv.launch_count() == before
 
