@@ -361,7 +361,7 @@ int launch_shift(const Call& c, const lmkv_rotary_detail::Rotary& rot, const int
     const bool vector = lmkv_rotary_detail::vector_fits(rot.half, rot.interleaved, c.pool->head_dim, sizeof(T));
     if (rot.interleaved)
         return vector ? launch_shift_kernel<B, T, V, true>(c, rot, shift, stream)
-                      : launch_shift_kernel<B, T, 2, true>(c, rot, shift, stream);
+                      : launch_shift_kernel<B, T, 1, true>(c, rot, shift, stream);
     return vector ? launch_shift_kernel<B, T, V, false>(c, rot, shift, stream)
                   : launch_shift_kernel<B, T, 1, false>(c, rot, shift, stream);
 }

@@ -177,7 +177,7 @@ template <class T>
 int append_typed(AppendParams& p, bool vector, void* stream) {
     constexpr int V = 16 / sizeof(T);
     if (p.rot.interleaved)
-        return vector ? launch_append<T, V, true>(p, stream) : launch_append<T, 2, true>(p, stream);
+        return vector ? launch_append<T, V, true>(p, stream) : launch_append<T, 1, true>(p, stream);
     return vector ? launch_append<T, V, false>(p, stream) : launch_append<T, 1, false>(p, stream);
 }
 

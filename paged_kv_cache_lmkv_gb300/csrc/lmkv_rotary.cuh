@@ -41,7 +41,7 @@ __device__ __forceinline__ float2 cos_sin(uint64_t turns, int64_t pos) {
 }
 
 // V elements of T in one register vector of 16 bytes (V = 16 / sizeof(T)), or
-// a single element.
+// a single element (V = 1).
 template <class T, int V>
 struct Vec {
     T x[V];
@@ -82,39 +82,42 @@ __device__ __forceinline__ void st_vec(T* p, const Vec<T, V>& v) {
 // A head is worked on in units.  Half layout: unit u < half / V turns V pairs,
 // the vectors at u * V and half + u * V; interleaved: unit u < 2 * half / V
 // turns the V / 2 pairs of the vector at u * V.  The units after these copy
-// the vectors behind rot_dim.  V is 16 bytes' worth where pointers, strides
-// and half allow it, else 1 element (half) or 2 (interleaved).
+// the vectors behind rot_dim.  V is 16 bytes' worth where pointers, strides,
+// half and head_dim allow it, else 1: a unit is then one pair of either layout,
+// or one element (head_dim may be odd).
 // (cos, sin) of the pairs lie in shared memory as [pair of the unit][unit], so
 // that the units of a warp read consecutive places.
 template <class T, int V, bool kInterleaved, bool kStream = false>
 struct Units {
-    static constexpr int kPairs = kInterleaved ? V / 2 : V;      // of a unit
+    static constexpr bool kTwo = !kInterleaved || V == 1;        // a turning unit is two vectors
+    static constexpr int kPairs = kTwo ? V : V / 2;              // of a unit
     // The place of pair i's (cos, sin).
     static __device__ __forceinline__ int place(int i, int half) {
         return (i % kPairs) * turning(half) + i / kPairs;
     }
-    static __device__ __host__ __forceinline__ int turning(int half) {
-        return kInterleaved ? 2 * half / V : half / V;
-    }
+    static __device__ __host__ __forceinline__ int turning(int half) { return half / kPairs; }
     static __device__ __host__ __forceinline__ int count(int half, int head_dim) {
         return turning(half) + (head_dim - 2 * half) / V;
     }
+    // Where a turning unit's vectors are.
+    static __device__ __forceinline__ int first(int u) { return kInterleaved && kTwo ? 2 * u : u * V; }
+    static __device__ __forceinline__ int second(int u, int half) { return kInterleaved ? 2 * u + 1 : half + u * V; }
     Vec<T, V> a, b;
 
     __device__ __forceinline__ void load(const T* head, int u, int half) {
         const int nt = turning(half);
-        if (kInterleaved || u >= nt) {
+        if (!kTwo || u >= nt) {
             a = ld_vec<T, V, kStream>(head + (u < nt ? u * V : 2 * half + (u - nt) * V));
         } else {
-            a = ld_vec<T, V, kStream>(head + u * V);
-            b = ld_vec<T, V, kStream>(head + half + u * V);
+            a = ld_vec<T, V, kStream>(head + first(u));
+            b = ld_vec<T, V, kStream>(head + second(u, half));
         }
     }
     // cs: this token's (cos, sin) table.
     __device__ __forceinline__ void turn(const float2* cs, int u, int half) {
         const int nt = turning(half);
         if (u >= nt) return;
-        if constexpr (kInterleaved) {
+        if constexpr (!kTwo) {
 #pragma unroll
             for (int i = 0; i < V / 2; ++i) {
                 const float2 w = cs[i * nt + u];
@@ -134,11 +137,11 @@ struct Units {
     }
     __device__ __forceinline__ void store(T* head, int u, int half) const {
         const int nt = turning(half);
-        if (kInterleaved || u >= nt) {
+        if (!kTwo || u >= nt) {
             st_vec<T, V, kStream>(head + (u < nt ? u * V : 2 * half + (u - nt) * V), a);
         } else {
-            st_vec<T, V, kStream>(head + u * V, a);
-            st_vec<T, V, kStream>(head + half + u * V, b);
+            st_vec<T, V, kStream>(head + first(u), a);
+            st_vec<T, V, kStream>(head + second(u, half), b);
         }
     }
 };

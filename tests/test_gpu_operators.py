@@ -93,6 +93,11 @@ def test_append_odd_head_dims():
     append_case([1, 2], [1, 2], 3, 1, 256, F32, 256)
 
 
+@pytest.mark.parametrize("dtype,rot,interleaved", [(BF, 64, True), (F32, 2, True), (FP, 64, False)])
+def test_append_head_dim_of_no_multiple_of_two(dtype, rot, interleaved):
+    append_case([2, 5], [8, 5], 16, 16, 65, dtype, rot, interleaved)
+
+
 def test_append_far_positions():
     p = [0, 1, -1, 131071, 2 ** 20 + 1, -(2 ** 24) - 3, 2 ** 31 + 5, 123456789]
     append_case([8], [8], 4, 2, 64, F32, 64, positions=p)
@@ -176,6 +181,11 @@ def test_shifted_scatter(dtype, interleaved, rot, heads, dim, page):
     look({1})
     pkg.check(pkg.scatter_chunks_shifted(*a, status=b.status))
     look({0, 1, 2})
+
+
+@pytest.mark.parametrize("dtype,rot,interleaved", [(BF, 64, True), (F32, 2, True), (FP, 64, False)])
+def test_shifted_scatter_head_dim_of_no_multiple_of_two(dtype, rot, interleaved):
+    test_shifted_scatter(dtype, interleaved, rot, 16, 65, 16)
 
 
 def test_shifted_scatter_many_requests_and_bad_block():
