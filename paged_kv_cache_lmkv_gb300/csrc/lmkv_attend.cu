@@ -504,6 +504,67 @@ struct TileShape {
     static constexpr int kSmem = (2 + kStages) * kStageBytes;
 };
 
+// Takes a row of a part again, by one warp: its sum of e^(x - m) v over the keys that
+// it sees, times inv where the part is all there is.  For rows that a value of
+// another request has spoiled: the tile's product multiplies every key's row
+// of v, those a row does not see by a weight of 0, and 0 times infinity or
+// NaN is NaN.  32 keys a step, a key a lane for the weights, D / 32 elements a
+// lane for the sums.  (m is in units of raw scores, the sign of scale applied.)
+template <class T, int D>
+__device__ __noinline__ void seen_only(const AttendParams& p, const Seg* segs, int32_t nseg, int32_t num_blocks,
+                                       const uint8_t* base, int32_t h, int32_t part, int32_t tile_row, float m, float inv) {
+    const int32_t group = (int32_t)p.by_group.d;
+    const int32_t tok = (int32_t)p.by_group.div((uint32_t)tile_row), head = h * group + (tile_row - tok * group);
+    const int32_t b0 = (int32_t)((int64_t)num_blocks * part / p.prefix_parts);
+    const int32_t b1 = (int32_t)((int64_t)num_blocks * (part + 1) / p.prefix_parts);
+    bool own = false;
+    constexpr int kPer = D / 32;
+    const int lane = threadIdx.x & 31;
+    const T* const q = p.q.row<T>(tok, head);
+    const uint8_t* const k_rows = base + (int64_t)h * (D * 2);
+    const uint8_t* const v_rows = k_rows + p.layer.half_bytes();
+    const float mu = m == -INFINITY ? 0.f : m * p.scale_log2;
+    float acc[kPer] = {};
+    for (int32_t si = 0; si < nseg; ++si) {
+        const Seg& sg = segs[si];
+        if (sg.n >= 0 && (tok < sg.q0 || tok >= sg.q0 + sg.n)) continue;
+        own = own || sg.n >= 0;
+        int64_t end = min((int64_t)sg.end, (int64_t)(b1 - sg.first) * kBlock);
+        if (sg.n >= 0) end = min(end, (int64_t)sg.limit0 + (tok - sg.q0));
+        for (int64_t k0 = (int64_t)max(b0 - sg.first, 0) * kBlock; k0 < end; k0 += 32) {
+            const int64_t at = k0 + lane < end ? p.layer.token_offset(sg.table, (int32_t)k0 + lane) : -1;
+            float w = 0.f;
+            if (at >= 0) {
+                float x = 0.f;
+#pragma unroll 4
+                for (int c = 0; c < D / 8; ++c) {
+                    const int4 k = *reinterpret_cast<const int4*>(k_rows + at + c * 16);
+                    const T* const e = reinterpret_cast<const T*>(&k);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x = fmaf(Elem<T>::to_float(q[c * 8 + i]), Elem<T>::to_float(e[i]), x);
+                }
+                x = p.scale_sign == 0 ? 0.f : p.scale_sign < 0 ? -x : x;
+                w = exp2_fast(fmaf(x, p.scale_log2, -mu));
+            }
+            for (int j = 0; j < 32; ++j) {
+                const int64_t from = __shfl_sync(0xFFFFFFFFu, at, j);
+                const float wj = __shfl_sync(0xFFFFFFFFu, w, j);
+                if (from < 0) continue;
+                const T* const v = reinterpret_cast<const T*>(v_rows + from) + lane * kPer;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) acc[i] = fmaf(wj, Elem<T>::to_float(v[i]), acc[i]);
+            }
+        }
+    }
+    T* const out = p.out.row<T>(tok, head) + lane * kPer;
+    float* const sum = p.part_o + ((int64_t)part * p.rows + (int64_t)tok * p.q_heads + head) * D + lane * kPer;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (own && p.prefix_parts == 1) out[i] = Elem<T>::from_float(acc[i] * inv);
+        else sum[i] = acc[i];
+    }
+}
+
 // Rows of all requests, (token, head of the group) in token order, 256 to a
 // CTA, against the prefix and then against the own pages of the big requests
 // among them.  Products and powers are both near their limits, so the two
@@ -535,6 +596,7 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
     __shared__ Seg segs[kMaxSegs];
     __shared__ int32_t num_segs, num_blocks;
     __shared__ uint4 key_mask[kMaskSlots];
+    __shared__ uint32_t spoiled[8];       // rows to take again, of each softmax warp
     pdl_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if ((int32_t)blockIdx.x >= p.tile_ctas) {
@@ -563,6 +625,7 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
         gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (tid < 8) spoiled[tid] = 0;
     if (warp == 10) tmem_alloc<512>(smem_u32(&tmem_base));
     pdl_wait();
 
@@ -769,6 +832,7 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
                     const float m2 = m == -INFINITY ? -INFINITY : m * scale;
                     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
                     T* const out = p.out.row<T>(tok, head);
+                    float z = 0.f;                    // NaN once a sum is not finite
 #pragma unroll
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t y[32];
@@ -780,6 +844,8 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
 #pragma unroll
                             for (int j = 0; j < 32; ++j) y[j] = 0u;
                         }
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) z = fmaf(__uint_as_float(y[j]), 0.f, z);
                         if (!wanted) continue;
                         if (final) {
 #pragma unroll
@@ -811,6 +877,12 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
                     if (wanted && final && p.lse != nullptr)
                         p.lse[row] = ((m == -INFINITY ? 0.f : m2) + log2f(l)) * kLn2;
                     if (wanted && !final) p.part_ml[at] = make_float2(m2, l);
+                    // keys of other requests, and a sum that is not finite: this row is taken again below
+                    const bool others = nseg > (p.prefix_len > 0 ? 1 : 0) + (own >= 0 ? 1 : 0);
+                    const uint32_t again = __ballot_sync(0xFFFFFFFFu, wanted && others && z != 0.f && l < INFINITY);
+                    if (lane == 0) spoiled[warp] = again;
+                    // (q has been read for the last time)
+                    if ((again >> lane) & 1) reinterpret_cast<float2*>(smem + t * S::kStageBytes)[tid & 127] = make_float2(m, inv);
                 }
             }
         } else if (warp < 8 + kLoadWarps) {
@@ -920,6 +992,13 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
     fence_after_sync();
     if (tid == 0 && gave_up) report(p.status, LMKV_ERR_TIMEOUT);
     if (warp == 10) tmem_free<512>(tmem);
+    if (warp < 8) {
+        for (uint32_t left = spoiled[warp]; left != 0; left &= left - 1) {
+            const int at = warp * 32 + __ffs(left) - 1;
+            const float2 x = reinterpret_cast<const float2*>(smem + (warp >> 2) * S::kStageBytes)[at & 127];
+            seen_only<T, D>(p, segs, num_segs, num_blocks, base, h, part, row0 + at, x.x, x.y);
+        }
+    }
 }
 
 // Joins the parts of the rows that have more than one: a warp per row, of all

@@ -394,6 +394,30 @@ def test_attend_not_finite():
     assert bool(lse[1].isfinite().all())
 
 
+@pytest.mark.parametrize("scale", [None, -0.25, 0.0])
+@pytest.mark.parametrize("dtype,dim,prefix,heads", [(BF, 128, 20, 8), (FP, 64, 0, 8), (BF, 64, 2000, 4), (FP, 128, 300, 6)])
+def test_attend_values_of_other_requests_not_finite(dtype, dim, prefix, heads, scale):
+    """Requests whose rows share a tile: one's infinite and NaN values stay its own."""
+    b = Batch([34, 33, 3, 40], [60, 200, 50, 40], heads, 2, dim, dtype, prefix=prefix, page=24)
+    b.scale = b.scale if scale is None else scale
+    flat = b.pool.layers[1].view(2, -1, 2 * dim)
+    flat[1, b.slots(1)[3]] = math.inf
+    flat[1, b.slots(1)[150]] = math.nan
+    flat[1, b.slots(3)[0]] = -math.inf
+    out, lse = attend(b)
+    torch.cuda.synchronize()
+    assert b.status.item() == 0
+    want, want_l, tol, tol_l = b.attend()
+    within(lse, want_l, tol_l, "lse")
+    for r in (0, 2):
+        at = slice(int(b.q_start[r]), int(b.q_start[r + 1]))
+        within(out[at], want[at], tol[at], f"request {r}")
+    at = slice(int(b.q_start[1]), int(b.q_start[2]))
+    assert not bool(out[at].isfinite().any())
+    at = slice(int(b.q_start[3]), int(b.q_start[4]))
+    assert not bool(out[at].isfinite().any())
+
+
 def test_attend_bad_lengths():
     b = Batch([1, 3], [40, 50], 4, 2, 64, BF, prefix=20)
     for qs, kv in (([0, 1, 9], [40, 50]), ([0, 1, 4], [40, 10 ** 6]), ([0, 1, 4], [-3, 50]), ([-2, 1, 4], [40, 50]),
