@@ -624,7 +624,8 @@ int lmkv_rotary_init(lmkv_rotary_t* out, int32_t rot_dim, int32_t interleaved, d
  * INVALID_ARG for null pointers, sizes <= 0, num_q_heads not a multiple of
  * num_kv_heads, max_kv_len beyond the table, or a rotary that does not fit.
  * num_tokens == 0 launches nothing.  max_new is not read.  Overlap of q_out
- * with q other than q itself, or of either with k or v, is not allowed. */
+ * with q other than q itself, or of either with k or v, is not allowed.  Tokens
+ * of two requests whose tables lead to the same page slot leave either's row. */
 int lmkv_append_layer(const lmkv_pool_t* pool, int32_t dtype, int32_t layer, const lmkv_batch_t* batch,
                       int32_t num_q_heads, const lmkv_rows_t* q, const lmkv_rows_t* k,
                       const lmkv_rows_t* v, const lmkv_rows_t* q_out, const int64_t* positions,
@@ -666,7 +667,8 @@ int lmkv_scatter_layer_shifted(const lmkv_pool_t* pool, int32_t dtype, const int
  * in a block with an id out of range is not attended to (BAD_BLOCK).  Page
  * slots past kv_len are never read, whatever they hold; within a request a
  * value that is not finite may reach the rows of new tokens before it.
- * head_dim 64 or 128, bf16 or fp16 (UNSUPPORTED otherwise); scale finite.
+ * head_dim 64 or 128, bf16 or fp16 (UNSUPPORTED otherwise); scale and scale *
+ * log2(e) finite, out->data not q->data (INVALID_ARG otherwise).
  * Products of bf16 / fp16 are accumulated in fp32; softmax weights are
  * rounded to the pool's type before they meet v. */
 int lmkv_attend_workspace_bytes(const lmkv_pool_t* pool, int32_t num_q_heads, int32_t num_tokens,
@@ -691,7 +693,8 @@ int lmkv_attend_layer(const lmkv_pool_t* pool, int32_t dtype, int32_t layer, con
  *   scores_out : the same shape; may be scores itself, else not overlapping it
  * score_stride >= max_kv_len.  The sum's order is fixed: repeated calls give
  * the same bits.  A token in a block with an id out of range receives
- * nothing (BAD_BLOCK).  Types and head_dim as lmkv_attend_layer. */
+ * nothing (BAD_BLOCK); one whose key is not finite may receive NaN.  fp16: lse
+ * / scale up to 2^31.  Types, head_dim and scale as lmkv_attend_layer. */
 int lmkv_weigh_layer(const lmkv_pool_t* pool, int32_t dtype, int32_t layer, const lmkv_batch_t* batch,
                      int32_t num_q_heads, const lmkv_rows_t* q, const float* lse, float scale,
                      float decay, const float* scores, float* scores_out, int64_t score_stride,
@@ -703,7 +706,9 @@ int lmkv_weigh_layer(const lmkv_pool_t* pool, int32_t dtype, int32_t layer, cons
  * all; equal scores (-0 and +0 are equal) go to the lowest token number, a NaN is lower than any
  * number.  The kept tokens' K and V rows move, in their order, to the front
  * of the request's pages, in place: slot i of head h receives token
- * keep[r][h][i].  Requests of at most `budget` tokens keep all.
+ * keep[r][h][i].  Requests of at most `budget` tokens keep all.  A page that is in
+ * two requests' tables (a shared prefix belongs in prefix_table) would be
+ * moved twice: such requests are not evicted in one call.
  *   kv_len      : DEVICE int32 [num_req] (outside 0..max_kv_len: clamped, BAD_LENGTH)
  *   scores      : DEVICE float32 [num_req][num_kv_heads][score_stride]
  *   keep        : DEVICE int32 [num_req][num_kv_heads][budget], written: kept

@@ -83,7 +83,7 @@ constexpr int kWarps = 4;
 constexpr int kChunk = 16;        // keys a warp takes at a time
 constexpr int kStages = 2;
 constexpr int kRowCtas = 3;       // CTAs an SM: more in flight than with three stages and two CTAs
-constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLn2 = 0.69314718055994530942f, kLog2e = 1.44269504088896340736f;
 
 // A row tile's place in the batch.
 struct Tile {
@@ -1145,7 +1145,8 @@ Plan make_plan(const lmkv_pool_t* pool, int32_t q_heads, int32_t num_tokens, int
     Plan x = {};
     const int64_t group = q_heads / pool->num_kv_heads;
     const int64_t batch_rows = (int64_t)num_tokens * group;            // per KV head
-    const int64_t req_rows = (int64_t)(max_new < num_tokens ? max_new : num_tokens) * group;
+    // (a bound of 0 still has rows to look at: lengths beyond it are reported)
+    const int64_t req_rows = (int64_t)(max_new < 1 ? 1 : max_new < num_tokens ? max_new : num_tokens) * group;
     x.rows = (int64_t)num_tokens * q_heads;
     x.big = req_rows >= kBigRows;
     if (x.big || (prefix_len > 0 && batch_rows > kRowTile)) {
@@ -1253,7 +1254,7 @@ int lmkv_attend_layer(const lmkv_pool_t* pool, int32_t dtype, int32_t layer, con
     int rc = check_shape(pool);
     if (rc != LMKV_OK) return rc;
     if (!type_fits(pool, dtype)) return LMKV_ERR_UNSUPPORTED;
-    if (layer < 0 || layer >= pool->num_layers || !std::isfinite(scale)) return LMKV_ERR_INVALID_ARG;
+    if (layer < 0 || layer >= pool->num_layers || !std::isfinite(scale * kLog2e)) return LMKV_ERR_INVALID_ARG;
     rc = check_batch(pool, batch, num_q_heads);
     if (rc != LMKV_OK) return rc;
     if (prefix_len < 0 || prefix_len > INT32_MAX - 65536 || batch->max_kv_len > INT32_MAX - 65536 ||
@@ -1265,6 +1266,7 @@ int lmkv_attend_layer(const lmkv_pool_t* pool, int32_t dtype, int32_t layer, con
                              (int32_t)prefix_len, batch->max_kv_len);
     if (x.bytes > 0 && (workspace == nullptr || workspace_bytes < x.bytes)) return LMKV_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(workspace) & 15) return LMKV_ERR_MISALIGNED;
+    if (out->data == q->data) return LMKV_ERR_INVALID_ARG;
     AttendParams p = {};
     p.layer = Layer::of(pool, layer);
     p.seqs = Seqs::of(batch);
@@ -1277,7 +1279,7 @@ int lmkv_attend_layer(const lmkv_pool_t* pool, int32_t dtype, int32_t layer, con
     p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + x.o_bytes);
     p.own_range = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + x.o_bytes + x.ml_bytes);
     p.scale_sign = scale > 0.f ? 1 : scale < 0.f ? -1 : 0;
-    p.scale_log2 = scale == 0.f ? 1.f : std::fabs(scale) * 1.44269504088896340736f;
+    p.scale_log2 = scale == 0.f ? 1.f : std::fabs(scale) * kLog2e;
     p.prefix_len = (int32_t)prefix_len;
     p.q_heads = num_q_heads;
     p.kv_heads = pool->num_kv_heads;

@@ -252,16 +252,18 @@ struct WeighShape {
     static constexpr int kSmem = kExtraK + kBlock * 32;
 };
 
-// x as a sum of three numbers of type T, each times its weight: hi 2^10 + mid +
-// lo 2^-10.  fp16 parts reach +-2^26 and hold 33 bits of it, bf16 parts 24 bits of any fp32.
+// x as a sum of three numbers of type T, each times its weight: hi 2^15 + mid 2^4 +
+// lo 2^-7.  fp16 parts reach +-2^31 (half steps of 2^-3 there, of 2^-31 near 0), bf16
+// parts hold 24 bits of any fp32.
+constexpr float kHi = 0x1p15f, kMid = 0x1p4f, kLo = 0x1p-7f;
 template <class T>
 __device__ __forceinline__ void extra_parts(float x, uint32_t* hi_mid, uint32_t* lo) {
-    const T hi = Elem<T>::from_float(x * 0x1p-10f);
-    float rest = isfinite(x) ? x - Elem<T>::to_float(hi) * 0x1p10f : 0.f;
-    const T mid = Elem<T>::from_float(rest);
-    rest -= Elem<T>::to_float(mid);
+    const T hi = Elem<T>::from_float(x * (1.f / kHi));
+    float rest = isfinite(x) ? x - Elem<T>::to_float(hi) * kHi : 0.f;
+    const T mid = Elem<T>::from_float(rest * (1.f / kMid));
+    rest -= Elem<T>::to_float(mid) * kMid;
     *hi_mid = Elem<T>::pack(Elem<T>::to_float(hi), Elem<T>::to_float(mid));
-    *lo = Elem<T>::pack(rest * 0x1p10f, 0.f);
+    *lo = Elem<T>::pack(rest * (1.f / kLo), 0.f);
 }
 
 // The share's parts in turn: keys of one request at a time.  Every role walks
@@ -317,7 +319,7 @@ weigh_tiles_kernel(const __grid_constant__ WeighParams p) {
     if (tid < kBlock) {
         // every key's extra columns: what the parts of -lse / scale count for
         *reinterpret_cast<uint4*>(smem + S::kExtraK + plain16_offset(tid, 0)) =
-            make_uint4(Elem<T>::pack(0x1p10f, 1.f), Elem<T>::pack(0x1p-10f, 0.f), 0u, 0u);
+            make_uint4(Elem<T>::pack(kHi, kMid), Elem<T>::pack(kLo, 0.f), 0u, 0u);
         *reinterpret_cast<uint4*>(smem + S::kExtraK + plain16_offset(tid, 1)) = make_uint4(0u, 0u, 0u, 0u);
     }
     if (tid == 0) {
@@ -905,7 +907,7 @@ constexpr int kTileMinRows = 48;
 template <class T, int D>
 int weigh_typed(WeighParams& p, void* stream) {
     const int64_t rows = (int64_t)(p.seqs.max_new < p.seqs.num_tokens ? p.seqs.max_new : p.seqs.num_tokens) * p.by_group.d;
-    // (the tile kernel carries -lse / scale, in fp16 up to 2^26: lse up to 16384 at the smallest scale it takes)
+    // (the tile kernel carries -lse / scale, in fp16 up to 2^31: lse up to 2^19 at the smallest scale it takes)
     const bool tiles = rows >= kTileMinRows && std::fabs(p.scale_log2) >= 0x1p-12f * kLog2e;
     p.lse_scale = kLog2e / p.scale_log2;
     const int64_t heads = p.kv_heads, req = p.seqs.num_req;
@@ -938,7 +940,7 @@ int lmkv_weigh_layer(const lmkv_pool_t* pool, int32_t dtype, int32_t layer, cons
     if (rc != LMKV_OK) return rc;
     if (pool->elem_bytes != 2 || (pool->head_dim != 64 && pool->head_dim != 128) || !type_fits(pool, dtype))
         return LMKV_ERR_UNSUPPORTED;
-    if (layer < 0 || layer >= pool->num_layers || !std::isfinite(scale) || !std::isfinite(decay))
+    if (layer < 0 || layer >= pool->num_layers || !std::isfinite(scale * kLog2e) || !std::isfinite(decay))
         return LMKV_ERR_INVALID_ARG;
     rc = check_batch(pool, batch, num_q_heads);
     if (rc != LMKV_OK) return rc;
@@ -986,7 +988,8 @@ int lmkv_evict_layer(const lmkv_pool_t* pool, int32_t layer, const int32_t* bloc
         (kept_scores != nullptr && kept_stride < budget))
         return LMKV_ERR_INVALID_ARG;
     if (num_req == 0) return LMKV_OK;
-    if (kv_len == nullptr || keep == nullptr || new_len == nullptr || new_len == kv_len || kept_scores == scores ||
+    if (kv_len == nullptr || keep == nullptr || new_len == nullptr || new_len == kv_len ||
+        (kept_scores != nullptr && kept_scores == scores) ||
         (max_kv_len > 0 && (block_table == nullptr || scores == nullptr)))
         return LMKV_ERR_INVALID_ARG;
     EvictParams p = {};

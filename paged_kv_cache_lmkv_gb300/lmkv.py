@@ -880,11 +880,12 @@ def _shifted_args(pool, block_table, start, end, chunk_size, save_unfull, chunk_
     t0 = pool.layers[0]
     dev = t0.get_device()
     _elsewhere(dev, ("block_table", "chunk_ptrs", "status"), (block_table, chunk_ptrs, status))
-    if block_table.dtype != torch.int32:
-        raise ValueError("block_table must be int32")
     s, e, sh = _i64_array(start), _i64_array(end), _i64_array(shift)
     if s.shape != e.shape or s.shape != sh.shape:
         raise ValueError("start, end and shift must have one entry per request")
+    if block_table.dtype != torch.int32 or not block_table.is_contiguous() or block_table.dim() != 2 or \
+            block_table.shape[0] < len(s):
+        raise ValueError("block_table must be contiguous int32 [requests][blocks]")
     # the host arrays go as bytes: they are read during the call
     return (pool.struct, _dtype_of(t0), block_table.data_ptr(), block_table.shape[-1], s.tobytes(), e.tobytes(),
             len(s), chunk_size, int(save_unfull), _ptr(chunk_ptrs), sh.tobytes(), rotary.struct), dev

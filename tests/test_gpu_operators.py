@@ -2,6 +2,9 @@
 retrieve, shared-prefix attention, attention weights, eviction, and a decode
 step of them together (eager, captured and replayed)."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -429,6 +432,16 @@ def test_attend_bad_lengths():
         assert st.item() == lmkv.ERR_BAD_LENGTH, (qs, kv)
 
 
+@pytest.mark.parametrize("prefix,kv", [(0, 50), (20, 50), (20, 900)])
+def test_attend_bound_of_no_new_tokens(prefix, kv):
+    """Tokens beyond a bound of 0 are reported and their rows left."""
+    b = Batch([1, 2], [40, kv], 4, 2, 64, BF, prefix=prefix)
+    out, lse = attend(b, max_new=0)
+    torch.cuda.synchronize()
+    assert b.status.item() == lmkv.ERR_BAD_LENGTH
+    assert bool((out == 7.0).all()) and bool((lse == 7.0).all())
+
+
 # ---- attention weights --------------------------------------------------
 
 def weigh_case(*a, decay=1.0, fresh=False, in_place=False, **kw):
@@ -471,6 +484,26 @@ def test_weigh_options():
     weigh_case([2, 3], [40, 9], 4, 2, 64, BF, decay=0.0)
     weigh_case([2, 4], [40, 2], 4, 2, 64, BF, in_place=True)           # tokens that see nothing
     weigh_case([0, 0], [40, 9], 4, 2, 64, BF, decay=0.5)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_weigh_window_of_large_products(dtype):
+    """Products of 2^28, whose weight against an lse of their size is exactly 1: powers of
+    two all along, which the product of a tile and -lse / scale leave as they are."""
+    b = Batch([70], [200], 2, 2, 64, dtype)
+    b.q.zero_()
+    b.q[:, :, 0] = 2.0 ** 14
+    flat = b.pool.layers[1].view(2, -1, 2, 64)
+    flat[0, b.slots(0)] = 0.0
+    flat[0, b.slots(0)[9], :, 0] = 2.0 ** 14
+    lse = torch.full((70, 2), 2.0 ** 24, device=DEV)
+    out = torch.full((1, 2, 200), 7.0, device=DEV)
+    pkg.check(pkg.weigh_layer(b.pool, 1, b.q, lse, b.q_start_d, b.kv_len_d, b.table_d, 2.0 ** -4, None, out, decay=0.0,
+                              status=b.status))
+    torch.cuda.synchronize()
+    want = torch.zeros(200)
+    want[9] = 70.0
+    assert torch.equal(out[0].cpu(), want.repeat(2, 1))
 
 
 def test_weigh_repeats_bits_and_bad_block():
@@ -576,6 +609,18 @@ def test_evict_ties_and_special_scores():
 def test_evict_repeated_call_is_the_same_move():
     evict_case([64] * 40, 48, 0, 0, kv_heads=1, dim=64, max_kv=64)
     evict_case([17] * 300, 16, 0, 0, kv_heads=1, dim=64)
+
+
+def test_evict_nothing_cached():
+    """A batch with no room for cached tokens: no scores, no table."""
+    b = Batch([0, 0], [0, 0], 2, 2, 64, BF)
+    keep = torch.full((2, 2, 3), 7, dtype=torch.int32, device=DEV)
+    new_len = torch.full((2,), 7, dtype=torch.int32, device=DEV)
+    pkg.check(pkg.evict_layer(b.pool, 1, b.table_d, b.kv_len_d, torch.empty((2, 2, 0), device=DEV), 1, 1, keep, new_len,
+                              status=b.status))
+    torch.cuda.synchronize()
+    assert b.status.item() == 0
+    assert bool((keep == -1).all()) and bool((new_len == 0).all())
 
 
 def test_evict_bad_block_and_length():
@@ -719,3 +764,61 @@ def test_two_streams_at_once():
                                        max_kv_len=max(b.kv), stream=s))
     torch.cuda.synchronize()
     assert torch.equal(bufs[0][1], ref) and torch.equal(bufs[1][1], ref)
+
+
+def test_first_calls_are_captured():
+    """A process whose first calls of the operators are made under capture."""
+    code = """
+import torch
+import paged_kv_cache_lmkv_gb300 as pkg
+from operator_util import Batch, DEV
+b = Batch([70, 1], [200, 90], 8, 2, 64, torch.bfloat16, prefix=150)
+c = Batch([1, 1], [1000, 90], 8, 2, 64, torch.bfloat16)
+k = torch.randn((71, 2, 64), device=DEV).bfloat16()
+rot = pkg.Rotary(64)
+s = torch.cuda.Stream()
+
+def run(b):
+    n, m, w = len(b.new), max(b.kv), max(b.new)
+    ws = torch.empty(pkg.attend_workspace_bytes(b.pool, b.heads, b.tokens, n, w, b.prefix, m), dtype=torch.uint8,
+                     device=DEV)
+    out, q = torch.zeros_like(b.q), torch.zeros_like(b.q)
+    lse = torch.zeros((b.tokens, b.heads), device=DEV)
+    scores = torch.zeros((n, b.kv_heads, m), device=DEV)
+    keep = torch.zeros((n, b.kv_heads, 32), dtype=torch.int32, device=DEV)
+    new_len = torch.zeros(n, dtype=torch.int32, device=DEV)
+    kk = k[:b.tokens]
+
+    def go():
+        pkg.check(pkg.append_layer(b.pool, 1, b.table_d, b.q, kk, kk, q, b.q_start_d, b.kv_len_d, rot, status=b.status))
+        pkg.check(pkg.attend_layer(b.pool, 1, q, out, b.q_start_d, b.kv_len_d, b.table_d, b.scale, ws,
+                                   prefix_table=b.prefix_table_d, prefix_len=b.prefix, lse=lse, max_new=w,
+                                   max_kv_len=m, status=b.status))
+        pkg.check(pkg.weigh_layer(b.pool, 1, q, lse, b.q_start_d, b.kv_len_d, b.table_d, b.scale, scores, scores,
+                                  max_new=w, status=b.status))
+        pkg.check(pkg.evict_layer(b.pool, 1, b.table_d, b.kv_len_d, scores, 2, 6, keep, new_len, status=b.status))
+    start = [x.clone() for x in b.pool.layers]
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=s):
+        go()
+    g.replay()
+    torch.cuda.synchronize()
+    first = [x.clone() for x in (q, out, lse, scores, keep, new_len, *b.pool.layers)]
+    for x, y in zip(b.pool.layers, start):
+        x.copy_(y)
+    scores.zero_()
+    go()
+    torch.cuda.synchronize()
+    assert b.status.item() == 0
+    for x, y in zip(first, (q, out, lse, scores, keep, new_len, *b.pool.layers)):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+run(b)
+run(c)
+print("same")
+"""
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([os.path.dirname(here), here, os.environ.get("PYTHONPATH", "")]))
+    r = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]

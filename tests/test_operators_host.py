@@ -185,6 +185,15 @@ def test_evict_refusals(lib):
     assert lmkv.launch_count() == before
 
 
+def test_refusals_of_scales_and_shared_rows(lib):
+    before = lmkv.launch_count()
+    for scale in (3e38, -3e38):                     # not finite once log2(e) is folded in
+        assert attend(lib, scale=scale, out=ROWS | dict(data=PTR + 4096)) == lmkv.ERR_INVALID_ARG
+        assert weigh(lib, scale=scale) == lmkv.ERR_INVALID_ARG
+    assert attend(lib) == lmkv.ERR_INVALID_ARG      # out is q
+    assert lmkv.launch_count() == before
+
+
 def shifted(lib, p=None, dtype=lmkv.BF16, shift=(5,), rot=None, layer=None, start=(0,), end=(300,), chunk=256):
     s, e = np.array(start, np.int64), np.array(end, np.int64)
     sh = None if shift is None else np.array(shift, np.int64)
@@ -257,3 +266,16 @@ def test_binding_refusals(lib):
     bad(lmkv.scatter_chunks_shifted, p, table, [0, 0], [64, 64], 64, True, ws, [1], rot)
     p.layers = [x.to(torch.uint8) for x in layers]
     bad(app)
+
+
+def test_binding_refuses_shifted_tables(lib):
+    import torch
+    p = lmkv.Pool.__new__(lmkv.Pool)
+    p.layers = [torch.zeros((2, 8, 16, 128), dtype=torch.bfloat16)]
+    p.num_kv_heads, p.head_dim, p.block_size, p.num_blocks, p.elem_bytes = 2, 64, 16, 8, 2
+    p._struct = pool(num_blocks=8, num_layers=1)
+    table, ptrs = torch.zeros((2, 8), dtype=torch.int32), torch.zeros(2, dtype=torch.int64)
+    for t in (table[:1], table[:, ::2], table[0], table.long()):
+        for fn, more in ((lmkv.scatter_chunks_shifted, ()), (lmkv.scatter_layer_shifted, (0,))):
+            with pytest.raises(ValueError):
+                fn(p, t, [0, 0], [64, 64], 64, True, ptrs, [1, 1], lmkv.Rotary(64), *more)
