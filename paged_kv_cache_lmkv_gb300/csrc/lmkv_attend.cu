@@ -36,7 +36,8 @@ struct Rows {
 // A request whose rows per KV head (new tokens x heads of the group) reach
 // kBigRows has its own pages attended to by the tile kernel, after the prefix
 // and in the same pass; the others', with too few rows for a tile of 128, by
-// the row kernel.
+// the row kernel.  (Tiles against rows, us: 64 requests of 1000 keys, 48 rows 120 :
+// 152, 64 rows 96 : 160; of 300 keys, 48 rows 61 : 50, 64 rows 50 : 58.)
 constexpr int kBigRows = 64;
 
 struct AttendParams {
@@ -1111,6 +1112,14 @@ struct Plan {
 
 constexpr int32_t kSms = 152;
 
+// Scores of a prefix (rows x keys x KV heads) from which its rows are taken by tiles.
+// Below, the row kernel's 16 rows at a time read the prefix again from L2 in
+// less time than tiles take to begin and to be joined.  (Rows against tiles,
+// us, 8 heads: 128 rows x 1000 keys 25 : 43, x 8192 48 : 51; 256 x 3000 48 : 57, x 8192
+// 72 : 63; 512 x 1000 50 : 63, x 3000 67 : 69, x 8192 117 : 78; 2 heads, 2048 x 3000 66 : 69; 32
+// heads, 128 x 3000 68 : 70, 256 x 3000 108 : 95.)
+constexpr double kTileScores = 12 << 20;
+
 // Splits of `keys` keys over `ctas` CTAs each: enough for six on every SM (two rounds of three),
 // none below 128 keys.
 void split(int64_t ctas, int32_t keys, int32_t* splits, int32_t* span) {
@@ -1149,7 +1158,7 @@ Plan make_plan(const lmkv_pool_t* pool, int32_t q_heads, int32_t num_tokens, int
     const int64_t req_rows = (int64_t)(max_new < 1 ? 1 : max_new < num_tokens ? max_new : num_tokens) * group;
     x.rows = (int64_t)num_tokens * q_heads;
     x.big = req_rows >= kBigRows;
-    if (x.big || (prefix_len > 0 && batch_rows > kRowTile)) {
+    if (x.big || (batch_rows > kRowTile && (double)batch_rows * prefix_len * pool->num_kv_heads > kTileScores)) {
         x.tiles = (int32_t)((batch_rows + kTileRows - 1) / kTileRows);
         const int64_t blocks = ((int64_t)prefix_len + kBlock - 1) / kBlock +
                                (x.big ? ((int64_t)max_kv_len + kBlock - 1) / kBlock : 0);
@@ -1162,12 +1171,17 @@ Plan make_plan(const lmkv_pool_t* pool, int32_t q_heads, int32_t num_tokens, int
     x.own_tiles = (x.own_cap + kRowTile - 1) / kRowTile;
     x.tile_rows = x.own_cap < kRowTile ? x.own_cap : kRowTile;
     x.own = max_kv_len > 0 || prefix_len == 0;
-    // a CTA per row tile while that is at most eight chunks a warp, else streams: as
-    // many warps as fit at once
-    if (max_kv_len > 8 * kWarps * kChunk) {
-        const int64_t heads = pool->num_kv_heads, tile_heads = x.tiles * heads;
+    // A CTA per row tile while that is at most 16 chunks a warp, else streams: as many warps
+    // as fit at once.  (CTAs against streams, us: 4 requests of 512 keys 15 : 19, 1024 23 : 23,
+    // 2048 35 : 26; 32 requests 23 : 30, 37 : 44, 62 : 67, all of the same length, which is where
+    // streams gain least.)  Streams that run beside the tiles gain at any length.  (One launch
+    // after the other against beside: 64 requests behind 16384 keys, of 32 keys 64 : 51, 512 100 :
+    // 68, 2048 178 : 132; 128 behind 8192, 65 : 46, 118 : 80, 239 : 205.)
+    const int64_t heads = pool->num_kv_heads, tile_heads = x.tiles * heads;
+    const bool beside = !x.big && x.tiles > 0 && tile_heads <= kSms / 2;
+    if (max_kv_len > (beside ? 0 : 16 * kWarps * kChunk)) {
         int64_t warps = kRowCtas * kSms * kWarps;
-        if (!x.big && x.tiles > 0 && tile_heads <= kSms / 2) {
+        if (beside) {
             // The SMs are divided by what each side would take of them: 2.3 us for 256 rows x 128
             // keys with its share of start and end, 45 GB/s of an SM for the own pages, half of
             // whose bound is there; the tiles get three eighths at least, as the bound may be

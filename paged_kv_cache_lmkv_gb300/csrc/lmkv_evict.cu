@@ -900,9 +900,11 @@ int launch_compact(const EvictParams& p, void* stream) {
                   pieces);
 }
 
-// Rows per KV head from which the tile kernel takes a batch: below, the row
-// kernel's products cost less than a tile of 128 rows that is mostly empty.
-constexpr int kTileMinRows = 48;
+// Rows per KV head from which the tile kernel takes a batch: beyond one second
+// operand of the row kernel, whose products are then many for the keys that it
+// reads.  (Rows against tiles, us: 8 requests of 8000 keys, 8 rows 40 : 42, 16 rows 58 : 42, 64
+// rows 95 : 42; 2 of 3000, 13 : 17, 17 : 16, 25 : 17; 24 of 2000, 33 : 36, 48 : 36, 80 : 38.)
+constexpr int kTileMinRows = 9;
 
 template <class T, int D>
 int weigh_typed(WeighParams& p, void* stream) {

@@ -293,6 +293,22 @@ def test_attend_longer_own_contexts(dtype, dim, prefix):
     attend_case([1, 15], [3000, 2], 16, 4, dim, dtype, prefix=prefix)
 
 
+@pytest.mark.parametrize("dtype,dim", [(BF, 128), (FP, 64)])
+def test_attend_longer_own_contexts_unseen_keys(dtype, dim):
+    attend_case([2, 30, 5], [1, 1100, 1030], 8, 2, dim, dtype)
+    attend_case([15, 3], [1500, 9], 8, 2, dim, dtype, prefix=30, page=24)
+
+
+@pytest.mark.parametrize("dtype,dim", [(BF, 128), (FP, 64)])
+@pytest.mark.parametrize("longest", [60, 900])
+def test_attend_long_prefix_of_many_rows(dtype, dim, longest):
+    """Rows and keys enough for tiles of the prefix, with short own contexts and with
+    longer ones (beside the tiles)."""
+    new = [1] * 78 + [0, 3]
+    attend_case(new, [1 + (i * 17) % 60 for i in range(78)] + [longest, longest - 7], 8, 2, dim, dtype, prefix=20011,
+                extra_rows=2)
+
+
 def test_attend_many_requests():
     n = 200
     attend_case([1] * n, [1 + (i * 13) % 60 for i in range(n)], 4, 1, 64, BF, prefix=333)
@@ -484,6 +500,23 @@ def test_weigh_options():
     weigh_case([2, 3], [40, 9], 4, 2, 64, BF, decay=0.0)
     weigh_case([2, 4], [40, 2], 4, 2, 64, BF, in_place=True)           # tokens that see nothing
     weigh_case([0, 0], [40, 9], 4, 2, 64, BF, decay=0.5)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -14, -2.0 ** -14, 0.0])
+@pytest.mark.parametrize("dtype,dim", [(BF, 64), (FP, 128)])
+def test_weigh_scales_near_zero(dtype, dim, scale):
+    b = Batch([70, 3, 1], [200, 90, 33], 8, 2, dim, dtype)
+    b.scale = scale
+    lse = b.attend()[1].float()
+    scores = torch.rand((3, 2, 200), generator=torch.Generator().manual_seed(4))
+    out = scores.to(DEV)
+    pkg.check(pkg.weigh_layer(b.pool, 1, b.q, lse.to(DEV), b.q_start_d, b.kv_len_d, b.table_d, scale, out, out, decay=0.5,
+                              status=b.status))
+    torch.cuda.synchronize()
+    assert b.status.item() == 0
+    want, tol = b.weigh(lse, scores, 0.5)
+    for r, n in enumerate(b.kv):
+        within(out[r, :, :n], want[r, :, :n], tol[r, :, :n], f"request {r}")
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
