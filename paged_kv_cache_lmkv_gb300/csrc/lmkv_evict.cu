@@ -52,21 +52,6 @@ __device__ __forceinline__ int4 load_q(const T* src, bool vec) {
                      (int)load_pair(src + 6, false));
 }
 
-// D elements of a row of q, all their loads on their way before the first is waited for.
-template <class T, int D>
-__device__ __forceinline__ void load_q_row(int4 (&v)[D / 8], const T* src, bool vec, bool on) {
-#pragma unroll
-    for (int c = 0; c < D / 8; ++c) v[c] = make_int4(0, 0, 0, 0);
-    if (!on) return;
-    if (vec) {
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) v[c] = *reinterpret_cast<const int4*>(src + c * 8);
-    } else {
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) v[c] = load_q(src + c * 8, false);
-    }
-}
-
 // A CTA's keys: its request, head and range.
 struct WeighPart {
     Req q;
@@ -377,19 +362,28 @@ weigh_tiles_kernel(const __grid_constant__ WeighParams p) {
                     bar_sync(1, 512);
                 }
                 {
-                    // half a row of q for each thread; rows that are not there weigh nothing
+                    // q by pieces of 16 bytes, a row's side by side (half a row a thread took 3.5 us: 32
+                    // lines a load), all on their way before the first is waited for; rows that are not
+                    // there weigh nothing
+                    constexpr int kPieces = D / 8, kMine = kTileRows * kPieces / 512;
+                    int4 qv[kMine];
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i) {
+                        const int32_t at = i * 512 + tid, r = at / kPieces;
+                        const int32_t n = (int32_t)p.by_group.div((uint32_t)(row0 + r));
+                        const int32_t head = x.h * group + (row0 + r - n * group);
+                        qv[i] = r < nrows ? load_q(p.q_row<T>(x.q.q0 + n, head) + at % kPieces * 8, p.q_vec)
+                                          : make_int4(0, 0, 0, 0);
+                    }
                     const int row = tid >> 1, part = tid & 1;
                     const bool on = row < nrows;
                     const int32_t n = (int32_t)p.by_group.div((uint32_t)(row0 + (on ? row : 0)));
                     const int32_t head = x.h * group + (on ? row0 + row - n * group : 0);
-                    int4 qv[D / 16];
-                    load_q_row<T, D / 2>(qv, p.q_row<T>(x.q.q0 + n, head) + part * (D / 2), p.q_vec, on);
                     const float lse = on ? p.lse[(int64_t)(x.q.q0 + n) * p.q_heads + head] : INFINITY;
-                    const uint32_t dst = q_smem + row * 128;
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        const int c = part * (D / 16) + i;
-                        const uint32_t to = dst + (c >> 3) * (kTileRows * 128) + (((c & 7) ^ (row & 7)) << 4);
+                    for (int i = 0; i < kMine; ++i) {
+                        const int32_t at = i * 512 + tid, r = at / kPieces, c = at % kPieces;
+                        const uint32_t to = q_smem + r * 128 + (c >> 3) * (kTileRows * 128) + (((c & 7) ^ (r & 7)) << 4);
                         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(qv[i].x), "r"(qv[i].y),
                                      "r"(qv[i].z), "r"(qv[i].w) : "memory");
                     }
