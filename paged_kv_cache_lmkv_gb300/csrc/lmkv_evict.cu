@@ -72,7 +72,8 @@ constexpr int kRowCtas = 5;        // CTAs an SM
 // rows, eight at a time; kOne: no request has more than eight, whose q stays
 // in registers.  One round of CTAs takes equal shares of the batch's tokens
 // (find_share): with a CTA per 1024 tokens the last round's idle SMs cost up to a
-// fifth.  Heads change fastest: the heads' CTAs of the same tokens read the
+// fifth (67 : 50 us).  24 requests of 1000 to 9000 tokens, 8 KV heads of 128: 49.6 us, 5.25
+// TB/s, 0.78 of the copy rate; q in registers 62 : 65 us on 24 of 5000.  Heads change fastest: the heads' CTAs of the same tokens read the
 // same pages' rows.
 template <class T, int D, bool kOne>
 __global__ void __launch_bounds__(kWarps * 32, kRowCtas)
@@ -224,7 +225,11 @@ weigh_rows_kernel(const __grid_constant__ WeighParams p) {
 // shared memory took as much of its bandwidth as the product's operands do,
 // and bound the kernel (2350 cycles a block, of which the powers take 1024).
 // Shares as the row kernel's, a CTA an SM; a request's rows beyond 256 go over
-// the share again, from L2.
+// the share again, from L2.  (4 windows of 64 tokens at 5000 to 16000, 32 heads on 8 of 128:
+// 31.5 us a call.  With three quarters of the powers left out it was 31 of 37: what
+// bounds it is the wait for a block's product, 1340 cycles, between two blocks of a
+// parity, the start, and CTAs whose share begins a second request.  Scores fetched ahead of their
+// use, 16 or 32 a time, spill: 41 and 51.)
 constexpr int kTileThreads = 608;
 constexpr int kTileRows = 256;
 
@@ -600,7 +605,8 @@ __device__ __forceinline__ int2 scan_pairs(int2 mine, int2* warp_sums) {
 // instructions, on the SM of the longest request.  Wide digits are for the
 // counters: scores crowd into few exponents, and threads that meet on a
 // counter take turns; the score that most tokens may share, zero, is counted
-// in registers.
+// in registers.  (12 requests of 3500 to 20000 tokens, 8 heads: 17.7 us.  With the move of 12
+// of 20000 staged 42 : 48 us not staged, of 48000 60 : 78.)
 template <bool kStaged>
 __global__ void __launch_bounds__(kSelectThreads)
 select_kernel(const __grid_constant__ EvictParams p) {
@@ -778,7 +784,10 @@ constexpr int kPieceBytes = 64;            // of a head's row: more CTAs, whole 
 // what it fetched itself, with one barrier a batch.  Where rows come from and
 // go to is looked up two batches ahead of the fetch, a slot a thread.  Slots whose token
 // stays (a leading run, as keep[i] - i never falls) are skipped.  Bound by
-// reading and writing the moved rows.
+// reading and writing the moved rows.  (The same batch to 4096 tokens: 76 us, 360 MB, 4.7
+// TB/s, 0.70 of the copy rate: the rows are read in pieces of 64 bytes from all over the
+// pages.  Pieces of 32 bytes 128 : 104 us a call, of 128 bytes 105; four batches on their way 103,
+// five 130.)
 template <int kBytes>
 __global__ void __launch_bounds__(kMoveThreads)
 compact_kernel(const __grid_constant__ EvictParams p, int32_t pieces) {
