@@ -224,13 +224,14 @@ weigh_rows_kernel(const __grid_constant__ WeighParams p) {
 // so that a thread needs nothing but the scores: reading 128 rows' lse from
 // shared memory took as much of its bandwidth as the product's operands do,
 // and bound the kernel (2350 cycles a block, of which the powers take 1024).
-// Shares as the row kernel's, a CTA an SM; a request's rows beyond 256 go over
-// the share again, from L2.  (4 windows of 64 tokens at 5000 to 16000, 32 heads on 8 of 128:
-// 31.5 us a call.  With three quarters of the powers left out it was 31 of 37: what
+// Shares as the row kernel's, a CTA an SM, where a request counts kTileBegin blocks
+// before its own; its rows beyond 256 go over the share again, from L2.  (4 windows of 64 tokens at 5000 to 16000, 32 heads on 8 of 128:
+// 29.0 us a call.  With three quarters of the powers left out it was 31 of 37: what
 // bounds it is the wait for a block's product, 1340 cycles, between two blocks of a
-// parity, the start, and CTAs whose share begins a second request.  Scores fetched ahead of their
+// parity, and the start.  Scores fetched ahead of their
 // use, 16 or 32 a time, spill: 41 and 51.)
 constexpr int kTileThreads = 608;
+constexpr int kTileBegin = 3;      // blocks' time that beginning a request costs (0: 31.5 us, 2: 29.6, 3: 29.2, 6: 29.6)
 constexpr int kTileRows = 256;
 
 template <int D>
@@ -268,14 +269,18 @@ struct WeighWalk {
     __device__ __forceinline__ bool next(bool there) {
         for (; share.n > 0 && share.r < p.seqs.num_req; ++share.r, share.first = 0) {
             x.q = load_req(p.seqs, share.r);
-            const int64_t here = min((int64_t)(x.q.len + kBlock - 1) / kBlock - share.first, share.n);
+            // a request counts kTileBegin units before its blocks
+            const int64_t all = x.q.len > 0 ? (int64_t)(x.q.len + kBlock - 1) / kBlock + kTileBegin : 0;
+            const int64_t here = min(all - share.first, share.n);
             if (here <= 0) continue;
             share.n -= here;
-            x.k0 = (int32_t)share.first * kBlock;
-            x.k1 = min(x.k0 + (int32_t)here * kBlock, x.q.len);
+            const int64_t b0 = max(share.first - kTileBegin, (int64_t)0), b1 = share.first + here - kTileBegin;
+            if (b1 <= b0) continue;
+            x.k0 = (int32_t)b0 * kBlock;
+            x.k1 = (int32_t)min(b1 * kBlock, (int64_t)x.q.len);
             x.table = p.seqs.table + (int64_t)share.r * p.seqs.table_stride;
             rows = there ? x.q.n * (int32_t)p.by_group.d : 0;
-            blocks = (int32_t)here;
+            blocks = (int32_t)(b1 - b0);
             passes = (rows + kTileRows - 1) / kTileRows;
             at = ((int64_t)share.r * p.kv_heads + x.h) * p.score_stride + x.k0;
             ++share.r;
@@ -332,7 +337,10 @@ weigh_tiles_kernel(const __grid_constant__ WeighParams p) {
     if (base == nullptr && tid == 0) report(p.status, LMKV_ERR_BAD_POINTER);
     if (warp == 0) {
         const Share s = find_share(p.seqs.num_req, blockIdx.x / p.kv_heads, p.splits,
-                                   [&](int32_t i) { return units_of(p.seqs, i, kBlock, p.status); });
+                                   [&](int32_t i) -> int64_t {
+                                       const int64_t n = units_of(p.seqs, i, kBlock, p.status);
+                                       return n > 0 ? n + kTileBegin : 0;
+                                   });
         if (lane == 0) share_s = s;
     }
     fence_before_sync();
