@@ -914,7 +914,9 @@ int launch_compact(const EvictParams& p, void* stream) {
 // Rows per KV head from which the tile kernel takes a batch: beyond one second
 // operand of the row kernel, whose products are then many for the keys that it
 // reads.  (Rows against tiles, us: 8 requests of 8000 keys, 8 rows 40 : 42, 16 rows 58 : 42, 64
-// rows 95 : 42; 2 of 3000, 13 : 17, 17 : 16, 25 : 17; 24 of 2000, 33 : 36, 48 : 36, 80 : 38.)
+// rows 95 : 42; 2 of 3000, 13 : 17, 17 : 16, 25 : 17; 24 of 2000, 33 : 36, 48 : 36, 80 : 38;
+// 300 of 500, 16 rows 132 : 95; only many requests of next to nothing lose: 1000 of 64 keys, 16 rows
+// 124 : 176, 64 rows 232 : 203.)
 constexpr int kTileMinRows = 9;
 
 template <class T, int D>
