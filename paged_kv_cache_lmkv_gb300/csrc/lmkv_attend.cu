@@ -373,7 +373,7 @@ attend_rows_kernel(const __grid_constant__ AttendParams p) {
 // is warp `g * kv_heads + h` of the launch: the heads' warps of the same tokens run
 // side by side and read the same pages' rows.  (128 requests of 2048 keys, 8 KV heads of
 // 128: 189 us with launch and join, 5.7 TB/s.)
-template <class T, int D, int kRing>
+template <class T, int D>
 __device__ __forceinline__ void run_stream(const AttendParams& p, int32_t worker, uint32_t ring) {
     using W = WarpRows<T, D>;
     const int lane = threadIdx.x & 31;
@@ -426,29 +426,29 @@ __device__ __forceinline__ void run_stream(const AttendParams& p, int32_t worker
         const int32_t k0 = c0 * kChunk;
         const int32_t k1 = base == nullptr ? k0 : max(k0, min(min(k0 + n * kChunk, q.len), t.limit0 + last));
         const int32_t mine = (k1 - k0 + kChunk - 1) / kChunk;
-        uint32_t there[kRing];
+        uint32_t there[kStages];
         ChunkCopy<D, true> rows(p.layer, t.table, base, t.h, k1);
         auto fill = [&](int32_t i) {
-            return rows.copy(k0 + i * kChunk, ring + (i % kRing) * (2 * W::kTileBytes), k0 + (i + 1) * kChunk, p.status);
+            return rows.copy(k0 + i * kChunk, ring + (i % kStages) * (2 * W::kTileBytes), k0 + (i + 1) * kChunk, p.status);
         };
         __syncwarp();
         rows.lookup(k0);
 #pragma unroll
-        for (int s = 0; s < kRing - 1; ++s) {
+        for (int s = 0; s < kStages - 1; ++s) {
             there[s] = s < mine ? fill(s) : 0u;
             cp_commit();
         }
         x.begin(p, t);
-        for (int32_t i0 = 0; i0 < mine; i0 += kRing) {
+        for (int32_t i0 = 0; i0 < mine; i0 += kStages) {
 #pragma unroll
-            for (int u = 0; u < kRing; ++u) {
+            for (int u = 0; u < kStages; ++u) {
                 const int32_t i = i0 + u;
                 if (i >= mine) break;
                 __syncwarp();      // the stage filled next was read by every lane
-                constexpr int kAhead = kRing - 1;
-                there[(u + kAhead) % kRing] = i + kAhead < mine ? fill(i + kAhead) : 0u;
+                constexpr int kAhead = kStages - 1;
+                there[(u + kAhead) % kStages] = i + kAhead < mine ? fill(i + kAhead) : 0u;
                 cp_commit();
-                cp_wait<kRing - 1>();
+                cp_wait<kStages - 1>();
                 __syncwarp();
                 x.chunk(ring + u * (2 * W::kTileBytes), k0 + i * kChunk, there[u], signed_scale);
             }
@@ -476,7 +476,7 @@ attend_streams_kernel(const __grid_constant__ AttendParams p) {
     pdl_launch_dependents();
     pdl_wait();
     const int warp = threadIdx.x >> 5;
-    run_stream<T, D, kStages>(p, blockIdx.x * kWarps + warp,
+    run_stream<T, D>(p, blockIdx.x * kWarps + warp,
                               smem_u32(smem) + warp * (kStages * 2 * WarpRows<T, D>::kTileBytes));
 }
 
@@ -488,7 +488,7 @@ constexpr int kTileRows = 256;        // two tiles of 128 rows share every K and
 constexpr int kTileThreads = 352;     // softmax 2 x 128, loads 64, products 1 (of 32)
 constexpr int kMaxSegs = 8;           // the prefix and every big request that 256 rows can touch
 constexpr int kMaskSlots = 8;
-constexpr int kStreamWarps = 8;       // streams of a CTA that has no tiles
+constexpr int kStreamWarps = 8;       // streams of a CTA that has no tiles (with rings of three, or 9 to 11, slower)
 
 // Keys in a row's order: the prefix, then each big request of the tile.
 struct Seg {
@@ -588,7 +588,7 @@ __device__ __noinline__ void seen_only(const AttendParams& p, const Seg* segs, i
 // Bound by the turn of the two tiles: a block of 128 keys takes 2830 cycles for 256
 // rows, of which the products are 2048 of the tensor core (and of shared memory's
 // bandwidth) and the powers 1024.  (12 prompts of 65 to 400 tokens, 64 heads of 128 behind 8192
-// keys: 557 us, 1.42 PFLOP/s.)  q and the results moved in pieces side by side, as the
+// keys: 550 us, 1.44 PFLOP/s.)  q and the results moved in pieces side by side, as the
 // weights' kernel reads q, take registers from the main loop: 598 us a call for 585.
 // Few tiles (a decode step's) do not fill the SMs for long and leave the memory
 // idle that the own pages' streams are bound by: then some of the SMs' CTAs take the
@@ -609,11 +609,10 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if ((int32_t)blockIdx.x >= p.tile_ctas) {
         pdl_wait();
-        constexpr int kRing = 3, kBytes = kRing * 2 * WarpRows<T, D>::kTileBytes;
+        constexpr int kBytes = kStages * 2 * WarpRows<T, D>::kTileBytes;
         static_assert(kStreamWarps * kBytes <= S::kSmem, "the streams' rings fit");
         if (warp < kStreamWarps)
-            run_stream<T, D, kRing>(p, ((int32_t)blockIdx.x - p.tile_ctas) * kStreamWarps + warp,
-                                    smem_u32(smem) + warp * kBytes);
+            run_stream<T, D>(p, ((int32_t)blockIdx.x - p.tile_ctas) * kStreamWarps + warp, smem_u32(smem) + warp * kBytes);
         return;
     }
     const uint32_t full = smem_u32(bars), empty = full + 8 * S::kStages, s_full = empty + 8 * S::kStages,
@@ -759,9 +758,8 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
                         if (j > 0) mbar_arrive(empty + 8 * ((2 * j - 1) % S::kStages));
                     }
                     fence_after_sync();
-                    const uint4 mask = key_mask[(b - b0) % kMaskSlots];
-                    const uint32_t words[4] = {mask.x, mask.y, mask.z, mask.w};
-                    const bool whole = __all_sync(0xFFFFFFFFu, seen >= kBlock && (mask.x & mask.y & mask.z & mask.w) == ~0u);
+                    const uint32_t* const words = reinterpret_cast<const uint32_t*>(&key_mask[(b - b0) % kMaskSlots]);
+                    const bool whole = __all_sync(0xFFFFFFFFu, seen >= kBlock && (words[0] & words[1] & words[2] & words[3]) == ~0u);
                     // scores of 32 keys, those not seen as -infinity
                     auto take = [&](uint32_t (&x)[32], int i) {
                         if (whole) return;
@@ -841,7 +839,8 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
                     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
                     T* const out = p.out.row<T>(tok, head);
                     float z = 0.f;                    // NaN once a sum is not finite
-#pragma unroll
+                    // (rolled: its addresses would take registers from the main loop, 614 : 580 us)
+#pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t y[32];
                         if (b1 > b0) {
@@ -1193,8 +1192,8 @@ Plan make_plan(const lmkv_pool_t* pool, int32_t q_heads, int32_t num_tokens, int
             // The SMs are divided by what each side would take of them: 2.3 us for 256 rows x 128
             // keys with its share of start and end, 45 GB/s of an SM for the own pages, half of
             // whose bound is there; the tiles get three eighths at least, as the bound may be
-            // far off.  (64 users behind 16384 tokens, us by SMs for the tiles: 40: 74, 57: 58,
-            // 64: 55, 72: 53, 80: 55, 96: 63; one launch after the other: 70.)
+            // far off.  (64 users behind 16384 tokens, us by SMs for the tiles: 64: 52, 72: 50, 80: 53,
+            // 88: 57; one launch after the other: 70.)
             const double tile_us = 2.3 * (double)tile_heads * (double)((prefix_len + kBlock - 1) / kBlock);
             const double own_us = (double)num_req * heads * max_kv_len * 0.5 * pool->head_dim * 4 / 45e3;
             int64_t n = (int64_t)(kSms * tile_us / (tile_us + own_us));
