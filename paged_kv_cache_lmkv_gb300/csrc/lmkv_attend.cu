@@ -54,6 +54,7 @@ struct AttendParams {
     float* part_o;
     float2* part_ml;
     float scale_log2;       // of |scale|
+    float lowest;           // least raw score that weights are relative to
     int32_t scale_sign;     // -1, 0 or 1
     int32_t prefix_len;
     int32_t q_heads, kv_heads;
@@ -488,6 +489,12 @@ constexpr int kTileRows = 256;        // two tiles of 128 rows share every K and
 constexpr int kTileThreads = 352;     // softmax 2 x 128, loads 64, products 1 (of 32)
 constexpr int kMaxSegs = 8;           // the prefix and every big request that 256 rows can touch
 constexpr int kMaskSlots = 8;
+// The main loop takes x * scale - m * scale as one product and sum, with m * scale rounded: all
+// weights of a row are off by the same power of that rounding (as is the part's m), which is harmless until it
+// leaves their range.  Rows of scores beyond this (in powers of 2), where it is 2^-8 of a power yet, are taken
+// again by differences.  No weights are relative to less than its negative, so that keys that far down come to nothing
+// beside others.
+constexpr float kFarScore = 0x1p16f;
 constexpr int kStreamWarps = 8;       // streams of a CTA that has no tiles (with rings of three, or 9 to 11, slower)
 
 // Keys in a row's order: the prefix, then each big request of the tile.
@@ -507,15 +514,15 @@ struct TileShape {
     static constexpr int kSmem = (2 + kStages) * kStageBytes;
 };
 
-// Takes a row of a part again, by one warp: its sum of e^(x - m) v over the keys that
-// it sees, times inv where the part is all there is.  For rows that a value of
+// Takes a row of a part again, by one warp: its running maximum, sum and sum of weighted v over the
+// keys that it sees.  For rows that a value of
 // another request has spoiled: the tile's product multiplies every key's row
 // of v, those a row does not see by a weight of 0, and 0 times infinity or
-// NaN is NaN.  32 keys a step, a key a lane for the weights, D / 32 elements a
-// lane for the sums.  (m is in units of raw scores, the sign of scale applied.)
+// NaN is NaN.  And for rows whose scores are far from 0 (kFarScore).  32 keys a step, a key a lane for
+// the weights, D / 32 elements a lane for the sums.
 template <class T, int D>
 __device__ __noinline__ void seen_only(const AttendParams& p, const Seg* segs, int32_t nseg, int32_t num_blocks,
-                                       const uint8_t* base, int32_t h, int32_t part, int32_t tile_row, float m, float inv) {
+                                       const uint8_t* base, int32_t h, int32_t part, int32_t tile_row) {
     const int32_t group = (int32_t)p.by_group.d;
     const int32_t tok = (int32_t)p.by_group.div((uint32_t)tile_row), head = h * group + (tile_row - tok * group);
     const int32_t b0 = (int32_t)((int64_t)num_blocks * part / p.prefix_parts);
@@ -526,8 +533,8 @@ __device__ __noinline__ void seen_only(const AttendParams& p, const Seg* segs, i
     const T* const q = p.q.row<T>(tok, head);
     const uint8_t* const k_rows = base + (int64_t)h * (D * 2);
     const uint8_t* const v_rows = k_rows + p.layer.half_bytes();
-    const float mu = m == -INFINITY ? 0.f : m * p.scale_log2;
-    float acc[kPer] = {};
+    const float scale = p.scale_log2 * (float)p.scale_sign;
+    float m = -INFINITY, l = 0.f, acc[kPer] = {};
     for (int32_t si = 0; si < nseg; ++si) {
         const Seg& sg = segs[si];
         if (sg.n >= 0 && (tok < sg.q0 || tok >= sg.q0 + sg.n)) continue;
@@ -536,9 +543,9 @@ __device__ __noinline__ void seen_only(const AttendParams& p, const Seg* segs, i
         if (sg.n >= 0) end = min(end, (int64_t)sg.limit0 + (tok - sg.q0));
         for (int64_t k0 = (int64_t)max(b0 - sg.first, 0) * kBlock; k0 < end; k0 += 32) {
             const int64_t at = k0 + lane < end ? p.layer.token_offset(sg.table, (int32_t)k0 + lane) : -1;
-            float w = 0.f;
+            float x = -INFINITY;
             if (at >= 0) {
-                float x = 0.f;
+                x = 0.f;
 #pragma unroll 4
                 for (int c = 0; c < D / 8; ++c) {
                     const int4 k = *reinterpret_cast<const int4*>(k_rows + at + c * 16);
@@ -546,9 +553,17 @@ __device__ __noinline__ void seen_only(const AttendParams& p, const Seg* segs, i
 #pragma unroll
                     for (int i = 0; i < 8; ++i) x = fmaf(Elem<T>::to_float(q[c * 8 + i]), Elem<T>::to_float(e[i]), x);
                 }
-                x = p.scale_sign == 0 ? 0.f : p.scale_sign < 0 ? -x : x;
-                w = exp2_fast(fmaf(x, p.scale_log2, -mu));
+                x *= scale;
             }
+            float top = x;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+            const float mn = fmaxf(m, top), mu = mn == -INFINITY ? 0.f : mn;
+            const float f = exp2_fast(m - mu), w = exp2_fast(x - mu);
+            m = mn;
+            l = l * f + w;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) acc[i] *= f;
             for (int j = 0; j < 32; ++j) {
                 const int64_t from = __shfl_sync(0xFFFFFFFFu, at, j);
                 const float wj = __shfl_sync(0xFFFFFFFFu, w, j);
@@ -559,12 +574,21 @@ __device__ __noinline__ void seen_only(const AttendParams& p, const Seg* segs, i
             }
         }
     }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+    const int64_t row = (int64_t)tok * p.q_heads + head, at = (int64_t)part * p.rows + row;
+    const bool final = own && p.prefix_parts == 1;
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
     T* const out = p.out.row<T>(tok, head) + lane * kPer;
-    float* const sum = p.part_o + ((int64_t)part * p.rows + (int64_t)tok * p.q_heads + head) * D + lane * kPer;
+    float* const sum = p.part_o + at * D + lane * kPer;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        if (own && p.prefix_parts == 1) out[i] = Elem<T>::from_float(acc[i] * inv);
+        if (final) out[i] = Elem<T>::from_float(acc[i] * inv);
         else sum[i] = acc[i];
+    }
+    if (lane == 0) {
+        if (!final) p.part_ml[at] = make_float2(m, l);
+        else if (p.lse != nullptr) p.lse[row] = ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
     }
 }
 
@@ -788,7 +812,7 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
                     // weights are relative to m; m moves when it would be exceeded by more than 2^8
                     const bool grow = mx > m && !((mx - m) * scale <= 8.f);
                     if (__any_sync(0xFFFFFFFFu, grow)) {
-                        const float mn = grow ? mx : m;
+                        const float mn = grow ? fmaxf(mx, p.lowest) : m;
                         const float f = grow && m != -INFINITY ? exp2_fast((m - mn) * scale) : grow ? 0.f : 1.f;
                         m = mn;
                         l2.x *= f;
@@ -884,12 +908,13 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
                     if (wanted && final && p.lse != nullptr)
                         p.lse[row] = ((m == -INFINITY ? 0.f : m2) + log2f(l)) * kLn2;
                     if (wanted && !final) p.part_ml[at] = make_float2(m2, l);
-                    // keys of other requests, and a sum that is not finite: this row is taken again below
+                    // rows to take again: spoiled ones (keys of other requests, and a sum that is not finite), and those
+                    // whose scores are far from 0
                     const bool others = nseg > (p.prefix_len > 0 ? 1 : 0) + (own >= 0 ? 1 : 0);
-                    const uint32_t again = __ballot_sync(0xFFFFFFFFu, wanted && others && z != 0.f && l < INFINITY);
+                    const bool spoilt = others && z != 0.f && l < INFINITY;
+                    const bool far = m != -INFINITY && (m <= p.lowest || m2 > kFarScore);
+                    const uint32_t again = __ballot_sync(0xFFFFFFFFu, wanted && (spoilt || far));
                     if (lane == 0) spoiled[warp] = again;
-                    // (q has been read for the last time)
-                    if ((again >> lane) & 1) reinterpret_cast<float2*>(smem + t * S::kStageBytes)[tid & 127] = make_float2(m, inv);
                 }
             }
         } else if (warp < 8 + kLoadWarps) {
@@ -1000,11 +1025,8 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
     if (tid == 0 && gave_up) report(p.status, LMKV_ERR_TIMEOUT);
     if (warp == 10) tmem_free<512>(tmem);
     if (warp < 8) {
-        for (uint32_t left = spoiled[warp]; left != 0; left &= left - 1) {
-            const int at = warp * 32 + __ffs(left) - 1;
-            const float2 x = reinterpret_cast<const float2*>(smem + (warp >> 2) * S::kStageBytes)[at & 127];
-            seen_only<T, D>(p, segs, num_segs, num_blocks, base, h, part, row0 + at, x.x, x.y);
-        }
+        for (uint32_t left = spoiled[warp]; left != 0; left &= left - 1)
+            seen_only<T, D>(p, segs, num_segs, num_blocks, base, h, part, row0 + warp * 32 + __ffs(left) - 1);
     }
 }
 
@@ -1301,6 +1323,7 @@ int lmkv_attend_layer(const lmkv_pool_t* pool, int32_t dtype, int32_t layer, con
     p.own_range = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + x.o_bytes + x.ml_bytes);
     p.scale_sign = scale > 0.f ? 1 : scale < 0.f ? -1 : 0;
     p.scale_log2 = scale == 0.f ? 1.f : std::fabs(scale) * kLog2e;
+    p.lowest = -kFarScore / p.scale_log2;
     p.prefix_len = (int32_t)prefix_len;
     p.q_heads = num_q_heads;
     p.kv_heads = pool->num_kv_heads;

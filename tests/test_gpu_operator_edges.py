@@ -1,0 +1,76 @@
+"""The attention-side operators where bounds, roundings and values are at their edges."""
+import math
+
+import pytest
+import torch
+
+import paged_kv_cache_lmkv_gb300 as pkg
+from paged_kv_cache_lmkv_gb300 import lmkv
+from gpu_util import require_gpu
+from operator_util import DEV, HALF_STEP, TINY, Batch, within
+
+pytestmark = pytest.mark.gpu
+BF, FP, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(autouse=True)
+def gpu():
+    require_gpu()
+
+
+def attend(b, max_new=None, max_kv=None, ws=None):
+    """One call with every row of out and lse at 7 before it: (out, lse)."""
+    max_new = max(b.new + [0]) if max_new is None else max_new
+    max_kv = max(b.kv + [0]) if max_kv is None else max_kv
+    if ws is None:
+        n = pkg.attend_workspace_bytes(b.pool, b.heads, b.tokens, len(b.new), max_new, b.prefix, max_kv)
+        ws = torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV)
+    out = torch.full(b.q.shape, 7.0, dtype=b.dtype, device=DEV)
+    lse = torch.full((b.tokens, b.heads), 7.0, device=DEV)
+    pkg.check(pkg.attend_layer(b.pool, b.layer, b.q, out, b.q_start_d, b.kv_len_d, b.table_d, b.scale, ws,
+                               prefix_table=b.prefix_table_d, prefix_len=b.prefix, lse=lse, max_new=max_new,
+                               max_kv_len=max_kv, status=b.status))
+    return out, lse
+
+
+# ---- scores far from zero -------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("new,kv,prefix", [([1, 2], [60, 900], 30), ([1, 70], [60, 90], 300)])
+def test_attend_keys_near_the_lowest_value(dtype, new, kv, prefix):
+    """Keys whose products are as low as fp32 has room for weigh nothing beside others; a row that sees only
+    such keys, all alike, takes the mean of their values."""
+    b = Batch(new, kv, 4, 2, 64, dtype, prefix=prefix)
+    b.q_cpu.copy_(b.q_cpu.abs() + 1)
+    b.q.copy_(b.q_cpu)
+    assert float(b.q_cpu.max()) < 16
+    # 64 products with |q| < 16 stay below the largest fp32 number
+    low = torch.tensor(torch.finfo(dtype).min / (4096 if dtype == BF else 1)).to(dtype)
+    for x in (b.pool_cpu[1], b.pool.layers[1]):
+        k = x.view(2, -1, 128)[0]
+        k[b.prefix_slots()] = low.to(x.device)      # the prefix, every other key of the first request,
+        k[b.slots(0)[::2]] = low.to(x.device)
+        k[b.slots(1)] = low.to(x.device)            # and all keys of the second
+    out, lse = attend(b)
+    torch.cuda.synchronize()
+    assert b.status.item() == 0
+    step, lo = HALF_STEP[dtype], int(b.q_start[1])
+    # the other requests' rows see equal scores, which make every weight exactly 1
+    vis = torch.cat((torch.ones((new[1], prefix), dtype=torch.bool), b.visible(1)), 1).double()
+    for h in range(2):
+        k, v = b.rows64(b.slots(0)[1::2], h, 0), b.rows64(b.slots(0)[1::2], h, 1)
+        v1 = torch.cat((b.rows64(b.prefix_slots(), h, 1), b.rows64(b.slots(1), h, 1)))
+        count = vis.sum(1, keepdim=True)
+        mean, size = vis @ v1 / count, vis @ v1.abs() / count
+        for a in (2 * h, 2 * h + 1):
+            q = b.q_cpu[0, a].double()
+            x = k @ q * b.scale
+            p = torch.softmax(x, 0)
+            # as Batch.attend counts: 64 products a score, the sum of 30 weights, each weight's half step
+            dx = 72 * 2.0 ** -23 * float((k.abs() @ q.abs()).max()) * b.scale
+            tol = (1.01 * step + 2 * dx + 46 * 2.0 ** -23 + 2.0 ** -21) * (p @ v.abs()) + 1.01 * step * (p @ v).abs() + \
+                (30 * 2.0 ** -25 * float(v.abs().max()) if dtype == FP else 0.0)
+            within(out[0, a], p @ v, tol, "others beside them")
+            want = torch.logsumexp(x, 0)
+            within(lse[0, a], want, dx + 46 * 2.0 ** -23 + 2.0 ** -21 * (1 + want.abs()), "their lse")
+            within(out[lo:, a], mean, 1.01 * step * mean.abs() + (count + 16) * 2.0 ** -23 * size + TINY[dtype], "mean")
