@@ -54,7 +54,7 @@ struct AttendParams {
     float* part_o;
     float2* part_ml;
     float scale_log2;       // of |scale|
-    float lowest;           // least raw score that weights are relative to
+    float lowest;           // least raw score that a tile's weights are relative to (kFarScore)
     int32_t scale_sign;     // -1, 0 or 1
     int32_t prefix_len;
     int32_t q_heads, kv_heads;
@@ -68,6 +68,8 @@ struct AttendParams {
     int32_t tile_rows;      // rows of a tile that there may be
     int32_t streams;        // warps that share the own tokens for a KV head; 0: a CTA per row tile
     int2* own_range;        // [request][row tile]: first and last stream that has some of it
+    uint32_t* again;        // [tile kernel's CTA][8]: its rows to take again (where a request may be big)
+    int32_t again_cta;      // first CTA of the row kernel that does so
     bool big;               // a request may have kBigRows rows
     bool own_final;         // the own part is all of a small request: no join
     bool q_pairs;           // q rows are 4-byte aligned
@@ -80,6 +82,7 @@ struct AttendParams {
     }
 };
 
+constexpr int kTileRows = 256;    // of the tile kernel: two tiles of 128 rows share every K and V block
 constexpr int kRowTile = 16;      // rows of a tile: one mma.sync operand
 constexpr int kWarps = 4;
 constexpr int kChunk = 16;        // keys a warp takes at a time
@@ -253,6 +256,187 @@ struct WarpRows {
     }
 };
 
+// Joins the results of a CTA's warps for the same rows (the first nrows of them) in shared
+// memory; put(row, first of four elements, m, l, their sums) takes what comes of it.
+template <class T, int D, class Put>
+__device__ __forceinline__ void join_warps(const WarpRows<T, D>& x, uint8_t* smem, float2 (*ml)[kRowTile], int32_t nrows,
+                                           Put put) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float* const wo = reinterpret_cast<float*>(smem) + warp * kRowTile * D;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int rr = (lane >> 2) + 8 * r;
+        if ((lane & 3) == 0) ml[warp][rr] = make_float2(x.m[r], x.l[r]);
+#pragma unroll
+        for (int d = 0; d < D / 8; ++d)
+            *reinterpret_cast<float2*>(wo + rr * D + d * 8 + (lane & 3) * 2) =
+                make_float2(x.o[d][2 * r], x.o[d][2 * r + 1]);
+    }
+    __syncthreads();
+    const float* const all = reinterpret_cast<const float*>(smem);
+    for (int i = threadIdx.x; i < kRowTile * (D / 4); i += kWarps * 32) {
+        const int rr = i / (D / 4), c = (i % (D / 4)) * 4;
+        if (rr >= nrows) break;
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w][rr].x);
+        const float mu = top == -INFINITY ? 0.f : top;
+        float sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = exp2_fast(ml[w][rr].x - mu);
+            const float4 y = *reinterpret_cast<const float4*>(all + (w * kRowTile + rr) * D + c);
+            sum += f * ml[w][rr].y;
+            acc.x += f * y.x;
+            acc.y += f * y.y;
+            acc.z += f * y.z;
+            acc.w += f * y.w;
+        }
+        put(rr, c, top, sum, acc);
+    }
+}
+
+// Four elements of a row whose sums are complete, and its lse.
+template <class T>
+__device__ __forceinline__ void put_final(const AttendParams& p, int32_t tok, int32_t head, int c, float top, float sum,
+                                          float4 acc) {
+    const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+    T* dst = p.out.row<T>(tok, head) + c;
+    dst[0] = Elem<T>::from_float(acc.x * inv);
+    dst[1] = Elem<T>::from_float(acc.y * inv);
+    dst[2] = Elem<T>::from_float(acc.z * inv);
+    dst[3] = Elem<T>::from_float(acc.w * inv);
+    if (c == 0 && p.lse != nullptr)
+        p.lse[(int64_t)tok * p.q_heads + head] = ((top == -INFINITY ? 0.f : top) + log2f(sum)) * kLn2;
+}
+
+// Takes rows of the tile kernel again, where a request may be big.  Most are rows that a value
+// of another request has spoiled: the tile's product multiplies every key's row of v, those a row
+// does not see by a weight of 0, and 0 times infinity or NaN is NaN.  Others have scores far from 0 (kFarScore).
+// The last CTAs of the row or stream kernel, which follow the tile kernel, share the windows of 16 rows
+// that hold some; one goes over the prefix and the own keys of one request
+// at a time, as the row kernel takes its rows.  What comes of the request's rows is the
+// whole result of a big one and the prefix's of others, and stands for all parts.  Without
+// any, which is the rule, 16 bits a window are looked at: 1 us.  (Requests of 70, 70, 70 and
+// 30 tokens behind 12000 keys, 16 heads of 128, one with a NaN: 0.29 ms, without it 0.054; a row a warp
+// took 7.8.)
+template <class T, int D>
+__device__ __forceinline__ void take_again(const AttendParams& p, int32_t cta, int32_t ctas, uint8_t* smem,
+                                           float2 (*ml)[kRowTile]) {
+    using W = WarpRows<T, D>;
+    __shared__ uint32_t found[kWarps][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t group = (int32_t)p.by_group.d;
+    const int32_t live_rows = min(max(p.seqs.q_start[p.seqs.num_req], 0), p.seqs.num_tokens) * group;
+    constexpr int kWindows = kTileRows / kRowTile;      // of a tile
+    const int32_t windows = p.tiles * kWindows * p.kv_heads;
+    const uint32_t ring = smem_u32(smem) + warp * (kStages * 2 * W::kTileBytes);
+    const float signed_scale = p.scale_log2 * (float)p.scale_sign;
+    const uint8_t* const base = p.layer.base();
+    // every thread looks at one of the CTA's windows, that many at a time
+    for (int32_t w0 = cta; w0 < windows; w0 += kWarps * 32 * ctas) {
+        const int32_t mine = w0 + (int32_t)threadIdx.x * ctas;
+        uint32_t bits = 0;
+        if (mine < windows) {
+            const int32_t tile = mine / kWindows % p.tiles, h = mine / kWindows / p.tiles, win = mine % kWindows;
+            for (int32_t part = 0; part < p.prefix_parts; ++part)
+                bits |= p.again[(((int64_t)part * p.kv_heads + h) * p.tiles + tile) * 8 + (win >> 1)];
+            bits = (bits >> ((win & 1) * kRowTile)) & 0xFFFFu;
+        }
+        if (!__syncthreads_or(bits != 0)) continue;
+        found[warp][lane] = bits;
+        __syncthreads();
+#pragma unroll 1
+        for (int32_t f = 0; f < kWarps * 32; ++f) {
+            uint32_t left = found[f >> 5][f & 31];      // the same for all threads
+            if (left == 0) continue;
+            const int32_t at = w0 + f * ctas;
+            Tile t;
+            t.h = at / kWindows / p.tiles;
+            t.t0 = 0;
+            t.row0 = at / kWindows % p.tiles * kTileRows + at % kWindows * kRowTile;
+            t.nrows = live_rows - t.row0;
+            t.limit0 = t.causal = 0;                    // (limits below)
+            while (left != 0) {
+                // the request of the first row left, and its rows of the window
+                const int32_t tok0 = (int32_t)p.by_group.div((uint32_t)(t.row0 + __ffs(left) - 1));
+                const Req q = load_req(p.seqs, find_request(p.seqs.num_req, tok0, [&](int32_t i) { return p.seqs.q_start[i]; }));
+                const bool big = q.n * group >= kBigRows;
+                uint32_t now = 0;
+                for (int r = 0; r < kRowTile; ++r) {
+                    const int32_t tok = (int32_t)p.by_group.div((uint32_t)(t.row0 + r));
+                    if (((left >> r) & 1) && tok >= q.q0 && tok < q.q0 + q.n) now |= 1u << r;
+                }
+                left &= ~(now | (left & -left));        // (a row of no request is left as it is)
+                if (now == 0) continue;
+                W x;
+                x.begin(p, t);
+#pragma unroll 1
+                for (int own = 0; own < (big ? 2 : 1); ++own) {
+                    // (rows of other requests come to nothing that is kept)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int32_t rr = min((lane >> 2) + 8 * i, t.nrows - 1);
+                        const int32_t tok = (int32_t)p.by_group.div((uint32_t)(t.row0 + rr));
+                        x.limit[i] = own ? q.len - q.n + 1 + (tok - q.q0) : p.prefix_len;
+                    }
+                    const int32_t end = base == nullptr ? 0 : own ? q.len : p.prefix_len;
+                    const int32_t chunks = (end + kChunk - 1) / kChunk;
+                    const int32_t mine = chunks > warp ? (chunks - warp + kWarps - 1) / kWarps : 0;
+                    uint32_t there[kStages];
+                    ChunkCopy<D, true> rows(p.layer, own ? p.seqs.table + (int64_t)q.r * p.seqs.table_stride : p.prefix_table,
+                                            base, t.h, end);
+                    auto key_of = [&](int32_t i) { return (i * kWarps + warp) * kChunk; };
+                    auto fill = [&](int32_t i) {        // (what is not there has been reported)
+                        return rows.copy(key_of(i), ring + (i % kStages) * (2 * W::kTileBytes), key_of(i + 1), nullptr);
+                    };
+                    __syncwarp();
+                    rows.lookup(key_of(0));
+#pragma unroll
+                    for (int s = 0; s < kStages - 1; ++s) {
+                        there[s] = s < mine ? fill(s) : 0u;
+                        cp_commit();
+                    }
+                    for (int32_t i0 = 0; i0 < mine; i0 += kStages) {
+#pragma unroll
+                        for (int u = 0; u < kStages; ++u) {
+                            const int32_t i = i0 + u;
+                            if (i >= mine) break;
+                            __syncwarp();      // the stage filled next was read by every lane
+                            constexpr int kAhead = kStages - 1;
+                            there[(u + kAhead) % kStages] = i + kAhead < mine ? fill(i + kAhead) : 0u;
+                            cp_commit();
+                            cp_wait<kStages - 1>();
+                            __syncwarp();
+                            x.chunk(ring + u * (2 * W::kTileBytes), key_of(i), there[u], signed_scale);
+                        }
+                    }
+                    cp_wait<0>();
+                }
+                __syncthreads();
+                x.end();
+                join_warps<T, D>(x, smem, ml, kRowTile, [&](int rr, int c, float top, float sum, float4 acc) {
+                    if (((now >> rr) & 1) == 0) return;
+                    const int32_t tok = (int32_t)p.by_group.div((uint32_t)(t.row0 + rr));
+                    const int32_t head = t.h * group + (t.row0 + rr - tok * group);
+                    if (big && p.prefix_parts == 1) {
+                        put_final<T>(p, tok, head, c, top, sum, acc);
+                        return;
+                    }
+                    for (int32_t part = 0; part < p.prefix_parts; ++part) {
+                        const int64_t row = (int64_t)part * p.rows + (int64_t)tok * p.q_heads + head;
+                        *reinterpret_cast<float4*>(p.part_o + row * D + c) = part == 0 ? acc : make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (c == 0) p.part_ml[row] = part == 0 ? make_float2(top, sum) : make_float2(-INFINITY, 0.f);
+                    }
+                });
+                __syncthreads();
+            }
+        }
+        __syncthreads();
+    }
+}
+
 // Small batches and short contexts: a CTA per row tile (and part of the
 // prefix).  Bound by the bytes of K and V: with a few rows per KV head the
 // products are a fraction of the loads' time, so the four warps of a CTA share
@@ -261,7 +445,8 @@ struct WarpRows {
 // its own running maximum, sum and output; they are joined in shared memory at
 // the end.  (4 requests of up to 90 keys behind 512, 2 KV heads of 64: 6.3 us, all of it
 // latency: a launch, three dependent look-ups, one round of rows.)
-template <class T, int D>
+// kBig: a request may be big, and the CTAs from again_cta on take_again.
+template <class T, int D, bool kBig>
 __global__ void __launch_bounds__(kWarps * 32)
 attend_rows_kernel(const __grid_constant__ AttendParams p) {
     using W = WarpRows<T, D>;
@@ -269,7 +454,11 @@ attend_rows_kernel(const __grid_constant__ AttendParams p) {
     __shared__ float2 ml[kWarps][kRowTile];
     pdl_launch_dependents();
     pdl_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (kBig && (int32_t)blockIdx.x >= p.again_cta) {
+        take_again<T, D>(p, blockIdx.x - p.again_cta, gridDim.x - p.again_cta, smem, ml);
+        return;
+    }
+    const int warp = threadIdx.x >> 5;
     Tile t;
     if (!find_tile(p, blockIdx.x, t)) return;
     const uint8_t* base = p.layer.base();
@@ -314,57 +503,19 @@ attend_rows_kernel(const __grid_constant__ AttendParams p) {
     cp_wait<0>();
     __syncthreads();
 
-    // join the warps in shared memory
     x.end();
-    float* const wo = reinterpret_cast<float*>(smem) + warp * kRowTile * D;
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int rr = (lane >> 2) + 8 * r;
-        if ((lane & 3) == 0) ml[warp][rr] = make_float2(x.m[r], x.l[r]);
-#pragma unroll
-        for (int d = 0; d < D / 8; ++d)
-            *reinterpret_cast<float2*>(wo + rr * D + d * 8 + (lane & 3) * 2) =
-                make_float2(x.o[d][2 * r], x.o[d][2 * r + 1]);
-    }
-    __syncthreads();
-    const float* const all = reinterpret_cast<const float*>(smem);
-    for (int i = threadIdx.x; i < kRowTile * (D / 4); i += kWarps * 32) {
-        const int rr = i / (D / 4), c = (i % (D / 4)) * 4;
-        if (rr >= t.nrows) break;
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w][rr].x);
-        const float mu = top == -INFINITY ? 0.f : top;
-        float sum = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = exp2_fast(ml[w][rr].x - mu);
-            const float4 y = *reinterpret_cast<const float4*>(all + (w * kRowTile + rr) * D + c);
-            sum += f * ml[w][rr].y;
-            acc.x += f * y.x;
-            acc.y += f * y.y;
-            acc.z += f * y.z;
-            acc.w += f * y.w;
-        }
+    join_warps<T, D>(x, smem, ml, t.nrows, [&](int rr, int c, float top, float sum, float4 acc) {
         const int32_t n = (int32_t)p.by_group.div((uint32_t)(t.row0 + rr));
         const int32_t tok = t.t0 + n, head = t.h * group + (t.row0 + rr - n * group);
-        const int32_t row = tok * p.q_heads + head;
         if (t.r >= 0 && p.own_final) {
-            const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-            T* dst = p.out.row<T>(tok, head) + c;
-            dst[0] = Elem<T>::from_float(acc.x * inv);
-            dst[1] = Elem<T>::from_float(acc.y * inv);
-            dst[2] = Elem<T>::from_float(acc.z * inv);
-            dst[3] = Elem<T>::from_float(acc.w * inv);
-            if (c == 0 && p.lse != nullptr) p.lse[row] = (mu + log2f(sum)) * kLn2;
+            put_final<T>(p, tok, head, c, top, sum, acc);
         } else {
-            const int64_t at = t.r < 0 ? (int64_t)t.part * p.rows + row
+            const int64_t at = t.r < 0 ? (int64_t)t.part * p.rows + tok * p.q_heads + head
                                        : p.own_part(0, t.r * p.own_tiles + t.row0 / kRowTile, rr, t.h);
             *reinterpret_cast<float4*>(p.part_o + at * D + c) = acc;
             if (c == 0) p.part_ml[at] = make_float2(top, sum);
         }
-    }
+    });
 }
 
 // Longer own contexts: streams.  The chunks of all small requests' row tiles,
@@ -470,12 +621,19 @@ __device__ __forceinline__ void run_stream(const AttendParams& p, int32_t worker
     }
 }
 
-template <class T, int D>
+template <class T, int D, bool kBig>
 __global__ void __launch_bounds__(kWarps * 32, kRowCtas)
 attend_streams_kernel(const __grid_constant__ AttendParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     pdl_launch_dependents();
     pdl_wait();
+    if constexpr (kBig) {
+        __shared__ float2 ml[kWarps][kRowTile];
+        if ((int32_t)blockIdx.x >= p.again_cta) {
+            take_again<T, D>(p, blockIdx.x - p.again_cta, gridDim.x - p.again_cta, smem, ml);
+            return;
+        }
+    }
     const int warp = threadIdx.x >> 5;
     run_stream<T, D>(p, blockIdx.x * kWarps + warp,
                               smem_u32(smem) + warp * (kStages * 2 * WarpRows<T, D>::kTileBytes));
@@ -485,7 +643,6 @@ attend_streams_kernel(const __grid_constant__ AttendParams p) {
 
 using namespace lmkv_tc;
 
-constexpr int kTileRows = 256;        // two tiles of 128 rows share every K and V block
 constexpr int kTileThreads = 352;     // softmax 2 x 128, loads 64, products 1 (of 32)
 constexpr int kMaxSegs = 8;           // the prefix and every big request that 256 rows can touch
 constexpr int kMaskSlots = 8;
@@ -514,20 +671,22 @@ struct TileShape {
     static constexpr int kSmem = (2 + kStages) * kStageBytes;
 };
 
-// Takes a row of a part again, by one warp: its running maximum, sum and sum of weighted v over the
-// keys that it sees.  For rows that a value of
-// another request has spoiled: the tile's product multiplies every key's row
-// of v, those a row does not see by a weight of 0, and 0 times infinity or
-// NaN is NaN.  And for rows whose scores are far from 0 (kFarScore).  32 keys a step, a key a lane for
-// the weights, D / 32 elements a lane for the sums.
+// Takes a row of a part again, by one warp, or leaves it to take_again where a request may
+// be big.  Only rows whose scores are far from 0 (kFarScore) need it where none is.  32 keys a step, a key
+// a lane for the weights, D / 32 elements a lane for the sums.  (As a function of its own, and
+// over the tile's segments, it leaves the main loop its registers: with the prefix alone
+// as its keys 635 us for 586.)
 template <class T, int D>
-__device__ __noinline__ void seen_only(const AttendParams& p, const Seg* segs, int32_t nseg, int32_t num_blocks,
+__device__ __noinline__ void take_row(const AttendParams& p, const Seg* segs, int32_t nseg, int32_t num_blocks,
                                        const uint8_t* base, int32_t h, int32_t part, int32_t tile_row) {
+    if (p.big) {
+        if ((threadIdx.x & 31) == 0) p.again[(int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)] |= 1u << (tile_row & 31);
+        return;
+    }
     const int32_t group = (int32_t)p.by_group.d;
     const int32_t tok = (int32_t)p.by_group.div((uint32_t)tile_row), head = h * group + (tile_row - tok * group);
     const int32_t b0 = (int32_t)((int64_t)num_blocks * part / p.prefix_parts);
     const int32_t b1 = (int32_t)((int64_t)num_blocks * (part + 1) / p.prefix_parts);
-    bool own = false;
     constexpr int kPer = D / 32;
     const int lane = threadIdx.x & 31;
     const T* const q = p.q.row<T>(tok, head);
@@ -538,7 +697,6 @@ __device__ __noinline__ void seen_only(const AttendParams& p, const Seg* segs, i
     for (int32_t si = 0; si < nseg; ++si) {
         const Seg& sg = segs[si];
         if (sg.n >= 0 && (tok < sg.q0 || tok >= sg.q0 + sg.n)) continue;
-        own = own || sg.n >= 0;
         int64_t end = min((int64_t)sg.end, (int64_t)(b1 - sg.first) * kBlock);
         if (sg.n >= 0) end = min(end, (int64_t)sg.limit0 + (tok - sg.q0));
         for (int64_t k0 = (int64_t)max(b0 - sg.first, 0) * kBlock; k0 < end; k0 += 32) {
@@ -577,19 +735,10 @@ __device__ __noinline__ void seen_only(const AttendParams& p, const Seg* segs, i
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
     const int64_t row = (int64_t)tok * p.q_heads + head, at = (int64_t)part * p.rows + row;
-    const bool final = own && p.prefix_parts == 1;
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-    T* const out = p.out.row<T>(tok, head) + lane * kPer;
     float* const sum = p.part_o + at * D + lane * kPer;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        if (final) out[i] = Elem<T>::from_float(acc[i] * inv);
-        else sum[i] = acc[i];
-    }
-    if (lane == 0) {
-        if (!final) p.part_ml[at] = make_float2(m, l);
-        else if (p.lse != nullptr) p.lse[row] = ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
-    }
+    for (int i = 0; i < kPer; ++i) sum[i] = acc[i];
+    if (lane == 0) p.part_ml[at] = make_float2(m, l);
 }
 
 // Rows of all requests, (token, head of the group) in token order, 256 to a
@@ -668,6 +817,7 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
     const int32_t row0 = tile * kTileRows;
     const int32_t live_rows = live_tokens * group;
     uint8_t* const base = p.layer.base();
+    if (p.big && tid < 8) p.again[(int64_t)blockIdx.x * 8 + tid] = 0;
     if (warp == 0 && row0 < live_rows) {
         const int32_t t_first = (int32_t)p.by_group.div((uint32_t)row0);
         const int32_t t_last = (int32_t)p.by_group.div((uint32_t)(min(row0 + kTileRows, live_rows) - 1));
@@ -1026,7 +1176,7 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
     if (warp == 10) tmem_free<512>(tmem);
     if (warp < 8) {
         for (uint32_t left = spoiled[warp]; left != 0; left &= left - 1)
-            seen_only<T, D>(p, segs, num_segs, num_blocks, base, h, part, row0 + warp * 32 + __ffs(left) - 1);
+            take_row<T, D>(p, segs, num_segs, num_blocks, base, h, part, row0 + warp * 32 + __ffs(left) - 1);
     }
 }
 
@@ -1136,7 +1286,7 @@ struct Plan {
     bool own, big, own_final, join;
     int32_t stream_ctas;      // of the tile kernel; 0: the streams have their own launch
     int64_t rows;
-    uint64_t o_bytes, ml_bytes, bytes;
+    uint64_t o_bytes, ml_bytes, range_bytes, bytes;
 };
 
 constexpr int32_t kSms = 152;
@@ -1236,7 +1386,9 @@ Plan make_plan(const lmkv_pool_t* pool, int32_t q_heads, int32_t num_tokens, int
     const uint64_t parts = x.join ? (uint64_t)x.prefix_parts * x.rows + own_rows : 0;
     x.o_bytes = parts * pool->head_dim * 4;
     x.ml_bytes = parts * 8;
-    x.bytes = x.o_bytes + x.ml_bytes + (x.join ? (uint64_t)num_req * x.own_tiles * 8 : 0);
+    x.range_bytes = x.join ? (uint64_t)num_req * x.own_tiles * 8 : 0;
+    x.bytes = x.o_bytes + x.ml_bytes + x.range_bytes +
+              (x.big ? (uint64_t)x.tiles * pool->num_kv_heads * x.prefix_parts * 32 : 0);
     return x;
 }
 
@@ -1247,29 +1399,43 @@ int check_shape(const lmkv_pool_t* pool) {
     return LMKV_OK;
 }
 
-template <class T, int D>
-int attend_typed(AttendParams& p, const Plan& x, void* stream) {
+template <class T, int D, bool kBig>
+int attend_launches(AttendParams& p, const Plan& x, void* stream) {
     constexpr int smem = kWarps * kStages * 2 * kChunk * D * 2;
-    int rc = allow_smem<attend_rows_kernel<T, D>, smem>();
-    if (rc == LMKV_OK) rc = allow_smem<attend_streams_kernel<T, D>, smem>();
+    int rc = allow_smem<attend_rows_kernel<T, D, kBig>, smem>();
+    if (rc == LMKV_OK) rc = allow_smem<attend_streams_kernel<T, D, kBig>, smem>();
     if (rc == LMKV_OK) rc = allow_smem<attend_tiles_kernel<T, D>, TileShape<D>::kSmem>();
     if (rc == LMKV_OK)
         rc = launch(attend_tiles_kernel<T, D>, (int64_t)x.tiles * p.kv_heads * x.prefix_parts + x.stream_ctas, kTileThreads,
                     TileShape<D>::kSmem, stream, 1, p);
     if (rc != LMKV_OK) return rc;
-    const int64_t ctas = ((int64_t)x.row_tiles * x.prefix_parts +
-                          (x.own && x.streams == 0 ? (int64_t)x.own_tiles * p.seqs.num_req : 0)) * p.kv_heads;
-    rc = launch(attend_rows_kernel<T, D>, ctas, kWarps * 32, smem, stream, 1, p);
-    if (rc != LMKV_OK) return rc;
-    if (x.streams > 0 && x.stream_ctas == 0)
-        rc = launch(attend_streams_kernel<T, D>, ((int64_t)x.streams * p.kv_heads + kWarps - 1) / kWarps, kWarps * 32, smem,
+    // the own pages, and the prefix where tiles do not have it; beside them the rows to take again
+    const int64_t windows = kBig ? (int64_t)x.tiles * (kTileRows / kRowTile) * p.kv_heads : 0, most = kRowCtas * kSms;
+    const int64_t again = windows < most ? windows : most;
+    if (x.streams == 0 || x.stream_ctas > 0) {
+        const int64_t ctas = ((int64_t)x.row_tiles * x.prefix_parts +
+                              (x.own && x.streams == 0 ? (int64_t)x.own_tiles * p.seqs.num_req : 0)) * p.kv_heads;
+        p.again_cta = (int32_t)ctas;
+        rc = launch(attend_rows_kernel<T, D, kBig>, ctas + again, kWarps * 32, smem, stream, 1, p);
+    } else {
+        rc = launch(attend_rows_kernel<T, D, kBig>, (int64_t)x.row_tiles * x.prefix_parts * p.kv_heads, kWarps * 32, smem,
                     stream, 1, p);
+        const int64_t ctas = ((int64_t)x.streams * p.kv_heads + kWarps - 1) / kWarps;
+        p.again_cta = (int32_t)ctas;
+        if (rc == LMKV_OK)
+            rc = launch(attend_streams_kernel<T, D, kBig>, ctas + again, kWarps * 32, smem, stream, 1, p);
+    }
     if (rc != LMKV_OK || !x.join) return rc;
     // the small requests' rows, where there are no others or those are done already
     if (!x.big || x.prefix_parts <= 1)
         return launch(attend_join_kernel<T, D, true>, ((int64_t)p.seqs.num_req * x.own_cap * p.kv_heads + 7) / 8, 256, 0,
                       stream, 1, p);
     return launch(attend_join_kernel<T, D, false>, (x.rows + 7) / 8, 256, 0, stream, 1, p);
+}
+
+template <class T, int D>
+int attend_typed(AttendParams& p, const Plan& x, void* stream) {
+    return x.big ? attend_launches<T, D, true>(p, x, stream) : attend_launches<T, D, false>(p, x, stream);
 }
 
 }  // namespace
@@ -1321,6 +1487,7 @@ int lmkv_attend_layer(const lmkv_pool_t* pool, int32_t dtype, int32_t layer, con
     p.part_o = static_cast<float*>(workspace);
     p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + x.o_bytes);
     p.own_range = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + x.o_bytes + x.ml_bytes);
+    p.again = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + x.o_bytes + x.ml_bytes + x.range_bytes);
     p.scale_sign = scale > 0.f ? 1 : scale < 0.f ? -1 : 0;
     p.scale_log2 = scale == 0.f ? 1.f : std::fabs(scale) * kLog2e;
     p.lowest = -kFarScore / p.scale_log2;

@@ -74,3 +74,59 @@ def test_attend_keys_near_the_lowest_value(dtype, new, kv, prefix):
             want = torch.logsumexp(x, 0)
             within(lse[0, a], want, dx + 46 * 2.0 ** -23 + 2.0 ** -21 * (1 + want.abs()), "their lse")
             within(out[lo:, a], mean, 1.01 * step * mean.abs() + (count + 16) * 2.0 ** -23 * size + TINY[dtype], "mean")
+
+
+# ---- values that are not finite -----------------------------------------
+
+def call_time(b):
+    """Shortest time of five calls, ms."""
+    n = pkg.attend_workspace_bytes(b.pool, b.heads, b.tokens, len(b.new), max(b.new), b.prefix, max(b.kv))
+    ws, out, times = torch.empty(n, dtype=torch.uint8, device=DEV), torch.empty_like(b.q), []
+    for _ in range(6):
+        first, last = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        first.record()
+        pkg.check(pkg.attend_layer(b.pool, 1, b.q, out, b.q_start_d, b.kv_len_d, b.table_d, b.scale, ws,
+                                   prefix_table=b.prefix_table_d, prefix_len=b.prefix, max_new=max(b.new),
+                                   max_kv_len=max(b.kv)))
+        last.record()
+        torch.cuda.synchronize()
+        times.append(first.elapsed_time(last))
+    return min(times[1:])
+
+
+def test_attend_one_bad_value_does_not_stall_the_batch():
+    """Rows that share a tile with a request whose values are not finite are taken again sixteen at a time, at
+    five times the clean call's cost here (a row a warp: 144 times)."""
+    b = Batch([70, 70, 70, 30], [200, 300, 70, 90], 16, 2, 128, BF, prefix=12000)
+    clean = call_time(b)
+    b.pool.layers[1].view(2, -1, 256)[1, b.slots(1)[0]] = math.nan
+    bad = call_time(b)
+    assert bad < 20 * clean, (clean, bad)
+
+
+@pytest.mark.parametrize("scale", [None, -0.25, 0.0])
+@pytest.mark.parametrize("dtype,dim,prefix,new,kv", [
+    (BF, 128, 3000, [34, 3, 0, 40, 90], [60, 50, 9, 400, 90]),          # parts of the prefix, small requests between
+    (FP, 64, 0, [70, 66, 1, 100], [70, 300, 5, 1200]), (BF, 64, 40, [64, 3, 65], [64, 900, 2000])])
+def test_attend_bad_values_in_parts(dtype, dim, prefix, new, kv, scale):
+    """Infinite and NaN values of one request, in its first and its last page, and a block that is not there."""
+    b = Batch(new, kv, 8, 2, dim, dtype, prefix=prefix, page=16)
+    b.scale = b.scale if scale is None else scale
+    r = len(new) - 1
+    flat = b.pool.layers[1].view(2, -1, 2 * dim)
+    flat[1, b.slots(r)[0]] = math.inf
+    flat[1, b.slots(r)[kv[r] - new[r]], dim + 3] = math.nan
+    table = b.table_d.clone()
+    table[0, 1] = -1
+    b.table_d = table
+    out, lse = attend(b)
+    torch.cuda.synchronize()
+    assert b.status.item() == lmkv.ERR_BAD_BLOCK
+
+    def hide(i, n):
+        return torch.arange(n) // 16 == 1 if i == 0 else torch.zeros(n, dtype=torch.bool)
+    want, want_l, tol, tol_l = b.attend(hide)
+    within(lse, want_l, tol_l, "lse")
+    at = int(b.q_start[r])
+    within(out[:at], want[:at], tol[:at], "the others")
+    assert not bool(out[at:, 4:].isfinite().all(-1).any()) and not bool(out[at:, :4].isfinite().any())
