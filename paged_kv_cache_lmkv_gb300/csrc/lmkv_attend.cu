@@ -1283,7 +1283,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
 struct Plan {
     int32_t row_tiles, tiles, prefix_parts, prefix_span;
     int32_t own_cap, own_tiles, tile_rows, streams;
-    bool own, big, own_final, join;
+    bool big, own_final, join;
     int32_t stream_ctas;      // of the tile kernel; 0: the streams have their own launch
     int64_t rows;
     uint64_t o_bytes, ml_bytes, range_bytes, bytes;
@@ -1349,7 +1349,6 @@ Plan make_plan(const lmkv_pool_t* pool, int32_t q_heads, int32_t num_tokens, int
     x.own_cap = (int32_t)(x.big ? kBigRows - 1 : req_rows);
     x.own_tiles = (x.own_cap + kRowTile - 1) / kRowTile;
     x.tile_rows = x.own_cap < kRowTile ? x.own_cap : kRowTile;
-    x.own = max_kv_len > 0 || prefix_len == 0;
     // A CTA per row tile while that is at most 16 chunks a warp, else streams: as many warps
     // as fit at once.  (CTAs against streams, us: 4 requests of 512 keys 15 : 19, 1024 23 : 23,
     // 2048 35 : 26; 32 requests 23 : 30, 37 : 44, 62 : 67, all of the same length, which is where
@@ -1413,8 +1412,9 @@ int attend_launches(AttendParams& p, const Plan& x, void* stream) {
     const int64_t windows = kBig ? (int64_t)x.tiles * (kTileRows / kRowTile) * p.kv_heads : 0, most = kRowCtas * kSms;
     const int64_t again = windows < most ? windows : most;
     if (x.streams == 0 || x.stream_ctas > 0) {
+        // (with no room for cached tokens too: lengths beyond that bound are reported)
         const int64_t ctas = ((int64_t)x.row_tiles * x.prefix_parts +
-                              (x.own && x.streams == 0 ? (int64_t)x.own_tiles * p.seqs.num_req : 0)) * p.kv_heads;
+                              (x.streams == 0 ? (int64_t)x.own_tiles * p.seqs.num_req : 0)) * p.kv_heads;
         p.again_cta = (int32_t)ctas;
         rc = launch(attend_rows_kernel<T, D, kBig>, ctas + again, kWarps * 32, smem, stream, 1, p);
     } else {

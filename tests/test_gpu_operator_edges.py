@@ -130,3 +130,30 @@ def test_attend_bad_values_in_parts(dtype, dim, prefix, new, kv, scale):
     at = int(b.q_start[r])
     within(out[:at], want[:at], tol[:at], "the others")
     assert not bool(out[at:, 4:].isfinite().all(-1).any()) and not bool(out[at:, :4].isfinite().any())
+
+
+# ---- bounds of no cached tokens -----------------------------------------
+
+@pytest.mark.parametrize("new,kv,prefix", [
+    ([1, 2], [40, 50], 0), ([1, 2], [40, 50], 20), ([0, 1], [40, 0], 20), ([70, 0], [0, 40], 0),
+    ([70, 0], [0, 40], 300), ([70, 0], [0, 40], 3000), ([1] * 80, [0] * 79 + [3], 20011), ([1, 1], [0, -4], 20)])
+def test_attend_bound_of_no_cached_tokens(new, kv, prefix):
+    """Cached tokens beyond a bound of 0 are reported, of requests without new tokens too, and not attended to."""
+    b = Batch(new, [max(n, 0) for n in kv], 8, 2, 64, BF, prefix=prefix)
+    b.kv_len_d = torch.tensor(kv, dtype=torch.int32, device=DEV)
+    out, lse = attend(b, max_kv=0)
+    torch.cuda.synchronize()
+    assert b.status.item() == lmkv.ERR_BAD_LENGTH
+    want, want_l, tol, tol_l = b.attend(lambda r, n: torch.full((n,), r is not None))
+    within(out, want, tol, "out")
+    within(lse, want_l, tol_l, "lse")
+
+
+def test_attend_bound_of_no_cached_tokens_kept():
+    b = Batch([1, 70, 0], [0, 0, 0], 8, 2, 64, BF, prefix=90)
+    out, lse = attend(b, max_kv=0)
+    torch.cuda.synchronize()
+    assert b.status.item() == 0
+    want, want_l, tol, tol_l = b.attend()
+    within(out, want, tol, "out")
+    within(lse, want_l, tol_l, "lse")
