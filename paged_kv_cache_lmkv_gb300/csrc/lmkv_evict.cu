@@ -99,7 +99,6 @@ weigh_rows_kernel(const __grid_constant__ WeighParams p) {
                              [&](int32_t i) { return units_of(p.seqs, i, kUnit, p.status); });
     for (; share.n > 0 && share.r < p.seqs.num_req; ++share.r, share.first = 0) {
         x.q = load_req(p.seqs, share.r);
-        if (!x.q.ok && threadIdx.x == 0) report(p.status, LMKV_ERR_BAD_LENGTH);
         const int64_t here = min((int64_t)(x.q.len + kUnit - 1) / kUnit - share.first, share.n);
         if (here <= 0) continue;
         share.n -= here;
@@ -359,7 +358,6 @@ weigh_tiles_kernel(const __grid_constant__ WeighParams p) {
         bool ok = true;
         int32_t it = 0, pass_no = 0;
         while (walk.next(base != nullptr)) {
-            if (!x.q.ok && tid == 0) report(p.status, LMKV_ERR_BAD_LENGTH);
             const int32_t keys = x.k1 - x.k0;
             if (walk.passes == 0) {                 // nothing but the decay
                 for (int32_t k = tid; k < keys; k += 512)
@@ -923,14 +921,15 @@ template <class T, int D>
 int weigh_typed(WeighParams& p, void* stream) {
     const int64_t rows = (int64_t)(p.seqs.max_new < p.seqs.num_tokens ? p.seqs.max_new : p.seqs.num_tokens) * p.by_group.d;
     // (the tile kernel carries -lse / scale, in fp16 up to 2^31: lse up to 2^19 at the smallest scale it takes)
-    const bool tiles = rows >= kTileMinRows && std::fabs(p.scale_log2) >= 0x1p-12f * kLog2e;
+    // (with no room for cached tokens a CTA of the row kernel looks at the lengths and has no shares)
+    const bool tiles = rows >= kTileMinRows && std::fabs(p.scale_log2) >= 0x1p-12f * kLog2e && p.seqs.max_kv_len > 0;
     p.lse_scale = kLog2e / p.scale_log2;
     const int64_t heads = p.kv_heads, req = p.seqs.num_req;
     // one round of CTAs
     const int64_t unit = tiles ? kBlock : kUnit;
     const int64_t want = (tiles ? 1 : kRowCtas) * 152 / heads, most = ((int64_t)p.seqs.max_kv_len + unit - 1) / unit * req;
-    p.splits = (int32_t)(want < 1 ? 1 : want > most ? most : want);
-    const int64_t grid = heads * p.splits;
+    p.splits = (int32_t)(want < 1 || most < 1 ? 1 : want > most ? most : want);
+    const int64_t grid = most < 1 ? 1 : heads * p.splits;
     if (!tiles) {
         constexpr int ring = kWarps * kStages * kChunk * D * 2;
         int rc = allow_smem<weigh_rows_kernel<T, D, true>, ring>();
@@ -960,15 +959,18 @@ int lmkv_weigh_layer(const lmkv_pool_t* pool, int32_t dtype, int32_t layer, cons
     rc = check_batch(pool, batch, num_q_heads);
     if (rc != LMKV_OK) return rc;
     if (batch->max_kv_len > INT32_MAX - 65536 || score_stride < batch->max_kv_len) return LMKV_ERR_INVALID_ARG;
-    if (batch->num_req == 0 || batch->max_kv_len == 0) return LMKV_OK;
-    if (batch->q_start == nullptr || batch->kv_len == nullptr || batch->block_table == nullptr ||
-        scores_out == nullptr || (decay != 0.f && scores == nullptr))
+    if (batch->num_req == 0) return LMKV_OK;
+    // (with no room for cached tokens only the lengths are looked at)
+    const bool room = batch->max_kv_len > 0;
+    if (!room && (batch->q_start == nullptr || batch->kv_len == nullptr)) return LMKV_OK;
+    if (batch->q_start == nullptr || batch->kv_len == nullptr || (room && batch->block_table == nullptr) ||
+        (room && (scores_out == nullptr || (decay != 0.f && scores == nullptr))))
         return LMKV_ERR_INVALID_ARG;
-    if (batch->num_tokens > 0 && (!rows_ok(q, 2) || lse == nullptr)) return LMKV_ERR_INVALID_ARG;
+    if (room && batch->num_tokens > 0 && (!rows_ok(q, 2) || lse == nullptr)) return LMKV_ERR_INVALID_ARG;
     WeighParams p = {};
     p.layer = Layer::of(pool, layer);
     p.seqs = Seqs::of(batch);
-    if (batch->num_tokens > 0) {
+    if (room && batch->num_tokens > 0) {
         p.q = static_cast<const uint8_t*>(q->data);
         p.q_token_stride = q->token_stride;
         p.q_head_stride = q->head_stride;

@@ -187,11 +187,11 @@ __device__ __forceinline__ Share find_share(int32_t num_req, int32_t part, int32
     x.n = 0;      // not reached: begin < all
     return x;
 }
-// Units of a request's cached tokens.
+// Units of a request's cached tokens; lengths of the request that had to be clamped are reported.
 __device__ __forceinline__ int64_t units_of(const Seqs& s, int32_t i, int32_t unit, int32_t* status) {
-    const int32_t len = s.kv_len[i];
-    if (len < 0 || len > s.max_kv_len) report(status, LMKV_ERR_BAD_LENGTH);
-    return (min(max(len, 0), s.max_kv_len) + unit - 1) / unit;
+    const Req q = load_req(s, i);
+    if (!q.ok) report(status, LMKV_ERR_BAD_LENGTH);
+    return (q.len + unit - 1) / unit;
 }
 
 // ---- element types ------------------------------------------------------

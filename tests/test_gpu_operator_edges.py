@@ -157,3 +157,52 @@ def test_attend_bound_of_no_cached_tokens_kept():
     want, want_l, tol, tol_l = b.attend()
     within(out, want, tol, "out")
     within(lse, want_l, tol_l, "lse")
+
+
+def weigh(b, lse, scores, out, decay=1.0, max_new=None, max_kv=None):
+    pkg.check(pkg.weigh_layer(b.pool, b.layer, b.q, lse, b.q_start_d, b.kv_len_d, b.table_d, b.scale, scores, out,
+                              decay=decay, max_new=max(b.new) if max_new is None else max_new,
+                              max_kv_len=max(b.kv) if max_kv is None else max_kv, status=b.status))
+
+
+@pytest.mark.parametrize("new", [[1, 1], [30, 1], [0, 0]])
+def test_weigh_bound_of_no_cached_tokens(new):
+    """Cached tokens beyond a bound of 0 are reported, and no score is touched."""
+    b = Batch(new, [40, 50], 8, 2, 64, BF, extra_rows=1)
+    lse, out = torch.zeros((b.tokens, 8), device=DEV), torch.full((2, 2, 50), 7.0, device=DEV)
+    weigh(b, lse, out, out, max_kv=0)
+    torch.cuda.synchronize()
+    assert b.status.item() == lmkv.ERR_BAD_LENGTH
+    assert bool((out == 7.0).all())
+    b.status.zero_()
+    b.kv_len_d.zero_()
+    weigh(b, lse, out, out, max_kv=0)
+    torch.cuda.synchronize()
+    assert b.status.item() == 0
+
+
+@pytest.mark.parametrize("max_new", [1, 20])
+def test_weigh_lengths_of_requests_without_cached_tokens(max_new):
+    """New tokens beyond their bound are reported of a request that has no cached ones too."""
+    b = Batch([1, max_new + 1], [40, 0], 8, 2, 64, BF)
+    lse, out = torch.zeros((b.tokens, 8), device=DEV), torch.full((2, 2, 40), 7.0, device=DEV)
+    weigh(b, lse, None, out, decay=0.0, max_new=max_new)
+    torch.cuda.synchronize()
+    assert b.status.item() == lmkv.ERR_BAD_LENGTH
+    assert bool((out[1] == 7.0).all())
+
+
+@pytest.mark.parametrize("new", [1, 3])
+def test_weigh_many_requests(new):
+    n = 150
+    b = Batch([new] * n, [(i * 13) % 70 for i in range(n)], 8, 2, 64, BF)
+    _, lse, _, _ = b.attend()
+    scores = torch.rand((n, 2, 75), generator=torch.Generator().manual_seed(2))
+    out = scores.to(DEV)
+    weigh(b, lse.float().to(DEV), out, out, decay=0.5)
+    torch.cuda.synchronize()
+    assert b.status.item() == 0
+    want, tol = b.weigh(lse.float(), scores, 0.5)
+    for r, m in enumerate(b.kv):
+        within(out[r, :, :m], want[r, :, :m], tol[r, :, :m], f"request {r}")
+        assert torch.equal(out[r, :, m:].cpu(), scores[r, :, m:])
