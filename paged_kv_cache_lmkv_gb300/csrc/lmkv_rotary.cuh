@@ -29,7 +29,7 @@ struct Rotary {
 int make_rotary(const lmkv_rotary_t* in, int32_t head_dim, Rotary* out);
 
 // For 16-bit rows the special function unit's sine and cosine will do: on
-// [-pi, pi] they are within 2^-21.4, a thousandth of those types' half step.
+// [-pi, pi] they are within 2^-21.1, less than a hundredth of those types' half step.
 template <class T>
 __device__ __forceinline__ float2 cos_sin(uint64_t turns, int64_t pos) {
     const uint64_t frac = turns * (uint64_t)pos;

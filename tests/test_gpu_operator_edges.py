@@ -206,3 +206,27 @@ def test_weigh_many_requests(new):
     for r, m in enumerate(b.kv):
         within(out[r, :, :m], want[r, :, :m], tol[r, :, :m], f"request {r}")
         assert torch.equal(out[r, :, m:].cpu(), scores[r, :, m:])
+
+
+# ---- rotary -------------------------------------------------------------
+
+@pytest.mark.parametrize("share", [0.25, 0.75])
+def test_append_slow_frequencies_at_far_positions(share):
+    """A frequency of (1000 + share) 2^-64 turns a position is taken to the nearest 2^-64 of a
+    turn, so at position 2^60 its angle is a whole number of sixteenths of a turn."""
+    k = 1000 + round(share)
+    f = 2 * math.pi * (1000 + share) * 2.0 ** -64
+    rotary = pkg.Rotary(64, inv_freq=[f] * 32)
+    b = Batch([1], [1], 2, 2, 64, F32)
+    x = torch.randn((1, 2, 64), generator=torch.Generator().manual_seed(3))
+    q, out = x.to(DEV), torch.empty((1, 2, 64), device=DEV)
+    pos = torch.tensor([2 ** 60], dtype=torch.int64, device=DEV)
+    pkg.check(pkg.append_layer(b.pool, 1, b.table_d, q, q, q, out, b.q_start_d, b.kv_len_d, rotary, positions=pos,
+                               status=b.status))
+    torch.cuda.synchronize()
+    assert b.status.item() == 0
+    t = 2 * math.pi * (k % 16) / 16
+    a, c = x.double()[..., :32], x.double()[..., 32:]
+    want = torch.cat((a * math.cos(t) - c * math.sin(t), a * math.sin(t) + c * math.cos(t)), -1)
+    mag = (a.abs() + c.abs()).repeat(1, 1, 2)
+    within(out, want, 2.0 ** -24 * 1.001 * want.abs() + 2.0 ** -21 * mag, "q")
