@@ -600,16 +600,23 @@ typedef enum lmkv_rotary_scaling {
     LMKV_ROTARY_BASE = 2,     /* base * factor^(rot_dim / (rot_dim - 2)) */
     LMKV_ROTARY_BANDS = 3,    /* by turns over `original` positions, n = original f / 2 pi:
                                  n <= low: f / factor; n >= high: f; linear in n between */
-    LMKV_ROTARY_RAMP = 4      /* linear in the pair's index between the (fractional) pairs
+    LMKV_ROTARY_RAMP = 4,     /* linear in the pair's index between the (fractional) pairs
                                  that make `high` and `low` turns over `original` positions:
                                  f on the fast side, f / factor on the slow side; the
-                                 magnitude is 0.1 ln(factor) + 1 ("YaRN", Peng et al., 2023) */
+                                 magnitude is 0.1 ln(factor) + 1.  No published form: YARN
+                                 without its whole ends */
+    LMKV_ROTARY_YARN = 5      /* RAMP between whole pairs, as the authors of "YaRN" (Peng et al.,
+                                 2023) released it and checkpoints that name it are made: the
+                                 fast end rounded down and at least 0, the slow end rounded up and at
+                                 most rot_dim - 1 (one and the same: a step behind it).  The paper's
+                                 text has BANDS in its place, with the same magnitude */
 } lmkv_rotary_scaling_t;
 
 /* Fill *out (host only): inv_freq[i] = base^(-2i / rot_dim), scaled.  `low`,
- * `high` and `original` are read by BANDS and RAMP.  INVALID_ARG for an odd
+ * `high` and `original` are read by BANDS, RAMP and YARN.  INVALID_ARG for an odd
  * or out-of-range rot_dim, base <= 1, factor < 1, low >= high or low <= 0, original
- * <= 0, a value that is not finite, or an unknown scaling. */
+ * <= 0, a YARN whose ends have changed places (all pairs are slower or faster than both), a value
+ * that is not finite, or an unknown scaling. */
 int lmkv_rotary_init(lmkv_rotary_t* out, int32_t rot_dim, int32_t interleaved, double base,
                      int32_t scaling, double factor, double low, double high, double original);
 

@@ -196,9 +196,9 @@ int lmkv_rotary_init(lmkv_rotary_t* out, int32_t rot_dim, int32_t interleaved, d
     if (out == nullptr || rot_dim < 2 || rot_dim % 2 != 0 || rot_dim > 2 * LMKV_ROTARY_MAX_PAIRS ||
         !finite_all(base, factor, low, high, original) || !(base > 1.0) || !(factor >= 1.0))
         return LMKV_ERR_INVALID_ARG;
-    if (scaling < LMKV_ROTARY_PLAIN || scaling > LMKV_ROTARY_RAMP) return LMKV_ERR_INVALID_ARG;
-    if ((scaling == LMKV_ROTARY_BANDS || scaling == LMKV_ROTARY_RAMP) &&
-        (!(low > 0.0) || !(low < high) || !(original > 0.0)))
+    if (scaling < LMKV_ROTARY_PLAIN || scaling > LMKV_ROTARY_YARN) return LMKV_ERR_INVALID_ARG;
+    const bool ramp = scaling == LMKV_ROTARY_RAMP || scaling == LMKV_ROTARY_YARN;
+    if ((scaling == LMKV_ROTARY_BANDS || ramp) && (!(low > 0.0) || !(low < high) || !(original > 0.0)))
         return LMKV_ERR_INVALID_ARG;
     if (scaling == LMKV_ROTARY_BASE) {
         if (rot_dim <= 2) return LMKV_ERR_INVALID_ARG;
@@ -208,9 +208,20 @@ int lmkv_rotary_init(lmkv_rotary_t* out, int32_t rot_dim, int32_t interleaved, d
     lmkv_rotary_t r = {};
     r.rot_dim = rot_dim;
     r.interleaved = interleaved != 0;
-    r.magnitude = scaling == LMKV_ROTARY_RAMP ? 0.1 * std::log(factor) + 1.0 : 1.0;
+    r.magnitude = ramp ? 0.1 * std::log(factor) + 1.0 : 1.0;
     // the (fractional) pair that makes n turns over `original` positions
     auto pair_of = [&](double n) { return rot_dim * std::log(original / (n * two_pi)) / (2.0 * std::log(base)); };
+    double first = 0.0, last = 0.0;      // ends of the ramp
+    if (ramp) {
+        first = pair_of(high);
+        last = pair_of(low);             // > first
+        if (scaling == LMKV_ROTARY_YARN) {
+            first = std::fmax(std::floor(first), 0.0);
+            last = std::fmin(std::ceil(last), rot_dim - 1.0);
+            if (last < first) return LMKV_ERR_INVALID_ARG;
+            if (last == first) last += 0.001;
+        }
+    }
     for (int i = 0; i < rot_dim / 2; ++i) {
         const double f = std::pow(base, -2.0 * i / rot_dim);
         double keep = 1.0;      // share of the unscaled frequency
@@ -218,8 +229,7 @@ int lmkv_rotary_init(lmkv_rotary_t* out, int32_t rot_dim, int32_t interleaved, d
             keep = 0.0;
         } else if (scaling == LMKV_ROTARY_BANDS) {
             keep = (original * f / two_pi - low) / (high - low);
-        } else if (scaling == LMKV_ROTARY_RAMP) {
-            const double first = pair_of(high), last = pair_of(low);     // first < last
+        } else if (ramp) {
             keep = 1.0 - (i - first) / (last - first);
         }
         keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;

@@ -32,7 +32,7 @@ ERR_BAD_DATA = 9
 ERR_BAD_LENGTH = 10
 BF16, FP16, FP32 = 0, 1, 2                  # lmkv_dtype_t
 ROTARY_MAX_PAIRS = 128
-ROTARY_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
+ROTARY_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4, "yarn": 5}
 NOALLOC_STAGING_BYTES = 64 << 20
 CACHEGEN_BATCH = 256
 CACHEGEN_MAX_CHANNELS = 2048
