@@ -667,7 +667,9 @@ int lmkv_scatter_layer_shifted(const lmkv_pool_t* pool, int32_t dtype, const int
  *   out = sum softmax(x) v   and   lse = ln sum exp(x),
  * query head h using KV head h / (num_q_heads / num_kv_heads).
  *   out : rows like q's, not overlapping it;  lse : DEVICE float32 [num_tokens][num_q_heads] or NULL
- *   workspace : DEVICE, 16-byte aligned, lmkv_attend_workspace_bytes bytes,
+ *   workspace : DEVICE, 16-byte aligned, lmkv_attend_workspace_bytes bytes for
+ *               bounds that the call's do not exceed (the same num_q_heads), so that
+ *               one buffer serves a program's largest and smaller batches;
  *               contents irrelevant, not shared with calls that may run at
  *               the same time (two captured graphs included)
  * A token that sees nothing gets out = 0 and lse = -infinity.  A cached token

@@ -1290,6 +1290,7 @@ struct Plan {
 };
 
 constexpr int32_t kSms = 152;
+constexpr int32_t kStreamKeys = 16 * kWarps * kChunk;     // own contexts longer than this go by streams
 
 // Scores of a prefix (rows x keys x KV heads) from which its rows are taken by tiles.
 // Below, the row kernel's 16 rows at a time read the prefix again from L2 in
@@ -1313,19 +1314,37 @@ void split(int64_t ctas, int32_t keys, int32_t* splits, int32_t* span) {
 
 // Parts of the tile kernel's blocks: the number that leaves the fewest rounds
 // of one CTA per SM, a part's cost being its blocks and the writing and
-// joining of its rows (about two blocks' time).
+// joining of its rows (about two blocks' time).  More than kMostRounds rounds would gain 3 % at most,
+// for more workspace.
+constexpr int32_t kMostParts = 64, kMostRounds = 16;
 int32_t tile_parts(int64_t ctas, int64_t blocks) {
     int32_t best = 1;
     double best_cost = 0;
-    for (int32_t n = 1; n <= 64 && n <= blocks; ++n) {
-        const double rounds = (double)((ctas * n + kSms - 1) / kSms);
-        const double cost = rounds * ((double)((blocks + n - 1) / n) + (n > 1 ? 2.0 : 0.0)) + (n > 1 ? 1.0 : 0.0);
+    for (int32_t n = 1; n <= kMostParts && n <= blocks; ++n) {
+        const int64_t rounds = (ctas * n + kSms - 1) / kSms;
+        if (n > 1 && rounds > kMostRounds) break;
+        const double cost = (double)rounds * ((double)((blocks + n - 1) / n) + (n > 1 ? 2.0 : 0.0)) + (n > 1 ? 1.0 : 0.0);
         if (n == 1 || cost < best_cost) {
             best = n;
             best_cost = cost;
         }
     }
     return best;
+}
+
+// The most CTAs that tile_parts makes of `ctas` for any number of blocks up to this.  With x =
+// ctas / kSms and b blocks, n parts cost more than x (b + 2 n) + 1; so n is not taken unless that is
+// below the cost of a single part, ceil(x) b, nor, where some n1 parts fill one round, unless it
+// is below theirs, b / n1 + 4.
+int64_t most_tile_ctas(int64_t ctas, int64_t blocks) {
+    const double x = (double)ctas / kSms, b = (double)blocks;
+    const int64_t n1 = kSms / ctas;
+    const double bound = n1 <= 1 ? (std::ceil(x) - x) * b : (1.0 / (double)n1 - x) * b + 3.0;
+    int64_t most = (int64_t)(bound * kSms / 2) + 1;
+    if (most < n1 * ctas) most = n1 * ctas;             // (and those beside streams)
+    if (most > kMostRounds * kSms) most = kMostRounds * kSms;
+    if (most > ctas * blocks) most = ctas * blocks;
+    return most < ctas ? ctas : most;
 }
 
 Plan make_plan(const lmkv_pool_t* pool, int32_t q_heads, int32_t num_tokens, int32_t num_req, int32_t max_new,
@@ -1357,7 +1376,7 @@ Plan make_plan(const lmkv_pool_t* pool, int32_t q_heads, int32_t num_tokens, int
     // 68, 2048 178 : 132; 128 behind 8192, 65 : 46, 118 : 80, 239 : 205.)
     const int64_t heads = pool->num_kv_heads, tile_heads = x.tiles * heads;
     const bool beside = !x.big && x.tiles > 0 && tile_heads <= kSms / 2;
-    if (max_kv_len > (beside ? 0 : 16 * kWarps * kChunk)) {
+    if (max_kv_len > (beside ? 0 : kStreamKeys)) {
         int64_t warps = kRowCtas * kSms * kWarps;
         if (beside) {
             // The SMs are divided by what each side would take of them: 2.3 us for 256 rows x 128
@@ -1389,6 +1408,45 @@ Plan make_plan(const lmkv_pool_t* pool, int32_t q_heads, int32_t num_tokens, int
     x.bytes = x.o_bytes + x.ml_bytes + x.range_bytes +
               (x.big ? (uint64_t)x.tiles * pool->num_kv_heads * x.prefix_parts * 32 : 0);
     return x;
+}
+
+// Bytes that hold the plan of any call within these bounds (a plan's own need falls where
+// a larger batch needs no parts).
+uint64_t most_bytes(const lmkv_pool_t* pool, int32_t q_heads, int32_t num_tokens, int32_t num_req, int32_t max_new,
+                    int32_t prefix_len, int32_t max_kv_len) {
+    const int64_t heads = pool->num_kv_heads, group = q_heads / heads;
+    const int64_t rows = (int64_t)num_tokens * q_heads;
+    const int64_t req_rows = (int64_t)(max_new < 1 ? 1 : max_new < num_tokens ? max_new : num_tokens) * group;
+    const bool big = req_rows >= kBigRows;
+    const bool far = max_kv_len > kStreamKeys;
+    if (!big && !far && prefix_len == 0) return 0;              // one part, written at once
+    // the prefix's parts, by tiles (of every number of them up to the call's) and by rows
+    uint64_t parts = 0, again = 0;
+    if (big || prefix_len > 0) {
+        const int64_t blocks = ((int64_t)prefix_len + kBlock - 1) / kBlock + (big ? ((int64_t)max_kv_len + kBlock - 1) / kBlock : 0);
+        const int64_t tiles = ((int64_t)num_tokens * group + kTileRows - 1) / kTileRows;
+        int64_t ctas = tiles * heads;
+        for (int64_t t = 1; t <= tiles && t * heads <= kMostRounds * kSms; ++t) {
+            const int64_t most = most_tile_ctas(t * heads, blocks < 1 ? 1 : blocks);
+            const int64_t tile_rows = t * kTileRows * heads < rows ? t * kTileRows * heads : rows;
+            const uint64_t n = (uint64_t)(most / (t * heads)) * tile_rows;
+            if (n > parts) parts = n;
+            if (most > ctas) ctas = most;
+        }
+        if ((uint64_t)rows > parts) parts = rows;
+        if (big) again = (uint64_t)ctas * 32;
+    }
+    if (prefix_len > 0) {
+        // split() makes two rounds of kRowCtas an SM, and as many again by rounding up
+        const int64_t by_keys = ((int64_t)prefix_len + 127) / 128 * rows, by_ctas = (int64_t)4 * kRowCtas * kSms * kRowTile;
+        const uint64_t n = by_keys < by_ctas ? by_keys : by_ctas;
+        if (n > parts) parts = n;
+    }
+    const int64_t warps = far ? kRowCtas * kSms * kWarps : prefix_len > 0 && max_kv_len > 0 ? kSms * kStreamWarps : 0;
+    const int64_t streams = warps == 0 ? 0 : warps / heads > 0 ? warps / heads : 1;
+    const int64_t own_cap = big ? kBigRows - 1 : req_rows, own_tiles = (own_cap + kRowTile - 1) / kRowTile;
+    const uint64_t own_rows = ((uint64_t)streams + (uint64_t)num_req * own_tiles) * (own_cap < kRowTile ? own_cap : kRowTile) * heads;
+    return (parts + own_rows) * ((uint64_t)pool->head_dim * 4 + 8) + (uint64_t)num_req * own_tiles * 8 + again;
 }
 
 int check_shape(const lmkv_pool_t* pool) {
@@ -1451,8 +1509,7 @@ int lmkv_attend_workspace_bytes(const lmkv_pool_t* pool, int32_t num_q_heads, in
         (int64_t)num_tokens * num_q_heads > (int64_t)1 << 30)
         return LMKV_ERR_INVALID_ARG;
     *bytes = num_tokens == 0 || num_req == 0
-                 ? 0 : make_plan(pool, num_q_heads, num_tokens, num_req, max_new, (int32_t)prefix_len,
-                             max_kv_len).bytes;
+                 ? 0 : most_bytes(pool, num_q_heads, num_tokens, num_req, max_new, (int32_t)prefix_len, max_kv_len);
     return LMKV_OK;
 }
 

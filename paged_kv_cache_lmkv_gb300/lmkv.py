@@ -909,7 +909,7 @@ def scatter_layer_shifted(pool, block_table, start, end, chunk_size, save_unfull
 
 def attend_workspace_bytes(pool, num_q_heads: int, num_tokens: int, num_req: int, max_new: int,
                            prefix_len: int = 0, max_kv_len: int = 0) -> int:
-    """Bytes of workspace an attend_layer call of these bounds needs."""
+    """Bytes of workspace for attend_layer calls within these bounds (smaller ones too)."""
     out = ctypes.c_uint64(0)
     check(load().lmkv_attend_workspace_bytes(pool.struct, int(num_q_heads), int(num_tokens), int(num_req),
                                              int(max_new), int(prefix_len), int(max_kv_len),
@@ -923,7 +923,7 @@ def attend_layer(pool, layer, q, out, q_start, kv_len, block_table, scale, works
     prefix and the requests' own cached tokens, into out (and lse, float32
     [tokens][heads]).  max_new and max_kv_len bound the lengths on the device
     (default: the rows of q, the table's width); tight ones cost less.
-    workspace: uint8 of attend_workspace_bytes for the same bounds."""
+    workspace: uint8 of attend_workspace_bytes for the same bounds or larger ones."""
     t0 = pool.layers[0]
     dt, dev = t0.dtype, t0.get_device()
     tokens, heads = _heads_of("q", q)

@@ -230,3 +230,25 @@ def test_append_slow_frequencies_at_far_positions(share):
     want = torch.cat((a * math.cos(t) - c * math.sin(t), a * math.sin(t) + c * math.cos(t)), -1)
     mag = (a.abs() + c.abs()).repeat(1, 1, 2)
     within(out, want, 2.0 ** -24 * 1.001 * want.abs() + 2.0 ** -21 * mag, "q")
+
+
+# ---- workspace ----------------------------------------------------------
+
+@pytest.mark.parametrize("prefix,max_kv,calls", [
+    (0, 1024, [([200, 250], [300, 1024]), ([64], [700]), ([1, 1, 30], [1000, 5, 30]), ([1], [1])]),
+    (0, 3000, [([1, 1, 1], [2900, 5, 30]), ([1, 80], [900, 2000]), ([1], [3000])]),
+    (700, 600, [([1] * 6, [40, 3, 600, 1, 1, 90]), ([90, 1], [90, 600]), ([2, 2], [9, 2])])])
+def test_attend_workspace_of_the_largest_batch_serves_smaller_ones(prefix, max_kv, calls):
+    """One workspace, sized for bounds that no call exceeds."""
+    b = Batch([1], [1], 8, 2, 64, BF, prefix=prefix)
+    n = pkg.attend_workspace_bytes(b.pool, 8, 8192, 8, 2048, prefix, max_kv)
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV)
+    for new, kv in calls:
+        for p in sorted({prefix, prefix // 3}):
+            b = Batch(new, kv, 8, 2, 64, BF, prefix=p)
+            out, lse = attend(b, ws=ws)
+            torch.cuda.synchronize()
+            assert b.status.item() == 0
+            want, want_l, tol, tol_l = b.attend()
+            within(out, want, tol, "out")
+            within(lse, want_l, tol_l, "lse")
