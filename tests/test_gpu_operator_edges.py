@@ -252,3 +252,72 @@ def test_attend_workspace_of_the_largest_batch_serves_smaller_ones(prefix, max_k
             want, want_l, tol, tol_l = b.attend()
             within(out, want, tol, "out")
             within(lse, want_l, tol_l, "lse")
+
+
+# ---- strides, ties, repeated calls ----------------------------------------
+
+def test_attend_strides_below_zero():
+    """Rows whose tokens and heads lie in falling order, as the C structure can say."""
+    b = Batch([1, 40, 2], [30, 41, 900], 8, 2, 64, BF, prefix=50)
+    t, d = b.tokens, 64
+    q = b.q.flip((0, 1)).contiguous()
+    out = torch.full_like(q, 7.0)
+    lse = torch.full((t, 8), 7.0, device=DEV)
+    n = pkg.attend_workspace_bytes(b.pool, 8, t, 3, 40, 50, 900)
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV)
+    last = 2 * d * (t * 8 - 1)                    # bytes to the last row, which is token 0's head 0
+    batch = lmkv._BatchT(b.q_start_d.data_ptr(), b.kv_len_d.data_ptr(), b.table_d.data_ptr(), b.table_d.shape[1], 3, t, 40, 900)
+    rows = [bytes(lmkv._RowsT(x.data_ptr() + last, -8 * d, -d)) for x in (q, out)]
+    pkg.check(lmkv.load().lmkv_attend_layer(
+        b.pool.struct, lmkv.BF16, 1, bytes(batch), 8, rows[0], b.prefix_table_d.data_ptr(), 50, b.scale, rows[1],
+        lse.data_ptr(), ws.data_ptr(), n, b.status.data_ptr(), torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    assert b.status.item() == 0
+    want, want_l, tol, tol_l = b.attend()
+    within(out.flip((0, 1)), want, tol, "out")
+    within(lse, want_l, tol_l, "lse")
+
+
+@pytest.mark.parametrize("new,kv,prefix", [([1, 2], [60, 900], 30), ([1, 70], [60, 90], 300)])
+def test_attend_equal_scores(new, kv, prefix):
+    """All keys alike: every weight is 1, lse is the score and the logarithm of the count."""
+    b = Batch(new, kv, 4, 2, 64, BF, prefix=prefix)
+    for x in (b.pool_cpu[1], b.pool.layers[1]):
+        k = x.view(2, -1, 128)[0]
+        for at in [b.slots(0), b.slots(1), b.prefix_slots()]:
+            k[at] = 0.5
+    out, lse = attend(b)
+    torch.cuda.synchronize()
+    want, want_l, tol, tol_l = b.attend()
+    within(out, want, tol, "out")
+    within(lse, want_l, tol_l, "lse")
+
+
+@pytest.mark.parametrize("kv,budget,kv_heads", [([64] * 40, 48, 1), ([17] * 300, 16, 1), ([9000, 300, 60000], 2000, 2)])
+def test_evict_same_start_same_bits(kv, budget, kv_heads):
+    """Calls from one start, again and again: pool, keep, new_len and kept scores have the same bits."""
+    b = Batch([0] * len(kv), kv, kv_heads, kv_heads, 64, BF)
+    g = torch.Generator().manual_seed(6)
+    scores = torch.randint(0, 9, (len(kv), kv_heads, max(kv)), generator=g).float().to(DEV)     # ties all over
+    start, first = b.pool.layers[1].clone(), None
+    for _ in range(4):
+        b.pool.layers[1].copy_(start)
+        keep = torch.full((len(kv), kv_heads, budget), 99, dtype=torch.int32, device=DEV)
+        new_len = torch.full((len(kv),), 99, dtype=torch.int32, device=DEV)
+        kept = torch.full((len(kv), kv_heads, budget), 99.0, device=DEV)
+        pkg.check(pkg.evict_layer(b.pool, 1, b.table_d, b.kv_len_d, scores, 2, 3, keep, new_len, kept_scores=kept,
+                                  status=b.status))
+        torch.cuda.synchronize()
+        assert b.status.item() == 0
+        now = [keep, new_len, kept, b.pool.layers[1].view(torch.int16).clone()]
+        first = now if first is None else first
+        for x, y in zip(first, now):
+            assert torch.equal(x, y)
+    before = start.view(2, -1, kv_heads, 64)
+    after = b.pool.layers[1].view(2, -1, kv_heads, 64)
+    for r in range(len(kv)):
+        at = b.slots(r).to(DEV)
+        n = min(kv[r], budget)
+        for h in range(kv_heads):
+            idx = keep[r, h, :n].long()
+            assert torch.equal(after[:, at[:n], h], before[:, at[idx], h])
