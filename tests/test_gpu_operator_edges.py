@@ -321,3 +321,44 @@ def test_evict_same_start_same_bits(kv, budget, kv_heads):
         for h in range(kv_heads):
             idx = keep[r, h, :n].long()
             assert torch.equal(after[:, at[:n], h], before[:, at[idx], h])
+
+
+@pytest.mark.parametrize("scale", [0.125, -0.125])
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("new,kv,prefix", [
+    ([1, 2], [60, 90], 30), ([1, 70], [60, 90], 300), ([70, 3], [90, 40], 0), ([1, 1], [1500, 40], 50),
+    ([1] * 78 + [0, 3], [1 + (i * 17) % 60 for i in range(78)] + [0, 9], 20011)])
+def test_attend_one_key_far_above(dtype, new, kv, prefix, scale):
+    """A key whose score is near the largest that fp32 has room for is all that its rows see: its value is
+    the result, its score lse, whichever kernel comes upon it; other requests' rows are as without it."""
+    b = Batch(new, kv, 8, 2, 64, dtype, prefix=prefix)
+    b.scale = scale
+    b.q_cpu.copy_(b.q_cpu.abs() + 1)
+    b.q.copy_(b.q_cpu)
+    top = torch.tensor(torch.finfo(dtype).max / (4096 if dtype == BF else 1)).to(dtype)
+    top = top if scale > 0 else -top
+    in_prefix = prefix > 0
+    at = int(b.prefix_slots()[prefix // 2]) if in_prefix else int(b.slots(0)[5])
+    for x in (b.pool_cpu[1], b.pool.layers[1]):
+        x.view(2, -1, 128)[0, at] = top.to(x.device)
+    out, lse = attend(b)
+    torch.cuda.synchronize()
+    assert b.status.item() == 0
+    for r, n in enumerate(new):
+        if not in_prefix and r > 0:
+            continue
+        for i in range(int(b.q_start[r]), int(b.q_start[r + 1])):
+            for h in range(2):
+                v = b.pool_cpu[1, 1].view(-1, 128)[at, h * 64:(h + 1) * 64]
+                for a in range(4 * h, 4 * h + 4):
+                    assert torch.equal(out[i, a].cpu(), v), (r, i, a)
+            score = b.q_cpu[i].double().sum(-1) * float(top) * scale
+            within(lse[i], score, 2.0 ** -18 * score.abs(), "lse")
+    if not in_prefix:
+        ref = Batch(new, kv, 8, 2, 64, dtype, prefix=prefix)
+        ref.scale = scale
+        ref.q_cpu.copy_(b.q_cpu)
+        want, want_l, tol, tol_l = ref.attend()
+        lo = int(b.q_start[1])
+        within(out[lo:], want[lo:], tol[lo:], "the others")
+        within(lse[lo:], want_l[lo:], tol_l[lo:], "lse of the others")
