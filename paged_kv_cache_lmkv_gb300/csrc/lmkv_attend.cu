@@ -313,128 +313,137 @@ __device__ __forceinline__ void put_final(const AttendParams& p, int32_t tok, in
         p.lse[(int64_t)tok * p.q_heads + head] = ((top == -INFINITY ? 0.f : top) + log2f(sum)) * kLn2;
 }
 
-// Takes rows of the tile kernel again, where a request may be big.  Most are rows that a value
+// Rows of the tile kernel are taken again where a request may be big.  Most are rows that a value
 // of another request has spoiled: the tile's product multiplies every key's row of v, those a row
-// does not see by a weight of 0, and 0 times infinity or NaN is NaN.  Others have scores far from 0 (kFarScore).
-// The last CTAs of the row or stream kernel, which follow the tile kernel, share the windows of 16 rows
-// that hold some; one goes over the prefix and the own keys of one request
-// at a time, as the row kernel takes its rows.  What comes of the request's rows is the
-// whole result of a big one and the prefix's of others, and stands for all parts.  Without
-// any, which is the rule, 16 bits a window are looked at: 1 us.  (Requests of 70, 70, 70 and
-// 30 tokens behind 12000 keys, 16 heads of 128, one with a NaN: 0.29 ms, without it 0.054; a row a warp
-// took 7.8.)
+// does not see by a weight of 0, and 0 times infinity or NaN is NaN.  Others have scores far from 0
+// (kFarScore).  The last CTAs of the row or stream kernel, which follow the tile kernel, share the
+// windows of 16 rows that hold some; one goes over the prefix and the own keys of one request at
+// a time, as the row kernel takes its rows.  What comes of the request's rows is the whole result of a
+// big one and the prefix's of others, and stands for all parts.  Without any, which is the rule,
+// 16 bits a window are looked at: 0 to 2 us.  (Requests of 70, 70, 70 and 30 tokens behind 12000 keys, 16
+// heads of 128, one with a NaN: 0.34 ms, without it 0.057; a row a warp took 7.8.)
+
+// The windows of a CTA: bits of the rows, those of window w0 + f * ctas in found[f].
 template <class T, int D>
-__device__ __forceinline__ void take_again(const AttendParams& p, int32_t cta, int32_t ctas, uint8_t* smem,
-                                           float2 (*ml)[kRowTile]) {
+__device__ __noinline__ void take_windows(const AttendParams& p, const uint32_t* found, int32_t w0, int32_t ctas, uint8_t* smem,
+                                          float2 (*ml)[kRowTile]) {
     using W = WarpRows<T, D>;
-    __shared__ uint32_t found[kWarps][32];
+    constexpr int kWindows = kTileRows / kRowTile;      // of a tile
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int32_t group = (int32_t)p.by_group.d;
     const int32_t live_rows = min(max(p.seqs.q_start[p.seqs.num_req], 0), p.seqs.num_tokens) * group;
-    constexpr int kWindows = kTileRows / kRowTile;      // of a tile
-    const int32_t windows = p.tiles * kWindows * p.kv_heads;
     const uint32_t ring = smem_u32(smem) + warp * (kStages * 2 * W::kTileBytes);
     const float signed_scale = p.scale_log2 * (float)p.scale_sign;
     const uint8_t* const base = p.layer.base();
+#pragma unroll 1
+    for (int32_t f = 0; f < kWarps * 32; ++f) {
+        uint32_t left = found[f];      // the same for all threads
+        if (left == 0) continue;
+        const int32_t at = w0 + f * ctas;
+        Tile t;
+        t.h = at / kWindows / p.tiles;
+        t.t0 = 0;
+        t.row0 = at / kWindows % p.tiles * kTileRows + at % kWindows * kRowTile;
+        t.nrows = live_rows - t.row0;
+        t.limit0 = t.causal = 0;                    // (limits below)
+        while (left != 0) {
+            // the request of the first row left, and its rows of the window
+            const int32_t tok0 = (int32_t)p.by_group.div((uint32_t)(t.row0 + __ffs(left) - 1));
+            const Req q = load_req(p.seqs, find_request(p.seqs.num_req, tok0, [&](int32_t i) { return p.seqs.q_start[i]; }));
+            const bool big = q.n * group >= kBigRows;
+            uint32_t now = 0;
+            for (int r = 0; r < kRowTile; ++r) {
+                const int32_t tok = (int32_t)p.by_group.div((uint32_t)(t.row0 + r));
+                if (((left >> r) & 1) && tok >= q.q0 && tok < q.q0 + q.n) now |= 1u << r;
+            }
+            left &= ~(now | (left & -left));        // (a row of no request is left as it is)
+            if (now == 0) continue;
+            W x;
+            x.begin(p, t);
+#pragma unroll 1
+            for (int own = 0; own < (big ? 2 : 1); ++own) {
+                // (rows of other requests come to nothing that is kept)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int32_t rr = min((lane >> 2) + 8 * i, t.nrows - 1);
+                    const int32_t tok = (int32_t)p.by_group.div((uint32_t)(t.row0 + rr));
+                    x.limit[i] = own ? q.len - q.n + 1 + (tok - q.q0) : p.prefix_len;
+                }
+                const int32_t end = base == nullptr ? 0 : own ? q.len : p.prefix_len;
+                const int32_t chunks = (end + kChunk - 1) / kChunk;
+                const int32_t mine = chunks > warp ? (chunks - warp + kWarps - 1) / kWarps : 0;
+                uint32_t there[kStages];
+                ChunkCopy<D, true> rows(p.layer, own ? p.seqs.table + (int64_t)q.r * p.seqs.table_stride : p.prefix_table,
+                                        base, t.h, end);
+                auto key_of = [&](int32_t i) { return (i * kWarps + warp) * kChunk; };
+                auto fill = [&](int32_t i) {        // (what is not there has been reported)
+                    return rows.copy(key_of(i), ring + (i % kStages) * (2 * W::kTileBytes), key_of(i + 1), nullptr);
+                };
+                __syncwarp();
+                rows.lookup(key_of(0));
+#pragma unroll
+                for (int s = 0; s < kStages - 1; ++s) {
+                    there[s] = s < mine ? fill(s) : 0u;
+                    cp_commit();
+                }
+                for (int32_t i0 = 0; i0 < mine; i0 += kStages) {
+#pragma unroll
+                    for (int u = 0; u < kStages; ++u) {
+                        const int32_t i = i0 + u;
+                        if (i >= mine) break;
+                        __syncwarp();      // the stage filled next was read by every lane
+                        constexpr int kAhead = kStages - 1;
+                        there[(u + kAhead) % kStages] = i + kAhead < mine ? fill(i + kAhead) : 0u;
+                        cp_commit();
+                        cp_wait<kStages - 1>();
+                        __syncwarp();
+                        x.chunk(ring + u * (2 * W::kTileBytes), key_of(i), there[u], signed_scale);
+                    }
+                }
+                cp_wait<0>();
+            }
+            __syncthreads();
+            x.end();
+            join_warps<T, D>(x, smem, ml, [&](int rr, int c, float top, float sum, float4 acc) {
+                if (((now >> rr) & 1) == 0) return;
+                const int32_t tok = (int32_t)p.by_group.div((uint32_t)(t.row0 + rr));
+                const int32_t head = t.h * group + (t.row0 + rr - tok * group);
+                if (big && p.prefix_parts == 1) {
+                    put_final<T>(p, tok, head, c, top, sum, acc);
+                    return;
+                }
+                for (int32_t part = 0; part < p.prefix_parts; ++part) {
+                    const int64_t row = (int64_t)part * p.rows + (int64_t)tok * p.q_heads + head;
+                    *reinterpret_cast<float4*>(p.part_o + row * D + c) = part == 0 ? acc : make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (c == 0) p.part_ml[row] = part == 0 ? make_float2(top, sum) : make_float2(-INFINITY, 0.f);
+                }
+            });
+            __syncthreads();
+        }
+    }
+}
+
+// Looks for windows; the CTA is number `cta` of those that do.
+template <class T, int D>
+__device__ __forceinline__ void take_again(const AttendParams& p, int32_t cta, int32_t ctas, uint8_t* smem,
+                                           float2 (*ml)[kRowTile]) {
+    __shared__ uint32_t found[kWarps * 32];
+    constexpr int kWindows = kTileRows / kRowTile;      // of a tile
+    const int32_t windows = p.tiles * kWindows * p.kv_heads;
     // every thread looks at one of the CTA's windows, that many at a time
     for (int32_t w0 = cta; w0 < windows; w0 += kWarps * 32 * ctas) {
         const int32_t mine = w0 + (int32_t)threadIdx.x * ctas;
         uint32_t bits = 0;
         if (mine < windows) {
-            const int32_t tile = mine / kWindows % p.tiles, h = mine / kWindows / p.tiles, win = mine % kWindows;
+            const int32_t at = mine / kWindows, win = mine % kWindows;        // tile + p.tiles * head
             for (int32_t part = 0; part < p.prefix_parts; ++part)
-                bits |= p.again[(((int64_t)part * p.kv_heads + h) * p.tiles + tile) * 8 + (win >> 1)];
+                bits |= p.again[((int64_t)part * p.kv_heads * p.tiles + at) * 8 + (win >> 1)];
             bits = (bits >> ((win & 1) * kRowTile)) & 0xFFFFu;
         }
         if (!__syncthreads_or(bits != 0)) continue;
-        found[warp][lane] = bits;
+        found[threadIdx.x] = bits;
         __syncthreads();
-#pragma unroll 1
-        for (int32_t f = 0; f < kWarps * 32; ++f) {
-            uint32_t left = found[f >> 5][f & 31];      // the same for all threads
-            if (left == 0) continue;
-            const int32_t at = w0 + f * ctas;
-            Tile t;
-            t.h = at / kWindows / p.tiles;
-            t.t0 = 0;
-            t.row0 = at / kWindows % p.tiles * kTileRows + at % kWindows * kRowTile;
-            t.nrows = live_rows - t.row0;
-            t.limit0 = t.causal = 0;                    // (limits below)
-            while (left != 0) {
-                // the request of the first row left, and its rows of the window
-                const int32_t tok0 = (int32_t)p.by_group.div((uint32_t)(t.row0 + __ffs(left) - 1));
-                const Req q = load_req(p.seqs, find_request(p.seqs.num_req, tok0, [&](int32_t i) { return p.seqs.q_start[i]; }));
-                const bool big = q.n * group >= kBigRows;
-                uint32_t now = 0;
-                for (int r = 0; r < kRowTile; ++r) {
-                    const int32_t tok = (int32_t)p.by_group.div((uint32_t)(t.row0 + r));
-                    if (((left >> r) & 1) && tok >= q.q0 && tok < q.q0 + q.n) now |= 1u << r;
-                }
-                left &= ~(now | (left & -left));        // (a row of no request is left as it is)
-                if (now == 0) continue;
-                W x;
-                x.begin(p, t);
-#pragma unroll 1
-                for (int own = 0; own < (big ? 2 : 1); ++own) {
-                    // (rows of other requests come to nothing that is kept)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int32_t rr = min((lane >> 2) + 8 * i, t.nrows - 1);
-                        const int32_t tok = (int32_t)p.by_group.div((uint32_t)(t.row0 + rr));
-                        x.limit[i] = own ? q.len - q.n + 1 + (tok - q.q0) : p.prefix_len;
-                    }
-                    const int32_t end = base == nullptr ? 0 : own ? q.len : p.prefix_len;
-                    const int32_t chunks = (end + kChunk - 1) / kChunk;
-                    const int32_t mine = chunks > warp ? (chunks - warp + kWarps - 1) / kWarps : 0;
-                    uint32_t there[kStages];
-                    ChunkCopy<D, true> rows(p.layer, own ? p.seqs.table + (int64_t)q.r * p.seqs.table_stride : p.prefix_table,
-                                            base, t.h, end);
-                    auto key_of = [&](int32_t i) { return (i * kWarps + warp) * kChunk; };
-                    auto fill = [&](int32_t i) {        // (what is not there has been reported)
-                        return rows.copy(key_of(i), ring + (i % kStages) * (2 * W::kTileBytes), key_of(i + 1), nullptr);
-                    };
-                    __syncwarp();
-                    rows.lookup(key_of(0));
-#pragma unroll
-                    for (int s = 0; s < kStages - 1; ++s) {
-                        there[s] = s < mine ? fill(s) : 0u;
-                        cp_commit();
-                    }
-                    for (int32_t i0 = 0; i0 < mine; i0 += kStages) {
-#pragma unroll
-                        for (int u = 0; u < kStages; ++u) {
-                            const int32_t i = i0 + u;
-                            if (i >= mine) break;
-                            __syncwarp();      // the stage filled next was read by every lane
-                            constexpr int kAhead = kStages - 1;
-                            there[(u + kAhead) % kStages] = i + kAhead < mine ? fill(i + kAhead) : 0u;
-                            cp_commit();
-                            cp_wait<kStages - 1>();
-                            __syncwarp();
-                            x.chunk(ring + u * (2 * W::kTileBytes), key_of(i), there[u], signed_scale);
-                        }
-                    }
-                    cp_wait<0>();
-                }
-                __syncthreads();
-                x.end();
-                join_warps<T, D>(x, smem, ml, [&](int rr, int c, float top, float sum, float4 acc) {
-                    if (((now >> rr) & 1) == 0) return;
-                    const int32_t tok = (int32_t)p.by_group.div((uint32_t)(t.row0 + rr));
-                    const int32_t head = t.h * group + (t.row0 + rr - tok * group);
-                    if (big && p.prefix_parts == 1) {
-                        put_final<T>(p, tok, head, c, top, sum, acc);
-                        return;
-                    }
-                    for (int32_t part = 0; part < p.prefix_parts; ++part) {
-                        const int64_t row = (int64_t)part * p.rows + (int64_t)tok * p.q_heads + head;
-                        *reinterpret_cast<float4*>(p.part_o + row * D + c) = part == 0 ? acc : make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (c == 0) p.part_ml[row] = part == 0 ? make_float2(top, sum) : make_float2(-INFINITY, 0.f);
-                    }
-                });
-                __syncthreads();
-            }
-        }
+        take_windows<T, D>(p, found, w0, ctas, smem, ml);
         __syncthreads();
     }
 }
@@ -449,7 +458,7 @@ __device__ __forceinline__ void take_again(const AttendParams& p, int32_t cta, i
 // latency: a launch, three dependent look-ups, one round of rows.)
 // kBig: a request may be big, and the CTAs from again_cta on take_again.
 template <class T, int D, bool kBig>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, kRowCtas)
 attend_rows_kernel(const __grid_constant__ AttendParams p) {
     using W = WarpRows<T, D>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -857,7 +866,7 @@ attend_tiles_kernel(const __grid_constant__ AttendParams p) {
     const int32_t row0 = tile * kTileRows;
     const int32_t live_rows = live_tokens * group;
     uint8_t* const base = p.layer.base();
-    if (p.big && tid < 8) p.again[(int64_t)blockIdx.x * 8 + tid] = 0;
+    if (p.big && warp == 10 && lane < 8) p.again[(int64_t)blockIdx.x * 8 + lane] = 0;
     if (warp == 0 && row0 < live_rows) {
         const int32_t t_first = (int32_t)p.by_group.div((uint32_t)row0);
         const int32_t t_last = (int32_t)p.by_group.div((uint32_t)(min(row0 + kTileRows, live_rows) - 1));
@@ -1507,21 +1516,25 @@ int attend_launches(AttendParams& p, const Plan& x, void* stream) {
                     TileShape<D>::kSmem, stream, 1, p);
     if (rc != LMKV_OK) return rc;
     // the own pages, and the prefix where tiles do not have it; beside them the rows to take again
-    const int64_t windows = kBig ? (int64_t)x.tiles * (kTileRows / kRowTile) * p.kv_heads : 0, most = kRowCtas * kSms;
-    const int64_t again = windows < most ? windows : most;
+    const int64_t windows = kBig ? (int64_t)x.tiles * (kTileRows / kRowTile) * p.kv_heads : 0;
+    // (CTAs for them: what the first round has left)
+    auto again = [&](int64_t ctas) {
+        const int64_t left = kRowCtas * kSms - ctas, most = left > kSms / 2 ? left : kSms / 2;
+        return windows < most ? windows : most;
+    };
     if (x.streams == 0 || x.stream_ctas > 0) {
         // (with no room for cached tokens too: lengths beyond that bound are reported)
         const int64_t ctas = ((int64_t)x.row_tiles * x.prefix_parts +
                               (x.streams == 0 ? (int64_t)x.own_tiles * p.seqs.num_req : 0)) * p.kv_heads;
         p.again_cta = (int32_t)ctas;
-        rc = launch(attend_rows_kernel<T, D, kBig>, ctas + again, kWarps * 32, smem, stream, 1, p);
+        rc = launch(attend_rows_kernel<T, D, kBig>, ctas + again(ctas), kWarps * 32, smem, stream, 1, p);
     } else {
         rc = launch(attend_rows_kernel<T, D, kBig>, (int64_t)x.row_tiles * x.prefix_parts * p.kv_heads, kWarps * 32, smem,
                     stream, 1, p);
         const int64_t ctas = ((int64_t)x.streams * p.kv_heads + kWarps - 1) / kWarps;
         p.again_cta = (int32_t)ctas;
         if (rc == LMKV_OK)
-            rc = launch(attend_streams_kernel<T, D, kBig>, ctas + again, kWarps * 32, smem, stream, 1, p);
+            rc = launch(attend_streams_kernel<T, D, kBig>, ctas + again(ctas), kWarps * 32, smem, stream, 1, p);
     }
     if (rc != LMKV_OK || !x.join) return rc;
     // the small requests' rows, where there are no others or those are done already

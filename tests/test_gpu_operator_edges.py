@@ -96,7 +96,7 @@ def call_time(b):
 
 def test_attend_one_bad_value_does_not_stall_the_batch():
     """Rows that share a tile with a request whose values are not finite are taken again sixteen at a time, at
-    five times the clean call's cost here (a row a warp: 144 times)."""
+    six times the clean call's cost here (a row a warp: 144 times)."""
     b = Batch([70, 70, 70, 30], [200, 300, 70, 90], 16, 2, 128, BF, prefix=12000)
     clean = call_time(b)
     b.pool.layers[1].view(2, -1, 256)[1, b.slots(1)[0]] = math.nan
