@@ -567,7 +567,9 @@ typedef struct lmkv_rows {
  * is cached token kv_len[r] - n_r + i.  The lengths live on the DEVICE, so a
  * captured call follows them; the HOST gives their bounds.  Rows behind
  * q_start[num_req] (a padded batch) are left as they are.  A length outside
- * its bounds is clamped and reported as BAD_LENGTH. */
+ * its bounds is clamped and reported as BAD_LENGTH, except by calls that launch nothing
+ * (no requests; no tokens, where only their rows would be written) and, of requests
+ * without new tokens, by lmkv_append_layer. */
 typedef struct lmkv_batch {
     const int32_t* q_start;       /* DEVICE [num_req + 1], ascending from >= 0 */
     const int32_t* kv_len;        /* DEVICE [num_req] */

@@ -1338,7 +1338,6 @@ struct Plan {
     uint64_t o_bytes, ml_bytes, range_bytes, bytes;
 };
 
-constexpr int32_t kSms = 152;
 constexpr int32_t kStreamKeys = 16 * kWarps * kChunk;     // own contexts longer than this go by streams
 
 // Scores of a prefix (rows x keys x KV heads) from which its rows are taken by tiles.
@@ -1472,7 +1471,8 @@ uint64_t most_bytes(const lmkv_pool_t* pool, int32_t q_heads, int32_t num_tokens
     // the prefix's parts, by tiles (of every number of them up to the call's) and by rows
     uint64_t parts = 0, again = 0;
     if (big || prefix_len > 0) {
-        const int64_t blocks = ((int64_t)prefix_len + kBlock - 1) / kBlock + (big ? ((int64_t)max_kv_len + kBlock - 1) / kBlock : 0);
+        const int64_t blocks = ((int64_t)prefix_len + kBlock - 1) / kBlock +
+                               (big ? ((int64_t)max_kv_len + kBlock - 1) / kBlock : 0);
         const int64_t tiles = ((int64_t)num_tokens * group + kTileRows - 1) / kTileRows;
         int64_t ctas = tiles * heads;
         for (int64_t t = 1; t <= tiles && t * heads <= kMostRounds * kSms; ++t) {
@@ -1494,7 +1494,8 @@ uint64_t most_bytes(const lmkv_pool_t* pool, int32_t q_heads, int32_t num_tokens
     const int64_t warps = far ? kRowCtas * kSms * kWarps : prefix_len > 0 && max_kv_len > 0 ? kSms * kStreamWarps : 0;
     const int64_t streams = warps == 0 ? 0 : warps / heads > 0 ? warps / heads : 1;
     const int64_t own_cap = big ? kBigRows - 1 : req_rows, own_tiles = (own_cap + kRowTile - 1) / kRowTile;
-    const uint64_t own_rows = ((uint64_t)streams + (uint64_t)num_req * own_tiles) * (own_cap < kRowTile ? own_cap : kRowTile) * heads;
+    const uint64_t own_rows = ((uint64_t)streams + (uint64_t)num_req * own_tiles) *
+                              (own_cap < kRowTile ? own_cap : kRowTile) * heads;
     return (parts + own_rows) * ((uint64_t)pool->head_dim * 4 + 8) + (uint64_t)num_req * own_tiles * 8 + again;
 }
 

@@ -927,7 +927,7 @@ int weigh_typed(WeighParams& p, void* stream) {
     const int64_t heads = p.kv_heads, req = p.seqs.num_req;
     // one round of CTAs
     const int64_t unit = tiles ? kBlock : kUnit;
-    const int64_t want = (tiles ? 1 : kRowCtas) * 152 / heads, most = ((int64_t)p.seqs.max_kv_len + unit - 1) / unit * req;
+    const int64_t want = (tiles ? 1 : kRowCtas) * kSms / heads, most = ((int64_t)p.seqs.max_kv_len + unit - 1) / unit * req;
     p.splits = (int32_t)(want < 1 || most < 1 ? 1 : want > most ? most : want);
     const int64_t grid = most < 1 ? 1 : heads * p.splits;
     if (!tiles) {

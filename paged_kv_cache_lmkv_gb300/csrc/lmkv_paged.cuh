@@ -225,6 +225,8 @@ struct Elem<float> {
 };
 
 // ---- launch -------------------------------------------------------------
+constexpr int32_t kSms = 152;
+
 // Launch with programmatic stream serialization: every kernel here waits for
 // its predecessors (griddepcontrol.wait) before it touches global memory.
 template <class Kernel, class... Args>
