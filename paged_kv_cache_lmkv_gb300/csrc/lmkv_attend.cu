@@ -810,7 +810,7 @@ __device__ __noinline__ void take_row(const AttendParams& p, const Seg* segs, in
 // Bound by the turn of the two tiles: a block of 128 keys takes 2830 cycles for 256
 // rows, of which the products are 2048 of the tensor core (and of shared memory's
 // bandwidth) and the powers 1024.  (12 prompts of 65 to 400 tokens, 64 heads of 128 behind 8192
-// keys: 550 us, 1.44 PFLOP/s.)  q and the results moved in pieces side by side, as the
+// keys: 547 us, 1.45 PFLOP/s.)  q and the results moved in pieces side by side, as the
 // weights' kernel reads q, take registers from the main loop: 598 us a call for 585.
 // Few tiles (a decode step's) do not fill the SMs for long and leave the memory
 // idle that the own pages' streams are bound by: then some of the SMs' CTAs take the
