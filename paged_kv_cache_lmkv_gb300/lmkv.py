@@ -742,7 +742,9 @@ _DTYPES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
 
 class Rotary:
     """A rotary encoding (lmkv_rotary_t): inv_freq[i] = base^(-2i / rot_dim), scaled as
-    lmkv_rotary_init describes, or the given inv_freq (radians per position)."""
+    lmkv_rotary_init describes, or the given inv_freq (radians per position).  scaling: "plain",
+    "linear", "base", "bands", "yarn" (as checkpoints that name it are made) or "ramp" (between fractional
+    pairs: no checkpoint's form)."""
 
     def __init__(self, rot_dim: int, base: float = 10000.0, interleaved: bool = False,
                  scaling: str = "plain", factor: float = 1.0, low: float = 1.0, high: float = 32.0,
