@@ -86,7 +86,8 @@ typedef enum lmkv_status {
                                    memory requests: treat the context as unusable. */
     LMKV_ERR_SCRATCH_LIMIT = 8, /* host: the batch needs more than the library's built-in scratch */
     LMKV_ERR_BAD_DATA = 9,      /* device: an encoded blob is inconsistent (stream skipped) */
-    LMKV_ERR_BAD_LENGTH = 10    /* device: a length outside the bounds of its call (clamped) */
+    LMKV_ERR_BAD_LENGTH = 10,   /* device: a length outside the bounds of its call (clamped) */
+    LMKV_ERR_NO_PAGES = 11      /* device: no free page was left (the table's entry is -1) */
 } lmkv_status;
 
 /* The paged KV pool.  layer_base is a DEVICE array of num_layers DEVICE
@@ -737,6 +738,121 @@ int lmkv_evict_layer(const lmkv_pool_t* pool, int32_t layer, const int32_t* bloc
                      const float* scores, int64_t score_stride, int32_t budget, int32_t sinks,
                      int32_t recent, int32_t* keep, int32_t* new_len, float* kept_scores,
                      int64_t kept_stride, int32_t* d_status, void* stream);
+
+/* ---- The 8-bit cache ----------------------------------------------------
+ * Pages of e4m3 codes, a byte an element (pool->elem_bytes == 1), with a power
+ * of two for each page and head: an element of K or V is
+ *   code * 2^(byte - 127),   byte = scales[layer][kv][page][kv head]
+ * (E8M0 of the OCP microscaling formats; a byte of 255 is NaN).  Powers of two
+ * make a change of scale exact but for codes that leave e4m3's range below,
+ * and cost a product nothing.
+ *   scales : DEVICE array of num_layers DEVICE pointers, each to
+ *            uint8 [2][num_blocks][num_kv_heads]; NULL with a 16-bit pool
+ * A null entry is reported as BAD_POINTER.  Scales belong to whole pages:
+ * lmkv_evict_layer, which moves rows from page to page, is not for such a pool, and
+ * the gather and scatter calls move its codes alone. */
+
+/* lmkv_append_layer for models that norm each head of q and k, into 16-bit or
+ * 8-bit pages.  Of each head of q and of k,
+ *   y = x / sqrt(mean(x^2) + eps) * norm   (Zhang and Sennrich, "Root Mean
+ *   Square Layer Normalization", 2019; left out where its norm is NULL)
+ * is turned as `rotary` says (left out when NULL); all in fp32, rounded once.
+ *   dtype  : of q, k, v and q_out, LMKV_BF16 or LMKV_FP16; a 16-bit pool's own
+ *   q_norm, k_norm : DEVICE float32 [head_dim] or NULL;  eps >= 0, finite
+ * 8-bit pages: where new tokens of a head come into a page, its exponent (byte
+ * - 127) becomes the least e in -60 .. 60 with all their values within 448 *
+ * 2^e, or stays if the page holds earlier tokens of the request and theirs is larger.
+ * If it grows, earlier tokens' codes are rounded again to the new scale (repeated calls give the
+ * same codes).  Codes are value / 2^e to nearest even, saturating; a value that is not finite
+ * becomes a NaN code and does not count for e.  Slots that hold no token are left as they are.
+ * A page that two requests of the batch write to is not allowed.
+ * head_dim 64 or 128 (UNSUPPORTED otherwise).  Everything else, errors too, as
+ * lmkv_append_layer. */
+int lmkv_append_layer_normed(const lmkv_pool_t* pool, void* const* scales, int32_t dtype, int32_t layer,
+                             const lmkv_batch_t* batch, int32_t num_q_heads, const lmkv_rows_t* q,
+                             const lmkv_rows_t* k, const lmkv_rows_t* v, const lmkv_rows_t* q_out,
+                             const int64_t* positions, const lmkv_rotary_t* rotary, const float* q_norm,
+                             const float* k_norm, float eps, int32_t* d_status, void* stream);
+
+/* Attention of a batch's new tokens to their own pages, 16-bit or 8-bit, with
+ * a sliding window and sinks ("Efficient Streaming Language Models with
+ * Attention Sinks", Xiao et al., 2023): new token i of request r, cached token
+ * t = kv_len[r] - n_r + i, sees cached tokens j <= t with
+ *   j > t - window  or  j < sinks      (window == 0: all j <= t)
+ * and out and lse are those of lmkv_attend_layer over them.  Pages that no row
+ * sees any of are not read, and their table entries may be anything.
+ *   dtype : of q and out, LMKV_BF16 or LMKV_FP16; a 16-bit pool's own
+ *   workspace : as lmkv_attend_layer's, lmkv_attend_window_workspace_bytes
+ *               bytes for bounds that the call's do not exceed
+ * A token that sees nothing gets out = 0 and lse = -infinity.  A value that is
+ * not finite reaches no row that does not see it but those of other new tokens
+ * of its request.  8-bit pages: q is taken to fp16 relative to its row's largest element (below 2^-38
+ * of that it loses bits), softmax weights times the page's V scale are
+ * rounded to fp16 before they meet the codes.  The V scales that one row sees
+ * may differ by up to 2^64; pages that are further below the largest may count as nothing.
+ * INVALID_ARG for window < 0, sinks < 0, scales that do not match elem_bytes;
+ * other types, sizes and errors as lmkv_attend_layer. */
+int lmkv_attend_window_workspace_bytes(const lmkv_pool_t* pool, int32_t num_q_heads, int32_t num_tokens,
+                                       int32_t num_req, int32_t max_new, int32_t max_kv_len, uint64_t* bytes);
+
+int lmkv_attend_layer_window(const lmkv_pool_t* pool, void* const* scales, int32_t dtype, int32_t layer,
+                             const lmkv_batch_t* batch, int32_t num_q_heads, const lmkv_rows_t* q, float scale,
+                             int32_t window, int32_t sinks, const lmkv_rows_t* out, float* lse, void* workspace,
+                             uint64_t workspace_bytes, int32_t* d_status, void* stream);
+
+/* ---- Pages --------------------------------------------------------------
+ * Which pages are held, and by how many rows of block tables, lives on the
+ * DEVICE, so that a captured step can fork, grow and free:
+ *   refs : DEVICE int32 [num_blocks], 16-byte aligned; 0: free, > 0: the number of rows that
+ *          hold the page, < 0: out of these calls' reach (never given, moved or
+ *          counted)
+ * A row of `len` tokens holds the pages of its first ceil(len / block_size)
+ * columns.  Free pages are given in ascending order, row by row, so the same
+ * state gives the same pages.  All calls write refs_out (may be refs itself)
+ * and a table whose columns behind a row's pages are -1; nothing may overlap
+ * otherwise.  Pages move with all layers, K and V, and their scales (NULL: a pool
+ * without).  An entry that is out of range stays as it is (BAD_BLOCK), a length beyond the
+ * table is clamped (BAD_LENGTH).  Where no free page is left the entry is -1 (NO_PAGES).
+ *   workspace : DEVICE, 16-byte aligned, lmkv_pages_workspace_bytes bytes for at least the
+ *               call's rows; contents irrelevant, not shared with calls that may run at the same time */
+int lmkv_pages_workspace_bytes(const lmkv_pool_t* pool, int32_t rows, uint64_t* bytes);
+
+/* Copy page src[i] to page dst[i], i < n (DEVICE int32).  A dst is neither
+ * another's dst nor a src.  src[i] == dst[i] does nothing; an id out of
+ * range is skipped (BAD_BLOCK). */
+int lmkv_copy_pages(const lmkv_pool_t* pool, void* const* scales, const int32_t* src, const int32_t* dst, int32_t n,
+                    int32_t* d_status, void* stream);
+
+/* Beams, or samples, that go on from others: row i of table_out continues row
+ * parents[i] of block_table (DEVICE int32 [rows_out]; out of 0 .. rows - 1: an
+ * empty row).  Every row of block_table gives its pages back; the full pages
+ * of a parent are shared by its children; the page that is not full goes on with the first
+ * row that wants it, if nobody else holds it, and the others get a free page
+ * with a copy of its tokens (pages that this call frees among them).
+ *   kv_len : DEVICE int32 [rows];  len_out : DEVICE int32 [rows_out], written
+ *   table_out : DEVICE int32 [rows_out][max_blocks], not overlapping block_table */
+int lmkv_fork_pages(const lmkv_pool_t* pool, void* const* scales, const int32_t* block_table, int32_t max_blocks,
+                    const int32_t* kv_len, int32_t rows, const int32_t* parents, int32_t rows_out,
+                    const int32_t* refs, int32_t* table_out, int32_t* len_out, int32_t* refs_out, void* workspace,
+                    uint64_t workspace_bytes, int32_t* d_status, void* stream);
+
+/* Rows of kv_len tokens become rows of new_len tokens: pages behind give up a
+ * reference (after an eviction, or new_len = 0 of a request that has ended), pages
+ * that are missing are given, those that this call frees among them.
+ * table_out may be block_table. */
+int lmkv_resize_pages(const lmkv_pool_t* pool, const int32_t* block_table, int32_t max_blocks, const int32_t* kv_len,
+                      const int32_t* new_len, int32_t rows, const int32_t* refs, int32_t* table_out,
+                      int32_t* refs_out, void* workspace, uint64_t workspace_bytes, int32_t* d_status, void* stream);
+
+/* Close the gaps: the highest held pages move into the lowest free ones until
+ * all held pages lie before all free ones (but for pages of refs < 0, which stay).
+ *   page_map : DEVICE int32 [num_blocks], written: where each page is now (tables
+ *              that are not given can follow it)
+ * table_out may be block_table: entries of the rows' pages follow page_map. */
+int lmkv_compact_pages(const lmkv_pool_t* pool, void* const* scales, const int32_t* block_table, int32_t max_blocks,
+                       const int32_t* kv_len, int32_t rows, const int32_t* refs, int32_t* table_out,
+                       int32_t* refs_out, int32_t* page_map, void* workspace, uint64_t workspace_bytes,
+                       int32_t* d_status, void* stream);
 
 /* Human-readable name of a status code (static storage). */
 const char* lmkv_status_string(int status);

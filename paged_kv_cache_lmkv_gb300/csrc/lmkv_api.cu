@@ -1053,6 +1053,7 @@ const char* lmkv_status_string(int status) {
         case LMKV_ERR_SCRATCH_LIMIT: return "batch needs more than the built-in staging area";
         case LMKV_ERR_BAD_DATA: return "encoded blob inconsistent with its size (stream skipped)";
         case LMKV_ERR_BAD_LENGTH: return "length outside the bounds of its call (clamped)";
+        case LMKV_ERR_NO_PAGES: return "no free page left";
         default: return "unknown status";
     }
 }

@@ -1,0 +1,1380 @@
+// lmkv_window.cu -- attention of a batch's new tokens to their own pages, of 16
+// or 8 bits, with a sliding window and sinks.
+//
+// With y_j = scale * q.k_j + log v_scale_j (powers of 2), and codes c_j of v,
+//   o = sum_j 2^(y_j) c_j / sum_j 2^(y_j) / v_scale_j,
+// which splits over any partition of the keys: a part keeps what its weights are
+// relative to (m), l = sum 2^(y - m) / v_scale and sum 2^(y - m) c; parts are joined by
+//   M = max m,  l = sum l 2^(m - M),  o = sum o 2^(m - M) / l
+// (the running maximum and sum of Milakov and Gimelshein, "Online normalizer
+// calculation for softmax", 2018).  So a page's scale of v costs its keys an
+// addition in the exponent, and its scale of k a factor of the score; codes go to the products as they are.
+// (The weights' product with v is of fp16, whose range y's maximum makes good use of whatever the scales are.)
+// 16-bit pages are the same with scales of 1.
+#include "lmkv_blocks.cuh"
+#include "lmkv_cache8.cuh"
+
+#include <cmath>
+
+namespace {
+
+using namespace lmkv_paged;
+using namespace lmkv_mma;
+using namespace lmkv_cache8;
+
+struct Rows {
+    uint8_t* data;
+    int64_t token_stride;
+    int64_t head_stride;
+    static Rows of(const lmkv_rows_t* x) {
+        return Rows{static_cast<uint8_t*>(x->data), x->token_stride, x->head_stride};
+    }
+    template <class T>
+    __device__ __forceinline__ T* row(int32_t token, int32_t head) const {
+        return reinterpret_cast<T*>(data) + (int64_t)token * token_stride + (int64_t)head * head_stride;
+    }
+};
+
+// A request whose rows per KV head (new tokens x heads of the group) reach
+// big_rows goes by the tile kernel, the others by streams.
+struct WindowParams {
+    Layer layer;
+    Seqs seqs;
+    Scales scales;
+    Rows q, out;
+    float* lse;
+    int32_t* status;
+    // Partial results: m (powers of 2), l and the weighted sum of codes.  Of the tiles
+    // [part][row], row = token * q_heads + head; then of the streams [stream + row tile of the batch's
+    // requests][row of the tile][KV head] (a stream's and a tile's number rise from
+    // part to part, so their sum names it).
+    float* part_o;
+    float2* part_ml;
+    int2* own_range;        // [request][row tile]: first and last stream that has some of it
+    float scale_log2;       // of |scale|
+    int32_t scale_sign;     // -1, 0 or 1
+    int32_t window;         // INT32_MAX: none
+    int32_t sinks;
+    int32_t q_heads, kv_heads;
+    int32_t rows;           // num_tokens * q_heads
+    int32_t big_rows;       // INT32_MAX: no tiles
+    int32_t own_cap;        // rows of a request that streams take at most
+    int32_t own_tiles;      // row tiles of that many rows
+    int32_t tile_rows;      // rows of a tile
+    int32_t streams;        // warps that share the keys of a KV head
+    int32_t slots;          // tile kernel: row tiles that there may be
+    int32_t parts;          // its parts of the keys
+    int64_t own_base;       // rows of partial results before the streams'
+    bool q_pairs;           // q rows are 4-byte aligned
+    bool q_vec, out_vec;    // 16-byte aligned
+    FastDiv by_group;
+
+    __device__ __forceinline__ int64_t own_part(int32_t stream, int32_t tile_no, int32_t row, int32_t h) const {
+        return own_base + (((int64_t)stream + tile_no) * tile_rows + row) * kv_heads + h;
+    }
+};
+
+constexpr float kLn2 = 0.69314718055994530942f, kLog2e = 1.44269504088896340736f;
+// Weights are relative to 2^kBelow less than a maximum that may lag by 2^kLag, so they are 2^14
+// at most, and those of 2^-20 of the largest are still normal fp16 numbers.
+constexpr float kBelow = 6.f, kLag = 8.f;
+
+// The keys that some row of tokens t0 .. t1 (cached numbers) sees, in units of
+// kUnit keys: first the sinks' units, then the window's.
+struct Seen {
+    int32_t first_units;      // units 0 .. first_units - 1
+    int32_t then;             // number of the unit after them
+    int32_t units;            // in all
+    int32_t sink_end, lo, end;      // keys [0, sink_end) and [lo, end)
+
+    __device__ __forceinline__ int32_t unit(int32_t i) const { return i < first_units ? i : i - first_units + then; }
+    __device__ __forceinline__ bool some(int32_t j) const { return j < end && (j < sink_end || j >= lo); }
+};
+__device__ __forceinline__ Seen seen_by(const WindowParams& p, int32_t t0, int32_t t1, int32_t unit) {
+    Seen s;
+    s.end = max(t1 + 1, 0);
+    s.lo = p.window == INT32_MAX ? 0 : max(t0 + 1 - p.window, 0);
+    s.sink_end = min(p.sinks, s.end);
+    if (s.lo <= s.sink_end) s.lo = s.sink_end = 0;      // one stretch
+    s.first_units = (s.sink_end + unit - 1) / unit;
+    s.then = max(s.lo / unit, s.first_units);
+    s.units = s.first_units + max((s.end + unit - 1) / unit - s.then, 0);
+    return s;
+}
+
+// ---- streams ------------------------------------------------------------
+
+constexpr int kWarps = 4;
+constexpr int kChunk = 16;        // keys a warp takes at a time
+
+// How KV rows of D elements lie in shared memory and come out as fragments.
+// A chunk's 16 rows of K are the first operand of S^T = K q^T, and V^T that of O^T =
+// V^T P^T, so that up to eight queries are the products' narrow side.  Either product's
+// order of elements is free: thread (g, c) = (lane / 4, lane % 4) takes K's 16-byte
+// pieces c, c + 4, .. of rows tau(g) and tau(g) + 8 whole, and D / 8 neighbouring elements of V's
+// rows c, c + 4, c + 8, c + 12, with tau(g) = g / 2 + 4 (g % 2) the row that the weights' fragment has
+// there.  Pieces are exchanged within a row so that neither read meets a bank twice.
+template <class KV, int D>
+struct Fragments {
+    static constexpr bool kCodes = sizeof(KV) == 1;
+    static constexpr int kRowBytes = D * (int)sizeof(KV);
+    static constexpr int kPieces = kRowBytes / 16;
+    static constexpr int kTileBytes = kChunk * kRowBytes;
+    static constexpr int kPer = 16 / (int)sizeof(KV);     // elements of a piece
+    static constexpr int kSteps = D / 16;
+
+    static __device__ __forceinline__ uint32_t place(int row, int piece) {
+        if constexpr (kRowBytes >= 128) {
+            return (uint32_t)(row * kRowBytes + ((piece ^ (((row & 3) << 1) ^ (row & 4))) << 4));
+        } else {        // two rows in 128 bytes
+            return (uint32_t)((row ^ ((row >> 2) & 1)) * kRowBytes + ((piece ^ (row & 2)) << 4));
+        }
+    }
+    // The element of V that row `half` (0, 1) of tile j of the product is, of lane group g.
+    static __device__ __forceinline__ int element(int j, int g) {
+        if constexpr (!kCodes && D == 128) return (j >> 2) * 64 + g * 8 + 2 * (j & 3);
+        return g * (D / 8) + 2 * j;
+    }
+};
+
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
+// The 8 x 8 matrix of 16-bit elements whose row lane / 4 has this word at columns 2 (lane % 4), transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t w) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(w));
+    return r;
+}
+
+// What a chunk is besides its rows: which of its keys some row sees, and the scale bytes
+// (k, v of row tau(g), then of row tau(g) + 8).
+struct ChunkInfo {
+    uint32_t mask, scales;
+};
+
+// Copies chunks of 16 keys' rows of one head, K and V, into a warp's ring.
+template <class KV, int D>
+struct ChunkLoad {
+    using F = Fragments<KV, D>;
+    static constexpr int kRowsPer = 32 / F::kPieces > 16 ? 16 : 32 / F::kPieces;     // rows of a warp-wide copy
+    const WindowParams& p;
+    const int32_t* table;
+    const uint8_t* base;
+    const uint8_t* scale_base;
+    int64_t half_bytes;
+    uint32_t row_bytes;
+    int32_t h;
+    bool runs;
+    Seen seen;
+    int32_t next_blk;
+
+    __device__ __forceinline__ ChunkLoad(const WindowParams& wp, const int32_t* t, const uint8_t* layer_base,
+                                         const uint8_t* scales, int32_t head, const Seen& s)
+        : p(wp), table(t), base(layer_base), scale_base(scales), half_bytes(wp.layer.half_bytes()),
+          row_bytes((uint32_t)wp.layer.row_bytes), h(head), runs(wp.layer.block_size % kChunk == 0), seen(s), next_blk(-1) {}
+    __device__ __forceinline__ void lookup(int32_t i, int32_t n) {
+        next_blk = runs && i < n ? table[p.layer.column(seen.unit(i) * kChunk)] : -1;
+    }
+    __device__ __forceinline__ uint32_t bytes_of(int64_t blk) const {
+        if constexpr (!F::kCodes) return 0;
+        return (uint32_t)scale_base[p.scales.at(0, blk, h)] | ((uint32_t)scale_base[p.scales.at(1, blk, h)] << 8);
+    }
+    // Unit i (looked up before) to dst; then looks up the next, of n.
+    __device__ __forceinline__ ChunkInfo copy(int32_t i, uint32_t dst, int32_t n) {
+        const int lane = threadIdx.x & 31, piece = lane % F::kPieces, rsub = lane / F::kPieces;
+        const int32_t blk = next_blk, key0 = seen.unit(i) * kChunk;
+        lookup(i + 1, n);
+        const uint8_t* const mine = base + (int64_t)h * F::kRowBytes + piece * 16;
+        const bool whole = key0 + kChunk <= seen.end && (key0 >= seen.lo || key0 + kChunk <= seen.sink_end);
+        if (runs && whole && blk >= 0 && blk < p.layer.num_blocks) {
+            const uint8_t* src = mine + ((uint64_t)p.layer.row_of(blk, key0, p.layer.column(key0)) + rsub) * row_bytes;
+#pragma unroll
+            for (int r = 0; r < kChunk; r += kRowsPer) {
+                const uint32_t at = dst + F::place(r + rsub, piece);
+                cp_async16(at, src + r * row_bytes);
+                cp_async16(at + F::kTileBytes, src + r * row_bytes + half_bytes);
+            }
+            const uint32_t s = bytes_of(blk);
+            return ChunkInfo{0xFFFFu, s | (s << 16)};
+        }
+        const int32_t tok = key0 + (lane & 15);
+        uint32_t row = Layer::kNoRow;
+        int32_t b = 0;
+        if (seen.some(tok)) {
+            const uint32_t col = p.layer.column(tok);
+            b = table[col];
+            row = p.layer.row_of(b, tok, col);
+            if (row == Layer::kNoRow && lane < 16) report(p.status, LMKV_ERR_BAD_BLOCK);
+        }
+        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, row != Layer::kNoRow) & 0xFFFFu;
+#pragma unroll
+        for (int r = 0; r < kChunk; r += kRowsPer) {
+            const uint32_t from = __shfl_sync(0xFFFFFFFFu, row, r + rsub);
+            const bool on = from != Layer::kNoRow;
+            const uint32_t at = dst + F::place(r + rsub, piece);
+            const uint8_t* const src = mine + (on ? (uint64_t)from * row_bytes : 0);
+            cp_async16(at, src, on);
+            cp_async16(at + F::kTileBytes, src + (on ? half_bytes : 0), on);
+        }
+        uint32_t s = 0x7F7F7F7Fu;
+        if constexpr (F::kCodes) {
+            const int g = lane >> 2, ta = (g >> 1) + 4 * (g & 1);
+            const int32_t ba = __shfl_sync(0xFFFFFFFFu, b, ta), bb = __shfl_sync(0xFFFFFFFFu, b, ta + 8);
+            const uint32_t sa = (mask >> ta) & 1 ? bytes_of(ba) : 0x7F7Fu, sb = (mask >> (ta + 8)) & 1 ? bytes_of(bb) : 0x7F7Fu;
+            s = sa | (sb << 16);
+        }
+        return ChunkInfo{mask, s};
+    }
+};
+
+// One warp's 8 * NT rows against chunks of 16 keys.  Thread (g, c) holds of every tile of 8
+// queries those numbered 2 c and 2 c + 1, and D / 8 elements of their output.
+template <class T, class KV, int D, int NT>
+struct StreamRows {
+    using F = Fragments<KV, D>;
+    using M = typename std::conditional<F::kCodes, __half, T>::type;       // of the products
+    uint32_t qf[NT][F::kSteps][2];
+    float o[NT][F::kSteps][4];
+    float m[NT][2], l[NT][2];      // the maximum (lagging); sums
+    float factor[NT][2];           // of raw scores
+    int32_t tok[NT][2];            // cached number of the row's token; -1: no row
+    int32_t t_first, t_last;       // of the tile's rows
+
+    // Rows row0 .. row0 + nrows - 1 of the request (token * group + head of the group).
+    __device__ __forceinline__ void begin(const WindowParams& p, const Req& r, int32_t h, int32_t row0, int32_t nrows) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+        const int32_t group = (int32_t)p.by_group.d;
+        const int32_t old = r.len - r.n;
+        t_first = old + (int32_t)p.by_group.div((uint32_t)row0);
+        t_last = old + (int32_t)p.by_group.div((uint32_t)(row0 + min(nrows, NT * 8) - 1));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int32_t rr = nt * 8 + g;
+            const bool on = rr < nrows;
+            const int32_t i = (int32_t)p.by_group.div((uint32_t)(row0 + (on ? rr : 0)));
+            const T* src = p.q.row<T>(r.q0 + i, h * group + (row0 + (on ? rr : 0) - i * group));
+#pragma unroll
+            for (int s = 0; s < F::kSteps; ++s) {
+                constexpr int kStepsPer = F::kPer / 4;
+                const int e = (c + 4 * (s / kStepsPer)) * F::kPer + 4 * (s % kStepsPer);
+                qf[nt][s][0] = on ? load_pair(src + e, p.q_pairs) : 0u;
+                qf[nt][s][1] = on ? load_pair(src + e + 2, p.q_pairs) : 0u;
+            }
+        }
+        const uint32_t flip = p.scale_sign < 0 ? 0x80008000u : 0u, all = p.scale_sign == 0 ? 0u : ~0u;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float f = p.scale_log2;
+#pragma unroll
+            for (int s = 0; s < F::kSteps; ++s)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) qf[nt][s][k] = (qf[nt][s][k] ^ flip) & all;
+            if constexpr (F::kCodes) {
+                // the row's q as fp16 with its largest element between 2^14 and 2^15: exact but for elements
+                // below 2^-28 of that
+                float top = 0.f;
+#pragma unroll
+                for (int s = 0; s < F::kSteps; ++s)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const T* const x = reinterpret_cast<const T*>(&qf[nt][s][k]);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float a = fabsf(Elem<T>::to_float(x[i]));
+                            if (a < INFINITY) top = fmaxf(top, a);
+                        }
+                    }
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                const int e = top > 0.f ? max((int)(__float_as_uint(top) >> 23) - 127, -100) : 0;
+                const float by = power_of_two(14 - e);
+                f *= power_of_two(e - 14);
+#pragma unroll
+                for (int s = 0; s < F::kSteps; ++s)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const T* const x = reinterpret_cast<const T*>(&qf[nt][s][k]);
+                        qf[nt][s][k] = Elem<__half>::pack(Elem<T>::to_float(x[0]) * by, Elem<T>::to_float(x[1]) * by);
+                    }
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                factor[nt][k] = __shfl_sync(0xFFFFFFFFu, f, (2 * c + k) * 4);
+                const int32_t rr = nt * 8 + 2 * c + k;
+                tok[nt][k] = rr < nrows ? old + (int32_t)p.by_group.div((uint32_t)(row0 + rr)) : -1;
+                m[nt][k] = -INFINITY;
+                l[nt][k] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < F::kSteps; ++j) o[nt][j][0] = o[nt][j][1] = o[nt][j][2] = o[nt][j][3] = 0.f;
+        }
+    }
+
+    // The chunk at key0 whose K rows are at kt and V rows behind them.
+    __device__ __forceinline__ void chunk(const WindowParams& p, uint32_t kt, int32_t key0, ChunkInfo info) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+        const int ta = (g >> 1) + 4 * (g & 1);
+        float sc[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+#pragma unroll
+        for (int i = 0; i < F::kPieces / 4; ++i) {
+            const uint4 a = lds128(kt + F::place(ta, c + 4 * i)), b = lds128(kt + F::place(ta + 8, c + 4 * i));
+            const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+            if constexpr (F::kCodes) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const uint32_t k[4] = {codes_to_half2((uint16_t)aw[w]), codes_to_half2((uint16_t)bw[w]),
+                                           codes_to_half2((uint16_t)(aw[w] >> 16)), codes_to_half2((uint16_t)(bw[w] >> 16))};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma16816<M>(sc[nt], k, qf[nt][i * 4 + w][0], qf[nt][i * 4 + w][1]);
+                }
+            } else {
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const uint32_t k[4] = {aw[2 * w], bw[2 * w], aw[2 * w + 1], bw[2 * w + 1]};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma16816<M>(sc[nt], k, qf[nt][i * 2 + w][0], qf[nt][i * 2 + w][1]);
+                }
+            }
+        }
+        // scores to powers of 2
+        float k_scale[2] = {1.f, 1.f}, v_power[2] = {0.f, 0.f}, v_back[2] = {1.f, 1.f};
+        if constexpr (F::kCodes) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int kb = (int)((info.scales >> (16 * i)) & 0xFF), vb = (int)((info.scales >> (16 * i + 8)) & 0xFF);
+                k_scale[i] = power_of_two(kb - 127);
+                v_power[i] = vb == 255 ? NAN : (float)(vb - 127);
+                v_back[i] = power_of_two(127 - vb);
+            }
+        }
+        const bool whole = info.mask == 0xFFFFu && key0 + kChunk - 1 <= t_first &&
+                           (p.window == INT32_MAX || key0 > t_last - p.window || key0 + kChunk <= p.sinks);
+        bool grow = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int k = i & 1, row = i >> 1;
+                float& x = sc[nt][i];
+                x = F::kCodes ? fmaf(x, factor[nt][k] * k_scale[row], v_power[row]) : x * factor[nt][k];
+                if (!whole) {
+                    const int32_t j = key0 + ta + 8 * row, t = tok[nt][k];
+                    const bool see = ((info.mask >> (ta + 8 * row)) & 1) && j <= t &&
+                                     (p.window == INT32_MAX || j > t - p.window || j < p.sinks);
+                    if (!see) x = -INFINITY;
+                }
+                grow = grow || x > m[nt][k] + kLag;
+            }
+        if (__any_sync(0xFFFFFFFFu, grow)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float top = fmaxf(sc[nt][k], sc[nt][2 + k]);
+                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
+                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+                    const float mn = fmaxf(m[nt][k], top);
+                    const float f = mn == m[nt][k] ? 1.f : exp2_fast(m[nt][k] - mn);
+                    m[nt][k] = mn;
+                    l[nt][k] *= f;
+#pragma unroll
+                    for (int j = 0; j < F::kSteps; ++j) {
+                        o[nt][j][k] *= f;
+                        o[nt][j][2 + k] *= f;
+                    }
+                }
+        }
+        uint32_t pf[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float top = m[nt][i & 1];
+                w[i] = exp2_fast(sc[nt][i] - (top == -INFINITY ? 0.f : top - kBelow));
+                l[nt][i & 1] = F::kCodes ? fmaf(w[i], v_back[i >> 1], l[nt][i & 1]) : l[nt][i & 1] + w[i];
+            }
+            // weights are rounded to 16 bits for the product with V, the sum takes them whole
+            pf[nt][0] = transposed(Elem<M>::pack(w[0], w[1]));
+            pf[nt][1] = transposed(Elem<M>::pack(w[2], w[3]));
+        }
+        const uint32_t vt = kt + F::kTileBytes;
+        auto product = [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+            const uint32_t a[4] = {a0, a1, a2, a3};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816<M>(o[nt][j], a, pf[nt][0], pf[nt][1]);
+        };
+        if constexpr (F::kCodes) {
+            constexpr int kWords = D / 32;
+            uint32_t v[4][kWords];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (D == 128) {
+                    const uint4 x = lds128(vt + F::place(c + 4 * i, g));
+                    v[i][0] = x.x, v[i][1] = x.y, v[i][kWords - 2] = x.z, v[i][kWords - 1] = x.w;
+                } else {
+                    const uint2 x = lds64(vt + F::place(c + 4 * i, g >> 1) + (g & 1) * 8);
+                    v[i][0] = x.x, v[i][1] = x.y;
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const uint32_t sel = u ? 0x7362u : 0x5140u;
+                    const uint32_t x = prmt(v[0][w], v[1][w], sel), y = prmt(v[2][w], v[3][w], sel);
+                    product(2 * w + u, codes_to_half2((uint16_t)x), codes_to_half2((uint16_t)(x >> 16)),
+                            codes_to_half2((uint16_t)y), codes_to_half2((uint16_t)(y >> 16)));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int piece = 0; piece < D / 64; ++piece) {
+                uint32_t v[4][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 x = lds128(vt + F::place(c + 4 * i, g + 8 * piece));
+                    v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+                }
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                    product(piece * 4 + w, prmt(v[0][w], v[1][w], 0x5410), prmt(v[0][w], v[1][w], 0x7632),
+                            prmt(v[2][w], v[3][w], 0x5410), prmt(v[2][w], v[3][w], 0x7632));
+            }
+        }
+    }
+
+    // This stream's part of the rows.
+    __device__ __forceinline__ void end(const WindowParams& p, int32_t stream, int32_t tile_no, int32_t h, int32_t nrows) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float s = l[nt][k];
+                s += __shfl_xor_sync(0xFFFFFFFFu, s, 4);
+                s += __shfl_xor_sync(0xFFFFFFFFu, s, 8);
+                s += __shfl_xor_sync(0xFFFFFFFFu, s, 16);
+                const int32_t rr = nt * 8 + 2 * c + k;
+                if (rr >= nrows) continue;
+                const int64_t at = p.own_part(stream, tile_no, rr, h);
+                if (g == 0) p.part_ml[at] = make_float2(m[nt][k] == -INFINITY ? -INFINITY : m[nt][k] - kBelow, s);
+                float* const row = p.part_o + at * D;
+#pragma unroll
+                for (int j = 0; j < F::kSteps; j += 2)
+                    *reinterpret_cast<float4*>(row + F::element(j, g)) =
+                        make_float4(o[nt][j][k], o[nt][j][2 + k], o[nt][j + 1][k], o[nt][j + 1][2 + k]);
+            }
+    }
+};
+
+template <class KV, int D>
+struct StreamShape {
+    static constexpr int kTile = Fragments<KV, D>::kTileBytes;             // 1, 2 or 4 KB
+    static constexpr int kStages = kTile >= 4096 ? 2 : kTile >= 2048 ? 3 : 6;
+    static constexpr int kWarpBytes = kStages * 2 * kTile;
+    static constexpr int kSmem = kWarps * kWarpBytes;
+    static constexpr int kCtas = kTile >= 4096 ? 3 : 4;                    // an SM
+};
+template <class KV, int D, int NT>
+constexpr int stream_ctas() {
+    return NT > 1 ? 3 : StreamShape<KV, D>::kCtas;
+}
+
+// The chunks of all small requests' row tiles, one after the other, are shared
+// equally among warps, whatever the lengths are; a warp runs through its share by itself, with
+// no barrier, a ring of its own in shared memory filled by cp.async, and leaves a partial result for each row
+// tile that it had some of.  Stream s of KV head h is warp s * kv_heads + h: the heads' warps of the same tokens run
+// side by side and read the same pages' rows.  Bound by the bytes of the pages.
+template <class T, class KV, int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32, stream_ctas<KV, D, NT>())
+window_streams_kernel(const __grid_constant__ WindowParams p) {
+    using X = StreamRows<T, KV, D, NT>;
+    using F = Fragments<KV, D>;
+    using Sh = StreamShape<KV, D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t worker = blockIdx.x * kWarps + warp, stream = worker / p.kv_heads, h = worker - stream * p.kv_heads;
+    if (stream >= p.streams) return;
+    const uint32_t ring = smem_u32(smem) + warp * Sh::kWarpBytes;
+    const int32_t group = (int32_t)p.by_group.d;
+    const uint8_t* const base = p.layer.base();
+    const uint8_t* const scales = F::kCodes ? p.scales.base() : nullptr;
+    const bool there = base != nullptr && (!F::kCodes || scales != nullptr);
+    if (!there && worker == 0 && lane == 0) report(p.status, LMKV_ERR_BAD_POINTER);
+    auto tiles_of = [&](const Req& r) {
+        const int32_t n = r.n * group;
+        return n >= p.big_rows ? 0 : (n + NT * 8 - 1) / (NT * 8);
+    };
+    auto seen_of = [&](const Req& r, int32_t tile) {
+        const int32_t old = r.len - r.n, row0 = tile * NT * 8, row1 = min(row0 + NT * 8, r.n * group) - 1;
+        return seen_by(p, old + (int32_t)p.by_group.div((uint32_t)row0), old + (int32_t)p.by_group.div((uint32_t)row1), kChunk);
+    };
+    // The tiles of a request see nearly the same keys: its units are the last tile's, which are at least as many.
+    auto units_of = [&](const Req& r, int32_t tiles) {
+        int32_t most = 0;
+        if (tiles > 0) most = seen_of(r, tiles - 1).units;
+        for (int32_t i = 0; i + 1 < tiles; ++i) most = max(most, seen_of(r, i).units);
+        return most;
+    };
+    Share share = find_share(p.seqs.num_req, stream, p.streams, [&](int32_t i) -> int64_t {
+        const Req r = load_req(p.seqs, i);
+        if (!r.ok) report(p.status, LMKV_ERR_BAD_LENGTH);
+        const int32_t tiles = tiles_of(r);
+        return (int64_t)tiles * units_of(r, tiles);
+    });
+    X x;
+    while (share.n > 0 && share.r < p.seqs.num_req) {
+        const Req r = load_req(p.seqs, share.r);
+        const int32_t tiles = tiles_of(r), units = units_of(r, tiles);
+        const int32_t tile = units > 0 ? (int32_t)(share.first / units) : 0;
+        if (units == 0 || tile >= tiles) {
+            ++share.r;
+            share.first = 0;
+            continue;
+        }
+        const int32_t u0 = (int32_t)(share.first - (int64_t)tile * units);
+        const int32_t n = (int32_t)min((int64_t)(units - u0), share.n);
+        share.first += n;
+        share.n -= n;
+        const int32_t tile_no = share.r * p.own_tiles + tile, row0 = tile * NT * 8, nrows = r.n * group - row0;
+        if (h == 0 && lane == 0) {
+            if (u0 == 0) p.own_range[tile_no].x = stream;
+            if (u0 + n == units) p.own_range[tile_no].y = stream;
+        }
+        const Seen seen = seen_of(r, tile);
+        const int32_t u1 = there ? min(u0 + n, seen.units) : u0;
+        ChunkLoad<KV, D> load(p, p.seqs.table + (int64_t)share.r * p.seqs.table_stride, base, scales, h, seen);
+        ChunkInfo info[Sh::kStages];
+        auto fill = [&](int32_t u) { return load.copy(u, ring + (u - u0) % Sh::kStages * (2 * F::kTileBytes), u1); };
+        __syncwarp();
+        load.lookup(u0, u1);
+#pragma unroll
+        for (int s = 0; s < Sh::kStages - 1; ++s) {
+            info[s] = u0 + s < u1 ? fill(u0 + s) : ChunkInfo{0, 0};
+            cp_commit();
+        }
+        x.begin(p, r, h, row0, nrows);
+        for (int32_t b = u0; b < u1; b += Sh::kStages) {
+#pragma unroll
+            for (int s = 0; s < Sh::kStages; ++s) {
+                const int32_t u = b + s;
+                if (u >= u1) break;
+                __syncwarp();      // the stage filled next was read by every lane
+                constexpr int kAhead = Sh::kStages - 1;
+                info[(s + kAhead) % Sh::kStages] = u + kAhead < u1 ? fill(u + kAhead) : ChunkInfo{0, 0};
+                cp_commit();
+                cp_wait<kAhead>();
+                __syncwarp();
+                x.chunk(p, ring + s * (2 * F::kTileBytes), seen.unit(u) * kChunk, info[s]);
+            }
+        }
+        cp_wait<0>();
+        x.end(p, stream, tile_no, h, nrows);
+    }
+}
+
+// Joins the parts of rows that have them, a warp a row: of the small requests' rows
+// (kTiles false: a stream's parts each) or of the big ones' (the tile kernel's parts).
+template <class T, int D, bool kTiles>
+__global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant__ WindowParams p) {
+    constexpr int kPer = D / 32;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int32_t group = (int32_t)p.by_group.d;
+    int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    int32_t tok, head, parts;
+    int64_t first, stride;
+    if constexpr (kTiles) {
+        if (i >= p.rows) return;
+        tok = (int32_t)(i / p.q_heads), head = (int32_t)(i - (int64_t)tok * p.q_heads);
+        const Req q = load_req(p.seqs, find_request(p.seqs.num_req, tok, [&](int32_t k) { return p.seqs.q_start[k]; }));
+        if (tok < q.q0 || tok >= q.q0 + q.n || q.n * group < p.big_rows) return;
+        first = i, stride = p.rows, parts = p.parts;
+    } else {
+        if (i >= (int64_t)p.seqs.num_req * p.own_cap * p.kv_heads) return;
+        const int32_t h = (int32_t)(i % p.kv_heads);
+        i /= p.kv_heads;
+        const int32_t r = (int32_t)(i / p.own_cap), row = (int32_t)(i % p.own_cap);
+        const Req q = load_req(p.seqs, r);
+        if (row >= q.n * group || q.n * group >= p.big_rows) return;
+        const int32_t n = (int32_t)p.by_group.div((uint32_t)row);
+        tok = q.q0 + n, head = h * group + (row - n * group);
+        // streams g, g + 1, .. have some of the row's tile (clamped: lengths that change while the call
+        // runs give a wrong sum, not a wild address); a request of no keys has none
+        const int32_t tile_no = r * p.own_tiles + row / p.tile_rows;
+        int32_t g = 0;
+        parts = 0;
+        if (q.len > 0) {
+            const int2 range = p.own_range[tile_no];
+            g = min(max(range.x, 0), p.streams - 1);
+            parts = min(max(range.y, g), p.streams - 1) - g + 1;
+        }
+        first = p.own_part(g, tile_no, row % p.tile_rows, h);
+        stride = (int64_t)p.tile_rows * p.kv_heads;
+    }
+    // m and l of 32 parts at a time, one a lane; then the parts' sums, whose loads
+    // do not wait for one another
+    float top = -INFINITY, sum = 0.f, acc[kPer] = {};
+    for (int32_t s0 = 0; s0 < parts; s0 += 32) {
+        const int32_t n = min(32, parts - s0);
+        const float2 v = lane < n ? p.part_ml[first + (s0 + lane) * stride] : make_float2(-INFINITY, 0.f);
+        float mn = v.x;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, d));
+        mn = fmaxf(mn, top);
+        const float mu = mn == -INFINITY ? 0.f : mn;
+        const float f = exp2_fast(v.x - mu), before = exp2_fast(top - mu);
+        top = mn;
+        float l = v.y * f;             // (a NaN stays one)
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+        sum = sum * before + l;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) acc[k] *= before;
+        constexpr int kAhead = 8;
+        for (int32_t s = 0; s < n; s += kAhead) {
+            float x[kAhead][kPer];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const float* src = p.part_o + (first + min(s0 + s + u, parts - 1) * stride) * D + lane * kPer;
+                if constexpr (kPer == 4) *reinterpret_cast<float4*>(x[u]) = *reinterpret_cast<const float4*>(src);
+                else *reinterpret_cast<float2*>(x[u]) = *reinterpret_cast<const float2*>(src);
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const float fs = __shfl_sync(0xFFFFFFFFu, f, (s + u) & 31);
+                if (s + u < n && fs != 0.f) {        // (a part of no keys has written no sums)
+#pragma unroll
+                    for (int k = 0; k < kPer; ++k) acc[k] += x[u][k] * fs;
+                }
+            }
+        }
+    }
+    const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+    T* dst = p.out.row<T>(tok, head) + lane * kPer;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) dst[k] = Elem<T>::from_float(acc[k] * inv);
+    if (lane == 0 && p.lse != nullptr)
+        p.lse[(int64_t)tok * p.q_heads + head] = ((top == -INFINITY ? 0.f : top) + log2f(sum)) * kLn2;
+}
+
+// ---- tiles of 128 rows on the tensor core -------------------------------
+
+using namespace lmkv_tc;
+
+constexpr int kTileRows = 256;        // two tiles of 128 rows share every K and V block
+constexpr int kLoaders = 3;           // warps that bring K and V
+constexpr int kTileThreads = (8 + kLoaders + 1) * 32;
+constexpr int kUnits = kBlock / kChunk;         // of 16 keys, in a block
+constexpr int kInfoSlots = 8;
+
+template <int D>
+struct WindowTile {
+    static constexpr int kHalfBytes = BlockShape<D>::kHalfBytes;
+    static constexpr int kStageBytes = BlockShape<D>::kBytes;      // 128 rows of K, V or q in 16 bits
+    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr int kSmem = (2 + kStages) * kStageBytes;
+};
+
+// Rows of one request, (token, head of the group) in token order, 256 to a CTA,
+// against the keys that they see, in blocks of 128.  Products and powers are both near their limits, so the two
+// tiles of 128 rows take turns: while the tensor core works on one tile's
+// weights x V and next q x K, the other tile's softmax runs.
+//   warps 0-3, 4-7   softmax of tile 0, 1: a thread holds a row.  Scores come
+//                    from tensor memory, weights go back over them as the next
+//                    product's first operand; the output stays in tensor memory until the end.
+//   warps 8-10       K and V in units of 16 rows (one page's) into a ring in shared memory that
+//                    both tiles read: codes through registers, where they become fp16, 16-bit rows by cp.async
+//   warp 11          one thread issues every product
+// A unit's scales are the same for its 16 keys: a factor and an addend of the exponent's multiply-add.
+// Tensor memory: scores of tile 0, 1 at columns 0, 128; outputs at 256, 384.
+template <class T, class KV, int D>
+__global__ void __launch_bounds__(kTileThreads, 1)
+window_tiles_kernel(const __grid_constant__ WindowParams p) {
+    using S = WindowTile<D>;
+    constexpr bool kCodes = sizeof(KV) == 1;
+    using M = typename std::conditional<kCodes, __half, T>::type;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ uint64_t bars[2 * S::kStages + 8];
+    __shared__ uint32_t tmem_base;
+    __shared__ int gave_up;
+    __shared__ int32_t place[2];
+    __shared__ uint32_t infos[kInfoSlots][kUnits];       // which of a unit's keys there are, K's and V's scale bytes
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t full = smem_u32(bars), empty = full + 8 * S::kStages, s_full = empty + 8 * S::kStages,
+                   p_ready = s_full + 16, o_full = p_ready + 32;
+    const uint32_t q_smem = smem_u32(smem), kv_smem = q_smem + 2 * S::kStageBytes;
+    if (tid == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(full + 8 * i, kCodes ? kUnits : kUnits * 33);
+            mbar_init(empty + 8 * i, 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(s_full + 8 * t, 1);
+            mbar_init(p_ready + 16 * t, 4);
+            mbar_init(p_ready + 16 * t + 8, 4);
+            mbar_init(o_full + 8 * t, 1);
+        }
+        gave_up = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 8 + kLoaders) tmem_alloc<512>(smem_u32(&tmem_base));
+    pdl_wait();
+    // the last row tiles of a request see the most keys: they begin first
+    const int32_t group = (int32_t)p.by_group.d;
+    const int32_t h = blockIdx.x % p.kv_heads;
+    const int32_t x = blockIdx.x / p.kv_heads, slot = p.slots - 1 - x % p.slots, part = x / p.slots;
+    if (warp == 0) {
+        // slots q_start[r] * group / 256 + r and on are request r's row tiles
+        auto key = [&](int32_t i) { return (int32_t)((int64_t)max(p.seqs.q_start[i], 0) * group / kTileRows) + i; };
+        const int32_t r = find_request(p.seqs.num_req, slot, key);
+        if (lane == 0) {
+            place[0] = r;
+            place[1] = slot >= key(r) ? (slot - key(r)) * kTileRows : -1;
+        }
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const Req req = load_req(p.seqs, place[0]);
+    const int32_t row0 = place[1], req_rows = req.n * group;
+    uint8_t* const base = p.layer.base();
+    const uint8_t* const scales = kCodes ? p.scales.base() : nullptr;
+    const bool there = base != nullptr && (!kCodes || scales != nullptr);
+    if (row0 >= 0 && row0 < req_rows && req_rows >= p.big_rows) {
+        const int32_t old = req.len - req.n;
+        const int32_t last_row = min(row0 + kTileRows, req_rows) - 1;
+        const Seen seen = seen_by(p, old + (int32_t)p.by_group.div((uint32_t)row0),
+                                  old + (int32_t)p.by_group.div((uint32_t)last_row), kBlock);
+        const int32_t units = there ? seen.units : 0;
+        const int32_t b0 = (int32_t)((int64_t)units * part / p.parts), b1 = (int32_t)((int64_t)units * (part + 1) / p.parts);
+        const int tiles = last_row - row0 >= 128 ? 2 : 1;
+        if (tid == 0) {
+            if (!req.ok) report(p.status, LMKV_ERR_BAD_LENGTH);
+            if (!there) report(p.status, LMKV_ERR_BAD_POINTER);
+        }
+
+        if (warp < 8) {
+            const int t = warp >> 2;
+            const int32_t R = row0 + tid;
+            const bool live = R < req_rows;
+            const int32_t n = (int32_t)p.by_group.div((uint32_t)(live ? R : row0));
+            const int32_t tok = req.q0 + n, head = h * group + ((live ? R : row0) - n * group);
+            if (t < tiles) {
+                // my row of q, negated for a negative scale, into shared memory
+                const T* src = p.q.row<T>(tok, head);
+                const uint32_t dst = q_smem + t * S::kStageBytes + (tid & 127) * 128;
+                const uint32_t flip = p.scale_sign < 0 ? 0x80008000u : 0u, all = p.scale_sign == 0 || !live ? 0u : ~0u;
+                uint4 qv[D / 8];              // all loads on their way before the first is waited for
+                if (p.q_vec) {
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) qv[c] = *reinterpret_cast<const uint4*>(src + c * 8);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c)
+                        qv[c] = make_uint4(load_pair(src + c * 8, p.q_pairs), load_pair(src + c * 8 + 2, p.q_pairs),
+                                           load_pair(src + c * 8 + 4, p.q_pairs), load_pair(src + c * 8 + 6, p.q_pairs));
+                }
+                float factor = p.scale_log2, by = 1.f;
+                if constexpr (kCodes) {
+                    // as fp16 with its largest element between 2^14 and 2^15
+                    float top = 0.f;
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) {
+                        const T* const e = reinterpret_cast<const T*>(&qv[c]);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float a = fabsf(Elem<T>::to_float(e[i]));
+                            if (a < INFINITY) top = fmaxf(top, a);
+                        }
+                    }
+                    const int e = top > 0.f ? max((int)(__float_as_uint(top) >> 23) - 127, -100) : 0;
+                    by = power_of_two(14 - e);
+                    factor *= power_of_two(e - 14);
+                }
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    uint4 v = qv[c];
+                    if constexpr (kCodes) {
+                        const T* const e = reinterpret_cast<const T*>(&qv[c]);
+                        v.x = Elem<__half>::pack(Elem<T>::to_float(e[0]) * by, Elem<T>::to_float(e[1]) * by);
+                        v.y = Elem<__half>::pack(Elem<T>::to_float(e[2]) * by, Elem<T>::to_float(e[3]) * by);
+                        v.z = Elem<__half>::pack(Elem<T>::to_float(e[4]) * by, Elem<T>::to_float(e[5]) * by);
+                        v.w = Elem<__half>::pack(Elem<T>::to_float(e[6]) * by, Elem<T>::to_float(e[7]) * by);
+                    }
+                    const uint32_t at = dst + (c >> 3) * S::kHalfBytes + (((c & 7) ^ (tid & 7)) << 4);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"((v.x ^ flip) & all),
+                                 "r"((v.y ^ flip) & all), "r"((v.z ^ flip) & all), "r"((v.w ^ flip) & all)
+                                 : "memory");
+                }
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_ready + 16 * t + 8);     // its phase 0: q is there
+
+                const uint32_t lane_base = tmem_base + ((uint32_t)(warp & 3) << 21);     // lane 32 * (warp % 4)
+                const uint32_t s_at = lane_base + t * 128, o_at = lane_base + 256 + t * 128;
+                // my row sees keys below end, from begin on or below the sinks
+                const int32_t end = live ? old + n + 1 : 0, begin = p.window == INT32_MAX ? 0 : end - p.window;
+                float m = -INFINITY;              // the maximum (lagging), in powers of 2
+                float2 l2 = make_float2(0.f, 0.f);
+                bool ok = true;
+                for (int32_t b = b0; b < b1; ++b) {
+                    const int32_t k = seen.unit(b) * kBlock;
+                    if (!mbar_wait(s_full + 8 * t, (b - b0) & 1, &gave_up)) {
+                        ok = false;
+                        break;
+                    }
+                    if (t == tiles - 1 && (tid & 127) == 0) {
+                        // every product up to these scores is done: K of this block and V of the last are free
+                        const int32_t j = b - b0;
+                        mbar_arrive(empty + 8 * (2 * j % S::kStages));
+                        if (j > 0) mbar_arrive(empty + 8 * ((2 * j - 1) % S::kStages));
+                    }
+                    fence_after_sync();
+                    const uint32_t* const info = infos[(b - b0) % kInfoSlots];
+                    uint32_t every = 0xFFFFu;
+#pragma unroll
+                    for (int u = 0; u < kUnits; ++u) every &= info[u];
+                    const bool whole = __all_sync(0xFFFFFFFFu, end - k >= kBlock && (begin <= k || k + kBlock <= p.sinks)) &&
+                                       (every & 0xFFFFu) == 0xFFFFu;
+                    // scores of 32 keys, those not seen as -infinity
+                    auto below = [](int32_t n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; };
+                    auto take = [&](uint32_t (&x)[32], int i) {
+                        if (whole) return;
+                        const int32_t at = k + 32 * i;
+                        const uint32_t bits = ((info[2 * i] & 0xFFFFu) | (info[2 * i + 1] << 16)) & below(end - at) &
+                                              (~below(begin - at) | below(p.sinks - at));
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (!((bits >> j) & 1)) x[j] = 0xFF800000u;
+                    };
+                    // a unit's factor (never 0: -infinity is to stay that) and addend
+                    auto factor_of = [&](int u) {
+                        if constexpr (!kCodes) return factor;
+                        const float f = factor * power_of_two((int)((info[u] >> 16) & 0xFF) - 127);
+                        return f != f ? f : fmaxf(f, 0x1p-126f);
+                    };
+                    auto power_of = [&](int u) {
+                        if constexpr (!kCodes) return 0.f;
+                        const int e = (int)(info[u] >> 24);
+                        return e == 255 ? NAN : (float)(e - 127);
+                    };
+                    uint32_t x[4][32];
+                    float mx = -INFINITY;
+                    tmem_ld32(x[0], s_at);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        wait_ld();
+                        loaded(x[i]);
+                        if (i < 3) tmem_ld32(x[i + 1], s_at + 32 * (i + 1));
+                        take(x[i], i);
+                        if constexpr (kCodes) {
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                float a = -INFINITY, c = -INFINITY;
+#pragma unroll
+                                for (int j = 16 * u; j < 16 * u + 16; j += 4) {
+                                    a = max3(a, __uint_as_float(x[i][j]), __uint_as_float(x[i][j + 1]));
+                                    c = max3(c, __uint_as_float(x[i][j + 2]), __uint_as_float(x[i][j + 3]));
+                                }
+                                mx = fmaxf(mx, fmaf(fmaxf(a, c), factor_of(2 * i + u), power_of(2 * i + u)));
+                            }
+                        } else {
+                            float a = -INFINITY, c = -INFINITY;
+#pragma unroll
+                            for (int j = 0; j < 32; j += 4) {
+                                a = max3(a, __uint_as_float(x[i][j]), __uint_as_float(x[i][j + 1]));
+                                c = max3(c, __uint_as_float(x[i][j + 2]), __uint_as_float(x[i][j + 3]));
+                            }
+                            mx = fmaxf(mx, fmaxf(a, c));
+                        }
+                    }
+                    if constexpr (!kCodes) mx *= factor;
+                    // the output is rescaled when the maximum has grown by more than 2^kLag
+                    const bool grow = mx > m + kLag;
+                    if (__any_sync(0xFFFFFFFFu, grow)) {
+                        const float f = grow ? exp2_fast(m - mx) : 1.f;
+                        if (grow) m = mx;
+                        l2.x *= f;
+                        l2.y *= f;
+                        if (b > b0) {
+                            // the scores were there, so the product before them, into the output, is done
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 16) tmem_scale16(o_at + c, f);
+                        }
+                    }
+                    const float neg = m == -INFINITY ? 0.f : kBelow - m;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const float f = factor_of(2 * i + u), a = neg + power_of(2 * i + u);
+                            const float2 f2 = make_float2(f, f), a2 = make_float2(a, a);
+                            float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+#pragma unroll
+                            for (int j = 8 * u; j < 8 * u + 8; ++j) {
+                                float2 e = fma2(make_float2(__uint_as_float(x[i][2 * j]), __uint_as_float(x[i][2 * j + 1])),
+                                                f2, a2);
+                                e.x = exp2_fast(e.x);
+                                e.y = exp2_fast(e.y);
+                                if (j & 1) s1 = add2(s1, e);
+                                else s0 = add2(s0, e);
+                                // weights are rounded to 16 bits for the product with V, the sum takes them whole
+                                w[j] = Elem<M>::pack(e.x, e.y);
+                            }
+                            if constexpr (kCodes) {
+                                const float back = power_of_two(127 - (int)(info[2 * i + u] >> 24));
+                                l2 = fma2(add2(s0, s1), make_float2(back, back), l2);
+                            } else {
+                                l2 = add2(l2, add2(s0, s1));
+                            }
+                        }
+                        tmem_st16(s_at + 16 * i, w);       // over scores that have been read
+                        if (i & 1) {                       // 64 keys' weights are there
+                            wait_st();
+                            fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(p_ready + 16 * t + 8 * (i >> 1));
+                        }
+                    }
+                }
+                // my row of the result
+                const float l = l2.x + l2.y;
+                if (ok && b1 > b0) ok = mbar_wait(o_full + 8 * t, 0, &gave_up);
+                if (ok) {
+                    fence_after_sync();
+                    const bool final = p.parts == 1;
+                    const int64_t row = (int64_t)tok * p.q_heads + head;
+                    const int64_t at = (int64_t)part * p.rows + row;
+                    const float ref = m == -INFINITY ? -INFINITY : m - kBelow;
+                    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+                    T* const out = p.out.row<T>(tok, head);
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t y[32];
+                        if (b1 > b0) {
+                            tmem_ld32(y, o_at + 32 * c);
+                            wait_ld();
+                            loaded(y);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) y[j] = 0u;
+                        }
+                        if (!live) continue;
+                        if (final) {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 8) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    w[i] = Elem<T>::pack(__uint_as_float(y[j + 2 * i]) * inv,
+                                                         __uint_as_float(y[j + 2 * i + 1]) * inv);
+                                T* dst = out + 32 * c + j;
+                                if (p.out_vec) {
+                                    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+                                } else {
+                                    uint16_t* d16 = reinterpret_cast<uint16_t*>(dst);
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        d16[2 * i] = (uint16_t)w[i];
+                                        d16[2 * i + 1] = (uint16_t)(w[i] >> 16);
+                                    }
+                                }
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 4)
+                                *reinterpret_cast<uint4*>(p.part_o + at * D + 32 * c + j) =
+                                    make_uint4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+                        }
+                    }
+                    if (live && final && p.lse != nullptr)
+                        p.lse[row] = ((m == -INFINITY ? 0.f : ref) + log2f(l)) * kLn2;
+                    if (live && !final) p.part_ml[at] = make_float2(ref, l);
+                }
+            }
+        } else if (warp < 8 + kLoaders) {
+            // Unit u of the CTA is rows 16 (u % 8) .. of item u / 8 (K, V of a block in turn); warp
+            // 8 + i takes units i, i + 3, ..
+            const int32_t* const table = p.seqs.table + (int64_t)req.r * p.seqs.table_stride;
+            const uint32_t row_bytes = (uint32_t)p.layer.row_bytes;
+            const int64_t half_bytes = p.layer.half_bytes();
+            constexpr int kRowBytes = D * (int)sizeof(KV), kPieces = kRowBytes / 16, kRowsPer = 32 / kPieces;
+            constexpr int kCopies = kChunk / kRowsPer;
+            const int c = lane % kPieces, rsub = lane / kPieces;
+            const uint8_t* const mine = base + (int64_t)h * kRowBytes + c * 16;
+            const int32_t all_units = (b1 - b0) * 2 * kUnits;
+            struct Unit {
+                int32_t k;                // its first key
+                int32_t blk;
+                uint32_t rows;            // which of its rows there are
+            };
+            auto look = [&](int32_t u) {
+                Unit x{0, -1, 0};
+                if (u >= all_units) return x;
+                x.k = seen.unit(b0 + u / (2 * kUnits)) * kBlock + u % kUnits * kChunk;
+                // keys [0, sink_end) and [lo, end) are seen
+                auto below = [](int32_t n) { return n >= 16 ? 0xFFFFu : n <= 0 ? 0u : (1u << n) - 1u; };
+                x.rows = below(seen.end - x.k) & (below(seen.sink_end - x.k) | ~below(seen.lo - x.k));
+                if (x.rows != 0) x.blk = table[p.layer.column(x.k)];
+                return x;
+            };
+            auto check = [&](Unit& x) {
+                if (x.rows != 0 && (x.blk < 0 || x.blk >= p.layer.num_blocks)) {
+                    if (lane == 0) report(p.status, LMKV_ERR_BAD_BLOCK);
+                    x.rows = 0;
+                }
+            };
+            auto source = [&](const Unit& x, bool v) {
+                return mine + (v ? half_bytes : 0) + ((uint64_t)p.layer.row_of(x.blk, x.k, p.layer.column(x.k)) + rsub) * row_bytes;
+            };
+            auto enter = [&](int32_t u) {      // the unit's stage is free
+                const int32_t item = u / kUnits, st = item % S::kStages;
+                return item < S::kStages || mbar_wait(empty + 8 * st, (item / S::kStages - 1) & 1, &gave_up);
+            };
+            auto tell = [&](int32_t u, const Unit& x, uint32_t bytes) {
+                if (u / kUnits % 2 == 0 && lane == 0) infos[u / (2 * kUnits) % kInfoSlots][u % kUnits] = x.rows | bytes;
+            };
+            const int32_t u_first = warp - 8;
+            bool ok = true;
+            if constexpr (kCodes) {
+                // three units on their way in registers, the table entries of one more
+                constexpr int kDeep = 3;
+                uint4 raw[kDeep][kCopies];
+                Unit unit[kDeep];
+                uint32_t bytes[kDeep];
+                Unit next = look(u_first);
+                auto start = [&](int s, int32_t u) {
+                    unit[s] = next;
+                    check(unit[s]);
+                    next = look(u + kLoaders);
+                    bytes[s] = 0x7F7F0000u;
+                    const bool v = u / kUnits % 2 != 0;
+                    if (unit[s].rows == 0) return;
+                    const uint8_t* const src = source(unit[s], v);
+#pragma unroll
+                    for (int r = 0; r < kCopies; ++r) {
+                        raw[s][r] = make_uint4(0u, 0u, 0u, 0u);
+                        if ((unit[s].rows >> (r * kRowsPer + rsub)) & 1)
+                            raw[s][r] = *reinterpret_cast<const uint4*>(src + r * kRowsPer * row_bytes);
+                    }
+                    if (!v)
+                        bytes[s] = ((uint32_t)scales[p.scales.at(0, unit[s].blk, h)] << 16) |
+                                   ((uint32_t)scales[p.scales.at(1, unit[s].blk, h)] << 24);
+                };
+#pragma unroll
+                for (int s = 0; s < kDeep - 1; ++s) start(s, u_first + s * kLoaders);
+                for (int32_t u0 = u_first; u0 < all_units && ok; u0 += kDeep * kLoaders) {
+#pragma unroll
+                    for (int s = 0; s < kDeep; ++s) {
+                        const int32_t u = u0 + s * kLoaders;
+                        if (u >= all_units || !ok) break;
+                        start((s + kDeep - 1) % kDeep, u + (kDeep - 1) * kLoaders);
+                        ok = enter(u);
+                        if (!ok) break;
+                        tell(u, unit[s], bytes[s]);
+                        const uint32_t dst = kv_smem + u / kUnits % S::kStages * S::kStageBytes + u % kUnits * (kChunk * 128);
+#pragma unroll
+                        for (int r = 0; r < kCopies; ++r) {
+                            const uint4 v = unit[s].rows != 0 ? raw[s][r] : make_uint4(0u, 0u, 0u, 0u);
+                            uint32_t e[8];
+                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                e[2 * i] = codes_to_half2((uint16_t)w[i]);
+                                e[2 * i + 1] = codes_to_half2((uint16_t)(w[i] >> 16));
+                            }
+                            const int row = r * kRowsPer + rsub;
+                            const uint32_t at = dst + (D == 128 ? (c >> 2) * S::kHalfBytes : 0) + row * 128;
+                            // (pieces of the two halves in turn, so that they meet no bank twice)
+                            const int odd = D == 128 ? c >> 2 : 0;
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const int which = i ^ odd;
+                                const uint32_t to = at + ((((2 * c + which) & 7) ^ (row & 7)) << 4);
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(which ? e[4] : e[0]),
+                                             "r"(which ? e[5] : e[1]), "r"(which ? e[6] : e[2]), "r"(which ? e[7] : e[3])
+                                             : "memory");
+                            }
+                        }
+                        fence_async_shared();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(full + 8 * (u / kUnits % S::kStages));
+                    }
+                }
+            } else {
+                Unit next = look(u_first);
+                for (int32_t u = u_first; u < all_units && ok; u += kLoaders) {
+                    Unit x = next;
+                    check(x);
+                    next = look(u + kLoaders);
+                    ok = enter(u);
+                    if (!ok) break;
+                    tell(u, x, 0x7F7F0000u);
+                    const uint32_t stage = u / kUnits % S::kStages;
+                    const uint32_t dst = kv_smem + stage * S::kStageBytes + u % kUnits * (kChunk * 128) +
+                                         (c >> 3) * S::kHalfBytes;
+                    const uint8_t* const src = x.rows != 0 ? source(x, u / kUnits % 2 != 0) : base;
+#pragma unroll
+                    for (int r = 0; r < kCopies; ++r) {
+                        const int row = r * kRowsPer + rsub;
+                        const bool on = (x.rows >> row) & 1;
+                        cp_async16(dst + row * 128 + (((c & 7) ^ (row & 7)) << 4), on ? src + r * kRowsPer * row_bytes : base, on);
+                    }
+                    copies_arrive(full + 8 * stage);
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+            }
+        } else if (b1 > b0) {
+            constexpr uint32_t qk = instr_desc<M, kBlock, false>(), pv = instr_desc<M, D, true>();
+            // all of tensor memory is this CTA's, so its columns count from 0
+            constexpr uint32_t kScores = 0, kOut = 256;
+            const int32_t blocks = b1 - b0;
+            const uint32_t lead = elect_lead();
+            const Desc q0 = desc_k_major(q_smem), k0 = desc_k_major(kv_smem), v0 = desc_n_major(kv_smem, S::kHalfBytes);
+            // places of the next K and V items in the ring, and their phases
+            int32_t ks = 0, vs = 1;
+            uint32_t kph = 0, vph = 0;
+            auto advance = [](int32_t& st, uint32_t& ph) {
+                st += 2;
+                if (st >= S::kStages) {
+                    st -= S::kStages;
+                    ph ^= 1;
+                }
+            };
+            auto scores = [&](int t, int32_t st) {         // tile t's q x K
+                const Desc a = q0.at(t * S::kStageBytes), k = k0.at(st * S::kStageBytes);
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) {
+                    const uint32_t at = (s >> 2) * S::kHalfBytes + (s & 3) * 32;
+                    mma_ss(lead, kScores + t * 128, a.at(at), k.at(at), qk, s > 0);
+                }
+                mma_commit(lead, s_full + 8 * t);
+            };
+            // the copies of an item, before the products that read them
+            auto landed = [&](int32_t st, uint32_t ph) {
+                const bool there = mbar_wait(full + 8 * st, ph, &gave_up);
+                fence_async_shared();
+                return there;
+            };
+            bool ok = landed(0, 0);
+            for (int t = 0; t < tiles && ok; ++t) {
+                ok = mbar_wait(p_ready + 16 * t + 8, 0, &gave_up);
+                if (ok) scores(t, 0);
+            }
+            advance(ks, kph);
+            ok = ok && landed(vs, vph);
+            for (int32_t j = 0; j < blocks && ok; ++j) {
+                const bool more = j + 1 < blocks;
+                const Desc v = v0.at(vs * S::kStageBytes);
+                advance(vs, vph);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (t >= tiles || !ok) break;
+                    // the weights come in two halves of 64 keys, a barrier each
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        ok = ok && mbar_wait(p_ready + 16 * t + 8 * half, (j + half) & 1, &gave_up);
+                        if (!ok) break;
+                        fence_after_sync();
+#pragma unroll
+                        for (int s = half * 4; s < half * 4 + 4; ++s)
+                            mma_ts(lead, kOut + t * 128, kScores + t * 128 + 8 * s, v.at(s * 2048), pv, j > 0 || s > 0);
+                    }
+                    if (!ok) break;
+                    // waits for loads stand where the tensor core has work
+                    if (more) {
+                        if (t == 0) ok = landed(ks, kph);
+                        // issued behind the product that reads the weights from the same columns
+                        if (ok) scores(t, ks);
+                        if (t == 0) ok = ok && landed(vs, vph);
+                    } else {
+                        mma_commit(lead, o_full + 8 * t);
+                    }
+                }
+                advance(ks, kph);
+            }
+        }
+    }
+    __syncwarp();
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    if (tid == 0 && gave_up) report(p.status, LMKV_ERR_TIMEOUT);
+    if (warp == 8 + kLoaders) tmem_free<512>(tmem_base);
+}
+
+// ---- host ---------------------------------------------------------------
+
+constexpr int kBigRows = 64;
+// CTAs of the tile kernel up to which it splits the keys: two rounds of one an SM.
+constexpr int64_t kMostTileCtas = 2 * kSms;
+
+struct Plan {
+    int32_t big_rows, own_cap, own_tiles, tile_rows, streams, slots, parts;
+    int64_t tile_part_rows, own_rows;
+    uint64_t bytes;
+};
+
+// What a call within these bounds takes; most: room for every smaller one too.
+Plan make_plan(const lmkv_pool_t* pool, int32_t q_heads, int32_t num_tokens, int32_t num_req, int32_t max_new,
+               int32_t max_kv_len, bool most) {
+    Plan x = {};
+    const int64_t heads = pool->num_kv_heads, group = q_heads / heads;
+    const int64_t rows = (int64_t)num_tokens * q_heads;
+    // (a bound of 0 still has rows to look at: lengths beyond it are reported)
+    const int64_t req_rows = (int64_t)(max_new < 1 ? 1 : max_new < num_tokens ? max_new : num_tokens) * group;
+    // tiles take a unit of 16 keys from one page
+    const bool big = req_rows >= kBigRows && pool->block_size % kChunk == 0;
+    x.big_rows = big ? kBigRows : INT32_MAX;
+    x.own_cap = (int32_t)(big ? kBigRows - 1 : req_rows);
+    x.tile_rows = x.own_cap <= 8 ? 8 : 16;
+    x.own_tiles = (x.own_cap + x.tile_rows - 1) / x.tile_rows;
+    const bool wide = pool->elem_bytes == 2 && pool->head_dim == 128;
+    const int64_t warps = (int64_t)kSms * kWarps * (most ? 4 : wide || x.tile_rows > 8 ? 3 : 4);
+    int64_t streams = warps / heads > 0 ? warps / heads : 1;
+    x.streams = (int32_t)streams;
+    // (smaller batches may have tiles of fewer rows, and so of more in number)
+    const int64_t per_req = most ? ((int64_t)x.own_tiles * x.tile_rows + 8) : (int64_t)x.own_tiles * x.tile_rows;
+    x.own_rows = (x.streams * (int64_t)x.tile_rows + num_req * per_req) * heads;
+    x.parts = 1;
+    if (big) {
+        const int64_t slots = (int64_t)num_tokens * group / kTileRows + num_req;
+        const int64_t blocks = ((int64_t)max_kv_len + kBlock - 1) / kBlock;
+        x.slots = (int32_t)slots;
+        if (slots * heads < kSms) {
+            const int64_t n = kMostTileCtas / (slots * heads);
+            x.parts = (int32_t)(n < blocks ? n : blocks < 1 ? 1 : blocks);
+        }
+        x.tile_part_rows = x.parts > 1 ? x.parts * rows : 0;
+        if (most) x.tile_part_rows = kMostTileCtas * kTileRows;        // a split call's rows are fewer
+    }
+    x.bytes = (uint64_t)(x.tile_part_rows + x.own_rows) * (pool->head_dim * 4 + 8) +
+              (uint64_t)num_req * (most ? (x.own_cap + 7) / 8 : x.own_tiles) * 8;
+    return x;
+}
+
+template <class T, class KV, int D, int NT>
+int launch_streams(const WindowParams& p, void* stream) {
+    return launch(window_streams_kernel<T, KV, D, NT>, ((int64_t)p.streams * p.kv_heads + kWarps - 1) / kWarps, kWarps * 32,
+                  StreamShape<KV, D>::kSmem, stream, 1, p);
+}
+
+template <class T, class KV, int D>
+int window_typed(const WindowParams& p, const Plan& x, void* stream) {
+    using Sh = StreamShape<KV, D>;
+    int rc = allow_smem<window_streams_kernel<T, KV, D, 1>, Sh::kSmem>();
+    if (rc == LMKV_OK) rc = allow_smem<window_streams_kernel<T, KV, D, 2>, Sh::kSmem>();
+    if (rc == LMKV_OK) rc = allow_smem<window_tiles_kernel<T, KV, D>, WindowTile<D>::kSmem>();
+    if (rc == LMKV_OK && x.big_rows < INT32_MAX)
+        rc = launch(window_tiles_kernel<T, KV, D>, (int64_t)x.slots * p.kv_heads * x.parts, kTileThreads,
+                    WindowTile<D>::kSmem, stream, 1, p);
+    if (rc == LMKV_OK) rc = x.tile_rows == 8 ? launch_streams<T, KV, D, 1>(p, stream) : launch_streams<T, KV, D, 2>(p, stream);
+    if (rc == LMKV_OK)
+        rc = launch(window_join_kernel<T, D, false>, ((int64_t)p.seqs.num_req * x.own_cap * p.kv_heads + 7) / 8, 256, 0, stream,
+                    1, p);
+    if (rc == LMKV_OK && x.parts > 1)
+        rc = launch(window_join_kernel<T, D, true>, ((int64_t)p.rows + 7) / 8, 256, 0, stream, 1, p);
+    return rc;
+}
+
+template <class T>
+int window_dims(const WindowParams& p, const Plan& x, const lmkv_pool_t* pool, void* stream) {
+    if (pool->elem_bytes == 1)
+        return pool->head_dim == 64 ? window_typed<T, uint8_t, 64>(p, x, stream) : window_typed<T, uint8_t, 128>(p, x, stream);
+    return pool->head_dim == 64 ? window_typed<T, T, 64>(p, x, stream) : window_typed<T, T, 128>(p, x, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+int lmkv_attend_window_workspace_bytes(const lmkv_pool_t* pool, int32_t num_q_heads, int32_t num_tokens, int32_t num_req,
+                                       int32_t max_new, int32_t max_kv_len, uint64_t* bytes) {
+    const int rc = lmkv_internal_check_pool(pool);
+    if (rc != LMKV_OK) return rc;
+    if ((pool->elem_bytes != 1 && pool->elem_bytes != 2) || (pool->head_dim != 64 && pool->head_dim != 128))
+        return LMKV_ERR_UNSUPPORTED;
+    if (bytes == nullptr || num_q_heads <= 0 || num_q_heads % pool->num_kv_heads != 0 || num_q_heads > (1 << 20) ||
+        num_tokens < 0 || num_req < 0 || num_req > (1 << 24) || max_new < 0 || max_kv_len < 0 ||
+        (int64_t)num_tokens * num_q_heads > (int64_t)1 << 30)
+        return LMKV_ERR_INVALID_ARG;
+    *bytes = num_tokens == 0 || num_req == 0
+                 ? 0 : make_plan(pool, num_q_heads, num_tokens, num_req, max_new, max_kv_len, true).bytes;
+    return LMKV_OK;
+}
+
+int lmkv_attend_layer_window(const lmkv_pool_t* pool, void* const* scales, int32_t dtype, int32_t layer,
+                             const lmkv_batch_t* batch, int32_t num_q_heads, const lmkv_rows_t* q, float scale,
+                             int32_t window, int32_t sinks, const lmkv_rows_t* out, float* lse, void* workspace,
+                             uint64_t workspace_bytes, int32_t* d_status, void* stream) {
+    int rc = lmkv_internal_check_pool(pool);
+    if (rc == LMKV_OK) rc = check_scales(pool, scales, dtype);
+    if (rc != LMKV_OK) return rc;
+    if (layer < 0 || layer >= pool->num_layers || !std::isfinite(scale * kLog2e) || window < 0 || sinks < 0)
+        return LMKV_ERR_INVALID_ARG;
+    rc = check_batch(pool, batch, num_q_heads);
+    if (rc != LMKV_OK) return rc;
+    if (batch->max_kv_len > INT32_MAX - 65536) return LMKV_ERR_INVALID_ARG;
+    if (batch->num_req == 0 || batch->num_tokens == 0) return LMKV_OK;
+    if (!rows_ok(q, 2) || !rows_ok(out, 2)) return LMKV_ERR_INVALID_ARG;
+    const Plan x = make_plan(pool, num_q_heads, batch->num_tokens, batch->num_req, batch->max_new, batch->max_kv_len, false);
+    if (workspace == nullptr || workspace_bytes < x.bytes) return LMKV_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(workspace) & 15) return LMKV_ERR_MISALIGNED;
+    if (out->data == q->data) return LMKV_ERR_INVALID_ARG;
+    WindowParams p = {};
+    p.layer = Layer::of(pool, layer);
+    p.seqs = Seqs::of(batch);
+    p.scales = Scales::of(pool, scales, layer);
+    p.q = Rows::of(q);
+    p.out = Rows::of(out);
+    p.lse = lse;
+    p.status = d_status;
+    const uint64_t parts = (uint64_t)(x.tile_part_rows + x.own_rows);
+    p.part_o = static_cast<float*>(workspace);
+    p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + parts * pool->head_dim * 4);
+    p.own_range = reinterpret_cast<int2*>(p.part_ml + parts);
+    p.own_base = x.tile_part_rows;
+    p.scale_sign = scale > 0.f ? 1 : scale < 0.f ? -1 : 0;
+    p.scale_log2 = scale == 0.f ? 1.f : std::fabs(scale) * kLog2e;
+    p.window = window == 0 ? INT32_MAX : window;
+    p.sinks = sinks;
+    p.q_heads = num_q_heads;
+    p.kv_heads = pool->num_kv_heads;
+    p.rows = batch->num_tokens * num_q_heads;
+    p.big_rows = x.big_rows;
+    p.own_cap = x.own_cap;
+    p.own_tiles = x.own_tiles;
+    p.tile_rows = x.tile_rows;
+    p.streams = x.streams;
+    p.slots = x.slots;
+    p.parts = x.parts;
+    auto aligned = [](const lmkv_rows_t* r, int64_t to) {
+        return reinterpret_cast<uintptr_t>(r->data) % to == 0 && r->token_stride * 2 % to == 0 && r->head_stride * 2 % to == 0;
+    };
+    p.q_vec = aligned(q, 16);
+    p.out_vec = aligned(out, 16);
+    p.q_pairs = aligned(q, 4);
+    p.by_group = FastDiv((uint32_t)(num_q_heads / pool->num_kv_heads));
+    return dtype == LMKV_BF16 ? window_dims<__nv_bfloat16>(p, x, pool, stream) : window_dims<__half>(p, x, pool, stream);
+}
+
+}  // extern "C"

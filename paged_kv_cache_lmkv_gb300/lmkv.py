@@ -30,6 +30,7 @@ ERR_TIMEOUT = 7
 ERR_SCRATCH_LIMIT = 8
 ERR_BAD_DATA = 9
 ERR_BAD_LENGTH = 10
+ERR_NO_PAGES = 11
 BF16, FP16, FP32 = 0, 1, 2                  # lmkv_dtype_t
 ROTARY_MAX_PAIRS = 128
 ROTARY_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4, "yarn": 5}
@@ -55,6 +56,9 @@ ENTRY_POINTS = (
     "lmkv_rotary_init", "lmkv_append_layer", "lmkv_scatter_chunks_shifted",
     "lmkv_scatter_layer_shifted", "lmkv_attend_workspace_bytes", "lmkv_attend_layer",
     "lmkv_weigh_layer", "lmkv_evict_layer",
+    "lmkv_append_layer_normed", "lmkv_attend_window_workspace_bytes", "lmkv_attend_layer_window",
+    "lmkv_pages_workspace_bytes", "lmkv_copy_pages", "lmkv_fork_pages", "lmkv_resize_pages",
+    "lmkv_compact_pages",
 )
 
 
@@ -184,7 +188,19 @@ def load() -> ctypes.CDLL:
         lib.lmkv_weigh_layer.argtypes = [pool_p, i32, i32, batch_p, i32, rows_p, P, f32, f32, P, P, i64, P, P]
         lib.lmkv_evict_layer.argtypes = [pool_p, i32, P, i32, P, i32, i32, P, i64, i32, i32, i32, P, P, P,
                                          i64, P, P]
-        for name in ("lmkv_rotary_init", "lmkv_append_layer", "lmkv_scatter_chunks_shifted",
+        lib.lmkv_append_layer_normed.argtypes = [pool_p, P, i32, i32, batch_p, i32, rows_p, rows_p, rows_p, rows_p,
+                                                 P, rot_p, P, P, f32, P, P]
+        lib.lmkv_attend_window_workspace_bytes.argtypes = [pool_p, i32, i32, i32, i32, i32, P]
+        lib.lmkv_attend_layer_window.argtypes = [pool_p, P, i32, i32, batch_p, i32, rows_p, f32, i32, i32, rows_p, P,
+                                                 P, ctypes.c_uint64, P, P]
+        lib.lmkv_pages_workspace_bytes.argtypes = [pool_p, i32, P]
+        lib.lmkv_copy_pages.argtypes = [pool_p, P, P, P, i32, P, P]
+        lib.lmkv_fork_pages.argtypes = [pool_p, P, P, i32, P, i32, P, i32, P, P, P, P, P, ctypes.c_uint64, P, P]
+        lib.lmkv_resize_pages.argtypes = [pool_p, P, i32, P, P, i32, P, P, P, P, ctypes.c_uint64, P, P]
+        lib.lmkv_compact_pages.argtypes = [pool_p, P, P, i32, P, i32, P, P, P, P, P, ctypes.c_uint64, P, P]
+        for name in ("lmkv_append_layer_normed", "lmkv_attend_window_workspace_bytes", "lmkv_attend_layer_window",
+                     "lmkv_pages_workspace_bytes", "lmkv_copy_pages", "lmkv_fork_pages", "lmkv_resize_pages",
+                     "lmkv_compact_pages", "lmkv_rotary_init", "lmkv_append_layer", "lmkv_scatter_chunks_shifted",
                      "lmkv_scatter_layer_shifted", "lmkv_attend_workspace_bytes", "lmkv_attend_layer",
                      "lmkv_weigh_layer", "lmkv_evict_layer",
                      "lmkv_count_chunks", "lmkv_enumerate_chunks", "lmkv_gather_chunks",
@@ -246,10 +262,16 @@ def _stream_handle(stream) -> int | None:
 class Pool:
     """A paged KV pool: per-layer device tensors [2][num_blocks][block_size][heads*head_dim].
 
-    Holds the DEVICE array of layer base pointers the ABI takes.
+    Holds the DEVICE array of layer base pointers the ABI takes.  scales: the
+    tensors of an 8-bit pool's powers of two, per layer [2][num_blocks][heads] in
+    float8_e8m0fnu or uint8 (value = code * 2^(byte - 127)); the layers then hold
+    e4m3 codes, as float8_e4m3fn or uint8.
     """
 
-    def __init__(self, layers: Sequence[torch.Tensor], num_kv_heads: int, head_dim: int):
+    scales = scale_ptrs = None
+
+    def __init__(self, layers: Sequence[torch.Tensor], num_kv_heads: int, head_dim: int,
+                 scales: Sequence[torch.Tensor] | None = None):
         t0 = layers[0]
         if t0.dim() != 4 or t0.shape[0] != 2 or t0.shape[3] != num_kv_heads * head_dim:
             raise ValueError("pool layers must be [2][num_blocks][block_size][heads*head_dim]")
@@ -266,6 +288,18 @@ class Pool:
                                  device=t0.device)
         self._struct = _PoolT(self.ptrs.data_ptr(), self.num_blocks, len(layers), num_kv_heads,
                               head_dim, self.block_size, self.elem_bytes)
+        if scales is not None:
+            if t0.dtype not in (torch.float8_e4m3fn, torch.uint8):
+                raise ValueError(f"scales belong to layers of e4m3 codes, got {t0.dtype}")
+            if len(scales) != len(layers):
+                raise ValueError("one tensor of scales for each layer")
+            for t in scales:
+                if t.shape != (2, self.num_blocks, num_kv_heads) or not t.is_contiguous() or t.device != t0.device or \
+                        t.dtype not in (torch.float8_e8m0fnu, torch.uint8):
+                    raise ValueError("scales must be contiguous float8_e8m0fnu or uint8 [2][num_blocks][heads] on the "
+                                     "layers' device")
+            self.scales = list(scales)
+            self.scale_ptrs = torch.tensor([t.data_ptr() for t in scales], dtype=torch.int64, device=t0.device)
 
     @property
     def num_layers(self) -> int:
@@ -977,8 +1011,11 @@ def evict_layer(pool, layer, block_table, kv_len, scores, sinks, recent, keep, n
     and move their rows to the front of the request's pages.  Writes keep
     (int32 [requests][kv heads][budget]), new_len and kept_scores; the caller
     then takes new_len as kv_len and frees the pages behind it.  max_kv_len
-    defaults to what the table and the scores have room for."""
+    defaults to what the table and the scores have room for.  Not for an 8-bit
+    pool with scales, which belong to whole pages."""
     dev = pool.layers[0].get_device()
+    if pool.scales is not None:
+        raise ValueError("rows of an 8-bit pool do not move apart from their page's scale")
     n, cols, kh = kv_len.shape[0], block_table.shape[-1], pool.num_kv_heads
     stride, budget = scores.shape[-1], keep.shape[-1]
     i32, f32 = torch.int32, torch.float32
@@ -993,6 +1030,146 @@ def evict_layer(pool, layer, block_table, kv_len, scores, sinks, recent, keep, n
         _whole("kv_len", kv_len, i32, dev, (n,)), n, int(max_kv_len),
         _whole("scores", scores, f32, dev, (n, kh, stride)), stride, budget, int(sinks), int(recent), _whole("keep", keep, i32, dev, (n, kh, budget)),
         _whole("new_len", new_len, i32, dev, (n,)), kp, kept_stride, _status(status, dev),
+        _stream_of(pool, dev, stream))
+
+
+# ---- the 8-bit cache ------------------------------------------------------
+
+def _cache_dtype(pool, name: str, t: torch.Tensor):
+    """(element type of the rows, lmkv_dtype_t, DEVICE array of scales or None) of a call on a
+    16-bit pool, whose type the rows have, or an 8-bit one."""
+    t0, dt = pool.layers[0], t.dtype
+    code = _DTYPES.get(dt)
+    if code is None or code == FP32:
+        raise ValueError(f"{name} must be bfloat16 or float16, got {dt}")
+    if pool.scale_ptrs is not None:
+        return dt, code, pool.scale_ptrs.data_ptr()
+    if t0.element_size() == 1:
+        raise ValueError("an 8-bit pool needs its scales (Pool(..., scales=))")
+    return t0.dtype, _dtype_of(t0), None
+
+
+def append_layer_normed(pool, layer, block_table, q, k, v, q_out, q_start, kv_len, rotary=None, q_norm=None,
+                        k_norm=None, eps=1e-6, positions=None, status=None, stream=None) -> int:
+    """lmkv_append_layer_normed: append_layer for models that norm each head of q and k
+    (q_norm, k_norm: float32 [head_dim], or None) before the rotation (rotary, or None),
+    into 16-bit pages or, with the pool's scales, pages of e4m3 codes."""
+    dev = pool.layers[0].get_device()
+    tokens, heads = _heads_of("q", q)
+    dt, code, scales = _cache_dtype(pool, "q", q)
+    d = pool.head_dim
+    qs, ks = (tokens, heads, d), (tokens, pool.num_kv_heads, d)
+    b, _ = _batch(pool, dev, block_table, q_start, kv_len, tokens, None, None)
+    f32 = torch.float32
+    return load().lmkv_append_layer_normed(
+        pool.struct, scales, code, int(layer), b, heads, _rows("q", q, dt, dev, qs), _rows("k", k, dt, dev, ks),
+        _rows("v", v, dt, dev, ks), _rows("q_out", q_out, dt, dev, qs),
+        None if positions is None else _whole("positions", positions, torch.int64, dev, (tokens,)),
+        None if rotary is None else rotary.struct,
+        None if q_norm is None else _whole("q_norm", q_norm, f32, dev, (d,)),
+        None if k_norm is None else _whole("k_norm", k_norm, f32, dev, (d,)), float(eps), _status(status, dev),
+        _stream_of(pool, dev, stream))
+
+
+def attend_window_workspace_bytes(pool, num_q_heads: int, num_tokens: int, num_req: int, max_new: int,
+                                  max_kv_len: int = 0) -> int:
+    """Bytes of workspace for attend_layer_window calls within these bounds (smaller ones too)."""
+    out = ctypes.c_uint64(0)
+    check(load().lmkv_attend_window_workspace_bytes(pool.struct, int(num_q_heads), int(num_tokens), int(num_req),
+                                                    int(max_new), int(max_kv_len), ctypes.byref(out)),
+          "lmkv_attend_window_workspace_bytes")
+    return out.value
+
+
+def attend_layer_window(pool, layer, q, out, q_start, kv_len, block_table, scale, workspace, window=0, sinks=0,
+                        lse=None, max_new=None, max_kv_len=None, status=None, stream=None) -> int:
+    """lmkv_attend_layer_window: attention of q [tokens][heads][head_dim] to the requests'
+    own cached tokens, 16-bit or 8-bit, into out (and lse, float32 [tokens][heads]).  With a
+    window (0: none) token t sees the last `window` tokens up to itself, and the first
+    `sinks`.  max_new and max_kv_len bound the lengths on the device, as in attend_layer."""
+    dev = pool.layers[0].get_device()
+    tokens, heads = _heads_of("q", q)
+    dt, code, scales = _cache_dtype(pool, "q", q)
+    qs = (tokens, heads, pool.head_dim)
+    b, _ = _batch(pool, dev, block_table, q_start, kv_len, tokens, max_new, max_kv_len)
+    return load().lmkv_attend_layer_window(
+        pool.struct, scales, code, int(layer), b, heads, _rows("q", q, dt, dev, qs), float(scale), int(window),
+        int(sinks), _rows("out", out, dt, dev, qs),
+        None if lse is None else _whole("lse", lse, torch.float32, dev, (tokens, heads)),
+        _whole("workspace", workspace, torch.uint8, dev, (workspace.numel(),)), workspace.numel(),
+        _status(status, dev), _stream_of(pool, dev, stream))
+
+
+# ---- pages ----------------------------------------------------------------
+
+def pages_workspace_bytes(pool, rows: int) -> int:
+    """Bytes of workspace for fork_pages, resize_pages and compact_pages on tables of up to this many rows."""
+    out = ctypes.c_uint64(0)
+    check(load().lmkv_pages_workspace_bytes(pool.struct, int(rows), ctypes.byref(out)), "lmkv_pages_workspace_bytes")
+    return out.value
+
+
+def _scales(pool):
+    return None if pool.scale_ptrs is None else pool.scale_ptrs.data_ptr()
+
+
+def copy_pages(pool, src, dst, status=None, stream=None) -> int:
+    """lmkv_copy_pages: page src[i] to page dst[i] (int32), all layers, K and V, and their scales."""
+    dev = pool.layers[0].get_device()
+    n = src.shape[0]
+    return load().lmkv_copy_pages(pool.struct, _scales(pool), _whole("src", src, torch.int32, dev, (n,)),
+                                  _whole("dst", dst, torch.int32, dev, (n,)), n, _status(status, dev),
+                                  _stream_of(pool, dev, stream))
+
+
+def fork_pages(pool, block_table, kv_len, parents, refs, table_out, len_out, refs_out, workspace, status=None,
+               stream=None) -> int:
+    """lmkv_fork_pages: row i of table_out (and len_out) continues row parents[i] of block_table,
+    whose rows give their pages back; full pages are shared, a last one that is not full
+    is copied for all rows but the first.  refs, refs_out: int32 [num_blocks], how many rows
+    hold each page."""
+    dev, i32 = pool.layers[0].get_device(), torch.int32
+    rows, cols, rows_out = kv_len.shape[0], block_table.shape[-1], parents.shape[0]
+    held = (pool.num_blocks,)
+    return load().lmkv_fork_pages(
+        pool.struct, _scales(pool), _whole("block_table", block_table, i32, dev, (rows, cols)), cols,
+        _whole("kv_len", kv_len, i32, dev, (rows,)), rows, _whole("parents", parents, i32, dev, (rows_out,)), rows_out,
+        _whole("refs", refs, i32, dev, held), _whole("table_out", table_out, i32, dev, (rows_out, cols)),
+        _whole("len_out", len_out, i32, dev, (rows_out,)), _whole("refs_out", refs_out, i32, dev, held),
+        _whole("workspace", workspace, torch.uint8, dev, (workspace.numel(),)), workspace.numel(), _status(status, dev),
+        _stream_of(pool, dev, stream))
+
+
+def resize_pages(pool, block_table, kv_len, new_len, refs, table_out, refs_out, workspace, status=None,
+                 stream=None) -> int:
+    """lmkv_resize_pages: rows of kv_len tokens become rows of new_len: pages behind give up a
+    reference, missing ones are given.  table_out may be block_table, refs_out refs."""
+    dev, i32 = pool.layers[0].get_device(), torch.int32
+    rows, cols = kv_len.shape[0], block_table.shape[-1]
+    held = (pool.num_blocks,)
+    return load().lmkv_resize_pages(
+        pool.struct, _whole("block_table", block_table, i32, dev, (rows, cols)), cols,
+        _whole("kv_len", kv_len, i32, dev, (rows,)), _whole("new_len", new_len, i32, dev, (rows,)), rows,
+        _whole("refs", refs, i32, dev, held), _whole("table_out", table_out, i32, dev, (rows, cols)),
+        _whole("refs_out", refs_out, i32, dev, held),
+        _whole("workspace", workspace, torch.uint8, dev, (workspace.numel(),)), workspace.numel(), _status(status, dev),
+        _stream_of(pool, dev, stream))
+
+
+def compact_pages(pool, block_table, kv_len, refs, table_out, refs_out, page_map, workspace, status=None,
+                  stream=None) -> int:
+    """lmkv_compact_pages: the highest held pages move into the lowest free ones; page_map
+    (int32 [num_blocks]) says where each page is now, and table_out, which may be
+    block_table, follows it."""
+    dev, i32 = pool.layers[0].get_device(), torch.int32
+    rows, cols = kv_len.shape[0], block_table.shape[-1]
+    held = (pool.num_blocks,)
+    return load().lmkv_compact_pages(
+        pool.struct, _scales(pool), _whole("block_table", block_table, i32, dev, (rows, cols)), cols,
+        _whole("kv_len", kv_len, i32, dev, (rows,)), rows, _whole("refs", refs, i32, dev, held),
+        _whole("table_out", table_out, i32, dev, (rows, cols)), _whole("refs_out", refs_out, i32, dev, held),
+        _whole("page_map", page_map, i32, dev, held),
+        _whole("workspace", workspace, torch.uint8, dev, (workspace.numel(),)), workspace.numel(), _status(status, dev),
         _stream_of(pool, dev, stream))
 
 
