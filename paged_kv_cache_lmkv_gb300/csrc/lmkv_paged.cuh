@@ -271,6 +271,23 @@ int allow_smem() {
     return rc;
 }
 
+// Has a kernel that needs little shared memory run with as much of it set aside as kernels
+// that fill it: an SM changes that only when it is idle, so the next one's blocks would otherwise not all fit
+// beside what is left of this one (once per device).
+template <auto kKernel>
+int keep_carveout() {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    const cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return lmkv_internal_cuda_status(err);
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return LMKV_OK;
+    const int rc = lmkv_internal_cuda_status(cudaFuncSetAttribute(kKernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                                                  cudaSharedmemCarveoutMaxShared));
+    if (rc == LMKV_OK) done.fetch_or(bit, std::memory_order_relaxed);
+    return rc;
+}
+
 // Checks of the host arguments that the operators have in common.
 inline bool type_fits(const lmkv_pool_t* pool, int32_t dtype) {
     return ((dtype == LMKV_BF16 || dtype == LMKV_FP16) && pool->elem_bytes == 2) ||

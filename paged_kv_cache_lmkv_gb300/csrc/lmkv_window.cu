@@ -142,6 +142,9 @@ __device__ __forceinline__ uint4 lds128(uint32_t at) {
     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
     return v;
 }
+__device__ __forceinline__ void sts128(uint32_t at, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
 __device__ __forceinline__ uint2 lds64(uint32_t at) {
     uint2 v;
     asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
@@ -679,7 +682,10 @@ __global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant_
 using namespace lmkv_tc;
 
 constexpr int kTileRows = 256;        // two tiles of 128 rows share every K and V block
-constexpr int kLoaders = 3;           // warps that bring K and V
+constexpr int kLoaders = 7;           // warps that bring K and V
+// Registers of a softmax thread and of the others: 256 of each share the launch's 512 x 128.
+constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
+static_assert(kSoftmaxRegs + kOtherRegs == 2 * 128, "what one half gives, the other takes");
 constexpr int kTileThreads = (8 + kLoaders + 1) * 32;
 constexpr int kUnits = kBlock / kChunk;         // of 16 keys, in a block
 constexpr int kInfoSlots = 8;
@@ -692,6 +698,10 @@ struct WindowTile {
     static constexpr int kSmem = (2 + kStages) * kStageBytes;
 };
 
+__device__ __forceinline__ void turn_to_loaders() {
+    asm volatile("barrier.cta.arrive 1, %0;" ::"n"((8 + kLoaders) * 32) : "memory");
+}
+
 // Rows of one request, (token, head of the group) in token order, 256 to a CTA,
 // against the keys that they see, in blocks of 128.  Products and powers are both near their limits, so the two
 // tiles of 128 rows take turns: while the tensor core works on one tile's
@@ -699,23 +709,24 @@ struct WindowTile {
 //   warps 0-3, 4-7   softmax of tile 0, 1: a thread holds a row.  Scores come
 //                    from tensor memory, weights go back over them as the next
 //                    product's first operand; the output stays in tensor memory until the end.
-//   warps 8-10       K and V in units of 16 rows (one page's) into a ring in shared memory that
+//   warps 8-14       K and V in units of 16 rows (one page's) into a ring in shared memory that
 //                    both tiles read: codes through registers, where they become fp16, 16-bit rows by cp.async
-//   warp 11          one thread issues every product
+//   warp 15          one thread issues every product
 // A unit's scales are the same for its 16 keys: a factor and an addend of the exponent's multiply-add.
 // Tensor memory: scores of tile 0, 1 at columns 0, 128; outputs at 256, 384.
 template <class T, class KV, int D>
 __global__ void __launch_bounds__(kTileThreads, 1)
 window_tiles_kernel(const __grid_constant__ WindowParams p) {
-    using S = WindowTile<D>;
     constexpr bool kCodes = sizeof(KV) == 1;
+    using S = WindowTile<D>;
     using M = typename std::conditional<kCodes, __half, T>::type;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint64_t bars[2 * S::kStages + 8];
     __shared__ uint32_t tmem_base;
     __shared__ int gave_up;
     __shared__ int32_t place[2];
-    __shared__ uint32_t infos[kInfoSlots][kUnits];       // which of a unit's keys there are, K's and V's scale bytes
+    __shared__ __align__(16) uint16_t masks[kInfoSlots][kUnits];      // which of a unit's keys there are
+    __shared__ float4 powers[kCodes ? kInfoSlots : 1][kUnits];        // its scale of K; V's as power, and inverse
     pdl_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t full = smem_u32(bars), empty = full + 8 * S::kStages, s_full = empty + 8 * S::kStages,
@@ -772,57 +783,78 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
         }
 
         if (warp < 8) {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
             const int t = warp >> 2;
             const int32_t R = row0 + tid;
             const bool live = R < req_rows;
             const int32_t n = (int32_t)p.by_group.div((uint32_t)(live ? R : row0));
             const int32_t tok = req.q0 + n, head = h * group + ((live ? R : row0) - n * group);
+            if (t >= tiles) turn_to_loaders();
             if (t < tiles) {
-                // my row of q, negated for a negative scale, into shared memory
-                const T* src = p.q.row<T>(tok, head);
-                const uint32_t dst = q_smem + t * S::kStageBytes + (tid & 127) * 128;
-                const uint32_t flip = p.scale_sign < 0 ? 0x80008000u : 0u, all = p.scale_sign == 0 || !live ? 0u : ~0u;
-                uint4 qv[D / 8];              // all loads on their way before the first is waited for
-                if (p.q_vec) {
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c) qv[c] = *reinterpret_cast<const uint4*>(src + c * 8);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c)
-                        qv[c] = make_uint4(load_pair(src + c * 8, p.q_pairs), load_pair(src + c * 8 + 2, p.q_pairs),
-                                           load_pair(src + c * 8 + 4, p.q_pairs), load_pair(src + c * 8 + 6, p.q_pairs));
-                }
-                float factor = p.scale_log2, by = 1.f;
-                if constexpr (kCodes) {
-                    // as fp16 with its largest element between 2^14 and 2^15
-                    float top = 0.f;
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c) {
-                        const T* const e = reinterpret_cast<const T*>(&qv[c]);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float a = fabsf(Elem<T>::to_float(e[i]));
-                            if (a < INFINITY) top = fmaxf(top, a);
-                        }
+                // The warp's rows of q into shared memory, 16 bytes a lane side by side.  (This and the end run once,
+                // out of memory that holds no instructions of theirs any more: loops, not lines, keep them
+                // short.  Unrolled, the rows took 31,000 cycles.)
+                constexpr int kRowLanes = D / 8, kSide = 32 / kRowLanes;
+                const uint32_t dst = q_smem + t * S::kStageBytes + (warp & 3) * (32 * 128);
+                const int piece = lane % kRowLanes;
+                auto row_at = [&](int i, int32_t& token, int32_t& hd) {      // the i-th row of this lane's; its place in dst
+                    const int r = i * kSide + lane / kRowLanes;
+                    const int32_t at = row0 + warp * 32 + r;
+                    const int32_t of = (int32_t)p.by_group.div((uint32_t)at);
+                    token = at < req_rows ? req.q0 + of : -1;
+                    hd = h * group + (at - of * group);
+                    return dst + (piece >> 3) * S::kHalfBytes + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
+                };
+#pragma unroll 1
+                for (int i = 0; i < kRowLanes; ++i) {
+                    int32_t token, hd;
+                    const uint32_t at = row_at(i, token, hd);
+                    const bool on = token >= 0 && p.scale_sign != 0;
+                    const T* const src = p.q.row<T>(on ? token : req.q0, hd) + piece * 8;
+                    if (p.q_vec) {
+                        cp_async16(at, src, on);
+                    } else {
+                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                        if (on) v = make_uint4(load_pair(src, p.q_pairs), load_pair(src + 2, p.q_pairs),
+                                               load_pair(src + 4, p.q_pairs), load_pair(src + 6, p.q_pairs));
+                        sts128(at, v);
                     }
-                    const int e = top > 0.f ? max((int)(__float_as_uint(top) >> 23) - 127, -100) : 0;
-                    by = power_of_two(14 - e);
-                    factor *= power_of_two(e - 14);
                 }
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    uint4 v = qv[c];
+                cp_commit();
+                turn_to_loaders();
+                cp_wait<0>();
+                __syncwarp();
+                float factor = p.scale_log2;
+                auto my_piece = [&](int c) { return dst + (c >> 3) * S::kHalfBytes + lane * 128 + (((c & 7) ^ (lane & 7)) << 4); };
+                if (kCodes || p.scale_sign < 0) {
+                    // my row: negated for a negative scale, and beside codes as fp16 with its largest element
+                    // between 2^14 and 2^15
+                    float by = p.scale_sign < 0 ? -1.f : 1.f;
                     if constexpr (kCodes) {
-                        const T* const e = reinterpret_cast<const T*>(&qv[c]);
-                        v.x = Elem<__half>::pack(Elem<T>::to_float(e[0]) * by, Elem<T>::to_float(e[1]) * by);
-                        v.y = Elem<__half>::pack(Elem<T>::to_float(e[2]) * by, Elem<T>::to_float(e[3]) * by);
-                        v.z = Elem<__half>::pack(Elem<T>::to_float(e[4]) * by, Elem<T>::to_float(e[5]) * by);
-                        v.w = Elem<__half>::pack(Elem<T>::to_float(e[6]) * by, Elem<T>::to_float(e[7]) * by);
+                        float top = 0.f;
+#pragma unroll 1
+                        for (int c = 0; c < kRowLanes; ++c) {
+                            const uint4 v = lds128(my_piece(c));
+                            const T* const e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const float a = fabsf(Elem<T>::to_float(e[j]));
+                                if (a < INFINITY) top = fmaxf(top, a);
+                            }
+                        }
+                        const int x = top > 0.f ? max((int)(__float_as_uint(top) >> 23) - 127, -100) : 0;
+                        by *= power_of_two(14 - x);
+                        factor *= power_of_two(x - 14);
                     }
-                    const uint32_t at = dst + (c >> 3) * S::kHalfBytes + (((c & 7) ^ (tid & 7)) << 4);
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"((v.x ^ flip) & all),
-                                 "r"((v.y ^ flip) & all), "r"((v.z ^ flip) & all), "r"((v.w ^ flip) & all)
-                                 : "memory");
+#pragma unroll 1
+                    for (int c = 0; c < kRowLanes; ++c) {
+                        const uint4 v = lds128(my_piece(c));
+                        const T* const e = reinterpret_cast<const T*>(&v);
+                        sts128(my_piece(c), make_uint4(Elem<M>::pack(Elem<T>::to_float(e[0]) * by, Elem<T>::to_float(e[1]) * by),
+                                                       Elem<M>::pack(Elem<T>::to_float(e[2]) * by, Elem<T>::to_float(e[3]) * by),
+                                                       Elem<M>::pack(Elem<T>::to_float(e[4]) * by, Elem<T>::to_float(e[5]) * by),
+                                                       Elem<M>::pack(Elem<T>::to_float(e[6]) * by, Elem<T>::to_float(e[7]) * by)));
+                    }
                 }
                 fence_async_shared();
                 __syncwarp();
@@ -848,39 +880,33 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                         if (j > 0) mbar_arrive(empty + 8 * ((2 * j - 1) % S::kStages));
                     }
                     fence_after_sync();
-                    const uint32_t* const info = infos[(b - b0) % kInfoSlots];
-                    uint32_t every = 0xFFFFu;
-#pragma unroll
-                    for (int u = 0; u < kUnits; ++u) every &= info[u];
+                    const int slot_of = (b - b0) % kInfoSlots;
+                    const uint4 words = *reinterpret_cast<const uint4*>(masks[slot_of]);
                     const bool whole = __all_sync(0xFFFFFFFFu, end - k >= kBlock && (begin <= k || k + kBlock <= p.sinks)) &&
-                                       (every & 0xFFFFu) == 0xFFFFu;
+                                       (words.x & words.y & words.z & words.w) == ~0u;
                     // scores of 32 keys, those not seen as -infinity
                     auto below = [](int32_t n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; };
                     auto take = [&](uint32_t (&x)[32], int i) {
                         if (whole) return;
                         const int32_t at = k + 32 * i;
-                        const uint32_t bits = ((info[2 * i] & 0xFFFFu) | (info[2 * i + 1] << 16)) & below(end - at) &
-                                              (~below(begin - at) | below(p.sinks - at));
+                        const uint32_t bits = (i == 0 ? words.x : i == 1 ? words.y : i == 2 ? words.z : words.w) &
+                                              below(end - at) & (~below(begin - at) | below(p.sinks - at));
+                        if (__all_sync(0xFFFFFFFFu, bits == ~0u)) return;
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if (!((bits >> j) & 1)) x[j] = 0xFF800000u;
                     };
-                    // a unit's factor (never 0: -infinity is to stay that) and addend
-                    auto factor_of = [&](int u) {
-                        if constexpr (!kCodes) return factor;
-                        const float f = factor * power_of_two((int)((info[u] >> 16) & 0xFF) - 127);
-                        return f != f ? f : fmaxf(f, 0x1p-126f);
-                    };
-                    auto power_of = [&](int u) {
-                        if constexpr (!kCodes) return 0.f;
-                        const int e = (int)(info[u] >> 24);
-                        return e == 255 ? NAN : (float)(e - 127);
+                    // a unit's factor (never 0: -infinity is to stay that)
+                    auto factor_of = [&](const float4& u) { return kCodes ? fmaxf(factor * u.x, 0x1p-126f) : factor; };
+                    auto powers_of = [&](int u) {
+                        return kCodes ? powers[kCodes ? slot_of : 0][u] : make_float4(1.f, 0.f, 1.f, 0.f);
                     };
                     uint32_t x[4][32];
                     float mx = -INFINITY;
                     tmem_ld32(x[0], s_at);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
+                        const float4 of[2] = {powers_of(2 * i), powers_of(2 * i + 1)};
                         wait_ld();
                         loaded(x[i]);
                         if (i < 3) tmem_ld32(x[i + 1], s_at + 32 * (i + 1));
@@ -894,7 +920,7 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                                     a = max3(a, __uint_as_float(x[i][j]), __uint_as_float(x[i][j + 1]));
                                     c = max3(c, __uint_as_float(x[i][j + 2]), __uint_as_float(x[i][j + 3]));
                                 }
-                                mx = fmaxf(mx, fmaf(fmaxf(a, c), factor_of(2 * i + u), power_of(2 * i + u)));
+                                mx = fmaxf(mx, fmaf(fmaxf(a, c), factor_of(of[u]), of[u].y));
                             }
                         } else {
                             float a = -INFINITY, c = -INFINITY;
@@ -921,12 +947,15 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                         }
                     }
                     const float neg = m == -INFINITY ? 0.f : kBelow - m;
+                    float4 next = powers_of(0);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t w[16];
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
-                            const float f = factor_of(2 * i + u), a = neg + power_of(2 * i + u);
+                            const float4 of = next;
+                            if (2 * i + u + 1 < kUnits) next = powers_of(2 * i + u + 1);
+                            const float f = factor_of(of), a = neg + of.y;
                             const float2 f2 = make_float2(f, f), a2 = make_float2(a, a);
                             float2 s0 = make_float2(0.f, 0.f), s1 = s0;
 #pragma unroll
@@ -941,8 +970,7 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                                 w[j] = Elem<M>::pack(e.x, e.y);
                             }
                             if constexpr (kCodes) {
-                                const float back = power_of_two(127 - (int)(info[2 * i + u] >> 24));
-                                l2 = fma2(add2(s0, s1), make_float2(back, back), l2);
+                                l2 = fma2(add2(s0, s1), make_float2(of.z, of.z), l2);
                             } else {
                                 l2 = add2(l2, add2(s0, s1));
                             }
@@ -966,44 +994,45 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                     const int64_t at = (int64_t)part * p.rows + row;
                     const float ref = m == -INFINITY ? -INFINITY : m - kBelow;
                     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-                    T* const out = p.out.row<T>(tok, head);
 #pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t y[32];
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t y[16];
                         if (b1 > b0) {
-                            tmem_ld32(y, o_at + 32 * c);
-                            wait_ld();
-                            loaded(y);
+                            tmem_ld16(y, o_at + c);
                         } else {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) y[j] = 0u;
+                            for (int j = 0; j < 16; ++j) y[j] = 0u;
                         }
-                        if (!live) continue;
                         if (final) {
+                            // over my row of q, which no product reads any more
 #pragma unroll
-                            for (int j = 0; j < 32; j += 8) {
-                                uint32_t w[4];
+                            for (int j = 0; j < 16; j += 8)
+                                sts128(my_piece((c + j) >> 3),
+                                       make_uint4(Elem<T>::pack(__uint_as_float(y[j]) * inv, __uint_as_float(y[j + 1]) * inv),
+                                                  Elem<T>::pack(__uint_as_float(y[j + 2]) * inv, __uint_as_float(y[j + 3]) * inv),
+                                                  Elem<T>::pack(__uint_as_float(y[j + 4]) * inv, __uint_as_float(y[j + 5]) * inv),
+                                                  Elem<T>::pack(__uint_as_float(y[j + 6]) * inv, __uint_as_float(y[j + 7]) * inv)));
+                        } else if (live) {
 #pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    w[i] = Elem<T>::pack(__uint_as_float(y[j + 2 * i]) * inv,
-                                                         __uint_as_float(y[j + 2 * i + 1]) * inv);
-                                T* dst = out + 32 * c + j;
-                                if (p.out_vec) {
-                                    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-                                } else {
-                                    uint16_t* d16 = reinterpret_cast<uint16_t*>(dst);
+                            for (int j = 0; j < 16; j += 4)
+                                *reinterpret_cast<uint4*>(p.part_o + at * D + c + j) = make_uint4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+                        }
+                    }
+                    if (final) {
+                        __syncwarp();
+#pragma unroll 1
+                        for (int i = 0; i < kRowLanes; ++i) {
+                            int32_t token, hd;
+                            const uint4 v = lds128(row_at(i, token, hd));
+                            if (token < 0) break;
+                            T* const to = p.out.row<T>(token, hd) + piece * 8;
+                            if (p.out_vec) {
+                                *reinterpret_cast<uint4*>(to) = v;
+                            } else {
+                                const uint16_t* const e = reinterpret_cast<const uint16_t*>(&v);
 #pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        d16[2 * i] = (uint16_t)w[i];
-                                        d16[2 * i + 1] = (uint16_t)(w[i] >> 16);
-                                    }
-                                }
+                                for (int j = 0; j < 8; ++j) reinterpret_cast<uint16_t*>(to)[j] = e[j];
                             }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; j += 4)
-                                *reinterpret_cast<uint4*>(p.part_o + at * D + 32 * c + j) =
-                                    make_uint4(y[j], y[j + 1], y[j + 2], y[j + 3]);
                         }
                     }
                     if (live && final && p.lse != nullptr)
@@ -1011,77 +1040,110 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                     if (live && !final) p.part_ml[at] = make_float2(ref, l);
                 }
             }
-        } else if (warp < 8 + kLoaders) {
+        } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp < 8 + kLoaders) {
             // Unit u of the CTA is rows 16 (u % 8) .. of item u / 8 (K, V of a block in turn); warp
-            // 8 + i takes units i, i + 3, ..
+            // 8 + i takes units i, i + 3, ..  Lane i < 8 holds what there is to know of unit i of a block, table
+            // entries fetched two blocks ahead and scales one, so that nothing is waited for.
             const int32_t* const table = p.seqs.table + (int64_t)req.r * p.seqs.table_stride;
             const uint32_t row_bytes = (uint32_t)p.layer.row_bytes;
             const int64_t half_bytes = p.layer.half_bytes();
             constexpr int kRowBytes = D * (int)sizeof(KV), kPieces = kRowBytes / 16, kRowsPer = 32 / kPieces;
             constexpr int kCopies = kChunk / kRowsPer;
             const int c = lane % kPieces, rsub = lane / kPieces;
-            const uint8_t* const mine = base + (int64_t)h * kRowBytes + c * 16;
-            const int32_t all_units = (b1 - b0) * 2 * kUnits;
-            struct Unit {
-                int32_t k;                // its first key
-                int32_t blk;
-                uint32_t rows;            // which of its rows there are
+            const uint8_t* const mine = base + (int64_t)h * kRowBytes + c * 16 + (int64_t)rsub * row_bytes;
+            const int32_t blocks = b1 - b0, all_units = blocks * 2 * kUnits;
+            struct Entry {
+                int32_t k, blk;           // the unit's first key, its page
+                uint32_t rows;            // which of its rows some row of the tile sees
             };
-            auto look = [&](int32_t u) {
-                Unit x{0, -1, 0};
-                if (u >= all_units) return x;
-                x.k = seen.unit(b0 + u / (2 * kUnits)) * kBlock + u % kUnits * kChunk;
-                // keys [0, sink_end) and [lo, end) are seen
-                auto below = [](int32_t n) { return n >= 16 ? 0xFFFFu : n <= 0 ? 0u : (1u << n) - 1u; };
-                x.rows = below(seen.end - x.k) & (below(seen.sink_end - x.k) | ~below(seen.lo - x.k));
-                if (x.rows != 0) x.blk = table[p.layer.column(x.k)];
+            auto look = [&](int32_t b) {
+                Entry x{0, 0, 0};
+                if (b < blocks && lane < kUnits) {
+                    x.k = seen.unit(b0 + b) * kBlock + lane * kChunk;
+                    // keys [0, sink_end) and [lo, end) are seen
+                    auto below = [](int32_t n) { return n >= 16 ? 0xFFFFu : n <= 0 ? 0u : (1u << n) - 1u; };
+                    x.rows = below(seen.end - x.k) & (below(seen.sink_end - x.k) | ~below(seen.lo - x.k));
+                    if (x.rows != 0) x.blk = table[p.layer.column(x.k)];
+                }
                 return x;
             };
-            auto check = [&](Unit& x) {
+            uint32_t row = 0, held = 0;   // of the block at hand: the unit's first row of the K half; its rows, K's and V's scale bytes
+            uint32_t next_row = 0, next_held = 0;
+            Entry ahead = look(0);
+            int32_t at_block = -1;
+            auto advance = [&] {
+                row = next_row;
+                held = next_held;
+                Entry x = ahead;
+                ahead = look(at_block + 3);
                 if (x.rows != 0 && (x.blk < 0 || x.blk >= p.layer.num_blocks)) {
-                    if (lane == 0) report(p.status, LMKV_ERR_BAD_BLOCK);
+                    report(p.status, LMKV_ERR_BAD_BLOCK);
                     x.rows = 0;
                 }
+                next_row = x.rows != 0 ? p.layer.row_of(x.blk, x.k, p.layer.column(x.k)) : 0u;
+                next_held = 0x7F7F0000u;
+                if (kCodes && x.rows != 0)
+                    next_held = ((uint32_t)scales[p.scales.at(0, x.blk, h)] << 16) |
+                                ((uint32_t)scales[p.scales.at(1, x.blk, h)] << 24);
+                next_held |= x.rows;
+                ++at_block;
             };
-            auto source = [&](const Unit& x, bool v) {
-                return mine + (v ? half_bytes : 0) + ((uint64_t)p.layer.row_of(x.blk, x.k, p.layer.column(x.k)) + rsub) * row_bytes;
+            if (blocks > 0) {
+                // (the first blocks' entries are waited for)
+                --at_block;
+                advance();
+            }
+            // What there is to know of unit u, and where this lane's part of it is.
+            struct Unit {
+                uint32_t held;
+                const uint8_t* src;
+                __device__ __forceinline__ bool on(int row) const { return (held >> row) & 1; }
+            };
+            auto find = [&](int32_t u) {
+                while (at_block < u / (2 * kUnits)) advance();
+                const uint32_t first = __shfl_sync(0xFFFFFFFFu, row, u % kUnits);
+                return Unit{__shfl_sync(0xFFFFFFFFu, held, u % kUnits),
+                            mine + (u / kUnits % 2 != 0 ? half_bytes : 0) + (uint64_t)first * row_bytes};
             };
             auto enter = [&](int32_t u) {      // the unit's stage is free
                 const int32_t item = u / kUnits, st = item % S::kStages;
                 return item < S::kStages || mbar_wait(empty + 8 * st, (item / S::kStages - 1) & 1, &gave_up);
             };
-            auto tell = [&](int32_t u, const Unit& x, uint32_t bytes) {
-                if (u / kUnits % 2 == 0 && lane == 0) infos[u / (2 * kUnits) % kInfoSlots][u % kUnits] = x.rows | bytes;
-            };
             const int32_t u_first = warp - 8;
-            bool ok = true;
+            // q's copies go first: K and V, a ring of them, would stand before them in the queue
+            bar_sync(1, (8 + kLoaders) * 32);
             if constexpr (kCodes) {
-                // three units on their way in registers, the table entries of one more
-                constexpr int kDeep = 3;
-                uint4 raw[kDeep][kCopies];
-                Unit unit[kDeep];
-                uint32_t bytes[kDeep];
-                Unit next = look(u_first);
+                // a unit on its way in registers while one goes to shared memory
+                constexpr int kDeep = 2;
+                uint4 codes[kDeep][kCopies];
+                uint32_t on_way[kDeep];
                 auto start = [&](int s, int32_t u) {
-                    unit[s] = next;
-                    check(unit[s]);
-                    next = look(u + kLoaders);
-                    bytes[s] = 0x7F7F0000u;
-                    const bool v = u / kUnits % 2 != 0;
-                    if (unit[s].rows == 0) return;
-                    const uint8_t* const src = source(unit[s], v);
+                    if (u >= all_units) return;
+                    const Unit x = find(u);
+                    on_way[s] = x.held;
 #pragma unroll
                     for (int r = 0; r < kCopies; ++r) {
-                        raw[s][r] = make_uint4(0u, 0u, 0u, 0u);
-                        if ((unit[s].rows >> (r * kRowsPer + rsub)) & 1)
-                            raw[s][r] = *reinterpret_cast<const uint4*>(src + r * kRowsPer * row_bytes);
+                        codes[s][r] = make_uint4(0u, 0u, 0u, 0u);
+                        if (x.on(r * kRowsPer + rsub))
+                            codes[s][r] = *reinterpret_cast<const uint4*>(x.src + r * kRowsPer * row_bytes);
                     }
-                    if (!v)
-                        bytes[s] = ((uint32_t)scales[p.scales.at(0, unit[s].blk, h)] << 16) |
-                                   ((uint32_t)scales[p.scales.at(1, unit[s].blk, h)] << 24);
                 };
+                // Of a lane's 16 codes the fp16 values are two pieces of a row: those of its two halves in turn, so
+                // that they meet no bank twice.
+                const bool odd = D == 128 && (c >> 2) != 0;
+                const uint32_t to = kv_smem + (D == 128 ? (c >> 2) * S::kHalfBytes : 0) + rsub * 128;
+                uint32_t place_of[2][2];       // of the even and odd copies' pieces
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        place_of[r][i] = to + ((((2 * c + (i ^ (odd ? 1 : 0))) & 7) ^ ((r * kRowsPer + rsub) & 7)) << 4);
 #pragma unroll
                 for (int s = 0; s < kDeep - 1; ++s) start(s, u_first + s * kLoaders);
+                bool ok = true;
+#pragma unroll 1
                 for (int32_t u0 = u_first; u0 < all_units && ok; u0 += kDeep * kLoaders) {
 #pragma unroll
                     for (int s = 0; s < kDeep; ++s) {
@@ -1090,55 +1152,50 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                         start((s + kDeep - 1) % kDeep, u + (kDeep - 1) * kLoaders);
                         ok = enter(u);
                         if (!ok) break;
-                        tell(u, unit[s], bytes[s]);
-                        const uint32_t dst = kv_smem + u / kUnits % S::kStages * S::kStageBytes + u % kUnits * (kChunk * 128);
+                        const uint32_t of = on_way[s];
+                        if (u / kUnits % 2 == 0 && lane == 0) {
+                            const int slot_of = u / (2 * kUnits) % kInfoSlots;
+                            masks[slot_of][u % kUnits] = (uint16_t)of;
+                            // (a scale of NaN makes its keys' exponents NaN)
+                            const int kb = (int)((of >> 16) & 0xFF), vb = (int)(of >> 24);
+                            powers[slot_of][u % kUnits] =
+                                make_float4(power_of_two(kb - 127), kb == 255 || vb == 255 ? NAN : (float)(vb - 127),
+                                            power_of_two(127 - vb), 0.f);
+                        }
+                        const uint32_t dst = u / kUnits % S::kStages * S::kStageBytes + u % kUnits * (kChunk * 128);
 #pragma unroll
                         for (int r = 0; r < kCopies; ++r) {
-                            const uint4 v = unit[s].rows != 0 ? raw[s][r] : make_uint4(0u, 0u, 0u, 0u);
-                            uint32_t e[8];
-                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                            const uint4 v = codes[s][r];
+                            const uint32_t w[4] = {odd ? v.z : v.x, odd ? v.w : v.y, odd ? v.x : v.z, odd ? v.y : v.w};
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                e[2 * i] = codes_to_half2((uint16_t)w[i]);
-                                e[2 * i + 1] = codes_to_half2((uint16_t)(w[i] >> 16));
-                            }
-                            const int row = r * kRowsPer + rsub;
-                            const uint32_t at = dst + (D == 128 ? (c >> 2) * S::kHalfBytes : 0) + row * 128;
-                            // (pieces of the two halves in turn, so that they meet no bank twice)
-                            const int odd = D == 128 ? c >> 2 : 0;
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int which = i ^ odd;
-                                const uint32_t to = at + ((((2 * c + which) & 7) ^ (row & 7)) << 4);
-                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(which ? e[4] : e[0]),
-                                             "r"(which ? e[5] : e[1]), "r"(which ? e[6] : e[2]), "r"(which ? e[7] : e[3])
-                                             : "memory");
-                            }
+                            for (int i = 0; i < 2; ++i)
+                                sts128(place_of[r & 1][i] + dst + r * (kRowsPer * 128),
+                                       make_uint4(codes_to_half2((uint16_t)w[2 * i]), codes_to_half2((uint16_t)(w[2 * i] >> 16)),
+                                                  codes_to_half2((uint16_t)w[2 * i + 1]),
+                                                  codes_to_half2((uint16_t)(w[2 * i + 1] >> 16))));
                         }
-                        fence_async_shared();
                         __syncwarp();
+                        // (the products' thread has the writes seen by the tensor core, once for an item)
                         if (lane == 0) mbar_arrive(full + 8 * (u / kUnits % S::kStages));
                     }
                 }
             } else {
-                Unit next = look(u_first);
-                for (int32_t u = u_first; u < all_units && ok; u += kLoaders) {
-                    Unit x = next;
-                    check(x);
-                    next = look(u + kLoaders);
-                    ok = enter(u);
-                    if (!ok) break;
-                    tell(u, x, 0x7F7F0000u);
+#pragma unroll 1
+                for (int32_t u = u_first; u < all_units; u += kLoaders) {
+                    if (!enter(u)) break;
                     const uint32_t stage = u / kUnits % S::kStages;
-                    const uint32_t dst = kv_smem + stage * S::kStageBytes + u % kUnits * (kChunk * 128) +
-                                         (c >> 3) * S::kHalfBytes;
-                    const uint8_t* const src = x.rows != 0 ? source(x, u / kUnits % 2 != 0) : base;
+                    const uint32_t dst = kv_smem + stage * S::kStageBytes + u % kUnits * (kChunk * 128) + (c >> 3) * S::kHalfBytes;
+                    const Unit x = find(u);
+                    const bool all = (x.held & 0xFFFFu) == 0xFFFFu;
 #pragma unroll
                     for (int r = 0; r < kCopies; ++r) {
-                        const int row = r * kRowsPer + rsub;
-                        const bool on = (x.rows >> row) & 1;
-                        cp_async16(dst + row * 128 + (((c & 7) ^ (row & 7)) << 4), on ? src + r * kRowsPer * row_bytes : base, on);
+                        const int i = r * kRowsPer + rsub;
+                        const uint32_t at = dst + i * 128 + (((c & 7) ^ (i & 7)) << 4);
+                        if (all) cp_async16(at, x.src + r * kRowsPer * row_bytes);
+                        else cp_async16(at, x.on(i) ? x.src + r * kRowsPer * row_bytes : base, x.on(i));
                     }
+                    if (u / kUnits % 2 == 0 && lane == 0)
+                        masks[u / (2 * kUnits) % kInfoSlots][u % kUnits] = (uint16_t)x.held;
                     copies_arrive(full + 8 * stage);
                 }
                 asm volatile("cp.async.wait_all;" ::: "memory");
@@ -1213,6 +1270,7 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                 advance(ks, kph);
             }
         }
+        }
     }
     __syncwarp();
     fence_before_sync();
@@ -1284,6 +1342,10 @@ int window_typed(const WindowParams& p, const Plan& x, void* stream) {
     int rc = allow_smem<window_streams_kernel<T, KV, D, 1>, Sh::kSmem>();
     if (rc == LMKV_OK) rc = allow_smem<window_streams_kernel<T, KV, D, 2>, Sh::kSmem>();
     if (rc == LMKV_OK) rc = allow_smem<window_tiles_kernel<T, KV, D>, WindowTile<D>::kSmem>();
+    if (rc == LMKV_OK) rc = keep_carveout<window_streams_kernel<T, KV, D, 1>>();
+    if (rc == LMKV_OK) rc = keep_carveout<window_streams_kernel<T, KV, D, 2>>();
+    if (rc == LMKV_OK) rc = keep_carveout<window_join_kernel<T, D, false>>();
+    if (rc == LMKV_OK) rc = keep_carveout<window_join_kernel<T, D, true>>();
     if (rc == LMKV_OK && x.big_rows < INT32_MAX)
         rc = launch(window_tiles_kernel<T, KV, D>, (int64_t)x.slots * p.kv_heads * x.parts, kTileThreads,
                     WindowTile<D>::kSmem, stream, 1, p);
