@@ -34,106 +34,179 @@ struct NormedParams {
     int32_t kv_ctas;           // CTAs of pages; those after them: a token's q
     int32_t head_sets;         // of kHeads heads, of K and of V
     float eps;
-    bool vec_q, vec_out, vec_k, vec_v;      // rows of 16-byte vectors
-    bool shuffles;             // a turned element's partner is a whole number of vectors away
+    bool vectors;              // a lane's pairs are two vectors of eight elements
+    bool vec_q, vec_out, vec_k, vec_v;      // and the rows allow loads of those
     FastDiv by_sets;
     Rotary rot;                // half == 0: none
 };
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kHeads = 4;      // heads of a page's CTA
 constexpr int kPer = 4;        // rows of a thread on their way together
 
-// A row of D elements lies with D / 8 neighbouring lanes, eight elements each.
-template <class T, int D>
-struct RowOf {
-    T raw[8];
+// A row of D elements lies with D / 16 neighbouring lanes, eight pairs each: pair n = 8 l + i is lane l's i-th.
+// The pairs that turn come first, then the other elements two by two.  In the half layout pair n is elements
+// (n, n + half), so where half is a multiple of 8 a lane's pairs are two vectors, the i-th of one with the i-th of
+// the other, and no lane needs another's elements; interleaved it is (2n, 2n + 1), in two vectors too.
+template <int D, bool kInterleaved>
+struct Pairs {
+    static constexpr int kLanes = D / 16;
+    static __device__ __forceinline__ int first(const NormedParams& p, int n) {
+        if (kInterleaved) return 2 * n;
+        if (n < p.rot.half) return n;
+        return p.vectors ? (n & ~7) * 2 + (n & 7) : 2 * n;
+    }
+    static __device__ __forceinline__ int second(const NormedParams& p, int n) {
+        if (kInterleaved) return 2 * n + 1;
+        if (n < p.rot.half) return n + p.rot.half;
+        return p.vectors ? (n & ~7) * 2 + 8 + (n & 7) : 2 * n + 1;
+    }
+    // Where lane l's two vectors begin.
+    static __device__ __forceinline__ int first_vector(const NormedParams& p, int l) {
+        return !kInterleaved && 8 * l < p.rot.half ? 8 * l : 16 * l;
+    }
+    static __device__ __forceinline__ int second_vector(const NormedParams& p, int l) {
+        return !kInterleaved && 8 * l < p.rot.half ? 8 * l + p.rot.half : 16 * l + 8;
+    }
+    // Pair n's place in a token's table: lanes side by side.
+    static __device__ __forceinline__ int place(int n) { return (n & 7) * kLanes + (n >> 3); }
+};
 
-    __device__ __forceinline__ void load(const T* row, int e0, bool vec) {
+// A lane's 16 elements of a row as they were loaded: the half layout's a_i, then its b_i; interleaved, pair by pair.
+template <class T, int D, bool kInterleaved>
+struct RowOf {
+    using P = Pairs<D, kInterleaved>;
+    uint32_t raw[8];
+
+    static __device__ __forceinline__ void ld16(const T* at, uint32_t& x, uint32_t& y, uint32_t& z, uint32_t& w) {
+        asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x), "=r"(y), "=r"(z), "=r"(w)
+                     : "l"(at) : "memory");
+    }
+    __device__ __forceinline__ void load(const NormedParams& p, const T* row, int l, bool vec) {
         if (vec) {
-            int4& r = *reinterpret_cast<int4*>(raw);
-            asm volatile("ld.global.L1::no_allocate.v4.s32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(row + e0) : "memory");
+            ld16(row + P::first_vector(p, l), raw[0], raw[1], raw[2], raw[3]);
+            ld16(row + P::second_vector(p, l), raw[4], raw[5], raw[6], raw[7]);
         } else {
+            const uint16_t* const e = reinterpret_cast<const uint16_t*>(row);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) raw[i] = row[e0 + i];
+            for (int i = 0; i < 8; i += 2) {
+                const uint32_t a = e[P::first(p, 8 * l + i)], b = e[P::second(p, 8 * l + i)];
+                const uint32_t c = e[P::first(p, 8 * l + i + 1)], d = e[P::second(p, 8 * l + i + 1)];
+                raw[kInterleaved ? i : i / 2] = a | ((kInterleaved ? b : c) << 16);
+                raw[kInterleaved ? i + 1 : 4 + i / 2] = (kInterleaved ? c : b) | (d << 16);
+            }
         }
     }
     __device__ __forceinline__ void clear() {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) raw[i] = Elem<T>::from_float(0.f);
+        for (int i = 0; i < 8; ++i) raw[i] = 0u;
+    }
+    __device__ __forceinline__ void take(float (&a)[8], float (&b)[8]) const {
+        const T* const x = reinterpret_cast<const T*>(raw);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            a[i] = Elem<T>::to_float(x[kInterleaved ? 2 * i : i]);
+            b[i] = Elem<T>::to_float(x[kInterleaved ? 2 * i + 1 : 8 + i]);
+        }
     }
 };
 
-// x / sqrt(mean(x^2) + eps) * norm, then turned by (cos, sin) cs[pair]; called by whole
-// warps.  row: the row in memory, for partners that no shuffle reaches.
-template <class T, int D>
-__device__ __forceinline__ void norm_and_turn(const NormedParams& p, const RowOf<T, D>& in, const T* row, const float* norm,
-                                              const float2* cs, float (&x)[8]) {
-    constexpr int kLanes = D / 8;
-    const int lane = threadIdx.x & 31, sub = lane % kLanes, e0 = sub * 8;
+// A token's table: pair n as (cos w_a, sin w_b, sin w_a, cos w_b), w the norm's weights.
+template <class T, int D, bool kInterleaved>
+__device__ __forceinline__ float4 table_entry(const NormedParams& p, const float* norm, int n, int64_t position) {
+    using P = Pairs<D, kInterleaved>;
+    const float wa = norm != nullptr ? norm[P::first(p, n)] : 1.f, wb = norm != nullptr ? norm[P::second(p, n)] : 1.f;
+    if (n >= p.rot.half) return make_float4(wa, 0.f, 0.f, wb);
+    float2 w = cos_sin<T>(p.rot.turns[n], position);
+    w.x *= p.rot.magnitude;
+    w.y *= p.rot.magnitude;
+    return make_float4(w.x * wa, w.y * wb, w.y * wa, w.x * wb);
+}
+
+// x / sqrt(mean(x^2) + eps) * norm, turned; called by whole warps.  table: the token's, from this lane's place on.
+template <class T, int D, bool kInterleaved>
+__device__ __forceinline__ void norm_and_turn(const NormedParams& p, const RowOf<T, D, kInterleaved>& in, int l, bool normed,
+                                              const float4* table, float (&a)[8], float (&b)[8]) {
+    constexpr int kLanes = D / 16;
+    in.take(a, b);
     float r = 1.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = Elem<T>::to_float(in.raw[i]);
-    if (norm != nullptr) {
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-        for (int d = kLanes / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
-        r = 1.f / sqrtf(ss * (1.f / D) + p.eps);
-        const float4 a = *reinterpret_cast<const float4*>(norm + e0), b = *reinterpret_cast<const float4*>(norm + e0 + 4);
-        const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= r * w[i];
-    }
-    const int half = p.rot.half;
-    if (half == 0) return;
-    if (p.rot.interleaved) {
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            if (e0 + i >= 2 * half) break;
-            const float2 w = cs[(e0 + i) >> 1];
-            const float a = x[i], b = x[i + 1];
-            x[i] = a * w.x - b * w.y;
-            x[i + 1] = a * w.y + b * w.x;
-        }
-    } else {
-        float y[8];            // the partners
-        if (p.shuffles) {
-            const int from = e0 < half ? lane + half / 8 : e0 < 2 * half ? lane - half / 8 : lane;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xFFFFFFFFu, x[i], from);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int e = e0 + i, to = e < half ? e + half : e < 2 * half ? e - half : e;
-                y[i] = row == nullptr ? 0.f : Elem<T>::to_float(row[to]) * (norm != nullptr ? r * norm[to] : 1.f);
-            }
-            __syncwarp();      // read before the row is written in place
-        }
+    if (normed) {
+        float s = 0.f, t = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int e = e0 + i;
-            if (e >= 2 * half) break;
-            const float2 w = cs[e < half ? e : e - half];
-            x[i] = e < half ? x[i] * w.x - y[i] * w.y : y[i] * w.y + x[i] * w.x;
+            s = fmaf(a[i], a[i], s);
+            t = fmaf(b[i], b[i], t);
+        }
+        s += t;
+#pragma unroll
+        for (int d = kLanes / 2; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+        r = rsqrtf(s * (1.f / D) + p.eps);        // (within 2^-22)
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float4 w = table[i * kLanes];
+        const bool turns = 8 * l + i < p.rot.half;         // others stay apart, whatever they hold
+        const float x = a[i], y = b[i];
+        a[i] = (turns ? x * w.x - y * w.y : x * w.x) * r;
+        b[i] = (turns ? x * w.z + y * w.w : y * w.w) * r;
+    }
+}
+
+// The lane's 16 values to a row of T.
+template <class T, int D, bool kInterleaved>
+__device__ __forceinline__ void store_row(const NormedParams& p, T* row, int l, const float (&a)[8], const float (&b)[8],
+                                          bool vec) {
+    using P = Pairs<D, kInterleaved>;
+    if (vec) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (kInterleaved) w[i] = Elem<T>::pack(a[i], b[i]);
+            else w[i] = i < 4 ? Elem<T>::pack(a[2 * i], a[2 * i + 1]) : Elem<T>::pack(b[2 * (i & 3)], b[2 * (i & 3) + 1]);
+        }
+        *reinterpret_cast<uint4*>(row + P::first_vector(p, l)) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(row + P::second_vector(p, l)) = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            row[P::first(p, 8 * l + i)] = Elem<T>::from_float(a[i]);
+            row[P::second(p, 8 * l + i)] = Elem<T>::from_float(b[i]);
+        }
+    }
+}
+// As codes of value * factor.
+template <int D, bool kInterleaved>
+__device__ __forceinline__ void store_codes(const NormedParams& p, uint8_t* row, int l, float (&a)[8], float (&b)[8], float factor) {
+    using P = Pairs<D, kInterleaved>;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        a[i] = fabsf(a[i]) < INFINITY ? a[i] * factor : NAN;
+        b[i] = fabsf(b[i]) < INFINITY ? b[i] * factor : NAN;
+    }
+    if (kInterleaved || p.vectors) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (kInterleaved)
+                w[i] = (uint32_t)floats_to_codes(a[2 * i], b[2 * i]) | ((uint32_t)floats_to_codes(a[2 * i + 1], b[2 * i + 1]) << 16);
+            else if (i < 2)
+                w[i] = (uint32_t)floats_to_codes(a[4 * i], a[4 * i + 1]) | ((uint32_t)floats_to_codes(a[4 * i + 2], a[4 * i + 3]) << 16);
+            else
+                w[i] = (uint32_t)floats_to_codes(b[4 * i - 8], b[4 * i - 7]) | ((uint32_t)floats_to_codes(b[4 * i - 6], b[4 * i - 5]) << 16);
+        }
+        *reinterpret_cast<uint2*>(row + P::first_vector(p, l)) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2*>(row + P::second_vector(p, l)) = make_uint2(w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint16_t c = floats_to_codes(a[i], b[i]);
+            row[P::first(p, 8 * l + i)] = (uint8_t)c;
+            row[P::second(p, 8 * l + i)] = (uint8_t)(c >> 8);
         }
     }
 }
 
-template <class T>
-__device__ __forceinline__ void store_row(T* dst, const float (&x)[8], bool vec) {
-    if (vec) {
-        *reinterpret_cast<uint4*>(dst) = make_uint4(Elem<T>::pack(x[0], x[1]), Elem<T>::pack(x[2], x[3]),
-                                                    Elem<T>::pack(x[4], x[5]), Elem<T>::pack(x[6], x[7]));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dst[i] = Elem<T>::from_float(x[i]);
-    }
-}
-
-// A token's request, cached number and position.
+// A token's cached number and position.
 struct Place {
     int32_t index;
     int64_t position;
@@ -141,20 +214,22 @@ struct Place {
 };
 
 // One token's heads of q.
-template <class T, int D>
-__device__ __forceinline__ void append_q(const NormedParams& p, int32_t t, float2* cs) {
-    constexpr int kLanes = D / 8, kGroups = kThreads / kLanes;
+template <class T, int D, bool kInterleaved>
+__device__ __forceinline__ void append_q(const NormedParams& p, int32_t t, float4* table) {
+    using P = Pairs<D, kInterleaved>;
+    constexpr int kGroups = kThreads / P::kLanes;
     __shared__ Place place;
-    const int sub = threadIdx.x % kLanes, g = threadIdx.x / kLanes;
-    RowOf<T, D> x[kPer];
+    const int l = threadIdx.x % P::kLanes, g = threadIdx.x / P::kLanes;
+    RowOf<T, D, kInterleaved> x[kPer];
     auto load = [&](int32_t h0) {
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
             const int32_t h = h0 + j * kGroups + g;
-            if (h < p.q_heads) x[j].load(p.q.row<T>(t, h), sub * 8, p.vec_q);
+            if (h < p.q_heads) x[j].load(p, p.q.row<T>(t, h), l, p.vec_q);
             else x[j].clear();
         }
     };
+    // the first rows are on their way before the look-ups
     load(0);
     if (threadIdx.x < 32) {
         const int32_t r = find_request(p.seqs.num_req, t, [&](int32_t i) { return p.seqs.q_start[i]; });
@@ -173,21 +248,19 @@ __device__ __forceinline__ void append_q(const NormedParams& p, int32_t t, float
     }
     __syncthreads();
     if (!place.live) return;
-    for (int i = threadIdx.x; i < p.rot.half; i += kThreads) {
-        const float2 w = cos_sin<T>(p.rot.turns[i], place.position);
-        cs[i] = make_float2(w.x * p.rot.magnitude, w.y * p.rot.magnitude);
-    }
+    for (int n = threadIdx.x; n < D / 2; n += kThreads)
+        table[P::place(n)] = table_entry<T, D, kInterleaved>(p, p.q_norm, n, place.position);
     __syncthreads();
+#pragma unroll 1
     for (int32_t h0 = 0; h0 < p.q_heads; h0 += kPer * kGroups) {
         if (h0 > 0) load(h0);
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
             const int32_t h = h0 + j * kGroups + g;
             if (h0 + j * kGroups >= p.q_heads) break;
-            const bool on = h < p.q_heads;
-            float y[8];
-            norm_and_turn<T, D>(p, x[j], on ? p.q.row<T>(t, h) : nullptr, p.q_norm, cs, y);
-            if (on) store_row<T>(p.q_out.row<T>(t, h) + sub * 8, y, p.vec_out);
+            float a[8], b[8];
+            norm_and_turn<T, D, kInterleaved>(p, x[j], l, p.q_norm != nullptr, table + l, a, b);
+            if (h < p.q_heads) store_row<T, D, kInterleaved>(p, p.q_out.row<T>(t, h), l, a, b, p.vec_out);
         }
     }
 }
@@ -203,9 +276,10 @@ constexpr int kLowest = -60, kHighest = 60;
 // The new tokens of one page: kHeads heads of K or of V.  A page's tokens of a head have to be seen
 // before the first is written, as they share a scale, so kHeads heads are spread over the
 // CTA token by token and meet in shared memory.  Pages of more tokens than fit its registers are read twice.
-template <class T, int D, bool kCodes>
-__device__ __forceinline__ void append_page(const NormedParams& p, int32_t cta, float2* cs) {
-    constexpr int kLanes = D / 8, kGroups = kThreads / kLanes;
+template <class T, int D, bool kCodes, bool kInterleaved>
+__device__ __forceinline__ void append_page(const NormedParams& p, int32_t cta, float4* table) {
+    using P = Pairs<D, kInterleaved>;
+    constexpr int kGroups = kThreads / P::kLanes;
     constexpr int kRows = kGroups / kHeads;         // tokens side by side
     constexpr int kRound = kRows * kPer;            // tokens of a round
     constexpr int kPairs = D / 2;
@@ -253,16 +327,15 @@ __device__ __forceinline__ void append_page(const NormedParams& p, int32_t cta, 
     __syncthreads();
     const int32_t t0 = first[0], a = first[1], b = first[2], blk = first[3], page0 = first[4];
     if (blk < 0) return;
-    const int sub = threadIdx.x % kLanes, g = threadIdx.x / kLanes;
+    const int l = threadIdx.x % P::kLanes, g = threadIdx.x / P::kLanes;
     const int hs = g % kHeads, row0 = g / kHeads;
     const int32_t h = (kv ? set - sets : set) * kHeads + hs;
     const bool head = h < p.kv_heads;
     const Rows& in = kv ? p.v : p.k;
     const bool vec = kv ? p.vec_v : p.vec_k;
-    // the page's row of token i of it, this lane's part
+    // the page's row of its token i
     auto place = [&](int32_t i) {
-        return base + kv * p.layer.half_bytes() + ((int64_t)blk * B + i) * p.layer.row_bytes +
-               ((int64_t)h * D + sub * 8) * (kCodes ? 1 : 2);
+        return base + kv * p.layer.half_bytes() + ((int64_t)blk * B + i) * p.layer.row_bytes + (int64_t)h * D * (kCodes ? 1 : 2);
     };
     uint8_t* scale = nullptr;
     int before = kLowest;                           // exponent of the page's earlier tokens
@@ -273,43 +346,35 @@ __device__ __forceinline__ void append_page(const NormedParams& p, int32_t cta, 
         }
     }
     const int rounds = (b - a + kRound - 1) / kRound;
-    float x[kPer][8];
+    RowOf<T, D, kInterleaved> raw[kPer];
+    // A round's rows, and its tokens' tables.
     auto take = [&](int round) {
         const int32_t i0 = a + round * kRound;
-        RowOf<T, D> raw[kPer];
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
             const int32_t i = i0 + j * kRows + row0;
-            if (head && i < b) raw[j].load(in.row<T>(t0 + (i - a), h), sub * 8, vec);
+            if (head && i < b) raw[j].load(p, in.row<T>(t0 + (i - a), h), l, vec);
             else raw[j].clear();
         }
-        if (!kv && p.rot.half > 0) {
-            __syncthreads();                        // the last round's are not read any more
-            for (int i = threadIdx.x; i < kRound; i += kThreads) {
-                const int32_t at = min(i0 + i, b - 1);
-                position[i] = p.positions != nullptr ? p.positions[t0 + at - a] : (int64_t)page0 + at;
-            }
+        if (!kv) {
+            const int tokens = min(kRound, b - i0);
+            if (round > 0) __syncthreads();         // the last round's are not read any more
+            for (int i = threadIdx.x; i < tokens; i += kThreads)
+                position[i] = p.positions != nullptr ? p.positions[t0 + i0 + i - a] : (int64_t)page0 + i0 + i;
             __syncthreads();
-            const int half = p.rot.half, tokens = min(kRound, b - i0);
-            for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
-                const int tok = i / half, pair = i - tok * half;
-                const float2 w = cos_sin<T>(p.rot.turns[pair], position[tok]);
-                cs[tok * kPairs + pair] = make_float2(w.x * p.rot.magnitude, w.y * p.rot.magnitude);
+            for (int i = threadIdx.x; i < tokens * kPairs; i += kThreads) {
+                const int tok = i / kPairs, n = i % kPairs;
+                table[tok * kPairs + P::place(n)] = table_entry<T, D, kInterleaved>(p, p.k_norm, n, position[tok]);
             }
             __syncthreads();
         }
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const int32_t i = i0 + j * kRows + row0;
-            const bool on = head && i < b;
-            if (kv) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[j][e] = Elem<T>::to_float(raw[j].raw[e]);
-            } else {
-                norm_and_turn<T, D>(p, raw[j], on ? in.row<T>(t0 + (i - a), h) : nullptr, p.k_norm,
-                                    cs + min((int)(i - i0), kRound - 1) * kPairs, x[j]);
-            }
-        }
+    };
+    // Row j of the round as it goes to the page.  (Worked out twice, for the scale and for the codes: held,
+    // the values of all rows would cost half the warps of an SM.)
+    auto value = [&](int j, float (&x)[8], float (&y)[8]) {
+        if (kv) raw[j].take(x, y);
+        else
+            norm_and_turn<T, D, kInterleaved>(p, raw[j], l, p.k_norm != nullptr, table + (j * kRows + row0) * kPairs + l, x, y);
     };
     float factor = 1.f;
     if constexpr (kCodes) {
@@ -317,16 +382,23 @@ __device__ __forceinline__ void append_page(const NormedParams& p, int32_t cta, 
             take(round);
             float top = 0.f;
 #pragma unroll
-            for (int j = 0; j < kPer; ++j)
-                if (head && a + round * kRound + j * kRows + row0 < b) {
+            for (int j = 0; j < kPer; ++j) {
+                const int32_t i = a + round * kRound + j * kRows;
+                if (i >= b) break;
+                float x[8], y[8];
+                value(j, x, y);
+                if (head && i + row0 < b) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (fabsf(x[j][e]) < INFINITY) top = fmaxf(top, fabsf(x[j][e]));
+                    for (int e = 0; e < 8; ++e) {
+                        if (fabsf(x[e]) < INFINITY) top = fmaxf(top, fabsf(x[e]));
+                        if (fabsf(y[e]) < INFINITY) top = fmaxf(top, fabsf(y[e]));
+                    }
                 }
+            }
 #pragma unroll
-            for (int d = kLanes / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+            for (int d = P::kLanes / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
             // magnitudes order as their bits do
-            if (sub == 0 && top > 0.f) atomicMax(&amax[hs], __float_as_uint(top));
+            if (l == 0 && top > 0.f) atomicMax(&amax[hs], __float_as_uint(top));
         }
         __syncthreads();
         const float top = __uint_as_float(amax[hs]);
@@ -335,57 +407,54 @@ __device__ __forceinline__ void append_page(const NormedParams& p, int32_t cta, 
             // the earlier tokens' codes, to the new scale
             const float by = power_of_two(before - e);
             for (int32_t i = row0; i < a; i += kRows) {
-                uint2* const at = reinterpret_cast<uint2*>(place(i));
-                const uint2 c = *at;
-                uint32_t w[2] = {c.x, c.y};
+                uint4* const at = reinterpret_cast<uint4*>(place(i) + l * 16);
+                const uint4 c = *at;
+                uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
+                for (int k = 0; k < 4; ++k) {
                     const uint32_t lo = codes_to_half2((uint16_t)w[k]), hi = codes_to_half2((uint16_t)(w[k] >> 16));
                     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&lo)),
                                  s = __half22float2(*reinterpret_cast<const __half2*>(&hi));
                     w[k] = (uint32_t)floats_to_codes(f.x * by, f.y * by) | ((uint32_t)floats_to_codes(s.x * by, s.y * by) << 16);
                 }
-                *at = make_uint2(w[0], w[1]);
+                *at = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
-        if (head && row0 == 0 && sub == 0) *scale = (uint8_t)(e + 127);
+        if (head && row0 == 0 && l == 0) *scale = (uint8_t)(e + 127);
         factor = power_of_two(-e);
     }
     for (int round = 0; round < rounds; ++round) {
         if (!kCodes || rounds > 1) take(round);
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            const int32_t i = a + round * kRound + j * kRows + row0;
-            if (!head || i >= b) continue;
-            if constexpr (kCodes) {
-                float y[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = fabsf(x[j][e]) < INFINITY ? x[j][e] * factor : NAN;
-                const uint32_t lo = (uint32_t)floats_to_codes(y[0], y[1]) | ((uint32_t)floats_to_codes(y[2], y[3]) << 16);
-                const uint32_t hi = (uint32_t)floats_to_codes(y[4], y[5]) | ((uint32_t)floats_to_codes(y[6], y[7]) << 16);
-                *reinterpret_cast<uint2*>(place(i)) = make_uint2(lo, hi);
-            } else {
-                store_row<T>(reinterpret_cast<T*>(place(i)), x[j], true);
-            }
+            const int32_t i = a + round * kRound + j * kRows;
+            if (i >= b) break;
+            float x[8], y[8];
+            value(j, x, y);
+            if (!head || i + row0 >= b) continue;
+            if constexpr (kCodes) store_codes<D, kInterleaved>(p, place(i + row0), l, x, y, factor);
+            else store_row<T, D, kInterleaved>(p, reinterpret_cast<T*>(place(i + row0)), l, x, y, kInterleaved || p.vectors);
         }
     }
 }
 
 // The CTAs of the pages come first, as theirs is the longer chain of waits, then a
 // CTA a token for q.
-template <class T, int D, bool kCodes>
-__global__ void __launch_bounds__(kThreads) append_normed_kernel(const __grid_constant__ NormedParams p) {
-    constexpr int kRound = kThreads / (D / 8) / kHeads * kPer;
-    __shared__ float2 cs[kRound * (D / 2)];
+template <class T, int D, bool kCodes, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads, 5) append_normed_kernel(const __grid_constant__ NormedParams p) {
+    constexpr int kRound = kThreads / (D / 16) / kHeads * kPer;
+    __shared__ float4 table[kRound * (D / 2)];
     pdl_launch_dependents();
     pdl_wait();
-    if ((int32_t)blockIdx.x < p.kv_ctas) append_page<T, D, kCodes>(p, blockIdx.x, cs);
-    else append_q<T, D>(p, blockIdx.x - p.kv_ctas, cs);
+    if ((int32_t)blockIdx.x < p.kv_ctas) append_page<T, D, kCodes, kInterleaved>(p, blockIdx.x, table);
+    else append_q<T, D, kInterleaved>(p, blockIdx.x - p.kv_ctas, table);
 }
 
 template <class T, int D, bool kCodes>
 int launch_normed(const NormedParams& p, void* stream) {
-    return launch(append_normed_kernel<T, D, kCodes>, (int64_t)p.kv_ctas + p.seqs.num_tokens, kThreads, 0, stream, 1, p);
+    const int64_t ctas = (int64_t)p.kv_ctas + p.seqs.num_tokens;
+    return p.rot.interleaved ? launch(append_normed_kernel<T, D, kCodes, true>, ctas, kThreads, 0, stream, 1, p)
+                             : launch(append_normed_kernel<T, D, kCodes, false>, ctas, kThreads, 0, stream, 1, p);
 }
 template <class T>
 int normed_typed(const NormedParams& p, int32_t head_dim, bool codes, void* stream) {
@@ -426,14 +495,14 @@ extern "C" int lmkv_append_layer_normed(const lmkv_pool_t* pool, void* const* sc
     p.q_heads = num_q_heads;
     p.kv_heads = pool->num_kv_heads;
     p.eps = eps;
-    auto vec = [](const lmkv_rows_t* x) {
-        return reinterpret_cast<uintptr_t>(x->data) % 16 == 0 && x->token_stride % 8 == 0 && x->head_stride % 8 == 0;
+    p.vectors = p.rot.half % 8 == 0;
+    auto vec = [&](const lmkv_rows_t* x) {
+        return (p.vectors || p.rot.interleaved) && reinterpret_cast<uintptr_t>(x->data) % 16 == 0 && x->token_stride % 8 == 0 && x->head_stride % 8 == 0;
     };
     p.vec_q = vec(q);
     p.vec_out = vec(q_out);
     p.vec_k = vec(k);
     p.vec_v = vec(v);
-    p.shuffles = p.rot.half % 8 == 0;
     p.head_sets = 2 * ((p.kv_heads + kHeads - 1) / kHeads);
     p.by_sets = FastDiv((uint32_t)p.head_sets);
     const int64_t slots = (int64_t)batch->num_tokens / pool->block_size + 2 * (int64_t)batch->num_req;
