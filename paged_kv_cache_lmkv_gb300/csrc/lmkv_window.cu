@@ -483,18 +483,17 @@ struct StreamRows {
     }
 };
 
-template <class KV, int D>
+// (An SM's shared memory is not all taken: behind a kernel that needs less of it, as the join, a launch that
+// depends on it did not get its blocks beside one another.  64 users of 1000 to 9000 tokens, 8 bits, 16 warps an SM: rings of
+// three, 192 KB, 124 us by themselves and 198 in a row, of two, 128 KB, 123 in a row.)
+template <class KV, int D, int NT>
 struct StreamShape {
     static constexpr int kTile = Fragments<KV, D>::kTileBytes;             // 1, 2 or 4 KB
-    static constexpr int kStages = kTile >= 4096 ? 2 : kTile >= 2048 ? 3 : 6;
+    static constexpr int kStages = kTile >= 4096 ? 2 : kTile >= 2048 ? (NT > 1 ? 3 : 2) : 4;
     static constexpr int kWarpBytes = kStages * 2 * kTile;
     static constexpr int kSmem = kWarps * kWarpBytes;
-    static constexpr int kCtas = kTile >= 4096 ? 3 : 4;                    // an SM
+    static constexpr int kCtas = kTile >= 4096 || NT > 1 ? 3 : 4;          // an SM
 };
-template <class KV, int D, int NT>
-constexpr int stream_ctas() {
-    return NT > 1 ? 3 : StreamShape<KV, D>::kCtas;
-}
 
 // The chunks of all small requests' row tiles, one after the other, are shared
 // equally among warps, whatever the lengths are; a warp runs through its share by itself, with
@@ -502,11 +501,11 @@ constexpr int stream_ctas() {
 // tile that it had some of.  Stream s of KV head h is warp s * kv_heads + h: the heads' warps of the same tokens run
 // side by side and read the same pages' rows.  Bound by the bytes of the pages.
 template <class T, class KV, int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, stream_ctas<KV, D, NT>())
+__global__ void __launch_bounds__(kWarps * 32, StreamShape<KV, D, NT>::kCtas)
 window_streams_kernel(const __grid_constant__ WindowParams p) {
     using X = StreamRows<T, KV, D, NT>;
     using F = Fragments<KV, D>;
-    using Sh = StreamShape<KV, D>;
+    using Sh = StreamShape<KV, D, NT>;
     extern __shared__ __align__(1024) uint8_t smem[];
     pdl_launch_dependents();
     pdl_wait();
@@ -1333,14 +1332,13 @@ Plan make_plan(const lmkv_pool_t* pool, int32_t q_heads, int32_t num_tokens, int
 template <class T, class KV, int D, int NT>
 int launch_streams(const WindowParams& p, void* stream) {
     return launch(window_streams_kernel<T, KV, D, NT>, ((int64_t)p.streams * p.kv_heads + kWarps - 1) / kWarps, kWarps * 32,
-                  StreamShape<KV, D>::kSmem, stream, 1, p);
+                  StreamShape<KV, D, NT>::kSmem, stream, 1, p);
 }
 
 template <class T, class KV, int D>
 int window_typed(const WindowParams& p, const Plan& x, void* stream) {
-    using Sh = StreamShape<KV, D>;
-    int rc = allow_smem<window_streams_kernel<T, KV, D, 1>, Sh::kSmem>();
-    if (rc == LMKV_OK) rc = allow_smem<window_streams_kernel<T, KV, D, 2>, Sh::kSmem>();
+    int rc = allow_smem<window_streams_kernel<T, KV, D, 1>, StreamShape<KV, D, 1>::kSmem>();
+    if (rc == LMKV_OK) rc = allow_smem<window_streams_kernel<T, KV, D, 2>, StreamShape<KV, D, 2>::kSmem>();
     if (rc == LMKV_OK) rc = allow_smem<window_tiles_kernel<T, KV, D>, WindowTile<D>::kSmem>();
     if (rc == LMKV_OK) rc = keep_carveout<window_streams_kernel<T, KV, D, 1>>();
     if (rc == LMKV_OK) rc = keep_carveout<window_streams_kernel<T, KV, D, 2>>();
