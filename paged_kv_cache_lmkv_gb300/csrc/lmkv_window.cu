@@ -78,6 +78,8 @@ constexpr float kLn2 = 0.69314718055994530942f, kLog2e = 1.44269504088896340736f
 // Weights are relative to 2^kBelow less than a maximum that may lag by 2^kLag, so they are 2^14
 // at most, and those of 2^-20 of the largest are still normal fp16 numbers.
 constexpr float kBelow = 6.f, kLag = 8.f;
+// A finite number below every score, so that the first keys need no case of their own.
+constexpr float kNone = -0x1p126f;
 
 // The keys that some row of tokens t0 .. t1 (cached numbers) sees, in units of
 // kUnit keys: first the sinks' units, then the window's.
@@ -173,7 +175,7 @@ struct ChunkLoad {
     const int32_t* table;
     const uint8_t* base;
     const uint8_t* scale_base;
-    int64_t half_bytes;
+    int64_t half_bytes, v_scales;
     uint32_t row_bytes;
     int32_t h;
     bool runs;
@@ -182,14 +184,18 @@ struct ChunkLoad {
 
     __device__ __forceinline__ ChunkLoad(const WindowParams& wp, const int32_t* t, const uint8_t* layer_base,
                                          const uint8_t* scales, int32_t head, const Seen& s)
-        : p(wp), table(t), base(layer_base), scale_base(scales), half_bytes(wp.layer.half_bytes()),
-          row_bytes((uint32_t)wp.layer.row_bytes), h(head), runs(wp.layer.block_size % kChunk == 0), seen(s), next_blk(-1) {}
+        : p(wp), table(t), base(layer_base), half_bytes(wp.layer.half_bytes()),
+          row_bytes((uint32_t)wp.layer.row_bytes), h(head), runs(wp.layer.block_size % kChunk == 0), seen(s), next_blk(-1) {
+        scale_base = F::kCodes ? scales + head : nullptr;
+        v_scales = wp.scales.num_blocks * wp.kv_heads;
+    }
     __device__ __forceinline__ void lookup(int32_t i, int32_t n) {
         next_blk = runs && i < n ? table[p.layer.column(seen.unit(i) * kChunk)] : -1;
     }
-    __device__ __forceinline__ uint32_t bytes_of(int64_t blk) const {
+    __device__ __forceinline__ uint32_t bytes_of(int32_t blk) const {
         if constexpr (!F::kCodes) return 0;
-        return (uint32_t)scale_base[p.scales.at(0, blk, h)] | ((uint32_t)scale_base[p.scales.at(1, blk, h)] << 8);
+        const uint8_t* const at = scale_base + (int64_t)blk * p.kv_heads;
+        return (uint32_t)at[0] | ((uint32_t)at[v_scales] << 8);
     }
     // Unit i (looked up before) to dst; then looks up the next, of n.
     __device__ __forceinline__ ChunkInfo copy(int32_t i, uint32_t dst, int32_t n) {
@@ -247,7 +253,7 @@ struct StreamRows {
     using M = typename std::conditional<F::kCodes, __half, T>::type;       // of the products
     uint32_t qf[NT][F::kSteps][2];
     float o[NT][F::kSteps][4];
-    float m[NT][2], l[NT][2];      // the maximum (lagging); sums
+    float ref[NT][2], l[NT][2];    // what weights are relative to (kNone: no key yet); sums
     float factor[NT][2];           // of raw scores
     int32_t tok[NT][2];            // cached number of the row's token; -1: no row
     int32_t t_first, t_last;       // of the tile's rows
@@ -314,7 +320,7 @@ struct StreamRows {
                 factor[nt][k] = __shfl_sync(0xFFFFFFFFu, f, (2 * c + k) * 4);
                 const int32_t rr = nt * 8 + 2 * c + k;
                 tok[nt][k] = rr < nrows ? old + (int32_t)p.by_group.div((uint32_t)(row0 + rr)) : -1;
-                m[nt][k] = -INFINITY;
+                ref[nt][k] = kNone;
                 l[nt][k] = 0.f;
             }
 #pragma unroll
@@ -355,15 +361,24 @@ struct StreamRows {
         if constexpr (F::kCodes) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int kb = (int)((info.scales >> (16 * i)) & 0xFF), vb = (int)((info.scales >> (16 * i + 8)) & 0xFF);
-                k_scale[i] = power_of_two(kb - 127);
-                v_power[i] = vb == 255 ? NAN : (float)(vb - 127);
-                v_back[i] = power_of_two(127 - vb);
+                // 2^(byte - 127), byte - 127 and 2^(127 - byte) by their bits (2^-127 is not a normal number)
+                const uint32_t kb = (info.scales >> (16 * i)) & 0xFF, vb = (info.scales >> (16 * i + 8)) & 0xFF;
+                k_scale[i] = __uint_as_float(max(kb << 23, 0x00400000u));
+                v_power[i] = __uint_as_float(0x4B000000u | vb) - (8388608.f + 127.f);
+                v_back[i] = __uint_as_float(max((254u - vb) << 23, 0x00400000u));
+            }
+            // a scale of NaN makes its keys' exponents NaN
+            if (__any_sync(0xFFFFFFFFu, __vcmpeq4(info.scales, 0xFFFFFFFFu) != 0u)) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (((info.scales >> (16 * i)) & 0xFF) == 0xFF || ((info.scales >> (16 * i + 8)) & 0xFF) == 0xFF)
+                        v_power[i] = NAN, v_back[i] = 1.f;
             }
         }
         const bool whole = info.mask == 0xFFFFu && key0 + kChunk - 1 <= t_first &&
                            (p.window == INT32_MAX || key0 > t_last - p.window || key0 + kChunk <= p.sinks);
         bool grow = false;
+        float d[NT][4];            // what the weights are powers of
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -377,7 +392,8 @@ struct StreamRows {
                                      (p.window == INT32_MAX || j > t - p.window || j < p.sinks);
                     if (!see) x = -INFINITY;
                 }
-                grow = grow || x > m[nt][k] + kLag;
+                d[nt][i] = x - ref[nt][k];
+                grow = grow || d[nt][i] > kBelow + kLag;
             }
         if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
@@ -388,10 +404,12 @@ struct StreamRows {
                     top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
                     top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
                     top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-                    const float mn = fmaxf(m[nt][k], top);
-                    const float f = mn == m[nt][k] ? 1.f : exp2_fast(m[nt][k] - mn);
-                    m[nt][k] = mn;
+                    const float to = fmaxf(ref[nt][k], top - kBelow);
+                    const float f = exp2_fast(ref[nt][k] - to);
+                    ref[nt][k] = to;
                     l[nt][k] *= f;
+                    d[nt][k] = sc[nt][k] - to;
+                    d[nt][2 + k] = sc[nt][2 + k] - to;
 #pragma unroll
                     for (int j = 0; j < F::kSteps; ++j) {
                         o[nt][j][k] *= f;
@@ -405,8 +423,7 @@ struct StreamRows {
             float w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float top = m[nt][i & 1];
-                w[i] = exp2_fast(sc[nt][i] - (top == -INFINITY ? 0.f : top - kBelow));
+                w[i] = exp2_fast(d[nt][i]);
                 l[nt][i & 1] = F::kCodes ? fmaf(w[i], v_back[i >> 1], l[nt][i & 1]) : l[nt][i & 1] + w[i];
             }
             // weights are rounded to 16 bits for the product with V, the sum takes them whole
@@ -473,7 +490,7 @@ struct StreamRows {
                 const int32_t rr = nt * 8 + 2 * c + k;
                 if (rr >= nrows) continue;
                 const int64_t at = p.own_part(stream, tile_no, rr, h);
-                if (g == 0) p.part_ml[at] = make_float2(m[nt][k] == -INFINITY ? -INFINITY : m[nt][k] - kBelow, s);
+                if (g == 0) p.part_ml[at] = make_float2(ref[nt][k] == kNone ? -INFINITY : ref[nt][k], s);
                 float* const row = p.part_o + at * D;
 #pragma unroll
                 for (int j = 0; j < F::kSteps; j += 2)
