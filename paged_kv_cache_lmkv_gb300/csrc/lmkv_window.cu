@@ -64,6 +64,8 @@ struct WindowParams {
     int32_t streams;        // warps that share the keys of a KV head
     int32_t slots;          // tile kernel: row tiles that there may be
     int32_t parts;          // its parts of the keys
+    int32_t items;          // its items: row tiles x KV heads x parts
+    int32_t* next_item;     // those taken (beyond one for each CTA); the streams begin it
     int64_t own_base;       // rows of partial results before the streams'
     bool q_pairs;           // q rows are 4-byte aligned
     bool q_vec, out_vec;    // 16-byte aligned
@@ -529,6 +531,7 @@ window_streams_kernel(const __grid_constant__ WindowParams p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int32_t worker = blockIdx.x * kWarps + warp, stream = worker / p.kv_heads, h = worker - stream * p.kv_heads;
     if (stream >= p.streams) return;
+    if (worker == 0 && lane == 0 && p.next_item != nullptr) *p.next_item = 0;
     const uint32_t ring = smem_u32(smem) + warp * Sh::kWarpBytes;
     const int32_t group = (int32_t)p.by_group.d;
     const uint8_t* const base = p.layer.base();
@@ -698,11 +701,11 @@ __global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant_
 using namespace lmkv_tc;
 
 constexpr int kTileRows = 256;        // two tiles of 128 rows share every K and V block
-constexpr int kLoaders = 7;           // warps that bring K and V
+constexpr int kLoaders = 6;           // warps that bring K and V
 // Registers of a softmax thread and of the others: 256 of each share the launch's 512 x 128.
 constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
 static_assert(kSoftmaxRegs + kOtherRegs == 2 * 128, "what one half gives, the other takes");
-constexpr int kTileThreads = (8 + kLoaders + 1) * 32;
+constexpr int kTileThreads = (8 + kLoaders + 2) * 32;
 constexpr int kUnits = kBlock / kChunk;         // of 16 keys, in a block
 constexpr int kInfoSlots = 8;
 
@@ -714,20 +717,33 @@ struct WindowTile {
     static constexpr int kSmem = (2 + kStages) * kStageBytes;
 };
 
-__device__ __forceinline__ void turn_to_loaders() {
-    asm volatile("barrier.cta.arrive 1, %0;" ::"n"((8 + kLoaders) * 32) : "memory");
-}
+// 256 rows of a request and KV head, or a part of their keys.
+struct Item {
+    int32_t h;               // KV head; -1: there are no more items
+    int32_t q0, n, old;      // the request's first row, new tokens, and tokens before them
+    int32_t row0;            // the first of the 256 rows
+    int32_t b0, b1;          // blocks of the keys that its rows see
+    int32_t part;
+    const int32_t* table;
+    Seen seen;
+};
+constexpr int kItems = 4;    // on their way
 
-// Rows of one request, (token, head of the group) in token order, 256 to a CTA,
+// Rows of one request, (token, head of the group) in token order, 256 at a time,
 // against the keys that they see, in blocks of 128.  Products and powers are both near their limits, so the two
 // tiles of 128 rows take turns: while the tensor core works on one tile's
 // weights x V and next q x K, the other tile's softmax runs.
 //   warps 0-3, 4-7   softmax of tile 0, 1: a thread holds a row.  Scores come
 //                    from tensor memory, weights go back over them as the next
 //                    product's first operand; the output stays in tensor memory until the end.
-//   warps 8-14       K and V in units of 16 rows (one page's) into a ring in shared memory that
+//   warps 8-13       K and V in units of 16 rows (one page's) into a ring in shared memory that
 //                    both tiles read: codes through registers, where they become fp16, 16-bit rows by cp.async
+//   warp 14          takes the next items, looks up what they are, and of their blocks the pages and scales
 //   warp 15          one thread issues every product
+// A CTA an SM goes from item to item, whichever is next (what comes of them does not depend on who takes
+// them).  K and V of the next are on their way while the last products run, and its q while the output is
+// written: by themselves, with their first loads and their output waited for, items of ten blocks took 53,000 cycles of
+// which 18,000 were that.
 // A unit's scales are the same for its 16 keys: a factor and an addend of the exponent's multiply-add.
 // Tensor memory: scores of tile 0, 1 at columns 0, 128; outputs at 256, 384.
 template <class T, class KV, int D>
@@ -737,16 +753,19 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
     using S = WindowTile<D>;
     using M = typename std::conditional<kCodes, __half, T>::type;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ uint64_t bars[2 * S::kStages + 8];
+    __shared__ uint64_t bars[2 * S::kStages + 8 + 2 * kItems + 2 * kInfoSlots];
     __shared__ uint32_t tmem_base;
     __shared__ int gave_up;
-    __shared__ int32_t place[2];
+    __shared__ Item items[kItems];
+    __shared__ uint2 infos[kInfoSlots][kUnits];      // of a block's units: first row of the K half, which of its rows there are
     __shared__ __align__(16) uint16_t masks[kInfoSlots][kUnits];      // which of a unit's keys there are
     __shared__ float4 powers[kCodes ? kInfoSlots : 1][kUnits];        // its scale of K; V's as power, and inverse
     pdl_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t full = smem_u32(bars), empty = full + 8 * S::kStages, s_full = empty + 8 * S::kStages,
-                   p_ready = s_full + 16, o_full = p_ready + 32;
+                   p_ready = s_full + 16, o_full = p_ready + 32, item_full = o_full + 16,
+                   item_empty = item_full + 8 * kItems, info_full = item_empty + 8 * kItems,
+                   info_empty = info_full + 8 * kInfoSlots;
     const uint32_t q_smem = smem_u32(smem), kv_smem = q_smem + 2 * S::kStageBytes;
     if (tid == 0) {
         for (int i = 0; i < S::kStages; ++i) {
@@ -759,66 +778,126 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
             mbar_init(p_ready + 16 * t + 8, 4);
             mbar_init(o_full + 8 * t, 1);
         }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(item_full + 8 * i, 1);
+            mbar_init(item_empty + 8 * i, 8 + kLoaders + 1);
+        }
+        for (int i = 0; i < kInfoSlots; ++i) {
+            mbar_init(info_full + 8 * i, 1);
+            mbar_init(info_empty + 8 * i, 1);
+        }
         gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 8 + kLoaders) tmem_alloc<512>(smem_u32(&tmem_base));
+    if (warp == 8 + kLoaders + 1) tmem_alloc<512>(smem_u32(&tmem_base));
     pdl_wait();
-    // the last row tiles of a request see the most keys: they begin first
     const int32_t group = (int32_t)p.by_group.d;
-    const int32_t h = blockIdx.x % p.kv_heads;
-    const int32_t x = blockIdx.x / p.kv_heads, slot = p.slots - 1 - x % p.slots, part = x / p.slots;
-    if (warp == 0) {
-        // slots q_start[r] * group / 256 + r and on are request r's row tiles
-        auto key = [&](int32_t i) { return (int32_t)((int64_t)max(p.seqs.q_start[i], 0) * group / kTileRows) + i; };
-        const int32_t r = find_request(p.seqs.num_req, slot, key);
-        if (lane == 0) {
-            place[0] = r;
-            place[1] = slot >= key(r) ? (slot - key(r)) * kTileRows : -1;
-        }
-    }
-    fence_before_sync();
-    __syncthreads();
-    fence_after_sync();
-    const Req req = load_req(p.seqs, place[0]);
-    const int32_t row0 = place[1], req_rows = req.n * group;
     uint8_t* const base = p.layer.base();
     const uint8_t* const scales = kCodes ? p.scales.base() : nullptr;
     const bool there = base != nullptr && (!kCodes || scales != nullptr);
-    if (row0 >= 0 && row0 < req_rows && req_rows >= p.big_rows) {
-        const int32_t old = req.len - req.n;
-        const int32_t last_row = min(row0 + kTileRows, req_rows) - 1;
-        const Seen seen = seen_by(p, old + (int32_t)p.by_group.div((uint32_t)row0),
-                                  old + (int32_t)p.by_group.div((uint32_t)last_row), kBlock);
-        const int32_t units = there ? seen.units : 0;
-        const int32_t b0 = (int32_t)((int64_t)units * part / p.parts), b1 = (int32_t)((int64_t)units * (part + 1) / p.parts);
-        const int tiles = last_row - row0 >= 128 ? 2 : 1;
-        if (tid == 0) {
-            if (!req.ok) report(p.status, LMKV_ERR_BAD_LENGTH);
-            if (!there) report(p.status, LMKV_ERR_BAD_POINTER);
-        }
-
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    // The it-th item of this CTA, once it is known; its place is free again when all warps but the one that takes
+    // items have read it.
+    auto get = [&](int32_t it, Item& x) {
+        const int slot = it % kItems;
+        if (!mbar_wait(item_full + 8 * slot, it / kItems & 1, &gave_up)) return false;
+        x = items[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(item_empty + 8 * slot);
+        return x.h >= 0;
+    };
+    // (Stages of the ring are counted on from item to item, K and V of a block in turn.)
+    {
         if (warp < 8) {
             asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
             const int t = warp >> 2;
-            const int32_t R = row0 + tid;
-            const bool live = R < req_rows;
-            const int32_t n = (int32_t)p.by_group.div((uint32_t)(live ? R : row0));
-            const int32_t tok = req.q0 + n, head = h * group + ((live ? R : row0) - n * group);
-            if (t >= tiles) turn_to_loaders();
-            if (t < tiles) {
+            const uint32_t lane_base = tmem_base + ((uint32_t)(warp & 3) << 21);     // lane 32 * (warp % 4)
+            const uint32_t s_at = lane_base + t * 128, o_at = lane_base + 256 + t * 128;
+            const uint32_t dst = q_smem + t * S::kStageBytes + (warp & 3) * (32 * 128);
+            constexpr int kRowLanes = D / 8, kSide = 32 / kRowLanes;
+            const int piece = lane % kRowLanes;
+            float m = -INFINITY;              // the maximum (lagging), in powers of 2
+            float2 l2 = make_float2(0.f, 0.f);
+            // of the item before: my row, whose result is still to be written
+            int32_t row_tok = -1, row_head = 0, row_part = 0, last_block = -1;
+            bool row_left = false, row_blocks = false;
+            uint32_t blocks_before = 0, scores_phase = 0, out_phase = 0;
+            auto finish = [&] {
+                row_left = false;
+                if (row_blocks) {
+                    if (!mbar_wait(o_full + 8 * t, out_phase, &gave_up)) return false;
+                    out_phase ^= 1;
+                    fence_after_sync();
+                    if (last_block >= 0 && (tid & 127) == 0) {
+                        mbar_arrive(empty + 8 * ((2 * (uint32_t)last_block + 1) % S::kStages));
+                        mbar_arrive(info_empty + 8 * (last_block % kInfoSlots));
+                    }
+                }
+                const float l = l2.x + l2.y;
+                const bool final = p.parts == 1, live = row_tok >= 0;
+                const int64_t row = (int64_t)(live ? row_tok : 0) * p.q_heads + row_head;
+                const int64_t at = (int64_t)row_part * p.rows + row;
+                const float ref = m == -INFINITY ? -INFINITY : m - kBelow;
+                const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+                T* const to = p.out.row<T>(live ? row_tok : 0, row_head);
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                    uint32_t y[16];
+                    if (row_blocks) {
+                        tmem_ld16(y, o_at + c);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) y[j] = 0u;
+                    }
+                    if (live && final) {
+#pragma unroll
+                        for (int j = 0; j < 16; j += 8) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                w[i] = Elem<T>::pack(__uint_as_float(y[j + 2 * i]) * inv, __uint_as_float(y[j + 2 * i + 1]) * inv);
+                            if (p.out_vec) {
+                                *reinterpret_cast<uint4*>(to + c + j) = make_uint4(w[0], w[1], w[2], w[3]);
+                            } else {
+                                uint16_t* const e = reinterpret_cast<uint16_t*>(to + c + j);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    e[2 * i] = (uint16_t)w[i];
+                                    e[2 * i + 1] = (uint16_t)(w[i] >> 16);
+                                }
+                            }
+                        }
+                    } else if (live) {
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4)
+                            *reinterpret_cast<uint4*>(p.part_o + at * D + c + j) = make_uint4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+                    }
+                }
+                if (live && final && p.lse != nullptr) p.lse[row] = ((m == -INFINITY ? 0.f : ref) + log2f(l)) * kLn2;
+                if (live && !final) p.part_ml[at] = make_float2(ref, l);
+                return true;
+            };
+            bool ok = true;
+            for (int32_t it = 0; ok; ++it) {
+                Item item;
+                const bool some = get(it, item);
+                const int32_t req_rows = item.n * group;
+                const int tiles = min(item.row0 + kTileRows, req_rows) - item.row0 > 128 ? 2 : 1;
+                const bool mine = some && t < tiles;
+                const int32_t blocks = some ? item.b1 - item.b0 : 0;
+                if (mine) {
                 // The warp's rows of q into shared memory, 16 bytes a lane side by side.  (This and the end run once,
                 // out of memory that holds no instructions of theirs any more: loops, not lines, keep them
                 // short.  Unrolled, the rows took 31,000 cycles.)
-                constexpr int kRowLanes = D / 8, kSide = 32 / kRowLanes;
-                const uint32_t dst = q_smem + t * S::kStageBytes + (warp & 3) * (32 * 128);
-                const int piece = lane % kRowLanes;
+                // (no product reads the last item's any more: its scores were all there)
                 auto row_at = [&](int i, int32_t& token, int32_t& hd) {      // the i-th row of this lane's; its place in dst
                     const int r = i * kSide + lane / kRowLanes;
-                    const int32_t at = row0 + warp * 32 + r;
+                    const int32_t at = item.row0 + warp * 32 + r;
                     const int32_t of = (int32_t)p.by_group.div((uint32_t)at);
-                    token = at < req_rows ? req.q0 + of : -1;
-                    hd = h * group + (at - of * group);
+                    token = at < req_rows ? item.q0 + of : -1;
+                    hd = item.h * group + (at - of * group);
                     return dst + (piece >> 3) * S::kHalfBytes + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
                 };
 #pragma unroll 1
@@ -826,7 +905,7 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                     int32_t token, hd;
                     const uint32_t at = row_at(i, token, hd);
                     const bool on = token >= 0 && p.scale_sign != 0;
-                    const T* const src = p.q.row<T>(on ? token : req.q0, hd) + piece * 8;
+                    const T* const src = p.q.row<T>(on ? token : item.q0, hd) + piece * 8;
                     if (p.q_vec) {
                         cp_async16(at, src, on);
                     } else {
@@ -837,7 +916,10 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                     }
                 }
                 cp_commit();
-                turn_to_loaders();
+                }
+                if (row_left) ok = finish();
+                if (!some || !ok) break;
+                if (mine) {
                 cp_wait<0>();
                 __syncwarp();
                 float factor = p.scale_log2;
@@ -876,27 +958,37 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_ready + 16 * t + 8);     // its phase 0: q is there
 
-                const uint32_t lane_base = tmem_base + ((uint32_t)(warp & 3) << 21);     // lane 32 * (warp % 4)
-                const uint32_t s_at = lane_base + t * 128, o_at = lane_base + 256 + t * 128;
+                const int32_t R = item.row0 + tid;
+                const bool live = R < req_rows;
+                const int32_t n = (int32_t)p.by_group.div((uint32_t)(live ? R : item.row0));
                 // my row sees keys below end, from begin on or below the sinks
-                const int32_t end = live ? old + n + 1 : 0, begin = p.window == INT32_MAX ? 0 : end - p.window;
-                float m = -INFINITY;              // the maximum (lagging), in powers of 2
-                float2 l2 = make_float2(0.f, 0.f);
-                bool ok = true;
-                for (int32_t b = b0; b < b1; ++b) {
-                    const int32_t k = seen.unit(b) * kBlock;
-                    if (!mbar_wait(s_full + 8 * t, (b - b0) & 1, &gave_up)) {
+                const int32_t end = live ? item.old + n + 1 : 0, begin = p.window == INT32_MAX ? 0 : end - p.window;
+                m = -INFINITY;
+                l2 = make_float2(0.f, 0.f);
+                row_left = true;
+                row_tok = live ? item.q0 + n : -1;
+                row_head = item.h * group + ((live ? R : item.row0) - n * group);
+                row_part = item.part;
+                row_blocks = blocks > 0;
+                last_block = t == tiles - 1 ? (int32_t)(blocks_before + blocks) - 1 : -1;
+                for (int32_t j = 0; j < blocks; ++j) {
+                    const int32_t k = item.seen.unit(item.b0 + j) * kBlock;
+                    if (!mbar_wait(s_full + 8 * t, scores_phase, &gave_up)) {
                         ok = false;
                         break;
                     }
+                    scores_phase ^= 1;
                     if (t == tiles - 1 && (tid & 127) == 0) {
                         // every product up to these scores is done: K of this block and V of the last are free
-                        const int32_t j = b - b0;
-                        mbar_arrive(empty + 8 * (2 * j % S::kStages));
-                        if (j > 0) mbar_arrive(empty + 8 * ((2 * j - 1) % S::kStages));
+                        const uint32_t kv = (blocks_before + j) * 2;
+                        mbar_arrive(empty + 8 * (kv % S::kStages));
+                        if (j > 0) {
+                            mbar_arrive(empty + 8 * ((kv - 1) % S::kStages));
+                            mbar_arrive(info_empty + 8 * ((blocks_before + j - 1) % kInfoSlots));
+                        }
                     }
                     fence_after_sync();
-                    const int slot_of = (b - b0) % kInfoSlots;
+                    const int slot_of = (blocks_before + j) % kInfoSlots;
                     const uint4 words = *reinterpret_cast<const uint4*>(masks[slot_of]);
                     const bool whole = __all_sync(0xFFFFFFFFu, end - k >= kBlock && (begin <= k || k + kBlock <= p.sinks)) &&
                                        (words.x & words.y & words.z & words.w) == ~0u;
@@ -909,8 +1001,8 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                                               below(end - at) & (~below(begin - at) | below(p.sinks - at));
                         if (__all_sync(0xFFFFFFFFu, bits == ~0u)) return;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (!((bits >> j) & 1)) x[j] = 0xFF800000u;
+                        for (int e = 0; e < 32; ++e)
+                            if (!((bits >> e) & 1)) x[e] = 0xFF800000u;
                     };
                     // a unit's factor (never 0: -infinity is to stay that)
                     auto factor_of = [&](const float4& u) { return kCodes ? fmaxf(factor * u.x, 0x1p-126f) : factor; };
@@ -956,7 +1048,7 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                         if (grow) m = mx;
                         l2.x *= f;
                         l2.y *= f;
-                        if (b > b0) {
+                        if (j > 0) {
                             // the scores were there, so the product before them, into the output, is done
 #pragma unroll 1
                             for (int c = 0; c < D; c += 16) tmem_scale16(o_at + c, f);
@@ -1000,117 +1092,26 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                         }
                     }
                 }
-                // my row of the result
-                const float l = l2.x + l2.y;
-                if (ok && b1 > b0) ok = mbar_wait(o_full + 8 * t, 0, &gave_up);
-                if (ok) {
-                    fence_after_sync();
-                    const bool final = p.parts == 1;
-                    const int64_t row = (int64_t)tok * p.q_heads + head;
-                    const int64_t at = (int64_t)part * p.rows + row;
-                    const float ref = m == -INFINITY ? -INFINITY : m - kBelow;
-                    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
-                        uint32_t y[16];
-                        if (b1 > b0) {
-                            tmem_ld16(y, o_at + c);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) y[j] = 0u;
-                        }
-                        if (final) {
-                            // over my row of q, which no product reads any more
-#pragma unroll
-                            for (int j = 0; j < 16; j += 8)
-                                sts128(my_piece((c + j) >> 3),
-                                       make_uint4(Elem<T>::pack(__uint_as_float(y[j]) * inv, __uint_as_float(y[j + 1]) * inv),
-                                                  Elem<T>::pack(__uint_as_float(y[j + 2]) * inv, __uint_as_float(y[j + 3]) * inv),
-                                                  Elem<T>::pack(__uint_as_float(y[j + 4]) * inv, __uint_as_float(y[j + 5]) * inv),
-                                                  Elem<T>::pack(__uint_as_float(y[j + 6]) * inv, __uint_as_float(y[j + 7]) * inv)));
-                        } else if (live) {
-#pragma unroll
-                            for (int j = 0; j < 16; j += 4)
-                                *reinterpret_cast<uint4*>(p.part_o + at * D + c + j) = make_uint4(y[j], y[j + 1], y[j + 2], y[j + 3]);
-                        }
-                    }
-                    if (final) {
-                        __syncwarp();
-#pragma unroll 1
-                        for (int i = 0; i < kRowLanes; ++i) {
-                            int32_t token, hd;
-                            const uint4 v = lds128(row_at(i, token, hd));
-                            if (token < 0) break;
-                            T* const to = p.out.row<T>(token, hd) + piece * 8;
-                            if (p.out_vec) {
-                                *reinterpret_cast<uint4*>(to) = v;
-                            } else {
-                                const uint16_t* const e = reinterpret_cast<const uint16_t*>(&v);
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) reinterpret_cast<uint16_t*>(to)[j] = e[j];
-                            }
-                        }
-                    }
-                    if (live && final && p.lse != nullptr)
-                        p.lse[row] = ((m == -INFINITY ? 0.f : ref) + log2f(l)) * kLn2;
-                    if (live && !final) p.part_ml[at] = make_float2(ref, l);
                 }
+                blocks_before += blocks;
             }
+            if (row_left && ok) finish();
         } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp < 8 + kLoaders) {
-            // Unit u of the CTA is rows 16 (u % 8) .. of item u / 8 (K, V of a block in turn); warp
-            // 8 + i takes units i, i + 3, ..  Lane i < 8 holds what there is to know of unit i of a block, table
-            // entries fetched two blocks ahead and scales one, so that nothing is waited for.
-            const int32_t* const table = p.seqs.table + (int64_t)req.r * p.seqs.table_stride;
+            // Unit u of an item is rows 16 (u % 8) .. of its u / 8-th stage (K, V of a block in turn); warp
+            // 8 + i takes units i, i + kLoaders, ..
             const uint32_t row_bytes = (uint32_t)p.layer.row_bytes;
             const int64_t half_bytes = p.layer.half_bytes();
             constexpr int kRowBytes = D * (int)sizeof(KV), kPieces = kRowBytes / 16, kRowsPer = 32 / kPieces;
             constexpr int kCopies = kChunk / kRowsPer;
             const int c = lane % kPieces, rsub = lane / kPieces;
-            const uint8_t* const mine = base + (int64_t)h * kRowBytes + c * 16 + (int64_t)rsub * row_bytes;
-            const int32_t blocks = b1 - b0, all_units = blocks * 2 * kUnits;
-            struct Entry {
-                int32_t k, blk;           // the unit's first key, its page
-                uint32_t rows;            // which of its rows some row of the tile sees
-            };
-            auto look = [&](int32_t b) {
-                Entry x{0, 0, 0};
-                if (b < blocks && lane < kUnits) {
-                    x.k = seen.unit(b0 + b) * kBlock + lane * kChunk;
-                    // keys [0, sink_end) and [lo, end) are seen
-                    auto below = [](int32_t n) { return n >= 16 ? 0xFFFFu : n <= 0 ? 0u : (1u << n) - 1u; };
-                    x.rows = below(seen.end - x.k) & (below(seen.sink_end - x.k) | ~below(seen.lo - x.k));
-                    if (x.rows != 0) x.blk = table[p.layer.column(x.k)];
-                }
-                return x;
-            };
-            uint32_t row = 0, held = 0;   // of the block at hand: the unit's first row of the K half; its rows, K's and V's scale bytes
-            uint32_t next_row = 0, next_held = 0;
-            Entry ahead = look(0);
-            int32_t at_block = -1;
-            auto advance = [&] {
-                row = next_row;
-                held = next_held;
-                Entry x = ahead;
-                ahead = look(at_block + 3);
-                if (x.rows != 0 && (x.blk < 0 || x.blk >= p.layer.num_blocks)) {
-                    report(p.status, LMKV_ERR_BAD_BLOCK);
-                    x.rows = 0;
-                }
-                next_row = x.rows != 0 ? p.layer.row_of(x.blk, x.k, p.layer.column(x.k)) : 0u;
-                next_held = 0x7F7F0000u;
-                if (kCodes && x.rows != 0)
-                    next_held = ((uint32_t)scales[p.scales.at(0, x.blk, h)] << 16) |
-                                ((uint32_t)scales[p.scales.at(1, x.blk, h)] << 24);
-                next_held |= x.rows;
-                ++at_block;
-            };
-            if (blocks > 0) {
-                // (the first blocks' entries are waited for)
-                --at_block;
-                advance();
-            }
+            uint32_t blocks_before = 0;
+            bool ok = true;
+            Item item;
+            for (int32_t it = 0; ok && get(it, item); ++it) {
+            const uint8_t* const mine = base + (int64_t)item.h * kRowBytes + c * 16 + (int64_t)rsub * row_bytes;
+            const int32_t all_units = (item.b1 - item.b0) * 2 * kUnits;
             // What there is to know of unit u, and where this lane's part of it is.
             struct Unit {
                 uint32_t held;
@@ -1118,27 +1119,24 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                 __device__ __forceinline__ bool on(int row) const { return (held >> row) & 1; }
             };
             auto find = [&](int32_t u) {
-                while (at_block < u / (2 * kUnits)) advance();
-                const uint32_t first = __shfl_sync(0xFFFFFFFFu, row, u % kUnits);
-                return Unit{__shfl_sync(0xFFFFFFFFu, held, u % kUnits),
-                            mine + (u / kUnits % 2 != 0 ? half_bytes : 0) + (uint64_t)first * row_bytes};
+                const uint32_t block = blocks_before + u / (2 * kUnits);
+                ok = ok && mbar_wait(info_full + 8 * (block % kInfoSlots), (block / kInfoSlots) & 1, &gave_up);
+                const uint2 x = infos[block % kInfoSlots][u % kUnits];
+                return Unit{ok ? x.y : 0u, mine + (u / kUnits % 2 != 0 ? half_bytes : 0) + (uint64_t)x.x * row_bytes};
             };
             auto enter = [&](int32_t u) {      // the unit's stage is free
-                const int32_t item = u / kUnits, st = item % S::kStages;
-                return item < S::kStages || mbar_wait(empty + 8 * st, (item / S::kStages - 1) & 1, &gave_up);
+                const uint32_t kv = blocks_before * 2 + u / kUnits, st = kv % S::kStages;
+                return kv < S::kStages || mbar_wait(empty + 8 * st, (kv / S::kStages - 1) & 1, &gave_up);
             };
+            auto stage_of = [&](int32_t u) { return (blocks_before * 2 + u / kUnits) % S::kStages; };
             const int32_t u_first = warp - 8;
-            // q's copies go first: K and V, a ring of them, would stand before them in the queue
-            bar_sync(1, (8 + kLoaders) * 32);
             if constexpr (kCodes) {
-                // a unit on its way in registers while one goes to shared memory
-                constexpr int kDeep = 2;
+                // two units on their way in registers while one goes to shared memory
+                constexpr int kDeep = 3;
                 uint4 codes[kDeep][kCopies];
-                uint32_t on_way[kDeep];
                 auto start = [&](int s, int32_t u) {
                     if (u >= all_units) return;
                     const Unit x = find(u);
-                    on_way[s] = x.held;
 #pragma unroll
                     for (int r = 0; r < kCopies; ++r) {
                         codes[s][r] = make_uint4(0u, 0u, 0u, 0u);
@@ -1150,15 +1148,10 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                 // that they meet no bank twice.
                 const bool odd = D == 128 && (c >> 2) != 0;
                 const uint32_t to = kv_smem + (D == 128 ? (c >> 2) * S::kHalfBytes : 0) + rsub * 128;
-                uint32_t place_of[2][2];       // of the even and odd copies' pieces
-#pragma unroll
-                for (int r = 0; r < 2; ++r)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        place_of[r][i] = to + ((((2 * c + (i ^ (odd ? 1 : 0))) & 7) ^ ((r * kRowsPer + rsub) & 7)) << 4);
+                // (the other piece is the next or the one before; rows r * kRowsPer further exchange by the next bits)
+                const uint32_t first_piece = to + ((((2 * c + (odd ? 1 : 0)) & 7) ^ (rsub & 7)) << 4);
 #pragma unroll
                 for (int s = 0; s < kDeep - 1; ++s) start(s, u_first + s * kLoaders);
-                bool ok = true;
 #pragma unroll 1
                 for (int32_t u0 = u_first; u0 < all_units && ok; u0 += kDeep * kLoaders) {
 #pragma unroll
@@ -1168,38 +1161,29 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                         start((s + kDeep - 1) % kDeep, u + (kDeep - 1) * kLoaders);
                         ok = enter(u);
                         if (!ok) break;
-                        const uint32_t of = on_way[s];
-                        if (u / kUnits % 2 == 0 && lane == 0) {
-                            const int slot_of = u / (2 * kUnits) % kInfoSlots;
-                            masks[slot_of][u % kUnits] = (uint16_t)of;
-                            // (a scale of NaN makes its keys' exponents NaN)
-                            const int kb = (int)((of >> 16) & 0xFF), vb = (int)(of >> 24);
-                            powers[slot_of][u % kUnits] =
-                                make_float4(power_of_two(kb - 127), kb == 255 || vb == 255 ? NAN : (float)(vb - 127),
-                                            power_of_two(127 - vb), 0.f);
-                        }
-                        const uint32_t dst = u / kUnits % S::kStages * S::kStageBytes + u % kUnits * (kChunk * 128);
+                        const uint32_t dst = stage_of(u) * S::kStageBytes + u % kUnits * (kChunk * 128);
 #pragma unroll
                         for (int r = 0; r < kCopies; ++r) {
                             const uint4 v = codes[s][r];
                             const uint32_t w[4] = {odd ? v.z : v.x, odd ? v.w : v.y, odd ? v.x : v.z, odd ? v.y : v.w};
 #pragma unroll
                             for (int i = 0; i < 2; ++i)
-                                sts128(place_of[r & 1][i] + dst + r * (kRowsPer * 128),
+                                sts128(((first_piece ^ (i << 4)) ^ ((r * kRowsPer & 7) << 4)) + dst + r * (kRowsPer * 128),
                                        make_uint4(codes_to_half2((uint16_t)w[2 * i]), codes_to_half2((uint16_t)(w[2 * i] >> 16)),
                                                   codes_to_half2((uint16_t)w[2 * i + 1]),
                                                   codes_to_half2((uint16_t)(w[2 * i + 1] >> 16))));
                         }
                         __syncwarp();
                         // (the products' thread has the writes seen by the tensor core, once for an item)
-                        if (lane == 0) mbar_arrive(full + 8 * (u / kUnits % S::kStages));
+                        if (lane == 0) mbar_arrive(full + 8 * stage_of(u));
                     }
                 }
             } else {
 #pragma unroll 1
                 for (int32_t u = u_first; u < all_units; u += kLoaders) {
-                    if (!enter(u)) break;
-                    const uint32_t stage = u / kUnits % S::kStages;
+                    ok = enter(u);
+                    if (!ok) break;
+                    const uint32_t stage = stage_of(u);
                     const uint32_t dst = kv_smem + stage * S::kStageBytes + u % kUnits * (kChunk * 128) + (c >> 3) * S::kHalfBytes;
                     const Unit x = find(u);
                     const bool all = (x.held & 0xFFFFu) == 0xFFFFu;
@@ -1210,17 +1194,105 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                         if (all) cp_async16(at, x.src + r * kRowsPer * row_bytes);
                         else cp_async16(at, x.on(i) ? x.src + r * kRowsPer * row_bytes : base, x.on(i));
                     }
-                    if (u / kUnits % 2 == 0 && lane == 0)
-                        masks[u / (2 * kUnits) % kInfoSlots][u % kUnits] = (uint16_t)x.held;
                     copies_arrive(full + 8 * stage);
                 }
-                asm volatile("cp.async.wait_all;" ::: "memory");
             }
-        } else if (b1 > b0) {
+            blocks_before += item.b1 - item.b0;
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+        } else if (warp == 8 + kLoaders) {
+            // the last row tiles of a request see the most keys: they begin first
+            uint32_t blocks_before = 0;
+            for (int32_t it = 0, next = blockIdx.x;; ) {
+                Item x = {};
+                x.h = -1;
+                if (next < p.items) {
+                    const int32_t h = next % p.kv_heads;
+                    const int32_t of = next / p.kv_heads, slot = p.slots - 1 - of % p.slots;
+                    // slots q_start[r] * group / 256 + r and on are request r's row tiles
+                    auto key = [&](int32_t i) { return (int32_t)((int64_t)max(p.seqs.q_start[i], 0) * group / kTileRows) + i; };
+                    const int32_t r = find_request(p.seqs.num_req, slot, key);
+                    const Req req = load_req(p.seqs, r);
+                    const int32_t req_rows = req.n * group;
+                    x.part = of / p.slots;
+                    x.row0 = slot >= key(r) ? (slot - key(r)) * kTileRows : req_rows;
+                    int32_t taken = 0;
+                    if (lane == 0) taken = atomicAdd(p.next_item, 1);
+                    next = (int32_t)gridDim.x + __shfl_sync(0xFFFFFFFFu, taken, 0);
+                    if (x.row0 >= req_rows || req_rows < p.big_rows) continue;       // a place of no rows
+                    if (lane == 0) {
+                        if (!req.ok) report(p.status, LMKV_ERR_BAD_LENGTH);
+                        if (!there) report(p.status, LMKV_ERR_BAD_POINTER);
+                    }
+                    x.h = h;
+                    x.q0 = req.q0;
+                    x.n = req.n;
+                    x.old = req.len - req.n;
+                    x.table = p.seqs.table + (int64_t)r * p.seqs.table_stride;
+                    const int32_t last = min(x.row0 + kTileRows, req_rows) - 1;
+                    x.seen = seen_by(p, x.old + (int32_t)p.by_group.div((uint32_t)x.row0),
+                                     x.old + (int32_t)p.by_group.div((uint32_t)last), kBlock);
+                    const int32_t units = there ? x.seen.units : 0;
+                    x.b0 = (int32_t)((int64_t)units * x.part / p.parts);
+                    x.b1 = (int32_t)((int64_t)units * (x.part + 1) / p.parts);
+                }
+                const int slot = it % kItems;
+                if (it >= kItems && !mbar_wait(item_empty + 8 * slot, (it / kItems - 1) & 1, &gave_up)) break;
+                if (lane == 0) {
+                    items[slot] = x;
+                    mbar_arrive(item_full + 8 * slot);
+                }
+                __syncwarp();
+                ++it;
+                if (x.h < 0) break;
+                // the units of four blocks at a time, one a lane
+                bool ok = true;
+                const int32_t blocks = x.b1 - x.b0;
+                for (int32_t j0 = 0; j0 < blocks && ok; j0 += 4) {
+                    const int32_t j = j0 + lane / kUnits, i = lane % kUnits;
+                    uint32_t row = 0, rows = 0, kb = 127, vb = 127;
+                    if (j < blocks) {
+                        const int32_t k = x.seen.unit(x.b0 + j) * kBlock + i * kChunk;
+                        // keys [0, sink_end) and [lo, end) are seen
+                        auto below = [](int32_t n) { return n >= 16 ? 0xFFFFu : n <= 0 ? 0u : (1u << n) - 1u; };
+                        rows = below(x.seen.end - k) & (below(x.seen.sink_end - k) | ~below(x.seen.lo - k));
+                        if (rows != 0) {
+                            const uint32_t col = p.layer.column(k);
+                            const int32_t blk = x.table[col];
+                            row = p.layer.row_of(blk, k, col);
+                            if (row == Layer::kNoRow) {
+                                report(p.status, LMKV_ERR_BAD_BLOCK);
+                                row = rows = 0;
+                            } else if (kCodes) {
+                                kb = scales[p.scales.at(0, blk, x.h)];
+                                vb = scales[p.scales.at(1, blk, x.h)];
+                            }
+                        }
+                    }
+                    for (int32_t f = 0; f < 4 && j0 + f < blocks && ok; ++f) {
+                        const uint32_t block = blocks_before + j0 + f, at = block % kInfoSlots;
+                        if (block >= kInfoSlots)
+                            ok = mbar_wait(info_empty + 8 * at, (block / kInfoSlots - 1) & 1, &gave_up);
+                        if (ok && lane / kUnits == f) {
+                            infos[at][i] = make_uint2(row, rows);
+                            masks[at][i] = (uint16_t)rows;
+                            // (a scale of NaN makes its keys' exponents NaN)
+                            if (kCodes)
+                                powers[kCodes ? at : 0][i] =
+                                    make_float4(power_of_two((int)kb - 127), kb == 255 || vb == 255 ? NAN : (float)((int)vb - 127),
+                                                power_of_two(127 - (int)vb), 0.f);
+                        }
+                        __syncwarp();
+                        if (ok && lane == 0) mbar_arrive(info_full + 8 * at);
+                    }
+                }
+                if (!ok) break;
+                blocks_before += blocks;
+            }
+        } else {
             constexpr uint32_t qk = instr_desc<M, kBlock, false>(), pv = instr_desc<M, D, true>();
             // all of tensor memory is this CTA's, so its columns count from 0
             constexpr uint32_t kScores = 0, kOut = 256;
-            const int32_t blocks = b1 - b0;
             const uint32_t lead = elect_lead();
             const Desc q0 = desc_k_major(q_smem), k0 = desc_k_major(kv_smem), v0 = desc_n_major(kv_smem, S::kHalfBytes);
             // places of the next K and V items in the ring, and their phases
@@ -1248,13 +1320,28 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                 fence_async_shared();
                 return there;
             };
-            bool ok = landed(0, 0);
-            for (int t = 0; t < tiles && ok; ++t) {
-                ok = mbar_wait(p_ready + 16 * t + 8, 0, &gave_up);
-                if (ok) scores(t, 0);
+            bool ok = true;
+            uint32_t ready[2][2] = {};            // phases of the weights' halves (the second's first: q)
+            auto weights = [&](int t, int half) {
+                const bool there = mbar_wait(p_ready + 16 * t + 8 * half, ready[t][half], &gave_up);
+                ready[t][half] ^= 1;
+                return there;
+            };
+            Item item;
+            for (int32_t it = 0; ok && get(it, item); ++it) {
+            const int32_t blocks = item.b1 - item.b0;
+            const int tiles = min(item.row0 + kTileRows, item.n * group) - item.row0 > 128 ? 2 : 1;
+            // (q of items without keys is not waited for with any product, but its phase passes)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (t >= tiles || !ok) break;
+                ok = weights(t, 1);
+                if (ok && t == 0 && blocks > 0) ok = landed(ks, kph);
+                if (ok && blocks > 0) scores(t, ks);
             }
+            if (blocks == 0 || !ok) continue;
             advance(ks, kph);
-            ok = ok && landed(vs, vph);
+            ok = landed(vs, vph);
             for (int32_t j = 0; j < blocks && ok; ++j) {
                 const bool more = j + 1 < blocks;
                 const Desc v = v0.at(vs * S::kStageBytes);
@@ -1265,7 +1352,7 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                     // the weights come in two halves of 64 keys, a barrier each
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        ok = ok && mbar_wait(p_ready + 16 * t + 8 * half, (j + half) & 1, &gave_up);
+                        ok = ok && weights(t, half);
                         if (!ok) break;
                         fence_after_sync();
 #pragma unroll
@@ -1283,7 +1370,8 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                         mma_commit(lead, o_full + 8 * t);
                     }
                 }
-                advance(ks, kph);
+                if (more) advance(ks, kph);
+            }
             }
         }
         }
@@ -1293,8 +1381,9 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
     __syncthreads();
     fence_after_sync();
     if (tid == 0 && gave_up) report(p.status, LMKV_ERR_TIMEOUT);
-    if (warp == 8 + kLoaders) tmem_free<512>(tmem_base);
+    if (warp == 8 + kLoaders + 1) tmem_free<512>(tmem_base);
 }
+
 
 // ---- host ---------------------------------------------------------------
 
@@ -1342,7 +1431,7 @@ Plan make_plan(const lmkv_pool_t* pool, int32_t q_heads, int32_t num_tokens, int
         if (most) x.tile_part_rows = kMostTileCtas * kTileRows;        // a split call's rows are fewer
     }
     x.bytes = (uint64_t)(x.tile_part_rows + x.own_rows) * (pool->head_dim * 4 + 8) +
-              (uint64_t)num_req * (most ? (x.own_cap + 7) / 8 : x.own_tiles) * 8;
+              (uint64_t)num_req * (most ? (x.own_cap + 7) / 8 : x.own_tiles) * 8 + 8;
     return x;
 }
 
@@ -1361,10 +1450,10 @@ int window_typed(const WindowParams& p, const Plan& x, void* stream) {
     if (rc == LMKV_OK) rc = keep_carveout<window_streams_kernel<T, KV, D, 2>>();
     if (rc == LMKV_OK) rc = keep_carveout<window_join_kernel<T, D, false>>();
     if (rc == LMKV_OK) rc = keep_carveout<window_join_kernel<T, D, true>>();
-    if (rc == LMKV_OK && x.big_rows < INT32_MAX)
-        rc = launch(window_tiles_kernel<T, KV, D>, (int64_t)x.slots * p.kv_heads * x.parts, kTileThreads,
-                    WindowTile<D>::kSmem, stream, 1, p);
     if (rc == LMKV_OK) rc = x.tile_rows == 8 ? launch_streams<T, KV, D, 1>(p, stream) : launch_streams<T, KV, D, 2>(p, stream);
+    if (rc == LMKV_OK && x.big_rows < INT32_MAX)
+        rc = launch(window_tiles_kernel<T, KV, D>, p.items < kSms ? p.items : kSms, kTileThreads, WindowTile<D>::kSmem, stream, 1,
+                    p);
     if (rc == LMKV_OK)
         rc = launch(window_join_kernel<T, D, false>, ((int64_t)p.seqs.num_req * x.own_cap * p.kv_heads + 7) / 8, 256, 0, stream,
                     1, p);
@@ -1414,6 +1503,7 @@ int lmkv_attend_layer_window(const lmkv_pool_t* pool, void* const* scales, int32
     if (batch->num_req == 0 || batch->num_tokens == 0) return LMKV_OK;
     if (!rows_ok(q, 2) || !rows_ok(out, 2)) return LMKV_ERR_INVALID_ARG;
     const Plan x = make_plan(pool, num_q_heads, batch->num_tokens, batch->num_req, batch->max_new, batch->max_kv_len, false);
+    if ((int64_t)x.slots * pool->num_kv_heads * x.parts > INT32_MAX / 2) return LMKV_ERR_INVALID_ARG;
     if (workspace == nullptr || workspace_bytes < x.bytes) return LMKV_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(workspace) & 15) return LMKV_ERR_MISALIGNED;
     if (out->data == q->data) return LMKV_ERR_INVALID_ARG;
@@ -1429,6 +1519,8 @@ int lmkv_attend_layer_window(const lmkv_pool_t* pool, void* const* scales, int32
     p.part_o = static_cast<float*>(workspace);
     p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + parts * pool->head_dim * 4);
     p.own_range = reinterpret_cast<int2*>(p.part_ml + parts);
+    p.next_item = x.big_rows < INT32_MAX ? reinterpret_cast<int32_t*>(p.own_range + (int64_t)batch->num_req * x.own_tiles) : nullptr;
+    p.items = x.slots * pool->num_kv_heads * x.parts;
     p.own_base = x.tile_part_rows;
     p.scale_sign = scale > 0.f ? 1 : scale < 0.f ? -1 : 0;
     p.scale_log2 = scale == 0.f ? 1.f : std::fabs(scale) * kLog2e;
