@@ -703,7 +703,7 @@ using namespace lmkv_tc;
 constexpr int kTileRows = 256;        // two tiles of 128 rows share every K and V block
 constexpr int kLoaders = 6;           // warps that bring K and V
 // Registers of a softmax thread and of the others: 256 of each share the launch's 512 x 128.
-constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
+constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
 static_assert(kSoftmaxRegs + kOtherRegs == 2 * 128, "what one half gives, the other takes");
 constexpr int kTileThreads = (8 + kLoaders + 2) * 32;
 constexpr int kUnits = kBlock / kChunk;         // of 16 keys, in a block
@@ -1108,10 +1108,15 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
             const int c = lane % kPieces, rsub = lane / kPieces;
             uint32_t blocks_before = 0;
             bool ok = true;
-            Item item;
-            for (int32_t it = 0; ok && get(it, item); ++it) {
-            const uint8_t* const mine = base + (int64_t)item.h * kRowBytes + c * 16 + (int64_t)rsub * row_bytes;
-            const int32_t all_units = (item.b1 - item.b0) * 2 * kUnits;
+            for (int32_t it = 0; ok; ++it) {
+            const uint8_t* mine;
+            int32_t all_units;
+            {
+                Item item;
+                if (!get(it, item)) break;
+                mine = base + (int64_t)item.h * kRowBytes + c * 16 + (int64_t)rsub * row_bytes;
+                all_units = (item.b1 - item.b0) * 2 * kUnits;
+            }
             // What there is to know of unit u, and where this lane's part of it is.
             struct Unit {
                 uint32_t held;
@@ -1131,8 +1136,8 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
             auto stage_of = [&](int32_t u) { return (blocks_before * 2 + u / kUnits) % S::kStages; };
             const int32_t u_first = warp - 8;
             if constexpr (kCodes) {
-                // two units on their way in registers while one goes to shared memory
-                constexpr int kDeep = 3;
+                // a unit on its way in registers while one goes to shared memory
+                constexpr int kDeep = 2;
                 uint4 codes[kDeep][kCopies];
                 auto start = [&](int s, int32_t u) {
                     if (u >= all_units) return;
@@ -1197,7 +1202,7 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                     copies_arrive(full + 8 * stage);
                 }
             }
-            blocks_before += item.b1 - item.b0;
+            blocks_before += all_units / (2 * kUnits);
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
         } else if (warp == 8 + kLoaders) {
