@@ -703,7 +703,7 @@ using namespace lmkv_tc;
 constexpr int kTileRows = 256;        // two tiles of 128 rows share every K and V block
 constexpr int kLoaders = 6;           // warps that bring K and V
 // Registers of a softmax thread and of the others: 256 of each share the launch's 512 x 128.
-constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
+constexpr int kSoftmaxRegs = 192, kOtherRegs = 64;
 static_assert(kSoftmaxRegs + kOtherRegs == 2 * 128, "what one half gives, the other takes");
 constexpr int kTileThreads = (8 + kLoaders + 2) * 32;
 constexpr int kUnits = kBlock / kChunk;         // of 16 keys, in a block
@@ -1136,52 +1136,43 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
             auto stage_of = [&](int32_t u) { return (blocks_before * 2 + u / kUnits) % S::kStages; };
             const int32_t u_first = warp - 8;
             if constexpr (kCodes) {
-                // a unit on its way in registers while one goes to shared memory
-                constexpr int kDeep = 2;
-                uint4 codes[kDeep][kCopies];
-                auto start = [&](int s, int32_t u) {
-                    if (u >= all_units) return;
-                    const Unit x = find(u);
-#pragma unroll
-                    for (int r = 0; r < kCopies; ++r) {
-                        codes[s][r] = make_uint4(0u, 0u, 0u, 0u);
-                        if (x.on(r * kRowsPer + rsub))
-                            codes[s][r] = *reinterpret_cast<const uint4*>(x.src + r * kRowsPer * row_bytes);
-                    }
-                };
+                // (One unit of a warp at a time: a second on its way in registers does not fit without spilling, 395 : 372 us for prompts
+                // on an 8-bit cache; by cp.async into the unit's own place, and from there, 402, for shared memory's bandwidth.)
                 // Of a lane's 16 codes the fp16 values are two pieces of a row: those of its two halves in turn, so
-                // that they meet no bank twice.
+                // that they meet no bank twice; the other piece is the next or the one before, and rows r * kRowsPer
+                // further exchange by the next bits.
                 const bool odd = D == 128 && (c >> 2) != 0;
-                const uint32_t to = kv_smem + (D == 128 ? (c >> 2) * S::kHalfBytes : 0) + rsub * 128;
-                // (the other piece is the next or the one before; rows r * kRowsPer further exchange by the next bits)
-                const uint32_t first_piece = to + ((((2 * c + (odd ? 1 : 0)) & 7) ^ (rsub & 7)) << 4);
-#pragma unroll
-                for (int s = 0; s < kDeep - 1; ++s) start(s, u_first + s * kLoaders);
+                const uint32_t first_piece = kv_smem + (D == 128 ? (c >> 2) * S::kHalfBytes : 0) + rsub * 128 +
+                                             ((((2 * c + (odd ? 1 : 0)) & 7) ^ (rsub & 7)) << 4);
 #pragma unroll 1
-                for (int32_t u0 = u_first; u0 < all_units && ok; u0 += kDeep * kLoaders) {
-#pragma unroll
-                    for (int s = 0; s < kDeep; ++s) {
-                        const int32_t u = u0 + s * kLoaders;
-                        if (u >= all_units || !ok) break;
-                        start((s + kDeep - 1) % kDeep, u + (kDeep - 1) * kLoaders);
-                        ok = enter(u);
-                        if (!ok) break;
-                        const uint32_t dst = stage_of(u) * S::kStageBytes + u % kUnits * (kChunk * 128);
+                for (int32_t u = u_first; u < all_units; u += kLoaders) {
+                    uint4 codes[kCopies];
+                    {
+                        const Unit x = find(u);
 #pragma unroll
                         for (int r = 0; r < kCopies; ++r) {
-                            const uint4 v = codes[s][r];
-                            const uint32_t w[4] = {odd ? v.z : v.x, odd ? v.w : v.y, odd ? v.x : v.z, odd ? v.y : v.w};
-#pragma unroll
-                            for (int i = 0; i < 2; ++i)
-                                sts128(((first_piece ^ (i << 4)) ^ ((r * kRowsPer & 7) << 4)) + dst + r * (kRowsPer * 128),
-                                       make_uint4(codes_to_half2((uint16_t)w[2 * i]), codes_to_half2((uint16_t)(w[2 * i] >> 16)),
-                                                  codes_to_half2((uint16_t)w[2 * i + 1]),
-                                                  codes_to_half2((uint16_t)(w[2 * i + 1] >> 16))));
+                            codes[r] = make_uint4(0u, 0u, 0u, 0u);
+                            if (x.on(r * kRowsPer + rsub))
+                                codes[r] = *reinterpret_cast<const uint4*>(x.src + r * kRowsPer * row_bytes);
                         }
-                        __syncwarp();
-                        // (the products' thread has the writes seen by the tensor core, once for an item)
-                        if (lane == 0) mbar_arrive(full + 8 * stage_of(u));
                     }
+                    ok = ok && enter(u);
+                    if (!ok) break;
+                    const uint32_t dst = stage_of(u) * S::kStageBytes + u % kUnits * (kChunk * 128);
+#pragma unroll
+                    for (int r = 0; r < kCopies; ++r) {
+                        const uint4 v = codes[r];
+                        const uint32_t w[4] = {odd ? v.z : v.x, odd ? v.w : v.y, odd ? v.x : v.z, odd ? v.y : v.w};
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            sts128(((first_piece ^ (i << 4)) ^ ((r * kRowsPer & 7) << 4)) + dst + r * (kRowsPer * 128),
+                                   make_uint4(codes_to_half2((uint16_t)w[2 * i]), codes_to_half2((uint16_t)(w[2 * i] >> 16)),
+                                              codes_to_half2((uint16_t)w[2 * i + 1]),
+                                              codes_to_half2((uint16_t)(w[2 * i + 1] >> 16))));
+                    }
+                    __syncwarp();
+                    // (the products' thread has the writes seen by the tensor core, once for an item)
+                    if (lane == 0) mbar_arrive(full + 8 * stage_of(u));
                 }
             } else {
 #pragma unroll 1
