@@ -68,7 +68,8 @@ struct WindowParams {
     int32_t* next_item;     // those taken (beyond one for each CTA); the streams begin it
     int64_t own_base;       // rows of partial results before the streams'
     bool q_pairs;           // q rows are 4-byte aligned
-    bool q_vec, out_vec;    // 16-byte aligned
+    bool q_vec;             // 16-byte aligned
+    bool out_wide;          // out rows are 32-byte aligned
     FastDiv by_group;
 
     __device__ __forceinline__ int64_t own_part(int32_t stream, int32_t tile_no, int32_t row, int32_t h) const {
@@ -852,21 +853,20 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                         for (int j = 0; j < 16; ++j) y[j] = 0u;
                     }
                     if (live && final) {
+                        // (a lane writes 32 bytes of its row at once: rows lie apart, and every part of one takes its own turn)
+                        uint32_t w[8];
 #pragma unroll
-                        for (int j = 0; j < 16; j += 8) {
-                            uint32_t w[4];
+                        for (int i = 0; i < 8; ++i)
+                            w[i] = Elem<T>::pack(__uint_as_float(y[2 * i]) * inv, __uint_as_float(y[2 * i + 1]) * inv);
+                        if (p.out_wide) {
+                            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + c), "r"(w[0]),
+                                         "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+                        } else {
+                            uint16_t* const e = reinterpret_cast<uint16_t*>(to + c);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                w[i] = Elem<T>::pack(__uint_as_float(y[j + 2 * i]) * inv, __uint_as_float(y[j + 2 * i + 1]) * inv);
-                            if (p.out_vec) {
-                                *reinterpret_cast<uint4*>(to + c + j) = make_uint4(w[0], w[1], w[2], w[3]);
-                            } else {
-                                uint16_t* const e = reinterpret_cast<uint16_t*>(to + c + j);
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    e[2 * i] = (uint16_t)w[i];
-                                    e[2 * i + 1] = (uint16_t)(w[i] >> 16);
-                                }
+                            for (int i = 0; i < 8; ++i) {
+                                e[2 * i] = (uint16_t)w[i];
+                                e[2 * i + 1] = (uint16_t)(w[i] >> 16);
                             }
                         }
                     } else if (live) {
@@ -1536,7 +1536,7 @@ int lmkv_attend_layer_window(const lmkv_pool_t* pool, void* const* scales, int32
         return reinterpret_cast<uintptr_t>(r->data) % to == 0 && r->token_stride * 2 % to == 0 && r->head_stride * 2 % to == 0;
     };
     p.q_vec = aligned(q, 16);
-    p.out_vec = aligned(out, 16);
+    p.out_wide = aligned(out, 32);
     p.q_pairs = aligned(q, 4);
     p.by_group = FastDiv((uint32_t)(num_q_heads / pool->num_kv_heads));
     return dtype == LMKV_BF16 ? window_dims<__nv_bfloat16>(p, x, pool, stream) : window_dims<__half>(p, x, pool, stream);
