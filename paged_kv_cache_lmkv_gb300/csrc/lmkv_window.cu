@@ -1136,26 +1136,29 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
             auto stage_of = [&](int32_t u) { return (blocks_before * 2 + u / kUnits) % S::kStages; };
             const int32_t u_first = warp - 8;
             if constexpr (kCodes) {
-                // (One unit of a warp at a time: a second on its way in registers does not fit without spilling, 395 : 372 us for prompts
-                // on an 8-bit cache; by cp.async into the unit's own place, and from there, 402, for shared memory's bandwidth.)
+                // Registers that a part of a unit has left take that part of the warp's next.  (Prompts on an 8-bit cache: one unit at a time
+                // 371 us, two in registers of their own, which spill, 395; by cp.async into the unit's own place, and from
+                // there, 402, for shared memory's bandwidth.)
                 // Of a lane's 16 codes the fp16 values are two pieces of a row: those of its two halves in turn, so
                 // that they meet no bank twice; the other piece is the next or the one before, and rows r * kRowsPer
                 // further exchange by the next bits.
                 const bool odd = D == 128 && (c >> 2) != 0;
                 const uint32_t first_piece = kv_smem + (D == 128 ? (c >> 2) * S::kHalfBytes : 0) + rsub * 128 +
                                              ((((2 * c + (odd ? 1 : 0)) & 7) ^ (rsub & 7)) << 4);
+                uint4 codes[kCopies];
+                auto load = [&](const Unit& x, int r) {
+                    codes[r] = make_uint4(0u, 0u, 0u, 0u);
+                    if (x.on(r * kRowsPer + rsub)) codes[r] = *reinterpret_cast<const uint4*>(x.src + r * kRowsPer * row_bytes);
+                };
+                if (u_first < all_units) {
+                    const Unit x = find(u_first);
+#pragma unroll
+                    for (int r = 0; r < kCopies; ++r) load(x, r);
+                }
 #pragma unroll 1
                 for (int32_t u = u_first; u < all_units; u += kLoaders) {
-                    uint4 codes[kCopies];
-                    {
-                        const Unit x = find(u);
-#pragma unroll
-                        for (int r = 0; r < kCopies; ++r) {
-                            codes[r] = make_uint4(0u, 0u, 0u, 0u);
-                            if (x.on(r * kRowsPer + rsub))
-                                codes[r] = *reinterpret_cast<const uint4*>(x.src + r * kRowsPer * row_bytes);
-                        }
-                    }
+                    Unit next{0u, mine};
+                    if (u + kLoaders < all_units) next = find(u + kLoaders);
                     ok = ok && enter(u);
                     if (!ok) break;
                     const uint32_t dst = stage_of(u) * S::kStageBytes + u % kUnits * (kChunk * 128);
@@ -1169,6 +1172,7 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                                    make_uint4(codes_to_half2((uint16_t)w[2 * i]), codes_to_half2((uint16_t)(w[2 * i] >> 16)),
                                               codes_to_half2((uint16_t)w[2 * i + 1]),
                                               codes_to_half2((uint16_t)(w[2 * i + 1] >> 16))));
+                        load(next, r);
                     }
                     __syncwarp();
                     // (the products' thread has the writes seen by the tensor core, once for an item)
@@ -1197,21 +1201,49 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
         } else if (warp == 8 + kLoaders) {
-            // the last row tiles of a request see the most keys: they begin first
+            // Where the requests are few: those with the most keys before others, lane r's row tiles from the
+            // first_tile-th on.
+            const bool sorted = p.seqs.num_req <= 32;
+            int32_t tiles = 0, first_tile = 0, all_tiles = p.slots;
+            if (sorted) {
+                int32_t keys = -1;
+                if (lane < p.seqs.num_req) {
+                    const Req r = load_req(p.seqs, lane);
+                    if (r.n * group >= p.big_rows) tiles = (r.n * group + kTileRows - 1) / kTileRows;
+                    keys = r.len;
+                }
+                all_tiles = 0;
+                for (int i = 0; i < 32; ++i) {
+                    const int32_t t = __shfl_sync(0xFFFFFFFFu, tiles, i), k = __shfl_sync(0xFFFFFFFFu, keys, i);
+                    if (k > keys || (k == keys && i < lane)) first_tile += t;
+                    all_tiles += t;
+                }
+            }
             uint32_t blocks_before = 0;
             for (int32_t it = 0, next = blockIdx.x;; ) {
                 Item x = {};
                 x.h = -1;
-                if (next < p.items) {
+                if (next < (int64_t)all_tiles * p.kv_heads * p.parts) {
                     const int32_t h = next % p.kv_heads;
-                    const int32_t of = next / p.kv_heads, slot = p.slots - 1 - of % p.slots;
-                    // slots q_start[r] * group / 256 + r and on are request r's row tiles
-                    auto key = [&](int32_t i) { return (int32_t)((int64_t)max(p.seqs.q_start[i], 0) * group / kTileRows) + i; };
-                    const int32_t r = find_request(p.seqs.num_req, slot, key);
-                    const Req req = load_req(p.seqs, r);
-                    const int32_t req_rows = req.n * group;
-                    x.part = of / p.slots;
-                    x.row0 = slot >= key(r) ? (slot - key(r)) * kTileRows : req_rows;
+                    const int32_t of = next / p.kv_heads, at = of % all_tiles;
+                    int32_t r, req_rows;
+                    Req req;
+                    x.part = of / all_tiles;
+                    // the last row tiles of a request see the most keys: they begin first
+                    if (sorted) {
+                        r = __ffs(__ballot_sync(0xFFFFFFFFu, at >= first_tile && at < first_tile + tiles)) - 1;
+                        req = load_req(p.seqs, r);
+                        req_rows = req.n * group;
+                        x.row0 = (__shfl_sync(0xFFFFFFFFu, first_tile + tiles, r) - 1 - at) * kTileRows;
+                    } else {
+                        // slots q_start[r] * group / 256 + r and on are request r's row tiles
+                        const int32_t slot = p.slots - 1 - at;
+                        auto key = [&](int32_t i) { return (int32_t)((int64_t)max(p.seqs.q_start[i], 0) * group / kTileRows) + i; };
+                        r = find_request(p.seqs.num_req, slot, key);
+                        req = load_req(p.seqs, r);
+                        req_rows = req.n * group;
+                        x.row0 = slot >= key(r) ? (slot - key(r)) * kTileRows : req_rows;
+                    }
                     int32_t taken = 0;
                     if (lane == 0) taken = atomicAdd(p.next_item, 1);
                     next = (int32_t)gridDim.x + __shfl_sync(0xFFFFFFFFu, taken, 0);
