@@ -1415,7 +1415,12 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
 
 // ---- host ---------------------------------------------------------------
 
-constexpr int kBigRows = 64;
+// Rows of a request from which tiles take it.  (Tiles against streams, us, 8 KV heads of 128, by rows: 8 bits, 8 requests of 4000
+// keys 24: 59 : 48, 32: 57 : 49, 48: 59 : 62; 64 of 1000 24: 100 : 85, 32: 94 : 89, 48: 98 : 122; 16 bits 8 of 4000 16: 54 : 53, 48: 53 : 80;
+// 64 of 1000 16: 86 : 68, 48: 85 : 147.  Between, tiles gain where all requests are alike and lose where few of them
+// are so big, as they then have the SMs to themselves for as long: 12 requests of 16 to 40 rows, 700 to 7000 keys, all in streams 60 and 71 us
+// for 8 and 16 bits, those of 40 in tiles 96 and 95.)
+constexpr int kBigRows = 48;
 // CTAs of the tile kernel up to which it splits the keys: two rounds of one an SM.
 constexpr int64_t kMostTileCtas = 2 * kSms;
 
