@@ -35,7 +35,6 @@ struct NormedParams {
     int32_t head_sets;         // of kHeads heads, of K and of V
     float eps;
     bool vectors;              // a lane's pairs are two vectors of eight elements
-    bool vec_q, vec_out, vec_k, vec_v;      // and the rows allow loads of those
     FastDiv by_sets;
     Rotary rot;                // half == 0: none
 };
@@ -82,8 +81,9 @@ struct RowOf {
         asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x), "=r"(y), "=r"(z), "=r"(w)
                      : "l"(at) : "memory");
     }
-    __device__ __forceinline__ void load(const NormedParams& p, const T* row, int l, bool vec) {
-        if (vec) {
+    template <bool kVec>
+    __device__ __forceinline__ void load(const NormedParams& p, const T* row, int l) {
+        if constexpr (kVec) {
             ld16(row + P::first_vector(p, l), raw[0], raw[1], raw[2], raw[3]);
             ld16(row + P::second_vector(p, l), raw[4], raw[5], raw[6], raw[7]);
         } else {
@@ -153,11 +153,10 @@ __device__ __forceinline__ void norm_and_turn(const NormedParams& p, const RowOf
 }
 
 // The lane's 16 values to a row of T.
-template <class T, int D, bool kInterleaved>
-__device__ __forceinline__ void store_row(const NormedParams& p, T* row, int l, const float (&a)[8], const float (&b)[8],
-                                          bool vec) {
+template <class T, int D, bool kInterleaved, bool kVec>
+__device__ __forceinline__ void store_row(const NormedParams& p, T* row, int l, const float (&a)[8], const float (&b)[8]) {
     using P = Pairs<D, kInterleaved>;
-    if (vec) {
+    if constexpr (kVec) {
         uint32_t w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -175,7 +174,7 @@ __device__ __forceinline__ void store_row(const NormedParams& p, T* row, int l, 
     }
 }
 // As codes of value * factor.
-template <int D, bool kInterleaved>
+template <int D, bool kInterleaved, bool kVec>
 __device__ __forceinline__ void store_codes(const NormedParams& p, uint8_t* row, int l, float (&a)[8], float (&b)[8], float factor) {
     using P = Pairs<D, kInterleaved>;
 #pragma unroll
@@ -183,7 +182,7 @@ __device__ __forceinline__ void store_codes(const NormedParams& p, uint8_t* row,
         a[i] = fabsf(a[i]) < INFINITY ? a[i] * factor : NAN;
         b[i] = fabsf(b[i]) < INFINITY ? b[i] * factor : NAN;
     }
-    if (kInterleaved || p.vectors) {
+    if constexpr (kVec) {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -206,15 +205,14 @@ __device__ __forceinline__ void store_codes(const NormedParams& p, uint8_t* row,
     }
 }
 
-// A token's cached number and position.
+// A token's position.
 struct Place {
-    int32_t index;
     int64_t position;
     bool live;         // not a padded row
 };
 
 // One token's heads of q.
-template <class T, int D, bool kInterleaved>
+template <class T, int D, bool kInterleaved, bool kVec>
 __device__ __forceinline__ void append_q(const NormedParams& p, int32_t t, float4* table) {
     using P = Pairs<D, kInterleaved>;
     constexpr int kGroups = kThreads / P::kLanes;
@@ -225,25 +223,28 @@ __device__ __forceinline__ void append_q(const NormedParams& p, int32_t t, float
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
             const int32_t h = h0 + j * kGroups + g;
-            if (h < p.q_heads) x[j].load(p, p.q.row<T>(t, h), l, p.vec_q);
+            if (h < p.q_heads) x[j].template load<kVec>(p, p.q.row<T>(t, h), l);
             else x[j].clear();
         }
     };
     // the first rows are on their way before the look-ups
     load(0);
-    if (threadIdx.x < 32) {
+    // The position, where it is given, needs no request; what another warp finds out about that is only reported.
+    const bool given = p.positions != nullptr;
+    if (given && threadIdx.x == 0)
+        place = Place{p.positions[t], t >= p.seqs.q_start[0] && t < p.seqs.q_start[p.seqs.num_req]};
+    if (threadIdx.x >= 32 && threadIdx.x < 64) {
         const int32_t r = find_request(p.seqs.num_req, t, [&](int32_t i) { return p.seqs.q_start[i]; });
-        if (threadIdx.x == 0) {
+        if (threadIdx.x == 32) {
             const Req q = load_req(p.seqs, r);
             const int32_t end = min(max(p.seqs.q_start[r + 1], q.q0), p.seqs.num_tokens);
-            Place x{0, 0, t >= q.q0 && t < end};
-            if (x.live) {
-                x.index = q.len - (end - q.q0) + (t - q.q0);
-                x.position = p.positions != nullptr ? p.positions[t] : (int64_t)x.index;
+            const bool live = t >= q.q0 && t < end;
+            const int32_t index = q.len - (end - q.q0) + (t - q.q0);
+            if (live) {
                 const bool whole = q.len == p.seqs.kv_len[r] && q.q0 == p.seqs.q_start[r] && end == p.seqs.q_start[r + 1];
-                if (!whole || x.index < 0) report(p.status, LMKV_ERR_BAD_LENGTH);
+                if (!whole || index < 0) report(p.status, LMKV_ERR_BAD_LENGTH);
             }
-            place = x;
+            if (!given) place = Place{index, live};
         }
     }
     __syncthreads();
@@ -260,7 +261,7 @@ __device__ __forceinline__ void append_q(const NormedParams& p, int32_t t, float
             if (h0 + j * kGroups >= p.q_heads) break;
             float a[8], b[8];
             norm_and_turn<T, D, kInterleaved>(p, x[j], l, p.q_norm != nullptr, table + l, a, b);
-            if (h < p.q_heads) store_row<T, D, kInterleaved>(p, p.q_out.row<T>(t, h), l, a, b, p.vec_out);
+            if (h < p.q_heads) store_row<T, D, kInterleaved, kVec>(p, p.q_out.row<T>(t, h), l, a, b);
         }
     }
 }
@@ -276,7 +277,7 @@ constexpr int kLowest = -60, kHighest = 60;
 // The new tokens of one page: kHeads heads of K or of V.  A page's tokens of a head have to be seen
 // before the first is written, as they share a scale, so kHeads heads are spread over the
 // CTA token by token and meet in shared memory.  Pages of more tokens than fit its registers are read twice.
-template <class T, int D, bool kCodes, bool kInterleaved>
+template <class T, int D, bool kCodes, bool kInterleaved, bool kVec>
 __device__ __forceinline__ void append_page(const NormedParams& p, int32_t cta, float4* table) {
     using P = Pairs<D, kInterleaved>;
     constexpr int kGroups = kThreads / P::kLanes;
@@ -332,7 +333,6 @@ __device__ __forceinline__ void append_page(const NormedParams& p, int32_t cta, 
     const int32_t h = (kv ? set - sets : set) * kHeads + hs;
     const bool head = h < p.kv_heads;
     const Rows& in = kv ? p.v : p.k;
-    const bool vec = kv ? p.vec_v : p.vec_k;
     // the page's row of its token i
     auto place = [&](int32_t i) {
         return base + kv * p.layer.half_bytes() + ((int64_t)blk * B + i) * p.layer.row_bytes + (int64_t)h * D * (kCodes ? 1 : 2);
@@ -353,7 +353,7 @@ __device__ __forceinline__ void append_page(const NormedParams& p, int32_t cta, 
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
             const int32_t i = i0 + j * kRows + row0;
-            if (head && i < b) raw[j].load(p, in.row<T>(t0 + (i - a), h), l, vec);
+            if (head && i < b) raw[j].template load<kVec>(p, in.row<T>(t0 + (i - a), h), l);
             else raw[j].clear();
         }
         if (!kv) {
@@ -432,34 +432,38 @@ __device__ __forceinline__ void append_page(const NormedParams& p, int32_t cta, 
             float x[8], y[8];
             value(j, x, y);
             if (!head || i + row0 >= b) continue;
-            if constexpr (kCodes) store_codes<D, kInterleaved>(p, place(i + row0), l, x, y, factor);
-            else store_row<T, D, kInterleaved>(p, reinterpret_cast<T*>(place(i + row0)), l, x, y, kInterleaved || p.vectors);
+            if constexpr (kCodes) store_codes<D, kInterleaved, kVec>(p, place(i + row0), l, x, y, factor);
+            else store_row<T, D, kInterleaved, kVec>(p, reinterpret_cast<T*>(place(i + row0)), l, x, y);
         }
     }
 }
 
 // The CTAs of the pages come first, as theirs is the longer chain of waits, then a
-// CTA a token for q.
-template <class T, int D, bool kCodes, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads, 5) append_normed_kernel(const __grid_constant__ NormedParams p) {
+// CTA a token for q.  (Rows that do not go by vectors have a kernel of their own: their loads, one by one, would
+// take its registers.)
+template <class T, int D, bool kCodes, bool kInterleaved, bool kVec>
+__global__ void __launch_bounds__(kThreads, kVec ? 5 : 4) append_normed_kernel(const __grid_constant__ NormedParams p) {
     constexpr int kRound = kThreads / (D / 16) / kHeads * kPer;
     __shared__ float4 table[kRound * (D / 2)];
     pdl_launch_dependents();
     pdl_wait();
-    if ((int32_t)blockIdx.x < p.kv_ctas) append_page<T, D, kCodes, kInterleaved>(p, blockIdx.x, table);
-    else append_q<T, D, kInterleaved>(p, blockIdx.x - p.kv_ctas, table);
+    if ((int32_t)blockIdx.x < p.kv_ctas) append_page<T, D, kCodes, kInterleaved, kVec>(p, blockIdx.x, table);
+    else append_q<T, D, kInterleaved, kVec>(p, blockIdx.x - p.kv_ctas, table);
 }
 
 template <class T, int D, bool kCodes>
-int launch_normed(const NormedParams& p, void* stream) {
+int launch_normed(const NormedParams& p, bool vec, void* stream) {
     const int64_t ctas = (int64_t)p.kv_ctas + p.seqs.num_tokens;
-    return p.rot.interleaved ? launch(append_normed_kernel<T, D, kCodes, true>, ctas, kThreads, 0, stream, 1, p)
-                             : launch(append_normed_kernel<T, D, kCodes, false>, ctas, kThreads, 0, stream, 1, p);
+    if (vec)
+        return p.rot.interleaved ? launch(append_normed_kernel<T, D, kCodes, true, true>, ctas, kThreads, 0, stream, 1, p)
+                                 : launch(append_normed_kernel<T, D, kCodes, false, true>, ctas, kThreads, 0, stream, 1, p);
+    return p.rot.interleaved ? launch(append_normed_kernel<T, D, kCodes, true, false>, ctas, kThreads, 0, stream, 1, p)
+                             : launch(append_normed_kernel<T, D, kCodes, false, false>, ctas, kThreads, 0, stream, 1, p);
 }
 template <class T>
-int normed_typed(const NormedParams& p, int32_t head_dim, bool codes, void* stream) {
-    if (head_dim == 64) return codes ? launch_normed<T, 64, true>(p, stream) : launch_normed<T, 64, false>(p, stream);
-    return codes ? launch_normed<T, 128, true>(p, stream) : launch_normed<T, 128, false>(p, stream);
+int normed_typed(const NormedParams& p, int32_t head_dim, bool codes, bool vec, void* stream) {
+    if (head_dim == 64) return codes ? launch_normed<T, 64, true>(p, vec, stream) : launch_normed<T, 64, false>(p, vec, stream);
+    return codes ? launch_normed<T, 128, true>(p, vec, stream) : launch_normed<T, 128, false>(p, vec, stream);
 }
 
 }  // namespace
@@ -496,13 +500,10 @@ extern "C" int lmkv_append_layer_normed(const lmkv_pool_t* pool, void* const* sc
     p.kv_heads = pool->num_kv_heads;
     p.eps = eps;
     p.vectors = p.rot.half % 8 == 0;
-    auto vec = [&](const lmkv_rows_t* x) {
-        return (p.vectors || p.rot.interleaved) && reinterpret_cast<uintptr_t>(x->data) % 16 == 0 && x->token_stride % 8 == 0 && x->head_stride % 8 == 0;
-    };
-    p.vec_q = vec(q);
-    p.vec_out = vec(q_out);
-    p.vec_k = vec(k);
-    p.vec_v = vec(v);
+    // 16-byte vectors where a lane's pairs are such and every row starts on 16 bytes
+    bool vec = p.vectors || p.rot.interleaved;
+    for (const lmkv_rows_t* x : {q, k, v, q_out})
+        vec = vec && reinterpret_cast<uintptr_t>(x->data) % 16 == 0 && x->token_stride % 8 == 0 && x->head_stride % 8 == 0;
     p.head_sets = 2 * ((p.kv_heads + kHeads - 1) / kHeads);
     p.by_sets = FastDiv((uint32_t)p.head_sets);
     const int64_t slots = (int64_t)batch->num_tokens / pool->block_size + 2 * (int64_t)batch->num_req;
@@ -510,6 +511,6 @@ extern "C" int lmkv_append_layer_normed(const lmkv_pool_t* pool, void* const* sc
     if (ctas + batch->num_tokens > INT32_MAX) return LMKV_ERR_INVALID_ARG;
     p.kv_ctas = (int32_t)ctas;
     const bool codes = pool->elem_bytes == 1;
-    return dtype == LMKV_BF16 ? normed_typed<__nv_bfloat16>(p, pool->head_dim, codes, stream)
-                              : normed_typed<__half>(p, pool->head_dim, codes, stream);
+    return dtype == LMKV_BF16 ? normed_typed<__nv_bfloat16>(p, pool->head_dim, codes, vec, stream)
+                              : normed_typed<__half>(p, pool->head_dim, codes, vec, stream);
 }
