@@ -756,7 +756,8 @@ int lmkv_evict_layer(const lmkv_pool_t* pool, int32_t layer, const int32_t* bloc
  * 8-bit pages.  Of each head of q and of k,
  *   y = x / sqrt(mean(x^2) + eps) * norm   (Zhang and Sennrich, "Root Mean
  *   Square Layer Normalization", 2019; left out where its norm is NULL)
- * is turned as `rotary` says (left out when NULL); all in fp32, rounded once.
+ * is turned as `rotary` says (left out when NULL); all in fp32 (the squares too: heads of values within
+ * 2^+-60), rounded once.
  *   dtype  : of q, k, v and q_out, LMKV_BF16 or LMKV_FP16; a 16-bit pool's own
  *   q_norm, k_norm : DEVICE float32 [head_dim] or NULL;  eps >= 0, finite
  * 8-bit pages: where new tokens of a head come into a page, its exponent (byte
@@ -788,7 +789,7 @@ int lmkv_append_layer_normed(const lmkv_pool_t* pool, void* const* scales, int32
  * not finite reaches no row that does not see it but those of other new tokens
  * of its request.  8-bit pages: q is taken to fp16 relative to its row's largest element (below 2^-38
  * of that it loses bits), softmax weights times the page's V scale are
- * rounded to fp16 before they meet the codes.  The V scales that one row sees
+ * rounded to fp16 before they meet the codes.  V scales below 2^-90 count as 2^-90.  Those that one row sees
  * may differ by up to 2^64; pages that are further below the largest may count as nothing.
  * INVALID_ARG for window < 0, sinks < 0, scales that do not match elem_bytes;
  * other types, sizes and errors as lmkv_attend_layer. */

@@ -81,6 +81,8 @@ constexpr float kLn2 = 0.69314718055994530942f, kLog2e = 1.44269504088896340736f
 // Weights are relative to 2^kBelow less than a maximum that may lag by 2^kLag, so they are 2^14
 // at most, and those of 2^-20 of the largest are still normal fp16 numbers.
 constexpr float kBelow = 6.f, kLag = 8.f;
+// V's scales are at least 2^-90: the sum of weights holds their inverse.
+constexpr uint32_t kLeastScale = 127 - 90;
 // A finite number below every score, so that the first keys need no case of their own.
 constexpr float kNone = -0x1p126f;
 
@@ -365,7 +367,7 @@ struct StreamRows {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 // 2^(byte - 127), byte - 127 and 2^(127 - byte) by their bits (2^-127 is not a normal number)
-                const uint32_t kb = (info.scales >> (16 * i)) & 0xFF, vb = (info.scales >> (16 * i + 8)) & 0xFF;
+                const uint32_t kb = (info.scales >> (16 * i)) & 0xFF, vb = max((info.scales >> (16 * i + 8)) & 0xFF, kLeastScale);
                 k_scale[i] = __uint_as_float(max(kb << 23, 0x00400000u));
                 v_power[i] = __uint_as_float(0x4B000000u | vb) - (8388608.f + 127.f);
                 v_back[i] = __uint_as_float(max((254u - vb) << 23, 0x00400000u));
@@ -1293,7 +1295,7 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                                 row = rows = 0;
                             } else if (kCodes) {
                                 kb = scales[p.scales.at(0, blk, x.h)];
-                                vb = scales[p.scales.at(1, blk, x.h)];
+                                vb = max((uint32_t)scales[p.scales.at(1, blk, x.h)], kLeastScale);
                             }
                         }
                     }

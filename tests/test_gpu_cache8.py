@@ -397,7 +397,7 @@ def test_attend_scales_of_scores(new, wide, scale):
 
 
 @pytest.mark.parametrize("new", [1, 5, 40])
-@pytest.mark.parametrize("exps", [(-60, -55), (50, 60), (-30, 10)])
+@pytest.mark.parametrize("exps", [(-60, -55), (50, 60), (-30, 10), (-89, -80), (90, 105)])
 def test_attend_page_scales(new, exps):
     """Scales far from 1 and far from one another; q is made to fit K's."""
     b = Cache([new], [300], 8, 2, 128, BF, exps=exps, seed=5)
