@@ -613,16 +613,20 @@ window_streams_kernel(const __grid_constant__ WindowParams p) {
     }
 }
 
-// Joins the parts of rows that have them, a warp a row: of the small requests' rows
-// (kTiles false: a stream's parts each) or of the big ones' (the tile kernel's parts).
-template <class T, int D, bool kTiles>
-__global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant__ WindowParams p) {
+// Joins the parts of rows that have them: of the small requests' rows (kTiles false: a
+// stream's parts each) or of the big ones' (the tile kernel's parts).  kRowWarps warps a row: one where there are many rows, of few parts
+// each, and all of a CTA's where few rows have many.
+template <class T, int D, bool kTiles, int kRowWarps>
+__global__ void __launch_bounds__(kRowWarps == 1 ? 256 : kRowWarps * 32) window_join_kernel(const __grid_constant__ WindowParams p) {
     constexpr int kPer = D / 32;
+    constexpr int kGroup = kRowWarps == 1 ? 32 : 8;        // parts at a time
+    __shared__ float sums[kRowWarps == 1 ? 1 : kRowWarps][kRowWarps == 1 ? 1 : D];
+    __shared__ float2 tops[kRowWarps];
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = kRowWarps == 1 ? 0 : threadIdx.x >> 5;
     const int32_t group = (int32_t)p.by_group.d;
-    int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    int64_t i = kRowWarps == 1 ? (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
     int32_t tok, head, parts;
     int64_t first, stride;
     if constexpr (kTiles) {
@@ -653,12 +657,23 @@ __global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant_
         first = p.own_part(g, tile_no, row % p.tile_rows, h);
         stride = (int64_t)p.tile_rows * p.kv_heads;
     }
-    // m and l of 32 parts at a time, one a lane; then the parts' sums, whose loads
+    // m and l of some parts at a time, one a lane; then the parts' sums, whose loads
     // do not wait for one another
     float top = -INFINITY, sum = 0.f, acc[kPer] = {};
-    for (int32_t s0 = 0; s0 < parts; s0 += 32) {
-        const int32_t n = min(32, parts - s0);
+    for (int32_t s0 = warp * kGroup; s0 < parts; s0 += kGroup * kRowWarps) {
+        const int32_t n = min(kGroup, parts - s0);
         const float2 v = lane < n ? p.part_ml[first + (s0 + lane) * stride] : make_float2(-INFINITY, 0.f);
+        constexpr int kAhead = 8;
+        float x[kAhead][kPer];
+        auto load = [&](int32_t s) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const float* src = p.part_o + (first + min(s0 + s + u, parts - 1) * stride) * D + lane * kPer;
+                if constexpr (kPer == 4) *reinterpret_cast<float4*>(x[u]) = *reinterpret_cast<const float4*>(src);
+                else *reinterpret_cast<float2*>(x[u]) = *reinterpret_cast<const float2*>(src);
+            }
+        };
+        load(0);
         float mn = v.x;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, d));
@@ -672,15 +687,8 @@ __global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant_
         sum = sum * before + l;
 #pragma unroll
         for (int k = 0; k < kPer; ++k) acc[k] *= before;
-        constexpr int kAhead = 8;
         for (int32_t s = 0; s < n; s += kAhead) {
-            float x[kAhead][kPer];
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const float* src = p.part_o + (first + min(s0 + s + u, parts - 1) * stride) * D + lane * kPer;
-                if constexpr (kPer == 4) *reinterpret_cast<float4*>(x[u]) = *reinterpret_cast<const float4*>(src);
-                else *reinterpret_cast<float2*>(x[u]) = *reinterpret_cast<const float2*>(src);
-            }
+            if (s > 0) load(s);
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 const float fs = __shfl_sync(0xFFFFFFFFu, f, (s + u) & 31);
@@ -689,6 +697,29 @@ __global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant_
                     for (int k = 0; k < kPer; ++k) acc[k] += x[u][k] * fs;
                 }
             }
+        }
+    }
+    if constexpr (kRowWarps > 1) {
+        if (lane == 0) tops[warp] = make_float2(top, sum);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) sums[warp][lane * kPer + k] = acc[k];
+        __syncthreads();
+        if (warp != 0) return;
+        const float2 v = lane < kRowWarps ? tops[lane] : make_float2(-INFINITY, 0.f);
+        top = v.x;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        const float f = exp2_fast(v.x - (top == -INFINITY ? 0.f : top));
+        sum = v.y * f;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kRowWarps; ++w) {
+            const float fw = __shfl_sync(0xFFFFFFFFu, f, w);
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) acc[k] += sums[w][lane * kPer + k] * fw;
         }
     }
     const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
@@ -1098,6 +1129,7 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                 blocks_before += blocks;
             }
             if (row_left && ok) finish();
+            cp_wait<0>();
         } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp < 8 + kLoaders) {
@@ -1426,6 +1458,10 @@ constexpr int kBigRows = 48;
 // CTAs of the tile kernel up to which it splits the keys: two rounds of one an SM.
 constexpr int64_t kMostTileCtas = 2 * kSms;
 
+// Rows up to which a CTA joins each.
+constexpr int kJoinWarps = 32;
+constexpr int64_t kFewRows = 4 * kSms;
+
 struct Plan {
     int32_t big_rows, own_cap, own_tiles, tile_rows, streams, slots, parts;
     int64_t tile_part_rows, own_rows;
@@ -1483,17 +1519,19 @@ int window_typed(const WindowParams& p, const Plan& x, void* stream) {
     if (rc == LMKV_OK) rc = allow_smem<window_tiles_kernel<T, KV, D>, WindowTile<D>::kSmem>();
     if (rc == LMKV_OK) rc = keep_carveout<window_streams_kernel<T, KV, D, 1>>();
     if (rc == LMKV_OK) rc = keep_carveout<window_streams_kernel<T, KV, D, 2>>();
-    if (rc == LMKV_OK) rc = keep_carveout<window_join_kernel<T, D, false>>();
-    if (rc == LMKV_OK) rc = keep_carveout<window_join_kernel<T, D, true>>();
+    if (rc == LMKV_OK) rc = keep_carveout<window_join_kernel<T, D, false, 1>>();
+    if (rc == LMKV_OK) rc = keep_carveout<window_join_kernel<T, D, false, kJoinWarps>>();
+    if (rc == LMKV_OK) rc = keep_carveout<window_join_kernel<T, D, true, 1>>();
     if (rc == LMKV_OK) rc = x.tile_rows == 8 ? launch_streams<T, KV, D, 1>(p, stream) : launch_streams<T, KV, D, 2>(p, stream);
     if (rc == LMKV_OK && x.big_rows < INT32_MAX)
         rc = launch(window_tiles_kernel<T, KV, D>, p.items < kSms ? p.items : kSms, kTileThreads, WindowTile<D>::kSmem, stream, 1,
                     p);
+    const int64_t rows = (int64_t)p.seqs.num_req * x.own_cap * p.kv_heads;
     if (rc == LMKV_OK)
-        rc = launch(window_join_kernel<T, D, false>, ((int64_t)p.seqs.num_req * x.own_cap * p.kv_heads + 7) / 8, 256, 0, stream,
-                    1, p);
+        rc = rows <= kFewRows ? launch(window_join_kernel<T, D, false, kJoinWarps>, rows, kJoinWarps * 32, 0, stream, 1, p)
+                              : launch(window_join_kernel<T, D, false, 1>, (rows + 7) / 8, 256, 0, stream, 1, p);
     if (rc == LMKV_OK && x.parts > 1)
-        rc = launch(window_join_kernel<T, D, true>, ((int64_t)p.rows + 7) / 8, 256, 0, stream, 1, p);
+        rc = launch(window_join_kernel<T, D, true, 1>, ((int64_t)p.rows + 7) / 8, 256, 0, stream, 1, p);
     return rc;
 }
 
