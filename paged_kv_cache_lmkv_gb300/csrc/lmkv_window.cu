@@ -505,16 +505,17 @@ struct StreamRows {
     }
 };
 
-// (An SM's shared memory is not all taken: behind a kernel that needs less of it, as the join, a launch that
+// (128 KB of an SM's shared memory are taken at most: behind a kernel that needs less of it, as the join, a launch that
 // depends on it did not get its blocks beside one another.  64 users of 1000 to 9000 tokens, 8 bits, 16 warps an SM: rings of
-// three, 192 KB, 124 us by themselves and 198 in a row, of two, 128 KB, 123 in a row.)
+// three, 192 KB, 124 us by themselves and 198 in a row, of two, 128 KB, 123 in a row.  48 users with a window of 4096, 16 bits: 12 warps
+// an SM, 192 KB, 135 us, 8 warps, 128 KB, 114.)
 template <class KV, int D, int NT>
 struct StreamShape {
     static constexpr int kTile = Fragments<KV, D>::kTileBytes;             // 1, 2 or 4 KB
-    static constexpr int kStages = kTile >= 4096 ? 2 : kTile >= 2048 ? (NT > 1 ? 3 : 2) : 4;
+    static constexpr int kStages = kTile >= 2048 ? 2 : 4;
     static constexpr int kWarpBytes = kStages * 2 * kTile;
     static constexpr int kSmem = kWarps * kWarpBytes;
-    static constexpr int kCtas = kTile >= 4096 || NT > 1 ? 3 : 4;          // an SM
+    static constexpr int kCtas = kTile >= 4096 ? 2 : NT > 1 ? 3 : 4;       // an SM
 };
 
 // The chunks of all small requests' row tiles, one after the other, are shared
@@ -1483,7 +1484,7 @@ Plan make_plan(const lmkv_pool_t* pool, int32_t q_heads, int32_t num_tokens, int
     x.tile_rows = x.own_cap <= 8 ? 8 : 16;
     x.own_tiles = (x.own_cap + x.tile_rows - 1) / x.tile_rows;
     const bool wide = pool->elem_bytes == 2 && pool->head_dim == 128;
-    const int64_t warps = (int64_t)kSms * kWarps * (most ? 4 : wide || x.tile_rows > 8 ? 3 : 4);
+    const int64_t warps = (int64_t)kSms * kWarps * (most ? 4 : wide ? 2 : x.tile_rows > 8 ? 3 : 4);
     int64_t streams = warps / heads > 0 ? warps / heads : 1;
     x.streams = (int32_t)streams;
     // (smaller batches may have tiles of fewer rows, and so of more in number)
