@@ -326,6 +326,11 @@ def test_attend_long_contexts_in_parts(wide):
     attend_case(Cache([40], [5000], 4, 2, 64, FP, wide), 3000, 4)
 
 
+def test_attend_one_long_context_among_many():
+    """Rows of many parts beside many rows of one."""
+    attend_case(Cache([1] * 200, [9000] + [5 + i % 20 for i in range(199)], 4, 1, 64, BF))
+
+
 def test_attend_more_items_than_sms():
     b = Cache([130, 90, 75], [131, 300, 75], 64, 16, 64, BF, False)
     attend_case(b)
