@@ -19,7 +19,7 @@ int make_rotary(const lmkv_rotary_t* in, int32_t head_dim, Rotary* out) {
         if (!std::isfinite(in->inv_freq[i])) return LMKV_ERR_INVALID_ARG;
         double t = in->inv_freq[i] * 0.15915494309189533577;    // 1 / 2 pi
         t -= std::floor(t);                                     // whole turns change nothing
-        const double scaled = std::nearbyint(std::ldexp(t, 64));
+        const double scaled = std::nearbyint(t * 18446744073709551616.0);     // 2^64
         out->turns[i] = scaled >= 18446744073709551616.0 ? 0 : (uint64_t)scaled;
     }
     return LMKV_OK;

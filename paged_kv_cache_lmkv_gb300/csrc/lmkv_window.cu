@@ -1513,8 +1513,16 @@ int launch_streams(const WindowParams& p, void* stream) {
                   StreamShape<KV, D, NT>::kSmem, stream, 1, p);
 }
 
+// What the kernels of one type need before their first launch, all at once (once per device; the first call,
+// made outside any capture).
 template <class T, class KV, int D>
-int window_typed(const WindowParams& p, const Plan& x, void* stream) {
+int get_ready() {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    const cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return lmkv_internal_cuda_status(err);
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return LMKV_OK;
     int rc = allow_smem<window_streams_kernel<T, KV, D, 1>, StreamShape<KV, D, 1>::kSmem>();
     if (rc == LMKV_OK) rc = allow_smem<window_streams_kernel<T, KV, D, 2>, StreamShape<KV, D, 2>::kSmem>();
     if (rc == LMKV_OK) rc = allow_smem<window_tiles_kernel<T, KV, D>, WindowTile<D>::kSmem>();
@@ -1523,6 +1531,13 @@ int window_typed(const WindowParams& p, const Plan& x, void* stream) {
     if (rc == LMKV_OK) rc = keep_carveout<window_join_kernel<T, D, false, 1>>();
     if (rc == LMKV_OK) rc = keep_carveout<window_join_kernel<T, D, false, kJoinWarps>>();
     if (rc == LMKV_OK) rc = keep_carveout<window_join_kernel<T, D, true, 1>>();
+    if (rc == LMKV_OK) done.fetch_or(bit, std::memory_order_relaxed);
+    return rc;
+}
+
+template <class T, class KV, int D>
+int window_typed(const WindowParams& p, const Plan& x, void* stream) {
+    int rc = get_ready<T, KV, D>();
     if (rc == LMKV_OK) rc = x.tile_rows == 8 ? launch_streams<T, KV, D, 1>(p, stream) : launch_streams<T, KV, D, 2>(p, stream);
     if (rc == LMKV_OK && x.big_rows < INT32_MAX)
         rc = launch(window_tiles_kernel<T, KV, D>, p.items < kSms ? p.items : kSms, kTileThreads, WindowTile<D>::kSmem, stream, 1,

@@ -1038,12 +1038,13 @@ def evict_layer(pool, layer, block_table, kv_len, scores, sinks, recent, keep, n
 def _cache_dtype(pool, name: str, t: torch.Tensor):
     """(element type of the rows, lmkv_dtype_t, DEVICE array of scales or None) of a call on a
     16-bit pool, whose type the rows have, or an 8-bit one."""
-    t0, dt = pool.layers[0], t.dtype
+    dt, scales = t.dtype, pool.scale_ptrs
     code = _DTYPES.get(dt)
     if code is None or code == FP32:
         raise ValueError(f"{name} must be bfloat16 or float16, got {dt}")
-    if pool.scale_ptrs is not None:
-        return dt, code, pool.scale_ptrs.data_ptr()
+    if scales is not None:
+        return dt, code, scales.data_ptr()
+    t0 = pool.layers[0]
     if t0.element_size() == 1:
         raise ValueError("an 8-bit pool needs its scales (Pool(..., scales=))")
     return t0.dtype, _dtype_of(t0), None
