@@ -522,7 +522,8 @@ struct StreamShape {
 // equally among warps, whatever the lengths are; a warp runs through its share by itself, with
 // no barrier, a ring of its own in shared memory filled by cp.async, and leaves a partial result for each row
 // tile that it had some of.  Stream s of KV head h is warp s * kv_heads + h: the heads' warps of the same tokens run
-// side by side and read the same pages' rows.  Bound by the bytes of the pages.
+// side by side and read the same pages' rows.  Bound by the bytes of the pages (with the join: 64 users of 1000 to 9000
+// tokens, 8 bits, 125 us, 5.3 TB/s; 48 users with a window of 4096, 16 bits, 115 us, 6.2 TB/s).
 template <class T, class KV, int D, int NT>
 __global__ void __launch_bounds__(kWarps * 32, StreamShape<KV, D, NT>::kCtas)
 window_streams_kernel(const __grid_constant__ WindowParams p) {
@@ -616,7 +617,8 @@ window_streams_kernel(const __grid_constant__ WindowParams p) {
 
 // Joins the parts of rows that have them: of the small requests' rows (kTiles false: a
 // stream's parts each) or of the big ones' (the tile kernel's parts).  kRowWarps warps a row: one where there are many rows, of few parts
-// each, and all of a CTA's where few rows have many.
+// each, and all of a CTA's where few rows have many.  (One request of 131072 tokens, 8 heads on one KV head: 214 us in all
+// with a warp a row, 33 with a CTA.)  Bound by waits for the parts, a load or two a warp.
 template <class T, int D, bool kTiles, int kRowWarps>
 __global__ void __launch_bounds__(kRowWarps == 1 ? 256 : kRowWarps * 32) window_join_kernel(const __grid_constant__ WindowParams p) {
     constexpr int kPer = D / 32;
@@ -781,6 +783,8 @@ constexpr int kItems = 4;    // on their way
 // which 18,000 were that.
 // A unit's scales are the same for its 16 keys: a factor and an addend of the exponent's multiply-add.
 // Tensor memory: scores of tile 0, 1 at columns 0, 128; outputs at 256, 384.
+// Bound by the softmax's instructions between two products.  (4 prompts of 65 to 1200 tokens behind 1500 to 8000 on an
+// 8-bit cache, 64 heads: 351 us, 1.05 PFLOP/s.)
 template <class T, class KV, int D>
 __global__ void __launch_bounds__(kTileThreads, 1)
 window_tiles_kernel(const __grid_constant__ WindowParams p) {
