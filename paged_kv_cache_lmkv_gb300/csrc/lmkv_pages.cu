@@ -64,6 +64,9 @@ constexpr int kCluster = 8;
 constexpr int kOne = 1024;         // threads of a CTA
 constexpr int kWarps = kOne / 32;
 constexpr int kAll = kCluster * kOne, kAllWarps = kCluster * kWarps;
+// Pages that a pool may have here: the threads' counters go beyond the last one by less than kAll, and
+// have 32 bits.
+constexpr int64_t kMostPages = (int64_t)INT32_MAX - kAll;
 
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -419,7 +422,7 @@ int begin(const lmkv_pool_t* pool, const int32_t* table, int32_t max_blocks, con
           uint64_t workspace_bytes, int32_t* d_status, PagesParams* p) {
     const int rc = lmkv_internal_check_pool(pool);
     if (rc != LMKV_OK) return rc;
-    if (pool->num_blocks > INT32_MAX - 4096) return LMKV_ERR_UNSUPPORTED;
+    if (pool->num_blocks > kMostPages) return LMKV_ERR_UNSUPPORTED;
     if (rows < 0 || rows_out < 0 || rows > kMostRows || rows_out > kMostRows || max_blocks < 0 ||
         (int64_t)max_blocks * (rows > rows_out ? rows : rows_out) > INT32_MAX ||
         refs == nullptr || refs_out == nullptr ||
@@ -473,7 +476,7 @@ extern "C" {
 int lmkv_pages_workspace_bytes(const lmkv_pool_t* pool, int32_t rows, uint64_t* bytes) {
     const int rc = lmkv_internal_check_pool(pool);
     if (rc != LMKV_OK) return rc;
-    if (pool->num_blocks > INT32_MAX - 4096) return LMKV_ERR_UNSUPPORTED;
+    if (pool->num_blocks > kMostPages) return LMKV_ERR_UNSUPPORTED;
     if (bytes == nullptr || rows < 0 || rows > kMostRows) return LMKV_ERR_INVALID_ARG;
     *bytes = workspace_need(pool, rows);
     return LMKV_OK;
