@@ -814,7 +814,8 @@ int lmkv_attend_layer_window(const lmkv_pool_t* pool, void* const* scales, int32
  * otherwise.  Pages move with all layers, K and V, and their scales (NULL: a pool
  * without).  An entry that is out of range stays as it is (BAD_BLOCK), a length beyond the
  * table is clamped (BAD_LENGTH).  Where no free page is left the entry is -1 (NO_PAGES).
- * Pools of more than 2^31 - 8193 pages are UNSUPPORTED.
+ * Pools of more than 2^31 - 8193 pages are UNSUPPORTED, tables of more entries
+ * than that INVALID_ARG.
  *   workspace : DEVICE, 16-byte aligned, lmkv_pages_workspace_bytes bytes for at least the
  *               call's rows; contents irrelevant, not shared with calls that may run at the same time */
 int lmkv_pages_workspace_bytes(const lmkv_pool_t* pool, int32_t rows, uint64_t* bytes);

@@ -67,6 +67,8 @@ constexpr int kAll = kCluster * kOne, kAllWarps = kCluster * kWarps;
 // Pages that a pool may have here: the threads' counters go beyond the last one by less than kAll, and
 // have 32 bits.
 constexpr int64_t kMostPages = (int64_t)INT32_MAX - kAll;
+// Entries of a table, whose columns a warp goes through 32 at a time.
+constexpr int64_t kMostEntries = (int64_t)INT32_MAX - kAll;
 
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -424,7 +426,7 @@ int begin(const lmkv_pool_t* pool, const int32_t* table, int32_t max_blocks, con
     if (rc != LMKV_OK) return rc;
     if (pool->num_blocks > kMostPages) return LMKV_ERR_UNSUPPORTED;
     if (rows < 0 || rows_out < 0 || rows > kMostRows || rows_out > kMostRows || max_blocks < 0 ||
-        (int64_t)max_blocks * (rows > rows_out ? rows : rows_out) > INT32_MAX ||
+        (int64_t)max_blocks * (rows > rows_out ? rows : rows_out) > kMostEntries ||
         refs == nullptr || refs_out == nullptr ||
         (rows > 0 && (kv_len == nullptr || (max_blocks > 0 && table == nullptr))) ||
         (rows_out > 0 && max_blocks > 0 && table_out == nullptr) || workspace == nullptr ||

@@ -39,3 +39,12 @@ def test_pages_that_a_counter_of_32_bits_would_step_past(lib, which):
     assert size(MOST) == lmkv.OK and out.value > 24 * MOST
     assert pages(lib, which, num_blocks=MOST) == INV                 # (the workspace)
     assert lmkv.launch_count() == before
+
+
+@pytest.mark.parametrize("which", ["fork", "resize", "compact"])
+def test_tables_whose_columns_a_counter_of_32_bits_would_step_past(lib, which):
+    """A lane's counter of columns passes the last one by up to 31 (128 where four steps are taken at once)."""
+    before = lmkv.launch_count()
+    for rows, cols in ((1, 2 ** 31 - 1), (1, 2 ** 31 - 128), (1, MOST + 1), (2, MOST // 2 + 1)):
+        assert pages(lib, which, rows=rows, cols=cols, ws_bytes=1 << 30) == INV, (rows, cols)
+    assert lmkv.launch_count() == before
