@@ -749,8 +749,9 @@ int lmkv_evict_layer(const lmkv_pool_t* pool, int32_t layer, const int32_t* bloc
  *   scales : DEVICE array of num_layers DEVICE pointers, each to
  *            uint8 [2][num_blocks][num_kv_heads]; NULL with a 16-bit pool
  * A null entry is reported as BAD_POINTER.  Scales belong to whole pages:
- * lmkv_evict_layer, which moves rows from page to page, is not for such a pool, and
- * the gather and scatter calls move its codes alone. */
+ * lmkv_evict_layer, which moves rows from page to page, is not for such a pool, nor
+ * are the gather, scatter, store and retrieve calls: they know of no scales and move codes alone, which are
+ * other values in another page's scale.  Whole pages move with theirs by the calls of "Pages". */
 
 /* lmkv_append_layer for models that norm each head of q and k, into 16-bit or
  * 8-bit pages.  Of each head of q and of k,

@@ -265,7 +265,9 @@ class Pool:
     Holds the DEVICE array of layer base pointers the ABI takes.  scales: the
     tensors of an 8-bit pool's powers of two, per layer [2][num_blocks][heads] in
     float8_e8m0fnu or uint8 (value = code * 2^(byte - 127)); the layers then hold
-    e4m3 codes, as float8_e4m3fn or uint8.
+    e4m3 codes, as float8_e4m3fn or uint8.  A scale belongs to a whole page, so the
+    calls that move rows (gather, scatter, store, retrieve, the codec, evict_layer)
+    refuse such a pool: whole pages move by copy_pages, fork_pages and compact_pages.
     """
 
     scales = scale_ptrs = None
@@ -399,6 +401,9 @@ def _ptr(t):
 
 def _common(pool: Pool, block_table: torch.Tensor, start, end):
     """(pool, table, max_blocks, start, end, num_req) plus the host arrays to keep alive."""
+    if pool.scales is not None:
+        raise ValueError("rows of an 8-bit pool do not move apart from their page's scale (a Pool of the layers without "
+                         "scales moves the codes alone)")
     if block_table.dtype != torch.int32:
         raise ValueError("block_table must be int32")
     s, e = _i64_array(start), _i64_array(end)

@@ -2,7 +2,9 @@
 before any CUDA call (CPU only)."""
 import ctypes
 
+import numpy as np
 import pytest
+import torch
 
 from paged_kv_cache_lmkv_gb300 import build, lmkv
 
@@ -48,3 +50,47 @@ def test_tables_whose_columns_a_counter_of_32_bits_would_step_past(lib, which):
     for rows, cols in ((1, 2 ** 31 - 1), (1, 2 ** 31 - 128), (1, MOST + 1), (2, MOST // 2 + 1)):
         assert pages(lib, which, rows=rows, cols=cols, ws_bytes=1 << 30) == INV, (rows, cols)
     assert lmkv.launch_count() == before
+
+
+def movement_calls():
+    """The calls that take rows out of pages or into them, on requests of no tokens."""
+    table = torch.zeros((1, 4), dtype=torch.int32)
+    a = (table, np.array([0]), np.array([16]), 16, True)
+    chunks, staging = torch.zeros(1, dtype=torch.int64), torch.zeros(64, dtype=torch.uint8)
+    host, bins, sizes = [staging], np.full((2, 2), 16, np.int32), torch.zeros(1, dtype=torch.int64)
+    some = dict(stream=0)
+    two = dict(stream=0, copy_stream=0)
+    return {
+        "gather_chunks": lambda p: lmkv.gather_chunks(p, *a, chunks, **some),
+        "scatter_chunks": lambda p: lmkv.scatter_chunks(p, *a, chunks, **some),
+        "gather_layer": lambda p: lmkv.gather_layer(p, *a, chunks, 0, **some),
+        "scatter_layer": lambda p: lmkv.scatter_layer(p, *a, chunks, 0, **some),
+        "gather_chunks_fp8e4m3": lambda p: lmkv.gather_chunks_fp8e4m3(p, *a, chunks, chunks, **some),
+        "scatter_chunks_fp8e4m3": lambda p: lmkv.scatter_chunks_fp8e4m3(p, *a, chunks, chunks, **some),
+        "store_layers": lambda p: lmkv.store_layers(p, *a, chunks, 0, 2, **some),
+        "retrieve_layers": lambda p: lmkv.retrieve_layers(p, *a, chunks, 0, 2, **some),
+        "store_layers_staged": lambda p: lmkv.store_layers_staged(p, *a, host, staging, 0, 2, **some),
+        "retrieve_layers_staged": lambda p: lmkv.retrieve_layers_staged(p, *a, host, staging, 0, 2, **some),
+        "store_layers_staged_noalloc": lambda p: lmkv.store_layers_staged_noalloc(p, *a, host, 0, 2, **some),
+        "store_layers_overlapped": lambda p: lmkv.store_layers_overlapped(p, *a, host, staging, 0, 2, None, **two),
+        "retrieve_layers_overlapped": lambda p: lmkv.retrieve_layers_overlapped(p, *a, host, staging, 0, 2, None, **two),
+        "cachegen_store_chunks": lambda p: lmkv.cachegen_store_chunks(p, *a, bins, chunks, sizes, staging, **some),
+        "cachegen_retrieve_chunks": lambda p: lmkv.cachegen_retrieve_chunks(p, *a, bins, chunks, sizes, staging, **some),
+    }
+
+
+@pytest.mark.parametrize("name", list(movement_calls()))
+@pytest.mark.parametrize("scales", [False, True])
+def test_rows_of_a_pool_with_scales_do_not_move_without_them(lib, name, scales):
+    """The calls that move chunks know of no scales: codes in another page's scale are other values.  A Pool of the same
+    layers without scales is taken as bytes, as before (here its layers are null, which the library says)."""
+    pool = lmkv.Pool.__new__(lmkv.Pool)
+    pool.num_kv_heads, pool.head_dim, pool.elem_bytes, pool.block_size, pool.num_blocks = 2, 64, 1, 16, 4
+    pool._struct = lmkv._PoolT(None, 4, 2, 2, 64, 16, 1)
+    call = movement_calls()[name]
+    if not scales:
+        assert call(pool) == INV
+        return
+    pool.scales = [None, None]
+    with pytest.raises(ValueError, match="scale"):
+        call(pool)
