@@ -97,10 +97,14 @@ struct Seen {
     __device__ __forceinline__ int32_t unit(int32_t i) const { return i < first_units ? i : i - first_units + then; }
     __device__ __forceinline__ bool some(int32_t j) const { return j < end && (j < sink_end || j >= lo); }
 };
+// The first key that token t's window has, t < 0 too: a difference of the two would not fit 32 bits for every window.
+__device__ __forceinline__ int32_t first_in_window(const WindowParams& p, int32_t t) {
+    return p.window == INT32_MAX ? 0 : max(t + 1, p.window) - p.window;
+}
 __device__ __forceinline__ Seen seen_by(const WindowParams& p, int32_t t0, int32_t t1, int32_t unit) {
     Seen s;
     s.end = max(t1 + 1, 0);
-    s.lo = p.window == INT32_MAX ? 0 : max(t0 + 1 - p.window, 0);
+    s.lo = first_in_window(p, t0);
     s.sink_end = min(p.sinks, s.end);
     if (s.lo <= s.sink_end) s.lo = s.sink_end = 0;      // one stretch
     s.first_units = (s.sink_end + unit - 1) / unit;
@@ -1000,7 +1004,7 @@ window_tiles_kernel(const __grid_constant__ WindowParams p) {
                 const bool live = R < req_rows;
                 const int32_t n = (int32_t)p.by_group.div((uint32_t)(live ? R : item.row0));
                 // my row sees keys below end, from begin on or below the sinks
-                const int32_t end = live ? item.old + n + 1 : 0, begin = p.window == INT32_MAX ? 0 : end - p.window;
+                const int32_t end = live ? item.old + n + 1 : 0, begin = first_in_window(p, end - 1);
                 m = -INFINITY;
                 l2 = make_float2(0.f, 0.f);
                 row_left = true;
