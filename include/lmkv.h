@@ -767,7 +767,8 @@ int lmkv_evict_layer(const lmkv_pool_t* pool, int32_t layer, const int32_t* bloc
  * If it grows, earlier tokens' codes are rounded again to the new scale (repeated calls give the
  * same codes).  Codes are value / 2^e to nearest even, saturating; a value that is not finite
  * becomes a NaN code and does not count for e.  Slots that hold no token are left as they are.
- * A page that two requests of the batch write to is not allowed.
+ * A page that new tokens go into is held by their request's row alone (with 8 bits its scale
+ * is the whole page's): lmkv_fork_pages sees to that, after lmkv_resize_pages too.
  * head_dim 64 or 128 (UNSUPPORTED otherwise).  Everything else, errors too, as
  * lmkv_append_layer. */
 int lmkv_append_layer_normed(const lmkv_pool_t* pool, void* const* scales, int32_t dtype, int32_t layer,
@@ -843,7 +844,11 @@ int lmkv_fork_pages(const lmkv_pool_t* pool, void* const* scales, const int32_t*
 /* Rows of kv_len tokens become rows of new_len tokens: pages behind give up a
  * reference (after an eviction, or new_len = 0 of a request that has ended), pages
  * that are missing are given, those that this call frees among them.
- * table_out may be block_table. */
+ * table_out may be block_table.
+ * A row that becomes shorter may end inside a page that other rows hold (a beam that goes back behind
+ * its fork): it keeps that page, and nothing may be appended to the row as it is, as the tokens there are the others'.
+ * lmkv_fork_pages with parents[i] = i gives every such row a copy of its own; where refs of a
+ * row's last page is 1, or the length a multiple of block_size, no other row is concerned. */
 int lmkv_resize_pages(const lmkv_pool_t* pool, const int32_t* block_table, int32_t max_blocks, const int32_t* kv_len,
                       const int32_t* new_len, int32_t rows, const int32_t* refs, int32_t* table_out,
                       int32_t* refs_out, void* workspace, uint64_t workspace_bytes, int32_t* d_status, void* stream);

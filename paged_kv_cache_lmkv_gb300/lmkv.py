@@ -1149,7 +1149,9 @@ def fork_pages(pool, block_table, kv_len, parents, refs, table_out, len_out, ref
 def resize_pages(pool, block_table, kv_len, new_len, refs, table_out, refs_out, workspace, status=None,
                  stream=None) -> int:
     """lmkv_resize_pages: rows of kv_len tokens become rows of new_len: pages behind give up a
-    reference, missing ones are given.  table_out may be block_table, refs_out refs."""
+    reference, missing ones are given.  table_out may be block_table, refs_out refs.
+    A row cut back to inside a page that other rows hold keeps that page: fork_pages with
+    parents 0, 1, 2, .. gives it a copy of its own, which an append to it needs."""
     dev, i32 = pool.layers[0].get_device(), torch.int32
     rows, cols = kv_len.shape[0], block_table.shape[-1]
     held = (pool.num_blocks,)

@@ -27,3 +27,64 @@ def test_attend_windows_that_end_near_32_bits(new, heads, wide, window):
     want, want_l = attend_case(b)
     assert torch.equal(out, want) and torch.equal(lse, want_l)
     attend_case(b, window, 3)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_a_beam_goes_back_into_a_page_that_it_shares(wide):
+    """Two beams of 40 tokens share two full pages; the second goes back to 20.  Its last page is then the first's full one,
+    until a fork of all rows by their own numbers gives it one of its own, which it may append to."""
+    page, dim, heads = 16, 64, 2
+    b = Cache([1], [40], heads, heads, dim, BF, wide, page, spare=8, layers=1, layer=0, seed=4)
+    i32 = dict(dtype=torch.int32, device=b.device)
+    refs = torch.zeros(b.num_blocks, **i32)
+    refs[b.table_d[0, :3].long()] = 1
+    cols = b.table.shape[1]
+    ws = torch.empty(pkg.pages_workspace_bytes(b.pool, 2), dtype=torch.uint8, device=b.device)
+    bits = torch.int16 if wide else torch.uint8
+
+    def fork(table, lens, parents):
+        out, n = torch.empty((2, cols), **i32), torch.empty(2, **i32)
+        pkg.check(pkg.fork_pages(b.pool, table, lens, torch.tensor(parents, **i32), refs, out, n, refs, ws, b.status))
+        return out, n
+
+    def resize(table, lens, to):
+        to = torch.tensor(to, **i32)
+        pkg.check(pkg.resize_pages(b.pool, table, lens, to, refs, table, refs, ws, b.status))
+        return to
+
+    def of_row(row, n):
+        """Bits of a row's tokens, and its pages' scales."""
+        j = torch.arange(n, device=b.device)
+        slots = table[row].long()[j // page] * page + j % page
+        rows = b.pool.layers[0].view(bits).view(2, -1, heads * dim)[:, slots].clone()
+        return rows, None if wide else b.scales_d[0][:, table[row, :-(-n // page)].long()].clone()
+
+    table, lens = fork(b.table_d, b.kv_len_d, [0, 0])
+    assert table[0, :2].tolist() == table[1, :2].tolist() and refs[table[0, 1]] == 2
+    lens = resize(table, lens, [40, 20])
+    assert refs[table[1, 1]] == 2                   # a last page, not full, that another row holds too
+    first, second = of_row(0, 40), of_row(1, 20)
+    table, lens = fork(table, lens, [0, 1])
+    for r, n in enumerate((40, 20)):
+        assert refs[table[r, (n - 1) // page]] == 1
+    grown = resize(table, lens, [41, 21])
+    g = torch.Generator().manual_seed(5)
+    q, k, v = ((torch.randn((2, heads, dim), generator=g) * 1000).to(BF).to(b.device) for _ in range(3))
+    pkg.check(pkg.append_layer_normed(b.pool, 0, table, q, k, v, q, torch.arange(3, **i32), grown, status=b.status))
+    torch.cuda.synchronize()
+    assert b.status.item() == 0
+    got = of_row(0, 32)                             # the pages that the append does not write to
+    assert torch.equal(got[0], first[0][:, :32]) and (wide or torch.equal(got[1], first[1][:, :2]))
+    got = of_row(1, 16)
+    assert torch.equal(got[0], second[0][:, :16]) and (wide or torch.equal(got[1], second[1][:, :1]))
+    if wide:
+        assert torch.equal(of_row(0, 40)[0], first[0]) and torch.equal(of_row(1, 20)[0], second[0])
+        assert torch.equal(of_row(1, 21)[0][1, 20], v[1].view(torch.int16).flatten())
+    else:                                           # the last pages' earlier codes, to the new token's scale
+        now, then = of_row(1, 20), second
+        assert bool((now[1][:, 1] > then[1][:, 1]).all())
+        code = lambda x: x.view(torch.float8_e4m3fn).double().view(2, -1, heads, dim)
+        value = lambda x, s: code(x[:, 16:20]) * torch.exp2(s[:, 1].double() - 127)[:, None, :, None]
+        step = torch.exp2(now[1][:, 1].double() - 127 - 10)[:, None, :, None]
+        a, z = value(*then), value(*now)
+        assert bool(((a - z).abs() <= torch.maximum(a.abs() * 2.0 ** -4, step)).all())
