@@ -1077,6 +1077,11 @@ def append_layer_normed(pool, layer, block_table, q, k, v, q_out, q_start, kv_le
         _stream_of(pool, dev, stream))
 
 
+def _count(n) -> int:
+    """A number of tokens for the library's 32 bits: as good as all of them where it is larger, refused below 0."""
+    return max(-1, min(int(n), 2 ** 31 - 1))
+
+
 def attend_window_workspace_bytes(pool, num_q_heads: int, num_tokens: int, num_req: int, max_new: int,
                                   max_kv_len: int = 0) -> int:
     """Bytes of workspace for attend_layer_window calls within these bounds (smaller ones too)."""
@@ -1099,8 +1104,8 @@ def attend_layer_window(pool, layer, q, out, q_start, kv_len, block_table, scale
     qs = (tokens, heads, pool.head_dim)
     b, _ = _batch(pool, dev, block_table, q_start, kv_len, tokens, max_new, max_kv_len)
     return load().lmkv_attend_layer_window(
-        pool.struct, scales, code, int(layer), b, heads, _rows("q", q, dt, dev, qs), float(scale), int(window),
-        int(sinks), _rows("out", out, dt, dev, qs),
+        pool.struct, scales, code, int(layer), b, heads, _rows("q", q, dt, dev, qs), float(scale), _count(window),
+        _count(sinks), _rows("out", out, dt, dev, qs),
         None if lse is None else _whole("lse", lse, torch.float32, dev, (tokens, heads)),
         _whole("workspace", workspace, torch.uint8, dev, (workspace.numel(),)), workspace.numel(),
         _status(status, dev), _stream_of(pool, dev, stream))

@@ -94,3 +94,27 @@ def test_rows_of_a_pool_with_scales_do_not_move_without_them(lib, name, scales):
     pool.scales = [None, None]
     with pytest.raises(ValueError, match="scale"):
         call(pool)
+
+
+@pytest.mark.parametrize("name,value", [("window", 2 ** 32 + 5), ("sinks", 2 ** 32 + 1), ("window", 2 ** 31), ("sinks", 2 ** 40)])
+def test_windows_and_sinks_beyond_32_bits_are_all_keys(monkeypatch, name, value):
+    """Not what is left of them in 32 bits, which would be another window; below zero they are refused all the same."""
+    seen = {}
+
+    class Library:
+        def lmkv_attend_layer_window(self, pool, scales, code, layer, batch, heads, q, scale, window, sinks, *rest):
+            seen.update(window=window, sinks=sinks)
+            return lmkv.OK
+    monkeypatch.setattr(lmkv, "load", lambda: Library())
+    monkeypatch.setattr(lmkv, "_stream_of", lambda *a: 0)
+    pool = lmkv.Pool.__new__(lmkv.Pool)
+    pool.layers, pool.num_kv_heads, pool.head_dim, pool.block_size = [torch.zeros((2, 4, 16, 128), dtype=torch.float16)], 2, 64, 16
+    pool._struct = lmkv._PoolT(None, 4, 1, 2, 64, 16, 2)
+    q, i32 = torch.zeros((1, 2, 64), dtype=torch.float16), torch.int32
+    call = lambda **kw: lmkv.attend_layer_window(
+        pool, 0, q, torch.zeros_like(q), torch.tensor([0, 1], dtype=i32), torch.tensor([3], dtype=i32),
+        torch.zeros((1, 4), dtype=i32), 0.125, torch.zeros(64, dtype=torch.uint8), **kw)
+    assert call(**{name: value}) == lmkv.OK and seen[name] == 2 ** 31 - 1
+    assert call(**{name: 7}) == lmkv.OK and seen[name] == 7
+    call(**{name: -2 ** 40})
+    assert -2 ** 31 <= seen[name] < 0
