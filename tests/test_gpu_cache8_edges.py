@@ -5,7 +5,8 @@ import torch
 import paged_kv_cache_lmkv_gb300 as pkg
 from cache8_util import Cache
 from gpu_util import require_gpu
-from test_gpu_cache8 import attend_case
+from paged_kv_cache_lmkv_gb300 import lmkv
+from test_gpu_cache8 import attend_case, run_attend
 
 pytestmark = pytest.mark.gpu
 BF, FP = torch.bfloat16, torch.float16
@@ -88,3 +89,77 @@ def test_a_beam_goes_back_into_a_page_that_it_shares(wide):
         step = torch.exp2(now[1][:, 1].double() - 127 - 10)[:, None, :, None]
         a, z = value(*then), value(*now)
         assert bool(((a - z).abs() <= torch.maximum(a.abs() * 2.0 ** -4, step)).all())
+
+
+@pytest.mark.parametrize("new", [1, 5, 40])
+@pytest.mark.parametrize("large", [0, 1, 2])
+def test_attend_scales_of_v_that_differ_by_2_to_the_64(new, large):
+    """Pages of 2^-24 beside pages of 2^40, every second page or one of them; scores alike, and far in favour of a page of
+    small values."""
+    b = Cache([new], [300], 8, 2, 128, BF, seed=5)
+    pages = b.table[0, :19].long()
+    b.scales_cpu[:, 0] = 127 - 7                    # (of K)
+    b.scales_cpu[:, 1] = 127 - 24
+    b.scales_cpu[:, 1, pages[::2] if large == 0 else pages[3 * large]] = 127 + 40
+    b.to(b.device)
+    attend_case(b)
+    attend_case(b, 64, 17)
+    if large:
+        flat = b.pool_cpu[1, 0].view(-1, 2, 128)
+        flat[b.slots(0)[[5, 290]]] = (b.q_cpu[:, ::4].float().mean(0) * 100).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        b.to(b.device)
+        attend_case(b)
+
+
+def back_to_front(x):
+    """Rows of a copy of x [tokens][heads][dim] laid out last token and last head first, and that copy."""
+    store = x.flip(0, 1).contiguous()
+    t, h, d = x.shape
+    return lmkv._RowsT(store.data_ptr() + (t * h - 1) * d * x.element_size(), -h * d, -d), store
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("wide", [False, True])
+def test_attend_strides_below_zero(new, wide):
+    b = Cache([new, 2], [90, 33], 6, 2, 64, BF, wide)
+    want, want_l = run_attend(b, 30, 2)
+    q, q_store = back_to_front(b.q)
+    out, out_store = back_to_front(torch.zeros_like(b.q))
+    lse = torch.zeros_like(want_l)
+    n = pkg.attend_window_workspace_bytes(b.pool, 6, b.tokens, 2, new if new > 2 else 2, 90)
+    ws = torch.empty(n, dtype=torch.uint8, device=b.device)
+    batch, _ = lmkv._batch(b.pool, ws.get_device(), b.table_d, b.q_start_d, b.kv_len_d, b.tokens, max(new, 2), 90)
+    pkg.check(lmkv.load().lmkv_attend_layer_window(
+        b.pool.struct, None if wide else b.pool.scale_ptrs.data_ptr(), lmkv.BF16, 1, batch, 6, bytes(q), b.scale, 30, 2,
+        bytes(out), lse.data_ptr(), ws.data_ptr(), n, b.status.data_ptr(), torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    assert b.status.item() == 0
+    assert torch.equal(out_store.flip(0, 1), want) and torch.equal(lse, want_l)
+
+
+@pytest.mark.parametrize("rot", [0, 34, 64])
+@pytest.mark.parametrize("wide", [False, True])
+def test_append_strides_below_zero(rot, wide):
+    """The same bits in the pages and in q_out."""
+    bs = [Cache([3, 20], [9, 41], 4, 2, 64, BF, wide, seed=8) for _ in range(2)]
+    g = torch.Generator().manual_seed(9)
+    q, k, v = (torch.randn((23, h, 64), generator=g).to(BF).to(bs[0].device) for h in (4, 2, 2))
+    norm = (torch.rand(64, generator=g) + 0.5).to(q.device)
+    rotary = pkg.Rotary(rot) if rot else None
+    want = torch.zeros_like(q)
+    b = bs[0]
+    pkg.check(pkg.append_layer_normed(b.pool, 1, b.table_d, q, k, v, want, b.q_start_d, b.kv_len_d, rotary, norm, norm,
+                                      status=b.status))
+    b = bs[1]
+    rows = [back_to_front(x) for x in (q, k, v, torch.zeros_like(q))]
+    batch, _ = lmkv._batch(b.pool, q.get_device(), b.table_d, b.q_start_d, b.kv_len_d, 23, None, None)
+    pkg.check(lmkv.load().lmkv_append_layer_normed(
+        b.pool.struct, None if wide else b.pool.scale_ptrs.data_ptr(), lmkv.BF16, 1, batch, 4, *(bytes(r) for r, _ in rows), None,
+        None if rotary is None else rotary.struct, norm.data_ptr(), norm.data_ptr(), 1e-6, b.status.data_ptr(),
+        torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    assert bs[0].status.item() == 0 and b.status.item() == 0
+    assert torch.equal(rows[3][1].flip(0, 1), want)
+    for x, y in zip(bs[0].pool.layers, b.pool.layers):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    assert wide or torch.equal(bs[0].scales_d, b.scales_d)
