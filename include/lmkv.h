@@ -789,8 +789,8 @@ int lmkv_append_layer_normed(const lmkv_pool_t* pool, void* const* scales, int32
  *               bytes for bounds that the call's do not exceed
  * A token that sees nothing gets out = 0 and lse = -infinity.  A value that is
  * not finite reaches no row that does not see it but those of other new tokens
- * of its request.  8-bit pages: q is taken to fp16 relative to its row's largest element (below 2^-38
- * of that it loses bits), softmax weights times the page's V scale are
+ * of its request.  8-bit pages: q is taken to fp16 relative to its row's largest element (below 2^-28
+ * of that elements lose bits, below 2^-38 nothing is left of them), softmax weights times the page's V scale are
  * rounded to fp16 before they meet the codes.  V scales below 2^-90 count as 2^-90.  Those that one row sees
  * may differ by up to 2^64; pages that are further below the largest may count as nothing.
  * INVALID_ARG for window < 0, sinks < 0, scales that do not match elem_bytes;

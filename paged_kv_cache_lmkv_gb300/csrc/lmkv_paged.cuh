@@ -71,7 +71,7 @@ struct Layer {
     }
     // The same in two steps, so that the table entry's load need not be waited
     // for at once: its place, then the row's number in the K half (below 2^32
-    // in any memory: rows of 128 bytes and more), or kNoRow.
+    // in any memory: K and V rows of 64 bytes and more), or kNoRow.
     __device__ __forceinline__ uint32_t column(int32_t tok) const { return by_block.div((uint32_t)tok); }
     __device__ __forceinline__ uint32_t row_of(int32_t blk, int32_t tok, uint32_t col) const {
         if (blk < 0 || blk >= num_blocks) return kNoRow;

@@ -329,7 +329,7 @@ struct CopyParams {
 constexpr int kVecs = 8;           // 16-byte loads of a thread in flight
 
 // A CTA an item, in turn: the tokens of one page, K or V of one layer, as one run
-// of rows.  Bound by the bytes, both ways.  (1000 pages of 16 layers, 680 MB both ways: 108 us, 6.3 TB/s.)
+// of rows.  Bound by the bytes, both ways.  (650 pages of 16 layers, 680 MB both ways: 108 us, 6.3 TB/s.)
 __global__ void __launch_bounds__(kThreads) pages_copy_kernel(const __grid_constant__ CopyParams p) {
     pdl_launch_dependents();
     pdl_wait();
