@@ -163,3 +163,71 @@ def test_append_strides_below_zero(rot, wide):
     for x, y in zip(bs[0].pool.layers, b.pool.layers):
         assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
     assert wide or torch.equal(bs[0].scales_d, b.scales_d)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_pages_beyond_32_bits_of_bytes(wide):
+    """A layer whose halves have more than 2^32 bytes each, with pages at their ends: append, attention (few rows and
+    tiles), copies and forks give the bits that they give in a small pool."""
+    page, heads, kv_heads, dim = 16, 16, 8, 128
+    small = Cache([1, 40, 3], [300, 200, 35], heads, kv_heads, dim, BF, wide, page, layers=1, layer=0, spare=6, seed=6)
+    size = 2 if wide else 1
+    blocks = 2 ** 32 // (page * kv_heads * dim * size) + 5000
+    dev = small.device
+    where = blocks - 1 - 7 * torch.arange(small.num_blocks, device=dev)        # of the small pool's pages
+    layer = torch.empty((2, blocks, page, kv_heads * dim), dtype=BF if wide else torch.uint8, device=dev)
+    bits = torch.int16 if wide else torch.uint8
+    layer[:, where] = small.pool.layers[0].view(layer.dtype)
+    scales = None
+    if not wide:
+        scales = torch.full((2, blocks, kv_heads), 255, dtype=torch.uint8, device=dev)
+        scales[:, where] = small.scales_d[0]
+    big = pkg.Pool([layer], kv_heads, dim, scales=None if wide else [scales])
+    far = torch.where(small.table_d >= 0, where[small.table_d.long().clamp(min=0)], -1).to(torch.int32)
+
+    def same():
+        torch.cuda.synchronize()
+        assert small.status.item() == 0
+        assert torch.equal(layer[:, where].view(bits), small.pool.layers[0].view(bits))
+        assert wide or torch.equal(scales[:, where], small.scales_d[0])
+
+    g = torch.Generator().manual_seed(3)
+    k, v = (torch.randn((44, kv_heads, dim), generator=g).to(BF).to(dev) for _ in range(2))
+    rotary = pkg.Rotary(dim)
+    got = []
+    for pool, table in ((small.pool, small.table_d), (big, far)):
+        q = torch.empty_like(small.q)
+        pkg.check(pkg.append_layer_normed(pool, 0, table, small.q, k, v, q, small.q_start_d, small.kv_len_d, rotary,
+                                          status=small.status))
+        n = pkg.attend_window_workspace_bytes(pool, heads, 44, 3, 40, 300)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        for window in (0, 33):
+            out, lse = torch.empty_like(q), torch.empty((44, heads), device=dev)
+            pkg.check(pkg.attend_layer_window(pool, 0, q, out, small.q_start_d, small.kv_len_d, table, small.scale, ws, window,
+                                              2, lse, max_new=40, max_kv_len=300, status=small.status))
+            got.append((q, out, lse))
+    same()
+    for a, b in zip(got[:2], got[2:]):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    # forks copy the last pages: from and to the far end
+    parents = torch.tensor([0, 0, 1, 2, 2], dtype=torch.int32, device=dev)
+    lens = torch.empty(5, dtype=torch.int32, device=dev)
+    rows = []
+    for pool, table, held in ((small.pool, small.table_d, torch.zeros(small.num_blocks, dtype=torch.int32, device=dev)),
+                              (big, far, torch.full((blocks,), -1, dtype=torch.int32, device=dev))):
+        if pool is big:
+            held[where] = 0
+        held[table[table >= 0].long()] = 1
+        out = torch.empty((5, table.shape[1]), dtype=torch.int32, device=dev)
+        ws = torch.empty(pkg.pages_workspace_bytes(pool, 5), dtype=torch.uint8, device=dev)
+        pkg.check(pkg.fork_pages(pool, table, small.kv_len_d, parents, held, out, lens, held, ws, small.status))
+        torch.cuda.synchronize()
+        rows.append([pool.layers[0].view(bits).view(2, -1, kv_heads * dim)[:, s] for s in (
+            (t.long()[j // page] * page + j % page) for t, j in zip(out, (torch.arange(int(n), device=dev) for n in lens)))])
+    assert small.status.item() == 0
+    assert all(torch.equal(a, b) for a, b in zip(*rows))
+    free = (held == 0).nonzero()[:2, 0].to(torch.int32)
+    src = far[0, :2].contiguous()
+    pkg.check(pkg.copy_pages(big, src, free, small.status))
+    torch.cuda.synchronize()
+    assert torch.equal(layer[:, free.long()].view(bits), layer[:, src.long()].view(bits)) and small.status.item() == 0
