@@ -786,7 +786,8 @@ int lmkv_append_layer_normed(const lmkv_pool_t* pool, void* const* scales, int32
  * sees any of are not read, and their table entries may be anything.
  *   dtype : of q and out, LMKV_BF16 or LMKV_FP16; a 16-bit pool's own
  *   workspace : as lmkv_attend_layer's, lmkv_attend_window_workspace_bytes
- *               bytes for bounds that the call's do not exceed
+ *               bytes for bounds that the call's do not exceed (pages of a multiple of 16 tokens take
+ *               far less of it, and of time, where requests bring many new tokens)
  * A token that sees nothing gets out = 0 and lse = -infinity.  A value that is
  * not finite reaches no row that does not see it but those of other new tokens
  * of its request.  8-bit pages: q is taken to fp16 relative to its row's largest element (below 2^-28
